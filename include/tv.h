@@ -69,6 +69,7 @@ typedef struct CUstream_st* tv_stream; /* same type as cudaStream_t */
 #define TV_MAX_SEQ 8    /* sequences in one launch */
 #define TV_MAX_NODES 64 /* nodes in one sequence's tree */
 #define TV_MAX_PATH 16  /* nodes on a root path, root included */
+#define TV_MAX_PROMPT_ROWS (1 << 20) /* packed rows of one prompt call */
 
 typedef enum {
   TV_OK = 0,
@@ -82,7 +83,8 @@ typedef enum {
   TV_ERR_WORKSPACE = 8, /* workspace smaller than the *_workspace_bytes bound */
   TV_ERR_TIMEOUT = 9,   /* device: a bounded wait inside a kernel expired */
   TV_ERR_LEN = 10,      /* device: a sequence length above the host bound max_len */
-  TV_ERR_SCRATCH = 11   /* host: request larger than the fixed scratch of tv_attn_tree_verify_static */
+  TV_ERR_SCRATCH = 11,  /* host: request larger than the fixed scratch of tv_attn_tree_verify_static */
+  TV_ERR_ROWS = 12      /* device: malformed row offsets of a prompt call */
 } tv_status;
 
 typedef enum { TV_F32 = 0, TV_BF16 = 1 } tv_dtype;
@@ -380,6 +382,103 @@ tv_status tv_gdn_decode_fused(const tv_gdn_layer* layer, const tv_gdn_front_laye
  * after every call that reads the tails for this round. */
 tv_status tv_gdn_conv_commit(const tv_gdn_front_layer* layer, const tv_tree* tree, int32_t n_seq, const void* x,
                              const int32_t* path, const int32_t* acc_len, int32_t* status, tv_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Prompts: whole prompts, or slices of them, through the mixers
+ * ------------------------------------------------------------------------
+ * "How ignis serves a request", "The shape of the process" (one call per
+ * prefill span); "One request, end to end", 2.5: a cold prompt is read into
+ * the caches before any round.  A prompt call takes the new rows of up to
+ * TV_MAX_SEQ sequences packed behind one another; sequence s owns packed rows
+ * row_off[s] .. row_off[s+1]-1 (none is allowed), which follow the len[s]
+ * rows its caches, states and tails already hold.  A long prompt may be fed
+ * in slices of any sizes.  One layer of a span runs
+ *   attention: tv_attn_prompt_front, tv_attn_prompt
+ *   GDN:       tv_gdn_prompt_front, tv_gdn_prompt, tv_gdn_out_norm
+ * and after the last layer len[s] += row_off[s+1] - row_off[s]
+ * (tv_len_advance): a verify round or a decode step then goes on from there.
+ *
+ * The offsets live on the device, so a captured graph serves every batch that
+ * fits its host bounds; rows from row_off[n_seq] on are padding, neither read
+ * nor written.  Offsets that do not start at 0, that fall, that give a sequence more
+ * than n_max rows or end past n_total set TV_ERR_ROWS; a length outside
+ * 0..max_len sets TV_ERR_LEN; rows past a cache's cap set TV_ERR_CAPACITY.
+ * Any of them makes the whole call a no-op.  Sequences of one call must not
+ * share a cache, state or tail.  n_total = 0 does nothing. */
+typedef struct {
+  int32_t n_seq;          /* sequences, 1..TV_MAX_SEQ (host) */
+  int32_t n_total;        /* rows the packed buffers hold, 0..TV_MAX_PROMPT_ROWS (host) */
+  int32_t n_max;          /* host bound on one sequence's rows, 0..n_total */
+  const int32_t* row_off; /* device [n_seq+1], row_off[0] = 0, not falling, row_off[n_seq] <= n_total */
+  int32_t* status;        /* device [1] error word, as in tv_tree */
+} tv_prompt;
+
+/* Head norms and rotation in one pass: tv_attn_rope's rotation (same planes,
+ * angles and positions) of rows that are first normalised per head,
+ *     x / sqrt(mean(x^2) + eps) * w,
+ * with the fp32 weights q_norm [D] for query heads and k_norm [D] for key
+ * heads, everything in fp32 and rounded once.  Both weights NULL: rotation
+ * alone (eps is then not read).  tree, n_seq, len, max_len, status, aliasing
+ * and errors as in tv_attn_rope; eps > 0 finite, weights 16-byte aligned.  A
+ * row's bits depend only on its own values and its position: tree, decode and
+ * prompt rows are equal bit for bit.  (tv_attn_rope forms its angles in fp64,
+ * this call in 64-bit integer fractions of a turn: their results may differ
+ * in the last bit.) */
+tv_status tv_attn_norm_rope(const tv_attn_layer* layer, const tv_tree* tree, int32_t n_seq, const int32_t* len,
+                            int32_t max_len, const float* q_norm, const float* k_norm, float eps,
+                            int32_t rot_dims, float theta, const void* q_raw, const void* k_raw, void* q, void* k,
+                            int32_t* status, tv_stream stream);
+
+/* The same for a prompt's rows, row i of sequence s at position len[s] + i:
+ * queries go to q, keys (normalised, rotated) and values (bit copies) into
+ * rows len[s] + i of the sequence's caches.
+ *  q_raw [n_total][Hq][D], k_raw, v [n_total][Hkv][D]; q [n_total][Hq][D]
+ *  (may alias q_raw).  The caches must not overlap the packed buffers. */
+tv_status tv_attn_prompt_front(const tv_attn_layer* layer, const tv_prompt* prompt, const int32_t* len,
+                               int32_t max_len, const float* q_norm, const float* k_norm, float eps,
+                               int32_t rot_dims, float theta, const void* q_raw, const void* k_raw, const void* v,
+                               void* q, tv_stream stream);
+
+/* Device scratch bytes tv_attn_prompt needs for this layer, these host bounds
+ * and contexts of at most max_len rows. */
+size_t tv_attn_prompt_workspace_bytes(const tv_attn_layer* layer, const tv_prompt* prompt, int32_t max_len);
+
+/* Causal attention of a prompt's rows over the cache: row i of sequence s
+ * sees cache rows 0 .. len[s] + i, its own included (tv_attn_prompt_front has
+ * put the prompt's rows there).
+ *  q, out [n_total][Hq][D] in the layer's dtype (out must not alias q)
+ *  gate   [n_total][Hq][D], applied as in tv_attn_tree_verify_gated, or NULL
+ *  scale  score scale > 0
+ *  workspace device scratch of at least tv_attn_prompt_workspace_bytes() bytes,
+ *         not shared with work that can run at the same time
+ * Rows of a cache behind the ones a sequence sees are not read into its
+ * results, whatever they hold. */
+tv_status tv_attn_prompt(const tv_attn_layer* layer, const tv_prompt* prompt, const int32_t* len, int32_t max_len,
+                         const void* q, const void* gate, void* out, float scale, void* workspace,
+                         size_t workspace_bytes, tv_stream stream);
+
+/* Device scratch bytes tv_gdn_prompt needs for this layer and these host
+ * bounds. */
+size_t tv_gdn_prompt_workspace_bytes(const tv_gdn_layer* layer, const tv_prompt* prompt);
+
+/* The gated delta rule over a prompt's rows: the recurrence of
+ * tv_gdn_tree_verify, row after row from the sequence's state, which is left
+ * advanced by all of them (a sequence without rows keeps its state).
+ *  q, k [n_total][Hk][dk]; v [n_total][Hv][dv]; alpha, beta fp32 [n_total][Hv]
+ *  out  [n_total][Hv][dv] (must not alias v); scale output scale > 0
+ *  workspace as in tv_attn_prompt. */
+tv_status tv_gdn_prompt(const tv_gdn_layer* layer, const tv_prompt* prompt, const void* q, const void* k,
+                        const void* v, const float* alpha, const float* beta, void* out, float scale,
+                        void* workspace, size_t workspace_bytes, tv_stream stream);
+
+/* tv_gdn_front over a prompt's rows: the convolution runs along each sequence
+ * and continues into its tail; unlike there the tails then advance to the
+ * last W-1 raw inputs (a prompt's rows are committed as they are read).
+ * Arguments as in tv_gdn_front with n_total rows, every pointer (wconv and
+ * tails too) 16-byte aligned; the outputs must not alias x. */
+tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* layer, const tv_prompt* prompt, const void* x,
+                              const float* a_raw, const float* b_raw, void* q, void* k, void* v, float* alpha,
+                              float* beta, tv_stream stream);
 
 /* ------------------------------------------------------------------------
  * Accept walk: longest agreeing path plus one token

@@ -24,7 +24,7 @@ TV_F32, TV_BF16 = 0, 1
 
 STATUS_NAMES = {0: "TV_OK", 1: "TV_ERR_ARG", 2: "TV_ERR_SHAPE", 3: "TV_ERR_DTYPE", 4: "TV_ERR_ALIGN",
                 5: "TV_ERR_TREE", 6: "TV_ERR_CAPACITY", 7: "TV_ERR_CUDA", 8: "TV_ERR_WORKSPACE",
-                9: "TV_ERR_TIMEOUT", 10: "TV_ERR_LEN", 11: "TV_ERR_SCRATCH"}
+                9: "TV_ERR_TIMEOUT", 10: "TV_ERR_LEN", 11: "TV_ERR_SCRATCH", 12: "TV_ERR_ROWS"}
 
 
 class TvError(RuntimeError):
@@ -58,6 +58,11 @@ class tv_gdn_front_layer(ctypes.Structure):
 
 class tv_plan(ctypes.Structure):
     _fields_ = [("split", c_int32)]
+
+
+class tv_prompt(ctypes.Structure):
+    _fields_ = [("n_seq", c_int32), ("n_total", c_int32), ("n_max", c_int32), ("row_off", c_void_p),
+                ("status", c_void_p)]
 
 
 _lib = None
@@ -134,6 +139,22 @@ def lib():
         L.tv_kvpool_reserved_bytes.argtypes = [vp]
         L.tv_kvpool_destroy.restype = c_int32
         L.tv_kvpool_destroy.argtypes = [vp]
+        R = POINTER(tv_prompt)
+        L.tv_attn_norm_rope.restype = c_int32
+        L.tv_attn_norm_rope.argtypes = [A, T, c_int32, vp, c_int32, vp, vp, c_float, c_int32, c_float, vp, vp, vp, vp,
+                                        vp, vp]
+        L.tv_attn_prompt_front.restype = c_int32
+        L.tv_attn_prompt_front.argtypes = [A, R, vp, c_int32, vp, vp, c_float, c_int32, c_float, vp, vp, vp, vp, vp]
+        L.tv_attn_prompt_workspace_bytes.restype = c_size_t
+        L.tv_attn_prompt_workspace_bytes.argtypes = [A, R, c_int32]
+        L.tv_attn_prompt.restype = c_int32
+        L.tv_attn_prompt.argtypes = [A, R, vp, c_int32, vp, vp, vp, c_float, vp, c_size_t, vp]
+        L.tv_gdn_prompt_workspace_bytes.restype = c_size_t
+        L.tv_gdn_prompt_workspace_bytes.argtypes = [G, R]
+        L.tv_gdn_prompt.restype = c_int32
+        L.tv_gdn_prompt.argtypes = [G, R, vp, vp, vp, vp, vp, vp, c_float, vp, c_size_t, vp]
+        L.tv_gdn_prompt_front.restype = c_int32
+        L.tv_gdn_prompt_front.argtypes = [F, R, vp, vp, vp, vp, vp, vp, vp, vp, vp]
         L.tv_wait_selftest.restype = c_int32
         L.tv_wait_selftest.argtypes = [vp, vp, ctypes.c_int64, vp]
         _lib = L
@@ -146,7 +167,9 @@ EXPORTED = ["tv_status_string", "tv_version", "tv_tree_meta_bytes", "tv_tree_pre
             "tv_kvpool_create", "tv_kvpool_reserve", "tv_kvpool_commit_rows", "tv_kvpool_release_rows",
             "tv_kvpool_committed_bytes", "tv_kvpool_reserved_bytes", "tv_kvpool_destroy", "tv_attn_rope",
             "tv_attn_tree_verify_gated", "tv_attn_decode_gated", "tv_gdn_front", "tv_gdn_out_norm",
-            "tv_gdn_conv_commit", "tv_gdn_tree_verify_fused", "tv_gdn_decode_fused", "tv_wait_selftest"]
+            "tv_gdn_conv_commit", "tv_gdn_tree_verify_fused", "tv_gdn_decode_fused", "tv_wait_selftest",
+            "tv_attn_norm_rope", "tv_attn_prompt_front", "tv_attn_prompt_workspace_bytes", "tv_attn_prompt",
+            "tv_gdn_prompt_workspace_bytes", "tv_gdn_prompt", "tv_gdn_prompt_front"]
 
 
 def _check(code: int, where: str):
@@ -230,6 +253,42 @@ class GdnLayer:
 
 def plan(split: int) -> tv_plan:
     return tv_plan(split)
+
+
+class Prompt:
+    """Device buffers of a tv_prompt for the given rows per sequence.
+    n_total and n_max may be larger than the rows need (padding behind the
+    last sequence, a graph's bounds); set_rows writes another batch's offsets
+    into the same buffer."""
+
+    def __init__(self, rows, device="cuda", n_total: int | None = None, n_max: int | None = None):
+        off = self._offsets(rows)
+        self.n_seq = len(rows)
+        self.n_total = off[-1] if n_total is None else n_total
+        self.n_max = max(rows) if n_max is None else n_max
+        self.row_off = torch.tensor(off, dtype=torch.int32, device=device)
+        self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        self.c = tv_prompt(self.n_seq, self.n_total, self.n_max, self.row_off.data_ptr(), self.status.data_ptr())
+
+    @staticmethod
+    def _offsets(rows):
+        off = [0]
+        for n in rows:
+            off.append(off[-1] + int(n))
+        return off
+
+    def set_rows(self, rows):
+        off = self._offsets(rows)
+        if len(rows) != self.n_seq or off[-1] > self.n_total or (rows and max(rows) > self.n_max):
+            raise ValueError(f"rows {rows} do not fit {self.n_seq} sequences, {self.n_total} rows, {self.n_max} each")
+        self.row_off.copy_(torch.tensor(off, dtype=torch.int32))
+
+    def counts(self) -> torch.Tensor:
+        """Rows of each sequence, on the device (tv_len_advance's `by`)."""
+        return (self.row_off[1:] - self.row_off[:-1]).contiguous()
+
+    def status_code(self) -> int:
+        return int(self.status[0].item())
 
 
 # ---------------------------------------------------------------------------
@@ -386,6 +445,95 @@ def tv_decode_step(pl, attn: AttnLayer | None, gdn: GdnLayer | None, n_seq, len_
 
 def tv_len_advance(len_, by, inc: int, n_seq: int, stream=None):
     _check(lib().tv_len_advance(_ptr(len_), _ptr(by), inc, n_seq, _stream(stream)), "tv_len_advance")
+
+
+# ---------------------------------------------------------------------------
+# prompts
+# ---------------------------------------------------------------------------
+def _need(where: str, **tensors):
+    """Raises where a buffer is not what the C side will take it for: each
+    value is (tensor, dtype, elements); the memory must be contiguous, on a
+    GPU, and hold at least that many elements."""
+    for name, (t, dtype, n) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype or not t.is_contiguous() or not t.is_cuda or t.numel() < n:
+            raise ValueError(f"{where}: {name} must be a contiguous {dtype} GPU tensor of at least {n} elements, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _ws_bytes(ws) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def tv_attn_norm_rope(layer: AttnLayer, tree: Tree | None, n_seq, len_, max_len, q_norm, k_norm, eps, rot_dims, theta,
+                      q_raw, k_raw, q, k, status=None, stream=None):
+    """Head norms and rotation of one layer's query and key rows (positions as in tv_attn_rope)."""
+    c, dt = layer.c, layer.K[0].dtype
+    n = tree.n_total if tree is not None else n_seq
+    nq, nk = n * c.Hq * c.D, n * c.Hkv * c.D
+    _need("tv_attn_norm_rope", len=(len_, torch.int32, tree.n_seq if tree is not None else n_seq),
+          q_norm=(q_norm, torch.float32, c.D), k_norm=(k_norm, torch.float32, c.D), q_raw=(q_raw, dt, nq),
+          k_raw=(k_raw, dt, nk), q=(q, dt, nq), k=(k, dt, nk))
+    _check(lib().tv_attn_norm_rope(ctypes.byref(c), ctypes.byref(tree.c) if tree is not None else None, n_seq,
+                                   _ptr(len_), max_len, _ptr(q_norm), _ptr(k_norm), eps, rot_dims, theta, _ptr(q_raw),
+                                   _ptr(k_raw), _ptr(q), _ptr(k), _ptr(status), _stream(stream)), "tv_attn_norm_rope")
+
+
+def tv_attn_prompt_front(layer: AttnLayer, prompt: Prompt, len_, max_len, q_norm, k_norm, eps, rot_dims, theta, q_raw,
+                         k_raw, v, q, stream=None):
+    """Head norms and rotation of a prompt's rows; keys and values go into the caches."""
+    c, dt, n = layer.c, layer.K[0].dtype, prompt.n_total
+    nq, nk = n * c.Hq * c.D, n * c.Hkv * c.D
+    _need("tv_attn_prompt_front", len=(len_, torch.int32, prompt.n_seq), q_norm=(q_norm, torch.float32, c.D),
+          k_norm=(k_norm, torch.float32, c.D), q_raw=(q_raw, dt, nq), k_raw=(k_raw, dt, nk), v=(v, dt, nk),
+          q=(q, dt, nq))
+    _check(lib().tv_attn_prompt_front(ctypes.byref(c), ctypes.byref(prompt.c), _ptr(len_), max_len, _ptr(q_norm),
+                                      _ptr(k_norm), eps, rot_dims, theta, _ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(q),
+                                      _stream(stream)), "tv_attn_prompt_front")
+
+
+def tv_attn_prompt_workspace_bytes(layer: AttnLayer, prompt: Prompt, max_len: int) -> int:
+    return int(lib().tv_attn_prompt_workspace_bytes(ctypes.byref(layer.c), ctypes.byref(prompt.c), max_len))
+
+
+def tv_attn_prompt(layer: AttnLayer, prompt: Prompt, len_, max_len, q, gate, out, scale, ws, stream=None):
+    """Causal attention of a prompt's rows over the caches that hold them."""
+    c, dt = layer.c, layer.K[0].dtype
+    nq = prompt.n_total * c.Hq * c.D
+    _need("tv_attn_prompt", len=(len_, torch.int32, prompt.n_seq), q=(q, dt, nq), gate=(gate, dt, nq),
+          out=(out, dt, nq))
+    _check(lib().tv_attn_prompt(ctypes.byref(c), ctypes.byref(prompt.c), _ptr(len_), max_len, _ptr(q), _ptr(gate),
+                                _ptr(out), scale, _ptr(ws), _ws_bytes(ws), _stream(stream)), "tv_attn_prompt")
+
+
+def tv_gdn_prompt_workspace_bytes(layer: GdnLayer, prompt: Prompt) -> int:
+    return int(lib().tv_gdn_prompt_workspace_bytes(ctypes.byref(layer.c), ctypes.byref(prompt.c)))
+
+
+def tv_gdn_prompt(layer: GdnLayer, prompt: Prompt, q, k, v, alpha, beta, out, scale, ws, stream=None):
+    """The gated delta rule over a prompt's rows; the states advance in place."""
+    c, n = layer.c, prompt.n_total
+    dt = torch.bfloat16 if c.dtype == TV_BF16 else torch.float32
+    nk, nv, nh = n * c.Hk * c.dk, n * c.Hv * c.dv, n * c.Hv
+    _need("tv_gdn_prompt", q=(q, dt, nk), k=(k, dt, nk), v=(v, dt, nv), alpha=(alpha, torch.float32, nh),
+          beta=(beta, torch.float32, nh), out=(out, dt, nv))
+    _check(lib().tv_gdn_prompt(ctypes.byref(c), ctypes.byref(prompt.c), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha),
+                               _ptr(beta), _ptr(out), scale, _ptr(ws), _ws_bytes(ws), _stream(stream)),
+           "tv_gdn_prompt")
+
+
+def tv_gdn_prompt_front(layer: GdnFrontLayer, prompt: Prompt, x, a_raw, b_raw, q, k, v, alpha, beta, stream=None):
+    """The GDN front end over a prompt's rows; the convolution tails advance."""
+    c, n = layer.c, prompt.n_total
+    dt = torch.bfloat16 if c.dtype == TV_BF16 else torch.float32
+    nk, nv, nh = n * c.Hk * c.dk, n * c.Hv * c.dv, n * c.Hv
+    _need("tv_gdn_prompt_front", x=(x, dt, 2 * nk + nv), a_raw=(a_raw, torch.float32, nh),
+          b_raw=(b_raw, torch.float32, nh), q=(q, dt, nk), k=(k, dt, nk), v=(v, dt, nv),
+          alpha=(alpha, torch.float32, nh), beta=(beta, torch.float32, nh))
+    _check(lib().tv_gdn_prompt_front(ctypes.byref(c), ctypes.byref(prompt.c), _ptr(x), _ptr(a_raw), _ptr(b_raw),
+                                     _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _stream(stream)),
+           "tv_gdn_prompt_front")
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,214 @@
+// Gated DeltaNet front end over a prompt's packed rows: the short convolution
+// along each sequence (continuing from its committed tail), SiLU, the q/k head
+// norms and the gates; then the tails move on to the sequence's last W-1 raw
+// inputs.  Formulas as in front_gdn.cu.
+//
+// Bound by HBM: every raw channel is read once and written once.  A group of
+// DH/8 lanes owns one head (eight consecutive channels a lane, one 16-byte
+// access a row) and walks kRows consecutive rows, keeping the W-1 rows before
+// the current one in registers; only a strip's first W-1 rows are read twice
+// (by this strip and the one before it).  Taps run in fp32 in order, oldest
+// first, as in the tree and decode forms.
+#include "prompt.cuh"
+#include "front_gdn.cuh"
+#include "launchers.hpp"
+
+namespace tv {
+
+struct GdnPromptFrontParams {
+  PromptRows pr;
+  const void* x;
+  const float* a_raw;
+  const float* b_raw;
+  void* q;
+  void* k;
+  void* v;
+  float* alpha;
+  float* beta;
+  const float* wconv;
+  void* tail[TV_MAX_SEQ];
+  int Hk, Hv, C, W, rows, strips, head_warps;
+};
+
+// WT: the width, or 0 for any width up to kMaxConvWidth.
+template <typename T, int DH, int WT>
+__global__ void __launch_bounds__(128) gdn_prompt_front_kernel(const __grid_constant__ GdnPromptFrontParams p) {
+  constexpr int LPH = DH / 8, HPW = 32 / LPH;  // lanes a head, heads a warp
+  constexpr int WM = WT ? WT : kMaxConvWidth;
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  if (status_bad(p.pr.status)) return;
+  const WarpSeqs w = load_seqs(p.pr, lane);
+  if (w.code) {
+    if (lane == 0) set_status(p.pr.status, w.code);
+    return;
+  }
+  const int n_live = __shfl_sync(0xffffffffu, w.off, p.pr.n_seq);
+  const int64_t conv_warps = static_cast<int64_t>(p.strips) * p.head_warps;
+  if (warp >= conv_warps) {  // gates: a thread a (row, value head)
+    const int64_t i = (warp - conv_warps) * 32 + lane;
+    if (i < static_cast<int64_t>(n_live) * p.Hv) front_gates(p.a_raw[i], p.b_raw[i], p.alpha[i], p.beta[i]);
+    return;
+  }
+  const int W = WT ? WT : p.W;
+  const int units = 2 * p.Hk + p.Hv;
+  const int u = static_cast<int>(warp % p.head_warps) * HPW + lane / LPH;
+  const bool act = u < units;
+  const int c0 = (act ? u : 0) * DH + (lane % LPH) * 8;  // dk = dv = DH: head u's channels start at u * DH
+  const int r0 = static_cast<int>(warp / p.head_warps) * p.rows;
+  const int r1 = min(r0 + p.rows, n_live);
+  if (r0 >= r1) return;
+  float tap[WM][8];  // tap[j] of channel c0 + e: wconv[c0 + e][j]
+#pragma unroll
+  for (int e = 0; e < 8; e++)
+#pragma unroll
+    for (int j = 0; j < WM; j++) tap[j][e] = j < W ? p.wconv[static_cast<size_t>(c0 + e) * W + j] : 0.f;
+  const T* x = static_cast<const T*>(p.x) + c0;
+  const bool norm = u < 2 * p.Hk;
+  T* dst;
+  size_t dstride;
+  if (u < p.Hk) {
+    dst = static_cast<T*>(p.q) + c0;
+    dstride = static_cast<size_t>(p.Hk) * DH;
+  } else if (u < 2 * p.Hk) {
+    dst = static_cast<T*>(p.k) + (c0 - p.Hk * DH);
+    dstride = static_cast<size_t>(p.Hk) * DH;
+  } else {
+    dst = static_cast<T*>(p.v) + (c0 - 2 * p.Hk * DH);
+    dstride = static_cast<size_t>(p.Hv) * DH;
+  }
+  int s = seq_of(w, p.pr, lane, r0);
+  int off = __shfl_sync(0xffffffffu, w.off, s), end = __shfl_sync(0xffffffffu, w.end, s);
+  float win[WM][8];  // win[j]: the input j - (W-1) rows from the current one
+  bool fresh = true;
+  for (int r = r0; r < r1; r++) {
+    if (r >= end) {  // the next sequence that has rows
+      s = seq_of(w, p.pr, lane, r);
+      off = __shfl_sync(0xffffffffu, w.off, s);
+      end = __shfl_sync(0xffffffffu, w.end, s);
+      fresh = true;
+    }
+    if (fresh) {
+      fresh = false;
+      const T* tail = static_cast<const T*>(p.tail[s]);
+#pragma unroll
+      for (int j = 0; j < WM - 1; j++)
+        if (j < W - 1) {
+          const int m = r - off + j - (W - 1);  // row of the sequence, negative: in the tail
+          load8(m >= 0 ? x + static_cast<size_t>(off + m) * p.C : tail + static_cast<size_t>(m + W - 1) * p.C + c0, win[j]);
+        }
+    }
+    float cur[8];
+    load8(x + static_cast<size_t>(r) * p.C, cur);
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) y[e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < WM; j++)
+      if (j < W) {
+#pragma unroll
+        for (int e = 0; e < 8; e++) y[e] = __fmaf_rn(tap[j][e], (j == W - 1) ? cur[e] : win[j][e], y[e]);
+      }
+    // move the window on
+#pragma unroll
+    for (int j = 0; j < WM - 1; j++)
+      if (j < W - 1) {
+#pragma unroll
+        for (int e = 0; e < 8; e++) win[j][e] = (j == W - 2) ? cur[e] : win[j + 1 < WM - 1 ? j + 1 : j][e];
+      }
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      y[e] = silu_f(y[e]);
+      ss = __fmaf_rn(y[e], y[e], ss);
+    }
+#pragma unroll
+    for (int o = LPH / 2; o >= 1; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+    if (norm) {
+      const float sc = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(ss, kNormEps)));
+#pragma unroll
+      for (int e = 0; e < 8; e++) y[e] = __fmul_rn(y[e], sc);
+    }
+    if (act) store8(dst + static_cast<size_t>(r) * dstride, y);
+  }
+}
+
+// One thread per (sequence, channel), after every read of the old tails.
+template <typename T>
+__global__ void __launch_bounds__(256) gdn_prompt_tail_kernel(const __grid_constant__ GdnPromptFrontParams p) {
+  const int lane = threadIdx.x & 31;
+  if (status_bad(p.pr.status)) return;
+  const WarpSeqs w = load_seqs(p.pr, lane);
+  if (w.code) return;  // reported by the first kernel
+  const int s = blockIdx.y;
+  const int off = __shfl_sync(0xffffffffu, w.off, s), n = __shfl_sync(0xffffffffu, w.end, s) - off;
+  const int c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= p.C || n <= 0) return;
+  T* tail = static_cast<T*>(p.tail[s]);
+  const T* x = static_cast<const T*>(p.x);
+  const int W1 = p.W - 1;
+  // ascending: row r comes from row r + n of the old tail (still unwritten) or from the prompt
+  for (int r = 0; r < W1; r++) {
+    const int m = n + r - W1;  // row of the sequence
+    tail[static_cast<size_t>(r) * p.C + c] =
+        m >= 0 ? x[static_cast<size_t>(off + m) * p.C + c] : tail[static_cast<size_t>(r + n) * p.C + c];
+  }
+}
+
+template <typename T, int DH>
+static void launch_prompt_front(const GdnPromptFrontParams& p, unsigned grid, cudaStream_t st) {
+  if (p.W == 4) gdn_prompt_front_kernel<T, DH, 4><<<grid, 128, 0, st>>>(p);
+  else gdn_prompt_front_kernel<T, DH, 0><<<grid, 128, 0, st>>>(p);
+}
+
+}  // namespace tv
+
+using namespace tv;
+
+extern "C" tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* f, const tv_prompt* pr, const void* x,
+                                         const float* a_raw, const float* b_raw, void* q, void* k, void* v,
+                                         float* alpha, float* beta, tv_stream stream) {
+  if (!f || !prompt_ok(pr)) return TV_ERR_ARG;
+  if (f->dtype != TV_F32 && f->dtype != TV_BF16) return TV_ERR_DTYPE;
+  if (!front_layer_ok(f) || f->Hk > 4096 || f->Hv > 4096) return TV_ERR_SHAPE;
+  GdnPromptFrontParams p{};
+  for (int s = 0; s < pr->n_seq; s++) {
+    if (f->width > 1 && !f->tail[s]) return TV_ERR_ARG;
+    if (!aligned16(f->tail[s])) return TV_ERR_ALIGN;
+    p.tail[s] = f->tail[s];
+  }
+  if (pr->n_total == 0) return TV_OK;
+  if (!x || !a_raw || !b_raw || !q || !k || !v || !alpha || !beta) return TV_ERR_ARG;
+  if (!aligned16(x) || !aligned16(a_raw) || !aligned16(b_raw) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+      !aligned16(alpha) || !aligned16(beta) || !aligned16(f->wconv))
+    return TV_ERR_ALIGN;
+  p.pr = prompt_rows(pr, nullptr, 0, 0);
+  p.x = x; p.a_raw = a_raw; p.b_raw = b_raw; p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.beta = beta;
+  p.wconv = f->wconv;
+  p.Hk = f->Hk; p.Hv = f->Hv; p.W = f->width;
+  p.C = 2 * f->Hk * f->dk + f->Hv * f->dv;
+  const int hpw = 256 / f->dk;
+  p.head_warps = (2 * f->Hk + f->Hv + hpw - 1) / hpw;
+  // rows a warp walks: 32 with many rows (a strip reads W-1 rows twice), fewer
+  // while the launch would not fill the SMs
+  p.rows = 32;
+  while (p.rows > 1 && static_cast<int64_t>((pr->n_total + p.rows - 1) / p.rows) * p.head_warps < 16 * num_sms()) p.rows >>= 1;
+  p.strips = (pr->n_total + p.rows - 1) / p.rows;
+  const int64_t warps = static_cast<int64_t>(p.strips) * p.head_warps + (static_cast<int64_t>(pr->n_total) * f->Hv + 31) / 32;
+  const int64_t grid = (warps + 3) / 4;
+  if (grid > 0x7fffffff) return TV_ERR_SHAPE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = f->dtype == TV_BF16;
+  const unsigned g = static_cast<unsigned>(grid);
+  if (f->dk == 128) {
+    if (bf) launch_prompt_front<__nv_bfloat16, 128>(p, g, st); else launch_prompt_front<float, 128>(p, g, st);
+  } else {
+    if (bf) launch_prompt_front<__nv_bfloat16, 64>(p, g, st); else launch_prompt_front<float, 64>(p, g, st);
+  }
+  if (f->width > 1) {
+    const dim3 tg((p.C + 255) / 256, pr->n_seq);
+    if (bf) gdn_prompt_tail_kernel<__nv_bfloat16><<<tg, 256, 0, st>>>(p);
+    else gdn_prompt_tail_kernel<float><<<tg, 256, 0, st>>>(p);
+  }
+  return launch_status();
+}
