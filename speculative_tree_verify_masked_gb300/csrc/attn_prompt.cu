@@ -1,5 +1,6 @@
-// Causal grouped-query attention over a prompt's packed rows, on the CUDA
-// cores.  Row i of a sequence sees cache rows 0 .. len + i (the prompt's own
+// Causal grouped-query attention over a prompt's packed rows: the entry point,
+// and the fp32 path on the CUDA cores (bf16 runs on the tensor cores,
+// attn_prompt_tc.cu).  Row i of a sequence sees cache rows 0 .. len + i (the prompt's own
 // keys and values are already in the cache).
 //
 // A CTA owns kRows consecutive (token, query head) rows of one KV head, token
@@ -164,19 +165,26 @@ static tv_status launch_cuda_d(const AttnPromptCudaParams& p, int D, cudaStream_
 
 using namespace tv;
 
+static tv_status prompt_layer_check(const tv_attn_layer* l, int32_t max_len) {
+  if (l->dtype != TV_F32 && l->dtype != TV_BF16) return TV_ERR_DTYPE;
+  if (l->Hq < 1 || l->Hkv < 1 || l->Hq % l->Hkv || l->Hq > 4096 || l->Hq / l->Hkv > 128 ||
+      (l->D != 64 && l->D != 128 && l->D != 256))
+    return TV_ERR_SHAPE;
+  return l->cap < 1 || max_len < 0 || max_len > l->cap ? TV_ERR_ARG : TV_OK;
+}
+
 extern "C" size_t tv_attn_prompt_workspace_bytes(const tv_attn_layer* l, const tv_prompt* pr, int32_t max_len) {
-  return 0;
+  if (!l || !prompt_ok(pr) || prompt_layer_check(l, max_len) != TV_OK || l->dtype != TV_BF16) return 0;
+  return attn_prompt_tc_ws_bytes(l, pr, max_len);
 }
 
 extern "C" tv_status tv_attn_prompt(const tv_attn_layer* l, const tv_prompt* pr, const int32_t* len, int32_t max_len,
                                     const void* q, const void* gate, void* out, float scale, void* ws,
                                     size_t ws_bytes, tv_stream stream) {
   if (!l || !prompt_ok(pr) || !len || !l->K || !l->V) return TV_ERR_ARG;
-  if (l->dtype != TV_F32 && l->dtype != TV_BF16) return TV_ERR_DTYPE;
-  if (l->Hq < 1 || l->Hkv < 1 || l->Hq % l->Hkv || l->Hq > 4096 || l->Hq / l->Hkv > 128 ||
-      (l->D != 64 && l->D != 128 && l->D != 256))
-    return TV_ERR_SHAPE;
-  if (l->cap < 1 || max_len < 0 || max_len > l->cap || !(scale > 0.f) || !std::isfinite(scale)) return TV_ERR_ARG;
+  const tv_status c = prompt_layer_check(l, max_len);
+  if (c != TV_OK) return c;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return TV_ERR_ARG;
   AttnPromptCudaParams p{};
   for (int s = 0; s < pr->n_seq; s++) {
     if (!l->K[s] || !l->V[s]) return TV_ERR_ARG;
@@ -189,6 +197,8 @@ extern "C" tv_status tv_attn_prompt(const tv_attn_layer* l, const tv_prompt* pr,
   if (!q || !out) return TV_ERR_ARG;
   if (!aligned16(q) || !aligned16(gate) || !aligned16(out)) return TV_ERR_ALIGN;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (l->dtype == TV_BF16)
+    return attn_prompt_tc_launch(AttnPromptCall{l, pr, len, max_len, q, gate, out, scale, ws, ws_bytes}, st);
   p.pr = prompt_rows(pr, len, max_len, l->cap);
   p.q = q;
   p.gate = gate;
@@ -196,6 +206,5 @@ extern "C" tv_status tv_attn_prompt(const tv_attn_layer* l, const tv_prompt* pr,
   p.Hq = l->Hq;
   p.Hkv = l->Hkv;
   p.c = scale * 1.4426950408889634f;
-  if (l->dtype == TV_BF16) return launch_cuda_d<__nv_bfloat16>(p, l->D, st);
   return launch_cuda_d<float>(p, l->D, st);
 }

@@ -16,4 +16,20 @@ struct AttnPromptCudaParams {
   float c;  // scale * log2(e)
 };
 
+// One tv_attn_prompt call whose arguments have been checked.
+struct AttnPromptCall {
+  const tv_attn_layer* layer;
+  const tv_prompt* prompt;
+  const int32_t* len;
+  int max_len;
+  const void* q;
+  const void* gate;
+  void* out;
+  float scale;
+  void* ws;
+  size_t ws_bytes;
+};
+tv_status attn_prompt_tc_launch(const AttnPromptCall& a, cudaStream_t st);
+size_t attn_prompt_tc_ws_bytes(const tv_attn_layer* l, const tv_prompt* pr, int max_len);
+
 }  // namespace tv

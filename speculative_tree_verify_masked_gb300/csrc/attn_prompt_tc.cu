@@ -1,0 +1,754 @@
+// Causal grouped-query attention over a prompt's packed rows for bf16 caches,
+// on the tcgen05 tensor cores.
+//
+// Row i of a sequence sees cache rows 0 .. len + i.  The rows of one KV head
+// are taken token major, the G query heads that share it side by side, so a
+// row tile of 128 holds T = 128 / G tokens (rows past T * G idle) and every
+// key and value tile serves all of them.  An item is one row tile of one KV
+// head against its keys; it runs flash style over key tiles of 128 positions:
+//   S = Q K^T (tensor core, fp32), m = running maximum of scaled scores,
+//   p = 2^(s c - m) rounded to bf16, l += sum of the rounded p,
+//   O = O 2^(m_old - m) + P V (tensor core, fp32), out = O / l (times the gate).
+// The maximum moves only when a tile exceeds it by more than 8 in log2 units
+// (p then stays below 2^8), so O is rescaled rarely.  p is rounded to bf16
+// because the tensor cores take P and V in one type; l adds the same rounded
+// values, so the weights still sum to one.
+//
+// Roles (320 threads, one CTA per SM, persistent).  Warp 0 streams key and
+// value units by TMA through one ring in the order the tensor core takes
+// them: K0, K1 V0, K2 V1, ...  Warp 1 issues the MMAs in that order from one
+// thread.  Warps 2-9 do the softmax, two threads to a row (64 columns each).
+// Tensor memory holds O [D columns], one S [128] and Q [D/2, the A operand of
+// Q K^T], 512 columns at D = 256; P goes through shared memory.  Because PV of
+// tile t-1 sits between Q K^T of t and of t+1 on the tensor pipe, S(t) is read
+// out during that PV and one S buffer is enough, and the softmax has two
+// products' time before PV(t) wants P(t).
+//
+// Masked places.  Scores of positions a row does not see are replaced, not
+// added to, so what the cache holds there (NaN, infinity) cannot pass.  In PV
+// a zero weight would still meet the value: value rows behind the sequence's
+// last position are zeroed in shared memory before the last tile's PV.
+//
+// Work split.  All CTAs derive the same plan from the device-side offsets and
+// lengths: items in order of falling length, dealt back and forth over the
+// workers; where there are too few of them (short prompts behind a long
+// context) each is cut along its keys into pieces of S tiles, whose O, m and l
+// go to the workspace as fp32 and are joined by a second kernel.
+#include <cmath>
+#include <cstring>
+
+#include "attn_prompt.cuh"
+#include "attn_shared.cuh"
+#include "ptx.cuh"
+
+namespace tv {
+
+constexpr int kKeyTile = 128;
+constexpr float kMoveMax = 8.f;
+constexpr int kPieceTiles = 2;     // shortest piece of a split item
+constexpr int kSlotsPerSm = 12;    // workspace records (pieces) per SM, at most
+
+struct PromptPlan {
+  int total, S;
+  int seq[TV_MAX_SEQ];                                       // sequences in order of falling key tiles
+  int cum[TV_MAX_SEQ + 1], slot0[TV_MAX_SEQ];                // by place in that order
+  int off[TV_MAX_SEQ], n[TV_MAX_SEQ], L[TV_MAX_SEQ], rt[TV_MAX_SEQ], pm[TV_MAX_SEQ];  // by sequence
+};
+
+template <int D, bool PAIR>
+struct Pa {
+  static constexpr int NC = PAIR ? 2 : 1;                   // CTAs that share an item
+  static constexpr int UPT = (!PAIR && D == 256) ? 2 : 1;   // ring units per key (or value) tile and CTA
+  static constexpr int UNIT = kKeyTile * D * 2 / NC / UPT;  // bytes of a unit
+  static constexpr int NU = PAIR ? (D == 256 ? 6 : 10) : (D == 64 ? 10 : 6);
+  static constexpr int KROWS = kKeyTile / NC;               // key rows of a K box
+  static constexpr int KBOX = KROWS * 128;                  // bytes of a K box (64 columns)
+  static constexpr int KBU = D / 64 / UPT;                  // K boxes per unit
+  static constexpr int VROWS = kKeyTile / UPT;              // positions of a V box
+  static constexpr int VBOX = VROWS * 128;
+  static constexpr int VB = D / 64 / NC;                    // V boxes per unit
+  static constexpr int PT = 128 * kKeyTile * 2;
+  static constexpr int T_O = 0, T_S = D, T_Q = D + 128;
+  static constexpr int COLS = D + 128 + D / 2 <= 256 ? 256 : 512;
+  static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128 * NC, kKeyTile, false, false);
+  static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128 * NC, D, false, true);
+  static constexpr int XOFF = NU * UNIT + PT;               // half-row maxima [2][2][128] fp32
+  static constexpr int BOFF = XOFF + 2 * 2 * 128 * 4;
+  static constexpr int NBAR = 2 * NU + 6 + 4 + 1;
+  static constexpr int LOFF = (BOFF + NBAR * 8 + 15) / 16 * 16;  // TMEM base, give-up flag, skip flag, plan
+  static constexpr int SMEM = LOFF + 16 + static_cast<int>(sizeof(PromptPlan));
+  static_assert(KBU * KBOX == UNIT && VB * VBOX == UNIT, "unit shape");
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct AttnPromptTcParams {
+  CUtensorMap tmK[TV_MAX_SEQ];
+  CUtensorMap tmV[TV_MAX_SEQ];
+  PromptRows pr;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* gate;
+  __nv_bfloat16* out;
+  float* ws;
+  int Hq, Hkv, G, T, TP;  // T tokens per CTA's row tile, TP per item
+  int workers, slots;
+  float c;  // scale * log2(e)
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// The plan, by one warp.  Cost of a candidate, in key tiles: the waves of
+// pieces at their mean length, the longest piece's overhang, about three tiles
+// to start and end a piece and four more to write and join a partial one.
+__device__ inline void make_plan(const AttnPromptTcParams& p, const WarpSeqs& w, int lane, PromptPlan& pl) {
+  const int n = w.end - w.off;
+  const bool live = lane < p.pr.n_seq && n > 0;
+  const int rt = live ? ceil_div(n, p.TP) : 0;
+  const int nk = live ? ceil_div(w.len + n, kKeyTile) : 0;
+  const int nk0 = live ? ceil_div(w.len + min(n, p.TP), kKeyTile) : 0;
+  int nkmax = nk;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) nkmax = max(nkmax, __shfl_xor_sync(0xffffffffu, nkmax, o));
+  const int wide = lane < 16 ? lane + 1 : 0;
+  // pieces of the longest item to try: 1 .. 16, then in steps of about a fifth
+  int cand = wide ? wide : static_cast<int>(16.f * exp2f((lane - 15) * 0.25f));
+  int S = max(max(ceil_div(nkmax, cand), kPieceTiles), 1);
+  float W = 0.f, P = 0.f, part = 0.f, longest = 0.f;
+  for (int s = 0; s < p.pr.n_seq; s++) {
+    const int r = __shfl_sync(0xffffffffu, rt, s), k1 = __shfl_sync(0xffffffffu, nk, s),
+              k0 = __shfl_sync(0xffffffffu, nk0, s);
+    if (r == 0) continue;
+    const float items = static_cast<float>(p.Hkv) * r;
+    const int pm = ceil_div(k1, S);
+    W += items * 0.5f * (k0 + k1);
+    P += items * pm;
+    if (pm > 1) part += items * pm;
+    longest = fmaxf(longest, static_cast<float>(min(S, k1)));
+  }
+  const float mean = W / fmaxf(P, 1.f);
+  float cost = ceilf(P / p.workers) * (mean + 3.f) + 0.5f * (longest - mean) + 4.f * part / p.workers;
+  if (part > static_cast<float>(p.slots)) cost = INFINITY;  // lane 0 (one piece) always fits
+  int best = lane;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    const float c2 = __shfl_xor_sync(0xffffffffu, cost, o);
+    const int b2 = __shfl_xor_sync(0xffffffffu, best, o);
+    if (c2 < cost || (c2 == cost && b2 < best)) {
+      cost = c2;
+      best = b2;
+    }
+  }
+  S = __shfl_sync(0xffffffffu, S, best);
+  const int pm = live ? ceil_div(nk, S) : 0;
+  if (lane < TV_MAX_SEQ) {
+    pl.off[lane] = w.off;
+    pl.n[lane] = n;
+    pl.L[lane] = w.len;
+    pl.rt[lane] = rt;
+    pl.pm[lane] = pm;
+    // place in the order: longer sequences (ties: earlier ones) come first
+  }
+  int place = 0;
+  for (int s = 0; s < p.pr.n_seq; s++) {
+    const int k2 = __shfl_sync(0xffffffffu, nk, s);
+    if (k2 > nk || (k2 == nk && s < lane)) place++;
+  }
+  if (lane < p.pr.n_seq) pl.seq[place] = lane;
+  __syncwarp();
+  if (lane == 0) {
+    pl.S = S;
+    int cum = 0, slot = 0;
+    for (int i = 0; i < p.pr.n_seq; i++) {
+      const int s = pl.seq[i];
+      pl.cum[i] = cum;
+      pl.slot0[i] = slot;
+      const int cnt = pl.rt[s] * p.Hkv * pl.pm[s];
+      cum += cnt;
+      if (pl.pm[s] > 1) slot += cnt;
+    }
+    pl.cum[p.pr.n_seq] = cum;
+    pl.total = cum;
+  }
+  __syncwarp();
+}
+
+struct PromptItem {
+  int s, g, i, t0, t1, slot;  // key tiles [t0, t1); slot -1: the item is whole
+};
+// Piece x of the plan (pieces past a shorter item's end are empty: t0 >= t1).
+__device__ __forceinline__ PromptItem item_of(const AttnPromptTcParams& p, const PromptPlan& pl, int x) {
+  int at = 0;
+  while (at < p.pr.n_seq - 1 && x >= pl.cum[at + 1]) at++;
+  PromptItem I;
+  I.s = pl.seq[at];
+  const int r = x - pl.cum[at], per = p.Hkv * pl.rt[I.s];
+  const int j = r / per, r2 = r % per;
+  I.i = pl.rt[I.s] - 1 - r2 / p.Hkv;  // longest row tiles first
+  I.g = r2 % p.Hkv;
+  const int nk = ceil_div(pl.L[I.s] + min((I.i + 1) * p.TP, pl.n[I.s]), kKeyTile);
+  I.t0 = j * pl.S;
+  I.t1 = min(I.t0 + pl.S, nk);
+  I.slot = nk > pl.S ? pl.slot0[at] + r : -1;
+  return I;
+}
+// The x-th piece of a worker: waves run back and forth over the workers, so
+// the one that got the longest piece of a wave gets the shortest of the next.
+__device__ __forceinline__ int piece_index(int wave, int worker, int workers) {
+  return wave * workers + ((wave & 1) ? workers - 1 - worker : worker);
+}
+
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_constant__ AttnPromptTcParams p) {
+  using C = Pa<D, PAIR>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];  // tiles are swizzled in 1024-byte atoms
+  uint8_t* gb = smem_raw;
+  const uint32_t sb = smem_u32(smem_raw);
+  const uint32_t ring = sb, pbuf = sb + C::NU * C::UNIT;
+  float* xmax = reinterpret_cast<float*>(gb + C::XOFF);
+  const uint32_t bars = sb + C::BOFF;
+  const uint32_t UFULL0 = bars, UEMPTY0 = bars + 8u * C::NU;
+  const uint32_t SFULL = bars + 16u * C::NU, SFREE = SFULL + 8u, PFULL = SFULL + 16u, ODONE = SFULL + 24u,
+                 QREADY = SFULL + 32u, VTAIL = SFULL + 40u, XBAR0 = SFULL + 48u, DRAIN = XBAR0 + 32u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + C::LOFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int& skip = *reinterpret_cast<int*>(tmem_slot + 2);
+  PromptPlan& pl = *reinterpret_cast<PromptPlan*>(gb + C::LOFF + 16);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const int worker = PAIR ? static_cast<int>(blockIdx.x) / 2 : static_cast<int>(blockIdx.x);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NU; i++) {
+      mbar_init(UFULL0 + 8u * i, 1);
+      mbar_init(UEMPTY0 + 8u * i, 1);
+    }
+    mbar_init(SFULL, 1);
+    mbar_init(SFREE, 8 * C::NC);
+    mbar_init(PFULL, 8 * C::NC);
+    mbar_init(ODONE, 1);
+    mbar_init(QREADY, 8 * C::NC);
+    mbar_init(VTAIL, 1);
+    for (int i = 0; i < 4; i++) mbar_init(XBAR0 + 8u * i, 2);
+    mbar_init(DRAIN, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {  // the plan; a bad launch sets its code and every CTA leaves
+    const bool bad = status_bad(p.pr.status);
+    const WarpSeqs w = load_seqs(p.pr, lane);
+    if (w.code && lane == 0) set_status(p.pr.status, w.code);
+    if (lane == 0) {
+      skip = bad || w.code || (sb & 1023u) ? 1 : 0;
+      if (sb & 1023u) set_status(p.pr.status, TV_ERR_CUDA);
+    }
+    if (!w.code) make_plan(p, w, lane, pl);
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), C::COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), C::COLS);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  // barriers that the issuing CTA (rank 0) waits on
+  const uint32_t rSFREE = PAIR ? map_to_cta(SFREE, 0) : SFREE, rPFULL = PAIR ? map_to_cta(PFULL, 0) : PFULL,
+                 rQREADY = PAIR ? map_to_cta(QREADY, 0) : QREADY;
+  auto arrive = [&](uint32_t bar) {  // one arrival per warp, after every lane's fences
+    __syncwarp();
+    if (lane == 0) {
+      if (PAIR) mbar_arrive_cluster(bar);
+      else mbar_arrive(bar);
+    }
+  };
+  const int total = skip ? 0 : pl.total;
+
+  if (warp == 0 && lane == 0) {
+    // ---------------- TMA producer ----------------
+    uint32_t it = 0, tails = 0;
+    bool ok = true;
+    for (int wave = 0; ok; wave++) {
+      if (wave * p.workers >= total) break;
+      const int x = piece_index(wave, worker, p.workers);
+      if (x >= total) continue;
+      const PromptItem I = item_of(p, pl, x);
+      if (I.t0 >= I.t1) continue;
+      const int n = I.t1 - I.t0, base = I.g * p.pr.cap, end = pl.L[I.s] + pl.n[I.s];
+      for (int e = 0; e < 2 * n && ok; e++) {
+        // load order K0, K1 V0, K2 V1, ..., V(n-1)
+        const bool is_k = e == 0 || ((e & 1) && e != 2 * n - 1);
+        const int k = e == 0 ? 0 : is_k ? (e + 1) / 2 : (e == 2 * n - 1 ? n - 1 : (e - 2) / 2);
+        const int pos = (I.t0 + k) * kKeyTile;
+        const bool tail = PAIR && !is_k && pos + kKeyTile > end;
+#pragma unroll
+        for (int u = 0; u < C::UPT; u++, it++) {
+          const uint32_t slot = it % C::NU;
+          if (!wait_role(UEMPTY0 + 8u * slot, ((it / C::NU) & 1) ^ 1, abort_flag, kWaitCycles)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = ring + slot * C::UNIT;
+          uint32_t full = UFULL0 + 8u * slot;
+          if (tail) {
+            // this CTA's softmax warps zero rows of the unit first: it lands on
+            // a barrier of their own, and their P arrival stands for it
+            if (rank == 0) mbar_arrive(full);
+            full = VTAIL;
+            mbar_arrive_expect_tx(full, C::UNIT);
+            tails++;
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(full, C::UNIT * C::NC);
+          }
+          const uint32_t rfull = PAIR ? map_to_cta(full, tail ? rank : 0) : full;
+          auto load = [&](uint32_t d, const CUtensorMap* m, int xx, int yy) {
+            if (PAIR) tma_load_2d_pair(d, m, rfull, xx, yy);
+            else tma_load_2d(d, m, rfull, xx, yy);
+          };
+          if (is_k) {
+#pragma unroll
+            for (int b = 0; b < C::KBU; b++)
+              load(dst + b * C::KBOX, &p.tmK[I.s], (u * C::KBU + b) * 64, base + pos + static_cast<int>(rank) * C::KROWS);
+          } else {
+#pragma unroll
+            for (int b = 0; b < C::VB; b++)
+              load(dst + b * C::VBOX, &p.tmV[I.s], (static_cast<int>(rank) * C::VB + b) * 64, base + pos + u * C::VROWS);
+          }
+        }
+      }
+    }
+    if (!ok) {
+      set_status(p.pr.status, TV_ERR_TIMEOUT);
+      // let every issued copy land before shared memory is released
+      if (rank == 0)
+        for (uint32_t i = it > C::NU ? it - C::NU : 0; i < it; i++)
+          mbar_wait(UFULL0 + 8u * (i % C::NU), (i / C::NU) & 1, kWaitCycles);
+      if (tails) mbar_wait(VTAIL, (tails - 1) & 1, kWaitCycles);
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------- MMA issuer: a whole-warp loop, one elected lane issues ----------------
+    uint32_t it = 0, t = 0, items = 0;  // units, tiles with an issued Q K^T, items
+    bool ok = true;
+    auto wait_in = [&](uint32_t bar, uint32_t par) {
+      return PAIR ? wait_warp_cluster(bar, par, abort_flag, kWaitCycles) : wait_warp(bar, par, abort_flag, kWaitCycles);
+    };
+    auto commit = [&](uint32_t bar) {
+      if (PAIR) tc_commit_pair(bar);
+      else tc_commit(bar);
+    };
+    auto do_qk = [&]() {
+      if (t > 0 && !wait_in(SFREE, (t - 1) & 1)) return false;
+#pragma unroll
+      for (int u = 0; u < C::UPT; u++, it++) {
+        const uint32_t slot = it % C::NU;
+        if (!wait_in(UFULL0 + 8u * slot, (it / C::NU) & 1)) return false;
+        tc_fence_after();
+        if (elect_one_sync()) {
+          const uint64_t k0 = sdesc_sw128(ring + slot * C::UNIT, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < C::KBU * 4; kk++) {
+            const uint64_t kd = k0 + static_cast<uint64_t>(((kk >> 2) * C::KBOX + (kk & 3) * 32) >> 4);
+            const uint32_t a = tbase + C::T_Q + (u * C::KBU * 4 + kk) * 8;
+            if (PAIR) tc_mma_ts_pair(tbase + C::T_S, a, kd, C::IDESC_QK, (u > 0 || kk > 0) ? 1u : 0u);
+            else tc_mma_ts(tbase + C::T_S, a, kd, C::IDESC_QK, (u > 0 || kk > 0) ? 1u : 0u);
+          }
+          commit(UEMPTY0 + 8u * slot);
+          if (u == C::UPT - 1) commit(SFULL);
+        }
+        __syncwarp();
+      }
+      t++;
+      return true;
+    };
+    uint32_t tp = 0;
+    auto do_pv = [&](bool acc) {
+      if (!wait_in(PFULL, tp & 1)) return false;
+#pragma unroll
+      for (int u = 0; u < C::UPT; u++, it++) {
+        const uint32_t slot = it % C::NU;
+        if (!wait_in(UFULL0 + 8u * slot, (it / C::NU) & 1)) return false;
+        tc_fence_after();
+        if (elect_one_sync()) {
+          const uint64_t v0 = sdesc_sw128(ring + slot * C::UNIT, C::VBOX, 1024);
+          const uint64_t p0 = sdesc_sw128(pbuf, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < C::VROWS / 16; kk++) {
+            const int pk = u * (C::VROWS / 16) + kk;  // 16-position step of the tile
+            const uint64_t pd = p0 + static_cast<uint64_t>(((pk >> 2) * 16384 + (pk & 3) * 32) >> 4);
+            const uint64_t vd = v0 + static_cast<uint64_t>((kk * 2048) >> 4);
+            const uint32_t on = (acc || pk > 0) ? 1u : 0u;
+            if (PAIR) tc_mma_ss_pair(tbase + C::T_O, pd, vd, C::IDESC_PV, on);
+            else tc_mma_ss(tbase + C::T_O, pd, vd, C::IDESC_PV, on);
+          }
+          commit(UEMPTY0 + 8u * slot);
+          if (u == C::UPT - 1) commit(ODONE);
+        }
+        __syncwarp();
+      }
+      tp++;
+      return true;
+    };
+    for (int wave = 0; ok; wave++) {
+      if (wave * p.workers >= total) break;
+      const int x = piece_index(wave, worker, p.workers);
+      if (x >= total) continue;
+      const PromptItem I = item_of(p, pl, x);
+      if (I.t0 >= I.t1) continue;
+      const int n = I.t1 - I.t0;
+      ok = wait_in(QREADY, items & 1);
+      items++;
+      if (ok) {
+        tc_fence_after();
+        ok = do_qk();
+      }
+      for (int k = 0; k < n && ok; k++) {
+        if (k + 1 < n) ok = do_qk();
+        if (ok) ok = do_pv(k > 0);
+      }
+    }
+    if (!ok && lane == 0) set_status(p.pr.status, TV_ERR_TIMEOUT);
+    // every MMA completes before tensor and shared memory are released
+    if (elect_one_sync()) {
+      if (PAIR) tc_commit_pair(DRAIN);
+      else tc_commit(DRAIN);
+    }
+    __syncwarp();
+    mbar_wait(DRAIN, 0, kWaitCycles);
+  } else if (warp >= 2) {
+    // ---------------- softmax and output, two threads to a row ----------------
+    const int hf = (warp - 2) >> 2, quad = warp & 3, lrow = quad * 32 + lane;
+    const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
+    const int tok = lrow / p.G, head = lrow % p.G;
+    uint32_t t = 0, xc = 0, tails = 0, it = 0;  // tiles, exchanges, zeroed value tiles, units before the item
+    bool ok = true;
+    // the two threads of a row exchange a value
+    auto exchange = [&](float v, float& other) {
+      float* x = xmax + (xc & 1) * 256;
+      x[hf * 128 + lrow] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(XBAR0 + 8u * quad);
+      if (!wait_warp(XBAR0 + 8u * quad, xc & 1, abort_flag, kWaitCycles)) return false;
+      other = x[(hf ^ 1) * 128 + lrow];
+      xc++;
+      return true;
+    };
+    for (int wave = 0; ok; wave++) {
+      if (wave * p.workers >= total) break;
+      const int x = piece_index(wave, worker, p.workers);
+      if (x >= total) continue;
+      const PromptItem I = item_of(p, pl, x);
+      if (I.t0 >= I.t1) continue;
+      const int n = I.t1 - I.t0, L = pl.L[I.s], end = L + pl.n[I.s];
+      const int token = I.i * p.TP + static_cast<int>(rank) * p.T + tok;
+      const bool act = tok < p.T && token < pl.n[I.s];
+      const int last = act ? L + token : -1;  // last position this row sees
+      const int seen_all = L + I.i * p.TP + static_cast<int>(rank) * p.T + 1;  // positions every row here sees
+      const size_t orow = act ? ((static_cast<size_t>(pl.off[I.s]) + token) * p.Hq + I.g * p.G + head) * D : 0;
+      {
+        uint4 qv[QShare<D>::N];
+        q_fetch<D>(act ? p.q + orow : nullptr, hf, qv);
+        q_store<D>(tl + C::T_Q, hf, qv);  // every Q K^T of the previous item has completed: its S was read
+        tmem_st_wait();
+        tc_fence_before();
+        arrive(rQREADY);
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < n; k++, t++) {
+        if (!wait_warp(SFULL, t & 1, abort_flag, kWaitCycles)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float sv[64];
+        {
+          uint32_t r[32];
+          tmem_ld32(tl + C::T_S + hf * 64, r);
+#pragma unroll
+          for (int i = 0; i < 32; i++) sv[i] = __uint_as_float(r[i]);
+          tmem_ld32(tl + C::T_S + hf * 64 + 32, r);
+#pragma unroll
+          for (int i = 0; i < 32; i++) sv[32 + i] = __uint_as_float(r[i]);
+        }
+        tc_fence_before();
+        arrive(rSFREE);
+        const int pos = (I.t0 + k) * kKeyTile;
+        if (pos + kKeyTile > seen_all) {  // a tile some row here does not see whole
+          const int vis = last - (pos + hf * 64);
+#pragma unroll
+          for (int j = 0; j < 64; j++) sv[j] = j <= vis ? sv[j] : -INFINITY;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 64; j++) mx[j & 3] = fmaxf(mx[j & 3], sv[j]);
+        float mo;
+        const float mh = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (!exchange(mh, mo)) {
+          ok = false;
+          break;
+        }
+        const float mt = __fmul_rn(fmaxf(mh, mo), p.c);
+        float alpha = 1.f;
+        if (mt > __fadd_rn(m, kMoveMax) || (m == -INFINITY && mt > -INFINITY)) {
+          alpha = ex2_approx(__fsub_rn(m, mt));  // 0 from m = -inf
+          m = mt;
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;  // nothing seen yet: every p below is 2^-inf = 0
+        uint32_t P[32];
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 64; j += 2) {
+          const uint32_t w = pack_bf16x2(ex2_approx(__fmaf_rn(sv[j], p.c, neg)), ex2_approx(__fmaf_rn(sv[j + 1], p.c, neg)));
+          P[j / 2] = w;
+          acc[(j / 2) & 3] = __fadd_rn(acc[(j / 2) & 3], __fadd_rn(bf16_lo(w), bf16_hi(w)));
+        }
+        l = __fmaf_rn(l, alpha, __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3])));
+        // PV of the previous tile is complete: P is free and O rests
+        if (t > 0 && !wait_warp(ODONE, (t - 1) & 1, abort_flag, kWaitCycles)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        {
+          const uint32_t line = pbuf + hf * 16384 + (lrow >> 3) * 1024 + (lrow & 7) * 128;
+#pragma unroll
+          for (int q = 0; q < 8; q++)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + (((q ^ lrow) & 7) << 4)), "r"(P[4 * q]),
+                         "r"(P[4 * q + 1]), "r"(P[4 * q + 2]), "r"(P[4 * q + 3])
+                         : "memory");
+        }
+        if (k > 0 && __any_sync(0xffffffffu, act && alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
+            uint32_t r[32];
+            tmem_ld32(tl + C::T_O + c, r);
+#pragma unroll
+            for (int i = 0; i < 32; i++) r[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[i]), alpha));
+            tmem_st32(tl + C::T_O + c, r);
+          }
+          tmem_st_wait();
+        }
+        if (pos + kKeyTile > end) {
+          // value rows behind the sequence's last position: zero them before
+          // PV (the last tile of the piece; its units follow the 2n-1 before)
+          const int first = end - pos;  // 1 .. 127
+          uint32_t slot[C::UPT];
+#pragma unroll
+          for (int u = 0; u < C::UPT; u++) {
+            const uint32_t i = it + (2 * n - 1) * C::UPT + u;
+            slot[u] = i % C::NU;
+            const bool landed = PAIR ? wait_warp(VTAIL, tails & 1, abort_flag, kWaitCycles)
+                                     : wait_warp(UFULL0 + 8u * slot[u], (i / C::NU) & 1, abort_flag, kWaitCycles);
+            ok = ok && landed;
+          }
+          tails++;
+          if (!ok) break;
+          for (int e = static_cast<int>(threadIdx.x) - 64; e < (kKeyTile - first) * C::VB * 8; e += 256) {
+            const int row = first + e / (C::VB * 8), c = e % (C::VB * 8);
+            const uint32_t a = ring + slot[C::UPT > 1 ? row / C::VROWS : 0] * C::UNIT + (c >> 3) * C::VBOX +
+                               (row % C::VROWS) * 128 + (c & 7) * 16;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        arrive(rPFULL);
+      }
+      it += 2 * n * C::UPT;
+      if (!ok) break;
+      float lo;
+      if (!exchange(l, lo) || !wait_warp(ODONE, (t - 1) & 1, abort_flag, kWaitCycles)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float inv = __fdiv_rn(1.f, __fadd_rn(l, lo));
+      float* rec = I.slot >= 0 ? p.ws + ((static_cast<size_t>(I.slot) * C::NC + rank) * 128 + lrow) * (D + 4) : nullptr;
+#pragma unroll 1
+      for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tl + C::T_O + c, r);
+        if (!act) continue;
+        if (rec) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(rec + c + i) = make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
+                                                                  __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+          continue;
+        }
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 32; i++) y[i] = __fmul_rn(__uint_as_float(r[i]), inv);
+        if (p.gate) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            float gv[8];
+            load8(p.gate + orow + c + i, gv);
+#pragma unroll
+            for (int e = 0; e < 8; e++) y[i + e] = gate_mul(y[i + e], gv[e]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          *reinterpret_cast<uint4*>(p.out + orow + c + i) =
+              make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]), pack_bf16x2(y[i + 4], y[i + 5]),
+                         pack_bf16x2(y[i + 6], y[i + 7]));
+      }
+      if (rec && act && hf == 0) {
+        rec[D] = m;
+        rec[D + 1] = __fadd_rn(l, lo);
+      }
+      tc_fence_before();
+    }
+    if (!ok && lane == 0) set_status(p.pr.status, TV_ERR_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync_all();  // no CTA's memory goes while the other still uses it
+  tc_fence_after();
+  if (warp == 1) {
+    if (PAIR) tmem_dealloc_pair(tbase, C::COLS);
+    else tmem_dealloc(tbase, C::COLS);
+  }
+}
+
+// Joins the pieces of split items: one warp a row, pieces in order.
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_constant__ AttnPromptTcParams p) {
+  constexpr int NC = PAIR ? 2 : 1, CPL = D / 32;
+  __shared__ PromptPlan pl;
+  __shared__ int skip;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  if (warp == 0) {
+    const bool bad = status_bad(p.pr.status);
+    const WarpSeqs w = load_seqs(p.pr, lane);
+    if (lane == 0) skip = bad || w.code ? 1 : 0;
+    if (!w.code) make_plan(p, w, lane, pl);
+  }
+  __syncthreads();
+  if (skip) return;
+  for (int at = 0; at < p.pr.n_seq; at++) {
+    const int s = pl.seq[at];
+    if (pl.pm[s] < 2) continue;
+    const int64_t rows = static_cast<int64_t>(pl.n[s]) * p.Hq;
+    for (int64_t x = static_cast<int64_t>(blockIdx.x) * 8 + warp; x < rows; x += static_cast<int64_t>(gridDim.x) * 8) {
+      const int token = static_cast<int>(x / p.Hq), h = static_cast<int>(x % p.Hq), g = h / p.G;
+      const int i = token / p.TP, rank = token % p.TP / p.T, lrow = (token % p.TP % p.T) * p.G + h % p.G;
+      const int nk = ceil_div(pl.L[s] + min((i + 1) * p.TP, pl.n[s]), kKeyTile);
+      const int np = ceil_div(nk, pl.S);
+      if (np < 2) continue;  // written whole
+      const int per = p.Hkv * pl.rt[s], first = pl.slot0[at] + (pl.rt[s] - 1 - i) * p.Hkv + g;
+      auto rec = [&](int j) {
+        return p.ws + ((static_cast<size_t>(first + j * per) * NC + rank) * 128 + lrow) * (D + 4);
+      };
+      float m = -INFINITY;
+      for (int j = lane; j < np; j += 32) m = fmaxf(m, rec(j)[D]);
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float l = 0.f, acc[CPL];
+#pragma unroll
+      for (int c = 0; c < CPL; c++) acc[c] = 0.f;
+#pragma unroll 4
+      for (int j = 0; j < np; j++) {
+        const float* r = rec(j);
+        const float mj = r[D];
+        const float f = mj == -INFINITY ? 0.f : exp2f(__fsub_rn(mj, m));
+        l = __fmaf_rn(f, r[D + 1], l);
+#pragma unroll
+        for (int c = 0; c < CPL; c++) acc[c] = __fmaf_rn(f, r[lane + 32 * c], acc[c]);
+      }
+      const size_t o = (static_cast<size_t>(pl.off[s]) * p.Hq + x) * D;
+      const float inv = __fdiv_rn(1.f, l);
+#pragma unroll
+      for (int c = 0; c < CPL; c++) {
+        const float y = __fmul_rn(acc[c], inv);
+        p.out[o + lane + 32 * c] = __float2bfloat16_rn(p.gate ? gate_mul(y, to_f32(p.gate[o + lane + 32 * c])) : y);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// [Hkv * cap rows][D] bf16 cache as a 2-D tensor in boxes of 64 columns.
+static bool encode_rows_map(CUtensorMap* m, void* base, int D, int64_t rows, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace records (one per piece, NC x 128 rows of D + 4 fp32) a call may
+// use: never more than its items can be cut into.
+template <int NC>
+static int64_t slots_for(const tv_attn_layer* l, const tv_prompt* pr, int max_len) {
+  const int64_t tp = 128 / (l->Hq / l->Hkv) * NC;
+  const int64_t items = l->Hkv * ((pr->n_total + tp - 1) / tp + pr->n_seq);
+  const int64_t nk = (static_cast<int64_t>(max_len) + pr->n_max + kKeyTile - 1) / kKeyTile;
+  if (nk <= kPieceTiles) return 0;
+  const int64_t all = items * ((nk + kPieceTiles - 1) / kPieceTiles), cap = static_cast<int64_t>(kSlotsPerSm) * 152 / NC;
+  return all < cap ? all : cap;
+}
+
+template <int D, bool PAIR>
+static tv_status launch_prompt_tc(AttnPromptTcParams& p, const AttnPromptCall& a, cudaStream_t st) {
+  using C = Pa<D, PAIR>;
+  const tv_attn_layer* l = a.layer;
+  for (int s = 0; s < a.prompt->n_seq; s++)
+    if (!encode_rows_map(&p.tmK[s], l->K[s], D, static_cast<int64_t>(l->Hkv) * l->cap, C::KROWS) ||
+        !encode_rows_map(&p.tmV[s], l->V[s], D, static_cast<int64_t>(l->Hkv) * l->cap, C::VROWS))
+      return TV_ERR_CUDA;
+  p.T = 128 / p.G;
+  p.TP = p.T * C::NC;
+  p.slots = static_cast<int>(slots_for<C::NC>(l, a.prompt, a.max_len));
+  static int workers = 0;
+  if (!workers) {
+    if (cudaFuncSetAttribute(attn_prompt_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+      return TV_ERR_CUDA;
+    workers = num_sms();
+  }
+  p.workers = workers;
+  attn_prompt_tc_kernel<D, PAIR><<<dim3(p.workers), 320, C::SMEM, st>>>(p);
+  // the join has work only where the plan, made on the device, split items
+  if (p.slots > 0) launch_k(true, attn_prompt_join_kernel<D, PAIR>, dim3(num_sms() * 4), dim3(256), 0, st, p);
+  return launch_status();
+}
+
+size_t attn_prompt_tc_ws_bytes(const tv_attn_layer* l, const tv_prompt* pr, int max_len) {
+  return static_cast<size_t>(slots_for<1>(l, pr, max_len)) * 128 * (l->D + 4) * 4;
+}
+
+tv_status attn_prompt_tc_launch(const AttnPromptCall& a, cudaStream_t st) {
+  const tv_attn_layer* l = a.layer;
+  if (static_cast<int64_t>(l->Hkv) * l->cap > 0x7fffffff) return TV_ERR_SHAPE;  // TMA row coordinates are 32-bit
+  const size_t need = attn_prompt_tc_ws_bytes(l, a.prompt, a.max_len);
+  if (need > 0 && (!a.ws || a.ws_bytes < need)) return TV_ERR_WORKSPACE;
+  if (!aligned16(a.ws)) return TV_ERR_ALIGN;
+  AttnPromptTcParams p;
+  memset(&p, 0, sizeof(p));
+  p.pr = prompt_rows(a.prompt, a.len, a.max_len, l->cap);
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.gate = static_cast<const __nv_bfloat16*>(a.gate);
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.ws = static_cast<float*>(a.ws);
+  p.Hq = l->Hq;
+  p.Hkv = l->Hkv;
+  p.G = l->Hq / l->Hkv;
+  p.c = a.scale * 1.4426950408889634f;
+  switch (l->D) {
+    case 64: return launch_prompt_tc<64, false>(p, a, st);
+    case 128: return launch_prompt_tc<128, false>(p, a, st);
+    default: return launch_prompt_tc<256, false>(p, a, st);
+  }
+}
+
+}  // namespace tv
