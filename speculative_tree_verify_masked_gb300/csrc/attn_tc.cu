@@ -54,6 +54,7 @@
 #include "common.cuh"
 #include "host.hpp"
 #include "launchers.hpp"
+#include "mma_tile.cuh"
 #include "ptx.cuh"
 
 namespace tv {
@@ -745,16 +746,6 @@ __global__ void __launch_bounds__(384, 1) attn_split_kernel(const __grid_constan
   if (warp == 1) tmem_dealloc(tbase, C::COLS);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait_group() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // ---------------------------------------------------------------------------
 // tail kernel: the row's own segment, then the merge
 // ---------------------------------------------------------------------------
@@ -762,29 +753,7 @@ __device__ __forceinline__ void cp_async_wait_group() {
 // segment's two small products: its rows are one node's G query heads, far
 // below the 64- or 128-row tiles of tcgen05, and these need no tensor memory,
 // so several tail CTAs share an SM.
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-// d += a b for one 16 x 8 x 16 tile (a: 16 x 16 row-major, b: 16 x 8 column-major)
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-               "{%0, %1, %2, %3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Byte offset of 16-byte chunk c of row r in a buffer of rows rb bytes long:
-// chunk c sits at c ^ (r mod 8), so the 8 rows of an 8 x 8 matrix load fall
-// on distinct banks.
-__device__ __forceinline__ uint32_t swz(int r, int c, int rb) {
-  return static_cast<uint32_t>(r * rb + ((c ^ (r & 7)) << 4));
-}
+// (ldsm_x4, mma16816 and swz: mma_tile.cuh)
 
 template <int D>
 struct Tail {

@@ -1,29 +1,17 @@
-// The gated delta rule over a prompt's packed rows, states advanced in place.
+// The gated delta rule over a prompt's packed rows, states advanced in place:
+// the entry point, and the row-by-row kernel (fp32 layers, state widths the
+// block form does not take, and short prompts; blocks: gdn_prompt_tc.cu).
 //
-// Row by row: a lane group holds one state row in registers and steps through
+// A lane group holds one state row in registers and steps through
 // its sequence's tokens with the step function of decode (gdn_step.cuh), the
 // next token's key, query, value and gates in flight during the current step.
 // The bits are those of decoding the tokens one by one.
 #include <cmath>
 
-#include "prompt.cuh"
+#include "gdn_prompt.cuh"
 #include "gdn_step.cuh"
-#include "launchers.hpp"
 
 namespace tv {
-
-struct GdnPromptParams {
-  PromptRows pr;
-  float* S[TV_MAX_SEQ];
-  const void* q;
-  const void* k;
-  const void* v;
-  const float* alpha;
-  const float* beta;
-  void* out;
-  int Hk, Hv, dv;
-  float scale;
-};
 
 template <typename T, int LPR>
 struct TokenIn {
@@ -91,16 +79,22 @@ static void launch_rec(const GdnPromptParams& p, cudaStream_t st) {
 
 using namespace tv;
 
-extern "C" size_t tv_gdn_prompt_workspace_bytes(const tv_gdn_layer* l, const tv_prompt* pr) { return 0; }
+static bool prompt_shape_ok(const tv_gdn_layer* l) {
+  return l->Hk >= 1 && l->Hv >= 1 && l->Hv % l->Hk == 0 && l->Hv <= 4096 && (l->dk == 64 || l->dk == 128) &&
+         l->dv >= 1 && l->dv <= 256;
+}
+
+extern "C" size_t tv_gdn_prompt_workspace_bytes(const tv_gdn_layer* l, const tv_prompt* pr) {
+  if (!l || !prompt_ok(pr) || !prompt_shape_ok(l) || !gdn_prompt_tc_fits(l, pr)) return 0;
+  return gdn_prompt_tc_ws_bytes(l, pr);
+}
 
 extern "C" tv_status tv_gdn_prompt(const tv_gdn_layer* l, const tv_prompt* pr, const void* q, const void* k,
                                    const void* v, const float* alpha, const float* beta, void* out, float scale,
                                    void* ws, size_t ws_bytes, tv_stream stream) {
   if (!l || !l->S || !prompt_ok(pr)) return TV_ERR_ARG;
   if (l->dtype != TV_F32 && l->dtype != TV_BF16) return TV_ERR_DTYPE;
-  if (l->Hk < 1 || l->Hv < 1 || l->Hv % l->Hk || l->Hv > 4096 || (l->dk != 64 && l->dk != 128) || l->dv < 1 ||
-      l->dv > 256)
-    return TV_ERR_SHAPE;
+  if (!prompt_shape_ok(l)) return TV_ERR_SHAPE;
   if (!(scale > 0.f) || !std::isfinite(scale)) return TV_ERR_ARG;
   GdnPromptParams p{};
   for (int s = 0; s < pr->n_seq; s++) {
@@ -116,6 +110,7 @@ extern "C" tv_status tv_gdn_prompt(const tv_gdn_layer* l, const tv_prompt* pr, c
   p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.beta = beta; p.out = out;
   p.Hk = l->Hk; p.Hv = l->Hv; p.dv = l->dv; p.scale = scale;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (gdn_prompt_tc_fits(l, pr)) return gdn_prompt_tc_launch(l, p, ws, ws_bytes, pr, st);
   const bool bf = l->dtype == TV_BF16;
   if (l->dk == 128) {
     if (bf) launch_rec<__nv_bfloat16, 8>(p, st); else launch_rec<float, 8>(p, st);
