@@ -162,5 +162,9 @@ __device__ __forceinline__ float f2_hsum(f2_t a) {
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// Two bf16 (low half first) as a packed fp32 pair, exactly.
+__device__ __forceinline__ f2_t f2_from_bf16x2(uint32_t w) {
+  return (static_cast<f2_t>(w & 0xffff0000u) << 32) | static_cast<f2_t>(w << 16);
+}
 
 }  // namespace tv

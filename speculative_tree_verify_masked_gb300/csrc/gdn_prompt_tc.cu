@@ -3,29 +3,31 @@
 // Within a block that starts from state S0 (rows i = 0 .. 63, D_ij the product
 // of alpha over j+1 .. i, g_i = alpha_0 .. alpha_i):
 //   A_ij = beta_i D_ij (k_i . k_j), j < i      T = (I + A)^-1 diag(beta)
-//   R_i  = v_i - g_i S0 k_i                     C = T R      (the corrections)
-//   o_i  = scale g_i S0 q_i + sum_j P_ij C_j,   P_ij = scale D_ij (q_i . k_j), j <= i
-//   S    = g_63 S0 + sum_j D_63,j C_j k_j^T
+//   R_i  = v_i - g_i S0 k_i                    (T R are the block's corrections)
+//   o_i  = scale g_i S0 q_i + (P T R)_i,       P_ij = scale D_ij (q_i . k_j), j <= i
+//   S    = g_63 S0 + (W R)^T,                  W = K^T diag(D_63) T   [dk x 64]
 // which is the recurrence exactly; rows that do not exist act as alpha = 1,
 // beta = 0.  The products D_ij are formed as products, never as quotients or
 // differences of logarithms, so decays of 0 and runs of tiny ones are exact.
 //
-// Two kernels.  The first forms T and P T of every block and value head, all
-// independent.  The second walks a sequence's blocks, one CTA per (value head,
-// 64 state columns dv), three chained products a block:
-//   [K; Q] S0^T  ->  [T; P T] R  ->  K^T (C D_63)
+// Two kernels.  The first forms W and P T of every block and value head, all
+// independent (with T applied ahead of time, the walk has two products in its
+// chain instead of three).  The second walks a sequence's blocks, one CTA per
+// (value head, 64 state columns dv):
+//   [K; Q] S0^T  ->  R  ->  W R  ->  S,   and beside the chain  P T R -> o,
 // each 128 rows tall on the tcgen05 tensor cores with fp32 sums in tensor
 // memory, the state in registers (a thread holds one key row, 32 columns).
 //
 // Precision.  k, q and v are bf16 as they come.  What is formed on the way (S,
-// R, C, T) enters a product as two bf16 parts, x = hi + lo with hi = bf16(x),
-// lo = bf16(x - hi), which leaves 2^-17 of each value: hi and lo stand side by
-// side in the product's columns (T: in a second pass), so the state keeps fp32
-// class accuracy over long prompts.  P T only reaches the bf16 output and is
-// rounded once.
+// R, W, A, T) enters a product as two bf16 parts, x = hi + lo with hi =
+// bf16(x), lo = bf16(x - hi), which leaves 2^-17 of each value at most: hi and
+// lo stand side by side in the product's columns, or take a pass each (lo lo is
+// left out).  One part alone would leave 2^-9, far above what a state that
+// lives over a long prompt can take; with two it stays within some 5e-6 of the
+// recurrence in 64 bits (rel-L2, 8,192 rows).  P T only reaches the bf16 output and is rounded once.
 //
-// Bound by the chain of products and tensor-memory round trips a block, not by
-// bytes; the first kernel by its triangular solves.
+// Bound by the chain of products, tensor-memory round trips and splits a
+// block, not by bytes.
 #include <cstring>
 
 #include "attn_shared.cuh"
@@ -35,12 +37,22 @@
 
 namespace tv {
 
-constexpr int kBlk = 64;                                // rows of a block
-constexpr int kTile64 = kBlk * kBlk * 2;                // one 64 x 64 bf16 tile
-constexpr int kBlkBytes = 3 * kTile64 + 2 * kBlk * 4;   // T hi, P T, T lo (swizzled images), g, D_63
+constexpr int kBlk = 64;                  // rows of a block
+constexpr int kTile64 = kBlk * kBlk * 2;  // one 64 x 64 bf16 tile
+
+// What the first kernel leaves of a block and value head: P T [64][64], then W
+// as hi and lo [DK rows][64], swizzled as the second kernel's operands; then g
+// and D_63 (fp32).
+template <int DK>
+struct Image {
+  static constexpr int WB = DK * 128;       // bytes of W hi (or lo)
+  static constexpr int W = kTile64;         // offset of W hi
+  static constexpr int G = W + 2 * WB;
+  static constexpr int BYTES = G + 2 * kBlk * 4;
+};
 
 struct GdnTcParams {
-  CUtensorMap tmK, tmQ;
+  CUtensorMap tmK, tmQ, tmV;
   PromptRows pr;
   float* S[TV_MAX_SEQ];
   const __nv_bfloat16* q;
@@ -74,23 +86,70 @@ __device__ __forceinline__ int block_base(const WarpSeqs& w, const PromptRows& p
 }
 
 // ---------------------------------------------------------------------------
-// first kernel: T and P T of one block, for the value heads of one key head
+// first kernel: W and P T of one block, for the value heads of one key head
 // ---------------------------------------------------------------------------
-constexpr int kLdA = kBlk + 4;
+// 16 x 16 blocks by warp-level tiles.  A matrix lives as accumulators (C
+// layout: row lane / 4 and +8, columns 2 (lane % 4) and +1 of two 8-wide
+// tiles), which are its A operand once packed; as B operand it is read back
+// from [64][64] bf16 hi and lo tiles in shared memory.
+struct Op16 {
+  uint32_t h[4], l[4];
+};
+__device__ __forceinline__ Op16 split_op(const float (&c0)[4], const float (&c1)[4]) {
+  Op16 o;
+  split2(c0[0], c0[1], o.h[0], o.l[0]);
+  split2(c0[2], c0[3], o.h[1], o.l[1]);
+  split2(c1[0], c1[1], o.h[2], o.l[2]);
+  split2(c1[2], c1[3], o.h[3], o.l[3]);
+  return o;
+}
+// B operand: block (rows r0 .., columns c0 ..) of a hi tile and the lo tile behind it
+__device__ __forceinline__ Op16 load_op(uint32_t tile, int r0, int c0, int lane) {
+  Op16 o;
+  const int mi = lane >> 3, r = r0 + (mi & 1) * 8 + (lane & 7);
+  const uint32_t a = tile + swz(r, c0 / 8 + (mi >> 1), 128);
+  ldsm_x4_t(a, o.h);
+  ldsm_x4_t(a + kTile64, o.l);
+  return o;
+}
+// acc += a b, hi hi + hi lo + lo hi
+__device__ __forceinline__ void mma_split(float (&c0)[4], float (&c1)[4], const Op16& a, const Op16& b) {
+  mma16816(c0, a.h, b.h[0], b.h[1]);
+  mma16816(c1, a.h, b.h[2], b.h[3]);
+  mma16816(c0, a.h, b.l[0], b.l[1]);
+  mma16816(c1, a.h, b.l[2], b.l[3]);
+  mma16816(c0, a.l, b.h[0], b.h[1]);
+  mma16816(c1, a.l, b.h[2], b.h[3]);
+}
+__device__ __forceinline__ void stsm_x4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
+// hi and lo parts of a block (the lo tile `lo_off` behind)
+__device__ __forceinline__ void store_op(uint32_t tile, uint32_t lo_off, int r0, int c0, int lane, const Op16& o) {
+  const int mi = lane >> 3, r = r0 + (mi & 1) * 8 + (lane & 7);
+  const uint32_t a = tile + swz(r, c0 / 8 + (mi >> 1), 128);
+  stsm_x4(a, o.h);
+  stsm_x4(a + lo_off, o.l);
+}
 
 template <int DK>
 struct Prep {
   static constexpr int ROWB = DK * 2;
-  static constexpr int KQ = 2 * kBlk * ROWB;               // K and Q rows, dead once G and P are formed
-  static constexpr int DM = 0, AM = kBlk * kLdA * 4;       // decay table, A / T (same place)
-  static constexpr int SMEM = KQ > 2 * AM ? KQ : 2 * AM;
+  static constexpr int KS = kBlk * ROWB;              // the key rows stay
+  static constexpr int DX = KS, AT = DX + 2 * kTile64, XT = AT + 2 * kTile64;  // hi and lo tiles
+  static constexpr int IMG = AT - kTile64;            // the image takes the place of DX lo, A and X
+  static constexpr int SMEM = XT + 2 * kTile64;       // 64 KB (DK = 128): three CTAs an SM
+  static_assert(IMG + Image<DK>::G <= SMEM, "image");
 };
 
 template <int DK>
-__global__ void __launch_bounds__(128) gdn_block_prep_kernel(const __grid_constant__ GdnTcParams p) {
+__global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_constant__ GdnTcParams p) {
   using C = Prep<DK>;
   extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ float al_s[kBlk], be_s[kBlk];
+  __shared__ float al_s[kBlk], be_s[kBlk], dl_s[kBlk];
+  __shared__ float win[4][16][17];  // win[b][i][j]: product of alpha over rows j+1 .. i of 16-row group b
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (status_bad(p.pr.status)) return;
   const WarpSeqs w = load_seqs(p.pr, lane);
@@ -107,7 +166,8 @@ __global__ void __launch_bounds__(128) gdn_block_prep_kernel(const __grid_consta
   const int row0 = __shfl_sync(0xffffffffu, w.off, s) + (blk - __shfl_sync(0xffffffffu, base, s)) * kBlk;
   const int nv = min(kBlk, __shfl_sync(0xffffffffu, w.end, s) - row0);
   const int g = blockIdx.y;
-  const uint32_t ks = smem_u32(sm), qs = ks + kBlk * C::ROWB;
+  const uint32_t ks = smem_u32(sm), qs = ks + C::DX;  // the query rows are dead before DX is written
+  const uint32_t dx = ks + C::DX, at = ks + C::AT, xt = ks + C::XT, img = ks + C::IMG;
   for (int e = tid; e < kBlk * (DK / 8); e += 128) {
     const int r = e / (DK / 8), c = e % (DK / 8);
     const bool ok = r < nv;
@@ -118,7 +178,7 @@ __global__ void __launch_bounds__(128) gdn_block_prep_kernel(const __grid_consta
   cp_async_commit();
   cp_async_wait_group<0>();
   __syncthreads();
-  // G = K K^T and Q K^T: warp w forms rows 16w .. 16w+15, columns up to its own rows
+  // K K^T and Q K^T: warp w forms rows 16w .. 16w+15, columns up to its own rows
   float G[8][4], Pq[8][4];
 #pragma unroll
   for (int t = 0; t < 8; t++)
@@ -143,14 +203,12 @@ __global__ void __launch_bounds__(128) gdn_block_prep_kernel(const __grid_consta
       }
     }
   }
-  __syncthreads();  // the rows are dead: the tables take their place
-  float* Dm = reinterpret_cast<float*>(sm + C::DM);
-  float* Am = reinterpret_cast<float*>(sm + C::AM);
-  const int fr = 16 * warp + (lane >> 2), fc = 2 * (lane & 3);  // fragment row (and +8), column in a tile
+  const int fr = lane >> 2, fc = 2 * (lane & 3);  // fragment row (and +8) and column in a 16-row group
   const int r = p.Hv / p.Hk;
   for (int hh = 0; hh < r; hh++) {
     const int h = g * r + hh;
-    uint8_t* dst = p.ws + (static_cast<size_t>(blk) * p.Hv + h) * kBlkBytes;
+    uint8_t* dst = p.ws + (static_cast<size_t>(blk) * p.Hv + h) * Image<DK>::BYTES;
+    if (tid == 0 && hh > 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last image has left
     if (tid < kBlk) {
       const size_t gi = static_cast<size_t>(row0 + tid) * p.Hv + h;
       al_s[tid] = tid < nv ? p.alpha[gi] : 1.f;
@@ -158,111 +216,209 @@ __global__ void __launch_bounds__(128) gdn_block_prep_kernel(const __grid_consta
     }
     __syncthreads();
     if (tid < kBlk) {
-      // column tid of the decay table, and g
-      float d = 1.f, gp = 1.f;
-      for (int i = 0; i < kBlk; i++) {
-        const float a = al_s[i];
-        if (i > tid) d = __fmul_rn(d, a);
-        if (i <= tid) gp = __fmul_rn(gp, a);
-        Dm[i * kLdA + tid] = i >= tid ? d : 0.f;
+      const int b = tid >> 4, j = tid & 15;
+      float d = 1.f;
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        if (i > j) d = __fmul_rn(d, al_s[16 * b + i]);
+        win[b][i][j] = i >= j ? d : 0.f;
       }
-      reinterpret_cast<float*>(dst + 3 * kTile64)[tid] = gp;
-      reinterpret_cast<float*>(dst + 3 * kTile64)[kBlk + tid] = d;
     }
     __syncthreads();
-    // A (zeros on and above the diagonal), and this warp's rows of P
-    float Pd[8][4];
+    float grp[4];  // product of alpha over each 16-row group
 #pragma unroll
-    for (int t = 0; t < 8; t++)
+    for (int b = 0; b < 4; b++) grp[b] = __fmul_rn(al_s[16 * b], win[b][15][0]);
+    if (tid < kBlk) {
+      const int b = tid >> 4, j = tid & 15;
+      float gi = __fmul_rn(al_s[16 * b], win[b][j][0]), dl = win[b][15][j];
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const int i = fr + (e >> 1) * 8, j = 8 * t + fc + (e & 1);
-        const float d = Dm[i * kLdA + j];
-        Am[i * kLdA + j] = j < i ? __fmul_rn(be_s[i], __fmul_rn(d, G[t][e])) : 0.f;
-        Pd[t][e] = j <= i ? __fmul_rn(p.scale, __fmul_rn(d, Pq[t][e])) : 0.f;
+      for (int x = 0; x < 4; x++) {
+        if (x < b) gi = __fmul_rn(gi, grp[x]);
+        if (x > b) dl = __fmul_rn(dl, grp[x]);
       }
-    __syncthreads();
-    // column c of (I + A)^-1 by substitution, two threads a column: thread
-    // `par` sums over the groups of four rows j with (j / 4) % 2 == par
-    const int c = tid >> 1, par = tid & 1;
-    float x[32];
-#pragma unroll
-    for (int i = 0; i < 32; i++) x[i] = 0.f;
-#pragma unroll
-    for (int i = 0; i < kBlk; i++) {
-      float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-#pragma unroll
-      for (int gp = 0; gp < (i + 7) / 8; gp++) {
-        const float4 a = *reinterpret_cast<const float4*>(Am + i * kLdA + 8 * gp + 4 * par);
-        a0 = __fmaf_rn(a.x, x[4 * gp], a0);
-        a1 = __fmaf_rn(a.y, x[4 * gp + 1], a1);
-        a2 = __fmaf_rn(a.z, x[4 * gp + 2], a2);
-        a3 = __fmaf_rn(a.w, x[4 * gp + 3], a3);
-      }
-      float sum = __fadd_rn(__fadd_rn(a0, a1), __fadd_rn(a2, a3));
-      sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 1));
-      const float xi = i == c ? 1.f : -sum;
-      if (((i >> 2) & 1) == par) x[(i >> 3) * 4 + (i & 3)] = xi;
+      dl_s[tid] = dl;
+      reinterpret_cast<float*>(dst + Image<DK>::G)[tid] = gi;
+      reinterpret_cast<float*>(dst + Image<DK>::G)[kBlk + tid] = dl;
     }
-    __syncthreads();
-    {
-      const float b = be_s[c];
+    // this warp's rows of A (hi and lo tiles) and of P (registers, A operands)
+    const float be0 = be_s[16 * warp + fr], be1 = be_s[16 * warp + fr + 8];
+    const float pre0 = __fmul_rn(al_s[16 * warp], win[warp][fr][0]), pre1 = __fmul_rn(al_s[16 * warp], win[warp][fr + 8][0]);
+    Op16 P[4];
+    float Ad[2][4];
 #pragma unroll
-      for (int e = 0; e < 32; e++) Am[((e >> 2) * 8 + par * 4 + (e & 3)) * kLdA + c] = __fmul_rn(x[e], b);
-    }
-    __syncthreads();
-    // T as two bf16 parts, in the swizzled image the second kernel copies
-    {
-      const int row = tid >> 1, c0 = (tid & 1) * 32;
+    for (int b = 0; b < 4; b++) {
+      if (b > warp) continue;
+      float mid = 1.f;  // the groups between
 #pragma unroll
-      for (int q4 = 0; q4 < 4; q4++) {
-        uint32_t hi[4], lo[4];
+      for (int x = 1; x < 3; x++)
+        if (x > b && x < warp) mid = __fmul_rn(mid, grp[x]);
+      float A[2][4], Pd[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; t++)
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          const float2 t2 = *reinterpret_cast<const float2*>(Am + row * kLdA + c0 + q4 * 8 + 2 * e);
-          split2(t2.x, t2.y, hi[e], lo[e]);
+          const int i = fr + (e >> 1) * 8, j = 8 * t + fc + (e & 1);
+          const float be = (e >> 1) ? be1 : be0;
+          float d;
+          if (b < warp) d = __fmul_rn(__fmul_rn(win[b][15][j], mid), (e >> 1) ? pre1 : pre0);
+          else d = win[b][i][j];
+          const bool low = b < warp || j < i, dia = b == warp && j == i;
+          A[t][e] = low ? __fmul_rn(be, __fmul_rn(d, G[2 * b + t][e])) : 0.f;
+          Pd[t][e] = low || dia ? __fmul_rn(p.scale, __fmul_rn(d, Pq[2 * b + t][e])) : 0.f;
         }
-        const int at = row * 128 + (((c0 / 8 + q4) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(dst + 2 * kTile64 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      P[b] = split_op(Pd[0], Pd[1]);
+      store_op(at, kTile64, 16 * warp, 16 * b, lane, split_op(A[0], A[1]));
+      if (b == warp) {
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) Ad[t][e] = A[t][e];
       }
     }
-    // P T by warp tiles, both split in two: P hi T hi + P hi T lo + P lo T hi
-    float O[8][4];
+    // inverse of this warp's diagonal block: A is strictly lower triangular, so
+    // (I + A)^-1 = (I - A)(I + A^2)(I + A^4)(I + A^8)
+    __syncwarp();
+    float X[4][2][4];  // this warp's row of blocks of (I + A)^-1; X[b] is block column b
+    float D[2][4];
+    {
+      float Q2[2][4];
 #pragma unroll
-    for (int t = 0; t < 8; t++)
+      for (int t = 0; t < 2; t++)
 #pragma unroll
-      for (int e = 0; e < 4; e++) O[t][e] = 0.f;
+        for (int e = 0; e < 4; e++) {
+          D[t][e] = (fr + (e >> 1) * 8 == 8 * t + fc + (e & 1) ? 1.f : 0.f) - Ad[t][e];
+          Q2[t][e] = 0.f;
+        }
+      mma_split(Q2[0], Q2[1], split_op(Ad[0], Ad[1]), load_op(at, 16 * warp, 16 * warp, lane));
 #pragma unroll
-    for (int kt = 0; kt < 4; kt++) {
-      if (kt > warp) continue;  // P is zero right of its rows
-      uint32_t ph[4], pl[4];
-      split2(Pd[2 * kt][0], Pd[2 * kt][1], ph[0], pl[0]);
-      split2(Pd[2 * kt][2], Pd[2 * kt][3], ph[1], pl[1]);
-      split2(Pd[2 * kt + 1][0], Pd[2 * kt + 1][1], ph[2], pl[2]);
-      split2(Pd[2 * kt + 1][2], Pd[2 * kt + 1][3], ph[3], pl[3]);
+      for (int it = 0; it < 3; it++) {
+        const Op16 q = split_op(Q2[0], Q2[1]);
+        __syncwarp();
+        store_op(xt, kTile64, 16 * warp, 16 * warp, lane, q);
+        __syncwarp();
+        const Op16 qb = load_op(xt, 16 * warp, 16 * warp, lane);
+        const Op16 x = split_op(D[0], D[1]);
+        mma_split(D[0], D[1], x, qb);
+        if (it < 2) {
+#pragma unroll
+          for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) Q2[t][e] = 0.f;
+          mma_split(Q2[0], Q2[1], q, qb);
+        }
+      }
+      __syncwarp();
+      store_op(xt, kTile64, 16 * warp, 16 * warp, lane, split_op(D[0], D[1]));
+    }
+    __syncthreads();
+    // the rest of the row: X_wj = -(sum over j < k <= w of X_wk A_kj) X_jj
+#pragma unroll
+    for (int b = 3; b >= 0; b--) {
+      if (b == warp) {
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) X[b][t][e] = D[t][e];
+      } else if (b < warp) {
+        float acc[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) acc[t][e] = X[b][t][e] = 0.f;
+#pragma unroll
+        for (int k = 3; k >= 1; k--)
+          if (k > b && k <= warp) mma_split(acc[0], acc[1], split_op(X[k][0], X[k][1]), load_op(at, 16 * k, 16 * b, lane));
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) acc[t][e] = -acc[t][e];
+        mma_split(X[b][0], X[b][1], split_op(acc[0], acc[1]), load_op(xt, 16 * b, 16 * b, lane));
+      }
+    }
+    {
+      const float d0 = dl_s[16 * warp + fr], d1 = dl_s[16 * warp + fr + 8];
+#pragma unroll
+      for (int b = 0; b < 4; b++) {
+        if (b > warp) continue;
+        if (b < warp) store_op(xt, kTile64, 16 * warp, 16 * b, lane, split_op(X[b][0], X[b][1]));
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) X[b][t][e] = __fmul_rn(X[b][t][e], (e >> 1) ? d1 : d0);
+        store_op(dx, kTile64, 16 * warp, 16 * b, lane, split_op(X[b][0], X[b][1]));
+      }
+    }
+    __syncthreads();
+    // P T: this warp's rows; columns scaled by beta
+    uint32_t pt[16];
+    {
+      float O[8][4];
+#pragma unroll
+      for (int t = 0; t < 8; t++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) O[t][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        if (k > warp) continue;
+#pragma unroll
+        for (int b = 0; b <= k; b++) mma_split(O[2 * b], O[2 * b + 1], P[k], load_op(xt, 16 * k, 16 * b, lane));
+      }
 #pragma unroll
       for (int t = 0; t < 8; t++) {
-        if (t > 2 * kt + 1) continue;  // T is zero right of its rows
-        const float* tb = Am + (16 * kt + fc) * kLdA + 8 * t + (lane >> 2);
-        uint32_t h0, l0, h1, l1;
-        split2(tb[0], tb[kLdA], h0, l0);
-        split2(tb[8 * kLdA], tb[9 * kLdA], h1, l1);
-        mma16816(O[t], ph, h0, h1);
-        mma16816(O[t], ph, l0, l1);
-        mma16816(O[t], pl, h0, h1);
+        const float b0 = be_s[8 * t + fc], b1 = be_s[8 * t + fc + 1];
+        pt[2 * t] = pack_bf16x2(__fmul_rn(O[t][0], b0), __fmul_rn(O[t][1], b1));
+        pt[2 * t + 1] = pack_bf16x2(__fmul_rn(O[t][2], b0), __fmul_rn(O[t][3], b1));
       }
     }
+    __syncthreads();  // A and X are dead: W takes their place
+    // W = K^T (D_63 X) diag(beta), k exact in bf16: this warp's key columns,
+    // 16 columns of W at a time
+    constexpr int MT = DK / 64;  // groups of 16 key columns a warp
 #pragma unroll
-    for (int t = 0; t < 8; t++)
+    for (int b = 0; b < 4; b++) {
+      float O[MT][2][4];
 #pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const int row = fr + e * 8;
-        *reinterpret_cast<uint32_t*>(dst + kTile64 + row * 128 + ((t ^ (row & 7)) << 4) + fc * 2) =
-            pack_bf16x2(O[t][2 * e], O[t][2 * e + 1]);
+      for (int t = 0; t < MT; t++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) O[t][0][e] = O[t][1][e] = 0.f;
+#pragma unroll
+      for (int k = b; k < 4; k++) {
+        const Op16 x = load_op(dx, 16 * k, 16 * b, lane);
+#pragma unroll
+        for (int t = 0; t < MT; t++) {
+          uint32_t a[4];
+          ldsm_x4_t(ks + swz(16 * k + (mi >> 1) * 8 + mr, 2 * (warp * MT + t) + (mi & 1), C::ROWB), a);
+          mma16816(O[t][0], a, x.h[0], x.h[1]);
+          mma16816(O[t][1], a, x.h[2], x.h[3]);
+          mma16816(O[t][0], a, x.l[0], x.l[1]);
+          mma16816(O[t][1], a, x.l[2], x.l[3]);
+        }
       }
-    __syncthreads();  // the tables are reused for the next head
+      const float b0 = be_s[16 * b + fc], b1 = be_s[16 * b + fc + 1], b2 = be_s[16 * b + 8 + fc], b3 = be_s[16 * b + 9 + fc];
+#pragma unroll
+      for (int t = 0; t < MT; t++) {
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          O[t][0][e] = __fmul_rn(O[t][0][e], (e & 1) ? b1 : b0);
+          O[t][1][e] = __fmul_rn(O[t][1][e], (e & 1) ? b3 : b2);
+        }
+        store_op(img + Image<DK>::W, Image<DK>::WB, 16 * (warp * MT + t), 16 * b, lane, split_op(O[t][0], O[t][1]));
+      }
+    }
+    __syncthreads();  // DX is dead: P T takes the place of its second half
+#pragma unroll
+    for (int b = 0; b < 4; b++) {
+      const uint32_t v[4] = {pt[4 * b], pt[4 * b + 1], pt[4 * b + 2], pt[4 * b + 3]};
+      stsm_x4(img + swz(16 * warp + (mi & 1) * 8 + mr, 2 * b + (mi >> 1), 128), v);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    if (tid == 0) {
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(img), "r"(Image<DK>::G) : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -274,27 +430,39 @@ template <int DK>
 struct Walk {
   static constexpr int KQ = 2 * kBlk * DK * 2;          // [box of 64 columns][K rows, Q rows]
   static constexpr int KQBOX = 2 * kBlk * 128;          // K and Q rows of one 64-column box
-  static constexpr int TIMG = 3 * kTile64;
-  static constexpr int STAGE = KQ + TIMG + kTile64;     // T lo is followed by zeros
-  static constexpr int B1 = 2 * DK * 128, B2 = 2 * kBlk * 128, B3 = B2;  // [hi | lo] rows of 64 columns each
-  static constexpr int BOFF = 2 * STAGE + B1 + B2 + B3;
-  static constexpr int NBAR = 2 + 2 + 6 + 1;
+  static constexpr int VOFF = KQ + Image<DK>::G;        // 64 value rows
+  static constexpr int GOFF = VOFF + kBlk * kDvs * 2;   // g and D_63
+  static constexpr int STAGE = GOFF + 1024;
+  static constexpr int B1 = 2 * DK * 128, B2 = 2 * kBlk * 128;  // [hi | lo] rows of 64 columns each
+  static constexpr int OBUF = 2 * STAGE + B1 + B2;      // output rows, turned around by their warps
+  static constexpr int BOFF = OBUF + 4 * 2048;
+  static constexpr int NBAR = 2 + 2 + 5 + 1;
   static constexpr int SMEM = BOFF + NBAR * 8 + 16;
   static constexpr int COLS = 512;
-  static constexpr int T_D1 = 0, T_D2 = 128, T_D3 = 256;
+  static constexpr int T_D1 = 0, T_D2 = 256, T_D3 = 384;  // D1 twice, by block parity: its output rows are read late
   static constexpr uint32_t IDESC = idesc_bf16_f32(128, 2 * kDvs, false, true);
-  static constexpr uint32_t IDESC_KT = idesc_bf16_f32(128, 2 * kDvs, true, true);
+  static constexpr uint32_t IDESC_HI = idesc_bf16_f32(128, kDvs, false, true);  // against the hi half alone
   static_assert(SMEM <= 232448, "shared memory");
 };
 
+// Packed pairs as bf16 pairs: the rounded pair, and hi and lo parts.
+__device__ __forceinline__ uint32_t pack_f2(f2_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return pack_bf16x2(a, b);
+}
+__device__ __forceinline__ void split_f2(f2_t x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_f2(x);
+  lo = pack_f2(f2_fma(f2_dup(-1.f), f2_from_bf16x2(hi), x));  // x - hi, exact
+}
 // 32 values as hi and lo parts into row r of a [rows][128 bytes] hi tile and
 // the lo tile `lo_off` behind it (16-byte chunks swizzled), column half wg.
-__device__ __forceinline__ void store_split(uint32_t tile, uint32_t lo_off, int r, int wg, const float (&x)[32]) {
+__device__ __forceinline__ void store_split(uint32_t tile, uint32_t lo_off, int r, int wg, const f2_t (&x)[16]) {
 #pragma unroll
   for (int q = 0; q < 4; q++) {
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int e = 0; e < 4; e++) split2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], lo[e]);
+    for (int e = 0; e < 4; e++) split_f2(x[4 * q + e], hi[e], lo[e]);
     const uint32_t a = tile + r * 128 + (((wg * 4 + q) ^ (r & 7)) << 4);
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a + lo_off), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
@@ -302,12 +470,15 @@ __device__ __forceinline__ void store_split(uint32_t tile, uint32_t lo_off, int 
   }
 }
 // The hi and lo halves of a product's 32 columns of this thread's row, added.
-__device__ __forceinline__ void load_sum(uint32_t taddr, float (&x)[32]) {
+__device__ __forceinline__ void load_sum(uint32_t taddr, f2_t (&x)[16]) {
   uint32_t a[32], b[32];
-  tmem_ld32(taddr, a);
-  tmem_ld32(taddr + kDvs, b);
+  tmem_ld32_nowait(taddr, a);
+  tmem_ld32_nowait(taddr + kDvs, b);
+  tmem_ld_wait(a, b);
 #pragma unroll
-  for (int i = 0; i < 32; i++) x[i] = __fadd_rn(__uint_as_float(a[i]), __uint_as_float(b[i]));
+  for (int i = 0; i < 16; i++)
+    x[i] = f2_add(f2_pack(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1])),
+                  f2_pack(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1])));
 }
 
 template <int DK>
@@ -315,10 +486,10 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
   using C = Walk<DK>;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
-  const uint32_t b1 = sb + 2 * C::STAGE, b2 = b1 + C::B1, b3 = b2 + C::B2;
+  const uint32_t b1 = sb + 2 * C::STAGE, b2 = b1 + C::B1;
   const uint32_t bars = sb + C::BOFF;
   const uint32_t FULL0 = bars, EMPTY0 = bars + 16u, B1R = bars + 32u, D1F = bars + 40u, B2R = bars + 48u,
-                 D2F = bars + 56u, B3R = bars + 64u, D3F = bars + 72u, DRAIN = bars + 80u;
+                 D2F = bars + 56u, D3F = bars + 64u, DRAIN = bars + 72u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::BOFF + C::NBAR * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* skip = reinterpret_cast<int*>(tmem_slot + 2);
@@ -346,9 +517,8 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
     }
     mbar_init(B1R, 8);
     mbar_init(D1F, 1);
-    mbar_init(B2R, 4);
+    mbar_init(B2R, 8);
     mbar_init(D2F, 1);
-    mbar_init(B3R, 4);
     mbar_init(D3F, 1);
     mbar_init(DRAIN, 1);
     *abort_flag = 0;
@@ -367,8 +537,8 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   const int nb = (n + kBlk - 1) / kBlk;
-  const size_t ws_step = static_cast<size_t>(p.Hv) * kBlkBytes;
-  const uint8_t* ws0 = p.ws + (static_cast<size_t>(blk0) * p.Hv + h) * kBlkBytes;
+  const size_t ws_step = static_cast<size_t>(p.Hv) * Image<DK>::BYTES;
+  const uint8_t* ws0 = p.ws + (static_cast<size_t>(blk0) * p.Hv + h) * Image<DK>::BYTES;
 
   if (warp == 9) {
     // ---------------- producer ----------------
@@ -378,13 +548,15 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
         const int st = c & 1;
         if (!wait_role(EMPTY0 + 8u * st, ((c >> 1) & 1) ^ 1, abort_flag, kWaitCycles)) break;
         const uint32_t full = FULL0 + 8u * st, dst = sb + st * C::STAGE;
-        mbar_arrive_expect_tx(full, C::KQ + C::TIMG);
+        mbar_arrive_expect_tx(full, C::KQ + Image<DK>::BYTES + kBlk * kDvs * 2);
 #pragma unroll
         for (int kb = 0; kb < DK / 64; kb++) {
           tma_load_2d(dst + kb * C::KQBOX, &p.tmK, full, g * DK + kb * 64, off + c * kBlk);
           tma_load_2d(dst + kb * C::KQBOX + kBlk * 128, &p.tmQ, full, g * DK + kb * 64, off + c * kBlk);
         }
-        bulk_g2s(dst + C::KQ, ws0 + c * ws_step, C::TIMG, full);
+        tma_load_2d(dst + C::VOFF, &p.tmV, full, h * p.dv + dv0, off + c * kBlk);
+        bulk_g2s(dst + C::GOFF, ws0 + c * ws_step + Image<DK>::G, 2 * kBlk * 4, full);
+        bulk_g2s(dst + C::KQ, ws0 + c * ws_step, Image<DK>::G, full);
       }
       if (c < nb) {
         set_status(p.pr.status, TV_ERR_TIMEOUT);
@@ -405,7 +577,7 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
         const uint64_t a0 = sdesc_sw128(kq, 16, 1024), d0 = sdesc_sw128(b1, DK * 128, 1024);
 #pragma unroll
         for (int kk = 0; kk < DK / 16; kk++)
-          tc_mma_ss(tbase + C::T_D1, a0 + static_cast<uint64_t>(((kk >> 2) * C::KQBOX + (kk & 3) * 32) >> 4),
+          tc_mma_ss(tbase + C::T_D1 + (c & 1) * 128, a0 + static_cast<uint64_t>(((kk >> 2) * C::KQBOX + (kk & 3) * 32) >> 4),
                     d0 + static_cast<uint64_t>((kk * 2048) >> 4), C::IDESC, kk > 0 ? 1u : 0u);
         tc_commit(D1F);
       }
@@ -414,27 +586,21 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
       if (!ok) break;
       tc_fence_after();
       if (elect_one_sync()) {
-        const uint64_t a0 = sdesc_sw128(ti, 16, 1024), d0 = sdesc_sw128(b2, kBlk * 128, 1024);
+        const uint64_t a0 = sdesc_sw128(ti + Image<DK>::W, 16, 1024), d0 = sdesc_sw128(b2, kBlk * 128, 1024);
+        // W hi against [hi | lo], W lo against hi (DK = 64: rows 64 .. 127 of
+        // the product come from what lies behind and are never read)
 #pragma unroll
-        for (int kk = 0; kk < 8; kk++)  // [T hi; P T], then [T lo; 0]
-          tc_mma_ss(tbase + C::T_D2, a0 + static_cast<uint64_t>(((kk >> 2) * 2 * kTile64 + (kk & 3) * 32) >> 4),
-                    d0 + static_cast<uint64_t>(((kk & 3) * 2048) >> 4), C::IDESC, kk > 0 ? 1u : 0u);
-        tc_commit(D2F);
-      }
-      __syncwarp();
-      ok = wait_warp(B3R, c & 1, abort_flag, kWaitCycles);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one_sync()) {
-        // K^T: 64-wide boxes of key columns; for DK = 64 the second box (rows
-        // 64 .. 127 of the product, never read) is the Q rows behind
-        const uint64_t a0 = sdesc_sw128(kq, DK == 128 ? C::KQBOX : kBlk * 128, 1024),
-                       d0 = sdesc_sw128(b3, kBlk * 128, 1024);
+        for (int kk = 0; kk < 8; kk++)
+          tc_mma_ss(tbase + C::T_D3, a0 + static_cast<uint64_t>(((kk >> 2) * Image<DK>::WB + (kk & 3) * 32) >> 4),
+                    d0 + static_cast<uint64_t>(((kk & 3) * 2048) >> 4), kk < 4 ? C::IDESC : C::IDESC_HI, kk > 0 ? 1u : 0u);
+        tc_commit(D3F);
+        // P T in rows 64 .. 127, the output rows' lanes (the rows before are never read)
+        const uint64_t p0 = sdesc_sw128(ti - kTile64, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < 4; kk++)
-          tc_mma_ss(tbase + C::T_D3, a0 + static_cast<uint64_t>((kk * 2048) >> 4),
-                    d0 + static_cast<uint64_t>((kk * 2048) >> 4), C::IDESC_KT, kk > 0 ? 1u : 0u);
-        tc_commit(D3F);
+          tc_mma_ss(tbase + C::T_D2, p0 + static_cast<uint64_t>((kk * 32) >> 4), d0 + static_cast<uint64_t>((kk * 2048) >> 4),
+                    C::IDESC, kk > 0 ? 1u : 0u);
+        tc_commit(D2F);
         tc_commit(EMPTY0 + 8u * st);
       }
       __syncwarp();
@@ -452,108 +618,101 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
     const int ri = krow ? i : i - kBlk;
     const uint32_t tl = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 32;
     float* Sg = p.S[s] + (static_cast<size_t>(h) * p.dv + dv0 + wg * 32) * DK + i;
-    float S[32];
+    f2_t S[16];
 #pragma unroll
-    for (int e = 0; e < 32; e++) S[e] = (DK == 128 || krow) ? Sg[static_cast<size_t>(e) * DK] : 0.f;
+    for (int e = 0; e < 16; e++)
+      S[e] = (DK == 128 || krow) ? f2_pack(Sg[static_cast<size_t>(2 * e) * DK], Sg[static_cast<size_t>(2 * e + 1) * DK]) : 0ull;
     auto arrive = [&](uint32_t bar) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // what block c needs from memory besides the copies: this row's value, g and D_63
-    uint4 vq[4];
-    float gi, dl, gl;
-    auto fetch = [&](int c) {
-      const float* gd = reinterpret_cast<const float*>(ws0 + c * ws_step + 3 * kTile64);
-      gi = gd[ri];
-      dl = gd[kBlk + ri];
-      gl = gd[kBlk - 1];
-      const bool live = krow && c * kBlk + ri < n;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.v + ((static_cast<size_t>(off) + c * kBlk + (live ? ri : 0)) * p.Hv + h) * p.dv + dv0 + wg * 32);
-#pragma unroll
-      for (int e = 0; e < 4; e++) vq[e] = live ? src[e] : make_uint4(0u, 0u, 0u, 0u);
-    };
     bool ok = true;
-    // the state's two parts for the first product of block c, whose rows
-    // behind the sequence's end (another sequence's, or anything) are zeroed:
-    // a zero correction would still meet them in the last product
-    auto offer = [&](int c) {
+    // the state's two parts for the first product of the next block
+    auto offer = [&]() {
       if (DK == 128 || krow) store_split(b1, DK * 128, i, wg, S);
-      const int live = n - c * kBlk;
-      if (live < kBlk) {
-        ok = wait_warp(FULL0 + 8u * (c & 1), (c >> 1) & 1, abort_flag, kWaitCycles);
-        if (!ok) return;
-        const uint32_t kq = sb + (c & 1) * C::STAGE;
-        for (int e = threadIdx.x; e < (kBlk - live) * (DK / 8); e += 256) {
-          const int r = live + e / (DK / 8), ch = e % (DK / 8);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(kq + (ch >> 3) * C::KQBOX + r * 128 + (ch & 7) * 16), "r"(0)
-                       : "memory");
-        }
-      }
       fence_proxy_async_smem();
       tc_fence_before();
       arrive(B1R);
     };
-    for (int e = threadIdx.x; e < 2 * (kTile64 / 16); e += 256)  // the zeros under T lo
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(sb + (e / (kTile64 / 16)) * C::STAGE + C::KQ + C::TIMG +
-                                                                      (e % (kTile64 / 16)) * 16), "r"(0)
-                   : "memory");
-    offer(0);
-    fetch(0);
+    offer();
     for (int c = 0; c < nb && ok; c++) {
-      float x[32];
+      const uint32_t stg = sb + (c & 1) * C::STAGE;
+      const float* gd = reinterpret_cast<const float*>(sm + (c & 1) * C::STAGE + C::GOFF);
+      const int live = n - c * kBlk;  // rows of the block that exist (64 and more: all)
+      f2_t x[16], z[16];
+      ok = wait_warp(FULL0 + 8u * (c & 1), (c >> 1) & 1, abort_flag, kWaitCycles);
+      if (!ok) break;
+      const float gr = gd[ri], gc = gd[kBlk - 1];
+      if (krow) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          uint4 v;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(stg + C::VOFF + ri * 128 + (((wg * 4 + q) ^ (ri & 7)) << 4)));
+          z[4 * q] = f2_from_bf16x2(v.x);
+          z[4 * q + 1] = f2_from_bf16x2(v.y);
+          z[4 * q + 2] = f2_from_bf16x2(v.z);
+          z[4 * q + 3] = f2_from_bf16x2(v.w);
+        }
+      }
       ok = wait_warp(D1F, c & 1, abort_flag, kWaitCycles);
       if (!ok) break;
       tc_fence_after();
-      load_sum(tl + C::T_D1, x);
-      const float gc = gl, gr = gi, dr = dl;
       if (krow) {
-        float v[8], r[32];
+        load_sum(tl + C::T_D1 + (c & 1) * 128, x);
+        const f2_t ng = f2_dup(-gr);
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-          widen8(vq[q], v);
-#pragma unroll
-          for (int e = 0; e < 8; e++) r[8 * q + e] = c * kBlk + ri < n ? __fmaf_rn(-gr, x[8 * q + e], v[e]) : 0.f;
-        }
-        store_split(b2, kBlk * 128, ri, wg, r);
+        for (int e = 0; e < 16; e++) z[e] = ri < live ? f2_fma(ng, x[e], z[e]) : 0ull;
+        store_split(b2, kBlk * 128, ri, wg, z);
         fence_proxy_async_smem();
-        tc_fence_before();
-        arrive(B2R);
       }
-      if (c + 1 < nb) fetch(c + 1);
-      ok = wait_warp(D2F, c & 1, abort_flag, kWaitCycles);
-      if (!ok) break;
-      tc_fence_after();
-      float z[32];
-      load_sum(tl + C::T_D2, z);
-      if (krow) {
-#pragma unroll
-        for (int e = 0; e < 32; e++) z[e] = __fmul_rn(z[e], dr);
-        store_split(b3, kBlk * 128, ri, wg, z);
-        fence_proxy_async_smem();
-        tc_fence_before();
-        arrive(B3R);
-      } else if (c * kBlk + ri < n) {
-        const float f = __fmul_rn(p.scale, gr);
-        uint32_t o[16];
-#pragma unroll
-        for (int e = 0; e < 16; e++)
-          o[e] = pack_bf16x2(__fmaf_rn(f, x[2 * e], z[2 * e]), __fmaf_rn(f, x[2 * e + 1], z[2 * e + 1]));
-        uint4* dst = reinterpret_cast<uint4*>(p.out + ((static_cast<size_t>(off) + c * kBlk + ri) * p.Hv + h) * p.dv + dv0 + wg * 32);
-#pragma unroll
-        for (int e = 0; e < 4; e++) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-      }
+      tc_fence_before();
+      arrive(B2R);  // (the output rows' warps: done with the stage and with the last P T R)
       ok = wait_warp(D3F, c & 1, abort_flag, kWaitCycles);
       if (!ok) break;
       tc_fence_after();
-      load_sum(tl + C::T_D3, x);
+      load_sum(tl + C::T_D3, z);
+      const f2_t g2 = f2_dup(gc);
 #pragma unroll
-      for (int e = 0; e < 32; e++) S[e] = __fmaf_rn(gc, S[e], x[e]);
-      if (c + 1 < nb) offer(c + 1);
+      for (int e = 0; e < 16; e++) S[e] = f2_fma(g2, S[e], z[e]);
+      if (c + 1 < nb) offer();
+      if (!krow) {
+        ok = wait_warp(D2F, c & 1, abort_flag, kWaitCycles);
+        if (!ok) break;
+        tc_fence_after();
+        load_sum(tl + C::T_D2, z);
+        load_sum(tl + C::T_D1 + (c & 1) * 128, x);
+        const f2_t f = f2_dup(__fmul_rn(p.scale, gr));
+        uint32_t o[16];
+#pragma unroll
+        for (int e = 0; e < 16; e++) o[e] = pack_f2(f2_fma(f, x[e], z[e]));
+        // a thread holds 64 bytes of one row: turned around so that a store
+        // covers whole rows' pieces, not 16 bytes of each of 32 rows
+        const uint32_t ob = sb + C::OBUF + (wg * 2 + (warp & 1)) * 2048;
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(ob + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)),
+                       "r"(o[4 * q]), "r"(o[4 * q + 1]), "r"(o[4 * q + 2]), "r"(o[4 * q + 3])
+                       : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const int rr = 8 * k + (lane >> 2), q = lane & 3, orow = (ri - lane) + rr;
+          uint4 v;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(ob + rr * 64 + ((q ^ ((rr >> 1) & 3)) << 4)));
+          if (orow < live)
+            reinterpret_cast<uint4*>(p.out + ((static_cast<size_t>(off) + c * kBlk + orow) * p.Hv + h) * p.dv + dv0 + wg * 32)[q] = v;
+        }
+      }
     }
     if (ok && (DK == 128 || krow)) {
 #pragma unroll
-      for (int e = 0; e < 32; e++) Sg[static_cast<size_t>(e) * DK] = S[e];
+      for (int e = 0; e < 16; e++)
+        f2_unpack(S[e], Sg[static_cast<size_t>(2 * e) * DK], Sg[static_cast<size_t>(2 * e + 1) * DK]);
     }
     if (!ok && lane == 0) set_status(p.pr.status, TV_ERR_TIMEOUT);
   }
@@ -575,14 +734,15 @@ bool gdn_prompt_tc_fits(const tv_gdn_layer* l, const tv_prompt* pr) {
 }
 
 size_t gdn_prompt_tc_ws_bytes(const tv_gdn_layer* l, const tv_prompt* pr) {
-  return static_cast<size_t>(blocks_bound(pr)) * l->Hv * kBlkBytes;
+  return static_cast<size_t>(blocks_bound(pr)) * l->Hv * (l->dk == 128 ? Image<128>::BYTES : Image<64>::BYTES);
 }
 
 template <int DK>
 static tv_status launch_tc(const GdnTcParams& p, int64_t blocks, cudaStream_t st) {
   static bool set = false;
   if (!set) {
-    if (cudaFuncSetAttribute(gdn_block_walk_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, Walk<DK>::SMEM) != cudaSuccess)
+    if (cudaFuncSetAttribute(gdn_block_walk_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, Walk<DK>::SMEM) != cudaSuccess ||
+        cudaFuncSetAttribute(gdn_block_prep_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, Prep<DK>::SMEM) != cudaSuccess)
       return TV_ERR_CUDA;
     set = true;
   }
@@ -599,14 +759,16 @@ tv_status gdn_prompt_tc_launch(const tv_gdn_layer* l, const GdnPromptParams& a, 
   memset(&p, 0, sizeof(p));
   auto fn = encode_fn();
   if (!fn) return TV_ERR_CUDA;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(l->Hk) * l->dk, static_cast<cuuint64_t>(pr->n_total)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(l->Hk) * l->dk * 2};
-  const cuuint32_t box[2] = {64, kBlk}, estr[2] = {1, 1};
-  for (int i = 0; i < 2; i++)
-    if (fn(i ? &p.tmQ : &p.tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(i ? a.q : a.k), dims, strides, box, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return TV_ERR_CUDA;
+  auto encode = [&](CUtensorMap* m, const void* base, int64_t cols) {  // [n_total][cols] in 64 x 64 boxes
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(pr->n_total)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+    const cuuint32_t box[2] = {64, kBlk}, estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const int64_t kcols = static_cast<int64_t>(l->Hk) * l->dk, vcols = static_cast<int64_t>(l->Hv) * l->dv;
+  if (!encode(&p.tmK, a.k, kcols) || !encode(&p.tmQ, a.q, kcols) || !encode(&p.tmV, a.v, vcols)) return TV_ERR_CUDA;
   p.pr = a.pr;
   for (int s = 0; s < pr->n_seq; s++) p.S[s] = a.S[s];
   p.q = static_cast<const __nv_bfloat16*>(a.q);

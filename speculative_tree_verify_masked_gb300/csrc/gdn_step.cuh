@@ -59,10 +59,6 @@ __device__ __forceinline__ void store_row(float* dst, const f2_t (&s)[kPairs], i
   }
 }
 
-// Two bf16 (low half first) as a packed fp32 pair, exactly.
-__device__ __forceinline__ f2_t f2_from_bf16x2(uint32_t w) {
-  return (static_cast<f2_t>(w & 0xffff0000u) << 32) | static_cast<f2_t>(w << 16);
-}
 // This lane's pairs of a dk-long row stored as bf16 (same columns as load_row).
 template <int LPR>
 __device__ __forceinline__ void load_row_bf16(f2_t (&d)[kPairs], const __nv_bfloat16* src, int j) {
