@@ -205,16 +205,23 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
   }
   const int fr = lane >> 2, fc = 2 * (lane & 3);  // fragment row (and +8) and column in a 16-row group
   const int r = p.Hv / p.Hk;
+  // a row's gates, one head ahead of their use
+  const bool gate_row = tid < nv;  // (nv <= 64)
+  const size_t gate0 = static_cast<size_t>(row0 + (gate_row ? tid : 0)) * p.Hv + g * r;
+  float al_n = gate_row ? p.alpha[gate0] : 1.f, be_n = gate_row ? p.beta[gate0] : 0.f;
   for (int hh = 0; hh < r; hh++) {
     const int h = g * r + hh;
     uint8_t* dst = p.ws + (static_cast<size_t>(blk) * p.Hv + h) * Image<DK>::BYTES;
-    if (tid == 0 && hh > 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last image has left
     if (tid < kBlk) {
-      const size_t gi = static_cast<size_t>(row0 + tid) * p.Hv + h;
-      al_s[tid] = tid < nv ? p.alpha[gi] : 1.f;
-      be_s[tid] = tid < nv ? p.beta[gi] : 0.f;
+      al_s[tid] = al_n;
+      be_s[tid] = be_n;
     }
     __syncthreads();
+    if (gate_row && hh + 1 < r) {
+      al_n = p.alpha[gate0 + hh + 1];
+      be_n = p.beta[gate0 + hh + 1];
+    }
+    if (tid == 0 && hh > 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last image has left
     if (tid < kBlk) {
       const int b = tid >> 4, j = tid & 15;
       float d = 1.f;
@@ -240,40 +247,50 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
       reinterpret_cast<float*>(dst + Image<DK>::G)[tid] = gi;
       reinterpret_cast<float*>(dst + Image<DK>::G)[kBlk + tid] = dl;
     }
-    // this warp's rows of A (hi and lo tiles) and of P (registers, A operands)
-    const float be0 = be_s[16 * warp + fr], be1 = be_s[16 * warp + fr + 8];
+    // the decays of this warp's rows against block column b, in C layout (zero
+    // above the diagonal; on it 1)
     const float pre0 = __fmul_rn(al_s[16 * warp], win[warp][fr][0]), pre1 = __fmul_rn(al_s[16 * warp], win[warp][fr + 8][0]);
-    Op16 P[4];
+    auto decays = [&](int b, float (&d)[2][4]) {
+      if (b < warp) {
+        float mid = 1.f;  // the groups between
+#pragma unroll
+        for (int x = 1; x < 3; x++)
+          if (x > b && x < warp) mid = __fmul_rn(mid, grp[x]);
+        const float m0 = __fmul_rn(mid, pre0), m1 = __fmul_rn(mid, pre1);
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const float sfx = win[b][15][8 * t + fc + e];
+            d[t][e] = __fmul_rn(sfx, m0);
+            d[t][e + 2] = __fmul_rn(sfx, m1);
+          }
+      } else {
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) d[t][e] = win[b][fr + (e >> 1) * 8][8 * t + fc + (e & 1)];
+      }
+    };
+    // this warp's rows of A, as hi and lo tiles
+    const float be0 = be_s[16 * warp + fr], be1 = be_s[16 * warp + fr + 8];
     float Ad[2][4];
 #pragma unroll
     for (int b = 0; b < 4; b++) {
       if (b > warp) continue;
-      float mid = 1.f;  // the groups between
-#pragma unroll
-      for (int x = 1; x < 3; x++)
-        if (x > b && x < warp) mid = __fmul_rn(mid, grp[x]);
-      float A[2][4], Pd[2][4];
+      float A[2][4];
+      decays(b, A);
 #pragma unroll
       for (int t = 0; t < 2; t++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const int i = fr + (e >> 1) * 8, j = 8 * t + fc + (e & 1);
-          const float be = (e >> 1) ? be1 : be0;
-          float d;
-          if (b < warp) d = __fmul_rn(__fmul_rn(win[b][15][j], mid), (e >> 1) ? pre1 : pre0);
-          else d = win[b][i][j];
-          const bool low = b < warp || j < i, dia = b == warp && j == i;
-          A[t][e] = low ? __fmul_rn(be, __fmul_rn(d, G[2 * b + t][e])) : 0.f;
-          Pd[t][e] = low || dia ? __fmul_rn(p.scale, __fmul_rn(d, Pq[2 * b + t][e])) : 0.f;
-        }
-      P[b] = split_op(Pd[0], Pd[1]);
-      store_op(at, kTile64, 16 * warp, 16 * b, lane, split_op(A[0], A[1]));
+        for (int e = 0; e < 4; e++) A[t][e] = __fmul_rn((e >> 1) ? be1 : be0, __fmul_rn(A[t][e], G[2 * b + t][e]));
       if (b == warp) {
 #pragma unroll
         for (int t = 0; t < 2; t++)
 #pragma unroll
-          for (int e = 0; e < 4; e++) Ad[t][e] = A[t][e];
+          for (int e = 0; e < 4; e++) Ad[t][e] = A[t][e] = 8 * t + fc + (e & 1) < fr + (e >> 1) * 8 ? A[t][e] : 0.f;
       }
+      store_op(at, kTile64, 16 * warp, 16 * b, lane, split_op(A[0], A[1]));
     }
     // inverse of this warp's diagonal block: A is strictly lower triangular, so
     // (I + A)^-1 = (I - A)(I + A^2)(I + A^4)(I + A^8)
@@ -360,8 +377,15 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < 4; k++) {
         if (k > warp) continue;
+        float P[2][4];
+        decays(k, P);
 #pragma unroll
-        for (int b = 0; b <= k; b++) mma_split(O[2 * b], O[2 * b + 1], P[k], load_op(xt, 16 * k, 16 * b, lane));
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) P[t][e] = __fmul_rn(p.scale, __fmul_rn(P[t][e], Pq[2 * k + t][e]));
+        const Op16 po = split_op(P[0], P[1]);
+#pragma unroll
+        for (int b = 0; b <= k; b++) mma_split(O[2 * b], O[2 * b + 1], po, load_op(xt, 16 * k, 16 * b, lane));
       }
 #pragma unroll
       for (int t = 0; t < 8; t++) {
