@@ -94,6 +94,20 @@ struct AttnPromptTcParams {
   float c;  // scale * log2(e)
 };
 
+constexpr int64_t kNoRow = -1;
+
+__device__ __forceinline__ void st_shared16(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+// x * sigmoid(g) with the fast exponential and divide (a few fp32 steps, far
+// below the bf16 rounding that follows).
+__device__ __forceinline__ float fast_gate(float x, float g) { return x * __fdividef(1.f, 1.f + __expf(-g)); }
+
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // The plan, by one warp.  Cost of a candidate, in key tiles: the waves of
@@ -422,6 +436,7 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
     // ---------------- softmax and output, two threads to a row ----------------
     const int hf = (warp - 2) >> 2, quad = warp & 3, lrow = quad * 32 + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t patch = pbuf + static_cast<uint32_t>(warp - 2) * 4096u;  // this warp's 4 KB between items
     const int tok = lrow / p.G, head = lrow % p.G;
     uint32_t t = 0, xc = 0, tails = 0, it = 0;  // tiles, exchanges, zeroed value tiles, units before the item
     bool ok = true;
@@ -447,15 +462,44 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
       const bool act = tok < p.T && token < pl.n[I.s];
       const int last = act ? L + token : -1;  // last position this row sees
       const int seen_all = L + I.i * p.TP + static_cast<int>(rank) * p.T + 1;  // positions every row here sees
-      const size_t orow = act ? ((static_cast<size_t>(pl.off[I.s]) + token) * p.Hq + I.g * p.G + head) * D : 0;
-      {
-        uint4 qv[QShare<D>::N];
-        q_fetch<D>(act ? p.q + orow : nullptr, hf, qv);
-        q_store<D>(tl + C::T_Q, hf, qv);  // every Q K^T of the previous item has completed: its S was read
+      // this thread's row of q and out (elements); kNoRow: none
+      const int64_t orow = act ? ((static_cast<int64_t>(pl.off[I.s]) + token) * p.Hq + I.g * p.G + head) * D : kNoRow;
+      // Q into tensor memory (every Q K^T of the previous item has completed:
+      // its S was read).  A warp reads its rows in whole 128-byte pieces and
+      // turns them around in shared memory.  P's buffer is free for it: no
+      // softmax warp writes P again before every warp's queries are in.
+      if (D >= 128 || hf == 0) {
+#pragma unroll
+        for (int pc = 0; pc < (D >= 128 ? D / 128 : 1); pc++) {
+          const int col = (D >= 128 ? hf * (D / 2) : 0) + pc * 64;
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const int64_t ro = __shfl_sync(0xffffffffu, orow, 4 * i + (lane >> 3));
+            v[i] = ro >= 0 ? *reinterpret_cast<const uint4*>(p.q + ro + col + (lane & 7) * 8) : make_uint4(0u, 0u, 0u, 0u);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const int rr = 4 * i + (lane >> 3);
+            st_shared16(patch + rr * 128 + (((lane ^ rr) & 7) << 4), v[i]);
+          }
+          __syncwarp();
+          uint32_t r[32];
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const uint4 x = ld_shared16(patch + lane * 128 + (((i ^ lane) & 7) << 4));
+            r[4 * i] = x.x;
+            r[4 * i + 1] = x.y;
+            r[4 * i + 2] = x.z;
+            r[4 * i + 3] = x.w;
+          }
+          tmem_st32(tl + C::T_Q + col / 2, r);
+        }
         tmem_st_wait();
-        tc_fence_before();
-        arrive(rQREADY);
       }
+      tc_fence_before();
+      arrive(rQREADY);
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < n; k++, t++) {
         if (!wait_warp(SFULL, t & 1, abort_flag, kWaitCycles)) {
@@ -567,35 +611,46 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
       tc_fence_after();
       const float inv = __fdiv_rn(1.f, __fadd_rn(l, lo));
       float* rec = I.slot >= 0 ? p.ws + ((static_cast<size_t>(I.slot) * C::NC + rank) * 128 + lrow) * (D + 4) : nullptr;
+      // O by 32 columns, turned around in this warp's patch (rows of 128 bytes)
+      // so that a store covers whole pieces of rows
 #pragma unroll 1
       for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
         uint32_t r[32];
         tmem_ld32(tl + C::T_O + c, r);
-        if (!act) continue;
-        if (rec) {
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(rec + c + i) = make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
-                                                                  __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+        for (int i = 0; i < 8; i++)
+          st_shared16(patch + lane * 128 + (((i ^ lane) & 7) << 4), make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
+        __syncwarp();
+        if (I.slot >= 0) {
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const int rr = 4 * i + (lane >> 3);
+            const uint4 x = ld_shared16(patch + rr * 128 + (((lane ^ rr) & 7) << 4));
+            if (__shfl_sync(0xffffffffu, orow, rr) >= 0)
+              *reinterpret_cast<uint4*>(rec + (rr - lane) * (D + 4) + c + (lane & 7) * 4) = x;
+          }
           continue;
         }
-        float y[32];
 #pragma unroll
-        for (int i = 0; i < 32; i++) y[i] = __fmul_rn(__uint_as_float(r[i]), inv);
-        if (p.gate) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
+        for (int i = 0; i < 4; i++) {
+          const int rr = 8 * i + (lane >> 2), q = (lane & 3) * 2;
+          const uint4 x0 = ld_shared16(patch + rr * 128 + (((q ^ rr) & 7) << 4)),
+                      x1 = ld_shared16(patch + rr * 128 + ((((q + 1) ^ rr) & 7) << 4));
+          const float f = __shfl_sync(0xffffffffu, inv, rr);
+          const int64_t ro = __shfl_sync(0xffffffffu, orow, rr);
+          if (ro < 0) continue;
+          float y[8] = {__uint_as_float(x0.x) * f, __uint_as_float(x0.y) * f, __uint_as_float(x0.z) * f, __uint_as_float(x0.w) * f,
+                        __uint_as_float(x1.x) * f, __uint_as_float(x1.y) * f, __uint_as_float(x1.z) * f, __uint_as_float(x1.w) * f};
+          const int64_t at = ro + c + (lane & 3) * 8;
+          if (p.gate) {
             float gv[8];
-            load8(p.gate + orow + c + i, gv);
+            load8(p.gate + at, gv);
 #pragma unroll
-            for (int e = 0; e < 8; e++) y[i + e] = gate_mul(y[i + e], gv[e]);
+            for (int e = 0; e < 8; e++) y[e] = fast_gate(y[e], gv[e]);
           }
+          store8(p.out + at, y);
         }
-#pragma unroll
-        for (int i = 0; i < 32; i += 8)
-          *reinterpret_cast<uint4*>(p.out + orow + c + i) =
-              make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]), pack_bf16x2(y[i + 4], y[i + 5]),
-                         pack_bf16x2(y[i + 6], y[i + 7]));
       }
       if (rec && act && hf == 0) {
         rec[D] = m;
@@ -615,10 +670,11 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
   }
 }
 
-// Joins the pieces of split items: one warp a row, pieces in order.
+// Joins the pieces of split items, in order: a warp takes 128 columns of a row,
+// four a lane, several pieces' loads in flight.
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_constant__ AttnPromptTcParams p) {
-  constexpr int NC = PAIR ? 2 : 1, CPL = D / 32;
+  constexpr int NC = PAIR ? 2 : 1, CB = D > 128 ? D / 128 : 1, LPR = D >= 128 ? 32 : D / 4, RPW = 32 / LPR;
   __shared__ PromptPlan pl;
   __shared__ int skip;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -634,40 +690,60 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
   for (int at = 0; at < p.pr.n_seq; at++) {
     const int s = pl.seq[at];
     if (pl.pm[s] < 2) continue;
-    const int64_t rows = static_cast<int64_t>(pl.n[s]) * p.Hq;
-    for (int64_t x = static_cast<int64_t>(blockIdx.x) * 8 + warp; x < rows; x += static_cast<int64_t>(gridDim.x) * 8) {
+    const int64_t units = (static_cast<int64_t>(pl.n[s]) * p.Hq + RPW - 1) / RPW * CB;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + warp; u < units; u += static_cast<int64_t>(gridDim.x) * 8) {
+      const int64_t x = u / CB * RPW + lane / LPR;  // row (token, head)
+      if (x >= static_cast<int64_t>(pl.n[s]) * p.Hq) continue;
+      const int col = static_cast<int>(u % CB) * 128 + (lane % LPR) * 4;
       const int token = static_cast<int>(x / p.Hq), h = static_cast<int>(x % p.Hq), g = h / p.G;
       const int i = token / p.TP, rank = token % p.TP / p.T, lrow = (token % p.TP % p.T) * p.G + h % p.G;
       const int nk = ceil_div(pl.L[s] + min((i + 1) * p.TP, pl.n[s]), kKeyTile);
       const int np = ceil_div(nk, pl.S);
       if (np < 2) continue;  // written whole
       const int per = p.Hkv * pl.rt[s], first = pl.slot0[at] + (pl.rt[s] - 1 - i) * p.Hkv + g;
-      auto rec = [&](int j) {
-        return p.ws + ((static_cast<size_t>(first + j * per) * NC + rank) * 128 + lrow) * (D + 4);
-      };
-      float m = -INFINITY;
-      for (int j = lane; j < np; j += 32) m = fmaxf(m, rec(j)[D]);
+      const float* rec = p.ws + ((static_cast<size_t>(first) * NC + rank) * 128 + lrow) * (D + 4);
+      const size_t step = static_cast<size_t>(per) * NC * 128 * (D + 4);
+      // one pass with a running maximum, four pieces at a time
+      float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int j0 = 0; j0 < np; j0 += 4) {
+        float4 o[4];
+        float2 ml[4];
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float l = 0.f, acc[CPL];
+        for (int j = 0; j < 4; j++) {
+          const float* r = rec + step * min(j0 + j, np - 1);
+          o[j] = *reinterpret_cast<const float4*>(r + col);
+          ml[j] = *reinterpret_cast<const float2*>(r + D);
+          if (j0 + j >= np) ml[j] = make_float2(-INFINITY, 0.f);
+        }
+        const float mn = fmaxf(m, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+        const float a = m == -INFINITY ? 0.f : exp2f(__fsub_rn(m, mn));
+        l = __fmul_rn(l, a);
 #pragma unroll
-      for (int c = 0; c < CPL; c++) acc[c] = 0.f;
-#pragma unroll 4
-      for (int j = 0; j < np; j++) {
-        const float* r = rec(j);
-        const float mj = r[D];
-        const float f = mj == -INFINITY ? 0.f : exp2f(__fsub_rn(mj, m));
-        l = __fmaf_rn(f, r[D + 1], l);
+        for (int e = 0; e < 4; e++) acc[e] = __fmul_rn(acc[e], a);
 #pragma unroll
-        for (int c = 0; c < CPL; c++) acc[c] = __fmaf_rn(f, r[lane + 32 * c], acc[c]);
+        for (int j = 0; j < 4; j++) {
+          if (ml[j].x == -INFINITY) continue;  // no position of this row in the piece (or no piece)
+          const float f = exp2f(__fsub_rn(ml[j].x, mn));
+          l = __fmaf_rn(f, ml[j].y, l);
+          acc[0] = __fmaf_rn(f, o[j].x, acc[0]);
+          acc[1] = __fmaf_rn(f, o[j].y, acc[1]);
+          acc[2] = __fmaf_rn(f, o[j].z, acc[2]);
+          acc[3] = __fmaf_rn(f, o[j].w, acc[3]);
+        }
+        m = mn;
       }
-      const size_t o = (static_cast<size_t>(pl.off[s]) * p.Hq + x) * D;
+      const size_t at_o = (static_cast<size_t>(pl.off[s]) * p.Hq + x) * D + col;
       const float inv = __fdiv_rn(1.f, l);
 #pragma unroll
-      for (int c = 0; c < CPL; c++) {
-        const float y = __fmul_rn(acc[c], inv);
-        p.out[o + lane + 32 * c] = __float2bfloat16_rn(p.gate ? gate_mul(y, to_f32(p.gate[o + lane + 32 * c])) : y);
+      for (int e = 0; e < 4; e++) acc[e] = __fmul_rn(acc[e], inv);
+      if (p.gate) {
+        const uint2 gv = *reinterpret_cast<const uint2*>(p.gate + at_o);
+        acc[0] = fast_gate(acc[0], bf16_lo(gv.x));
+        acc[1] = fast_gate(acc[1], bf16_hi(gv.x));
+        acc[2] = fast_gate(acc[2], bf16_lo(gv.y));
+        acc[3] = fast_gate(acc[3], bf16_hi(gv.y));
       }
+      *reinterpret_cast<uint2*>(p.out + at_o) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
     }
   }
 }

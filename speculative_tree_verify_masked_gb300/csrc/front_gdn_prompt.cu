@@ -5,9 +5,9 @@
 //
 // Bound by HBM: every raw channel is read once and written once.  A group of
 // DH/8 lanes owns one head (eight consecutive channels a lane, one 16-byte
-// access a row) and walks kRows consecutive rows, keeping the W-1 rows before
-// the current one in registers; only a strip's first W-1 rows are read twice
-// (by this strip and the one before it).  Taps run in fp32 in order, oldest
+// access a row) and walks a strip of consecutive rows, a few loaded ahead, with
+// the W-1 rows before the current one in registers; only a strip's last W-1
+// rows are read twice (by it and the next strip).  Taps run in fp32 in order, oldest
 // first, as in the tree and decode forms.
 #include "prompt.cuh"
 #include "front_gdn.cuh"
@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(128) gdn_prompt_front_kernel(const __grid_cons
     for (int j = 0; j < WM; j++) tap[j][e] = j < W ? p.wconv[static_cast<size_t>(c0 + e) * W + j] : 0.f;
   const T* x = static_cast<const T*>(p.x) + c0;
   const bool norm = u < 2 * p.Hk;
+  const bool any_norm = __any_sync(0xffffffffu, norm);
   T* dst;
   size_t dstride;
   if (u < p.Hk) {
@@ -79,57 +80,65 @@ __global__ void __launch_bounds__(128) gdn_prompt_front_kernel(const __grid_cons
   }
   int s = seq_of(w, p.pr, lane, r0);
   int off = __shfl_sync(0xffffffffu, w.off, s), end = __shfl_sync(0xffffffffu, w.end, s);
-  float win[WM][8];  // win[j]: the input j - (W-1) rows from the current one
+  // win[(r + j) % WM]: the input j - (W-1) rows from row r, so that a step
+  // overwrites the oldest and nothing moves
+  float win[WM][8];
   bool fresh = true;
-  for (int r = r0; r < r1; r++) {
-    if (r >= end) {  // the next sequence that has rows
-      s = seq_of(w, p.pr, lane, r);
-      off = __shfl_sync(0xffffffffu, w.off, s);
-      end = __shfl_sync(0xffffffffu, w.end, s);
-      fresh = true;
-    }
-    if (fresh) {
-      fresh = false;
-      const T* tail = static_cast<const T*>(p.tail[s]);
+  for (int rg = r0; rg < r1; rg += WM) {
+    float cur[WM][8];  // the group's rows, loaded ahead
 #pragma unroll
-      for (int j = 0; j < WM - 1; j++)
-        if (j < W - 1) {
-          const int m = r - off + j - (W - 1);  // row of the sequence, negative: in the tail
-          load8(m >= 0 ? x + static_cast<size_t>(off + m) * p.C : tail + static_cast<size_t>(m + W - 1) * p.C + c0, win[j]);
+    for (int u = 0; u < WM; u++) load8(x + static_cast<size_t>(min(rg + u, r1 - 1)) * p.C, cur[u]);
+#pragma unroll
+    for (int u = 0; u < WM; u++) {
+      const int r = rg + u;
+      if (r >= r1) break;
+      if (r >= end) {  // the next sequence that has rows
+        s = seq_of(w, p.pr, lane, r);
+        off = __shfl_sync(0xffffffffu, w.off, s);
+        end = __shfl_sync(0xffffffffu, w.end, s);
+        fresh = true;
+      }
+      if (fresh) {
+        fresh = false;
+        const T* tail = static_cast<const T*>(p.tail[s]);
+#pragma unroll
+        for (int j = 0; j < WM - 1; j++)
+          if (j < W - 1) {
+            const int m = r - off + j - (W - 1);  // row of the sequence, negative: in the tail
+            load8(m >= 0 ? x + static_cast<size_t>(off + m) * p.C : tail + static_cast<size_t>(m + W - 1) * p.C + c0,
+                  win[(u + j) % WM]);
+          }
+      }
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; e++) y[e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < WM; j++)
+        if (j < W) {
+#pragma unroll
+          for (int e = 0; e < 8; e++) y[e] = __fmaf_rn(tap[j][e], (j == W - 1) ? cur[u][e] : win[(u + j) % WM][e], y[e]);
         }
-    }
-    float cur[8];
-    load8(x + static_cast<size_t>(r) * p.C, cur);
-    float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; e++) y[e] = 0.f;
+      for (int j = 0; j < WM; j++)
+        if (j == W - 1) {
 #pragma unroll
-    for (int j = 0; j < WM; j++)
-      if (j < W) {
+          for (int e = 0; e < 8; e++) win[(u + j) % WM][e] = cur[u][e];
+        }
+      float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; e++) y[e] = __fmaf_rn(tap[j][e], (j == W - 1) ? cur[e] : win[j][e], y[e]);
+      for (int e = 0; e < 8; e++) {
+        y[e] = silu_f(y[e]);
+        ss = __fmaf_rn(y[e], y[e], ss);
       }
-    // move the window on
+      if (any_norm) {
 #pragma unroll
-    for (int j = 0; j < WM - 1; j++)
-      if (j < W - 1) {
+        for (int o = LPH / 2; o >= 1; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+        const float sc = norm ? rsqrtf(__fadd_rn(ss, kNormEps)) : 1.f;
 #pragma unroll
-        for (int e = 0; e < 8; e++) win[j][e] = (j == W - 2) ? cur[e] : win[j + 1 < WM - 1 ? j + 1 : j][e];
+        for (int e = 0; e < 8; e++) y[e] = __fmul_rn(y[e], sc);
       }
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      y[e] = silu_f(y[e]);
-      ss = __fmaf_rn(y[e], y[e], ss);
+      if (act) store8(dst + static_cast<size_t>(r) * dstride, y);
     }
-#pragma unroll
-    for (int o = LPH / 2; o >= 1; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
-    if (norm) {
-      const float sc = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(ss, kNormEps)));
-#pragma unroll
-      for (int e = 0; e < 8; e++) y[e] = __fmul_rn(y[e], sc);
-    }
-    if (act) store8(dst + static_cast<size_t>(r) * dstride, y);
   }
 }
 
@@ -137,6 +146,7 @@ __global__ void __launch_bounds__(128) gdn_prompt_front_kernel(const __grid_cons
 template <typename T>
 __global__ void __launch_bounds__(256) gdn_prompt_tail_kernel(const __grid_constant__ GdnPromptFrontParams p) {
   const int lane = threadIdx.x & 31;
+  pdl_wait();
   if (status_bad(p.pr.status)) return;
   const WarpSeqs w = load_seqs(p.pr, lane);
   if (w.code) return;  // reported by the first kernel
@@ -207,8 +217,8 @@ extern "C" tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* f, const tv_p
   }
   if (f->width > 1) {
     const dim3 tg((p.C + 255) / 256, pr->n_seq);
-    if (bf) gdn_prompt_tail_kernel<__nv_bfloat16><<<tg, 256, 0, st>>>(p);
-    else gdn_prompt_tail_kernel<float><<<tg, 256, 0, st>>>(p);
+    if (bf) launch_k(true, gdn_prompt_tail_kernel<__nv_bfloat16>, tg, dim3(256), 0, st, p);
+    else launch_k(true, gdn_prompt_tail_kernel<float>, tg, dim3(256), 0, st, p);
   }
   return launch_status();
 }

@@ -16,7 +16,8 @@
 // A group of D/8 lanes owns a head, eight consecutive dimensions a lane, so a
 // row moves with one 16-byte access a lane (two for fp32).  A warp keeps one
 // row: its lanes form the row's sines and cosines once, in shared memory, and
-// its groups walk heads_per_warp of the row's query, key and value heads.
+// its groups walk a part of the row's heads, up to eight (fp32: four) loads in
+// flight before the first is used.  Values are copied by warps of their own.
 // Bound by HBM: each row is read once and written once.  A row's bits depend
 // only on its own values and position, and the three forms run the same code,
 // so verified, decoded and prompt rows are equal.
@@ -42,25 +43,67 @@ struct NormRopeParams {
   const int32_t* node_off;
   const void* meta;
   int form;  // 0 tree, 1 decode, 2 prompt
-  int n_rows, n_seq, n_total, Hq, Hkv, rot, max_len, cap, heads_per_warp;
+  int n_rows, n_seq, n_total, Hq, Hkv, rot, max_len, cap;
+  int heads_per_warp, qk_parts, parts;  // warps a row: qk_parts for queries and keys, the rest for values
   float eps;
   uint64_t rate[kMaxPlanes];  // turns per position of each plane, as 64-bit fractions
 };
 
+// Eight values of a row as they lie in memory.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ void widen(float (&x)[8]) const { widen8(v, x); }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void widen(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-  constexpr int LPH = D / 8;    // lanes per head
-  constexpr int GPW = 32 / LPH; // heads a warp holds at once
+  constexpr int LPH = D / 8;                  // lanes per head
+  constexpr int GPW = 32 / LPH;               // heads a warp holds at once
+  constexpr int HB = sizeof(T) == 2 ? 8 : 4;  // loads a lane keeps in flight
   __shared__ __align__(16) float cs_s[8][D / 2], sn_s[8][D / 2];
   __shared__ __align__(16) float row_s[8][GPW][D];
   const int wib = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * 8 + wib;
-  const int heads = p.Hq + p.Hkv + (p.form == 2 ? p.Hkv : 0);
-  const int parts = (heads + p.heads_per_warp - 1) / p.heads_per_warp;
-  const int row = static_cast<int>(warp / parts), part = static_cast<int>(warp % parts);
-  if (row >= p.n_rows || status_bad(p.pr.status)) return;  // whole warps leave
+  const int row = static_cast<int>(warp / p.parts), part = static_cast<int>(warp % p.parts);
+  if (row >= p.n_rows) return;  // whole warps leave
+  const int grp = lane / LPH, gl = lane % LPH, d0 = gl * 8;
+  // this warp's heads; the first loads start before the row's place is known
+  const bool vals = part >= p.qk_parts;
+  const int h_first = (vals ? part - p.qk_parts : part) * p.heads_per_warp;
+  const int h_end = min(vals ? p.Hkv : p.Hq + p.Hkv, h_first + p.heads_per_warp);
+  const T* qr = static_cast<const T*>(p.q_raw) + static_cast<size_t>(row) * p.Hq * D + d0;
+  const T* kr = static_cast<const T*>(vals ? p.v_raw : p.k_raw) + static_cast<size_t>(row) * p.Hkv * D + d0;
+  auto src = [&](int h) { return vals ? kr + static_cast<size_t>(h) * D : h < p.Hq ? qr + static_cast<size_t>(h) * D : kr + static_cast<size_t>(h - p.Hq) * D; };
+  Raw8<T> raw[HB];
+#pragma unroll
+  for (int i = 0; i < HB; i++) {
+    const int h = h_first + i * GPW + grp;
+    if (h < h_end) raw[i].load(src(h));
+  }
+  if (status_bad(p.pr.status)) return;
   // the row's sequence, position and (prompt) cache row
-  int s, pos, len;
+  int s, pos;
   if (p.form == 2) {
     const WarpSeqs w = load_seqs(p.pr, lane);
     if (w.code) {
@@ -69,8 +112,7 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
     }
     s = seq_of(w, p.pr, lane, row);
     if (s < 0) return;  // padding behind the last sequence
-    len = __shfl_sync(0xffffffffu, w.len, s);
-    pos = len + row - __shfl_sync(0xffffffffu, w.off, s);
+    pos = __shfl_sync(0xffffffffu, w.len, s) + row - __shfl_sync(0xffffffffu, w.off, s);
   } else {
     s = row;
     int depth = 0;
@@ -79,12 +121,29 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
       while (s < p.n_seq - 1 && row >= p.node_off[s + 1]) s++;
       depth = meta_view(const_cast<void*>(p.meta), p.n_total).depth[row];
     }
-    len = p.pr.len[s];
+    const int len = p.pr.len[s];
     if (len < 0 || len > p.max_len) {
       if (lane == 0) set_status(p.pr.status, TV_ERR_LEN);
       return;
     }
     pos = len + depth;
+  }
+  if (vals) {  // bit copies into the value cache
+    T* dst = static_cast<T*>(p.V[s]) + static_cast<size_t>(pos) * D + d0;
+    for (int h0 = h_first;;) {
+#pragma unroll
+      for (int i = 0; i < HB; i++) {
+        const int h = h0 + i * GPW + grp;
+        if (h < h_end) raw[i].store(dst + static_cast<size_t>(h) * p.cap * D);
+      }
+      h0 += HB * GPW;
+      if (h0 >= h_end) return;
+#pragma unroll
+      for (int i = 0; i < HB; i++) {
+        const int h = h0 + i * GPW + grp;
+        if (h < h_end) raw[i].load(src(h));
+      }
+    }
   }
   const int half = p.rot >> 1;
   for (int j = lane; j < half; j += 32) {
@@ -93,7 +152,6 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
     sincospif(x, &sn_s[wib][j], &cs_s[wib][j]);
   }
   __syncwarp();
-  const int grp = lane / LPH, gl = lane % LPH, d0 = gl * 8;
   // this lane's rotation factors: dimension d < rot belongs to plane d mod half;
   // the first half of a plane takes -sin of its partner, the second +sin
   float cs[8], sn[8];
@@ -105,61 +163,62 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
     sn[e] = d < p.rot ? (d < half ? -sn_s[wib][j] : sn_s[wib][j]) : 0.f;
   }
   float wq[8], wk[8];
-#pragma unroll
-  for (int e = 0; e < 8; e++) wq[e] = wk[e] = 1.f;
   if (p.q_norm) {
     load8(p.q_norm + d0, wq);
     load8(p.k_norm + d0, wk);
   }
   const bool aligned = half % 8 == 0;  // a lane's eight partners sit in one other lane
-  const int src = d0 < half ? gl + half / 8 : (d0 < p.rot ? gl - half / 8 : gl);
-  const int h_end = min(heads, (part + 1) * p.heads_per_warp);
-  for (int h0 = part * p.heads_per_warp; h0 < h_end; h0 += GPW) {
-    const int h = h0 + grp;
-    const bool act = h < h_end;
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-    const int g = is_q ? 0 : (is_v ? h - p.Hq - p.Hkv : h - p.Hq);
-    const size_t ri = is_q ? static_cast<size_t>(row) * p.Hq + h : static_cast<size_t>(row) * p.Hkv + g;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (act) load8(static_cast<const T*>(is_q ? p.q_raw : is_v ? p.v_raw : p.k_raw) + ri * D + d0, x);
-    if (p.q_norm) {
-      float ss = 0.f;
+  const int partner = d0 < half ? gl + half / 8 : (d0 < p.rot ? gl - half / 8 : gl);
+  for (int h0 = h_first; h0 < h_end; h0 += HB * GPW) {
+    if (h0 != h_first) {
 #pragma unroll
-      for (int e = 0; e < 8; e++) ss = __fmaf_rn(x[e], x[e], ss);
+      for (int i = 0; i < HB; i++) {
+        const int h = h0 + i * GPW + grp;
+        if (h < h_end) raw[i].load(src(h));
+      }
+    }
 #pragma unroll
-      for (int o = LPH / 2; o >= 1; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
-      const float inv = __fdiv_rn(1.f, __fsqrt_rn(__fmaf_rn(ss, 1.f / D, p.eps)));
-      if (!is_v) {
+    for (int i = 0; i < HB; i++) {
+      if (h0 + i * GPW >= h_end) break;  // the whole warp
+      const int h = h0 + i * GPW + grp;
+      const bool act = h < h_end, is_q = h < p.Hq;
+      float x[8];
+      raw[i].widen(x);
+      if (p.q_norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; e++) ss = __fmaf_rn(x[e], x[e], ss);
+#pragma unroll
+        for (int o = LPH / 2; o >= 1; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+        const float inv = rsqrtf(__fmaf_rn(ss, 1.f / D, p.eps));  // 2 units in the last place, far below the output's rounding
 #pragma unroll
         for (int e = 0; e < 8; e++) x[e] = __fmul_rn(__fmul_rn(x[e], inv), is_q ? wq[e] : wk[e]);
       }
-    }
-    float y[8];
-    if (aligned) {
+      float y[8];
+      if (aligned) {
 #pragma unroll
-      for (int e = 0; e < 8; e++) y[e] = __shfl_sync(0xffffffffu, x[e], src, LPH);
-    } else {
-      store8(&row_s[wib][grp][d0], x);
-      __syncwarp();
+        for (int e = 0; e < 8; e++) y[e] = __shfl_sync(0xffffffffu, x[e], partner, LPH);
+      } else {
+        store8(&row_s[wib][grp][d0], x);
+        __syncwarp();
 #pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const int d = d0 + e;
-        y[e] = d < p.rot ? row_s[wib][grp][d < half ? d + half : d - half] : 0.f;
+        for (int e = 0; e < 8; e++) {
+          const int d = d0 + e;
+          y[e] = d < p.rot ? row_s[wib][grp][d < half ? d + half : d - half] : 0.f;
+        }
+        __syncwarp();
       }
-      __syncwarp();
-    }
-    if (!is_v) {
       // dimensions past rot pass bit for bit (0 times a partner would not, were it infinite)
 #pragma unroll
       for (int e = 0; e < 8; e++)
         if (d0 + e < p.rot) x[e] = __fmaf_rn(x[e], cs[e], __fmul_rn(y[e], sn[e]));
-    }
-    if (act) {
-      T* dst;
-      if (is_q) dst = static_cast<T*>(p.q) + ri * D;
-      else if (p.form != 2) dst = static_cast<T*>(p.k) + ri * D;
-      else dst = static_cast<T*>(is_v ? p.V[s] : p.K[s]) + (static_cast<size_t>(g) * p.cap + pos) * D;
-      store8(dst + d0, x);
+      if (act) {
+        T* dst;
+        if (is_q) dst = static_cast<T*>(p.q) + (static_cast<size_t>(row) * p.Hq + h) * D;
+        else if (p.form != 2) dst = static_cast<T*>(p.k) + (static_cast<size_t>(row) * p.Hkv + h - p.Hq) * D;
+        else dst = static_cast<T*>(p.K[s]) + (static_cast<size_t>(h - p.Hq) * p.cap + pos) * D;
+        store8(dst + d0, x);
+      }
     }
   }
 }
@@ -178,14 +237,18 @@ static tv_status norm_rope_launch(const tv_attn_layer* l, NormRopeParams& p, con
     const double turns = std::pow(static_cast<double>(theta), -2.0 * j / rot) * 0.15915494309189533577;  // / 2 pi
     p.rate[j] = static_cast<uint64_t>(std::ldexp(turns, 64));
   }
-  const int heads = l->Hq + l->Hkv + (p.form == 2 ? l->Hkv : 0);
-  // heads a warp walks: eight with many rows (the row's sines are formed once
-  // for them), fewer while the launch would leave SMs without work
-  int hpw = 8;
+  // heads a warp walks: one round of its loads with many rows (the row's sines
+  // are formed once for them), fewer while the launch would leave SMs without work
   const int gpw = 256 / l->D;
-  while (hpw > gpw && static_cast<int64_t>(p.n_rows) * ((heads + hpw - 1) / hpw) < 16 * num_sms()) hpw >>= 1;
+  int hpw = gpw * (l->dtype == TV_BF16 ? 8 : 4);
+  auto split = [&]() {
+    p.qk_parts = (l->Hq + l->Hkv + hpw - 1) / hpw;
+    p.parts = p.qk_parts + (p.form == 2 ? (l->Hkv + hpw - 1) / hpw : 0);
+    return static_cast<int64_t>(p.n_rows) * p.parts;
+  };
+  while (hpw > gpw && split() < 16 * num_sms()) hpw >>= 1;
   p.heads_per_warp = hpw;
-  const int64_t warps = static_cast<int64_t>(p.n_rows) * ((heads + hpw - 1) / hpw);
+  const int64_t warps = split();
   const int64_t grid = (warps + 7) / 8;
   if (grid > 0x7fffffff) return TV_ERR_SHAPE;
   const dim3 g(static_cast<unsigned>(grid));
