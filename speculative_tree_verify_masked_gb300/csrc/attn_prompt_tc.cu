@@ -14,9 +14,9 @@
 // because the tensor cores take P and V in one type; l adds the same rounded
 // values, so the weights still sum to one.
 //
-// Roles (320 threads, one CTA per SM, persistent).  Warp 0 streams key and
+// Roles (352 threads, one CTA per SM, persistent).  Warp 0 streams key and
 // value units by TMA through one ring in the order the tensor core takes
-// them: K0, K1 V0, K2 V1, ...  Warp 1 issues the MMAs in that order from one
+// them: K0, K1 V0, K2 V1, ...  Warp 1 issues Q K^T, warp 10 P V, each from one
 // thread.  Warps 2-9 do the softmax, two threads to a row (64 columns each).
 // Tensor memory holds O [D columns], one S [128] and Q [D/2, the A operand of
 // Q K^T], 512 columns at D = 256; P goes through shared memory.  Because PV of
@@ -55,26 +55,24 @@ struct PromptPlan {
   int off[TV_MAX_SEQ], n[TV_MAX_SEQ], L[TV_MAX_SEQ], rt[TV_MAX_SEQ], pm[TV_MAX_SEQ];  // by sequence
 };
 
-template <int D, bool PAIR>
+template <int D>
 struct Pa {
-  static constexpr int NC = PAIR ? 2 : 1;                   // CTAs that share an item
-  static constexpr int UPT = (!PAIR && D == 256) ? 2 : 1;   // ring units per key (or value) tile and CTA
-  static constexpr int UNIT = kKeyTile * D * 2 / NC / UPT;  // bytes of a unit
-  static constexpr int NU = PAIR ? (D == 256 ? 6 : 10) : (D == 64 ? 10 : 6);
-  static constexpr int KROWS = kKeyTile / NC;               // key rows of a K box
-  static constexpr int KBOX = KROWS * 128;                  // bytes of a K box (64 columns)
+  static constexpr int UPT = D == 256 ? 2 : 1;              // ring units per key (or value) tile
+  static constexpr int UNIT = kKeyTile * D * 2 / UPT;       // bytes of a unit
+  static constexpr int NU = D == 64 ? 10 : 6;
+  static constexpr int KBOX = kKeyTile * 128;               // bytes of a K box (128 rows, 64 columns)
   static constexpr int KBU = D / 64 / UPT;                  // K boxes per unit
   static constexpr int VROWS = kKeyTile / UPT;              // positions of a V box
   static constexpr int VBOX = VROWS * 128;
-  static constexpr int VB = D / 64 / NC;                    // V boxes per unit
+  static constexpr int VB = D / 64;                         // V boxes per unit
   static constexpr int PT = 128 * kKeyTile * 2;
   static constexpr int T_O = 0, T_S = D, T_Q = D + 128;
   static constexpr int COLS = D + 128 + D / 2 <= 256 ? 256 : 512;
-  static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128 * NC, kKeyTile, false, false);
-  static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128 * NC, D, false, true);
+  static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, kKeyTile, false, false);
+  static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, false, true);
   static constexpr int XOFF = NU * UNIT + PT;               // half-row maxima [2][2][128] fp32
   static constexpr int BOFF = XOFF + 2 * 2 * 128 * 4;
-  static constexpr int NBAR = 2 * NU + 6 + 4 + 1;
+  static constexpr int NBAR = 2 * NU + 5 + 4 + 2;
   static constexpr int LOFF = (BOFF + NBAR * 8 + 15) / 16 * 16;  // TMEM base, give-up flag, skip flag, plan
   static constexpr int SMEM = LOFF + 16 + static_cast<int>(sizeof(PromptPlan));
   static_assert(KBU * KBOX == UNIT && VB * VBOX == UNIT, "unit shape");
@@ -89,7 +87,7 @@ struct AttnPromptTcParams {
   const __nv_bfloat16* gate;
   __nv_bfloat16* out;
   float* ws;
-  int Hq, Hkv, G, T, TP;  // T tokens per CTA's row tile, TP per item
+  int Hq, Hkv, G, T;  // T tokens per row tile
   int workers, slots;
   float c;  // scale * log2(e)
 };
@@ -116,9 +114,9 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 __device__ inline void make_plan(const AttnPromptTcParams& p, const WarpSeqs& w, int lane, PromptPlan& pl) {
   const int n = w.end - w.off;
   const bool live = lane < p.pr.n_seq && n > 0;
-  const int rt = live ? ceil_div(n, p.TP) : 0;
+  const int rt = live ? ceil_div(n, p.T) : 0;
   const int nk = live ? ceil_div(w.len + n, kKeyTile) : 0;
-  const int nk0 = live ? ceil_div(w.len + min(n, p.TP), kKeyTile) : 0;
+  const int nk0 = live ? ceil_div(w.len + min(n, p.T), kKeyTile) : 0;
   int nkmax = nk;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) nkmax = max(nkmax, __shfl_xor_sync(0xffffffffu, nkmax, o));
@@ -198,7 +196,7 @@ __device__ __forceinline__ PromptItem item_of(const AttnPromptTcParams& p, const
   const int j = r / per, r2 = r % per;
   I.i = pl.rt[I.s] - 1 - r2 / p.Hkv;  // longest row tiles first
   I.g = r2 % p.Hkv;
-  const int nk = ceil_div(pl.L[I.s] + min((I.i + 1) * p.TP, pl.n[I.s]), kKeyTile);
+  const int nk = ceil_div(pl.L[I.s] + min((I.i + 1) * p.T, pl.n[I.s]), kKeyTile);
   I.t0 = j * pl.S;
   I.t1 = min(I.t0 + pl.S, nk);
   I.slot = nk > pl.S ? pl.slot0[at] + r : -1;
@@ -210,9 +208,9 @@ __device__ __forceinline__ int piece_index(int wave, int worker, int workers) {
   return wave * workers + ((wave & 1) ? workers - 1 - worker : worker);
 }
 
-template <int D, bool PAIR>
-__global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_constant__ AttnPromptTcParams p) {
-  using C = Pa<D, PAIR>;
+template <int D>
+__global__ void __launch_bounds__(352, 1) attn_prompt_tc_kernel(const __grid_constant__ AttnPromptTcParams p) {
+  using C = Pa<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];  // tiles are swizzled in 1024-byte atoms
   uint8_t* gb = smem_raw;
   const uint32_t sb = smem_u32(smem_raw);
@@ -221,14 +219,13 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
   const uint32_t bars = sb + C::BOFF;
   const uint32_t UFULL0 = bars, UEMPTY0 = bars + 8u * C::NU;
   const uint32_t SFULL = bars + 16u * C::NU, SFREE = SFULL + 8u, PFULL = SFULL + 16u, ODONE = SFULL + 24u,
-                 QREADY = SFULL + 32u, VTAIL = SFULL + 40u, XBAR0 = SFULL + 48u, DRAIN = XBAR0 + 32u;
+                 QREADY = SFULL + 32u, XBAR0 = SFULL + 40u, DRAIN = XBAR0 + 32u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + C::LOFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int& skip = *reinterpret_cast<int*>(tmem_slot + 2);
   PromptPlan& pl = *reinterpret_cast<PromptPlan*>(gb + C::LOFF + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_rank() : 0u;
-  const int worker = PAIR ? static_cast<int>(blockIdx.x) / 2 : static_cast<int>(blockIdx.x);
+  const int worker = static_cast<int>(blockIdx.x);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NU; i++) {
@@ -236,13 +233,13 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
       mbar_init(UEMPTY0 + 8u * i, 1);
     }
     mbar_init(SFULL, 1);
-    mbar_init(SFREE, 8 * C::NC);
-    mbar_init(PFULL, 8 * C::NC);
+    mbar_init(SFREE, 8);
+    mbar_init(PFULL, 8);
     mbar_init(ODONE, 1);
-    mbar_init(QREADY, 8 * C::NC);
-    mbar_init(VTAIL, 1);
+    mbar_init(QREADY, 8);
     for (int i = 0; i < 4; i++) mbar_init(XBAR0 + 8u * i, 2);
     mbar_init(DRAIN, 1);
+    mbar_init(DRAIN + 8u, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -257,34 +254,22 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
     if (!w.code) make_plan(p, w, lane, pl);
   }
   if (warp == 1) {
-    if (PAIR) {
-      tmem_alloc_pair(smem_u32(tmem_slot), C::COLS);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(smem_u32(tmem_slot), C::COLS);
-      tmem_relinquish();
-    }
+    tmem_alloc(smem_u32(tmem_slot), C::COLS);
+    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync_all();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  // barriers that the issuing CTA (rank 0) waits on
-  const uint32_t rSFREE = PAIR ? map_to_cta(SFREE, 0) : SFREE, rPFULL = PAIR ? map_to_cta(PFULL, 0) : PFULL,
-                 rQREADY = PAIR ? map_to_cta(QREADY, 0) : QREADY;
   auto arrive = [&](uint32_t bar) {  // one arrival per warp, after every lane's fences
     __syncwarp();
-    if (lane == 0) {
-      if (PAIR) mbar_arrive_cluster(bar);
-      else mbar_arrive(bar);
-    }
+    if (lane == 0) mbar_arrive(bar);
   };
   const int total = skip ? 0 : pl.total;
 
   if (warp == 0 && lane == 0) {
     // ---------------- TMA producer ----------------
-    uint32_t it = 0, tails = 0;
+    uint32_t it = 0;
     bool ok = true;
     for (int wave = 0; ok; wave++) {
       if (wave * p.workers >= total) break;
@@ -292,45 +277,27 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
       if (x >= total) continue;
       const PromptItem I = item_of(p, pl, x);
       if (I.t0 >= I.t1) continue;
-      const int n = I.t1 - I.t0, base = I.g * p.pr.cap, end = pl.L[I.s] + pl.n[I.s];
+      const int n = I.t1 - I.t0, base = I.g * p.pr.cap;
       for (int e = 0; e < 2 * n && ok; e++) {
         // load order K0, K1 V0, K2 V1, ..., V(n-1)
         const bool is_k = e == 0 || ((e & 1) && e != 2 * n - 1);
         const int k = e == 0 ? 0 : is_k ? (e + 1) / 2 : (e == 2 * n - 1 ? n - 1 : (e - 2) / 2);
-        const int pos = (I.t0 + k) * kKeyTile;
-        const bool tail = PAIR && !is_k && pos + kKeyTile > end;
+        const int row = base + (I.t0 + k) * kKeyTile;
 #pragma unroll
         for (int u = 0; u < C::UPT; u++, it++) {
-          const uint32_t slot = it % C::NU;
+          const uint32_t slot = it % C::NU, full = UFULL0 + 8u * slot;
           if (!wait_role(UEMPTY0 + 8u * slot, ((it / C::NU) & 1) ^ 1, abort_flag, kWaitCycles)) {
             ok = false;
             break;
           }
           const uint32_t dst = ring + slot * C::UNIT;
-          uint32_t full = UFULL0 + 8u * slot;
-          if (tail) {
-            // this CTA's softmax warps zero rows of the unit first: it lands on
-            // a barrier of their own, and their P arrival stands for it
-            if (rank == 0) mbar_arrive(full);
-            full = VTAIL;
-            mbar_arrive_expect_tx(full, C::UNIT);
-            tails++;
-          } else {
-            if (rank == 0) mbar_arrive_expect_tx(full, C::UNIT * C::NC);
-          }
-          const uint32_t rfull = PAIR ? map_to_cta(full, tail ? rank : 0) : full;
-          auto load = [&](uint32_t d, const CUtensorMap* m, int xx, int yy) {
-            if (PAIR) tma_load_2d_pair(d, m, rfull, xx, yy);
-            else tma_load_2d(d, m, rfull, xx, yy);
-          };
+          mbar_arrive_expect_tx(full, C::UNIT);
           if (is_k) {
 #pragma unroll
-            for (int b = 0; b < C::KBU; b++)
-              load(dst + b * C::KBOX, &p.tmK[I.s], (u * C::KBU + b) * 64, base + pos + static_cast<int>(rank) * C::KROWS);
+            for (int b = 0; b < C::KBU; b++) tma_load_2d(dst + b * C::KBOX, &p.tmK[I.s], full, (u * C::KBU + b) * 64, row);
           } else {
 #pragma unroll
-            for (int b = 0; b < C::VB; b++)
-              load(dst + b * C::VBOX, &p.tmV[I.s], (static_cast<int>(rank) * C::VB + b) * 64, base + pos + u * C::VROWS);
+            for (int b = 0; b < C::VB; b++) tma_load_2d(dst + b * C::VBOX, &p.tmV[I.s], full, b * 64, row + u * C::VROWS);
           }
         }
       }
@@ -338,74 +305,19 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
     if (!ok) {
       set_status(p.pr.status, TV_ERR_TIMEOUT);
       // let every issued copy land before shared memory is released
-      if (rank == 0)
-        for (uint32_t i = it > C::NU ? it - C::NU : 0; i < it; i++)
-          mbar_wait(UFULL0 + 8u * (i % C::NU), (i / C::NU) & 1, kWaitCycles);
-      if (tails) mbar_wait(VTAIL, (tails - 1) & 1, kWaitCycles);
+      for (uint32_t i = it > C::NU ? it - C::NU : 0; i < it; i++)
+        mbar_wait(UFULL0 + 8u * (i % C::NU), (i / C::NU) & 1, kWaitCycles);
     }
-  } else if (warp == 1 && rank == 0) {
-    // ---------------- MMA issuer: a whole-warp loop, one elected lane issues ----------------
-    uint32_t it = 0, t = 0, items = 0;  // units, tiles with an issued Q K^T, items
+  } else if (warp == 1 || warp == 10) {
+    // ---------------- MMA issuers, one warp each, whole-warp loops with one
+    // elected lane issuing.  Issuing blocks while the tensor pipe's short queue
+    // is full, and a wait between two products costs some hundred cycles in
+    // which a single issuer would let the queue run dry: with one warp for both
+    // products a tile took 2,750 cycles, with two it takes about the pipe's
+    // time.  Unit numbers follow the load order. ----------------
+    const bool is_qk = warp == 1;
+    uint32_t base = 0, t = 0, items = 0;  // units and tiles before the item, items
     bool ok = true;
-    auto wait_in = [&](uint32_t bar, uint32_t par) {
-      return PAIR ? wait_warp_cluster(bar, par, abort_flag, kWaitCycles) : wait_warp(bar, par, abort_flag, kWaitCycles);
-    };
-    auto commit = [&](uint32_t bar) {
-      if (PAIR) tc_commit_pair(bar);
-      else tc_commit(bar);
-    };
-    auto do_qk = [&]() {
-      if (t > 0 && !wait_in(SFREE, (t - 1) & 1)) return false;
-#pragma unroll
-      for (int u = 0; u < C::UPT; u++, it++) {
-        const uint32_t slot = it % C::NU;
-        if (!wait_in(UFULL0 + 8u * slot, (it / C::NU) & 1)) return false;
-        tc_fence_after();
-        if (elect_one_sync()) {
-          const uint64_t k0 = sdesc_sw128(ring + slot * C::UNIT, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < C::KBU * 4; kk++) {
-            const uint64_t kd = k0 + static_cast<uint64_t>(((kk >> 2) * C::KBOX + (kk & 3) * 32) >> 4);
-            const uint32_t a = tbase + C::T_Q + (u * C::KBU * 4 + kk) * 8;
-            if (PAIR) tc_mma_ts_pair(tbase + C::T_S, a, kd, C::IDESC_QK, (u > 0 || kk > 0) ? 1u : 0u);
-            else tc_mma_ts(tbase + C::T_S, a, kd, C::IDESC_QK, (u > 0 || kk > 0) ? 1u : 0u);
-          }
-          commit(UEMPTY0 + 8u * slot);
-          if (u == C::UPT - 1) commit(SFULL);
-        }
-        __syncwarp();
-      }
-      t++;
-      return true;
-    };
-    uint32_t tp = 0;
-    auto do_pv = [&](bool acc) {
-      if (!wait_in(PFULL, tp & 1)) return false;
-#pragma unroll
-      for (int u = 0; u < C::UPT; u++, it++) {
-        const uint32_t slot = it % C::NU;
-        if (!wait_in(UFULL0 + 8u * slot, (it / C::NU) & 1)) return false;
-        tc_fence_after();
-        if (elect_one_sync()) {
-          const uint64_t v0 = sdesc_sw128(ring + slot * C::UNIT, C::VBOX, 1024);
-          const uint64_t p0 = sdesc_sw128(pbuf, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < C::VROWS / 16; kk++) {
-            const int pk = u * (C::VROWS / 16) + kk;  // 16-position step of the tile
-            const uint64_t pd = p0 + static_cast<uint64_t>(((pk >> 2) * 16384 + (pk & 3) * 32) >> 4);
-            const uint64_t vd = v0 + static_cast<uint64_t>((kk * 2048) >> 4);
-            const uint32_t on = (acc || pk > 0) ? 1u : 0u;
-            if (PAIR) tc_mma_ss_pair(tbase + C::T_O, pd, vd, C::IDESC_PV, on);
-            else tc_mma_ss(tbase + C::T_O, pd, vd, C::IDESC_PV, on);
-          }
-          commit(UEMPTY0 + 8u * slot);
-          if (u == C::UPT - 1) commit(ODONE);
-        }
-        __syncwarp();
-      }
-      tp++;
-      return true;
-    };
     for (int wave = 0; ok; wave++) {
       if (wave * p.workers >= total) break;
       const int x = piece_index(wave, worker, p.workers);
@@ -413,32 +325,70 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
       const PromptItem I = item_of(p, pl, x);
       if (I.t0 >= I.t1) continue;
       const int n = I.t1 - I.t0;
-      ok = wait_in(QREADY, items & 1);
+      if (is_qk) ok = wait_warp(QREADY, items & 1, abort_flag, kWaitCycles);
       items++;
-      if (ok) {
-        tc_fence_after();
-        ok = do_qk();
+      for (int k = 0; k < n && ok; k++, t++) {
+        if (is_qk) {
+          if (t > 0) ok = wait_warp(SFREE, (t - 1) & 1, abort_flag, kWaitCycles);
+          const uint32_t u0 = base + (k == 0 ? 0 : 2 * k - 1) * C::UPT;
+#pragma unroll
+          for (int u = 0; u < C::UPT; u++) {
+            const uint32_t slot = (u0 + u) % C::NU;
+            ok = ok && wait_warp(UFULL0 + 8u * slot, ((u0 + u) / C::NU) & 1, abort_flag, kWaitCycles);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one_sync()) {
+              const uint64_t k0 = sdesc_sw128(ring + slot * C::UNIT, 16, 1024);
+#pragma unroll
+              for (int kk = 0; kk < C::KBU * 4; kk++)
+                tc_mma_ts(tbase + C::T_S, tbase + C::T_Q + (u * C::KBU * 4 + kk) * 8,
+                          k0 + static_cast<uint64_t>(((kk >> 2) * C::KBOX + (kk & 3) * 32) >> 4), C::IDESC_QK,
+                          (u > 0 || kk > 0) ? 1u : 0u);
+              tc_commit(UEMPTY0 + 8u * slot);
+              if (u == C::UPT - 1) tc_commit(SFULL);
+            }
+            __syncwarp();
+          }
+        } else {
+          ok = wait_warp(PFULL, t & 1, abort_flag, kWaitCycles);
+          const uint32_t u0 = base + (k < n - 1 ? 2 * k + 2 : 2 * n - 1) * C::UPT;
+#pragma unroll
+          for (int u = 0; u < C::UPT; u++) {
+            const uint32_t slot = (u0 + u) % C::NU;
+            ok = ok && wait_warp(UFULL0 + 8u * slot, ((u0 + u) / C::NU) & 1, abort_flag, kWaitCycles);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one_sync()) {
+              const uint64_t v0 = sdesc_sw128(ring + slot * C::UNIT, C::VBOX, 1024);
+              const uint64_t p0 = sdesc_sw128(pbuf, 16, 1024);
+#pragma unroll
+              for (int kk = 0; kk < C::VROWS / 16; kk++) {
+                const int pk = u * (C::VROWS / 16) + kk;  // 16-position step of the tile
+                tc_mma_ss(tbase + C::T_O, p0 + static_cast<uint64_t>(((pk >> 2) * 16384 + (pk & 3) * 32) >> 4),
+                          v0 + static_cast<uint64_t>((kk * 2048) >> 4), C::IDESC_PV, (k > 0 || pk > 0) ? 1u : 0u);
+              }
+              tc_commit(UEMPTY0 + 8u * slot);
+              if (u == C::UPT - 1) tc_commit(ODONE);
+            }
+            __syncwarp();
+          }
+        }
       }
-      for (int k = 0; k < n && ok; k++) {
-        if (k + 1 < n) ok = do_qk();
-        if (ok) ok = do_pv(k > 0);
-      }
+      base += 2 * n * C::UPT;
     }
     if (!ok && lane == 0) set_status(p.pr.status, TV_ERR_TIMEOUT);
-    // every MMA completes before tensor and shared memory are released
-    if (elect_one_sync()) {
-      if (PAIR) tc_commit_pair(DRAIN);
-      else tc_commit(DRAIN);
-    }
+    // every MMA of this warp completes before tensor and shared memory are released
+    const uint32_t drain = DRAIN + (is_qk ? 0u : 8u);
+    if (elect_one_sync()) tc_commit(drain);
     __syncwarp();
-    mbar_wait(DRAIN, 0, kWaitCycles);
+    mbar_wait(drain, 0, kWaitCycles);
   } else if (warp >= 2) {
     // ---------------- softmax and output, two threads to a row ----------------
     const int hf = (warp - 2) >> 2, quad = warp & 3, lrow = quad * 32 + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t patch = pbuf + static_cast<uint32_t>(warp - 2) * 4096u;  // this warp's 4 KB between items
     const int tok = lrow / p.G, head = lrow % p.G;
-    uint32_t t = 0, xc = 0, tails = 0, it = 0;  // tiles, exchanges, zeroed value tiles, units before the item
+    uint32_t t = 0, xc = 0, it = 0;  // tiles, exchanges, units before the item
     bool ok = true;
     // the two threads of a row exchange a value
     auto exchange = [&](float v, float& other) {
@@ -458,10 +408,10 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
       const PromptItem I = item_of(p, pl, x);
       if (I.t0 >= I.t1) continue;
       const int n = I.t1 - I.t0, L = pl.L[I.s], end = L + pl.n[I.s];
-      const int token = I.i * p.TP + static_cast<int>(rank) * p.T + tok;
+      const int token = I.i * p.T + tok;
       const bool act = tok < p.T && token < pl.n[I.s];
       const int last = act ? L + token : -1;  // last position this row sees
-      const int seen_all = L + I.i * p.TP + static_cast<int>(rank) * p.T + 1;  // positions every row here sees
+      const int seen_all = L + I.i * p.T + 1;  // positions every row here sees
       // this thread's row of q and out (elements); kNoRow: none
       const int64_t orow = act ? ((static_cast<int64_t>(pl.off[I.s]) + token) * p.Hq + I.g * p.G + head) * D : kNoRow;
       // Q into tensor memory (every Q K^T of the previous item has completed:
@@ -499,7 +449,25 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
         tmem_st_wait();
       }
       tc_fence_before();
-      arrive(rQREADY);
+      arrive(QREADY);
+      // into L2 while this item runs: its gate rows, and the next item's queries
+      if (p.gate && act && I.slot < 0) {
+#pragma unroll
+        for (int b = 0; b < D; b += 128) prefetch_l2(reinterpret_cast<const char*>(p.gate + orow) + hf * D + b);
+      }
+      {
+        const int xn = (wave + 1) * p.workers < total ? piece_index(wave + 1, worker, p.workers) : total;
+        if (xn < total) {
+          const PromptItem N = item_of(p, pl, xn);
+          const int tn = N.i * p.T + tok;
+          if (tok < p.T && tn < pl.n[N.s]) {
+            const char* qn = reinterpret_cast<const char*>(
+                p.q + ((static_cast<int64_t>(pl.off[N.s]) + tn) * p.Hq + N.g * p.G + head) * D);
+#pragma unroll
+            for (int b = 0; b < D; b += 128) prefetch_l2(qn + hf * D + b);
+          }
+        }
+      }
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < n; k++, t++) {
         if (!wait_warp(SFULL, t & 1, abort_flag, kWaitCycles)) {
@@ -518,7 +486,7 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
           for (int i = 0; i < 32; i++) sv[32 + i] = __uint_as_float(r[i]);
         }
         tc_fence_before();
-        arrive(rSFREE);
+        arrive(SFREE);
         const int pos = (I.t0 + k) * kKeyTile;
         if (pos + kKeyTile > seen_all) {  // a tile some row here does not see whole
           const int vis = last - (pos + hf * 64);
@@ -584,11 +552,8 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
           for (int u = 0; u < C::UPT; u++) {
             const uint32_t i = it + (2 * n - 1) * C::UPT + u;
             slot[u] = i % C::NU;
-            const bool landed = PAIR ? wait_warp(VTAIL, tails & 1, abort_flag, kWaitCycles)
-                                     : wait_warp(UFULL0 + 8u * slot[u], (i / C::NU) & 1, abort_flag, kWaitCycles);
-            ok = ok && landed;
+            ok = ok && wait_warp(UFULL0 + 8u * slot[u], (i / C::NU) & 1, abort_flag, kWaitCycles);
           }
-          tails++;
           if (!ok) break;
           for (int e = static_cast<int>(threadIdx.x) - 64; e < (kKeyTile - first) * C::VB * 8; e += 256) {
             const int row = first + e / (C::VB * 8), c = e % (C::VB * 8);
@@ -599,7 +564,7 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        arrive(rPFULL);
+        arrive(PFULL);
       }
       it += 2 * n * C::UPT;
       if (!ok) break;
@@ -610,11 +575,19 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
       }
       tc_fence_after();
       const float inv = __fdiv_rn(1.f, __fadd_rn(l, lo));
-      float* rec = I.slot >= 0 ? p.ws + ((static_cast<size_t>(I.slot) * C::NC + rank) * 128 + lrow) * (D + 4) : nullptr;
+      float* rec = I.slot >= 0 ? p.ws + (static_cast<size_t>(I.slot) * 128 + lrow) * (D + 4) : nullptr;
       // O by 32 columns, turned around in this warp's patch (rows of 128 bytes)
       // so that a store covers whole pieces of rows
 #pragma unroll 1
       for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
+        uint4 gv[4];  // the gates of the rows this lane writes
+        if (p.gate && I.slot < 0) {
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int64_t ro = __shfl_sync(0xffffffffu, orow, 8 * i + (lane >> 2));
+            if (ro >= 0) gv[i] = *reinterpret_cast<const uint4*>(p.gate + ro + c + (lane & 3) * 8);
+          }
+        }
         uint32_t r[32];
         tmem_ld32(tl + C::T_O + c, r);
         __syncwarp();
@@ -644,10 +617,10 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
                         __uint_as_float(x1.x) * f, __uint_as_float(x1.y) * f, __uint_as_float(x1.z) * f, __uint_as_float(x1.w) * f};
           const int64_t at = ro + c + (lane & 3) * 8;
           if (p.gate) {
-            float gv[8];
-            load8(p.gate + at, gv);
+            float gf[8];
+            widen8(gv[i], gf);
 #pragma unroll
-            for (int e = 0; e < 8; e++) y[e] = fast_gate(y[e], gv[e]);
+            for (int e = 0; e < 8; e++) y[e] = fast_gate(y[e], gf[e]);
           }
           store8(p.out + at, y);
         }
@@ -662,19 +635,15 @@ __global__ void __launch_bounds__(320, 1) attn_prompt_tc_kernel(const __grid_con
   }
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync_all();  // no CTA's memory goes while the other still uses it
   tc_fence_after();
-  if (warp == 1) {
-    if (PAIR) tmem_dealloc_pair(tbase, C::COLS);
-    else tmem_dealloc(tbase, C::COLS);
-  }
+  if (warp == 1) tmem_dealloc(tbase, C::COLS);
 }
 
 // Joins the pieces of split items, in order: a warp takes 128 columns of a row,
 // four a lane, several pieces' loads in flight.
-template <int D, bool PAIR>
+template <int D>
 __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_constant__ AttnPromptTcParams p) {
-  constexpr int NC = PAIR ? 2 : 1, CB = D > 128 ? D / 128 : 1, LPR = D >= 128 ? 32 : D / 4, RPW = 32 / LPR;
+  constexpr int CB = D > 128 ? D / 128 : 1, LPR = D >= 128 ? 32 : D / 4, RPW = 32 / LPR;
   __shared__ PromptPlan pl;
   __shared__ int skip;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -696,13 +665,13 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
       if (x >= static_cast<int64_t>(pl.n[s]) * p.Hq) continue;
       const int col = static_cast<int>(u % CB) * 128 + (lane % LPR) * 4;
       const int token = static_cast<int>(x / p.Hq), h = static_cast<int>(x % p.Hq), g = h / p.G;
-      const int i = token / p.TP, rank = token % p.TP / p.T, lrow = (token % p.TP % p.T) * p.G + h % p.G;
-      const int nk = ceil_div(pl.L[s] + min((i + 1) * p.TP, pl.n[s]), kKeyTile);
+      const int i = token / p.T, lrow = token % p.T * p.G + h % p.G;
+      const int nk = ceil_div(pl.L[s] + min((i + 1) * p.T, pl.n[s]), kKeyTile);
       const int np = ceil_div(nk, pl.S);
       if (np < 2) continue;  // written whole
       const int per = p.Hkv * pl.rt[s], first = pl.slot0[at] + (pl.rt[s] - 1 - i) * p.Hkv + g;
-      const float* rec = p.ws + ((static_cast<size_t>(first) * NC + rank) * 128 + lrow) * (D + 4);
-      const size_t step = static_cast<size_t>(per) * NC * 128 * (D + 4);
+      const float* rec = p.ws + (static_cast<size_t>(first) * 128 + lrow) * (D + 4);
+      const size_t step = static_cast<size_t>(per) * 128 * (D + 4);
       // one pass with a running maximum, four pieces at a time
       float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
       for (int j0 = 0; j0 < np; j0 += 4) {
@@ -763,44 +732,42 @@ static bool encode_rows_map(CUtensorMap* m, void* base, int D, int64_t rows, int
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Workspace records (one per piece, NC x 128 rows of D + 4 fp32) a call may
-// use: never more than its items can be cut into.
-template <int NC>
+// Workspace records (one per piece, 128 rows of D + 4 fp32) a call may use:
+// never more than its items can be cut into.
 static int64_t slots_for(const tv_attn_layer* l, const tv_prompt* pr, int max_len) {
-  const int64_t tp = 128 / (l->Hq / l->Hkv) * NC;
-  const int64_t items = l->Hkv * ((pr->n_total + tp - 1) / tp + pr->n_seq);
+  const int64_t t = 128 / (l->Hq / l->Hkv);
+  const int64_t items = l->Hkv * ((pr->n_total + t - 1) / t + pr->n_seq);
   const int64_t nk = (static_cast<int64_t>(max_len) + pr->n_max + kKeyTile - 1) / kKeyTile;
   if (nk <= kPieceTiles) return 0;
-  const int64_t all = items * ((nk + kPieceTiles - 1) / kPieceTiles), cap = static_cast<int64_t>(kSlotsPerSm) * 152 / NC;
+  const int64_t all = items * ((nk + kPieceTiles - 1) / kPieceTiles), cap = static_cast<int64_t>(kSlotsPerSm) * 152;
   return all < cap ? all : cap;
 }
 
-template <int D, bool PAIR>
+template <int D>
 static tv_status launch_prompt_tc(AttnPromptTcParams& p, const AttnPromptCall& a, cudaStream_t st) {
-  using C = Pa<D, PAIR>;
+  using C = Pa<D>;
   const tv_attn_layer* l = a.layer;
   for (int s = 0; s < a.prompt->n_seq; s++)
-    if (!encode_rows_map(&p.tmK[s], l->K[s], D, static_cast<int64_t>(l->Hkv) * l->cap, C::KROWS) ||
+    if (!encode_rows_map(&p.tmK[s], l->K[s], D, static_cast<int64_t>(l->Hkv) * l->cap, kKeyTile) ||
         !encode_rows_map(&p.tmV[s], l->V[s], D, static_cast<int64_t>(l->Hkv) * l->cap, C::VROWS))
       return TV_ERR_CUDA;
   p.T = 128 / p.G;
-  p.TP = p.T * C::NC;
-  p.slots = static_cast<int>(slots_for<C::NC>(l, a.prompt, a.max_len));
-  static int workers = 0;
-  if (!workers) {
-    if (cudaFuncSetAttribute(attn_prompt_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+  p.slots = static_cast<int>(slots_for(l, a.prompt, a.max_len));
+  p.workers = num_sms();
+  static bool set = false;
+  if (!set) {
+    if (cudaFuncSetAttribute(attn_prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
       return TV_ERR_CUDA;
-    workers = num_sms();
+    set = true;
   }
-  p.workers = workers;
-  attn_prompt_tc_kernel<D, PAIR><<<dim3(p.workers), 320, C::SMEM, st>>>(p);
+  attn_prompt_tc_kernel<D><<<dim3(p.workers), 352, C::SMEM, st>>>(p);
   // the join has work only where the plan, made on the device, split items
-  if (p.slots > 0) launch_k(true, attn_prompt_join_kernel<D, PAIR>, dim3(num_sms() * 4), dim3(256), 0, st, p);
+  if (p.slots > 0) launch_k(true, attn_prompt_join_kernel<D>, dim3(num_sms() * 4), dim3(256), 0, st, p);
   return launch_status();
 }
 
 size_t attn_prompt_tc_ws_bytes(const tv_attn_layer* l, const tv_prompt* pr, int max_len) {
-  return static_cast<size_t>(slots_for<1>(l, pr, max_len)) * 128 * (l->D + 4) * 4;
+  return static_cast<size_t>(slots_for(l, pr, max_len)) * 128 * (l->D + 4) * 4;
 }
 
 tv_status attn_prompt_tc_launch(const AttnPromptCall& a, cudaStream_t st) {
@@ -821,9 +788,9 @@ tv_status attn_prompt_tc_launch(const AttnPromptCall& a, cudaStream_t st) {
   p.G = l->Hq / l->Hkv;
   p.c = a.scale * 1.4426950408889634f;
   switch (l->D) {
-    case 64: return launch_prompt_tc<64, false>(p, a, st);
-    case 128: return launch_prompt_tc<128, false>(p, a, st);
-    default: return launch_prompt_tc<256, false>(p, a, st);
+    case 64: return launch_prompt_tc<64>(p, a, st);
+    case 128: return launch_prompt_tc<128>(p, a, st);
+    default: return launch_prompt_tc<256>(p, a, st);
   }
 }
 
