@@ -14,10 +14,10 @@
 // because the tensor cores take P and V in one type; l adds the same rounded
 // values, so the weights still sum to one.
 //
-// Roles (352 threads, one CTA per SM, persistent).  Warp 0 streams key and
+// Roles (384 threads, one CTA per SM, persistent).  Warp 0 streams key and
 // value units by TMA through one ring in the order the tensor core takes
-// them: K0, K1 V0, K2 V1, ...  Warp 1 issues Q K^T, warp 10 P V, each from one
-// thread.  Warps 2-9 do the softmax, two threads to a row (64 columns each).
+// them: K0, K1 V0, K2 V1, ...  Warp 11 brings each item's queries, warp 1
+// issues Q K^T, warp 10 P V, each from one thread.  Warps 2-9 do the softmax, two threads to a row (64 columns each).
 // Tensor memory holds O [D columns], one S [128] and Q [D/2, the A operand of
 // Q K^T], 512 columns at D = 256; P goes through shared memory.  Because PV of
 // tile t-1 sits between Q K^T of t and of t+1 on the tensor pipe, S(t) is read
@@ -59,20 +59,24 @@ template <int D>
 struct Pa {
   static constexpr int UPT = D == 256 ? 2 : 1;              // ring units per key (or value) tile
   static constexpr int UNIT = kKeyTile * D * 2 / UPT;       // bytes of a unit
-  static constexpr int NU = D == 64 ? 10 : 6;
+  static constexpr int NU = D == 64 ? 10 : 5;
   static constexpr int KBOX = kKeyTile * 128;               // bytes of a K box (128 rows, 64 columns)
   static constexpr int KBU = D / 64 / UPT;                  // K boxes per unit
   static constexpr int VROWS = kKeyTile / UPT;              // positions of a V box
   static constexpr int VBOX = VROWS * 128;
   static constexpr int VB = D / 64;                         // V boxes per unit
   static constexpr int PT = 128 * kKeyTile * 2;
+  static constexpr int QR = D == 256 ? 2 : 1;               // 64-column boxes of Q per half of the softmax, one at a time
+  static constexpr int QH = D == 64 ? 1 : 2;                // halves that move Q
+  static constexpr int QBOX = 128 * 128;
   static constexpr int T_O = 0, T_S = D, T_Q = D + 128;
   static constexpr int COLS = D + 128 + D / 2 <= 256 ? 256 : 512;
   static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, kKeyTile, false, false);
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, false, true);
-  static constexpr int XOFF = NU * UNIT + PT;               // half-row maxima [2][2][128] fp32
+  static constexpr int QOFF = NU * UNIT + PT;               // Q on its way into tensor memory
+  static constexpr int XOFF = QOFF + QH * QBOX;             // half-row maxima [2][2][128] fp32
   static constexpr int BOFF = XOFF + 2 * 2 * 128 * 4;
-  static constexpr int NBAR = 2 * NU + 5 + 4 + 2;
+  static constexpr int NBAR = 2 * NU + 5 + 4 + 2 + 4;
   static constexpr int LOFF = (BOFF + NBAR * 8 + 15) / 16 * 16;  // TMEM base, give-up flag, skip flag, plan
   static constexpr int SMEM = LOFF + 16 + static_cast<int>(sizeof(PromptPlan));
   static_assert(KBU * KBOX == UNIT && VB * VBOX == UNIT, "unit shape");
@@ -82,8 +86,8 @@ struct Pa {
 struct AttnPromptTcParams {
   CUtensorMap tmK[TV_MAX_SEQ];
   CUtensorMap tmV[TV_MAX_SEQ];
+  CUtensorMap tmQ;  // [n_total][Hq][D] in boxes of T tokens, G heads, 64 columns
   PromptRows pr;
-  const __nv_bfloat16* q;
   const __nv_bfloat16* gate;
   __nv_bfloat16* out;
   float* ws;
@@ -105,6 +109,16 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
 // x * sigmoid(g) with the fast exponential and divide (a few fp32 steps, far
 // below the bf16 rounding that follows).
 __device__ __forceinline__ float fast_gate(float x, float g) { return x * __fdividef(1.f, 1.f + __expf(-g)); }
+// Two at a time with one reciprocal, 1/a = b (1/ab): the special-function unit
+// bounds the epilogue.  e^-g is held below 2^63 so that the product stays
+// finite (a gate under -43.6 then leaves 1e-19 of x, not less).
+__device__ __forceinline__ void fast_gate2(float& x, float& y, float gx, float gy) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float a = 1.f + ex2_approx(fminf(-kLog2e * gx, 63.f)), b = 1.f + ex2_approx(fminf(-kLog2e * gy, 63.f));
+  const float r = __fdividef(1.f, a * b);
+  x *= b * r;
+  y *= a * r;
+}
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -208,8 +222,21 @@ __device__ __forceinline__ int piece_index(int wave, int worker, int workers) {
   return wave * workers + ((wave & 1) ? workers - 1 - worker : worker);
 }
 
+// The worker's next piece with tiles, from wave `wave` on; false: none left.
+__device__ __forceinline__ bool next_item(const AttnPromptTcParams& p, const PromptPlan& pl, int total, int worker, int& wave,
+                                          PromptItem& I) {
+  while (wave * p.workers < total) {
+    const int x = piece_index(wave, worker, p.workers);
+    wave++;
+    if (x >= total) continue;
+    I = item_of(p, pl, x);
+    if (I.t0 < I.t1) return true;
+  }
+  return false;
+}
+
 template <int D>
-__global__ void __launch_bounds__(352, 1) attn_prompt_tc_kernel(const __grid_constant__ AttnPromptTcParams p) {
+__global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_constant__ AttnPromptTcParams p) {
   using C = Pa<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];  // tiles are swizzled in 1024-byte atoms
   uint8_t* gb = smem_raw;
@@ -219,7 +246,8 @@ __global__ void __launch_bounds__(352, 1) attn_prompt_tc_kernel(const __grid_con
   const uint32_t bars = sb + C::BOFF;
   const uint32_t UFULL0 = bars, UEMPTY0 = bars + 8u * C::NU;
   const uint32_t SFULL = bars + 16u * C::NU, SFREE = SFULL + 8u, PFULL = SFULL + 16u, ODONE = SFULL + 24u,
-                 QREADY = SFULL + 32u, XBAR0 = SFULL + 40u, DRAIN = XBAR0 + 32u;
+                 QREADY = SFULL + 32u, XBAR0 = SFULL + 40u, DRAIN = XBAR0 + 32u,
+                 QFULL0 = DRAIN + 16u, QEMPTY0 = QFULL0 + 16u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + C::LOFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int& skip = *reinterpret_cast<int*>(tmem_slot + 2);
@@ -240,6 +268,10 @@ __global__ void __launch_bounds__(352, 1) attn_prompt_tc_kernel(const __grid_con
     for (int i = 0; i < 4; i++) mbar_init(XBAR0 + 8u * i, 2);
     mbar_init(DRAIN, 1);
     mbar_init(DRAIN + 8u, 1);
+    for (int i = 0; i < 2; i++) {
+      mbar_init(QFULL0 + 8u * i, 1);
+      mbar_init(QEMPTY0 + 8u * i, 4);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -271,12 +303,9 @@ __global__ void __launch_bounds__(352, 1) attn_prompt_tc_kernel(const __grid_con
     // ---------------- TMA producer ----------------
     uint32_t it = 0;
     bool ok = true;
-    for (int wave = 0; ok; wave++) {
-      if (wave * p.workers >= total) break;
-      const int x = piece_index(wave, worker, p.workers);
-      if (x >= total) continue;
-      const PromptItem I = item_of(p, pl, x);
-      if (I.t0 >= I.t1) continue;
+    int wave = 0;
+    PromptItem I;
+    while (ok && next_item(p, pl, total, worker, wave, I)) {
       const int n = I.t1 - I.t0, base = I.g * p.pr.cap;
       for (int e = 0; e < 2 * n && ok; e++) {
         // load order K0, K1 V0, K2 V1, ..., V(n-1)
@@ -308,6 +337,31 @@ __global__ void __launch_bounds__(352, 1) attn_prompt_tc_kernel(const __grid_con
       for (uint32_t i = it > C::NU ? it - C::NU : 0; i < it; i++)
         mbar_wait(UFULL0 + 8u * (i % C::NU), (i / C::NU) & 1, kWaitCycles);
     }
+  } else if (warp == 11 && lane == 0) {
+    // ---------------- queries (and, into L2, gates) of the items ahead ----------------
+    uint32_t t = 0;
+    bool ok = true;
+    int wave = 0;
+    PromptItem I;
+    while (ok && next_item(p, pl, total, worker, wave, I)) {
+      const int first = pl.off[I.s] + I.i * p.T, live = min(p.T, pl.n[I.s] - I.i * p.T);
+      for (int r = 0; r < C::QR && ok; r++, t++)
+#pragma unroll
+        for (int h = 0; h < C::QH; h++) {
+          ok = ok && wait_role(QEMPTY0 + 8u * h, (t & 1) ^ 1, abort_flag, kWaitCycles);
+          if (!ok) break;
+          mbar_arrive_expect_tx(QFULL0 + 8u * h, static_cast<uint32_t>(p.T * p.G) * 128u);
+          tma_load_3d(sb + C::QOFF + h * C::QBOX, &p.tmQ, QFULL0 + 8u * h, (h * C::QR + r) * 64, I.g * p.G, first);
+        }
+      if (p.gate && I.slot < 0)  // (a token's heads of one KV head are contiguous)
+        for (int x = 0; x < live; x++)
+          bulk_prefetch_l2(p.gate + ((static_cast<int64_t>(first) + x) * p.Hq + I.g * p.G) * D, p.G * D * 2);
+    }
+    if (!ok) {
+      set_status(p.pr.status, TV_ERR_TIMEOUT);
+      for (int h = 0; h < C::QH; h++)
+        if (t > 0) mbar_wait(QFULL0 + 8u * h, (t - 1) & 1, kWaitCycles);
+    }
   } else if (warp == 1 || warp == 10) {
     // ---------------- MMA issuers, one warp each, whole-warp loops with one
     // elected lane issuing.  Issuing blocks while the tensor pipe's short queue
@@ -318,12 +372,9 @@ __global__ void __launch_bounds__(352, 1) attn_prompt_tc_kernel(const __grid_con
     const bool is_qk = warp == 1;
     uint32_t base = 0, t = 0, items = 0;  // units and tiles before the item, items
     bool ok = true;
-    for (int wave = 0; ok; wave++) {
-      if (wave * p.workers >= total) break;
-      const int x = piece_index(wave, worker, p.workers);
-      if (x >= total) continue;
-      const PromptItem I = item_of(p, pl, x);
-      if (I.t0 >= I.t1) continue;
+    int wave = 0;
+    PromptItem I;
+    while (ok && next_item(p, pl, total, worker, wave, I)) {
       const int n = I.t1 - I.t0;
       if (is_qk) ok = wait_warp(QREADY, items & 1, abort_flag, kWaitCycles);
       items++;
@@ -382,11 +433,11 @@ __global__ void __launch_bounds__(352, 1) attn_prompt_tc_kernel(const __grid_con
     if (elect_one_sync()) tc_commit(drain);
     __syncwarp();
     mbar_wait(drain, 0, kWaitCycles);
-  } else if (warp >= 2) {
+  } else if (warp >= 2 && warp < 10) {
     // ---------------- softmax and output, two threads to a row ----------------
     const int hf = (warp - 2) >> 2, quad = warp & 3, lrow = quad * 32 + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t patch = pbuf + static_cast<uint32_t>(warp - 2) * 4096u;  // this warp's 4 KB between items
+    const uint32_t patch = pbuf + hf * 16384 + quad * 4096;  // where this warp writes P: 4 KB of its own between items
     const int tok = lrow / p.G, head = lrow % p.G;
     uint32_t t = 0, xc = 0, it = 0;  // tiles, exchanges, units before the item
     bool ok = true;
@@ -401,73 +452,50 @@ __global__ void __launch_bounds__(352, 1) attn_prompt_tc_kernel(const __grid_con
       xc++;
       return true;
     };
-    for (int wave = 0; ok; wave++) {
-      if (wave * p.workers >= total) break;
-      const int x = piece_index(wave, worker, p.workers);
-      if (x >= total) continue;
-      const PromptItem I = item_of(p, pl, x);
-      if (I.t0 >= I.t1) continue;
-      const int n = I.t1 - I.t0, L = pl.L[I.s], end = L + pl.n[I.s];
+    // this thread's row of q and out of an item (elements); kNoRow: none
+    auto row_of = [&](const PromptItem& I) -> int64_t {
       const int token = I.i * p.T + tok;
-      const bool act = tok < p.T && token < pl.n[I.s];
-      const int last = act ? L + token : -1;  // last position this row sees
-      const int seen_all = L + I.i * p.T + 1;  // positions every row here sees
-      // this thread's row of q and out (elements); kNoRow: none
-      const int64_t orow = act ? ((static_cast<int64_t>(pl.off[I.s]) + token) * p.Hq + I.g * p.G + head) * D : kNoRow;
-      // Q into tensor memory (every Q K^T of the previous item has completed:
-      // its S was read).  A warp reads its rows in whole 128-byte pieces and
-      // turns them around in shared memory.  P's buffer is free for it: no
-      // softmax warp writes P again before every warp's queries are in.
-      if (D >= 128 || hf == 0) {
+      return tok < p.T && token < pl.n[I.s] ? ((static_cast<int64_t>(pl.off[I.s]) + token) * p.Hq + I.g * p.G + head) * D : kNoRow;
+    };
+    // Q of an item into tensor memory, each thread its half of its row, once
+    // every Q K^T of the item before has completed (its last S has been read)
+    uint32_t qt = 0;
+    auto load_q = [&]() {
+      if (hf < C::QH) {
 #pragma unroll
-        for (int pc = 0; pc < (D >= 128 ? D / 128 : 1); pc++) {
-          const int col = (D >= 128 ? hf * (D / 2) : 0) + pc * 64;
-          uint4 v[8];
+        for (int r = 0; r < C::QR; r++, qt++) {
+          if (!wait_warp(QFULL0 + 8u * hf, qt & 1, abort_flag, kWaitCycles)) return false;
+          uint32_t v[32];
 #pragma unroll
           for (int i = 0; i < 8; i++) {
-            const int64_t ro = __shfl_sync(0xffffffffu, orow, 4 * i + (lane >> 3));
-            v[i] = ro >= 0 ? *reinterpret_cast<const uint4*>(p.q + ro + col + (lane & 7) * 8) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 x = ld_shared16(sb + C::QOFF + hf * C::QBOX + lrow * 128 + (((i ^ lrow) & 7) << 4));
+            v[4 * i] = x.x;
+            v[4 * i + 1] = x.y;
+            v[4 * i + 2] = x.z;
+            v[4 * i + 3] = x.w;
           }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; i++) {
-            const int rr = 4 * i + (lane >> 3);
-            st_shared16(patch + rr * 128 + (((lane ^ rr) & 7) << 4), v[i]);
-          }
-          __syncwarp();
-          uint32_t r[32];
-#pragma unroll
-          for (int i = 0; i < 8; i++) {
-            const uint4 x = ld_shared16(patch + lane * 128 + (((i ^ lane) & 7) << 4));
-            r[4 * i] = x.x;
-            r[4 * i + 1] = x.y;
-            r[4 * i + 2] = x.z;
-            r[4 * i + 3] = x.w;
-          }
-          tmem_st32(tl + C::T_Q + col / 2, r);
+          arrive(QEMPTY0 + 8u * hf);
+          tmem_st32(tl + C::T_Q + (hf * C::QR + r) * 32, v);
         }
         tmem_st_wait();
       }
       tc_fence_before();
       arrive(QREADY);
-      // into L2 while this item runs: its gate rows, and the next item's queries
-      if (p.gate && act && I.slot < 0) {
-#pragma unroll
-        for (int b = 0; b < D; b += 128) prefetch_l2(reinterpret_cast<const char*>(p.gate + orow) + hf * D + b);
-      }
-      {
-        const int xn = (wave + 1) * p.workers < total ? piece_index(wave + 1, worker, p.workers) : total;
-        if (xn < total) {
-          const PromptItem N = item_of(p, pl, xn);
-          const int tn = N.i * p.T + tok;
-          if (tok < p.T && tn < pl.n[N.s]) {
-            const char* qn = reinterpret_cast<const char*>(
-                p.q + ((static_cast<int64_t>(pl.off[N.s]) + tn) * p.Hq + N.g * p.G + head) * D);
-#pragma unroll
-            for (int b = 0; b < D; b += 128) prefetch_l2(qn + hf * D + b);
-          }
-        }
-      }
+      return true;
+    };
+    int wave = 0;
+    PromptItem I;
+    bool more = next_item(p, pl, total, worker, wave, I);
+    int64_t orow = kNoRow;
+    if (more) {
+      orow = row_of(I);
+      ok = load_q();
+    }
+    while (ok && more) {
+      const int n = I.t1 - I.t0, L = pl.L[I.s], end = L + pl.n[I.s];
+      const bool act = orow >= 0;
+      const int last = act ? L + I.i * p.T + tok : -1;  // last position this row sees
+      const int seen_all = L + I.i * p.T + 1;           // positions every row here sees
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < n; k++, t++) {
         if (!wait_warp(SFULL, t & 1, abort_flag, kWaitCycles)) {
@@ -568,6 +596,29 @@ __global__ void __launch_bounds__(352, 1) attn_prompt_tc_kernel(const __grid_con
       }
       it += 2 * n * C::UPT;
       if (!ok) break;
+      const int slot = I.slot;
+      const int64_t row = orow;
+      more = next_item(p, pl, total, worker, wave, I);
+      if (more) {  // the next item's first Q K^T runs beside this one's last P V and output
+        orow = row_of(I);
+        if (!load_q()) {
+          ok = false;
+          break;
+        }
+      }
+      // the gates of this warp's rows, 16-byte pieces spread over its lanes, CW
+      // columns at a time, each loaded while the columns before are worked on
+      constexpr int CW = D >= 128 ? 64 : 32, Q = CW / 8;
+      const int prow = lane / Q, pq = lane % Q;  // the row (of 32 / Q) and piece this lane moves
+      uint4 gv[Q];
+      auto fetch_gate = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < Q; i++) {
+          const int64_t ro = __shfl_sync(0xffffffffu, row, i * (32 / Q) + prow);  // (idle rows: any row will do)
+          gv[i] = *reinterpret_cast<const uint4*>(p.gate + (ro < 0 ? 0 : ro) + c + pq * 8);
+        }
+      };
+      if (p.gate && slot < 0) fetch_gate(hf * (D / 2));
       float lo;
       if (!exchange(l, lo) || !wait_warp(ODONE, (t - 1) & 1, abort_flag, kWaitCycles)) {
         ok = false;
@@ -575,59 +626,74 @@ __global__ void __launch_bounds__(352, 1) attn_prompt_tc_kernel(const __grid_con
       }
       tc_fence_after();
       const float inv = __fdiv_rn(1.f, __fadd_rn(l, lo));
-      float* rec = I.slot >= 0 ? p.ws + (static_cast<size_t>(I.slot) * 128 + lrow) * (D + 4) : nullptr;
-      // O by 32 columns, turned around in this warp's patch (rows of 128 bytes)
-      // so that a store covers whole pieces of rows
+      // Rows leave through this warp's patch, where they are turned around so
+      // that an instruction covers whole pieces of rows.
+      if (slot >= 0) {  // a piece: O, m and l as they are, 32 columns at a time
+        float* rec = p.ws + (static_cast<size_t>(slot) * 128 + lrow) * (D + 4);
 #pragma unroll 1
-      for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
-        uint4 gv[4];  // the gates of the rows this lane writes
-        if (p.gate && I.slot < 0) {
+        for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
+          uint32_t r[32];
+          tmem_ld32(tl + C::T_O + c, r);
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const int64_t ro = __shfl_sync(0xffffffffu, orow, 8 * i + (lane >> 2));
-            if (ro >= 0) gv[i] = *reinterpret_cast<const uint4*>(p.gate + ro + c + (lane & 3) * 8);
-          }
-        }
-        uint32_t r[32];
-        tmem_ld32(tl + C::T_O + c, r);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-          st_shared16(patch + lane * 128 + (((i ^ lane) & 7) << 4), make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
-        __syncwarp();
-        if (I.slot >= 0) {
+          for (int i = 0; i < 8; i++)
+            st_shared16(patch + lane * 128 + (((i ^ lane) & 7) << 4), make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; i++) {
             const int rr = 4 * i + (lane >> 3);
             const uint4 x = ld_shared16(patch + rr * 128 + (((lane ^ rr) & 7) << 4));
-            if (__shfl_sync(0xffffffffu, orow, rr) >= 0)
+            if (__shfl_sync(0xffffffffu, row, rr) >= 0)
               *reinterpret_cast<uint4*>(rec + (rr - lane) * (D + 4) + c + (lane & 7) * 4) = x;
           }
-          continue;
         }
+        if (act && hf == 0) {
+          rec[D] = m;
+          rec[D + 1] = __fadd_rn(l, lo);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += CW) {
+          float y[CW];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int rr = 8 * i + (lane >> 2), q = (lane & 3) * 2;
-          const uint4 x0 = ld_shared16(patch + rr * 128 + (((q ^ rr) & 7) << 4)),
-                      x1 = ld_shared16(patch + rr * 128 + ((((q + 1) ^ rr) & 7) << 4));
-          const float f = __shfl_sync(0xffffffffu, inv, rr);
-          const int64_t ro = __shfl_sync(0xffffffffu, orow, rr);
-          if (ro < 0) continue;
-          float y[8] = {__uint_as_float(x0.x) * f, __uint_as_float(x0.y) * f, __uint_as_float(x0.z) * f, __uint_as_float(x0.w) * f,
-                        __uint_as_float(x1.x) * f, __uint_as_float(x1.y) * f, __uint_as_float(x1.z) * f, __uint_as_float(x1.w) * f};
-          const int64_t at = ro + c + (lane & 3) * 8;
-          if (p.gate) {
-            float gf[8];
-            widen8(gv[i], gf);
+          for (int b = 0; b < CW; b += 32) {
+            uint32_t r[32];
+            tmem_ld32(tl + C::T_O + c + b, r);
 #pragma unroll
-            for (int e = 0; e < 8; e++) y[e] = fast_gate(y[e], gf[e]);
+            for (int i = 0; i < 32; i++) y[b + i] = __fmul_rn(__uint_as_float(r[i]), inv);
           }
-          store8(p.out + at, y);
+          if (p.gate) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < Q; i++) {
+              const int rr = i * (32 / Q) + prow;
+              st_shared16(patch + rr * 128 + (((pq ^ rr) & 7) << 4), gv[i]);
+            }
+            __syncwarp();
+            if (c + CW < (hf + 1) * (D / 2)) fetch_gate(c + CW);
+#pragma unroll
+            for (int i = 0; i < Q; i++) {
+              float gf[8];
+              widen8(ld_shared16(patch + lane * 128 + (((i ^ lane) & 7) << 4)), gf);
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) fast_gate2(y[8 * i + e], y[8 * i + e + 1], gf[e], gf[e + 1]);
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < Q; i++)
+            st_shared16(patch + lane * 128 + (((i ^ lane) & 7) << 4),
+                        make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                   pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7])));
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < Q; i++) {
+            const int rr = i * (32 / Q) + prow;
+            const uint4 x = ld_shared16(patch + rr * 128 + (((pq ^ rr) & 7) << 4));
+            const int64_t ro = __shfl_sync(0xffffffffu, row, rr);
+            if (ro >= 0) *reinterpret_cast<uint4*>(p.out + ro + c + pq * 8) = x;
+          }
         }
-      }
-      if (rec && act && hf == 0) {
-        rec[D] = m;
-        rec[D + 1] = __fadd_rn(l, lo);
       }
       tc_fence_before();
     }
@@ -732,6 +798,18 @@ static bool encode_rows_map(CUtensorMap* m, void* base, int D, int64_t rows, int
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries [n_total][Hq][D] as a 3-D tensor in boxes of t tokens, g heads, 64 columns.
+static bool encode_q_map(CUtensorMap* m, const void* base, int D, int Hq, int n_total, int g, int t) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(n_total)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(D) * 2 * Hq};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(g), static_cast<cuuint32_t>(t)}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Workspace records (one per piece, 128 rows of D + 4 fp32) a call may use:
 // never more than its items can be cut into.
 static int64_t slots_for(const tv_attn_layer* l, const tv_prompt* pr, int max_len) {
@@ -752,6 +830,7 @@ static tv_status launch_prompt_tc(AttnPromptTcParams& p, const AttnPromptCall& a
         !encode_rows_map(&p.tmV[s], l->V[s], D, static_cast<int64_t>(l->Hkv) * l->cap, C::VROWS))
       return TV_ERR_CUDA;
   p.T = 128 / p.G;
+  if (!encode_q_map(&p.tmQ, a.q, D, l->Hq, a.prompt->n_total, p.G, p.T)) return TV_ERR_CUDA;
   p.slots = static_cast<int>(slots_for(l, a.prompt, a.max_len));
   p.workers = num_sms();
   static bool set = false;
@@ -760,7 +839,7 @@ static tv_status launch_prompt_tc(AttnPromptTcParams& p, const AttnPromptCall& a
       return TV_ERR_CUDA;
     set = true;
   }
-  attn_prompt_tc_kernel<D><<<dim3(p.workers), 352, C::SMEM, st>>>(p);
+  attn_prompt_tc_kernel<D><<<dim3(p.workers), 384, C::SMEM, st>>>(p);
   // the join has work only where the plan, made on the device, split items
   if (p.slots > 0) launch_k(true, attn_prompt_join_kernel<D>, dim3(num_sms() * 4), dim3(256), 0, st, p);
   return launch_status();
@@ -779,7 +858,6 @@ tv_status attn_prompt_tc_launch(const AttnPromptCall& a, cudaStream_t st) {
   AttnPromptTcParams p;
   memset(&p, 0, sizeof(p));
   p.pr = prompt_rows(a.prompt, a.len, a.max_len, l->cap);
-  p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.gate = static_cast<const __nv_bfloat16*>(a.gate);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.ws = static_cast<float*>(a.ws);
