@@ -12,6 +12,7 @@
 #include "prompt.cuh"
 #include "front_gdn.cuh"
 #include "launchers.hpp"
+#include "ptx.cuh"
 
 namespace tv {
 
@@ -30,9 +31,40 @@ struct GdnPromptFrontParams {
   int Hk, Hv, C, W, rows, strips, head_warps;
 };
 
+// Eight channels of a row, as packed fp32 pairs.
+template <typename T>
+struct Row8;
+template <>
+struct Row8<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ f2_t pair(int i) const { return f2_from_bf16x2(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w); }
+};
+template <>
+struct Row8<float> {
+  ulonglong2 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const ulonglong2*>(p)[0];
+    b = reinterpret_cast<const ulonglong2*>(p)[1];
+  }
+  __device__ __forceinline__ f2_t pair(int i) const { return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? b.x : b.y; }
+};
+
+// SiLU of a pair, x / (1 + e^-x), with one reciprocal for both (1/a = b (1/ab)):
+// the special-function unit comes close to bounding this kernel.  e^-x is held
+// below 2^63 so that the product stays finite; an x under -43.6 then gives
+// 1e-19 x instead of something smaller still.
+__device__ __forceinline__ f2_t silu2(f2_t x) {
+  float u, v;
+  f2_unpack(f2_mul(x, f2_dup(-1.4426950408889634f)), u, v);
+  f2_unpack(f2_add(f2_pack(ex2_approx(fminf(u, 63.f)), ex2_approx(fminf(v, 63.f))), f2_dup(1.f)), u, v);
+  const float r = __fdividef(1.f, __fmul_rn(u, v));
+  return f2_mul(x, f2_mul(f2_dup(r), f2_pack(v, u)));
+}
+
 // WT: the width, or 0 for any width up to kMaxConvWidth.
 template <typename T, int DH, int WT>
-__global__ void __launch_bounds__(128) gdn_prompt_front_kernel(const __grid_constant__ GdnPromptFrontParams p) {
+__global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_front_kernel(const __grid_constant__ GdnPromptFrontParams p) {
   constexpr int LPH = DH / 8, HPW = 32 / LPH;  // lanes a head, heads a warp
   constexpr int WM = WT ? WT : kMaxConvWidth;
   const int lane = threadIdx.x & 31;
@@ -58,11 +90,21 @@ __global__ void __launch_bounds__(128) gdn_prompt_front_kernel(const __grid_cons
   const int r0 = static_cast<int>(warp / p.head_warps) * p.rows;
   const int r1 = min(r0 + p.rows, n_live);
   if (r0 >= r1) return;
-  float tap[WM][8];  // tap[j] of channel c0 + e: wconv[c0 + e][j]
+  f2_t tap[WM][4];  // tap[j] of channels c0 + 2e, c0 + 2e + 1: wconv[c][j]
 #pragma unroll
-  for (int e = 0; e < 8; e++)
+  for (int e = 0; e < 4; e++) {
+    if constexpr (WT == 4) {
+      const float4 a = reinterpret_cast<const float4*>(p.wconv)[c0 + 2 * e], b = reinterpret_cast<const float4*>(p.wconv)[c0 + 2 * e + 1];
+      tap[0][e] = f2_pack(a.x, b.x);
+      tap[1][e] = f2_pack(a.y, b.y);
+      tap[2][e] = f2_pack(a.z, b.z);
+      tap[3][e] = f2_pack(a.w, b.w);
+    } else {
 #pragma unroll
-    for (int j = 0; j < WM; j++) tap[j][e] = j < W ? p.wconv[static_cast<size_t>(c0 + e) * W + j] : 0.f;
+      for (int j = 0; j < WM; j++)
+        tap[j][e] = j < W ? f2_pack(p.wconv[static_cast<size_t>(c0 + 2 * e) * W + j], p.wconv[static_cast<size_t>(c0 + 2 * e + 1) * W + j]) : 0ull;
+    }
+  }
   const T* x = static_cast<const T*>(p.x) + c0;
   const bool norm = u < 2 * p.Hk;
   const bool any_norm = __any_sync(0xffffffffu, norm);
@@ -82,12 +124,77 @@ __global__ void __launch_bounds__(128) gdn_prompt_front_kernel(const __grid_cons
   int off = __shfl_sync(0xffffffffu, w.off, s), end = __shfl_sync(0xffffffffu, w.end, s);
   // win[(r + j) % WM]: the input j - (W-1) rows from row r, so that a step
   // overwrites the oldest and nothing moves
-  float win[WM][8];
+  f2_t win[WM][4];
   bool fresh = true;
-  for (int rg = r0; rg < r1; rg += WM) {
-    float cur[WM][8];  // the group's rows, loaded ahead
+  Row8<T> cur[WM], next[WT ? WM : 1];  // rows of this group of WM and (fixed widths) of the one after, in flight
+  auto fetch = [&](int rg, Row8<T>* to) {
 #pragma unroll
-    for (int u = 0; u < WM; u++) load8(x + static_cast<size_t>(min(rg + u, r1 - 1)) * p.C, cur[u]);
+    for (int u = 0; u < WM; u++) to[u].load(x + static_cast<size_t>(min(rg + u, r1 - 1)) * p.C);
+  };
+  if (WT) fetch(r0, next);
+  for (int rg = r0; rg < r1; rg += WM) {
+    if (WT) {
+#pragma unroll
+      for (int u = 0; u < WM; u++) cur[u] = next[u % (WT ? WM : 1)];
+      if (rg + WM < r1) fetch(rg + WM, next);
+    } else {
+      fetch(rg, cur);
+    }
+    // row u of the group: the window takes it in, then convolution and SiLU
+    auto conv = [&](int u, f2_t (&acc)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) acc[e] = 0ull;
+#pragma unroll
+      for (int j = 0; j < WM; j++) {
+        if (j == W - 1) {
+#pragma unroll
+          for (int e = 0; e < 4; e++) win[(u + j) % WM][e] = cur[u].pair(e);
+        }
+        if (j < W) {
+#pragma unroll
+          for (int e = 0; e < 4; e++) acc[e] = f2_fma(tap[j][e], win[(u + j) % WM][e], acc[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; e++) acc[e] = silu2(acc[e]);
+    };
+    auto squares = [&](const f2_t (&acc)[4]) {
+      f2_t ss = 0ull;
+#pragma unroll
+      for (int e = 0; e < 4; e++) ss = f2_fma(acc[e], acc[e], ss);
+      return f2_hsum(ss);
+    };
+    auto put = [&](int r, f2_t (&acc)[4], float ss) {
+      if (any_norm) {
+        const f2_t sc = f2_dup(norm ? rsqrtf(__fadd_rn(ss, kNormEps)) : 1.f);
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[e] = f2_mul(acc[e], sc);
+      }
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 4; e++) f2_unpack(acc[e], y[2 * e], y[2 * e + 1]);
+      if (act) store8(dst + static_cast<size_t>(r) * dstride, y);
+    };
+    if (WT && !fresh && rg + WM <= r1 && rg + WM <= end) {  // a whole group of one sequence: two rows side by side
+#pragma unroll
+      for (int u = 0; u < WM; u += 2) {
+        f2_t acc[2][4];
+        float ss[2];
+        conv(u, acc[0]);
+        conv(u + 1, acc[1]);
+        if (any_norm) {
+          ss[0] = squares(acc[0]);
+          ss[1] = squares(acc[1]);
+#pragma unroll
+          for (int o = LPH / 2; o >= 1; o >>= 1)
+#pragma unroll
+            for (int v = 0; v < 2; v++) ss[v] = __fadd_rn(ss[v], __shfl_xor_sync(0xffffffffu, ss[v], o));
+        }
+        put(rg + u, acc[0], ss[0]);
+        put(rg + u + 1, acc[1], ss[1]);
+      }
+      continue;
+    }
 #pragma unroll
     for (int u = 0; u < WM; u++) {
       const int r = rg + u;
@@ -105,39 +212,21 @@ __global__ void __launch_bounds__(128) gdn_prompt_front_kernel(const __grid_cons
         for (int j = 0; j < WM - 1; j++)
           if (j < W - 1) {
             const int m = r - off + j - (W - 1);  // row of the sequence, negative: in the tail
-            load8(m >= 0 ? x + static_cast<size_t>(off + m) * p.C : tail + static_cast<size_t>(m + W - 1) * p.C + c0,
-                  win[(u + j) % WM]);
+            Row8<T> old;
+            old.load(m >= 0 ? x + static_cast<size_t>(off + m) * p.C : tail + static_cast<size_t>(m + W - 1) * p.C + c0);
+#pragma unroll
+            for (int e = 0; e < 4; e++) win[(u + j) % WM][e] = old.pair(e);
           }
       }
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; e++) y[e] = 0.f;
-#pragma unroll
-      for (int j = 0; j < WM; j++)
-        if (j < W) {
-#pragma unroll
-          for (int e = 0; e < 8; e++) y[e] = __fmaf_rn(tap[j][e], (j == W - 1) ? cur[u][e] : win[(u + j) % WM][e], y[e]);
-        }
-#pragma unroll
-      for (int j = 0; j < WM; j++)
-        if (j == W - 1) {
-#pragma unroll
-          for (int e = 0; e < 8; e++) win[(u + j) % WM][e] = cur[u][e];
-        }
+      f2_t acc[4];
+      conv(u, acc);
       float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        y[e] = silu_f(y[e]);
-        ss = __fmaf_rn(y[e], y[e], ss);
-      }
       if (any_norm) {
+        ss = squares(acc);
 #pragma unroll
         for (int o = LPH / 2; o >= 1; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
-        const float sc = norm ? rsqrtf(__fadd_rn(ss, kNormEps)) : 1.f;
-#pragma unroll
-        for (int e = 0; e < 8; e++) y[e] = __fmul_rn(y[e], sc);
       }
-      if (act) store8(dst + static_cast<size_t>(r) * dstride, y);
+      put(r, acc, ss);
     }
   }
 }
@@ -199,9 +288,9 @@ extern "C" tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* f, const tv_p
   p.C = 2 * f->Hk * f->dk + f->Hv * f->dv;
   const int hpw = 256 / f->dk;
   p.head_warps = (2 * f->Hk + f->Hv + hpw - 1) / hpw;
-  // rows a warp walks: 32 with many rows (a strip reads W-1 rows twice), fewer
-  // while the launch would not fill the SMs
-  p.rows = 32;
+  // rows a warp walks: 64 with many rows (a strip loads the taps and reads W-1
+  // rows twice), fewer while the launch would not fill the SMs
+  p.rows = 64;
   while (p.rows > 1 && static_cast<int64_t>((pr->n_total + p.rows - 1) / p.rows) * p.head_warps < 16 * num_sms()) p.rows >>= 1;
   p.strips = (pr->n_total + p.rows - 1) / p.rows;
   const int64_t warps = static_cast<int64_t>(p.strips) * p.head_warps + (static_cast<int64_t>(pr->n_total) * f->Hv + 31) / 32;

@@ -15,9 +15,12 @@
 //
 // A group of D/8 lanes owns a head, eight consecutive dimensions a lane, so a
 // row moves with one 16-byte access a lane (two for fp32).  A warp keeps one
-// row: its lanes form the row's sines and cosines once, in shared memory, and
-// its groups walk a part of the row's heads, up to eight (fp32: four) loads in
-// flight before the first is used.  Values are copied by warps of their own.
+// row and one kind of head (query, key or value): its lanes form the row's
+// sines and cosines once, and its groups walk a part of the heads, four at a
+// time with the next four in flight.  Norm weights and rotation are one
+// pair of factors a dimension, y_d = inv (x_d (w_d cos) + x_p (w_p sin)), formed
+// once a warp, so a head costs two packed products a pair of dimensions and its
+// partners travel unwidened.
 // Bound by HBM: each row is read once and written once.  A row's bits depend
 // only on its own values and position, and the three forms run the same code,
 // so verified, decoded and prompt rows are equal.
@@ -44,76 +47,78 @@ struct NormRopeParams {
   const void* meta;
   int form;  // 0 tree, 1 decode, 2 prompt
   int n_rows, n_seq, n_total, Hq, Hkv, rot, max_len, cap;
-  int heads_per_warp, qk_parts, parts;  // warps a row: qk_parts for queries and keys, the rest for values
+  int heads_per_warp, q_parts, k_parts, parts;  // warps a row: for queries, for keys, the rest for values
   float eps;
   uint64_t rate[kMaxPlanes];  // turns per position of each plane, as 64-bit fractions
 };
 
-// Eight values of a row as they lie in memory.
+// Eight values of a row as they lie in memory, and as packed fp32 pairs.
 template <typename T>
 struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
-  uint4 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
-  __device__ __forceinline__ void widen(float (&x)[8]) const { widen8(v, x); }
+  static constexpr int W = 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]); }
+  __device__ __forceinline__ f2_t pair(int i) const { return f2_from_bf16x2(w[i]); }
 };
 template <>
 struct Raw8<float> {
-  float4 a, b;
+  static constexpr int W = 8;
+  uint32_t w[W];
   __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
   __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
-  __device__ __forceinline__ void widen(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
+  __device__ __forceinline__ f2_t pair(int i) const { return f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])); }
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(128, sizeof(T) == 2 ? 5 : 4) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPH = D / 8;                  // lanes per head
   constexpr int GPW = 32 / LPH;               // heads a warp holds at once
-  constexpr int HB = sizeof(T) == 2 ? 8 : 4;  // loads a lane keeps in flight
-  __shared__ __align__(16) float cs_s[8][D / 2], sn_s[8][D / 2];
-  __shared__ __align__(16) float row_s[8][GPW][D];
+  constexpr int HB = 4;                       // heads a group works on at once
+  __shared__ __align__(16) float cs_s[4][D / 2], sn_s[4][D / 2];
+  __shared__ __align__(16) float row_s[4][GPW][D];
   const int wib = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * 8 + wib;
-  const int row = static_cast<int>(warp / p.parts), part = static_cast<int>(warp % p.parts);
+  const int row = blockIdx.x * 4 + wib, part = blockIdx.y;  // a CTA's warps have one kind of head: they end together
   if (row >= p.n_rows) return;  // whole warps leave
   const int grp = lane / LPH, gl = lane % LPH, d0 = gl * 8;
   // this warp's heads; the first loads start before the row's place is known
-  const bool vals = part >= p.qk_parts;
-  const int h_first = (vals ? part - p.qk_parts : part) * p.heads_per_warp;
-  const int h_end = min(vals ? p.Hkv : p.Hq + p.Hkv, h_first + p.heads_per_warp);
-  const T* qr = static_cast<const T*>(p.q_raw) + static_cast<size_t>(row) * p.Hq * D + d0;
-  const T* kr = static_cast<const T*>(vals ? p.v_raw : p.k_raw) + static_cast<size_t>(row) * p.Hkv * D + d0;
-  auto src = [&](int h) { return vals ? kr + static_cast<size_t>(h) * D : h < p.Hq ? qr + static_cast<size_t>(h) * D : kr + static_cast<size_t>(h - p.Hq) * D; };
+  const int kind = part < p.q_parts ? 0 : part < p.q_parts + p.k_parts ? 1 : 2;  // query, key, value
+  const int H = kind == 0 ? p.Hq : p.Hkv;
+  const int h_first = (part - (kind == 0 ? 0 : kind == 1 ? p.q_parts : p.q_parts + p.k_parts)) * p.heads_per_warp + grp;
+  const int h_end = min(H, h_first - grp + p.heads_per_warp);
+  const T* src = static_cast<const T*>(kind == 0 ? p.q_raw : kind == 1 ? p.k_raw : p.v_raw) + static_cast<size_t>(row) * H * D + d0;
   Raw8<T> raw[HB];
+  auto fetch = [&](int h0, Raw8<T> (&to)[HB]) {
 #pragma unroll
-  for (int i = 0; i < HB; i++) {
-    const int h = h_first + i * GPW + grp;
-    if (h < h_end) raw[i].load(src(h));
-  }
-  if (status_bad(p.pr.status)) return;
+    for (int i = 0; i < HB; i++) to[i].load(src + static_cast<size_t>(min(h0 + i * GPW, h_end - 1)) * D);
+  };
+  fetch(h_first, raw);
   // the row's sequence, position and (prompt) cache row
+  const bool bad = status_bad(p.pr.status);
   int s, pos;
   if (p.form == 2) {
     const WarpSeqs w = load_seqs(p.pr, lane);
-    if (w.code) {
-      if (lane == 0) set_status(p.pr.status, w.code);
+    if (w.code || bad) {
+      if (lane == 0 && w.code) set_status(p.pr.status, w.code);
       return;
     }
     s = seq_of(w, p.pr, lane, row);
     if (s < 0) return;  // padding behind the last sequence
     pos = __shfl_sync(0xffffffffu, w.len, s) + row - __shfl_sync(0xffffffffu, w.off, s);
   } else {
+    if (bad) return;
     s = row;
     int depth = 0;
     if (p.form == 0) {
@@ -128,21 +133,25 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
     }
     pos = len + depth;
   }
-  if (vals) {  // bit copies into the value cache
-    T* dst = static_cast<T*>(p.V[s]) + static_cast<size_t>(pos) * D + d0;
+  // where the heads go: head h at dst + h * step
+  T* dst;
+  size_t step = D;
+  if (kind == 0) {
+    dst = static_cast<T*>(p.q) + static_cast<size_t>(row) * H * D + d0;
+  } else if (p.form != 2) {
+    dst = static_cast<T*>(p.k) + static_cast<size_t>(row) * H * D + d0;
+  } else {
+    dst = static_cast<T*>(kind == 1 ? p.K[s] : p.V[s]) + static_cast<size_t>(pos) * D + d0;
+    step = static_cast<size_t>(p.cap) * D;
+  }
+  if (kind == 2) {  // values: bit copies
     for (int h0 = h_first;;) {
 #pragma unroll
-      for (int i = 0; i < HB; i++) {
-        const int h = h0 + i * GPW + grp;
-        if (h < h_end) raw[i].store(dst + static_cast<size_t>(h) * p.cap * D);
-      }
+      for (int i = 0; i < HB; i++)
+        if (h0 + i * GPW < h_end) raw[i].store(dst + (h0 + i * GPW) * step);
       h0 += HB * GPW;
-      if (h0 >= h_end) return;
-#pragma unroll
-      for (int i = 0; i < HB; i++) {
-        const int h = h0 + i * GPW + grp;
-        if (h < h_end) raw[i].load(src(h));
-      }
+      if (h0 - grp >= h_end) return;
+      fetch(h0, raw);
     }
   }
   const int half = p.rot >> 1;
@@ -152,73 +161,94 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
     sincospif(x, &sn_s[wib][j], &cs_s[wib][j]);
   }
   __syncwarp();
-  // this lane's rotation factors: dimension d < rot belongs to plane d mod half;
-  // the first half of a plane takes -sin of its partner, the second +sin
-  float cs[8], sn[8];
+  // this lane's factors: dimension d < rot belongs to plane d mod half; the
+  // first half of a plane takes -sin of its partner, the second +sin
+  const float* wn = kind == 0 ? p.q_norm : p.k_norm;
+  f2_t own[4], oth[4];
 #pragma unroll
-  for (int e = 0; e < 8; e++) {
-    const int d = d0 + e;
-    const int j = d < half ? d : d - half;
-    cs[e] = d < p.rot ? cs_s[wib][j] : 1.f;
-    sn[e] = d < p.rot ? (d < half ? -sn_s[wib][j] : sn_s[wib][j]) : 0.f;
-  }
-  float wq[8], wk[8];
-  if (p.q_norm) {
-    load8(p.q_norm + d0, wq);
-    load8(p.k_norm + d0, wk);
+  for (int i = 0; i < 4; i++) {
+    float a[2], b[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      const int d = d0 + 2 * i + e, j = d < half ? d : d - half, q = d < half ? d + half : d - half;
+      const bool turns = d < p.rot;
+      a[e] = (wn ? wn[d] : 1.f) * (turns ? cs_s[wib][j] : 1.f);
+      b[e] = turns ? (wn ? wn[q] : 1.f) * (d < half ? -sn_s[wib][j] : sn_s[wib][j]) : 0.f;
+    }
+    own[i] = f2_pack(a[0], a[1]);
+    oth[i] = f2_pack(b[0], b[1]);
   }
   const bool aligned = half % 8 == 0;  // a lane's eight partners sit in one other lane
-  const int partner = d0 < half ? gl + half / 8 : (d0 < p.rot ? gl - half / 8 : gl);
-  for (int h0 = h_first; h0 < h_end; h0 += HB * GPW) {
-    if (h0 != h_first) {
+  const bool turning = d0 < p.rot;     // (aligned: all eight dimensions of the lane or none)
+  const int partner = d0 < half ? gl + half / 8 : turning ? gl - half / 8 : gl;
+  for (int h0 = h_first; h0 - grp < h_end; h0 += HB * GPW) {
+    Raw8<T> next[HB];
+    const bool more = h0 - grp + HB * GPW < h_end;
+    if (more) fetch(h0 + HB * GPW, next);
+    float inv[HB];
+    if (wn) {  // the heads' sums side by side: their shuffles overlap
 #pragma unroll
       for (int i = 0; i < HB; i++) {
-        const int h = h0 + i * GPW + grp;
-        if (h < h_end) raw[i].load(src(h));
+        f2_t q2 = 0ull;
+#pragma unroll
+        for (int e = 0; e < 4; e++) q2 = f2_fma(raw[i].pair(e), raw[i].pair(e), q2);
+        inv[i] = f2_hsum(q2);
       }
+#pragma unroll
+      for (int o = LPH / 2; o >= 1; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < HB; i++) inv[i] = __fadd_rn(inv[i], __shfl_xor_sync(0xffffffffu, inv[i], o));
+#pragma unroll
+      for (int i = 0; i < HB; i++) inv[i] = rsqrtf(__fmaf_rn(inv[i], 1.f / D, p.eps));  // 2 ulp, far below the output's rounding
+    } else {
+#pragma unroll
+      for (int i = 0; i < HB; i++) inv[i] = 1.f;
     }
 #pragma unroll
     for (int i = 0; i < HB; i++) {
-      if (h0 + i * GPW >= h_end) break;  // the whole warp
-      const int h = h0 + i * GPW + grp;
-      const bool act = h < h_end, is_q = h < p.Hq;
-      float x[8];
-      raw[i].widen(x);
-      if (p.q_norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; e++) ss = __fmaf_rn(x[e], x[e], ss);
-#pragma unroll
-        for (int o = LPH / 2; o >= 1; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
-        const float inv = rsqrtf(__fmaf_rn(ss, 1.f / D, p.eps));  // 2 units in the last place, far below the output's rounding
-#pragma unroll
-        for (int e = 0; e < 8; e++) x[e] = __fmul_rn(__fmul_rn(x[e], inv), is_q ? wq[e] : wk[e]);
-      }
-      float y[8];
+      const int h = h0 + i * GPW;
+      f2_t y[4];
       if (aligned) {
+        Raw8<T> far;
 #pragma unroll
-        for (int e = 0; e < 8; e++) y[e] = __shfl_sync(0xffffffffu, x[e], partner, LPH);
+        for (int e = 0; e < Raw8<T>::W; e++) far.w[e] = __shfl_sync(0xffffffffu, raw[i].w[e], partner, LPH);
+#pragma unroll
+        for (int e = 0; e < 4; e++) y[e] = far.pair(e);
       } else {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; e++) f2_unpack(raw[i].pair(e), x[2 * e], x[2 * e + 1]);
         store8(&row_s[wib][grp][d0], x);
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < 8; e++) {
           const int d = d0 + e;
-          y[e] = d < p.rot ? row_s[wib][grp][d < half ? d + half : d - half] : 0.f;
+          x[e] = d < p.rot ? row_s[wib][grp][d < half ? d + half : d - half] : 0.f;
         }
         __syncwarp();
-      }
-      // dimensions past rot pass bit for bit (0 times a partner would not, were it infinite)
 #pragma unroll
-      for (int e = 0; e < 8; e++)
-        if (d0 + e < p.rot) x[e] = __fmaf_rn(x[e], cs[e], __fmul_rn(y[e], sn[e]));
-      if (act) {
-        T* dst;
-        if (is_q) dst = static_cast<T*>(p.q) + (static_cast<size_t>(row) * p.Hq + h) * D;
-        else if (p.form != 2) dst = static_cast<T*>(p.k) + (static_cast<size_t>(row) * p.Hkv + h - p.Hq) * D;
-        else dst = static_cast<T*>(p.K[s]) + (static_cast<size_t>(h - p.Hq) * p.cap + pos) * D;
-        store8(dst + d0, x);
+        for (int e = 0; e < 4; e++) y[e] = f2_pack(x[2 * e], x[2 * e + 1]);
       }
+      const f2_t inv2 = f2_dup(inv[i]);
+      if (turning) {
+        // (a dimension past rot in a turning lane has a factor of 0 for a
+        // partner that the unaligned path has set to 0)
+#pragma unroll
+        for (int e = 0; e < 4; e++) y[e] = f2_mul(inv2, f2_fma(raw[i].pair(e), own[e], f2_mul(y[e], oth[e])));
+      } else {  // no partner: 0 times one would not do, were it infinite
+#pragma unroll
+        for (int e = 0; e < 4; e++) y[e] = f2_mul(inv2, f2_mul(raw[i].pair(e), own[e]));
+      }
+      if (h < h_end) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; e++) f2_unpack(y[e], x[2 * e], x[2 * e + 1]);
+        store8(dst + h * step, x);
+      }
+    }
+    if (more) {
+#pragma unroll
+      for (int i = 0; i < HB; i++) raw[i] = next[i];
     }
   }
 }
@@ -237,31 +267,32 @@ static tv_status norm_rope_launch(const tv_attn_layer* l, NormRopeParams& p, con
     const double turns = std::pow(static_cast<double>(theta), -2.0 * j / rot) * 0.15915494309189533577;  // / 2 pi
     p.rate[j] = static_cast<uint64_t>(std::ldexp(turns, 64));
   }
-  // heads a warp walks: one round of its loads with many rows (the row's sines
-  // are formed once for them), fewer while the launch would leave SMs without work
+  // heads a warp walks: all of a kind with many rows (the row's factors are
+  // formed once for them; up to eight rounds), fewer while the launch would
+  // leave SMs without work
   const int gpw = 256 / l->D;
-  int hpw = gpw * (l->dtype == TV_BF16 ? 8 : 4);
+  int hpw = 32 * gpw;
   auto split = [&]() {
-    p.qk_parts = (l->Hq + l->Hkv + hpw - 1) / hpw;
-    p.parts = p.qk_parts + (p.form == 2 ? (l->Hkv + hpw - 1) / hpw : 0);
+    p.q_parts = (l->Hq + hpw - 1) / hpw;
+    p.k_parts = (l->Hkv + hpw - 1) / hpw;
+    p.parts = p.q_parts + p.k_parts + (p.form == 2 ? p.k_parts : 0);
     return static_cast<int64_t>(p.n_rows) * p.parts;
   };
   while (hpw > gpw && split() < 16 * num_sms()) hpw >>= 1;
   p.heads_per_warp = hpw;
-  const int64_t warps = split();
-  const int64_t grid = (warps + 7) / 8;
-  if (grid > 0x7fffffff) return TV_ERR_SHAPE;
-  const dim3 g(static_cast<unsigned>(grid));
+  split();
+  if (p.parts > 65535) return TV_ERR_SHAPE;
+  const dim3 g(static_cast<unsigned>((p.n_rows + 3) / 4), static_cast<unsigned>(p.parts));
   const bool bf = l->dtype == TV_BF16;
   switch (l->D) {
     case 64:
-      if (bf) norm_rope_kernel<__nv_bfloat16, 64><<<g, 256, 0, st>>>(p); else norm_rope_kernel<float, 64><<<g, 256, 0, st>>>(p);
+      if (bf) norm_rope_kernel<__nv_bfloat16, 64><<<g, 128, 0, st>>>(p); else norm_rope_kernel<float, 64><<<g, 128, 0, st>>>(p);
       break;
     case 128:
-      if (bf) norm_rope_kernel<__nv_bfloat16, 128><<<g, 256, 0, st>>>(p); else norm_rope_kernel<float, 128><<<g, 256, 0, st>>>(p);
+      if (bf) norm_rope_kernel<__nv_bfloat16, 128><<<g, 128, 0, st>>>(p); else norm_rope_kernel<float, 128><<<g, 128, 0, st>>>(p);
       break;
     default:
-      if (bf) norm_rope_kernel<__nv_bfloat16, 256><<<g, 256, 0, st>>>(p); else norm_rope_kernel<float, 256><<<g, 256, 0, st>>>(p);
+      if (bf) norm_rope_kernel<__nv_bfloat16, 256><<<g, 128, 0, st>>>(p); else norm_rope_kernel<float, 256><<<g, 128, 0, st>>>(p);
   }
   return launch_status();
 }
