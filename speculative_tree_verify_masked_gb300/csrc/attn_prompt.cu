@@ -3,29 +3,39 @@
 // attn_prompt_tc.cu).  Row i of a sequence sees cache rows 0 .. len + i (the prompt's own
 // keys and values are already in the cache).
 //
-// A CTA owns kRows consecutive (token, query head) rows of one KV head, token
+// A CTA owns a few consecutive (token, query head) rows of one KV head, token
 // major, so the G heads that share a KV head share its tiles too.  Keys and
-// values pass through shared memory in tiles of 32 positions; a warp keeps
-// four rows with one running maximum and sum each: lane j scores position j
-// of the tile in fp32, and the value rows are added in position order, up to
-// each row's own last position and no further, so nothing behind it (later
-// rows, rows the cache does not hold yet) can reach the result.
+// values pass through shared memory in tiles of 32 positions, the next tile by
+// cp.async under this one's arithmetic; a warp keeps RPW rows with one running
+// maximum and sum each: lane j scores position j of the tile in fp32, and the
+// value rows are added in position order, up to each row's own last position
+// and no further, so nothing behind it (later rows, rows the cache does not
+// hold yet) can reach the result.
 #include <cmath>
 
 #include "attn_prompt.cuh"
+#include "mma_tile.cuh"
 #include "ptx.cuh"
 
 namespace tv {
 
-constexpr int kRowsCuda = 16;
+template <int D, int RPW>
+struct Cuda {
+  static constexpr int ROWS = 4 * RPW;  // rows of a CTA
+  static constexpr int LD = D + 4;      // a lane reads its own key row, 16 bytes at a time: rows 4 banks apart
+  static constexpr int TILE = 32 * LD;
+  static constexpr int SMEM = (ROWS * D + 4 * TILE + 4 * 32 * RPW) * 4;
+};
 
-template <typename T, int D>
+template <int D, int RPW>
 __global__ void __launch_bounds__(128) attn_prompt_cuda_kernel(const __grid_constant__ AttnPromptCudaParams p) {
-  constexpr int CPL = D / 32, RPW = kRowsCuda / 4, LD = D + 4;
+  using C = Cuda<D, RPW>;
+  constexpr int CPL = D / 32, LD = C::LD;
   extern __shared__ __align__(16) float sm[];
-  float* qs = sm;                     // [kRowsCuda][D]
-  float* kv = qs + kRowsCuda * D;     // [32][LD]: keys, then values
-  __shared__ float ps[kRowsCuda][32];
+  float* qs = sm;                      // [ROWS][D]
+  float* kb = qs + C::ROWS * D;        // [2][32][LD] keys
+  float* vb = kb + 2 * C::TILE;        // [2][32][LD] values
+  float* ps = vb + 2 * C::TILE;        // [warp][32][RPW] probabilities
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (status_bad(p.pr.status)) return;
   const WarpSeqs w = load_seqs(p.pr, lane);
@@ -37,19 +47,31 @@ __global__ void __launch_bounds__(128) attn_prompt_cuda_kernel(const __grid_cons
   const int off = __shfl_sync(0xffffffffu, w.off, s), n = __shfl_sync(0xffffffffu, w.end, s) - off;
   const int L = __shfl_sync(0xffffffffu, w.len, s);
   const int64_t rows = static_cast<int64_t>(n) * G;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRowsCuda;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * C::ROWS;
   if (row0 >= rows) return;
-  const int live = static_cast<int>(rows - row0 < kRowsCuda ? rows - row0 : kRowsCuda);
-  const T* q = static_cast<const T*>(p.q);
+  const int live = static_cast<int>(rows - row0 < C::ROWS ? rows - row0 : C::ROWS);
   auto row_at = [&](int r) {  // packed (token, head) row of the buffers
     const int64_t fr = row0 + r;
     return (static_cast<size_t>(off) + static_cast<size_t>(fr / G)) * p.Hq + static_cast<size_t>(g) * G + static_cast<size_t>(fr % G);
   };
-  for (int e = threadIdx.x; e < kRowsCuda * (D / 8); e += 128) {
-    const int r = e / (D / 8), c = e % (D / 8) * 8;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (r < live) load8(q + row_at(r) * D + c, x);
-    store8(qs + r * D + c, x);
+  const int end = L + static_cast<int>((row0 + live - 1) / G) + 1;  // positions any row here sees
+  const float* K = static_cast<const float*>(p.K[s]) + static_cast<size_t>(g) * p.pr.cap * D;
+  const float* V = static_cast<const float*>(p.V[s]) + static_cast<size_t>(g) * p.pr.cap * D;
+  auto fetch = [&](int t0, int b) {  // rows behind `end` come in as zeros
+    for (int e = threadIdx.x; e < 2 * 32 * (D / 4); e += 128) {
+      const int r = e / (2 * (D / 4)), c = e % (2 * (D / 4)), cc = c % (D / 4) * 4;
+      const bool ok = t0 + r < end;
+      const size_t src = static_cast<size_t>(ok ? t0 + r : 0) * D + cc;
+      if (c < D / 4) cp_async16(smem_u32(kb + b * C::TILE + r * LD + cc), K + src, ok);
+      else cp_async16(smem_u32(vb + b * C::TILE + r * LD + cc), V + src, ok);
+    }
+    cp_async_commit();
+  };
+  fetch(0, 0);
+  for (int e = threadIdx.x; e < C::ROWS * (D / 4); e += 128) {
+    const int r = e / (D / 4), c = e % (D / 4) * 4;
+    reinterpret_cast<float4*>(qs + r * D + c)[0] =
+        r < live ? *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + row_at(r) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   int last[RPW];  // last visible position of each of this warp's rows, -1: no row
   float m[RPW], l[RPW], acc[RPW][CPL];
@@ -62,63 +84,69 @@ __global__ void __launch_bounds__(128) attn_prompt_cuda_kernel(const __grid_cons
 #pragma unroll
     for (int c = 0; c < CPL; c++) acc[i][c] = 0.f;
   }
-  const int end = L + static_cast<int>((row0 + live - 1) / G) + 1;  // positions any row here sees
-  const T* K = static_cast<const T*>(p.K[s]) + static_cast<size_t>(g) * p.pr.cap * D;
-  const T* V = static_cast<const T*>(p.V[s]) + static_cast<size_t>(g) * p.pr.cap * D;
-  for (int t0 = 0; t0 < end; t0 += 32) {
-    const int nt = min(32, end - t0);
-    auto fill = [&](const T* src) {
-      for (int e = threadIdx.x; e < 32 * (D / 8); e += 128) {
-        const int r = e / (D / 8), c = e % (D / 8) * 8;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (r < nt) load8(src + static_cast<size_t>(t0 + r) * D + c, x);
-        store8(kv + r * LD + c, x);
-      }
-    };
-    __syncthreads();
-    fill(K);
-    __syncthreads();
+  float* pw = ps + warp * 32 * RPW;
+  for (int t0 = 0, b = 0; t0 < end; t0 += 32, b ^= 1) {
+    cp_async_wait_group<0>();
+    __syncthreads();  // the tile is in; every warp is done with the other buffer
+    if (t0 + 32 < end) fetch(t0 + 32, b ^ 1);
+    const float* kt = kb + b * C::TILE + lane * LD;
     float sc[RPW];
 #pragma unroll
     for (int i = 0; i < RPW; i++) sc[i] = 0.f;
+#pragma unroll 4
     for (int d = 0; d < D; d += 4) {
-      const float4 k4 = *reinterpret_cast<const float4*>(kv + lane * LD + d);
+      const float4 k4 = *reinterpret_cast<const float4*>(kt + d);
 #pragma unroll
       for (int i = 0; i < RPW; i++) {
         const float4 q4 = *reinterpret_cast<const float4*>(qs + (warp * RPW + i) * D + d);
         sc[i] = __fmaf_rn(q4.w, k4.w, __fmaf_rn(q4.z, k4.z, __fmaf_rn(q4.y, k4.y, __fmaf_rn(q4.x, k4.x, sc[i]))));
       }
     }
+    float mx[RPW], sum[RPW];
+#pragma unroll
+    for (int i = 0; i < RPW; i++) mx[i] = sc[i] = t0 + lane <= last[i] ? __fmul_rn(sc[i], p.c) : -INFINITY;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < RPW; i++) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
 #pragma unroll
     for (int i = 0; i < RPW; i++) {
-      const float v = t0 + lane <= last[i] ? __fmul_rn(sc[i], p.c) : -INFINITY;
-      float mx = v;
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float mn = fmaxf(m[i], mx);
+      const float mn = fmaxf(m[i], mx[i]);
       const float alpha = mn == m[i] ? 1.f : exp2f(__fsub_rn(m[i], mn));
-      const float pj = t0 + lane <= last[i] ? exp2f(__fsub_rn(v, mn)) : 0.f;
-      float sum = pj;
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
-      l[i] = __fmaf_rn(l[i], alpha, sum);
+      const float pj = t0 + lane <= last[i] ? exp2f(__fsub_rn(sc[i], mn)) : 0.f;
+      pw[lane * RPW + i] = sum[i] = pj;
+      l[i] = __fmul_rn(l[i], alpha);
       m[i] = mn;
 #pragma unroll
       for (int c = 0; c < CPL; c++) acc[i][c] = __fmul_rn(acc[i][c], alpha);
-      ps[warp * RPW + i][lane] = pj;
     }
-    __syncthreads();
-    fill(V);
-    __syncthreads();
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < RPW; i++) sum[i] = __fadd_rn(sum[i], __shfl_xor_sync(0xffffffffu, sum[i], o));
+    int most = -1;  // the warp's rows see at most this far
 #pragma unroll
     for (int i = 0; i < RPW; i++) {
-      const int nv = min(nt, last[i] - t0 + 1);
-      for (int j = 0; j < nv; j++) {
-        const float pj = ps[warp * RPW + i][j];
+      l[i] = __fadd_rn(l[i], sum[i]);
+      most = max(most, last[i]);
+    }
+    __syncwarp();
+    const int nv = min(32, most - t0 + 1);
+    const float* vt = vb + b * C::TILE + lane;
+#pragma unroll 4
+    for (int j = 0; j < nv; j++) {
+      float v[CPL];
 #pragma unroll
-        for (int c = 0; c < CPL; c++) acc[i][c] = __fmaf_rn(pj, kv[j * LD + lane + 32 * c], acc[i][c]);
+      for (int c = 0; c < CPL; c++) v[c] = vt[j * LD + 32 * c];
+#pragma unroll
+      for (int i = 0; i < RPW; i++) {
+        if (t0 + j > last[i]) continue;  // the whole warp
+        const float pj = pw[j * RPW + i];
+#pragma unroll
+        for (int c = 0; c < CPL; c++) acc[i][c] = __fmaf_rn(pj, v[c], acc[i][c]);
       }
     }
+    __syncwarp();
   }
 #pragma unroll
   for (int i = 0; i < RPW; i++) {
@@ -129,35 +157,40 @@ __global__ void __launch_bounds__(128) attn_prompt_cuda_kernel(const __grid_cons
     for (int c = 0; c < CPL; c++) {
       const size_t oi = o + lane + 32 * c;
       const float y = __fdiv_rn(acc[i][c], l[i]);
-      static_cast<T*>(p.out)[oi] = from_f32<T>(p.gate ? gate_mul(y, to_f32(static_cast<const T*>(p.gate)[oi])) : y);
+      static_cast<float*>(p.out)[oi] = p.gate ? gate_mul(y, static_cast<const float*>(p.gate)[oi]) : y;
     }
   }
 }
 
-template <typename T, int D>
+template <int D, int RPW>
 static tv_status launch_cuda(const AttnPromptCudaParams& p, cudaStream_t st) {
-  constexpr int smem = (kRowsCuda * D + 32 * (D + 4)) * 4;
+  using C = Cuda<D, RPW>;
   const int64_t rows = static_cast<int64_t>(p.pr.n_max) * (p.Hq / p.Hkv);
-  const int64_t gx = (rows + kRowsCuda - 1) / kRowsCuda;
+  const int64_t gx = (rows + C::ROWS - 1) / C::ROWS;
   if (gx > 0x7fffffff || p.Hkv > 65535) return TV_ERR_SHAPE;
-  if (smem > 48 * 1024) {
-    static bool set = false;
-    if (!set) {
-      if (cudaFuncSetAttribute(attn_prompt_cuda_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return TV_ERR_CUDA;
-      set = true;
-    }
+  static bool set = false;
+  if (!set) {
+    if (cudaFuncSetAttribute(attn_prompt_cuda_kernel<D, RPW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+      return TV_ERR_CUDA;
+    set = true;
   }
-  attn_prompt_cuda_kernel<T, D><<<dim3(static_cast<unsigned>(gx), p.Hkv, p.pr.n_seq), 128, smem, st>>>(p);
+  attn_prompt_cuda_kernel<D, RPW><<<dim3(static_cast<unsigned>(gx), p.Hkv, p.pr.n_seq), 128, C::SMEM, st>>>(p);
   return launch_status();
 }
 
-template <typename T>
+// Four rows a warp, or one while four would leave SMs without a CTA (a call's
+// time is then one CTA's walk over the keys, which is shorter with fewer rows).
+template <int D>
+static tv_status launch_cuda_rows(const AttnPromptCudaParams& p, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(p.pr.n_total) * p.Hq;
+  return rows >= 16 * 2 * num_sms() ? launch_cuda<D, 4>(p, st) : launch_cuda<D, 1>(p, st);
+}
+
 static tv_status launch_cuda_d(const AttnPromptCudaParams& p, int D, cudaStream_t st) {
   switch (D) {
-    case 64: return launch_cuda<T, 64>(p, st);
-    case 128: return launch_cuda<T, 128>(p, st);
-    default: return launch_cuda<T, 256>(p, st);
+    case 64: return launch_cuda_rows<64>(p, st);
+    case 128: return launch_cuda_rows<128>(p, st);
+    default: return launch_cuda_rows<256>(p, st);
   }
 }
 
@@ -206,5 +239,5 @@ extern "C" tv_status tv_attn_prompt(const tv_attn_layer* l, const tv_prompt* pr,
   p.Hq = l->Hq;
   p.Hkv = l->Hkv;
   p.c = scale * 1.4426950408889634f;
-  return launch_cuda_d<float>(p, l->D, st);
+  return launch_cuda_d(p, l->D, st);
 }

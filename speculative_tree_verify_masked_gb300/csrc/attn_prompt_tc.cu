@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
 }
 
 // Joins the pieces of split items, in order: a warp takes 128 columns of a row,
-// four a lane, several pieces' loads in flight.
+// four a lane.
 template <int D>
 __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_constant__ AttnPromptTcParams p) {
   constexpr int CB = D > 128 ? D / 128 : 1, LPR = D >= 128 ? 32 : D / 4, RPW = 32 / LPR;
@@ -738,25 +738,28 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
       const int per = p.Hkv * pl.rt[s], first = pl.slot0[at] + (pl.rt[s] - 1 - i) * p.Hkv + g;
       const float* rec = p.ws + (static_cast<size_t>(first) * 128 + lrow) * (D + 4);
       const size_t step = static_cast<size_t>(per) * 128 * (D + 4);
-      // one pass with a running maximum, four pieces at a time
+      // one pass with a running maximum, kJ pieces' loads in flight at a time
+      constexpr int kJ = 8;
       float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int j0 = 0; j0 < np; j0 += 4) {
-        float4 o[4];
-        float2 ml[4];
+      for (int j0 = 0; j0 < np; j0 += kJ) {
+        float4 o[kJ];
+        float2 ml[kJ];
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
+        for (int j = 0; j < kJ; j++) {
           const float* r = rec + step * min(j0 + j, np - 1);
           o[j] = *reinterpret_cast<const float4*>(r + col);
           ml[j] = *reinterpret_cast<const float2*>(r + D);
           if (j0 + j >= np) ml[j] = make_float2(-INFINITY, 0.f);
         }
-        const float mn = fmaxf(m, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+        float mn = m;
+#pragma unroll
+        for (int j = 0; j < kJ; j++) mn = fmaxf(mn, ml[j].x);
         const float a = m == -INFINITY ? 0.f : exp2f(__fsub_rn(m, mn));
         l = __fmul_rn(l, a);
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[e] = __fmul_rn(acc[e], a);
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
+        for (int j = 0; j < kJ; j++) {
           if (ml[j].x == -INFINITY) continue;  // no position of this row in the piece (or no piece)
           const float f = exp2f(__fsub_rn(ml[j].x, mn));
           l = __fmaf_rn(f, ml[j].y, l);
