@@ -457,15 +457,15 @@ struct Walk {
   static constexpr int VOFF = KQ + Image<DK>::G;        // 64 value rows
   static constexpr int GOFF = VOFF + kBlk * kDvs * 2;   // g and D_63
   static constexpr int STAGE = GOFF + 1024;
-  static constexpr int B1 = 2 * DK * 128, B2 = 2 * kBlk * 128;  // [hi | lo] rows of 64 columns each
-  static constexpr int OBUF = 2 * STAGE + B1 + B2;      // output rows, turned around by their warps
+  static constexpr int B1 = DK * 128, B2 = kBlk * 128;  // of one half: rows of [32 hi | 32 lo] columns
+  static constexpr int OBUF = 2 * STAGE + 2 * (B1 + B2);  // output rows, turned around by their warps
   static constexpr int BOFF = OBUF + 4 * 2048;
-  static constexpr int NBAR = 2 + 2 + 5 + 1;
+  static constexpr int NBAR = 4 + 2 * 6;
   static constexpr int SMEM = BOFF + NBAR * 8 + 16;
   static constexpr int COLS = 512;
-  static constexpr int T_D1 = 0, T_D2 = 256, T_D3 = 384;  // D1 twice, by block parity: its output rows are read late
-  static constexpr uint32_t IDESC = idesc_bf16_f32(128, 2 * kDvs, false, true);
-  static constexpr uint32_t IDESC_HI = idesc_bf16_f32(128, kDvs, false, true);  // against the hi half alone
+  // of one half, 256 columns: D1 twice, by block parity (its output rows are read late)
+  static constexpr int T_D1 = 0, T_D2 = 128, T_D3 = 192;
+  static constexpr uint32_t IDESC = idesc_bf16_f32(128, kDvs, false, true);
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -479,25 +479,24 @@ __device__ __forceinline__ void split_f2(f2_t x, uint32_t& hi, uint32_t& lo) {
   hi = pack_f2(x);
   lo = pack_f2(f2_fma(f2_dup(-1.f), f2_from_bf16x2(hi), x));  // x - hi, exact
 }
-// 32 values as hi and lo parts into row r of a [rows][128 bytes] hi tile and
-// the lo tile `lo_off` behind it (16-byte chunks swizzled), column half wg.
-__device__ __forceinline__ void store_split(uint32_t tile, uint32_t lo_off, int r, int wg, const f2_t (&x)[16]) {
+// 32 values into row r (128 bytes) of a half's tile: hi parts, then lo parts
+// (16-byte chunks swizzled).
+__device__ __forceinline__ void store_split(uint32_t tile, int r, const f2_t (&x)[16]) {
 #pragma unroll
   for (int q = 0; q < 4; q++) {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e = 0; e < 4; e++) split_f2(x[4 * q + e], hi[e], lo[e]);
-    const uint32_t a = tile + r * 128 + (((wg * 4 + q) ^ (r & 7)) << 4);
+    const uint32_t a = tile + r * 128 + ((q ^ (r & 7)) << 4);
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a + lo_off), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
-                 : "memory");
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a ^ 64u), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
   }
 }
-// The hi and lo halves of a product's 32 columns of this thread's row, added.
+// The hi and lo parts of a product's 32 columns of this thread's row, added.
 __device__ __forceinline__ void load_sum(uint32_t taddr, f2_t (&x)[16]) {
   uint32_t a[32], b[32];
   tmem_ld32_nowait(taddr, a);
-  tmem_ld32_nowait(taddr + kDvs, b);
+  tmem_ld32_nowait(taddr + 32, b);
   tmem_ld_wait(a, b);
 #pragma unroll
   for (int i = 0; i < 16; i++)
@@ -506,18 +505,21 @@ __device__ __forceinline__ void load_sum(uint32_t taddr, f2_t (&x)[16]) {
 }
 
 template <int DK>
-__global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_constant__ GdnTcParams p) {
+__global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_constant__ GdnTcParams p) {
   using C = Walk<DK>;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
-  const uint32_t b1 = sb + 2 * C::STAGE, b2 = b1 + C::B1;
   const uint32_t bars = sb + C::BOFF;
-  const uint32_t FULL0 = bars, EMPTY0 = bars + 16u, B1R = bars + 32u, D1F = bars + 40u, B2R = bars + 48u,
-                 D2F = bars + 56u, D3F = bars + 64u, DRAIN = bars + 72u;
+  const uint32_t FULL0 = bars, EMPTY0 = bars + 16u, half0 = bars + 32u;  // then six barriers a half
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::BOFF + C::NBAR * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* skip = reinterpret_cast<int*>(tmem_slot + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // warps 0-3 and 8 serve columns 0 .. 31 of the slice, warps 4-7 and 9 the rest
+  const int hf = warp < 8 ? warp >> 2 : warp & 1;
+  const uint32_t hb = half0 + 48u * hf;
+  const uint32_t B1R = hb, D1F = hb + 8u, B2R = hb + 16u, D2F = hb + 24u, D3F = hb + 32u, DRAIN = hb + 40u;
+  const uint32_t b1 = sb + 2 * C::STAGE + hf * C::B1, b2 = sb + 2 * C::STAGE + 2 * C::B1 + hf * C::B2;
   const WarpSeqs w = load_seqs(p.pr, lane);
   int all;
   const int base = block_base(w, p.pr, lane, all);
@@ -537,14 +539,15 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
     if (sb & 1023u) set_status(p.pr.status, TV_ERR_CUDA);
     for (int i = 0; i < 2; i++) {
       mbar_init(FULL0 + 8u * i, 1);
-      mbar_init(EMPTY0 + 8u * i, 1);
+      mbar_init(EMPTY0 + 8u * i, 2);
+      const uint32_t x = half0 + 48u * i;
+      mbar_init(x, 4);        // B1R
+      mbar_init(x + 8u, 1);   // D1F
+      mbar_init(x + 16u, 4);  // B2R
+      mbar_init(x + 24u, 1);  // D2F
+      mbar_init(x + 32u, 1);  // D3F
+      mbar_init(x + 40u, 1);  // DRAIN
     }
-    mbar_init(B1R, 8);
-    mbar_init(D1F, 1);
-    mbar_init(B2R, 8);
-    mbar_init(D2F, 1);
-    mbar_init(D3F, 1);
-    mbar_init(DRAIN, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -559,12 +562,12 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
+  const uint32_t tbase = *tmem_slot + hf * 256;
   const int nb = (n + kBlk - 1) / kBlk;
   const size_t ws_step = static_cast<size_t>(p.Hv) * Image<DK>::BYTES;
   const uint8_t* ws0 = p.ws + (static_cast<size_t>(blk0) * p.Hv + h) * Image<DK>::BYTES;
 
-  if (warp == 9) {
+  if (warp == 10) {
     // ---------------- producer ----------------
     if (lane == 0) {
       int c = 0;
@@ -587,8 +590,8 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
         for (int i = c > 2 ? c - 2 : 0; i < c; i++) mbar_wait(FULL0 + 8u * (i & 1), (i >> 1) & 1, kWaitCycles);
       }
     }
-  } else if (warp == 8) {
-    // ---------------- MMA issuer ----------------
+  } else if (warp >= 8) {
+    // ---------------- MMA issuers, one a half ----------------
     bool ok = true;
     for (int c = 0; c < nb && ok; c++) {
       const int st = c & 1;
@@ -598,10 +601,10 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
       if (!ok) break;
       tc_fence_after();
       if (elect_one_sync()) {
-        const uint64_t a0 = sdesc_sw128(kq, 16, 1024), d0 = sdesc_sw128(b1, DK * 128, 1024);
+        const uint64_t a0 = sdesc_sw128(kq, 16, 1024), d0 = sdesc_sw128(b1, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < DK / 16; kk++)
-          tc_mma_ss(tbase + C::T_D1 + (c & 1) * 128, a0 + static_cast<uint64_t>(((kk >> 2) * C::KQBOX + (kk & 3) * 32) >> 4),
+          tc_mma_ss(tbase + C::T_D1 + (c & 1) * 64, a0 + static_cast<uint64_t>(((kk >> 2) * C::KQBOX + (kk & 3) * 32) >> 4),
                     d0 + static_cast<uint64_t>((kk * 2048) >> 4), C::IDESC, kk > 0 ? 1u : 0u);
         tc_commit(D1F);
       }
@@ -610,13 +613,13 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
       if (!ok) break;
       tc_fence_after();
       if (elect_one_sync()) {
-        const uint64_t a0 = sdesc_sw128(ti + Image<DK>::W, 16, 1024), d0 = sdesc_sw128(b2, kBlk * 128, 1024);
-        // W hi against [hi | lo], W lo against hi (DK = 64: rows 64 .. 127 of
-        // the product come from what lies behind and are never read)
+        const uint64_t a0 = sdesc_sw128(ti + Image<DK>::W, 16, 1024), d0 = sdesc_sw128(b2, 16, 1024);
+        // W hi, then W lo (its lo lo part is far below the rest; DK = 64: rows
+        // 64 .. 127 of the product come from what lies behind and are never read)
 #pragma unroll
         for (int kk = 0; kk < 8; kk++)
           tc_mma_ss(tbase + C::T_D3, a0 + static_cast<uint64_t>(((kk >> 2) * Image<DK>::WB + (kk & 3) * 32) >> 4),
-                    d0 + static_cast<uint64_t>(((kk & 3) * 2048) >> 4), kk < 4 ? C::IDESC : C::IDESC_HI, kk > 0 ? 1u : 0u);
+                    d0 + static_cast<uint64_t>(((kk & 3) * 2048) >> 4), C::IDESC, kk > 0 ? 1u : 0u);
         tc_commit(D3F);
         // P T in rows 64 .. 127, the output rows' lanes (the rows before are never read)
         const uint64_t p0 = sdesc_sw128(ti - kTile64, 16, 1024);
@@ -635,13 +638,13 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
     mbar_wait(DRAIN, 0, kWaitCycles);
   } else {
     // ---------------- state, splits and outputs: 8 warps ----------------
-    // warps 0-3 hold columns dv0 .. +31, warps 4-7 the next 32; a thread's
+    // a thread's
     // tensor-memory lane i is key row i of the state, row i of [K; Q] and of [T; P T]
-    const int wg = warp >> 2, i = (warp & 3) * 32 + lane;
+    const int i = (warp & 3) * 32 + lane;
     const bool krow = (warp & 3) < 2;  // lanes 0 .. 63: corrections; 64 .. 127: outputs
     const int ri = krow ? i : i - kBlk;
-    const uint32_t tl = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 32;
-    float* Sg = p.S[s] + (static_cast<size_t>(h) * p.dv + dv0 + wg * 32) * DK + i;
+    const uint32_t tl = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float* Sg = p.S[s] + (static_cast<size_t>(h) * p.dv + dv0 + hf * 32) * DK + i;
     f2_t S[16];
 #pragma unroll
     for (int e = 0; e < 16; e++)
@@ -653,7 +656,7 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
     bool ok = true;
     // the state's two parts for the first product of the next block
     auto offer = [&]() {
-      if (DK == 128 || krow) store_split(b1, DK * 128, i, wg, S);
+      if (DK == 128 || krow) store_split(b1, i, S);
       fence_proxy_async_smem();
       tc_fence_before();
       arrive(B1R);
@@ -673,7 +676,7 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
           uint4 v;
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(stg + C::VOFF + ri * 128 + (((wg * 4 + q) ^ (ri & 7)) << 4)));
+                       : "r"(stg + C::VOFF + ri * 128 + (((hf * 4 + q) ^ (ri & 7)) << 4)));
           z[4 * q] = f2_from_bf16x2(v.x);
           z[4 * q + 1] = f2_from_bf16x2(v.y);
           z[4 * q + 2] = f2_from_bf16x2(v.z);
@@ -684,11 +687,15 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
       if (!ok) break;
       tc_fence_after();
       if (krow) {
-        load_sum(tl + C::T_D1 + (c & 1) * 128, x);
+        load_sum(tl + C::T_D1 + (c & 1) * 64, x);
         const f2_t ng = f2_dup(-gr);
 #pragma unroll
-        for (int e = 0; e < 16; e++) z[e] = ri < live ? f2_fma(ng, x[e], z[e]) : 0ull;
-        store_split(b2, kBlk * 128, ri, wg, z);
+        for (int e = 0; e < 16; e++) z[e] = f2_fma(ng, x[e], z[e]);
+        if (live < kBlk && ri >= live) {  // no such row
+#pragma unroll
+          for (int e = 0; e < 16; e++) z[e] = 0ull;
+        }
+        store_split(b2, ri, z);
         fence_proxy_async_smem();
       }
       tc_fence_before();
@@ -706,14 +713,14 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
         if (!ok) break;
         tc_fence_after();
         load_sum(tl + C::T_D2, z);
-        load_sum(tl + C::T_D1 + (c & 1) * 128, x);
+        load_sum(tl + C::T_D1 + (c & 1) * 64, x);
         const f2_t f = f2_dup(__fmul_rn(p.scale, gr));
         uint32_t o[16];
 #pragma unroll
         for (int e = 0; e < 16; e++) o[e] = pack_f2(f2_fma(f, x[e], z[e]));
         // a thread holds 64 bytes of one row: turned around so that a store
         // covers whole rows' pieces, not 16 bytes of each of 32 rows
-        const uint32_t ob = sb + C::OBUF + (wg * 2 + (warp & 1)) * 2048;
+        const uint32_t ob = sb + C::OBUF + (hf * 2 + (warp & 1)) * 2048;
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 4; q++)
@@ -729,7 +736,7 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
                        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                        : "r"(ob + rr * 64 + ((q ^ ((rr >> 1) & 3)) << 4)));
           if (orow < live)
-            reinterpret_cast<uint4*>(p.out + ((static_cast<size_t>(off) + c * kBlk + orow) * p.Hv + h) * p.dv + dv0 + wg * 32)[q] = v;
+            reinterpret_cast<uint4*>(p.out + ((static_cast<size_t>(off) + c * kBlk + orow) * p.Hv + h) * p.dv + dv0 + hf * 32)[q] = v;
         }
       }
     }
@@ -743,7 +750,7 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tbase, C::COLS);
+  if (warp == 8) tmem_dealloc(*tmem_slot, C::COLS);
 }
 
 // ---------------------------------------------------------------------------
@@ -751,8 +758,6 @@ __global__ void __launch_bounds__(320, 1) gdn_block_walk_kernel(const __grid_con
 // ---------------------------------------------------------------------------
 static int64_t blocks_bound(const tv_prompt* pr) { return pr->n_total / kBlk + pr->n_seq; }
 
-// Blocks pay from about one block of rows on: below that the row-by-row
-// kernel ends sooner.
 bool gdn_prompt_tc_fits(const tv_gdn_layer* l, const tv_prompt* pr) {
   return l->dtype == TV_BF16 && l->dv % kDvs == 0 && pr->n_max >= kBlocksFrom;
 }
@@ -771,7 +776,7 @@ static tv_status launch_tc(const GdnTcParams& p, int64_t blocks, cudaStream_t st
     set = true;
   }
   gdn_block_prep_kernel<DK><<<dim3(static_cast<unsigned>(blocks), p.Hk), 128, Prep<DK>::SMEM, st>>>(p);
-  gdn_block_walk_kernel<DK><<<dim3(p.pr.n_seq * p.Hv * (p.dv / kDvs)), 320, Walk<DK>::SMEM, st>>>(p);
+  gdn_block_walk_kernel<DK><<<dim3(p.pr.n_seq * p.Hv * (p.dv / kDvs)), 352, Walk<DK>::SMEM, st>>>(p);
   return launch_status();
 }
 
