@@ -554,7 +554,11 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
   __syncthreads();
   const int off = __shfl_sync(0xffffffffu, w.off, s), n = __shfl_sync(0xffffffffu, w.end, s) - off;
   const int blk0 = __shfl_sync(0xffffffffu, base, s);
-  if (*skip || n <= 0) return;
+  // the images come from the launch before; all else was there before that began
+  if (*skip || n <= 0) {
+    pdl_wait();
+    return;
+  }
   if (warp == 8) {
     tmem_alloc(smem_u32(tmem_slot), C::COLS);
     tmem_relinquish();
@@ -569,6 +573,7 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
 
   if (warp == 10) {
     // ---------------- producer ----------------
+    pdl_wait();
     if (lane == 0) {
       int c = 0;
       for (; c < nb; c++) {
@@ -776,7 +781,7 @@ static tv_status launch_tc(const GdnTcParams& p, int64_t blocks, cudaStream_t st
     set = true;
   }
   gdn_block_prep_kernel<DK><<<dim3(static_cast<unsigned>(blocks), p.Hk), 128, Prep<DK>::SMEM, st>>>(p);
-  gdn_block_walk_kernel<DK><<<dim3(p.pr.n_seq * p.Hv * (p.dv / kDvs)), 352, Walk<DK>::SMEM, st>>>(p);
+  launch_k(true, gdn_block_walk_kernel<DK>, dim3(p.pr.n_seq * p.Hv * (p.dv / kDvs)), dim3(352), Walk<DK>::SMEM, st, p);
   return launch_status();
 }
 
