@@ -178,15 +178,16 @@ def _check(code: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        return c_void_p(torch.cuda.current_stream().cuda_stream)
+        # the current stream's handle without building a Stream object (a small call's largest host cost)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
-        return c_void_p(stream.cuda_stream)
-    return c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _dtype_code(dt: torch.dtype) -> int:
@@ -455,9 +456,7 @@ def _need(where: str, **tensors):
     value is (tensor, dtype, elements); the memory must be contiguous, on a
     GPU, and hold at least that many elements."""
     for name, (t, dtype, n) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != dtype or not t.is_contiguous() or not t.is_cuda or t.numel() < n:
+        if t is not None and (t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda or t.numel() < n):
             raise ValueError(f"{where}: {name} must be a contiguous {dtype} GPU tensor of at least {n} elements, got "
                              f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
