@@ -1,7 +1,6 @@
 // Gated DeltaNet front end over a prompt's packed rows: the short convolution
 // along each sequence (continuing from its committed tail), SiLU, the q/k head
-// norms and the gates; then the tails move on to the sequence's last W-1 raw
-// inputs.  Formulas as in front_gdn.cu.
+// norms and the gates; the tails move on to the sequence's last W-1 raw inputs.  Formulas as in front_gdn.cu.
 //
 // Bound by HBM: every raw channel is read once and written once.  A group of
 // DH/8 lanes owns one head (eight consecutive channels a lane, one 16-byte
@@ -38,6 +37,7 @@ template <>
 struct Row8<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
   __device__ __forceinline__ f2_t pair(int i) const { return f2_from_bf16x2(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w); }
 };
 template <>
@@ -46,6 +46,10 @@ struct Row8<float> {
   __device__ __forceinline__ void load(const float* p) {
     a = reinterpret_cast<const ulonglong2*>(p)[0];
     b = reinterpret_cast<const ulonglong2*>(p)[1];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<ulonglong2*>(p)[0] = a;
+    reinterpret_cast<ulonglong2*>(p)[1] = b;
   }
   __device__ __forceinline__ f2_t pair(int i) const { return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? b.x : b.y; }
 };
@@ -84,12 +88,16 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
   }
   const int W = WT ? WT : p.W;
   const int units = 2 * p.Hk + p.Hv;
+  int strips;
+  const int base = strip_base(w, p.pr, lane, p.rows, strips);
+  const int strip = static_cast<int>(warp / p.head_warps);
+  if (strip >= strips) return;
+  const int s = strip_seq(w, p.pr, lane, base, strip);
+  const int off = __shfl_sync(0xffffffffu, w.off, s), end = __shfl_sync(0xffffffffu, w.end, s);
+  const int r0 = off + (strip - __shfl_sync(0xffffffffu, base, s)) * p.rows, r1 = min(r0 + p.rows, end);
   const int u = static_cast<int>(warp % p.head_warps) * HPW + lane / LPH;
   const bool act = u < units;
   const int c0 = (act ? u : 0) * DH + (lane % LPH) * 8;  // dk = dv = DH: head u's channels start at u * DH
-  const int r0 = static_cast<int>(warp / p.head_warps) * p.rows;
-  const int r1 = min(r0 + p.rows, n_live);
-  if (r0 >= r1) return;
   f2_t tap[WM][4];  // tap[j] of channels c0 + 2e, c0 + 2e + 1: wconv[c][j]
 #pragma unroll
   for (int e = 0; e < 4; e++) {
@@ -120,18 +128,34 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
     dst = static_cast<T*>(p.v) + (c0 - 2 * p.Hk * DH);
     dstride = static_cast<size_t>(p.Hv) * DH;
   }
-  int s = seq_of(w, p.pr, lane, r0);
-  int off = __shfl_sync(0xffffffffu, w.off, s), end = __shfl_sync(0xffffffffu, w.end, s);
-  // win[(r + j) % WM]: the input j - (W-1) rows from row r, so that a step
-  // overwrites the oldest and nothing moves
+  // win[(r + j) % WM]: the input j - (W-1) rows from row r of the strip, so that
+  // a step overwrites the oldest and nothing moves
   f2_t win[WM][4];
-  bool fresh = true;
   Row8<T> cur[WM], next[WT ? WM : 1];  // rows of this group of WM and (fixed widths) of the one after, in flight
   auto fetch = [&](int rg, Row8<T>* to) {
 #pragma unroll
     for (int u = 0; u < WM; u++) to[u].load(x + static_cast<size_t>(min(rg + u, r1 - 1)) * p.C);
   };
   if (WT) fetch(r0, next);
+  // The rows before the strip: the tail's for a sequence's first strip, which
+  // has the W-1 rows that read it, so that it alone then moves the tail on.
+  T* tail = static_cast<T*>(p.tail[s]) + c0;
+#pragma unroll
+  for (int j = 0; j < WM - 1; j++)
+    if (j < W - 1) {
+      Row8<T> old;
+      old.load(r0 > off ? x + static_cast<size_t>(r0 + j - (W - 1)) * p.C : tail + static_cast<size_t>(j) * p.C);
+#pragma unroll
+      for (int e = 0; e < 4; e++) win[j][e] = old.pair(e);
+    }
+  if (r0 == off && act) {
+    for (int j = 0; j < W - 1; j++) {  // ascending: row j comes from the prompt or from a later row of the old tail
+      const int m = end - off + j - (W - 1);
+      Row8<T> to;
+      to.load(m >= 0 ? x + static_cast<size_t>(off + m) * p.C : tail + static_cast<size_t>(m + W - 1) * p.C);
+      to.store(tail + static_cast<size_t>(j) * p.C);
+    }
+  }
   for (int rg = r0; rg < r1; rg += WM) {
     if (WT) {
 #pragma unroll
@@ -175,7 +199,7 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
       for (int e = 0; e < 4; e++) f2_unpack(acc[e], y[2 * e], y[2 * e + 1]);
       if (act) store8(dst + static_cast<size_t>(r) * dstride, y);
     };
-    if (WT && !fresh && rg + WM <= r1 && rg + WM <= end) {  // a whole group of one sequence: two rows side by side
+    if (WT && rg + WM <= r1) {  // a whole group: two rows side by side
 #pragma unroll
       for (int u = 0; u < WM; u += 2) {
         f2_t acc[2][4];
@@ -199,25 +223,6 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
     for (int u = 0; u < WM; u++) {
       const int r = rg + u;
       if (r >= r1) break;
-      if (r >= end) {  // the next sequence that has rows
-        s = seq_of(w, p.pr, lane, r);
-        off = __shfl_sync(0xffffffffu, w.off, s);
-        end = __shfl_sync(0xffffffffu, w.end, s);
-        fresh = true;
-      }
-      if (fresh) {
-        fresh = false;
-        const T* tail = static_cast<const T*>(p.tail[s]);
-#pragma unroll
-        for (int j = 0; j < WM - 1; j++)
-          if (j < W - 1) {
-            const int m = r - off + j - (W - 1);  // row of the sequence, negative: in the tail
-            Row8<T> old;
-            old.load(m >= 0 ? x + static_cast<size_t>(off + m) * p.C : tail + static_cast<size_t>(m + W - 1) * p.C + c0);
-#pragma unroll
-            for (int e = 0; e < 4; e++) win[(u + j) % WM][e] = old.pair(e);
-          }
-      }
       f2_t acc[4];
       conv(u, acc);
       float ss = 0.f;
@@ -228,29 +233,6 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
       }
       put(r, acc, ss);
     }
-  }
-}
-
-// One thread per (sequence, channel), after every read of the old tails.
-template <typename T>
-__global__ void __launch_bounds__(256) gdn_prompt_tail_kernel(const __grid_constant__ GdnPromptFrontParams p) {
-  const int lane = threadIdx.x & 31;
-  pdl_wait();
-  if (status_bad(p.pr.status)) return;
-  const WarpSeqs w = load_seqs(p.pr, lane);
-  if (w.code) return;  // reported by the first kernel
-  const int s = blockIdx.y;
-  const int off = __shfl_sync(0xffffffffu, w.off, s), n = __shfl_sync(0xffffffffu, w.end, s) - off;
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= p.C || n <= 0) return;
-  T* tail = static_cast<T*>(p.tail[s]);
-  const T* x = static_cast<const T*>(p.x);
-  const int W1 = p.W - 1;
-  // ascending: row r comes from row r + n of the old tail (still unwritten) or from the prompt
-  for (int r = 0; r < W1; r++) {
-    const int m = n + r - W1;  // row of the sequence
-    tail[static_cast<size_t>(r) * p.C + c] =
-        m >= 0 ? x[static_cast<size_t>(off + m) * p.C + c] : tail[static_cast<size_t>(r + n) * p.C + c];
   }
 }
 
@@ -289,10 +271,13 @@ extern "C" tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* f, const tv_p
   const int hpw = 256 / f->dk;
   p.head_warps = (2 * f->Hk + f->Hv + hpw - 1) / hpw;
   // rows a warp walks: 64 with many rows (a strip loads the taps and reads W-1
-  // rows twice), fewer while the launch would not fill the SMs
+  // rows twice), fewer while the launch would not fill the SMs, never fewer than
+  // read a tail
   p.rows = 64;
-  while (p.rows > 1 && static_cast<int64_t>((pr->n_total + p.rows - 1) / p.rows) * p.head_warps < 16 * num_sms()) p.rows >>= 1;
-  p.strips = (pr->n_total + p.rows - 1) / p.rows;
+  while (p.rows > kMaxConvWidth / 2 && p.rows / 2 >= f->width - 1 &&
+         static_cast<int64_t>((pr->n_total + p.rows - 1) / p.rows) * p.head_warps < 16 * num_sms())
+    p.rows >>= 1;
+  p.strips = pr->n_total / p.rows + pr->n_seq;
   const int64_t warps = static_cast<int64_t>(p.strips) * p.head_warps + (static_cast<int64_t>(pr->n_total) * f->Hv + 31) / 32;
   const int64_t grid = (warps + 3) / 4;
   if (grid > 0x7fffffff) return TV_ERR_SHAPE;
@@ -303,11 +288,6 @@ extern "C" tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* f, const tv_p
     if (bf) launch_prompt_front<__nv_bfloat16, 128>(p, g, st); else launch_prompt_front<float, 128>(p, g, st);
   } else {
     if (bf) launch_prompt_front<__nv_bfloat16, 64>(p, g, st); else launch_prompt_front<float, 64>(p, g, st);
-  }
-  if (f->width > 1) {
-    const dim3 tg((p.C + 255) / 256, pr->n_seq);
-    if (bf) launch_k(true, gdn_prompt_tail_kernel<__nv_bfloat16>, tg, dim3(256), 0, st, p);
-    else launch_k(true, gdn_prompt_tail_kernel<float>, tg, dim3(256), 0, st, p);
   }
   return launch_status();
 }

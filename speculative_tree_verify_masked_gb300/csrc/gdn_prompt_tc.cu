@@ -72,19 +72,6 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = pack_bf16x2(__fsub_rn(a, bf16_lo(hi)), __fsub_rn(b, bf16_hi(hi)));
 }
 
-// Blocks of the sequences before this lane's, and of all.
-__device__ __forceinline__ int block_base(const WarpSeqs& w, const PromptRows& p, int lane, int& all) {
-  const int mine = lane < p.n_seq ? (w.end - w.off + kBlk - 1) / kBlk : 0;
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  all = __shfl_sync(0xffffffffu, incl, 31);
-  return incl - mine;
-}
-
 // ---------------------------------------------------------------------------
 // first kernel: W and P T of one block, for the value heads of one key head
 // ---------------------------------------------------------------------------
@@ -158,11 +145,10 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
     return;
   }
   int all;
-  const int base = block_base(w, p.pr, lane, all);
+  const int base = strip_base(w, p.pr, lane, kBlk, all);
   const int blk = blockIdx.x;
   if (blk >= all) return;
-  const unsigned m = __ballot_sync(0xffffffffu, lane < p.pr.n_seq && w.end > w.off && base <= blk);
-  const int s = 31 - __clz(static_cast<int>(m));
+  const int s = strip_seq(w, p.pr, lane, base, blk);
   const int row0 = __shfl_sync(0xffffffffu, w.off, s) + (blk - __shfl_sync(0xffffffffu, base, s)) * kBlk;
   const int nv = min(kBlk, __shfl_sync(0xffffffffu, w.end, s) - row0);
   const int g = blockIdx.y;
@@ -522,7 +508,7 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
   const uint32_t b1 = sb + 2 * C::STAGE + hf * C::B1, b2 = sb + 2 * C::STAGE + 2 * C::B1 + hf * C::B2;
   const WarpSeqs w = load_seqs(p.pr, lane);
   int all;
-  const int base = block_base(w, p.pr, lane, all);
+  const int base = strip_base(w, p.pr, lane, kBlk, all);
   // sequences in order of falling length along the grid: the long ones start first
   const int per = p.Hv * (p.dv / kDvs);
   const int place = blockIdx.x / per, rem = blockIdx.x % per;

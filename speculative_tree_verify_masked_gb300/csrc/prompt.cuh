@@ -47,6 +47,24 @@ __device__ __forceinline__ int seq_of(const WarpSeqs& w, const PromptRows& p, in
   return s >= p.n_seq ? -1 : s;
 }
 
+// Each sequence cut into strips of `rows` rows from its first: the strips of the
+// sequences before this lane's, and of all.
+__device__ __forceinline__ int strip_base(const WarpSeqs& w, const PromptRows& p, int lane, int rows, int& all) {
+  const int mine = lane < p.n_seq ? (w.end - w.off + rows - 1) / rows : 0;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  all = __shfl_sync(0xffffffffu, incl, 31);
+  return incl - mine;
+}
+// The sequence that strip `i` of these belongs to.
+__device__ __forceinline__ int strip_seq(const WarpSeqs& w, const PromptRows& p, int lane, int base, int i) {
+  return 31 - __clz(static_cast<int>(__ballot_sync(0xffffffffu, lane < p.n_seq && w.end > w.off && base <= i)));
+}
+
 // The host's half: a well-formed descriptor (rows may be zero).
 inline bool prompt_ok(const tv_prompt* p) {
   return p && p->n_seq >= 1 && p->n_seq <= TV_MAX_SEQ && p->n_total >= 0 && p->n_total <= TV_MAX_PROMPT_ROWS &&
