@@ -270,13 +270,16 @@ extern "C" tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* f, const tv_p
   p.C = 2 * f->Hk * f->dk + f->Hv * f->dv;
   const int hpw = 256 / f->dk;
   p.head_warps = (2 * f->Hk + f->Hv + hpw - 1) / hpw;
-  // rows a warp walks: 64 with many rows (a strip loads the taps and reads W-1
-  // rows twice), fewer while the launch would not fill the SMs, never fewer than
-  // read a tail
-  p.rows = 64;
-  while (p.rows > kMaxConvWidth / 2 && p.rows / 2 >= f->width - 1 &&
-         static_cast<int64_t>((pr->n_total + p.rows - 1) / p.rows) * p.head_warps < 16 * num_sms())
-    p.rows >>= 1;
+  // Rows a warp walks: at most 64 and as even a number of waves (16 warps an SM)
+  // as groups of four rows allow, since a strip loads the taps and reads W-1 rows
+  // twice; never fewer than read a tail.  At 16 + 48 heads of 128, 731 rows take
+  // 13.5 us in strips of 12, 15.2 of 8, 16.9 of 32; 8,192 rows 68.8 us in strips
+  // of 48 (three even waves), 70.8 of 32, 74.9 of 64.
+  const int64_t work = static_cast<int64_t>(pr->n_total) * p.head_warps, slots = 16 * num_sms();
+  const int64_t waves = (work + slots * 64 - 1) / (slots * 64);
+  const int64_t even = (work + slots * waves - 1) / (slots * waves);
+  const int64_t rows = even > f->width - 1 ? even : f->width - 1;
+  p.rows = static_cast<int>((rows + 3) / 4 * 4);
   p.strips = pr->n_total / p.rows + pr->n_seq;
   const int64_t warps = static_cast<int64_t>(p.strips) * p.head_warps + (static_cast<int64_t>(pr->n_total) * f->Hv + 31) / 32;
   const int64_t grid = (warps + 3) / 4;
