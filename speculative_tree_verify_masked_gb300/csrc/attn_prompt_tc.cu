@@ -25,9 +25,11 @@
 // products' time before PV(t) wants P(t).
 //
 // Masked places.  Scores of positions a row does not see are replaced, not
-// added to, so what the cache holds there (NaN, infinity) cannot pass.  In PV
-// a zero weight would still meet the value: value rows behind the sequence's
-// last position are zeroed in shared memory before the last tile's PV.
+// added to, so a key that is not finite there cannot pass.  In PV a zero weight
+// would still meet the value: in a tile that some row here does not see whole,
+// values that are not finite are zeroed in shared memory before its PV (one look
+// at the tile, 16 KB a warp at most), and the rows that do see them take them
+// in afterwards, from the cache (put_nonfinite).
 //
 // Work split.  All CTAs derive the same plan from the device-side offsets and
 // lengths: items in order of falling length, dealt back and forth over the
@@ -88,6 +90,7 @@ struct AttnPromptTcParams {
   CUtensorMap tmV[TV_MAX_SEQ];
   CUtensorMap tmQ;  // [n_total][Hq][D] in boxes of T tokens, G heads, 64 columns
   PromptRows pr;
+  const __nv_bfloat16* V[TV_MAX_SEQ];
   const __nv_bfloat16* gate;
   __nv_bfloat16* out;
   float* ws;
@@ -118,6 +121,31 @@ __device__ __forceinline__ void fast_gate2(float& x, float& y, float gx, float g
   const float r = __fdividef(1.f, a * b);
   x *= b * r;
   y *= a * r;
+}
+
+// 0xffff in each half of a bf16 pair that is finite, 0 in others.
+__device__ __forceinline__ uint32_t finite2(uint32_t x) { return __vcmpltu2(x & 0x7f807f80u, 0x7f807f80u); }
+__device__ __forceinline__ uint32_t times_zero_plus(uint32_t x, uint32_t acc) {  // bf16 pairs
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+  return r;
+}
+// The columns in which one of value rows [from, to) is not finite get the sum of
+// those that are not: into a piece's record, or else into the output row.
+static __device__ __noinline__ void put_nonfinite(const __nv_bfloat16* v, int stride, int cols, int from, int to, float* rec,
+                                                  __nv_bfloat16* out) {
+  for (int c = 0; c < cols; c++) {
+    float sum = 0.f;
+    bool any = false;
+    for (int t = from; t < to; t++) {
+      const float x = __bfloat162float(v[static_cast<size_t>(t) * stride + c]);
+      if (isfinite(x)) continue;
+      sum = __fadd_rn(sum, x);
+      any = true;
+    }
+    if (any && rec) rec[c] = sum;
+    else if (any) out[c] = __float2bfloat16_rn(sum);
+  }
 }
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -251,6 +279,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + C::LOFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int& skip = *reinterpret_cast<int*>(tmem_slot + 2);
+  volatile uint16_t* met = reinterpret_cast<volatile uint16_t*>(tmem_slot + 3);  // items that met values to zero
   PromptPlan& pl = *reinterpret_cast<PromptPlan*>(gb + C::LOFF + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int worker = static_cast<int>(blockIdx.x);
@@ -273,6 +302,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
       mbar_init(QEMPTY0 + 8u * i, 4);
     }
     *abort_flag = 0;
+    met[0] = met[1] = 0;
     fence_mbar_init();
   }
   if (warp == 2) {  // the plan; a bad launch sets its code and every CTA leaves
@@ -491,8 +521,12 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
       orow = row_of(I);
       ok = load_q();
     }
+    // met[id & 1] = id: item id met a value to zero.  (A warp may be an item
+    // ahead of another, not two: their P arrivals hold them together.)
+    uint16_t id = 0;
     while (ok && more) {
-      const int n = I.t1 - I.t0, L = pl.L[I.s], end = L + pl.n[I.s];
+      id++;
+      const int n = I.t1 - I.t0, L = pl.L[I.s];
       const bool act = orow >= 0;
       const int last = act ? L + I.i * p.T + tok : -1;  // last position this row sees
       const int seen_all = L + I.i * p.T + 1;           // positions every row here sees
@@ -571,23 +605,37 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
           }
           tmem_st_wait();
         }
-        if (pos + kKeyTile > end) {
-          // value rows behind the sequence's last position: zero them before
-          // PV (the last tile of the piece; its units follow the 2n-1 before)
-          const int first = end - pos;  // 1 .. 127
+        if (pos + kKeyTile > seen_all) {
+          const int first = max(seen_all - pos, 0);
+          const uint32_t u0 = it + (k < n - 1 ? 2 * k + 2 : 2 * n - 1) * C::UPT;  // the tile's value units
           uint32_t slot[C::UPT];
 #pragma unroll
           for (int u = 0; u < C::UPT; u++) {
-            const uint32_t i = it + (2 * n - 1) * C::UPT + u;
-            slot[u] = i % C::NU;
-            ok = ok && wait_warp(UFULL0 + 8u * slot[u], (i / C::NU) & 1, abort_flag, kWaitCycles);
+            slot[u] = (u0 + u) % C::NU;
+            ok = ok && wait_warp(UFULL0 + 8u * slot[u], ((u0 + u) / C::NU) & 1, abort_flag, kWaitCycles);
           }
           if (!ok) break;
-          for (int e = static_cast<int>(threadIdx.x) - 64; e < (kKeyTile - first) * C::VB * 8; e += 256) {
-            const int row = first + e / (C::VB * 8), c = e % (C::VB * 8);
-            const uint32_t a = ring + slot[C::UPT > 1 ? row / C::VROWS : 0] * C::UNIT + (c >> 3) * C::VBOX +
-                               (row % C::VROWS) * 128 + (c & 7) * 16;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+          constexpr int PPR = C::VB * 8, RPW = 32 / PPR;  // 16-byte pieces of a row, rows a warp looks at
+          const uint32_t piece = (lane % PPR >> 3) * C::VBOX + (lane & 7) * 16;
+          auto at = [&](int row) {
+            return ring + (C::UPT > 1 && row >= C::VROWS ? slot[C::UPT - 1] : slot[0]) * C::UNIT + (row % C::VROWS) * 128 + piece;
+          };
+          const int row0 = first + (warp - 2) * RPW + lane / PPR;
+          uint32_t sum[4] = {0u, 0u, 0u, 0u};  // of value x 0: zero, or NaN
+#pragma unroll 4
+          for (int row = row0; row < kKeyTile; row += 8 * RPW) {
+            const uint4 v = ld_shared16(at(row));
+            sum[0] = times_zero_plus(v.x, sum[0]);
+            sum[1] = times_zero_plus(v.y, sum[1]);
+            sum[2] = times_zero_plus(v.z, sum[2]);
+            sum[3] = times_zero_plus(v.w, sum[3]);
+          }
+          if ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) {
+            for (int row = row0; row < kKeyTile; row += 8 * RPW) {
+              const uint4 v = ld_shared16(at(row));
+              st_shared16(at(row), make_uint4(v.x & finite2(v.x), v.y & finite2(v.y), v.z & finite2(v.z), v.w & finite2(v.w)));
+            }
+            met[id & 1] = id;
           }
         }
         fence_proxy_async_smem();
@@ -598,6 +646,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
       if (!ok) break;
       const int slot = I.slot;
       const int64_t row = orow;
+      const int mine = wave;
       more = next_item(p, pl, total, worker, wave, I);
       if (more) {  // the next item's first Q K^T runs beside this one's last P V and output
         orow = row_of(I);
@@ -695,6 +744,16 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
           }
         }
       }
+      if (met[id & 1] == id) {
+        __syncwarp();
+        const PromptItem J = item_of(p, pl, piece_index(mine - 1, worker, p.workers));  // this item again
+        const int before = pl.L[J.s] + J.i * p.T + 1;  // seen by all rows
+        const int end = min(before + tok, J.t1 * kKeyTile);
+        put_nonfinite(p.V[J.s] + static_cast<size_t>(J.g) * p.pr.cap * D + hf * (D / 2), D, D / 2, max(before, J.t0 * kKeyTile),
+                      row >= 0 ? end : 0,
+                      slot >= 0 ? p.ws + (static_cast<size_t>(slot) * 128 + lrow) * (D + 4) + hf * (D / 2) : nullptr,
+                      p.out + row + hf * (D / 2));
+      }
       tc_fence_before();
     }
     if (!ok && lane == 0) set_status(p.pr.status, TV_ERR_TIMEOUT);
@@ -760,7 +819,7 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
         for (int e = 0; e < 4; e++) acc[e] = __fmul_rn(acc[e], a);
 #pragma unroll
         for (int j = 0; j < kJ; j++) {
-          if (ml[j].x == -INFINITY) continue;  // no position of this row in the piece (or no piece)
+          if (ml[j].y == 0.f) continue;  // no position of this row in the piece (or no piece)
           const float f = exp2f(__fsub_rn(ml[j].x, mn));
           l = __fmaf_rn(f, ml[j].y, l);
           acc[0] = __fmaf_rn(f, o[j].x, acc[0]);
@@ -828,10 +887,12 @@ template <int D>
 static tv_status launch_prompt_tc(AttnPromptTcParams& p, const AttnPromptCall& a, cudaStream_t st) {
   using C = Pa<D>;
   const tv_attn_layer* l = a.layer;
-  for (int s = 0; s < a.prompt->n_seq; s++)
+  for (int s = 0; s < a.prompt->n_seq; s++) {
     if (!encode_rows_map(&p.tmK[s], l->K[s], D, static_cast<int64_t>(l->Hkv) * l->cap, kKeyTile) ||
         !encode_rows_map(&p.tmV[s], l->V[s], D, static_cast<int64_t>(l->Hkv) * l->cap, C::VROWS))
       return TV_ERR_CUDA;
+    p.V[s] = static_cast<const __nv_bfloat16*>(l->V[s]);
+  }
   p.T = 128 / p.G;
   if (!encode_q_map(&p.tmQ, a.q, D, l->Hq, a.prompt->n_total, p.G, p.T)) return TV_ERR_CUDA;
   p.slots = static_cast<int>(slots_for(l, a.prompt, a.max_len));
