@@ -123,8 +123,6 @@ __device__ __forceinline__ void fast_gate2(float& x, float& y, float gx, float g
   y *= a * r;
 }
 
-// 0xffff in each half of a bf16 pair that is finite, 0 in others.
-__device__ __forceinline__ uint32_t finite2(uint32_t x) { return __vcmpltu2(x & 0x7f807f80u, 0x7f807f80u); }
 __device__ __forceinline__ uint32_t times_zero_plus(uint32_t x, uint32_t acc) {  // bf16 pairs
   uint32_t r;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));

@@ -41,14 +41,13 @@ constexpr int kBlk = 64;                  // rows of a block
 constexpr int kTile64 = kBlk * kBlk * 2;  // one 64 x 64 bf16 tile
 
 // What the first kernel leaves of a block and value head: P T [64][64], then W
-// as hi and lo [DK rows][64], swizzled as the second kernel's operands; then g
-// and D_63 (fp32).
+// as hi and lo [DK rows][64], swizzled as the second kernel's operands; then g (fp32).
 template <int DK>
 struct Image {
   static constexpr int WB = DK * 128;       // bytes of W hi (or lo)
   static constexpr int W = kTile64;         // offset of W hi
   static constexpr int G = W + 2 * WB;
-  static constexpr int BYTES = G + 2 * kBlk * 4;
+  static constexpr int BYTES = G + kBlk * 4;
 };
 
 struct GdnTcParams {
@@ -136,6 +135,7 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
   using C = Prep<DK>;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ float al_s[kBlk], be_s[kBlk], dl_s[kBlk];
+  __shared__ int cut_s[2];  // first row with a gate that is not finite, in rows 0 .. 31 and 32 .. 63
   __shared__ float win[4][16][17];  // win[b][i][j]: product of alpha over rows j+1 .. i of 16-row group b
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (status_bad(p.pr.status)) return;
@@ -163,6 +163,16 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
   }
   cp_async_commit();
   cp_async_wait_group<0>();
+  // a key that is not finite must not meet the zeros of rows before it (this
+  // thread's own pieces; the walk reads the key as it is)
+  for (int e = tid; e < kBlk * (DK / 8); e += 128) {
+    const uint32_t a = ks + swz(e / (DK / 8), e % (DK / 8), C::ROWB);
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    const uint32_t x = finite2(v.x), y = finite2(v.y), z = finite2(v.z), u = finite2(v.w);
+    if (~(x & y & z & u))
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x & x), "r"(v.y & y), "r"(v.z & z), "r"(v.w & u) : "memory");
+  }
   __syncthreads();
   // K K^T and Q K^T: warp w forms rows 16w .. 16w+15, columns up to its own rows
   float G[8][4], Pq[8][4];
@@ -199,8 +209,11 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
     const int h = g * r + hh;
     uint8_t* dst = p.ws + (static_cast<size_t>(blk) * p.Hv + h) * Image<DK>::BYTES;
     if (tid < kBlk) {
-      al_s[tid] = al_n;
-      be_s[tid] = be_n;
+      const bool fin = isfinite(al_n) && isfinite(be_n);
+      al_s[tid] = fin ? al_n : 1.f;
+      be_s[tid] = fin ? be_n : 0.f;
+      const unsigned m = __ballot_sync(0xffffffffu, !fin);
+      if (lane == 0) cut_s[warp] = m ? 32 * warp + __ffs(m) - 1 : kBlk;
     }
     __syncthreads();
     if (gate_row && hh + 1 < r) {
@@ -230,8 +243,8 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
         if (x > b) dl = __fmul_rn(dl, grp[x]);
       }
       dl_s[tid] = dl;
-      reinterpret_cast<float*>(dst + Image<DK>::G)[tid] = gi;
-      reinterpret_cast<float*>(dst + Image<DK>::G)[kBlk + tid] = dl;
+      // from a gate that is not finite on, nothing of the head is: the walk takes that from g
+      reinterpret_cast<float*>(dst + Image<DK>::G)[tid] = tid < min(cut_s[0], cut_s[1]) ? gi : __int_as_float(0x7fc00000);
     }
     // the decays of this warp's rows against block column b, in C layout (zero
     // above the diagonal; on it 1)
@@ -441,13 +454,13 @@ struct Walk {
   static constexpr int KQ = 2 * kBlk * DK * 2;          // [box of 64 columns][K rows, Q rows]
   static constexpr int KQBOX = 2 * kBlk * 128;          // K and Q rows of one 64-column box
   static constexpr int VOFF = KQ + Image<DK>::G;        // 64 value rows
-  static constexpr int GOFF = VOFF + kBlk * kDvs * 2;   // g and D_63
+  static constexpr int GOFF = VOFF + kBlk * kDvs * 2;   // g
   static constexpr int STAGE = GOFF + 1024;
   static constexpr int B1 = DK * 128, B2 = kBlk * 128;  // of one half: rows of [32 hi | 32 lo] columns
   static constexpr int OBUF = 2 * STAGE + 2 * (B1 + B2);  // output rows, turned around by their warps
   static constexpr int BOFF = OBUF + 4 * 2048;
   static constexpr int NBAR = 4 + 2 * 6;
-  static constexpr int SMEM = BOFF + NBAR * 8 + 16;
+  static constexpr int SMEM = BOFF + NBAR * 8 + 16 + (128 + 4) * 4;
   static constexpr int COLS = 512;
   // of one half, 256 columns: D1 twice, by block parity (its output rows are read late)
   static constexpr int T_D1 = 0, T_D2 = 128, T_D3 = 192;
@@ -498,6 +511,7 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
   const uint32_t bars = sb + C::BOFF;
   const uint32_t FULL0 = bars, EMPTY0 = bars + 16u, half0 = bars + 32u;  // then six barriers a half
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::BOFF + C::NBAR * 8);
+  int* first_bad = reinterpret_cast<int*>(tmem_slot + 4);  // [block parity][64 columns], then [parity][half]: see mark()
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* skip = reinterpret_cast<int*>(tmem_slot + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -520,6 +534,7 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
   }
   const int s = __ffs(__ballot_sync(0xffffffffu, lane < p.pr.n_seq && pos == place)) - 1;
   const int h = rem / (p.dv / kDvs), dv0 = rem % (p.dv / kDvs) * kDvs, g = h / (p.Hv / p.Hk);
+  if (threadIdx.x < 128 + 4) first_bad[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     *skip = status_bad(p.pr.status) || w.code || (sb & 1023u) ? 1 : 0;
     if (sb & 1023u) set_status(p.pr.status, TV_ERR_CUDA);
@@ -573,7 +588,7 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
           tma_load_2d(dst + kb * C::KQBOX + kBlk * 128, &p.tmQ, full, g * DK + kb * 64, off + c * kBlk);
         }
         tma_load_2d(dst + C::VOFF, &p.tmV, full, h * p.dv + dv0, off + c * kBlk);
-        bulk_g2s(dst + C::GOFF, ws0 + c * ws_step + Image<DK>::G, 2 * kBlk * 4, full);
+        bulk_g2s(dst + C::GOFF, ws0 + c * ws_step + Image<DK>::G, kBlk * 4, full);
         bulk_g2s(dst + C::KQ, ws0 + c * ws_step, Image<DK>::G, full);
       }
       if (c < nb) {
@@ -645,6 +660,38 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
       if (lane == 0) mbar_arrive(bar);
     };
     bool ok = true;
+    // Corrections that are not finite.  A zero of W or P T would carry them to
+    // rows before their own, so they enter the products as zeros, and what they
+    // reach is set afterwards: of their column, the outputs from their row on
+    // and the state.  A column's entry holds (block + 1) * 64 + 63 - row, raised
+    // by its block's rows: the first such row, if it is of this block.  By block
+    // parity, since the output rows' warps may be a block behind.
+    int* const col_bad = first_bad + hf * 32;
+    auto bad_row = [&](int c, int col) {  // (64 and more: none)
+      const int e = *reinterpret_cast<volatile int*>(col_bad + (c & 1) * 64 + col);
+      return e >> 6 == c + 1 ? 63 - (e & 63) : kBlk;
+    };
+    auto any_bad = [&](int c) { return *reinterpret_cast<volatile int*>(first_bad + 128 + (c & 1) * 2 + hf) == c + 1; };
+    auto mark = [&](int c, f2_t (&z)[16]) {
+#pragma unroll
+      for (int e = 0; e < 16; e++) {
+        float a, b;
+        f2_unpack(z[e], a, b);
+        if (!isfinite(a)) atomicMax(col_bad + (c & 1) * 64 + 2 * e, (c + 1) * 64 + 63 - ri);
+        if (!isfinite(b)) atomicMax(col_bad + (c & 1) * 64 + 2 * e + 1, (c + 1) * 64 + 63 - ri);
+        z[e] = f2_pack(isfinite(a) ? a : 0.f, isfinite(b) ? b : 0.f);
+      }
+      *reinterpret_cast<volatile int*>(first_bad + 128 + (c & 1) * 2 + hf) = c + 1;
+    };
+    auto poison = [&](f2_t (&x)[16], int c, int row) {  // NaN in the columns whose first such row is `row` or before
+#pragma unroll
+      for (int e = 0; e < 16; e++) {
+        float a, b;
+        f2_unpack(x[e], a, b);
+        x[e] = f2_pack(bad_row(c, 2 * e) <= row ? __int_as_float(0x7fc00000) : a,
+                       bad_row(c, 2 * e + 1) <= row ? __int_as_float(0x7fc00000) : b);
+      }
+    };
     // the state's two parts for the first product of the next block
     auto offer = [&]() {
       if (DK == 128 || krow) store_split(b1, i, S);
@@ -686,6 +733,10 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
 #pragma unroll
           for (int e = 0; e < 16; e++) z[e] = 0ull;
         }
+        f2_t nil[4] = {0ull, 0ull, 0ull, 0ull};  // sums of z x 0: zero, or NaN
+#pragma unroll
+        for (int e = 0; e < 16; e++) nil[e & 3] = f2_fma(z[e], 0ull, nil[e & 3]);
+        if (!(f2_hsum(f2_add(f2_add(nil[0], nil[1]), f2_add(nil[2], nil[3]))) == 0.f)) mark(c, z);
         store_split(b2, ri, z);
         fence_proxy_async_smem();
       }
@@ -698,6 +749,8 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
       const f2_t g2 = f2_dup(gc);
 #pragma unroll
       for (int e = 0; e < 16; e++) S[e] = f2_fma(g2, S[e], z[e]);
+      const bool bad = any_bad(c);
+      if (bad) poison(S, c, kBlk - 1);
       if (c + 1 < nb) offer();
       if (!krow) {
         ok = wait_warp(D2F, c & 1, abort_flag, kWaitCycles);
@@ -708,7 +761,10 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
         const f2_t f = f2_dup(__fmul_rn(p.scale, gr));
         uint32_t o[16];
 #pragma unroll
-        for (int e = 0; e < 16; e++) o[e] = pack_f2(f2_fma(f, x[e], z[e]));
+        for (int e = 0; e < 16; e++) x[e] = f2_fma(f, x[e], z[e]);
+        if (bad) poison(x, c, ri);
+#pragma unroll
+        for (int e = 0; e < 16; e++) o[e] = pack_f2(x[e]);
         // a thread holds 64 bytes of one row: turned around so that a store
         // covers whole rows' pieces, not 16 bytes of each of 32 rows
         const uint32_t ob = sb + C::OBUF + (hf * 2 + (warp & 1)) * 2048;

@@ -75,6 +75,9 @@ inline PromptRows prompt_rows(const tv_prompt* p, const int32_t* len, int max_le
   return PromptRows{p->row_off, len, p->status, p->n_seq, p->n_total, p->n_max, max_len, cap};
 }
 
+// 0xffff in each half of a bf16 pair that is finite, 0 in others.
+__device__ __forceinline__ uint32_t finite2(uint32_t x) { return __vcmpltu2(x & 0x7f807f80u, 0x7f807f80u); }
+
 // Eight consecutive values of a row, widened to fp32 (16-byte aligned).
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
