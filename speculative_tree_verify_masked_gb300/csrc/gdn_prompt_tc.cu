@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
   cp_async_wait_group<0>();
   // a key that is not finite must not meet the zeros of rows before it (this
   // thread's own pieces; the walk reads the key as it is)
+#pragma unroll 2
   for (int e = tid; e < kBlk * (DK / 8); e += 128) {
     const uint32_t a = ks + swz(e / (DK / 8), e % (DK / 8), C::ROWB);
     uint4 v;
@@ -736,8 +737,11 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
         f2_t nil[4] = {0ull, 0ull, 0ull, 0ull};  // sums of z x 0: zero, or NaN
 #pragma unroll
         for (int e = 0; e < 16; e++) nil[e & 3] = f2_fma(z[e], 0ull, nil[e & 3]);
-        if (!(f2_hsum(f2_add(f2_add(nil[0], nil[1]), f2_add(nil[2], nil[3]))) == 0.f)) mark(c, z);
         store_split(b2, ri, z);
+        if (!(f2_hsum(f2_add(f2_add(nil[0], nil[1]), f2_add(nil[2], nil[3]))) == 0.f)) {
+          mark(c, z);
+          store_split(b2, ri, z);
+        }
         fence_proxy_async_smem();
       }
       tc_fence_before();
@@ -745,11 +749,11 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
       ok = wait_warp(D3F, c & 1, abort_flag, kWaitCycles);
       if (!ok) break;
       tc_fence_after();
+      const bool bad = any_bad(c);
       load_sum(tl + C::T_D3, z);
       const f2_t g2 = f2_dup(gc);
 #pragma unroll
       for (int e = 0; e < 16; e++) S[e] = f2_fma(g2, S[e], z[e]);
-      const bool bad = any_bad(c);
       if (bad) poison(S, c, kBlk - 1);
       if (c + 1 < nb) offer();
       if (!krow) {
