@@ -400,11 +400,15 @@ tv_status tv_gdn_conv_commit(const tv_gdn_front_layer* layer, const tv_tree* tre
  *
  * The offsets live on the device, so a captured graph serves every batch that
  * fits its host bounds; rows from row_off[n_seq] on are padding, neither read
- * nor written.  Offsets that do not start at 0, that fall, that give a sequence more
- * than n_max rows or end past n_total set TV_ERR_ROWS; a length outside
+ * nor written.  Offsets that do not start at 0, that fall, that give a sequence
+ * more than n_max rows or end past n_total set TV_ERR_ROWS; a length outside
  * 0..max_len sets TV_ERR_LEN; rows past a cache's cap set TV_ERR_CAPACITY.
  * Any of them makes the whole call a no-op.  Sequences of one call must not
- * share a cache, state or tail.  n_total = 0 does nothing. */
+ * share a cache, state or tail.  n_total = 0 does nothing.
+ *
+ * An infinity or NaN in a row reaches what the formulas let it reach: rows
+ * before it, other sequences and (where they are apart) other heads and
+ * columns are as if it were finite. */
 typedef struct {
   int32_t n_seq;          /* sequences, 1..TV_MAX_SEQ (host) */
   int32_t n_total;        /* rows the packed buffers hold, 0..TV_MAX_PROMPT_ROWS (host) */
@@ -446,7 +450,7 @@ size_t tv_attn_prompt_workspace_bytes(const tv_attn_layer* layer, const tv_promp
 /* Causal attention of a prompt's rows over the cache: row i of sequence s
  * sees cache rows 0 .. len[s] + i, its own included (tv_attn_prompt_front has
  * put the prompt's rows there).
- *  q, out [n_total][Hq][D] in the layer's dtype (out must not alias q)
+ *  q, out [n_total][Hq][D] in the layer's dtype (memory shared by q and out: TV_ERR_ARG)
  *  gate   [n_total][Hq][D], applied as in tv_attn_tree_verify_gated, or NULL
  *  scale  score scale > 0
  *  workspace device scratch of at least tv_attn_prompt_workspace_bytes() bytes,
@@ -465,7 +469,7 @@ size_t tv_gdn_prompt_workspace_bytes(const tv_gdn_layer* layer, const tv_prompt*
  * tv_gdn_tree_verify, row after row from the sequence's state, which is left
  * advanced by all of them (a sequence without rows keeps its state).
  *  q, k [n_total][Hk][dk]; v [n_total][Hv][dv]; alpha, beta fp32 [n_total][Hv]
- *  out  [n_total][Hv][dv] (must not alias v); scale output scale > 0
+ *  out  [n_total][Hv][dv] (memory shared with q, k or v: TV_ERR_ARG); scale output scale > 0
  *  workspace as in tv_attn_prompt. */
 tv_status tv_gdn_prompt(const tv_gdn_layer* layer, const tv_prompt* prompt, const void* q, const void* k,
                         const void* v, const float* alpha, const float* beta, void* out, float scale,
@@ -475,7 +479,7 @@ tv_status tv_gdn_prompt(const tv_gdn_layer* layer, const tv_prompt* prompt, cons
  * and continues into its tail; unlike there the tails then advance to the
  * last W-1 raw inputs (a prompt's rows are committed as they are read).
  * Arguments as in tv_gdn_front with n_total rows, every pointer (wconv and
- * tails too) 16-byte aligned; the outputs must not alias x. */
+ * tails too) 16-byte aligned; memory shared by x and q, k or v: TV_ERR_ARG. */
 tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* layer, const tv_prompt* prompt, const void* x,
                               const float* a_raw, const float* b_raw, void* q, void* k, void* v, float* alpha,
                               float* beta, tv_stream stream);

@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
   PromptPlan& pl = *reinterpret_cast<PromptPlan*>(gb + C::LOFF + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int worker = static_cast<int>(blockIdx.x);
+  pdl_trigger();  // the join makes its plan on SMs that are done
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NU; i++) {
@@ -770,15 +771,14 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
   __shared__ PromptPlan pl;
   __shared__ int skip;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  if (warp == 0) {
-    const bool bad = status_bad(p.pr.status);
+  if (warp == 0) {  // (offsets and lengths were there before the launch that this one follows)
     const WarpSeqs w = load_seqs(p.pr, lane);
-    if (lane == 0) skip = bad || w.code ? 1 : 0;
+    if (lane == 0) skip = w.code;
     if (!w.code) make_plan(p, w, lane, pl);
   }
   __syncthreads();
-  if (skip) return;
+  pdl_wait();
+  if (skip || status_bad(p.pr.status)) return;
   for (int at = 0; at < p.pr.n_seq; at++) {
     const int s = pl.seq[at];
     if (pl.pm[s] < 2) continue;
@@ -803,10 +803,13 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
         float2 ml[kJ];
 #pragma unroll
         for (int j = 0; j < kJ; j++) {
-          const float* r = rec + step * min(j0 + j, np - 1);
-          o[j] = *reinterpret_cast<const float4*>(r + col);
-          ml[j] = *reinterpret_cast<const float2*>(r + D);
-          if (j0 + j >= np) ml[j] = make_float2(-INFINITY, 0.f);
+          const float* r = rec + step * (j0 + j);
+          o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          ml[j] = make_float2(-INFINITY, 0.f);
+          if (j0 + j < np) {
+            o[j] = *reinterpret_cast<const float4*>(r + col);
+            ml[j] = *reinterpret_cast<const float2*>(r + D);
+          }
         }
         float mn = m;
 #pragma unroll

@@ -263,6 +263,10 @@ extern "C" tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* f, const tv_p
   if (!aligned16(x) || !aligned16(a_raw) || !aligned16(b_raw) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
       !aligned16(alpha) || !aligned16(beta) || !aligned16(f->wconv))
     return TV_ERR_ALIGN;
+  const int64_t kc = static_cast<int64_t>(f->Hk) * f->dk, vc = static_cast<int64_t>(f->Hv) * f->dv, C = 2 * kc + vc;
+  if (overlap(x, q, pr->n_total, C, kc, f->dtype) || overlap(x, k, pr->n_total, C, kc, f->dtype) ||
+      overlap(x, v, pr->n_total, C, vc, f->dtype))
+    return TV_ERR_ARG;  // a row is read again by the rows after it
   p.pr = prompt_rows(pr, nullptr, 0, 0);
   p.x = x; p.a_raw = a_raw; p.b_raw = b_raw; p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.beta = beta;
   p.wconv = f->wconv;

@@ -166,6 +166,10 @@ extern "C" tv_status tv_gdn_prompt(const tv_gdn_layer* l, const tv_prompt* pr, c
   if (!q || !k || !v || !alpha || !beta || !out) return TV_ERR_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(alpha) || !aligned16(beta) || !aligned16(out))
     return TV_ERR_ALIGN;
+  const int64_t kc = static_cast<int64_t>(l->Hk) * l->dk, vc = static_cast<int64_t>(l->Hv) * l->dv;
+  if (overlap(v, out, pr->n_total, vc, vc, l->dtype) || overlap(q, out, pr->n_total, kc, vc, l->dtype) ||
+      overlap(k, out, pr->n_total, kc, vc, l->dtype))
+    return TV_ERR_ARG;  // other heads and blocks still read them
   p.pr = prompt_rows(pr, nullptr, 0, 0);
   p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.beta = beta; p.out = out;
   p.Hk = l->Hk; p.Hv = l->Hv; p.dv = l->dv; p.scale = scale;

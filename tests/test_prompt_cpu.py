@@ -216,3 +216,25 @@ def test_oracle_front_ends_are_the_tree_forms_of_a_chain():
         assert np.abs(turned[i].numpy() - OA.rope(h[i], 11 + i, 6, 1e4)).max() < 1e-12
     unit = OP.norm_rope(torch.tensor(h), torch.ones(8), torch.zeros(n), 1e-12, 0, 1e4)
     assert np.abs((unit.numpy() ** 2).mean(-1) - 1).max() < 1e-9
+
+
+def test_shared_memory_refused(L):
+    """Outputs that share memory with inputs other rows still read: TV_ERR_ARG, before anything is launched."""
+    q, n = 1 << 20, 8
+    a = attn_layer()
+    row = 24 * 256 * 2
+    for out in (q, q + 16, q + n * row - 16, q - n * row + 16):
+        assert L.tv_attn_prompt(ref(a), ref(good_prompt(n)), vp(16), 8, vp(q), None, vp(out), 0.1, None, 0, None) == 1
+    for out in (q + n * row, q - n * row):  # side by side: on to the next check (here the missing workspace)
+        big = B.tv_attn_layer(B.TV_BF16, 24, 4, 256, 1 << 20, (vp * 8)(*[0x3000] * 8), (vp * 8)(*[0x4000] * 8))
+        assert L.tv_attn_prompt(ref(big), ref(good_prompt(n)), vp(16), 1 << 19, vp(q), None, vp(out), 0.1, None, 0, None) == 8
+    g = B.tv_gdn_layer(B.TV_BF16, 4, 8, 128, 128, (vp * 8)(*[0x3000] * 8))
+    k, v, far = q + (1 << 20), q + (2 << 20), 1 << 30
+    for out in (q + 16, k, v - 16):
+        assert L.tv_gdn_prompt(ref(g), ref(good_prompt(n)), vp(q), vp(k), vp(v), vp(far), vp(far), vp(out), 0.1, None, 0, None) == 1
+    f = B.tv_gdn_front_layer(B.TV_BF16, 4, 8, 128, 128, 4, 0x2000, (vp * 8)(*[0x3000] * 8))
+    c = 2 * 4 * 128 + 8 * 128
+    for i in range(3):
+        outs = [q, k, v]
+        x = outs[i] - n * c * 2 + 16
+        assert L.tv_gdn_prompt_front(ref(f), ref(good_prompt(n)), vp(x), vp(far), vp(far), *map(vp, outs), vp(far), vp(far), None) == 1
