@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(128) attn_prompt_cuda_kernel(const __grid_cons
   float* vb = kb + 2 * C::TILE;        // [2][32][LD] values
   float* ps = vb + 2 * C::TILE;        // [warp][32][RPW] probabilities
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
   if (status_bad(p.pr.status)) return;
   const WarpSeqs w = load_seqs(p.pr, lane);
   if (w.code) {
@@ -174,7 +175,7 @@ static tv_status launch_cuda(const AttnPromptCudaParams& p, cudaStream_t st) {
       return TV_ERR_CUDA;
     set = true;
   }
-  attn_prompt_cuda_kernel<D, RPW><<<dim3(static_cast<unsigned>(gx), p.Hkv, p.pr.n_seq), 128, C::SMEM, st>>>(p);
+  launch_k(true, attn_prompt_cuda_kernel<D, RPW>, dim3(static_cast<unsigned>(gx), p.Hkv, p.pr.n_seq), dim3(128), C::SMEM, st, p);
   return launch_status();
 }
 

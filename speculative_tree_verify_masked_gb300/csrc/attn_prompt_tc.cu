@@ -281,7 +281,6 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
   PromptPlan& pl = *reinterpret_cast<PromptPlan*>(gb + C::LOFF + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int worker = static_cast<int>(blockIdx.x);
-  pdl_trigger();  // the join makes its plan on SMs that are done
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NU; i++) {
@@ -304,6 +303,8 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
     met[0] = met[1] = 0;
     fence_mbar_init();
   }
+  pdl_wait();
+  pdl_trigger();  // the join makes its plan on SMs that are done
   if (warp == 2) {  // the plan; a bad launch sets its code and every CTA leaves
     const bool bad = status_bad(p.pr.status);
     const WarpSeqs w = load_seqs(p.pr, lane);
@@ -904,7 +905,7 @@ static tv_status launch_prompt_tc(AttnPromptTcParams& p, const AttnPromptCall& a
       return TV_ERR_CUDA;
     set = true;
   }
-  attn_prompt_tc_kernel<D><<<dim3(p.workers), 384, C::SMEM, st>>>(p);
+  launch_k(true, attn_prompt_tc_kernel<D>, dim3(p.workers), dim3(384), C::SMEM, st, p);
   // the join has work only where the plan, made on the device, split items
   if (p.slots > 0) launch_k(true, attn_prompt_join_kernel<D>, dim3(num_sms() * 4), dim3(256), 0, st, p);
   return launch_status();

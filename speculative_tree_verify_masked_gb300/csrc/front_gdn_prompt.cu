@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
   constexpr int WM = WT ? WT : kMaxConvWidth;
   const int lane = threadIdx.x & 31;
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  pdl_wait();
   if (status_bad(p.pr.status)) return;
   const WarpSeqs w = load_seqs(p.pr, lane);
   if (w.code) {
@@ -238,8 +239,8 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
 
 template <typename T, int DH>
 static void launch_prompt_front(const GdnPromptFrontParams& p, unsigned grid, cudaStream_t st) {
-  if (p.W == 4) gdn_prompt_front_kernel<T, DH, 4><<<grid, 128, 0, st>>>(p);
-  else gdn_prompt_front_kernel<T, DH, 0><<<grid, 128, 0, st>>>(p);
+  if (p.W == 4) launch_k(true, gdn_prompt_front_kernel<T, DH, 4>, dim3(grid), dim3(128), 0, st, p);
+  else launch_k(true, gdn_prompt_front_kernel<T, DH, 0>, dim3(grid), dim3(128), 0, st, p);
 }
 
 }  // namespace tv

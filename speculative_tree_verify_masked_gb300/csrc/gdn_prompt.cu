@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(128) gdn_prompt_rec_kernel(const __grid_consta
   const int s = blockIdx.y, tid = threadIdx.x;
   const int rb_per_head = (p.dv + R - 1) / R;
   const int h = blockIdx.x / rb_per_head, rb = blockIdx.x % rb_per_head;
+  pdl_wait();
   if (status_bad(p.pr.status)) return;
   const WarpSeqs w = load_seqs(p.pr, tid & 31);
   if (w.code) {
@@ -132,7 +133,7 @@ template <typename T, int LPR>
 static void launch_rec(const GdnPromptParams& p, cudaStream_t st) {
   constexpr int R = 128 / LPR;
   const dim3 grid(p.Hv * ((p.dv + R - 1) / R), p.pr.n_seq);
-  gdn_prompt_rec_kernel<T, LPR><<<grid, 128, 0, st>>>(p);
+  launch_k(true, gdn_prompt_rec_kernel<T, LPR>, grid, dim3(128), 0, st, p);
 }
 
 }  // namespace tv

@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
   __shared__ int cut_s[2];  // first row with a gate that is not finite, in rows 0 .. 31 and 32 .. 63
   __shared__ float win[4][16][17];  // win[b][i][j]: product of alpha over rows j+1 .. i of 16-row group b
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
   if (status_bad(p.pr.status)) return;
   const WarpSeqs w = load_seqs(p.pr, lane);
   if (w.code) {
@@ -826,7 +827,7 @@ static tv_status launch_tc(const GdnTcParams& p, int64_t blocks, cudaStream_t st
       return TV_ERR_CUDA;
     set = true;
   }
-  gdn_block_prep_kernel<DK><<<dim3(static_cast<unsigned>(blocks), p.Hk), 128, Prep<DK>::SMEM, st>>>(p);
+  launch_k(true, gdn_block_prep_kernel<DK>, dim3(static_cast<unsigned>(blocks), p.Hk), dim3(128), Prep<DK>::SMEM, st, p);
   launch_k(true, gdn_block_walk_kernel<DK>, dim3(p.pr.n_seq * p.Hv * (p.dv / kDvs)), dim3(352), Walk<DK>::SMEM, st, p);
   return launch_status();
 }

@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 5 : 4) norm_rope_kernel(
   __shared__ __align__(16) float row_s[4][GPW][D];
   const int wib = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x * 4 + wib, part = blockIdx.y;  // a CTA's warps have one kind of head: they end together
+  pdl_wait();
   if (row >= p.n_rows) return;  // whole warps leave
   const int grp = lane / LPH, gl = lane % LPH, d0 = gl * 8;
   // this warp's heads; the first loads start before the row's place is known
@@ -286,13 +287,13 @@ static tv_status norm_rope_launch(const tv_attn_layer* l, NormRopeParams& p, con
   const bool bf = l->dtype == TV_BF16;
   switch (l->D) {
     case 64:
-      if (bf) norm_rope_kernel<__nv_bfloat16, 64><<<g, 128, 0, st>>>(p); else norm_rope_kernel<float, 64><<<g, 128, 0, st>>>(p);
+      if (bf) launch_k(true, norm_rope_kernel<__nv_bfloat16, 64>, g, dim3(128), 0, st, p); else launch_k(true, norm_rope_kernel<float, 64>, g, dim3(128), 0, st, p);
       break;
     case 128:
-      if (bf) norm_rope_kernel<__nv_bfloat16, 128><<<g, 128, 0, st>>>(p); else norm_rope_kernel<float, 128><<<g, 128, 0, st>>>(p);
+      if (bf) launch_k(true, norm_rope_kernel<__nv_bfloat16, 128>, g, dim3(128), 0, st, p); else launch_k(true, norm_rope_kernel<float, 128>, g, dim3(128), 0, st, p);
       break;
     default:
-      if (bf) norm_rope_kernel<__nv_bfloat16, 256><<<g, 128, 0, st>>>(p); else norm_rope_kernel<float, 256><<<g, 128, 0, st>>>(p);
+      if (bf) launch_k(true, norm_rope_kernel<__nv_bfloat16, 256>, g, dim3(128), 0, st, p); else launch_k(true, norm_rope_kernel<float, 256>, g, dim3(128), 0, st, p);
   }
   return launch_status();
 }
