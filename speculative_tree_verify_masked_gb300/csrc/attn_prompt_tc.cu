@@ -17,7 +17,8 @@
 // Roles (384 threads, one CTA per SM, persistent).  Warp 0 streams key and
 // value units by TMA through one ring in the order the tensor core takes
 // them: K0, K1 V0, K2 V1, ...  Warp 11 brings each item's queries, warp 1
-// issues Q K^T, warp 10 P V, each from one thread.  Warps 2-9 do the softmax, two threads to a row (64 columns each).
+// issues Q K^T, warp 10 P V, each from one thread.  Warps 2-9 do the softmax,
+// two threads to a row (64 columns each).
 // Tensor memory holds O [D columns], one S [128] and Q [D/2, the A operand of
 // Q K^T], 512 columns at D = 256; P goes through shared memory.  Because PV of
 // tile t-1 sits between Q K^T of t and of t+1 on the tensor pipe, S(t) is read
@@ -36,12 +37,20 @@
 // workers; where there are too few of them (short prompts behind a long
 // context) each is cut along its keys into pieces of S tiles, whose O, m and l
 // go to the workspace as fp32 and are joined by a second kernel.
+//
+// Bound by the tensor cores: at D = 256 a tile's two products take 2,048 cycles
+// and a tile takes about 2,300 (tensor pipe 76 % active over a whole call of
+// 8,192 rows under a power cap).  24 + 4 heads of 256, and the same operations at
+// the measured rate of a large library product: 8,192 rows 495 us (432), 1,024
+// rows behind 130,048 2,030 us (1,722), packed 2,047 + 1 + 515 + 4,096 rows with a
+// gate 261 us (159; tiles that are half masked and short items), 24 rows behind
+// 65,536 70 us (40 of bytes; pieces of a few tiles, then the join).
 #include <cmath>
 #include <cstring>
 
 #include "attn_prompt.cuh"
-#include "attn_shared.cuh"
 #include "ptx.cuh"
+#include "tensor_map.hpp"
 
 namespace tv {
 

@@ -50,12 +50,12 @@
 #include <cmath>
 #include <cstring>
 
-#include "attn_shared.cuh"
 #include "common.cuh"
 #include "host.hpp"
 #include "launchers.hpp"
 #include "mma_tile.cuh"
 #include "ptx.cuh"
+#include "tensor_map.hpp"
 
 namespace tv {
 
@@ -261,6 +261,38 @@ __device__ __forceinline__ void store_state(uint32_t tO, float* rec, int hf, flo
     } else {
       rec[D + 2] = lh;
     }
+  }
+}
+
+// Queries of one row into TMEM (bf16 pairs, columns T_Q ..).  For D >= 128
+// each half-tile thread moves its half of the row (D/4 columns from hf*D/4);
+// for D = 64 the half-0 thread moves the whole row (32 columns).
+template <int D>
+struct QShare {
+  static constexpr int N = D >= 128 ? D / 16 : D / 8;  // 16-byte pieces per thread
+  static constexpr int COL0 = D >= 128 ? D / 4 : 0;    // first column of half 1
+};
+template <int D>
+__device__ __forceinline__ void q_fetch(const __nv_bfloat16* qrow, int hf, uint4 (&qv)[QShare<D>::N]) {
+  const bool act = qrow != nullptr && (D >= 128 || hf == 0);
+  const uint4* q4 = act ? reinterpret_cast<const uint4*>(qrow) + hf * QShare<D>::N : nullptr;
+#pragma unroll
+  for (int i = 0; i < QShare<D>::N; i++) qv[i] = act ? q4[i] : make_uint4(0u, 0u, 0u, 0u);
+}
+template <int D>
+__device__ __forceinline__ void q_store(uint32_t tq, int hf, const uint4 (&qv)[QShare<D>::N]) {
+  if (D < 128 && hf != 0) return;
+#pragma unroll
+  for (int j = 0; j < QShare<D>::N / 8; j++) {
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      r[4 * i] = qv[8 * j + i].x;
+      r[4 * i + 1] = qv[8 * j + i].y;
+      r[4 * i + 2] = qv[8 * j + i].z;
+      r[4 * i + 3] = qv[8 * j + i].w;
+    }
+    tmem_st32(tq + hf * QShare<D>::COL0 + 32 * j, r);
   }
 }
 
@@ -752,8 +784,7 @@ __global__ void __launch_bounds__(384, 1) attn_split_kernel(const __grid_constan
 // Warp-level bf16 tensor-core tiles (m16n8k16, fp32 accumulate) for the own
 // segment's two small products: its rows are one node's G query heads, far
 // below the 64- or 128-row tiles of tcgen05, and these need no tensor memory,
-// so several tail CTAs share an SM.
-// (ldsm_x4, mma16816 and swz: mma_tile.cuh)
+// so several tail CTAs share an SM (pieces: mma_tile.cuh).
 
 template <int D>
 struct Tail {

@@ -2,12 +2,16 @@
 // along each sequence (continuing from its committed tail), SiLU, the q/k head
 // norms and the gates; the tails move on to the sequence's last W-1 raw inputs.  Formulas as in front_gdn.cu.
 //
-// Bound by HBM: every raw channel is read once and written once.  A group of
-// DH/8 lanes owns one head (eight consecutive channels a lane, one 16-byte
-// access a row) and walks a strip of consecutive rows, a few loaded ahead, with
-// the W-1 rows before the current one in registers; only a strip's last W-1
-// rows are read twice (by it and the next strip).  Taps run in fp32 in order, oldest
-// first, as in the tree and decode forms.
+// A group of DH/8 lanes owns one head (eight consecutive channels a lane, one
+// 16-byte access a row) and walks a strip of consecutive rows of one sequence, a
+// few loaded ahead, with the W-1 rows before the current one in registers; only
+// a strip's last W-1 rows are read twice (by it and the next strip).  Taps run
+// in fp32 in order, oldest first, as in the tree and decode forms.
+//
+// Bound by HBM, every raw channel read once and written once, with the issue
+// slots close behind (53 % at 57 % of DRAM throughput).  16 + 48 heads of 128,
+// W = 4: 8,192 rows (342 MB) 66.5 us, 5.1 TB/s, 0.77 of a copy's rate; 731 rows
+// in four sequences 11.5 us, two thirds of that one strip's latency.
 #include "prompt.cuh"
 #include "front_gdn.cuh"
 #include "launchers.hpp"

@@ -12,28 +12,35 @@
 //
 // Two kernels.  The first forms W and P T of every block and value head, all
 // independent (with T applied ahead of time, the walk has two products in its
-// chain instead of three).  The second walks a sequence's blocks, one CTA per
-// (value head, 64 state columns dv):
+// chain instead of three: 359 us against 544 at 8,192 rows).  The second walks a
+// sequence's blocks, one CTA per (value head, 64 state columns dv), as two
+// halves of 32 columns that run for themselves, so that one's products run
+// under the other's splits:
 //   [K; Q] S0^T  ->  R  ->  W R  ->  S,   and beside the chain  P T R -> o,
 // each 128 rows tall on the tcgen05 tensor cores with fp32 sums in tensor
 // memory, the state in registers (a thread holds one key row, 32 columns).
 //
 // Precision.  k, q and v are bf16 as they come.  What is formed on the way (S,
 // R, W, A, T) enters a product as two bf16 parts, x = hi + lo with hi =
-// bf16(x), lo = bf16(x - hi), which leaves 2^-17 of each value at most: hi and
-// lo stand side by side in the product's columns, or take a pass each (lo lo is
-// left out).  One part alone would leave 2^-9, far above what a state that
-// lives over a long prompt can take; with two it stays within some 5e-6 of the
-// recurrence in 64 bits (rel-L2, 8,192 rows).  P T only reaches the bf16 output and is rounded once.
+// bf16(x), lo = bf16(x - hi), which leaves 2^-17 of each value at most: in the
+// walk hi and lo of S and R stand side by side in a product's columns and W's
+// take a pass each; in the first kernel lo lo is left out.  One part alone would
+// leave 2^-9, far above what a state that lives over a long prompt can take;
+// with two it stays within 5e-6 of the recurrence in 64 bits (rel-L2, 8,192
+// rows: 4.3e-6, and 5.1e-6 without W lo's product with R lo).  P T only reaches
+// the bf16 output and is rounded once.
 //
-// Bound by the chain of products, tensor-memory round trips and splits a
-// block, not by bytes.
+// Bound by the chain of products, tensor-memory round trips and splits a block,
+// not by bytes: 16 + 48 heads of 128 x 128, 8,192 rows 334 us (128 + 206; 41.5
+// of bytes), about 3,000 cycles a block and CTA, the tensor pipe busy for 65 % of
+// them; 2,047 + 1 + 515 + 4,096 rows 234 us (105 + 126).  The first kernel waits
+// for its own steps (33 % of issue slots; registers hold it to three CTAs an SM).
 #include <cstring>
 
-#include "attn_shared.cuh"
 #include "gdn_prompt.cuh"
 #include "mma_tile.cuh"
 #include "ptx.cuh"
+#include "tensor_map.hpp"
 
 namespace tv {
 
