@@ -182,7 +182,9 @@ static tv_status launch_cuda(const AttnPromptCudaParams& p, cudaStream_t st) {
 }
 
 // Four rows a warp, or one while four would leave SMs without a CTA (a call's
-// time is then one CTA's walk over the keys, which is shorter with fewer rows).
+// time is then one CTA's walk over the keys, which is shorter with fewer rows):
+// 256 + 37 rows of 2 heads of 64 take 13.8 us with one and 20.7 with four, 512
+// rows of 8 heads 46 either way, 2,048 rows of 8 heads 472 and 296.
 template <int D>
 static tv_status launch_cuda_rows(const AttnPromptCudaParams& p, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.pr.n_total) * p.Hq;

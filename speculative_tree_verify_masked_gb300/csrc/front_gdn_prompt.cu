@@ -241,6 +241,9 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
   }
 }
 
+// Width 4 keeps its taps and window in registers at fixed places and loads a
+// group of rows ahead; any width's form has room for 8 and does neither: 66.9 and
+// 184.7 us at 8,192 rows of 16 + 48 heads of 128, 11.4 and 26.9 at 731.
 template <typename T, int DH>
 static void launch_prompt_front(const GdnPromptFrontParams& p, unsigned grid, cudaStream_t st) {
   if (p.W == 4) launch_k(true, gdn_prompt_front_kernel<T, DH, 4>, dim3(grid), dim3(128), 0, st, p);

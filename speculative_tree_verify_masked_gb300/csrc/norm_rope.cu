@@ -272,9 +272,11 @@ static tv_status norm_rope_launch(const tv_attn_layer* l, NormRopeParams& p, con
     const double turns = std::pow(static_cast<double>(theta), -2.0 * j / rot) * 0.15915494309189533577;  // / 2 pi
     p.rate[j] = static_cast<uint64_t>(std::ldexp(turns, 64));
   }
-  // heads a warp walks: all of a kind with many rows (the row's factors are
+  // Heads a warp walks: all of a kind with many rows (the row's factors are
   // formed once for them; up to eight rounds), fewer while the launch would
-  // leave SMs without work
+  // leave SMs without work, down to one round of four.  24 + 4 + 4 heads of 256:
+  // 4 rows take 3.6 us in rounds of four, 6.1 with all 24 heads a warp; 64 rows
+  // 3.8 and 6.2 (4.7 with one head a warp); 8,192 rows 50 either way.
   const int gpw = 256 / l->D;
   int hpw = 32 * gpw;
   auto split = [&]() {
@@ -283,7 +285,7 @@ static tv_status norm_rope_launch(const tv_attn_layer* l, NormRopeParams& p, con
     p.parts = p.q_parts + p.k_parts + (p.form == 2 ? p.k_parts : 0);
     return static_cast<int64_t>(p.n_rows) * p.parts;
   };
-  while (hpw > gpw && split() < 16 * num_sms()) hpw >>= 1;
+  while (hpw > 4 * gpw && split() < 16 * num_sms()) hpw >>= 1;
   p.heads_per_warp = hpw;
   split();
   if (p.parts > 65535) return TV_ERR_SHAPE;
