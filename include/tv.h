@@ -455,8 +455,9 @@ size_t tv_attn_prompt_workspace_bytes(const tv_attn_layer* layer, const tv_promp
  *  scale  score scale > 0
  *  workspace device scratch of at least tv_attn_prompt_workspace_bytes() bytes,
  *         not shared with work that can run at the same time
- * Rows of a cache behind the ones a sequence sees are not read into its
- * results, whatever they hold. */
+ * No cache row from len[s] + rows on is read, so pooled caches need no page
+ * behind the last row that a sequence holds; padding rows of q and gate are not
+ * read into any result. */
 tv_status tv_attn_prompt(const tv_attn_layer* layer, const tv_prompt* prompt, const int32_t* len, int32_t max_len,
                          const void* q, const void* gate, void* out, float scale, void* workspace,
                          size_t workspace_bytes, tv_stream stream);

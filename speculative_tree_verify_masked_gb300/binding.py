@@ -462,7 +462,11 @@ def _need(where: str, **tensors):
 
 
 def _ws_bytes(ws) -> int:
-    return 0 if ws is None else ws.numel() * ws.element_size()
+    if ws is None:
+        return 0
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous GPU memory")
+    return ws.numel() * ws.element_size()
 
 
 def tv_attn_norm_rope(layer: AttnLayer, tree: Tree | None, n_seq, len_, max_len, q_norm, k_norm, eps, rot_dims, theta,

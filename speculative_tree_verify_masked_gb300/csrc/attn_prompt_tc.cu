@@ -155,6 +155,12 @@ static __device__ __noinline__ void put_nonfinite(const __nv_bfloat16* v, int st
   }
 }
 
+// The first row that is loaded for the key tile at position pos: a tile that
+// would reach past the rows the sequence holds (the cache may end there, or its
+// pages) is taken from further up, and the positions before pos in it are masked.
+// Rows before the cache's first come in as zeros.
+__device__ __forceinline__ int tile_row(int pos, int end) { return min(pos, end - kKeyTile); }
+
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // The plan, by one warp.  Cost of a candidate, in key tiles: the waves of
@@ -345,12 +351,12 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
     int wave = 0;
     PromptItem I;
     while (ok && next_item(p, pl, total, worker, wave, I)) {
-      const int n = I.t1 - I.t0, base = I.g * p.pr.cap;
+      const int n = I.t1 - I.t0, end = pl.L[I.s] + pl.n[I.s];
       for (int e = 0; e < 2 * n && ok; e++) {
         // load order K0, K1 V0, K2 V1, ..., V(n-1)
         const bool is_k = e == 0 || ((e & 1) && e != 2 * n - 1);
         const int k = e == 0 ? 0 : is_k ? (e + 1) / 2 : (e == 2 * n - 1 ? n - 1 : (e - 2) / 2);
-        const int row = base + (I.t0 + k) * kKeyTile;
+        const int row = tile_row((I.t0 + k) * kKeyTile, end);
 #pragma unroll
         for (int u = 0; u < C::UPT; u++, it++) {
           const uint32_t slot = it % C::NU, full = UFULL0 + 8u * slot;
@@ -362,10 +368,10 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
           mbar_arrive_expect_tx(full, C::UNIT);
           if (is_k) {
 #pragma unroll
-            for (int b = 0; b < C::KBU; b++) tma_load_2d(dst + b * C::KBOX, &p.tmK[I.s], full, (u * C::KBU + b) * 64, row);
+            for (int b = 0; b < C::KBU; b++) tma_load_3d(dst + b * C::KBOX, &p.tmK[I.s], full, (u * C::KBU + b) * 64, row, I.g);
           } else {
 #pragma unroll
-            for (int b = 0; b < C::VB; b++) tma_load_2d(dst + b * C::VBOX, &p.tmV[I.s], full, b * 64, row + u * C::VROWS);
+            for (int b = 0; b < C::VB; b++) tma_load_3d(dst + b * C::VBOX, &p.tmV[I.s], full, b * 64, row + u * C::VROWS, I.g);
           }
         }
       }
@@ -535,7 +541,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
     uint16_t id = 0;
     while (ok && more) {
       id++;
-      const int n = I.t1 - I.t0, L = pl.L[I.s];
+      const int n = I.t1 - I.t0, L = pl.L[I.s], end = L + pl.n[I.s];
       const bool act = orow >= 0;
       const int last = act ? L + I.i * p.T + tok : -1;  // last position this row sees
       const int seen_all = L + I.i * p.T + 1;           // positions every row here sees
@@ -560,9 +566,9 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
         arrive(SFREE);
         const int pos = (I.t0 + k) * kKeyTile;
         if (pos + kKeyTile > seen_all) {  // a tile some row here does not see whole
-          const int vis = last - (pos + hf * 64);
+          const int row = tile_row(pos, end), vis = last - (row + hf * 64), from = pos - (row + hf * 64);
 #pragma unroll
-          for (int j = 0; j < 64; j++) sv[j] = j <= vis ? sv[j] : -INFINITY;
+          for (int j = 0; j < 64; j++) sv[j] = j >= from && j <= vis ? sv[j] : -INFINITY;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -615,7 +621,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
           tmem_st_wait();
         }
         if (pos + kKeyTile > seen_all) {
-          const int first = max(seen_all - pos, 0);
+          const int first = max(seen_all - tile_row(pos, end), 0);
           const uint32_t u0 = it + (k < n - 1 ? 2 * k + 2 : 2 * n - 1) * C::UPT;  // the tile's value units
           uint32_t slot[C::UPT];
 #pragma unroll
@@ -859,15 +865,14 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// [Hkv * cap rows][D] bf16 cache as a 2-D tensor in boxes of 64 columns.
-static bool encode_rows_map(CUtensorMap* m, void* base, int D, int64_t rows, int box_rows) {
+// A bf16 cache [Hkv][cap][D] as a 3-D tensor in boxes of 64 columns of one head.
+static bool encode_cache_map(CUtensorMap* m, void* base, int D, int cap, int Hkv, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(cap), static_cast<cuuint64_t>(Hkv)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(D) * 2 * cap};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -899,8 +904,8 @@ static tv_status launch_prompt_tc(AttnPromptTcParams& p, const AttnPromptCall& a
   using C = Pa<D>;
   const tv_attn_layer* l = a.layer;
   for (int s = 0; s < a.prompt->n_seq; s++) {
-    if (!encode_rows_map(&p.tmK[s], l->K[s], D, static_cast<int64_t>(l->Hkv) * l->cap, kKeyTile) ||
-        !encode_rows_map(&p.tmV[s], l->V[s], D, static_cast<int64_t>(l->Hkv) * l->cap, C::VROWS))
+    if (!encode_cache_map(&p.tmK[s], l->K[s], D, l->cap, l->Hkv, kKeyTile) ||
+        !encode_cache_map(&p.tmV[s], l->V[s], D, l->cap, l->Hkv, C::VROWS))
       return TV_ERR_CUDA;
     p.V[s] = static_cast<const __nv_bfloat16*>(l->V[s]);
   }
@@ -926,7 +931,6 @@ size_t attn_prompt_tc_ws_bytes(const tv_attn_layer* l, const tv_prompt* pr, int 
 
 tv_status attn_prompt_tc_launch(const AttnPromptCall& a, cudaStream_t st) {
   const tv_attn_layer* l = a.layer;
-  if (static_cast<int64_t>(l->Hkv) * l->cap > 0x7fffffff) return TV_ERR_SHAPE;  // TMA row coordinates are 32-bit
   const size_t need = attn_prompt_tc_ws_bytes(l, a.prompt, a.max_len);
   if (need > 0 && (!a.ws || a.ws_bytes < need)) return TV_ERR_WORKSPACE;
   if (!aligned16(a.ws)) return TV_ERR_ALIGN;

@@ -238,3 +238,12 @@ def test_shared_memory_refused(L):
         outs = [q, k, v]
         x = outs[i] - n * c * 2 + 16
         assert L.tv_gdn_prompt_front(ref(f), ref(good_prompt(n)), vp(x), vp(far), vp(far), *map(vp, outs), vp(far), vp(far), None) == 1
+
+
+def test_binding_refuses_host_memory():
+    """Buffers that are not GPU memory never reach the library."""
+    with pytest.raises(ValueError):
+        B._ws_bytes(torch.zeros(16, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        B._need("call", q=(torch.zeros(16), torch.float32, 16))
+    assert B._ws_bytes(None) == 0
