@@ -406,6 +406,13 @@ tv_status tv_gdn_conv_commit(const tv_gdn_front_layer* layer, const tv_tree* tre
  * Any of them makes the whole call a no-op.  Sequences of one call must not
  * share a cache, state or tail.  n_total = 0 does nothing.
  *
+ * The prompt calls and tv_attn_norm_rope always launch with programmatic
+ * dependent launch.  Their kernels read nothing before they wait, but for second
+ * kernels of a call, whose predecessor is always the first: the delta rule's
+ * reads the states, the attention's the offsets and lengths.  tv_gdn_prompt
+ * writes the states, so with TV_TREE_OVERLAP a tv_gdn_tree_verify must not come
+ * directly behind it (a tv_tree_prepare between them is enough).
+ *
  * An infinity or NaN in a row reaches what the formulas let it reach: rows
  * before it, other sequences and (where they are apart) other heads and
  * columns are as if it were finite. */
