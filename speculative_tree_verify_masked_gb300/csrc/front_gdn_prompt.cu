@@ -31,7 +31,7 @@ struct GdnPromptFrontParams {
   float* beta;
   const float* wconv;
   void* tail[TV_MAX_SEQ];
-  int Hk, Hv, C, W, rows, strips, head_warps;
+  int Hk, Hv, C, rows, strips, head_warps;
 };
 
 // Eight channels of a row, as packed fp32 pairs.
@@ -70,11 +70,20 @@ __device__ __forceinline__ f2_t silu2(f2_t x) {
   return f2_mul(x, f2_mul(f2_dup(r), f2_pack(v, u)));
 }
 
-// WT: the width, or 0 for any width up to kMaxConvWidth.
-template <typename T, int DH, int WT>
-__global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_front_kernel(const __grid_constant__ GdnPromptFrontParams p) {
+// What a width needs in registers: the window as a ring of RING rows (even for
+// widths over 2, so that rows go two at a time), groups of GROUP rows loaded one
+// ahead, and the CTAs of four warps that an SM then holds.
+template <typename T, int W>
+struct Width {
+  static constexpr int RING = W <= 2 ? W : (W + 1) / 2 * 2;
+  static constexpr int GROUP = RING < 4 ? 4 : RING;
+  static constexpr int CTAS = sizeof(T) == 4 ? (W <= 4 ? 2 : 1) : W <= 4 ? 4 : W <= 6 ? 3 : 2;
+};
+
+template <typename T, int DH, int W>
+__global__ void __launch_bounds__(128, Width<T, W>::CTAS) gdn_prompt_front_kernel(const __grid_constant__ GdnPromptFrontParams p) {
   constexpr int LPH = DH / 8, HPW = 32 / LPH;  // lanes a head, heads a warp
-  constexpr int WM = WT ? WT : kMaxConvWidth;
+  constexpr int RING = Width<T, W>::RING, GROUP = Width<T, W>::GROUP;
   const int lane = threadIdx.x & 31;
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   pdl_wait();
@@ -91,7 +100,6 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
     if (i < static_cast<int64_t>(n_live) * p.Hv) front_gates(p.a_raw[i], p.b_raw[i], p.alpha[i], p.beta[i]);
     return;
   }
-  const int W = WT ? WT : p.W;
   const int units = 2 * p.Hk + p.Hv;
   int strips;
   const int base = strip_base(w, p.pr, lane, p.rows, strips);
@@ -103,20 +111,21 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
   const int u = static_cast<int>(warp % p.head_warps) * HPW + lane / LPH;
   const bool act = u < units;
   const int c0 = (act ? u : 0) * DH + (lane % LPH) * 8;  // dk = dv = DH: head u's channels start at u * DH
-  f2_t tap[WM][4];  // tap[j] of channels c0 + 2e, c0 + 2e + 1: wconv[c][j]
+  f2_t tap[W][4];  // tap[j] of channels c0 + 2e, c0 + 2e + 1: wconv[c][j]
+  {
+    float f[8 * W];  // the lane's eight channels' taps lie side by side
 #pragma unroll
-  for (int e = 0; e < 4; e++) {
-    if constexpr (WT == 4) {
-      const float4 a = reinterpret_cast<const float4*>(p.wconv)[c0 + 2 * e], b = reinterpret_cast<const float4*>(p.wconv)[c0 + 2 * e + 1];
-      tap[0][e] = f2_pack(a.x, b.x);
-      tap[1][e] = f2_pack(a.y, b.y);
-      tap[2][e] = f2_pack(a.z, b.z);
-      tap[3][e] = f2_pack(a.w, b.w);
-    } else {
-#pragma unroll
-      for (int j = 0; j < WM; j++)
-        tap[j][e] = j < W ? f2_pack(p.wconv[static_cast<size_t>(c0 + 2 * e) * W + j], p.wconv[static_cast<size_t>(c0 + 2 * e + 1) * W + j]) : 0ull;
+    for (int i = 0; i < 2 * W; i++) {
+      const float4 a = reinterpret_cast<const float4*>(p.wconv + static_cast<size_t>(c0) * W)[i];
+      f[4 * i] = a.x;
+      f[4 * i + 1] = a.y;
+      f[4 * i + 2] = a.z;
+      f[4 * i + 3] = a.w;
     }
+#pragma unroll
+    for (int j = 0; j < W; j++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) tap[j][e] = f2_pack(f[2 * e * W + j], f[(2 * e + 1) * W + j]);
   }
   const T* x = static_cast<const T*>(p.x) + c0;
   const bool norm = u < 2 * p.Hk;
@@ -133,26 +142,25 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
     dst = static_cast<T*>(p.v) + (c0 - 2 * p.Hk * DH);
     dstride = static_cast<size_t>(p.Hv) * DH;
   }
-  // win[(r + j) % WM]: the input j - (W-1) rows from row r of the strip, so that
+  // win[(r + j) % RING]: the input j - (W-1) rows from row r of the strip, so that
   // a step overwrites the oldest and nothing moves
-  f2_t win[WM][4];
-  Row8<T> cur[WM], next[WT ? WM : 1];  // rows of this group of WM and (fixed widths) of the one after, in flight
+  f2_t win[RING][4];
+  Row8<T> cur[GROUP], next[GROUP];  // rows of this group and of the one after, in flight
   auto fetch = [&](int rg, Row8<T>* to) {
 #pragma unroll
-    for (int u = 0; u < WM; u++) to[u].load(x + static_cast<size_t>(min(rg + u, r1 - 1)) * p.C);
+    for (int u = 0; u < GROUP; u++) to[u].load(x + static_cast<size_t>(min(rg + u, r1 - 1)) * p.C);
   };
-  if (WT) fetch(r0, next);
+  fetch(r0, next);
   // The rows before the strip: the tail's for a sequence's first strip, which
   // has the W-1 rows that read it, so that it alone then moves the tail on.
   T* tail = static_cast<T*>(p.tail[s]) + c0;
 #pragma unroll
-  for (int j = 0; j < WM - 1; j++)
-    if (j < W - 1) {
-      Row8<T> old;
-      old.load(r0 > off ? x + static_cast<size_t>(r0 + j - (W - 1)) * p.C : tail + static_cast<size_t>(j) * p.C);
+  for (int j = 0; j < W - 1; j++) {
+    Row8<T> old;
+    old.load(r0 > off ? x + static_cast<size_t>(r0 + j - (W - 1)) * p.C : tail + static_cast<size_t>(j) * p.C);
 #pragma unroll
-      for (int e = 0; e < 4; e++) win[j][e] = old.pair(e);
-    }
+    for (int e = 0; e < 4; e++) win[j][e] = old.pair(e);
+  }
   if (r0 == off && act) {
     for (int j = 0; j < W - 1; j++) {  // ascending: row j comes from the prompt or from a later row of the old tail
       const int m = end - off + j - (W - 1);
@@ -161,29 +169,21 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
       to.store(tail + static_cast<size_t>(j) * p.C);
     }
   }
-  for (int rg = r0; rg < r1; rg += WM) {
-    if (WT) {
+  for (int rg = r0; rg < r1; rg += GROUP) {
 #pragma unroll
-      for (int u = 0; u < WM; u++) cur[u] = next[u % (WT ? WM : 1)];
-      if (rg + WM < r1) fetch(rg + WM, next);
-    } else {
-      fetch(rg, cur);
-    }
+    for (int u = 0; u < GROUP; u++) cur[u] = next[u];
+    if (rg + GROUP < r1) fetch(rg + GROUP, next);
     // row u of the group: the window takes it in, then convolution and SiLU
     auto conv = [&](int u, f2_t (&acc)[4]) {
 #pragma unroll
-      for (int e = 0; e < 4; e++) acc[e] = 0ull;
-#pragma unroll
-      for (int j = 0; j < WM; j++) {
-        if (j == W - 1) {
-#pragma unroll
-          for (int e = 0; e < 4; e++) win[(u + j) % WM][e] = cur[u].pair(e);
-        }
-        if (j < W) {
-#pragma unroll
-          for (int e = 0; e < 4; e++) acc[e] = f2_fma(tap[j][e], win[(u + j) % WM][e], acc[e]);
-        }
+      for (int e = 0; e < 4; e++) {
+        win[(u + W - 1) % RING][e] = cur[u].pair(e);
+        acc[e] = 0ull;
       }
+#pragma unroll
+      for (int j = 0; j < W; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[e] = f2_fma(tap[j][e], win[(u + j) % RING][e], acc[e]);
 #pragma unroll
       for (int e = 0; e < 4; e++) acc[e] = silu2(acc[e]);
     };
@@ -204,9 +204,9 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
       for (int e = 0; e < 4; e++) f2_unpack(acc[e], y[2 * e], y[2 * e + 1]);
       if (act) store8(dst + static_cast<size_t>(r) * dstride, y);
     };
-    if (WT && rg + WM <= r1) {  // a whole group: two rows side by side
+    if (rg + GROUP <= r1) {  // a whole group: two rows side by side
 #pragma unroll
-      for (int u = 0; u < WM; u += 2) {
+      for (int u = 0; u < GROUP; u += 2) {
         f2_t acc[2][4];
         float ss[2];
         conv(u, acc[0]);
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
       continue;
     }
 #pragma unroll
-    for (int u = 0; u < WM; u++) {
+    for (int u = 0; u < GROUP; u++) {
       const int r = rg + u;
       if (r >= r1) break;
       f2_t acc[4];
@@ -241,13 +241,39 @@ __global__ void __launch_bounds__(128, WT && sizeof(T) == 2 ? 4 : 1) gdn_prompt_
   }
 }
 
-// Width 4 keeps its taps and window in registers at fixed places and loads a
-// group of rows ahead; any width's form has room for 8 and does neither: 66.9 and
-// 184.7 us at 8,192 rows of 16 + 48 heads of 128, 11.4 and 26.9 at 731.
+// Rows a warp walks: at most 64, in as even a number of waves as whole groups
+// allow, since a strip loads the taps and reads W-1 rows twice; never fewer than
+// read a tail.  At W = 4 and 16 + 48 heads of 128, 731 rows take 13.5 us in strips
+// of 12, 15.2 of 8, 16.9 of 32; 8,192 rows 68.8 us in strips of 48 (three even
+// waves), 70.8 of 32, 74.9 of 64.
+template <typename T, int DH, int W>
+static tv_status launch_width(GdnPromptFrontParams& p, cudaStream_t st) {
+  using C = Width<T, W>;
+  const int64_t n = p.pr.n_total, work = n * p.head_warps, slots = static_cast<int64_t>(4) * C::CTAS * num_sms();
+  const int64_t waves = (work + slots * 64 - 1) / (slots * 64), even = (work + slots * waves - 1) / (slots * waves);
+  p.rows = static_cast<int>(((even > W - 1 ? even : W - 1) + C::GROUP - 1) / C::GROUP * C::GROUP);
+  p.strips = static_cast<int>(n / p.rows) + p.pr.n_seq;
+  const int64_t warps = static_cast<int64_t>(p.strips) * p.head_warps + (n * p.Hv + 31) / 32, grid = (warps + 3) / 4;
+  if (grid > 0x7fffffff) return TV_ERR_SHAPE;
+  launch_k(true, gdn_prompt_front_kernel<T, DH, W>, dim3(static_cast<unsigned>(grid)), dim3(128), 0, st, p);
+  return launch_status();
+}
+// A kernel of its own for every width: taps, window and rows ahead stay in
+// registers at fixed places (one for any width, without that, took 184.7 us
+// against 66.9 at W = 4 and 8,192 rows).
 template <typename T, int DH>
-static void launch_prompt_front(const GdnPromptFrontParams& p, unsigned grid, cudaStream_t st) {
-  if (p.W == 4) launch_k(true, gdn_prompt_front_kernel<T, DH, 4>, dim3(grid), dim3(128), 0, st, p);
-  else launch_k(true, gdn_prompt_front_kernel<T, DH, 0>, dim3(grid), dim3(128), 0, st, p);
+static tv_status launch_prompt_front(GdnPromptFrontParams& p, int W, cudaStream_t st) {
+  static_assert(kMaxConvWidth == 8, "widths");
+  switch (W) {
+    case 1: return launch_width<T, DH, 1>(p, st);
+    case 2: return launch_width<T, DH, 2>(p, st);
+    case 3: return launch_width<T, DH, 3>(p, st);
+    case 4: return launch_width<T, DH, 4>(p, st);
+    case 5: return launch_width<T, DH, 5>(p, st);
+    case 6: return launch_width<T, DH, 6>(p, st);
+    case 7: return launch_width<T, DH, 7>(p, st);
+    default: return launch_width<T, DH, 8>(p, st);
+  }
 }
 
 }  // namespace tv
@@ -278,31 +304,12 @@ extern "C" tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* f, const tv_p
   p.pr = prompt_rows(pr, nullptr, 0, 0);
   p.x = x; p.a_raw = a_raw; p.b_raw = b_raw; p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.beta = beta;
   p.wconv = f->wconv;
-  p.Hk = f->Hk; p.Hv = f->Hv; p.W = f->width;
+  p.Hk = f->Hk; p.Hv = f->Hv;
   p.C = 2 * f->Hk * f->dk + f->Hv * f->dv;
   const int hpw = 256 / f->dk;
   p.head_warps = (2 * f->Hk + f->Hv + hpw - 1) / hpw;
-  // Rows a warp walks: at most 64 and as even a number of waves (16 warps an SM)
-  // as groups of four rows allow, since a strip loads the taps and reads W-1 rows
-  // twice; never fewer than read a tail.  At 16 + 48 heads of 128, 731 rows take
-  // 13.5 us in strips of 12, 15.2 of 8, 16.9 of 32; 8,192 rows 68.8 us in strips
-  // of 48 (three even waves), 70.8 of 32, 74.9 of 64.
-  const int64_t work = static_cast<int64_t>(pr->n_total) * p.head_warps, slots = 16 * num_sms();
-  const int64_t waves = (work + slots * 64 - 1) / (slots * 64);
-  const int64_t even = (work + slots * waves - 1) / (slots * waves);
-  const int64_t rows = even > f->width - 1 ? even : f->width - 1;
-  p.rows = static_cast<int>((rows + 3) / 4 * 4);
-  p.strips = pr->n_total / p.rows + pr->n_seq;
-  const int64_t warps = static_cast<int64_t>(p.strips) * p.head_warps + (static_cast<int64_t>(pr->n_total) * f->Hv + 31) / 32;
-  const int64_t grid = (warps + 3) / 4;
-  if (grid > 0x7fffffff) return TV_ERR_SHAPE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = f->dtype == TV_BF16;
-  const unsigned g = static_cast<unsigned>(grid);
-  if (f->dk == 128) {
-    if (bf) launch_prompt_front<__nv_bfloat16, 128>(p, g, st); else launch_prompt_front<float, 128>(p, g, st);
-  } else {
-    if (bf) launch_prompt_front<__nv_bfloat16, 64>(p, g, st); else launch_prompt_front<float, 64>(p, g, st);
-  }
-  return launch_status();
+  if (f->dk == 128) return bf ? launch_prompt_front<__nv_bfloat16, 128>(p, f->width, st) : launch_prompt_front<float, 128>(p, f->width, st);
+  return bf ? launch_prompt_front<__nv_bfloat16, 64>(p, f->width, st) : launch_prompt_front<float, 64>(p, f->width, st);
 }
