@@ -519,8 +519,10 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
             v[4 * i + 2] = x.z;
             v[4 * i + 3] = x.w;
           }
-          arrive(QEMPTY0 + 8u * hf);
           tmem_st32(tl + C::T_Q + (hf * C::QR + r) * 32, v);
+          // Only now: the store has waited for the loads.  An arrival does not, and
+          // products keep shared memory busy enough for the next box to overtake them.
+          arrive(QEMPTY0 + 8u * hf);
         }
         tmem_st_wait();
       }

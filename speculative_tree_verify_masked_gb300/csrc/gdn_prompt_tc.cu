@@ -716,7 +716,8 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
       f2_t x[16], z[16];
       ok = wait_warp(FULL0 + 8u * (c & 1), (c >> 1) & 1, abort_flag, kWaitCycles);
       if (!ok) break;
-      const float gr = gd[ri], gc = gd[kBlk - 1];
+      // (through a shuffle, which waits for the loads: the arrivals that free the stage do not)
+      const float gr = __shfl_sync(0xffffffffu, gd[ri], lane), gc = __shfl_sync(0xffffffffu, gd[kBlk - 1], lane);
       if (krow) {
 #pragma unroll
         for (int q = 0; q < 4; q++) {
