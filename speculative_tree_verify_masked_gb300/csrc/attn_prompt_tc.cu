@@ -7,23 +7,28 @@
 // key and value tile serves all of them.  An item is one row tile of one KV
 // head against its keys; it runs flash style over key tiles of 128 positions:
 //   S = Q K^T (tensor core, fp32), m = running maximum of scaled scores,
-//   p = 2^(s c - m) rounded to bf16, l += sum of the rounded p,
+//   p = 2^(s c - m), l += sum of p (fp32), p rounded to bf16,
 //   O = O 2^(m_old - m) + P V (tensor core, fp32), out = O / l (times the gate).
 // The maximum moves only when a tile exceeds it by more than 8 in log2 units
 // (p then stays below 2^8), so O is rescaled rarely.  p is rounded to bf16
-// because the tensor cores take P and V in one type; l adds the same rounded
-// values, so the weights still sum to one.
+// because the tensor cores take P and V in one type; each weight is off by 2^-9
+// at most, independently, and l adds them as they were (adding the rounded ones
+// takes a quarter of the softmax's instructions more and is no nearer: 2.3e-3
+// from the result in 64 bits either way, of which 1.7e-3 is the output's rounding).
 //
 // Roles (384 threads, one CTA per SM, persistent).  Warp 0 streams key and
 // value units by TMA through one ring in the order the tensor core takes
 // them: K0, K1 V0, K2 V1, ...  Warp 11 brings each item's queries, warp 1
-// issues Q K^T, warp 10 P V, each from one thread.  Warps 2-9 do the softmax,
-// two threads to a row (64 columns each).
-// Tensor memory holds O [D columns], one S [128] and Q [D/2, the A operand of
-// Q K^T], 512 columns at D = 256; P goes through shared memory.  Because PV of
-// tile t-1 sits between Q K^T of t and of t+1 on the tensor pipe, S(t) is read
-// out during that PV and one S buffer is enough, and the softmax has two
-// products' time before PV(t) wants P(t).
+// issues Q K^T, warp 10 P V, each from one thread.  Warps 2-9 do the softmax.
+// D = 256: two threads to a row (64 columns each).  Tensor memory holds O [D
+// columns], one S [128] and Q [D/2, the A operand of Q K^T], 512 columns; P goes
+// through shared memory.  Because PV of tile t-1 sits between Q K^T of t and of
+// t+1 on the tensor pipe, S(t) is read out during that PV and one S buffer is
+// enough, and the softmax has two products' time before PV(t) wants P(t).
+// D <= 128: two groups of four warps take turns at the tiles, a thread to a row.
+// A group hands the row's maximum on before it forms its weights, so that the
+// other's tile can follow; each keeps its own part of l, and whichever moves the
+// maximum rescales O.
 //
 // Masked places.  Scores of positions a row does not see are replaced, not
 // added to, so a key that is not finite there cannot pass.  In PV a zero weight
@@ -70,7 +75,14 @@ template <int D>
 struct Pa {
   static constexpr int UPT = D == 256 ? 2 : 1;              // ring units per key (or value) tile
   static constexpr int UNIT = kKeyTile * D * 2 / UPT;       // bytes of a unit
-  static constexpr int NU = D == 64 ? 10 : 5;
+  // Two groups of softmax warps that take turns at the tiles, a thread a row, each
+  // with an S, a P and barriers of its own, where tensor memory has room: the
+  // softmax of a tile takes longer than its products there (D = 256: not so, and
+  // no room).  8,192 rows of 16 + 2 heads of 128 take 229 us, 270 with one group
+  // (144 of operations), 8 + 8 heads of 64 112 and 135 (36).
+  static constexpr bool TURNS = D <= 128;
+  static constexpr int SB = TURNS ? 2 : 1;                  // S and P buffers
+  static constexpr int NU = D == 64 ? 8 : D == 128 ? 4 : 5;
   static constexpr int KBOX = kKeyTile * 128;               // bytes of a K box (128 rows, 64 columns)
   static constexpr int KBU = D / 64 / UPT;                  // K boxes per unit
   static constexpr int VROWS = kKeyTile / UPT;              // positions of a V box
@@ -80,14 +92,15 @@ struct Pa {
   static constexpr int QR = D == 256 ? 2 : 1;               // 64-column boxes of Q per half of the softmax, one at a time
   static constexpr int QH = D == 64 ? 1 : 2;                // halves that move Q
   static constexpr int QBOX = 128 * 128;
-  static constexpr int T_O = 0, T_S = D, T_Q = D + 128;
-  static constexpr int COLS = D + 128 + D / 2 <= 256 ? 256 : 512;
+  static constexpr int T_O = 0, T_S = D, T_Q = D + SB * 128;
+  static constexpr int COLS = 512;
+  static_assert(T_Q + D / 2 <= COLS, "tensor memory");
   static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, kKeyTile, false, false);
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, false, true);
-  static constexpr int QOFF = NU * UNIT + PT;               // Q on its way into tensor memory
-  static constexpr int XOFF = QOFF + QH * QBOX;             // half-row maxima [2][2][128] fp32
+  static constexpr int QOFF = NU * UNIT + SB * PT;               // Q on its way into tensor memory
+  static constexpr int XOFF = QOFF + QH * QBOX;             // exchanged values [2][2][128] fp32 (turns: [2][128], then maxima [2][128])
   static constexpr int BOFF = XOFF + 2 * 2 * 128 * 4;
-  static constexpr int NBAR = 2 * NU + 5 + 4 + 2 + 4;
+  static constexpr int NBAR = 2 * NU + 4 * SB + 2 + 4 + 2 + 4 + 8;
   static constexpr int LOFF = (BOFF + NBAR * 8 + 15) / 16 * 16;  // TMEM base, give-up flag, skip flag, plan
   static constexpr int SMEM = LOFF + 16 + static_cast<int>(sizeof(PromptPlan));
   static_assert(KBU * KBOX == UNIT && VB * VBOX == UNIT, "unit shape");
@@ -118,13 +131,12 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
-// x * sigmoid(g) with the fast exponential and divide (a few fp32 steps, far
-// below the bf16 rounding that follows).
-__device__ __forceinline__ float fast_gate(float x, float g) { return x * __fdividef(1.f, 1.f + __expf(-g)); }
-// Two at a time with one reciprocal, 1/a = b (1/ab): the special-function unit
-// bounds the epilogue.  e^-g is held below 2^63 so that the product stays
-// finite (a gate under -43.6 then leaves 1e-19 of x, not less).
-__device__ __forceinline__ void fast_gate2(float& x, float& y, float gx, float gy) {
+// Two values times the sigmoids of their gates, by the fast exponential and
+// divide (a few fp32 steps, far below the bf16 rounding that follows) with one
+// reciprocal for both, 1/a = b (1/ab): the special-function unit bounds the
+// epilogue.  e^-g is held below 2^63 so that the product stays finite (a gate
+// under -43.6 then leaves 1e-19 of x, not less).
+__device__ __forceinline__ void gate2(float& x, float& y, float gx, float gy) {
   constexpr float kLog2e = 1.4426950408889634f;
   const float a = 1.f + ex2_approx(fminf(-kLog2e * gx, 63.f)), b = 1.f + ex2_approx(fminf(-kLog2e * gy, 63.f));
   const float r = __fdividef(1.f, a * b);
@@ -132,6 +144,15 @@ __device__ __forceinline__ void fast_gate2(float& x, float& y, float gx, float g
   y *= a * r;
 }
 
+// 2^(s c + neg) of two scores, added to a sum, and as a bf16 pair.
+__device__ __forceinline__ uint32_t weights(float s0, float s1, f2_t c, f2_t neg, f2_t& sum) {
+  float a, b;
+  f2_unpack(f2_fma(f2_pack(s0, s1), c, neg), a, b);
+  a = ex2_approx(a);
+  b = ex2_approx(b);
+  sum = f2_add(sum, f2_pack(a, b));
+  return pack_bf16x2(a, b);
+}
 __device__ __forceinline__ uint32_t times_zero_plus(uint32_t x, uint32_t acc) {  // bf16 pairs
   uint32_t r;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
@@ -286,9 +307,12 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
   float* xmax = reinterpret_cast<float*>(gb + C::XOFF);
   const uint32_t bars = sb + C::BOFF;
   const uint32_t UFULL0 = bars, UEMPTY0 = bars + 8u * C::NU;
-  const uint32_t SFULL = bars + 16u * C::NU, SFREE = SFULL + 8u, PFULL = SFULL + 16u, ODONE = SFULL + 24u,
-                 QREADY = SFULL + 32u, XBAR0 = SFULL + 40u, DRAIN = XBAR0 + 32u,
-                 QFULL0 = DRAIN + 16u, QEMPTY0 = QFULL0 + 16u;
+  const uint32_t SFULL0 = bars + 16u * C::NU, SFREE0 = SFULL0 + 8u * C::SB, PFULL0 = SFREE0 + 8u * C::SB,
+                 ODONE0 = PFULL0 + 8u * C::SB, QREADY = ODONE0 + 8u * C::SB, OFREE = QREADY + 8u, XBAR0 = QREADY + 16u,
+                 DRAIN = XBAR0 + 32u, QFULL0 = DRAIN + 16u, QEMPTY0 = QFULL0 + 16u, MBAR0 = QEMPTY0 + 16u;
+  // tile t's barrier of a kind, and the parity of its phase there
+  auto bar = [](uint32_t first, uint32_t t) { return first + (C::TURNS ? 8u * (t & 1) : 0u); };
+  auto par = [](uint32_t t) { return C::TURNS ? (t >> 1) & 1 : t & 1; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + C::LOFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int& skip = *reinterpret_cast<int*>(tmem_slot + 2);
@@ -302,11 +326,15 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
       mbar_init(UFULL0 + 8u * i, 1);
       mbar_init(UEMPTY0 + 8u * i, 1);
     }
-    mbar_init(SFULL, 1);
-    mbar_init(SFREE, 8);
-    mbar_init(PFULL, 8);
-    mbar_init(ODONE, 1);
+    for (int i = 0; i < C::SB; i++) {
+      mbar_init(SFULL0 + 8u * i, 1);
+      mbar_init(SFREE0 + 8u * i, C::TURNS ? 4 : 8);
+      mbar_init(PFULL0 + 8u * i, C::TURNS ? 4 : 8);
+      mbar_init(ODONE0 + 8u * i, 1);
+    }
     mbar_init(QREADY, 8);
+    mbar_init(OFREE, 8);
+    for (int i = 0; i < 8; i++) mbar_init(MBAR0 + 8u * i, 1);
     for (int i = 0; i < 4; i++) mbar_init(XBAR0 + 8u * i, 2);
     mbar_init(DRAIN, 1);
     mbar_init(DRAIN + 8u, 1);
@@ -425,7 +453,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
       items++;
       for (int k = 0; k < n && ok; k++, t++) {
         if (is_qk) {
-          if (t > 0) ok = wait_warp(SFREE, (t - 1) & 1, abort_flag, kWaitCycles);
+          if (t >= C::SB) ok = wait_warp(bar(SFREE0, t), par(t - C::SB), abort_flag, kWaitCycles);
           const uint32_t u0 = base + (k == 0 ? 0 : 2 * k - 1) * C::UPT;
 #pragma unroll
           for (int u = 0; u < C::UPT; u++) {
@@ -437,16 +465,18 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
               const uint64_t k0 = sdesc_sw128(ring + slot * C::UNIT, 16, 1024);
 #pragma unroll
               for (int kk = 0; kk < C::KBU * 4; kk++)
-                tc_mma_ts(tbase + C::T_S, tbase + C::T_Q + (u * C::KBU * 4 + kk) * 8,
+                tc_mma_ts(tbase + C::T_S + (t % C::SB) * 128, tbase + C::T_Q + (u * C::KBU * 4 + kk) * 8,
                           k0 + static_cast<uint64_t>(((kk >> 2) * C::KBOX + (kk & 3) * 32) >> 4), C::IDESC_QK,
                           (u > 0 || kk > 0) ? 1u : 0u);
               tc_commit(UEMPTY0 + 8u * slot);
-              if (u == C::UPT - 1) tc_commit(SFULL);
+              if (u == C::UPT - 1) tc_commit(bar(SFULL0, t));
             }
             __syncwarp();
           }
         } else {
-          ok = wait_warp(PFULL, t & 1, abort_flag, kWaitCycles);
+          ok = wait_warp(bar(PFULL0, t), par(t), abort_flag, kWaitCycles);
+          // (turns: O may still be on its way out of the item before)
+          if (C::TURNS && k == 0 && items > 1) ok = ok && wait_warp(OFREE, (items - 2) & 1, abort_flag, kWaitCycles);
           const uint32_t u0 = base + (k < n - 1 ? 2 * k + 2 : 2 * n - 1) * C::UPT;
 #pragma unroll
           for (int u = 0; u < C::UPT; u++) {
@@ -456,7 +486,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
             tc_fence_after();
             if (elect_one_sync()) {
               const uint64_t v0 = sdesc_sw128(ring + slot * C::UNIT, C::VBOX, 1024);
-              const uint64_t p0 = sdesc_sw128(pbuf, 16, 1024);
+              const uint64_t p0 = sdesc_sw128(pbuf + (t % C::SB) * C::PT, 16, 1024);
 #pragma unroll
               for (int kk = 0; kk < C::VROWS / 16; kk++) {
                 const int pk = u * (C::VROWS / 16) + kk;  // 16-position step of the tile
@@ -464,7 +494,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
                           v0 + static_cast<uint64_t>((kk * 2048) >> 4), C::IDESC_PV, (k > 0 || pk > 0) ? 1u : 0u);
               }
               tc_commit(UEMPTY0 + 8u * slot);
-              if (u == C::UPT - 1) tc_commit(ODONE);
+              if (u == C::UPT - 1) tc_commit(bar(ODONE0, t));
             }
             __syncwarp();
           }
@@ -479,16 +509,16 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
     __syncwarp();
     mbar_wait(drain, 0, kWaitCycles);
   } else if (warp >= 2 && warp < 10) {
-    // ---------------- softmax and output, two threads to a row ----------------
+    // ---------------- softmax and output, a row's columns of O to two threads ----------------
     const int hf = (warp - 2) >> 2, quad = warp & 3, lrow = quad * 32 + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t patch = pbuf + hf * 16384 + quad * 4096;  // where this warp writes P: 4 KB of its own between items
+    const uint32_t patch = pbuf + hf * (C::TURNS ? C::PT : 16384) + quad * 4096;  // where this warp writes P: 4 KB of its own between items
     const int tok = lrow / p.G, head = lrow % p.G;
     uint32_t t = 0, xc = 0, it = 0;  // tiles, exchanges, units before the item
     bool ok = true;
     // the two threads of a row exchange a value
     auto exchange = [&](float v, float& other) {
-      float* x = xmax + (xc & 1) * 256;
+      float* x = xmax + (C::TURNS ? 0 : xc & 1) * 256;  // (turns: once an item, with QREADY between)
       x[hf * 128 + lrow] = v;
       __syncwarp();
       if (lane == 0) mbar_arrive(XBAR0 + 8u * quad);
@@ -547,117 +577,237 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
       const bool act = orow >= 0;
       const int last = act ? L + I.i * p.T + tok : -1;  // last position this row sees
       const int seen_all = L + I.i * p.T + 1;           // positions every row here sees
-      float m = -INFINITY, l = 0.f;
-      for (int k = 0; k < n; k++, t++) {
-        if (!wait_warp(SFULL, t & 1, abort_flag, kWaitCycles)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        float sv[64];
-        {
-          uint32_t r[32];
-          tmem_ld32(tl + C::T_S + hf * 64, r);
+      float m = -INFINITY, l = 0.f, lo = 0.f;  // maximum, and the sum's two parts
+      // values of tile k that are not finite, where some row here does not see all
+      auto look = [&](int k, int pos) {
+        const int first = max(seen_all - tile_row(pos, end), 0);
+        const uint32_t u0 = it + (k < n - 1 ? 2 * k + 2 : 2 * n - 1) * C::UPT;  // the tile's value units
+        uint32_t slot[C::UPT];
 #pragma unroll
-          for (int i = 0; i < 32; i++) sv[i] = __uint_as_float(r[i]);
-          tmem_ld32(tl + C::T_S + hf * 64 + 32, r);
-#pragma unroll
-          for (int i = 0; i < 32; i++) sv[32 + i] = __uint_as_float(r[i]);
+        for (int u = 0; u < C::UPT; u++) {
+          slot[u] = (u0 + u) % C::NU;
+          ok = ok && wait_warp(UFULL0 + 8u * slot[u], ((u0 + u) / C::NU) & 1, abort_flag, kWaitCycles);
         }
-        tc_fence_before();
-        arrive(SFREE);
-        const int pos = (I.t0 + k) * kKeyTile;
-        if (pos + kKeyTile > seen_all) {  // a tile some row here does not see whole
-          const int row = tile_row(pos, end), vis = last - (row + hf * 64), from = pos - (row + hf * 64);
-#pragma unroll
-          for (int j = 0; j < 64; j++) sv[j] = j >= from && j <= vis ? sv[j] : -INFINITY;
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < 64; j++) mx[j & 3] = fmaxf(mx[j & 3], sv[j]);
-        float mo;
-        const float mh = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (!exchange(mh, mo)) {
-          ok = false;
-          break;
-        }
-        const float mt = __fmul_rn(fmaxf(mh, mo), p.c);
-        float alpha = 1.f;
-        if (mt > __fadd_rn(m, kMoveMax) || (m == -INFINITY && mt > -INFINITY)) {
-          alpha = ex2_approx(__fsub_rn(m, mt));  // 0 from m = -inf
-          m = mt;
-        }
-        const float neg = m == -INFINITY ? 0.f : -m;  // nothing seen yet: every p below is 2^-inf = 0
-        uint32_t P[32];
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 64; j += 2) {
-          const uint32_t w = pack_bf16x2(ex2_approx(__fmaf_rn(sv[j], p.c, neg)), ex2_approx(__fmaf_rn(sv[j + 1], p.c, neg)));
-          P[j / 2] = w;
-          acc[(j / 2) & 3] = __fadd_rn(acc[(j / 2) & 3], __fadd_rn(bf16_lo(w), bf16_hi(w)));
-        }
-        l = __fmaf_rn(l, alpha, __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3])));
-        // PV of the previous tile is complete: P is free and O rests
-        if (t > 0 && !wait_warp(ODONE, (t - 1) & 1, abort_flag, kWaitCycles)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        {
-          const uint32_t line = pbuf + hf * 16384 + (lrow >> 3) * 1024 + (lrow & 7) * 128;
-#pragma unroll
-          for (int q = 0; q < 8; q++)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + (((q ^ lrow) & 7) << 4)), "r"(P[4 * q]),
-                         "r"(P[4 * q + 1]), "r"(P[4 * q + 2]), "r"(P[4 * q + 3])
-                         : "memory");
-        }
-        if (k > 0 && __any_sync(0xffffffffu, act && alpha != 1.f)) {
-#pragma unroll 1
-          for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
-            uint32_t r[32];
-            tmem_ld32(tl + C::T_O + c, r);
-#pragma unroll
-            for (int i = 0; i < 32; i++) r[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[i]), alpha));
-            tmem_st32(tl + C::T_O + c, r);
-          }
-          tmem_st_wait();
-        }
-        if (pos + kKeyTile > seen_all) {
-          const int first = max(seen_all - tile_row(pos, end), 0);
-          const uint32_t u0 = it + (k < n - 1 ? 2 * k + 2 : 2 * n - 1) * C::UPT;  // the tile's value units
-          uint32_t slot[C::UPT];
-#pragma unroll
-          for (int u = 0; u < C::UPT; u++) {
-            slot[u] = (u0 + u) % C::NU;
-            ok = ok && wait_warp(UFULL0 + 8u * slot[u], ((u0 + u) / C::NU) & 1, abort_flag, kWaitCycles);
-          }
-          if (!ok) break;
-          constexpr int PPR = C::VB * 8, RPW = 32 / PPR;  // 16-byte pieces of a row, rows a warp looks at
-          const uint32_t piece = (lane % PPR >> 3) * C::VBOX + (lane & 7) * 16;
-          auto at = [&](int row) {
-            return ring + (C::UPT > 1 && row >= C::VROWS ? slot[C::UPT - 1] : slot[0]) * C::UNIT + (row % C::VROWS) * 128 + piece;
-          };
-          const int row0 = first + (warp - 2) * RPW + lane / PPR;
-          uint32_t sum[4] = {0u, 0u, 0u, 0u};  // of value x 0: zero, or NaN
+        if (!ok) return false;
+        constexpr int PPR = C::VB * 8, RPW = 32 / PPR;  // 16-byte pieces of a row, rows a warp looks at
+        const uint32_t piece = (lane % PPR >> 3) * C::VBOX + (lane & 7) * 16;
+        auto at = [&](int row) {
+          return ring + (C::UPT > 1 && row >= C::VROWS ? slot[C::UPT - 1] : slot[0]) * C::UNIT + (row % C::VROWS) * 128 + piece;
+        };
+        const int row0 = first + (C::TURNS ? quad : warp - 2) * RPW + lane / PPR;
+        uint32_t sum[4] = {0u, 0u, 0u, 0u};  // of value x 0: zero, or NaN
 #pragma unroll 4
-          for (int row = row0; row < kKeyTile; row += 8 * RPW) {
-            const uint4 v = ld_shared16(at(row));
-            sum[0] = times_zero_plus(v.x, sum[0]);
-            sum[1] = times_zero_plus(v.y, sum[1]);
-            sum[2] = times_zero_plus(v.z, sum[2]);
-            sum[3] = times_zero_plus(v.w, sum[3]);
-          }
-          if ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) {
-            for (int row = row0; row < kKeyTile; row += 8 * RPW) {
-              const uint4 v = ld_shared16(at(row));
-              st_shared16(at(row), make_uint4(v.x & finite2(v.x), v.y & finite2(v.y), v.z & finite2(v.z), v.w & finite2(v.w)));
-            }
-            met[id & 1] = id;
-          }
+        for (int row = row0; row < kKeyTile; row += (C::TURNS ? 4 : 8) * RPW) {
+          const uint4 v = ld_shared16(at(row));
+          sum[0] = times_zero_plus(v.x, sum[0]);
+          sum[1] = times_zero_plus(v.y, sum[1]);
+          sum[2] = times_zero_plus(v.z, sum[2]);
+          sum[3] = times_zero_plus(v.w, sum[3]);
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        arrive(PFULL);
+        if ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) {
+          for (int row = row0; row < kKeyTile; row += (C::TURNS ? 4 : 8) * RPW) {
+            const uint4 v = ld_shared16(at(row));
+            st_shared16(at(row), make_uint4(v.x & finite2(v.x), v.y & finite2(v.y), v.z & finite2(v.z), v.w & finite2(v.w)));
+          }
+          met[id & 1] = id;
+        }
+        return true;
+      };
+      if constexpr (C::TURNS) {
+        float mine_m = -INFINITY;  // the maximum that l counts from
+        float* const mrow = xmax + 256;
+        for (int k = 0; k < n; k++, t++) {
+          if ((t & 1) != static_cast<uint32_t>(hf)) continue;  // the other group's
+          if (!wait_warp(bar(SFULL0, t), par(t), abort_flag, kWaitCycles)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ts = tl + C::T_S + hf * 128;
+          const int pos = (I.t0 + k) * kKeyTile, first_row = tile_row(pos, end);
+          const bool whole = pos + kKeyTile <= seen_all;
+          const int vis = last - first_row, from = pos - first_row;
+          // 64 scores at a time: loops, not 128 scores in a row, since the code of two
+          // groups and the issuers has to stay in the instruction cache
+          uint32_t a[32], b[32];
+          auto load = [&](int c) {
+            tmem_ld32_nowait(ts + c, a);
+            tmem_ld32_nowait(ts + c + 32, b);
+            tmem_ld_wait(a, b);
+            if (!whole) {
+#pragma unroll
+              for (int j = 0; j < 32; j++) {
+                if (c + j < from || c + j > vis) a[j] = __float_as_uint(-INFINITY);
+                if (c + 32 + j < from || c + 32 + j > vis) b[j] = __float_as_uint(-INFINITY);
+              }
+            }
+          };
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 64) {
+            load(c);
+#pragma unroll
+            for (int j = 0; j < 32; j++) mx[j & 3] = fmaxf(mx[j & 3], fmaxf(__uint_as_float(a[j]), __uint_as_float(b[j])));
+          }
+          const float mt = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), p.c);
+          float before = -INFINITY;  // the maximum after the tile before, from the other group
+          if (k > 0) {
+            if (!wait_warp(MBAR0 + 8u * (quad * 2 + (hf ^ 1)), par(t - 1), abort_flag, kWaitCycles)) {
+              ok = false;
+              break;
+            }
+            before = mrow[(hf ^ 1) * 128 + lrow];
+          }
+          m = before;
+          if (mt > __fadd_rn(m, kMoveMax) || (m == -INFINITY && mt > -INFINITY)) m = mt;
+          mrow[hf * 128 + lrow] = m;
+          arrive(MBAR0 + 8u * (quad * 2 + hf));
+          const float neg = m == -INFINITY ? 0.f : -m;  // nothing seen yet: every p below is 2^-inf = 0
+          // this group's last P has been read
+          if (t >= 2 && !wait_warp(bar(ODONE0, t), par(t - 2), abort_flag, kWaitCycles)) {
+            ok = false;
+            break;
+          }
+          f2_t acc[2] = {0ull, 0ull};
+          const f2_t c2 = f2_dup(p.c), neg2 = f2_dup(neg);
+          uint32_t line = pbuf + hf * C::PT + (lrow >> 3) * 1024 + (lrow & 7) * 128;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 64, line += 16384) {
+            load(c);
+            if (c > 0) {  // S is free for the tile after next, half the weights ahead of P
+              tc_fence_before();
+              arrive(bar(SFREE0, t));
+            }
+            auto put = [&](const uint32_t (&x)[32], int q0) {
+#pragma unroll
+              for (int q = 0; q < 4; q++) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                  w[e] = weights(__uint_as_float(x[8 * q + 2 * e]), __uint_as_float(x[8 * q + 2 * e + 1]), c2, neg2, acc[e & 1]);
+                st_shared16(line + ((((q0 + q) ^ lrow) & 7) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+              }
+            };
+            put(a, 0);
+            put(b, 4);
+          }
+          l = __fmaf_rn(l, mine_m == m ? 1.f : ex2_approx(__fsub_rn(mine_m, m)), f2_hsum(f2_add(acc[0], acc[1])));
+          mine_m = m;
+          const float alpha = before == m ? 1.f : ex2_approx(__fsub_rn(before, m));
+          if (k > 0 && __any_sync(0xffffffffu, act && alpha != 1.f)) {  // once O rests
+            if (!wait_warp(bar(ODONE0, t - 1), par(t - 1), abort_flag, kWaitCycles)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t r[32];
+              tmem_ld32(tl + C::T_O + c, r);
+#pragma unroll
+              for (int i = 0; i < 32; i++) r[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[i]), alpha));
+              tmem_st32(tl + C::T_O + c, r);
+            }
+            tmem_st_wait();
+          }
+          if (!whole && !look(k, pos)) {
+            ok = false;
+            break;
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          arrive(bar(PFULL0, t));
+        }
+        if (ok) {
+          // the item's last maximum and S, whichever group's they were
+          ok = wait_warp(MBAR0 + 8u * (quad * 2 + ((t - 1) & 1)), par(t - 1), abort_flag, kWaitCycles) &&
+               wait_warp(bar(SFULL0, t - 1), par(t - 1), abort_flag, kWaitCycles);
+          m = mrow[((t - 1) & 1) * 128 + lrow];
+          if (mine_m != m) l = __fmul_rn(l, ex2_approx(__fsub_rn(mine_m, m)));
+          tc_fence_after();
+          // (before QREADY, so that the next item's cannot overtake it)
+          ok = ok && exchange(l, lo);
+        }
+      } else {
+        for (int k = 0; k < n; k++, t++) {
+          if (!wait_warp(SFULL0, t & 1, abort_flag, kWaitCycles)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          float sv[64];
+          {
+            uint32_t r[32];
+            tmem_ld32(tl + C::T_S + hf * 64, r);
+#pragma unroll
+            for (int i = 0; i < 32; i++) sv[i] = __uint_as_float(r[i]);
+            tmem_ld32(tl + C::T_S + hf * 64 + 32, r);
+#pragma unroll
+            for (int i = 0; i < 32; i++) sv[32 + i] = __uint_as_float(r[i]);
+          }
+          tc_fence_before();
+          arrive(SFREE0);
+          const int pos = (I.t0 + k) * kKeyTile;
+          if (pos + kKeyTile > seen_all) {  // a tile some row here does not see whole
+            const int row = tile_row(pos, end), vis = last - (row + hf * 64), from = pos - (row + hf * 64);
+#pragma unroll
+            for (int j = 0; j < 64; j++) sv[j] = j >= from && j <= vis ? sv[j] : -INFINITY;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 64; j += 2) mx[(j / 2) & 3] = fmaxf(mx[(j / 2) & 3], fmaxf(sv[j], sv[j + 1]));
+          float mo;
+          const float mh = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (!exchange(mh, mo)) {
+            ok = false;
+            break;
+          }
+          const float mt = __fmul_rn(fmaxf(mh, mo), p.c);
+          float alpha = 1.f;
+          if (mt > __fadd_rn(m, kMoveMax) || (m == -INFINITY && mt > -INFINITY)) {
+            alpha = ex2_approx(__fsub_rn(m, mt));  // 0 from m = -inf
+            m = mt;
+          }
+          const float neg = m == -INFINITY ? 0.f : -m;  // nothing seen yet: every p below is 2^-inf = 0
+          uint32_t P[32];
+          f2_t acc[2] = {0ull, 0ull};
+          const f2_t c2 = f2_dup(p.c), neg2 = f2_dup(neg);
+#pragma unroll
+          for (int j = 0; j < 64; j += 2) P[j / 2] = weights(sv[j], sv[j + 1], c2, neg2, acc[(j / 2) & 1]);
+          l = __fmaf_rn(l, alpha, f2_hsum(f2_add(acc[0], acc[1])));
+          // PV of the previous tile is complete: P is free and O rests
+          if (t > 0 && !wait_warp(ODONE0, (t - 1) & 1, abort_flag, kWaitCycles)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          {
+            const uint32_t line = pbuf + hf * 16384 + (lrow >> 3) * 1024 + (lrow & 7) * 128;
+#pragma unroll
+            for (int q = 0; q < 8; q++)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + (((q ^ lrow) & 7) << 4)), "r"(P[4 * q]),
+                           "r"(P[4 * q + 1]), "r"(P[4 * q + 2]), "r"(P[4 * q + 3])
+                           : "memory");
+          }
+          if (k > 0 && __any_sync(0xffffffffu, act && alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
+              uint32_t r[32];
+              tmem_ld32(tl + C::T_O + c, r);
+#pragma unroll
+              for (int i = 0; i < 32; i++) r[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[i]), alpha));
+              tmem_st32(tl + C::T_O + c, r);
+            }
+            tmem_st_wait();
+          }
+          if (pos + kKeyTile > seen_all && !look(k, pos)) {
+            ok = false;
+            break;
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          arrive(PFULL0);
+        }
       }
       it += 2 * n * C::UPT;
       if (!ok) break;
@@ -685,8 +835,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
         }
       };
       if (p.gate && slot < 0) fetch_gate(hf * (D / 2));
-      float lo;
-      if (!exchange(l, lo) || !wait_warp(ODONE, (t - 1) & 1, abort_flag, kWaitCycles)) {
+      if ((!C::TURNS && !exchange(l, lo)) || !wait_warp(bar(ODONE0, t - 1), par(t - 1), abort_flag, kWaitCycles)) {
         ok = false;
         break;
       }
@@ -742,7 +891,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
               float gf[8];
               widen8(ld_shared16(patch + lane * 128 + (((i ^ lane) & 7) << 4)), gf);
 #pragma unroll
-              for (int e = 0; e < 8; e += 2) fast_gate2(y[8 * i + e], y[8 * i + e + 1], gf[e], gf[e + 1]);
+              for (int e = 0; e < 8; e += 2) gate2(y[8 * i + e], y[8 * i + e + 1], gf[e], gf[e + 1]);
             }
           }
           __syncwarp();
@@ -760,6 +909,10 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
             if (ro >= 0) *reinterpret_cast<uint4*>(p.out + ro + c + pq * 8) = x;
           }
         }
+      }
+      if (C::TURNS) {
+        tc_fence_before();
+        arrive(OFREE);
       }
       if (met[id & 1] == id) {
         __syncwarp();
@@ -854,10 +1007,8 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
       for (int e = 0; e < 4; e++) acc[e] = __fmul_rn(acc[e], inv);
       if (p.gate) {
         const uint2 gv = *reinterpret_cast<const uint2*>(p.gate + at_o);
-        acc[0] = fast_gate(acc[0], bf16_lo(gv.x));
-        acc[1] = fast_gate(acc[1], bf16_hi(gv.x));
-        acc[2] = fast_gate(acc[2], bf16_lo(gv.y));
-        acc[3] = fast_gate(acc[3], bf16_hi(gv.y));
+        gate2(acc[0], acc[1], bf16_lo(gv.x), bf16_hi(gv.x));
+        gate2(acc[2], acc[3], bf16_lo(gv.y), bf16_hi(gv.y));
       }
       *reinterpret_cast<uint2*>(p.out + at_o) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
     }

@@ -84,17 +84,9 @@ inline PromptRows prompt_rows(const tv_prompt* p, const int32_t* len, int max_le
 __device__ __forceinline__ uint32_t finite2(uint32_t x) { return __vcmpltu2(x & 0x7f807f80u, 0x7f807f80u); }
 
 // Eight consecutive values of a row, widened to fp32 (16-byte aligned).
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
 __device__ __forceinline__ void widen8(const uint4& v, float (&x)[8]) {
   x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
   x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  widen8(*reinterpret_cast<const uint4*>(p), x);
 }
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   uint32_t r;
