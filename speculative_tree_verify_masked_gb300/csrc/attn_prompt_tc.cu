@@ -136,12 +136,17 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
 // reciprocal for both, 1/a = b (1/ab): the special-function unit bounds the
 // epilogue.  e^-g is held below 2^63 so that the product stays finite (a gate
 // under -43.6 then leaves 1e-19 of x, not less).
-__device__ __forceinline__ void gate2(float& x, float& y, float gx, float gy) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  const float a = 1.f + ex2_approx(fminf(-kLog2e * gx, 63.f)), b = 1.f + ex2_approx(fminf(-kLog2e * gy, 63.f));
-  const float r = __fdividef(1.f, a * b);
-  x *= b * r;
-  y *= a * r;
+__device__ __forceinline__ f2_t gate2(f2_t x, uint32_t g) {
+  float u, v, r;
+  f2_unpack(f2_mul(f2_from_bf16x2(g), f2_dup(-1.4426950408889634f)), u, v);
+  f2_unpack(f2_add(f2_pack(ex2_approx(fminf(u, 63.f)), ex2_approx(fminf(v, 63.f))), f2_dup(1.f)), u, v);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fmul_rn(u, v)));
+  return f2_mul(x, f2_mul(f2_dup(r), f2_pack(v, u)));
+}
+__device__ __forceinline__ uint32_t bf16_of(f2_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return pack_bf16x2(a, b);
 }
 
 // 2^(s c + neg) of two scores, added to a sum, and as a bf16 pair.
@@ -869,13 +874,15 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
       } else {
 #pragma unroll 1
         for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += CW) {
-          float y[CW];
+          f2_t y[CW / 2];
+          const f2_t inv2 = f2_dup(inv);
 #pragma unroll
           for (int b = 0; b < CW; b += 32) {
             uint32_t r[32];
             tmem_ld32(tl + C::T_O + c + b, r);
 #pragma unroll
-            for (int i = 0; i < 32; i++) y[b + i] = __fmul_rn(__uint_as_float(r[i]), inv);
+            for (int i = 0; i < 16; i++)
+              y[b / 2 + i] = f2_mul(f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), inv2);
           }
           if (p.gate) {
             __syncwarp();
@@ -888,18 +895,18 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
             if (c + CW < (hf + 1) * (D / 2)) fetch_gate(c + CW);
 #pragma unroll
             for (int i = 0; i < Q; i++) {
-              float gf[8];
-              widen8(ld_shared16(patch + lane * 128 + (((i ^ lane) & 7) << 4)), gf);
-#pragma unroll
-              for (int e = 0; e < 8; e += 2) gate2(y[8 * i + e], y[8 * i + e + 1], gf[e], gf[e + 1]);
+              const uint4 g = ld_shared16(patch + lane * 128 + (((i ^ lane) & 7) << 4));
+              y[4 * i] = gate2(y[4 * i], g.x);
+              y[4 * i + 1] = gate2(y[4 * i + 1], g.y);
+              y[4 * i + 2] = gate2(y[4 * i + 2], g.z);
+              y[4 * i + 3] = gate2(y[4 * i + 3], g.w);
             }
           }
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < Q; i++)
             st_shared16(patch + lane * 128 + (((i ^ lane) & 7) << 4),
-                        make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
-                                   pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7])));
+                        make_uint4(bf16_of(y[4 * i]), bf16_of(y[4 * i + 1]), bf16_of(y[4 * i + 2]), bf16_of(y[4 * i + 3])));
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < Q; i++) {
@@ -1007,8 +1014,8 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
       for (int e = 0; e < 4; e++) acc[e] = __fmul_rn(acc[e], inv);
       if (p.gate) {
         const uint2 gv = *reinterpret_cast<const uint2*>(p.gate + at_o);
-        gate2(acc[0], acc[1], bf16_lo(gv.x), bf16_hi(gv.x));
-        gate2(acc[2], acc[3], bf16_lo(gv.y), bf16_hi(gv.y));
+        f2_unpack(gate2(f2_pack(acc[0], acc[1]), gv.x), acc[0], acc[1]);
+        f2_unpack(gate2(f2_pack(acc[2], acc[3]), gv.y), acc[2], acc[3]);
       }
       *reinterpret_cast<uint2*>(p.out + at_o) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
     }
