@@ -137,11 +137,10 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
 // epilogue.  e^-g is held below 2^63 so that the product stays finite (a gate
 // under -43.6 then leaves 1e-19 of x, not less).
 __device__ __forceinline__ f2_t gate2(f2_t x, uint32_t g) {
-  float u, v, r;
+  float u, v;
   f2_unpack(f2_mul(f2_from_bf16x2(g), f2_dup(-1.4426950408889634f)), u, v);
   f2_unpack(f2_add(f2_pack(ex2_approx(fminf(u, 63.f)), ex2_approx(fminf(v, 63.f))), f2_dup(1.f)), u, v);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fmul_rn(u, v)));
-  return f2_mul(x, f2_mul(f2_dup(r), f2_pack(v, u)));
+  return f2_mul(x, f2_mul(f2_dup(rcp_approx(__fmul_rn(u, v))), f2_pack(v, u)));
 }
 __device__ __forceinline__ uint32_t bf16_of(f2_t x) {
   float a, b;

@@ -66,8 +66,7 @@ __device__ __forceinline__ f2_t silu2(f2_t x) {
   float u, v;
   f2_unpack(f2_mul(x, f2_dup(-1.4426950408889634f)), u, v);
   f2_unpack(f2_add(f2_pack(ex2_approx(fminf(u, 63.f)), ex2_approx(fminf(v, 63.f))), f2_dup(1.f)), u, v);
-  const float r = __fdividef(1.f, __fmul_rn(u, v));
-  return f2_mul(x, f2_mul(f2_dup(r), f2_pack(v, u)));
+  return f2_mul(x, f2_mul(f2_dup(rcp_approx(__fmul_rn(u, v))), f2_pack(v, u)));
 }
 
 // What a width needs in registers: the window as a ring of RING rows (even for

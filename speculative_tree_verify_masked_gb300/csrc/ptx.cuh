@@ -41,6 +41,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// 1 / x to about 2^-23, results below the smallest normal value flushed to 0.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Pack two floats into one bf16x2 word, round-to-nearest-even:
 // `lo` goes to bits [0,16), `hi` to bits [16,32).
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
