@@ -47,8 +47,8 @@
 // and a tile takes about 2,300 (tensor pipe 76 % active over a whole call of
 // 8,192 rows under a power cap).  24 + 4 heads of 256, and the same operations at
 // the measured rate of a large library product: 8,192 rows 495 us (432), 1,024
-// rows behind 130,048 2,030 us (1,722), packed 2,047 + 1 + 515 + 4,096 rows with a
-// gate 261 us (159; tiles that are half masked and short items), 24 rows behind
+// rows behind 130,048 2,040 us (1,722), packed 2,047 + 1 + 515 + 4,096 rows with a
+// gate 256 us (159; tiles that are half masked and short items), 24 rows behind
 // 65,536 70 us (40 of bytes; pieces of a few tiles, then the join).
 #include <cmath>
 #include <cstring>
@@ -78,8 +78,8 @@ struct Pa {
   // Two groups of softmax warps that take turns at the tiles, a thread a row, each
   // with an S, a P and barriers of its own, where tensor memory has room: the
   // softmax of a tile takes longer than its products there (D = 256: not so, and
-  // no room).  8,192 rows of 16 + 2 heads of 128 take 229 us, 270 with one group
-  // (144 of operations), 8 + 8 heads of 64 112 and 135 (36).
+  // no room).  8,192 rows of 16 + 2 heads of 128 take 230 us, 270 with one group
+  // (144 of operations), 8 + 8 heads of 64 109 and 135 (36).
   static constexpr bool TURNS = D <= 128;
   static constexpr int SB = TURNS ? 2 : 1;                  // S and P buffers
   static constexpr int NU = D == 64 ? 8 : D == 128 ? 4 : 5;
