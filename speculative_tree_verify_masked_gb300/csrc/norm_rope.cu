@@ -7,8 +7,8 @@
 //
 // in fp32, rounded once to the row type.  The angle is carried in turns: the
 // rate theta^(-2j/rot) / 2pi of plane j is a 64-bit binary fraction F_j formed
-// on the host in fp64, and pos * F_j modulo 2^64 is the fraction of a turn to
-// 2^-47 at any 20-bit position with three integer multiplies; its top 32 bits
+// on the host in fp64, and pos * F_j modulo 2^64 is the fraction of a turn, with
+// three integer multiplies and nothing lost at any 20-bit position; its top 32 bits
 // give sincospi's argument to half an fp32 step.  (fp64 sine and cosine per
 // row, as tv_attn_rope forms them per row and head, would take longer here
 // than the memory traffic: this GPU's fp64 rate is 1/60 of its fp32 rate.)
@@ -268,10 +268,12 @@ static tv_status norm_rope_launch(const tv_attn_layer* l, NormRopeParams& p, con
   p.Hq = l->Hq;
   p.Hkv = l->Hkv;
   p.cap = l->cap;
-  for (int j = 0; j < rot / 2; j++) {
-    const double turns = std::pow(static_cast<double>(theta), -2.0 * j / rot) * 0.15915494309189533577;  // / 2 pi
-    p.rate[j] = static_cast<uint64_t>(std::ldexp(turns, 64));
-  }
+  // theta^(-2j/rot) / 2 pi by repeated products: j 2^-53 off at most, so an angle
+  // at a 20-bit position is off by 2^-28 of a turn (theta near 1; far less above).
+  // (a power for every plane is a fifth of a small call's time on the host)
+  const double step = rot ? std::pow(static_cast<double>(theta), -2.0 / rot) : 0.0;
+  double rate = 0.15915494309189533577 * 0x1p64;
+  for (int j = 0; j < rot / 2; j++, rate *= step) p.rate[j] = static_cast<uint64_t>(rate);
   // Heads a warp walks: all of a kind with many rows (the row's factors are
   // formed once for them; up to eight rounds), fewer while the launch would
   // leave SMs without work, down to one round of four.  24 + 4 + 4 heads of 256:
