@@ -5,10 +5,11 @@
 
 namespace tv {
 
-// Longest sequence (host bound) from which a call takes the block form: one
-// full block.  Measured for 48 value heads of 128 x 128: 64 rows take 28.7 us in
-// blocks and 28.6 row by row, 32 rows 27.7 and 16.4, 128 rows 30.8 and 51.2.
-constexpr int kBlocksFrom = 64;
+// Longest sequence (host bound) from which a call takes the block form.  In
+// blocks and row by row: 48 value heads of 128 x 128 take 15.8 us and 14.7 at 32
+// rows, 15.8 and 20.4 at 48, 16.0 and 26.0 at 63; 32 of them 15.7 and 11.9, 15.8 and
+// 16.3, 16.0 and 20.5; 8 of 64 x 64 13.3 and 9.0, 13.4 and 12.4, 13.5 and 15.5.
+constexpr int kBlocksFrom = 48;
 
 struct GdnPromptParams {
   PromptRows pr;

@@ -69,6 +69,7 @@ struct GdnTcParams {
   __nv_bfloat16* out;
   uint8_t* ws;
   int Hk, Hv, dv;
+  int heads;  // value heads a CTA of the first kernel takes, one after the other
   float scale;
 };
 
@@ -79,7 +80,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 }
 
 // ---------------------------------------------------------------------------
-// first kernel: W and P T of one block, for the value heads of one key head
+// first kernel: W and P T of one block, for value heads of one key head
 // ---------------------------------------------------------------------------
 // 16 x 16 blocks by warp-level tiles.  A matrix lives as accumulators (C
 // layout: row lane / 4 and +8, columns 2 (lane % 4) and +1 of two 8-wide
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
   const int s = strip_seq(w, p.pr, lane, base, blk);
   const int row0 = __shfl_sync(0xffffffffu, w.off, s) + (blk - __shfl_sync(0xffffffffu, base, s)) * kBlk;
   const int nv = min(kBlk, __shfl_sync(0xffffffffu, w.end, s) - row0);
-  const int g = blockIdx.y;
+  const int h0 = blockIdx.y * p.heads, g = h0 / (p.Hv / p.Hk);  // this CTA's first value head, their key head
   const uint32_t ks = smem_u32(sm), qs = ks + C::DX;  // the query rows are dead before DX is written
   const uint32_t dx = ks + C::DX, at = ks + C::AT, xt = ks + C::XT, img = ks + C::IMG;
   for (int e = tid; e < kBlk * (DK / 8); e += 128) {
@@ -209,13 +210,12 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
     }
   }
   const int fr = lane >> 2, fc = 2 * (lane & 3);  // fragment row (and +8) and column in a 16-row group
-  const int r = p.Hv / p.Hk;
   // a row's gates, one head ahead of their use
   const bool gate_row = tid < nv;  // (nv <= 64)
-  const size_t gate0 = static_cast<size_t>(row0 + (gate_row ? tid : 0)) * p.Hv + g * r;
+  const size_t gate0 = static_cast<size_t>(row0 + (gate_row ? tid : 0)) * p.Hv + h0;
   float al_n = gate_row ? p.alpha[gate0] : 1.f, be_n = gate_row ? p.beta[gate0] : 0.f;
-  for (int hh = 0; hh < r; hh++) {
-    const int h = g * r + hh;
+  for (int hh = 0; hh < p.heads; hh++) {
+    const int h = h0 + hh;
     uint8_t* dst = p.ws + (static_cast<size_t>(blk) * p.Hv + h) * Image<DK>::BYTES;
     if (tid < kBlk) {
       const bool fin = isfinite(al_n) && isfinite(be_n);
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
       if (lane == 0) cut_s[warp] = m ? 32 * warp + __ffs(m) - 1 : kBlk;
     }
     __syncthreads();
-    if (gate_row && hh + 1 < r) {
+    if (gate_row && hh + 1 < p.heads) {
       al_n = p.alpha[gate0 + hh + 1];
       be_n = p.beta[gate0 + hh + 1];
     }
@@ -711,13 +711,19 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
     offer();
     for (int c = 0; c < nb && ok; c++) {
       const uint32_t stg = sb + (c & 1) * C::STAGE;
-      const float* gd = reinterpret_cast<const float*>(sm + (c & 1) * C::STAGE + C::GOFF);
       const int live = n - c * kBlk;  // rows of the block that exist (64 and more: all)
       f2_t x[16], z[16];
       ok = wait_warp(FULL0 + 8u * (c & 1), (c >> 1) & 1, abort_flag, kWaitCycles);
       if (!ok) break;
-      // (through a shuffle, which waits for the loads: the arrivals that free the stage do not)
-      const float gr = __shfl_sync(0xffffffffu, gd[ri], lane), gc = __shfl_sync(0xffffffffu, gd[kBlk - 1], lane);
+      const float* gd = reinterpret_cast<const float*>(sm + (c & 1) * C::STAGE + C::GOFF);
+      const float gr = gd[ri];
+      // The state decays here, so that both loads have been served before the
+      // arrival below gives the stage back: an arrival does not wait for them, and
+      // the products can keep them waiting.  (g, NaN from some row on if at all, is
+      // so in the last row: gr's share of 0 changes nothing.)
+      const f2_t g2 = f2_dup(__fmaf_rn(gr, 0.f, gd[kBlk - 1]));
+#pragma unroll
+      for (int e = 0; e < 16; e++) S[e] = f2_mul(g2, S[e]);
       if (krow) {
 #pragma unroll
         for (int q = 0; q < 4; q++) {
@@ -760,9 +766,8 @@ __global__ void __launch_bounds__(352, 1) gdn_block_walk_kernel(const __grid_con
       tc_fence_after();
       const bool bad = any_bad(c);
       load_sum(tl + C::T_D3, z);
-      const f2_t g2 = f2_dup(gc);
 #pragma unroll
-      for (int e = 0; e < 16; e++) S[e] = f2_fma(g2, S[e], z[e]);
+      for (int e = 0; e < 16; e++) S[e] = f2_add(S[e], z[e]);
       if (bad) poison(S, c, kBlk - 1);
       if (c + 1 < nb) offer();
       if (!krow) {
@@ -835,7 +840,7 @@ static tv_status launch_tc(const GdnTcParams& p, int64_t blocks, cudaStream_t st
       return TV_ERR_CUDA;
     set = true;
   }
-  launch_k(true, gdn_block_prep_kernel<DK>, dim3(static_cast<unsigned>(blocks), p.Hk), dim3(128), Prep<DK>::SMEM, st, p);
+  launch_k(true, gdn_block_prep_kernel<DK>, dim3(static_cast<unsigned>(blocks), p.Hv / p.heads), dim3(128), Prep<DK>::SMEM, st, p);
   launch_k(true, gdn_block_walk_kernel<DK>, dim3(p.pr.n_seq * p.Hv * (p.dv / kDvs)), dim3(352), Walk<DK>::SMEM, st, p);
   return launch_status();
 }
@@ -871,6 +876,11 @@ tv_status gdn_prompt_tc_launch(const tv_gdn_layer* l, const GdnPromptParams& a, 
   p.Hv = a.Hv;
   p.dv = a.dv;
   p.scale = a.scale;
+  // The value heads of a key head share its K K^T and Q K^T, but one after the
+  // other they are a call's latency where a CTA for each still makes one wave:
+  // 48 heads of 128, 64 rows 16.0 us (25.9), 300 rows 25.5 (33.0), 512 rows 32.8
+  // (38.9); 1,024 rows, two waves, 58.4 (57.9), 1,536 rows 84.1 (76.9).
+  p.heads = blocks_bound(pr) * a.Hv <= 3 * num_sms() ? 1 : a.Hv / a.Hk;
   return l->dk == 128 ? launch_tc<128>(p, blocks_bound(pr), st) : launch_tc<64>(p, blocks_bound(pr), st);
 }
 
