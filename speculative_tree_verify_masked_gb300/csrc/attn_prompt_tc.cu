@@ -941,8 +941,8 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
 }
 
 // Joins the pieces of split items, in order: a warp takes 128 columns of a row,
-// four a lane.
-template <int D>
+// four a lane, the loads of kJ pieces in flight.
+template <int D, int kJ>
 __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_constant__ AttnPromptTcParams p) {
   constexpr int CB = D > 128 ? D / 128 : 1, LPR = D >= 128 ? 32 : D / 4, RPW = 32 / LPR;
   __shared__ PromptPlan pl;
@@ -973,7 +973,6 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
       const float* rec = p.ws + (static_cast<size_t>(first) * 128 + lrow) * (D + 4);
       const size_t step = static_cast<size_t>(per) * 128 * (D + 4);
       // one pass with a running maximum, kJ pieces' loads in flight at a time
-      constexpr int kJ = 8;
       float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
       for (int j0 = 0; j0 < np; j0 += kJ) {
         float4 o[kJ];
@@ -1079,8 +1078,22 @@ static tv_status launch_prompt_tc(AttnPromptTcParams& p, const AttnPromptCall& a
     set = true;
   }
   launch_k(true, attn_prompt_tc_kernel<D>, dim3(p.workers), dim3(384), C::SMEM, st, p);
-  // the join has work only where the plan, made on the device, split items
-  if (p.slots > 0) launch_k(true, attn_prompt_join_kernel<D>, dim3(num_sms() * 4), dim3(256), 0, st, p);
+  // The join has work only where the plan, made on the device, split items: with
+  // few of them.  With few rows too, a warp each, its time is that of one row's
+  // pieces, and 24 loads in flight serve best (24 rows behind 65,536: 59.9 us, 61.1
+  // with 12; 8 behind 50,000, 16 + 2 heads: 22.8 and 26.9); with more rows warps do
+  // (200 behind 20,000, 32 + 4 heads: 76.6 us with 12 loads and twice the CTAs, 102.7
+  // with 24).  Whole prompts have next to nothing to join and want few CTAs that
+  // take the SMs of the kernel before as they come free (packed 6,659 rows without
+  // a gate: 235 us and 241).
+  if (p.slots > 0) {
+    const int sms = num_sms();
+    const int64_t rows = static_cast<int64_t>(a.prompt->n_total) * l->Hq, units = rows * (D > 128 ? D / 128 : 1);
+    if (units <= 8 * sms || rows >= 4 * sms * static_cast<int64_t>(p.T) * p.G)
+      launch_k(true, attn_prompt_join_kernel<D, 24>, dim3(sms), dim3(256), 0, st, p);
+    else
+      launch_k(true, attn_prompt_join_kernel<D, 12>, dim3(2 * sms), dim3(256), 0, st, p);
+  }
   return launch_status();
 }
 
