@@ -47,9 +47,9 @@
 // and a tile takes about 2,300 (tensor pipe 76 % active over a whole call of
 // 8,192 rows under a power cap).  24 + 4 heads of 256, and the same operations at
 // the measured rate of a large library product: 8,192 rows 495 us (432), 1,024
-// rows behind 130,048 2,040 us (1,722), packed 2,047 + 1 + 515 + 4,096 rows with a
-// gate 256 us (159; tiles that are half masked and short items), 24 rows behind
-// 65,536 70 us (40 of bytes; pieces of a few tiles, then the join).
+// rows behind 130,048 2,020 us (1,722), packed 2,047 + 1 + 515 + 4,096 rows with a
+// gate 254 us (159; tiles that are half masked and short items), 24 rows behind
+// 65,536 67 us (40 of bytes; pieces of a few tiles, then the join).
 #include <cmath>
 #include <cstring>
 

@@ -49,3 +49,32 @@ def test_gdn_prompt_repeats(kw):
 
     repeat(1000, run, [g.out] + g.S, g.ws)
     assert g.prompt.status_code() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Two batches of each kind side by side, each with its own buffers, give what each gives alone."""
+    runs = [Attn([900], [300], seed=4, gate=True), Attn([40, 500], [3000, 0], Hq=16, Hkv=2, D=128, seed=5),
+            Gdn([700, 20], Hk=4, Hv=8, seed=6), Gdn([30], Hk=2, Hv=4, dk=64, dv=64, seed=7)]
+
+    def go(x, stream=None):
+        if isinstance(x, Gdn):
+            for s, z in zip(x.S, x.S0):
+                s.copy_(z)
+        x.run(stream)
+
+    refs = []
+    for x in runs:
+        go(x)
+        refs.append([x.out.clone()] + [s.clone() for s in getattr(x, "S", [])])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(50):
+        for x, s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                x.out.fill_(7.0)
+                go(x)
+    torch.cuda.synchronize()
+    for x, ref in zip(runs, refs):
+        assert x.prompt.status_code() == 0
+        for a, b in zip([x.out] + list(getattr(x, "S", [])), ref):
+            assert torch.equal(a, b)
