@@ -44,7 +44,7 @@
 // go to the workspace as fp32 and are joined by a second kernel.
 //
 // Bound by the tensor cores: at D = 256 a tile's two products take 2,048 cycles
-// and a tile takes about 2,300 (tensor pipe 76 % active over a whole call of
+// and a tile takes about 2,300 (tensor pipe 77 % active over a whole call of
 // 8,192 rows under a power cap).  24 + 4 heads of 256, and the same operations at
 // the measured rate of a large library product: 8,192 rows 495 us (432), 1,024
 // rows behind 130,048 2,020 us (1,722), packed 2,047 + 1 + 515 + 4,096 rows with a

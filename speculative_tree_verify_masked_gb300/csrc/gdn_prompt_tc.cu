@@ -31,9 +31,9 @@
 // the bf16 output and is rounded once.
 //
 // Bound by the chain of products, tensor-memory round trips and splits a block,
-// not by bytes: 16 + 48 heads of 128 x 128, 8,192 rows 335 us (128 + 206; 41.5
-// of bytes), about 3,000 cycles a block and CTA, the tensor pipe busy for 65 % of
-// them; 2,047 + 1 + 515 + 4,096 rows 234 us (105 + 126).  The first kernel waits
+// not by bytes: 16 + 48 heads of 128 x 128, 8,192 rows 335 us (127 + 207; 41.5
+// of bytes), about 3,000 cycles a block and CTA, the tensor pipe busy for 62 % of
+// them; 2,047 + 1 + 515 + 4,096 rows 234 us (104 + 127).  The first kernel waits
 // for its own steps (33 % of issue slots; registers hold it to three CTAs an SM).
 #include <cstring>
 
