@@ -190,7 +190,9 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 
 // The plan, by one warp.  Cost of a candidate, in key tiles: the waves of
 // pieces at their mean length, the longest piece's overhang, about three tiles
-// to start and end a piece and four more to write and join a partial one.
+// to start and end a piece and four more to write and join a partial one.  Both
+// kernels make it for themselves, so every step rounds by itself: contracted
+// differently in the two, near ties would give two plans.
 __device__ inline void make_plan(const AttnPromptTcParams& p, const WarpSeqs& w, int lane, PromptPlan& pl) {
   const int n = w.end - w.off;
   const bool live = lane < p.pr.n_seq && n > 0;
@@ -209,15 +211,18 @@ __device__ inline void make_plan(const AttnPromptTcParams& p, const WarpSeqs& w,
     const int r = __shfl_sync(0xffffffffu, rt, s), k1 = __shfl_sync(0xffffffffu, nk, s),
               k0 = __shfl_sync(0xffffffffu, nk0, s);
     if (r == 0) continue;
-    const float items = static_cast<float>(p.Hkv) * r;
+    const float items = __fmul_rn(static_cast<float>(p.Hkv), static_cast<float>(r));
     const int pm = ceil_div(k1, S);
-    W += items * 0.5f * (k0 + k1);
-    P += items * pm;
-    if (pm > 1) part += items * pm;
+    const float pieces = __fmul_rn(items, static_cast<float>(pm));
+    W = __fadd_rn(W, __fmul_rn(__fmul_rn(items, 0.5f), static_cast<float>(k0 + k1)));
+    P = __fadd_rn(P, pieces);
+    if (pm > 1) part = __fadd_rn(part, pieces);
     longest = fmaxf(longest, static_cast<float>(min(S, k1)));
   }
-  const float mean = W / fmaxf(P, 1.f);
-  float cost = ceilf(P / p.workers) * (mean + 3.f) + 0.5f * (longest - mean) + 4.f * part / p.workers;
+  const float workers = static_cast<float>(p.workers), mean = __fdiv_rn(W, fmaxf(P, 1.f));
+  float cost = __fmul_rn(ceilf(__fdiv_rn(P, workers)), __fadd_rn(mean, 3.f));
+  cost = __fadd_rn(cost, __fmul_rn(0.5f, __fsub_rn(longest, mean)));
+  cost = __fadd_rn(cost, __fdiv_rn(__fmul_rn(4.f, part), workers));
   if (part > static_cast<float>(p.slots)) cost = INFINITY;  // lane 0 (one piece) always fits
   int best = lane;
 #pragma unroll
