@@ -21,14 +21,19 @@
 // memory, the state in registers (a thread holds one key row, 32 columns).
 //
 // Precision.  k, q and v are bf16 as they come.  What is formed on the way (S,
-// R, W, A, T) enters a product as two bf16 parts, x = hi + lo with hi =
-// bf16(x), lo = bf16(x - hi), which leaves 2^-17 of each value at most: in the
-// walk hi and lo of S and R stand side by side in a product's columns and W's
-// take a pass each; in the first kernel lo lo is left out.  One part alone would
-// leave 2^-9, far above what a state that lives over a long prompt can take;
-// with two it stays within 5e-6 of the recurrence in 64 bits (rel-L2, 8,192
-// rows: 4.3e-6, and 5.1e-6 without W lo's product with R lo).  P T only reaches
-// the bf16 output and is rounded once.
+// R, W, and T where it enters W and P T) enters a product as two bf16 parts, x =
+// hi + lo with hi = bf16(x), lo = bf16(x - hi), which leaves 2^-17 of each value
+// at most: in the walk hi and lo of S and R stand side by side in a product's
+// columns and W's take a pass each; in the first kernel lo lo is left out.  One
+// part alone would leave 2^-9, far above what a state that lives over a long
+// prompt can take.  The inverse itself is formed in fp32 (diagonal blocks) and
+// two tf32 parts: where keys resemble each other A is far from zero and the
+// inverse's entries are what its sums leave.  From the recurrence in 64 bits the
+// state is (rel-L2) 4.3e-6 after 8,192 rows with independent keys and drawn gates;
+// over gates beta 0.9 .. 1, alpha 0.99 .. 1 and up to 2,000 rows 6.0e-6 with
+// independent keys, 7.0e-6 at a mean cosine of 0.8, 2.1e-5 with equal keys, 2.7e-5
+// with two keys in turn (heads of 64: 3.9e-5), where W's two parts add up.  P T
+// only reaches the bf16 output and is rounded once.
 //
 // Bound by the chain of products, tensor-memory round trips and splits a block,
 // not by bytes: 16 + 48 heads of 128 x 128, 8,192 rows 335 us (127 + 207; 41.5
@@ -114,6 +119,58 @@ __device__ __forceinline__ void mma_split(float (&c0)[4], float (&c1)[4], const 
   mma16816(c1, a.h, b.l[2], b.l[3]);
   mma16816(c0, a.l, b.h[0], b.h[1]);
   mma16816(c1, a.l, b.h[2], b.h[3]);
+}
+// Forming the inverse takes more: what is left of its sums cancels where keys
+// resemble each other.  A and the inverse's diagonal blocks lie in shared memory
+// as fp32 [64][64], column c of row r at c ^ 8 (r / 2 mod 4) so that a warp's
+// reads below fall on distinct banks, and a product takes both operands as two
+// tf32 parts (11 bits each, lo lo left out: 2^-22).
+__device__ __forceinline__ uint32_t f32_at(uint32_t tile, int r, int c) {
+  return tile + static_cast<uint32_t>((r * kBlk + (c ^ ((r >> 1 & 3) << 3))) * 4);
+}
+__device__ __forceinline__ float ld_f32(uint32_t a) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+  return x;
+}
+__device__ __forceinline__ void st_f32x2(uint32_t a, float x, float y) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+struct Tf32 {
+  uint32_t h, l;
+};
+__device__ __forceinline__ Tf32 split_tf32(float x) {
+  Tf32 t;
+  t.h = __float_as_uint(x) & 0xffffe000u;
+  t.l = __float_as_uint(__fsub_rn(x, __uint_as_float(t.h))) & 0xffffe000u;
+  return t;
+}
+// d += a b for one 16 x 8 x 8 tile
+__device__ __forceinline__ void mma1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// acc += x B of 16 x 16 blocks: x as accumulators, B the fp32 tile's block at (r0,
+// c0).  The sum runs over columns 2t, 2t+1 of x where a tile has k = t, t+4, so
+// that accumulators are operands as they lie; B's rows are taken likewise.
+__device__ __forceinline__ void mma_block(float (&acc)[2][4], const float (&x)[2][4], uint32_t tile, int r0, int c0, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int s = 0; s < 2; s++) {
+    Tf32 a[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) a[e] = split_tf32(x[s][e]);
+#pragma unroll
+    for (int n = 0; n < 2; n++) {
+      const Tf32 b0 = split_tf32(ld_f32(f32_at(tile, r0 + 8 * s + 2 * t, c0 + 8 * n + g)));
+      const Tf32 b1 = split_tf32(ld_f32(f32_at(tile, r0 + 8 * s + 2 * t + 1, c0 + 8 * n + g)));
+      mma1688(acc[n], a[0].h, a[2].h, a[1].h, a[3].h, b0.h, b1.h);
+      mma1688(acc[n], a[0].h, a[2].h, a[1].h, a[3].h, b0.l, b1.l);
+      mma1688(acc[n], a[0].l, a[2].l, a[1].l, a[3].l, b0.h, b1.h);
+    }
+  }
 }
 __device__ __forceinline__ void stsm_x4(uint32_t addr, const uint32_t (&r)[4]) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
@@ -280,9 +337,8 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
           for (int e = 0; e < 4; e++) d[t][e] = win[b][fr + (e >> 1) * 8][8 * t + fc + (e & 1)];
       }
     };
-    // this warp's rows of A, as hi and lo tiles
+    // this warp's rows of A
     const float be0 = be_s[16 * warp + fr], be1 = be_s[16 * warp + fr + 8];
-    float Ad[2][4];
 #pragma unroll
     for (int b = 0; b < 4; b++) {
       if (b > warp) continue;
@@ -291,49 +347,48 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
 #pragma unroll
       for (int t = 0; t < 2; t++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) A[t][e] = __fmul_rn((e >> 1) ? be1 : be0, __fmul_rn(A[t][e], G[2 * b + t][e]));
-      if (b == warp) {
-#pragma unroll
-        for (int t = 0; t < 2; t++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) Ad[t][e] = A[t][e] = 8 * t + fc + (e & 1) < fr + (e >> 1) * 8 ? A[t][e] : 0.f;
-      }
-      store_op(at, kTile64, 16 * warp, 16 * b, lane, split_op(A[0], A[1]));
+        for (int e = 0; e < 2; e++) {
+          const int r = 16 * warp + fr + 8 * e, c = 16 * b + 8 * t + fc;
+          const float x0 = __fmul_rn(e ? be1 : be0, __fmul_rn(A[t][2 * e], G[2 * b + t][2 * e]));
+          const float x1 = __fmul_rn(e ? be1 : be0, __fmul_rn(A[t][2 * e + 1], G[2 * b + t][2 * e + 1]));
+          st_f32x2(f32_at(at, r, c), x0, x1);  // (on and above the diagonal: not read)
+        }
     }
-    // inverse of this warp's diagonal block: A is strictly lower triangular, so
-    // (I + A)^-1 = (I - A)(I + A^2)(I + A^4)(I + A^8)
+    // The inverse of this warp's diagonal block by forward substitution, a column
+    // a lane, into a block of A's tile above the diagonal.  (As a product of
+    // powers, (I - A)(I + A^2)(I + A^4)(I + A^8), it loses what A^8 grows by: for
+    // equal keys and gates of 1 its entries reach 3,432, the inverse's 1.)
     __syncwarp();
+    const int ir = warp < 3 ? 0 : 16, ic = warp < 3 ? 16 * (warp + 1) : 32;  // where that block lies
     float X[4][2][4];  // this warp's row of blocks of (I + A)^-1; X[b] is block column b
     float D[2][4];
     {
-      float Q2[2][4];
+      const int c = lane & 15;  // (the upper lanes do the same once more)
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        float r = i == c ? 1.f : 0.f;
+#pragma unroll
+        for (int k = 0; k < i; k += 4) {
+          float a[4];
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3])
+                       : "r"(f32_at(at, 16 * warp + i, 16 * warp + k))
+                       : "memory");
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            if (k + e < i) r = __fmaf_rn(-a[e], x[k + e], r);
+        }
+        x[i] = r;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; i++)
+        if (lane < 16) asm volatile("st.shared.f32 [%0], %1;" ::"r"(f32_at(at, ir + i, ic + c)), "f"(x[i]) : "memory");
+      __syncwarp();
 #pragma unroll
       for (int t = 0; t < 2; t++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          D[t][e] = (fr + (e >> 1) * 8 == 8 * t + fc + (e & 1) ? 1.f : 0.f) - Ad[t][e];
-          Q2[t][e] = 0.f;
-        }
-      mma_split(Q2[0], Q2[1], split_op(Ad[0], Ad[1]), load_op(at, 16 * warp, 16 * warp, lane));
-#pragma unroll
-      for (int it = 0; it < 3; it++) {
-        const Op16 q = split_op(Q2[0], Q2[1]);
-        __syncwarp();
-        store_op(xt, kTile64, 16 * warp, 16 * warp, lane, q);
-        __syncwarp();
-        const Op16 qb = load_op(xt, 16 * warp, 16 * warp, lane);
-        const Op16 x = split_op(D[0], D[1]);
-        mma_split(D[0], D[1], x, qb);
-        if (it < 2) {
-#pragma unroll
-          for (int t = 0; t < 2; t++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) Q2[t][e] = 0.f;
-          mma_split(Q2[0], Q2[1], q, qb);
-        }
-      }
-      __syncwarp();
-      store_op(xt, kTile64, 16 * warp, 16 * warp, lane, split_op(D[0], D[1]));
+        for (int e = 0; e < 4; e++) D[t][e] = ld_f32(f32_at(at, ir + fr + 8 * (e >> 1), ic + 8 * t + fc + (e & 1)));
     }
     __syncthreads();
     // the rest of the row: X_wj = -(sum over j < k <= w of X_wk A_kj) X_jj
@@ -352,12 +407,12 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
           for (int e = 0; e < 4; e++) acc[t][e] = X[b][t][e] = 0.f;
 #pragma unroll
         for (int k = 3; k >= 1; k--)
-          if (k > b && k <= warp) mma_split(acc[0], acc[1], split_op(X[k][0], X[k][1]), load_op(at, 16 * k, 16 * b, lane));
+          if (k > b && k <= warp) mma_block(acc, X[k], at, 16 * k, 16 * b, lane);
 #pragma unroll
         for (int t = 0; t < 2; t++)
 #pragma unroll
           for (int e = 0; e < 4; e++) acc[t][e] = -acc[t][e];
-        mma_split(X[b][0], X[b][1], split_op(acc[0], acc[1]), load_op(xt, 16 * b, 16 * b, lane));
+        mma_block(X[b], acc, at, 0, 16 * (b + 1), lane);  // X_jj
       }
     }
     {
@@ -365,7 +420,7 @@ __global__ void __launch_bounds__(128, 3) gdn_block_prep_kernel(const __grid_con
 #pragma unroll
       for (int b = 0; b < 4; b++) {
         if (b > warp) continue;
-        if (b < warp) store_op(xt, kTile64, 16 * warp, 16 * b, lane, split_op(X[b][0], X[b][1]));
+        store_op(xt, kTile64, 16 * warp, 16 * b, lane, split_op(X[b][0], X[b][1]));
 #pragma unroll
         for (int t = 0; t < 2; t++)
 #pragma unroll
