@@ -190,6 +190,31 @@ def _stream(stream):
     return int(stream)
 
 
+def _torch_stream(stream):
+    """The torch stream of a call's stream argument."""
+    if stream is None:
+        return torch.cuda.current_stream()
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+
+
+def _upload(dst, values, stream):
+    """Writes a few int32 to a device buffer in the stream's order: without
+    waiting for it, or, on the current stream (None), until they are there."""
+    src = torch.tensor(values, dtype=torch.int32)
+    if not dst.is_cuda:
+        dst.copy_(src)
+        return
+    with torch.cuda.stream(_torch_stream(stream)):
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("rows are written from the host: before a graph's replay, not inside its capture")
+        if stream is None:
+            dst.copy_(src)
+        else:
+            dst.copy_(src.pin_memory(), non_blocking=True)  # (the memory is not reused before the copy has run)
+
+
 def _dtype_code(dt: torch.dtype) -> int:
     if dt == torch.bfloat16:
         return TV_BF16
@@ -260,7 +285,9 @@ class Prompt:
     """Device buffers of a tv_prompt for the given rows per sequence.
     n_total and n_max may be larger than the rows need (padding behind the
     last sequence, a graph's bounds); set_rows writes another batch's offsets
-    into the same buffer."""
+    into the same buffer: with `stream`, the calls' one, behind what it holds
+    (calls enqueued there before keep their rows) and without waiting; without,
+    on the current stream, whose calls before it are waited for."""
 
     def __init__(self, rows, device="cuda", n_total: int | None = None, n_max: int | None = None):
         off = self._offsets(rows)
@@ -278,11 +305,11 @@ class Prompt:
             off.append(off[-1] + int(n))
         return off
 
-    def set_rows(self, rows):
+    def set_rows(self, rows, stream=None):
         off = self._offsets(rows)
         if len(rows) != self.n_seq or off[-1] > self.n_total or (rows and max(rows) > self.n_max):
             raise ValueError(f"rows {rows} do not fit {self.n_seq} sequences, {self.n_total} rows, {self.n_max} each")
-        self.row_off.copy_(torch.tensor(off, dtype=torch.int32))
+        _upload(self.row_off, off, stream)
 
     def counts(self) -> torch.Tensor:
         """Rows of each sequence, on the device (tv_len_advance's `by`)."""

@@ -53,10 +53,14 @@ class PromptPass:
         # tv_len_advance reads the spans' rows from the device; a graph keeps the buffer
         self.rows = torch.zeros(r.cfg.n_seq, dtype=torch.int32, device=dev)
 
-    def set_rows(self, rows):
-        """The next span's rows per sequence (0: none), written to the device."""
-        self.prompt.set_rows(rows)
-        self.rows.copy_(self.prompt.counts())
+    def set_rows(self, rows, stream=None):
+        """The next span's rows per sequence (0: none), written to the device.
+        With the stream that run() gets, behind what that holds, so spans can
+        be fed one behind the other without waiting; without, on the current
+        stream, which is waited for (no earlier span may run on another)."""
+        self.prompt.set_rows(rows, stream)
+        with torch.cuda.stream(B._torch_stream(stream)):
+            self.rows.copy_(self.prompt.counts())
 
     def layer(self, li, x: dict, stream=None):
         """One layer over the span.  Attention: x holds q, k, v, out and, for
