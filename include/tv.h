@@ -395,15 +395,18 @@ tv_status tv_gdn_conv_commit(const tv_gdn_front_layer* layer, const tv_tree* tre
  * in slices of any sizes.  One layer of a span runs
  *   attention: tv_attn_prompt_front, tv_attn_prompt
  *   GDN:       tv_gdn_prompt_front, tv_gdn_prompt, tv_gdn_out_norm
- * and after the last layer len[s] += row_off[s+1] - row_off[s]
- * (tv_len_advance): a verify round or a decode step then goes on from there.
+ * between tv_prompt_check before the first layer and tv_prompt_advance after
+ * the last: a verify round or a decode step then goes on from there.
  *
  * The offsets live on the device, so a captured graph serves every batch that
  * fits its host bounds; rows from row_off[n_seq] on are padding, neither read
  * nor written.  Offsets that do not start at 0, that fall, that give a sequence
  * more than n_max rows or end past n_total set TV_ERR_ROWS; a length outside
  * 0..max_len sets TV_ERR_LEN; rows past a cache's cap set TV_ERR_CAPACITY.
- * Any of them makes the whole call a no-op.  Sequences of one call must not
+ * Any of them makes the whole call a no-op, and, once the word is set, every
+ * later one that is given it.  The GDN calls see no lengths: tv_prompt_check
+ * ahead of a span's first layer keeps a span that an attention layer would
+ * refuse from moving the states and tails of layers before it.  Sequences of one call must not
  * share a cache, state or tail.  n_total = 0 does nothing.
  *
  * The prompt calls and tv_attn_norm_rope always launch with programmatic
@@ -423,6 +426,17 @@ typedef struct {
   const int32_t* row_off; /* device [n_seq+1], row_off[0] = 0, not falling, row_off[n_seq] <= n_total */
   int32_t* status;        /* device [1] error word, as in tv_tree */
 } tv_prompt;
+
+/* The checks of a whole span, before anything of it is written: offsets, lengths
+ * against max_len and, with the rows, against cap (the attention layers').  Sets
+ * the status word as the calls themselves do. */
+tv_status tv_prompt_check(const tv_prompt* prompt, const int32_t* len, int32_t max_len, int32_t cap,
+                          tv_stream stream);
+
+/* len[s] += the span's rows of sequence s, after its last layer; does nothing
+ * once the status word is set (a refused span moves no length, so it can be fed
+ * again, when the word has been cleared). */
+tv_status tv_prompt_advance(const tv_prompt* prompt, int32_t* len, tv_stream stream);
 
 /* Head norms and rotation in one pass: tv_attn_rope's rotation (same planes,
  * angles and positions) of rows that are first normalised per head,

@@ -140,6 +140,10 @@ def lib():
         L.tv_kvpool_destroy.restype = c_int32
         L.tv_kvpool_destroy.argtypes = [vp]
         R = POINTER(tv_prompt)
+        L.tv_prompt_check.restype = c_int32
+        L.tv_prompt_check.argtypes = [R, vp, c_int32, c_int32, vp]
+        L.tv_prompt_advance.restype = c_int32
+        L.tv_prompt_advance.argtypes = [R, vp, vp]
         L.tv_attn_norm_rope.restype = c_int32
         L.tv_attn_norm_rope.argtypes = [A, T, c_int32, vp, c_int32, vp, vp, c_float, c_int32, c_float, vp, vp, vp, vp,
                                         vp, vp]
@@ -168,7 +172,7 @@ EXPORTED = ["tv_status_string", "tv_version", "tv_tree_meta_bytes", "tv_tree_pre
             "tv_kvpool_committed_bytes", "tv_kvpool_reserved_bytes", "tv_kvpool_destroy", "tv_attn_rope",
             "tv_attn_tree_verify_gated", "tv_attn_decode_gated", "tv_gdn_front", "tv_gdn_out_norm",
             "tv_gdn_conv_commit", "tv_gdn_tree_verify_fused", "tv_gdn_decode_fused", "tv_wait_selftest",
-            "tv_attn_norm_rope", "tv_attn_prompt_front", "tv_attn_prompt_workspace_bytes", "tv_attn_prompt",
+            "tv_prompt_check", "tv_prompt_advance", "tv_attn_norm_rope", "tv_attn_prompt_front", "tv_attn_prompt_workspace_bytes", "tv_attn_prompt",
             "tv_gdn_prompt_workspace_bytes", "tv_gdn_prompt", "tv_gdn_prompt_front"]
 
 
@@ -494,6 +498,18 @@ def _ws_bytes(ws) -> int:
     if not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("the workspace must be contiguous GPU memory")
     return ws.numel() * ws.element_size()
+
+
+def tv_prompt_check(prompt: Prompt, len_, max_len: int, cap: int, stream=None):
+    """The checks of a span, before its first layer."""
+    _need("tv_prompt_check", len=(len_, torch.int32, prompt.n_seq))
+    _check(lib().tv_prompt_check(ctypes.byref(prompt.c), _ptr(len_), max_len, cap, _stream(stream)), "tv_prompt_check")
+
+
+def tv_prompt_advance(prompt: Prompt, len_, stream=None):
+    """The lengths past the span, after its last layer; not past a refused one."""
+    _need("tv_prompt_advance", len=(len_, torch.int32, prompt.n_seq))
+    _check(lib().tv_prompt_advance(ctypes.byref(prompt.c), _ptr(len_), _stream(stream)), "tv_prompt_advance")
 
 
 def tv_attn_norm_rope(layer: AttnLayer, tree: Tree | None, n_seq, len_, max_len, q_norm, k_norm, eps, rot_dims, theta,

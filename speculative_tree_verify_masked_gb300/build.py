@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtreeverify.so")
 SOURCES = ["tree.cu", "gdn.cu", "attn_f32.cu", "attn_tc.cu", "commit.cu", "api.cu", "attn_static.cu", "kvpool.cu", "front.cu", "front_gdn.cu",
-           "norm_rope.cu", "front_gdn_prompt.cu", "attn_prompt.cu", "attn_prompt_tc.cu", "gdn_prompt.cu", "gdn_prompt_tc.cu"]
+           "prompt.cu", "norm_rope.cu", "front_gdn_prompt.cu", "attn_prompt.cu", "attn_prompt_tc.cu", "gdn_prompt.cu", "gdn_prompt_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -8,7 +8,9 @@ them, of the round's sequences) through every mixer of the round's layers,
   GDN:       tv_gdn_prompt_front, tv_gdn_prompt, tv_gdn_out_norm
 
 and then advances the round's lengths, so that the next verify round or decode
-step goes on behind the span.  ("How ignis serves a request", "The shape of
+step goes on behind the span.  A span that does not fit (malformed rows, a length
+above the round's bound, rows past a cache's end) is refused before its first
+layer: status() names the reason, and caches, states, tails and lengths stay.  ("How ignis serves a request", "The shape of
 the process": one call per prefill span; "One request, end to end", 2.5.)
 
 The pass owns what lies between the calls of one layer (rotated queries,
@@ -50,8 +52,6 @@ class PromptPass:
             layer = next(iter(r.gdn.values()))["layer"]
             ws = max(ws, B.tv_gdn_prompt_workspace_bytes(layer, self.prompt))
         self.ws = torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None
-        # tv_len_advance reads the spans' rows from the device; a graph keeps the buffer
-        self.rows = torch.zeros(r.cfg.n_seq, dtype=torch.int32, device=dev)
 
     def set_rows(self, rows, stream=None):
         """The next span's rows per sequence (0: none), written to the device.
@@ -59,8 +59,13 @@ class PromptPass:
         be fed one behind the other without waiting; without, on the current
         stream, which is waited for (no earlier span may run on another)."""
         self.prompt.set_rows(rows, stream)
-        with torch.cuda.stream(B._torch_stream(stream)):
-            self.rows.copy_(self.prompt.counts())
+
+    def check(self, stream=None):
+        """Refuses a span that does not fit; before its first layer.  (Without
+        attention layers only its offsets can be wrong.)"""
+        most = (1 << 31) - 1
+        B.tv_prompt_check(self.prompt, self.r.len, *((self.r.max_len, self.r.cap) if self.r.attn else (most, most)),
+                          stream)
 
     def layer(self, li, x: dict, stream=None):
         """One layer over the span.  Attention: x holds q, k, v, out and, for
@@ -84,13 +89,16 @@ class PromptPass:
             B.tv_gdn_out_norm(f, self.prompt.n_total, self.o, x["z"], x["w_norm"], x["out"], stream)
 
     def advance(self, stream=None):
-        """The round's lengths past the span; after its last layer."""
-        B.tv_len_advance(self.r.len, self.rows, 0, self.r.cfg.n_seq, stream)
+        """The round's lengths past the span, unless it was refused; after its last layer."""
+        B.tv_prompt_advance(self.prompt, self.r.len, stream)
 
     def run(self, inputs: dict, stream=None):
         """One span through every layer (inputs by layer index, as layer()
         takes them), then the lengths.  With a KV pool the rows that the span
-        writes are committed first (VerifyRound.commit_kv)."""
+        writes are committed first (VerifyRound.commit_kv).  After a refused
+        span nothing runs until its status is cleared (prompt.status.zero_());
+        the layers' outputs then hold nothing of use."""
+        self.check(stream)
         for li in self.r.layers:
             self.layer(li, inputs[li], stream)
         self.advance(stream)

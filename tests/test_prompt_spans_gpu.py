@@ -71,3 +71,59 @@ def test_rows_are_not_set_inside_a_capture():
     g.replay()
     torch.cuda.synchronize()
     assert p.status() == 0 and st.r.len.tolist() == [20, 10]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("why,code", [("len", 10), ("capacity", 6), ("rows", 12), ("len below 0", 10)])
+def test_a_refused_span_moves_nothing(dtype, why, code):
+    """GDN layers come first here: they must not move either; cleared, the span runs."""
+    st = Stack(dtype, [65, 40])
+    r = st.r
+    p = st.make(105, 65)
+    for a in r.attn.values():  # (NaN is not equal to itself)
+        for t in a["layer"].K + a["layer"].V:
+            t.fill_(3.0)
+    p.set_rows([65, 40])
+    L = {"len": [0, r.max_len + 1], "capacity": [r.max_len, 0], "rows": [7, 9], "len below 0": [-1, 0]}[why]
+    assert r.cap == r.max_len + 64
+    if why == "rows":
+        p.prompt.row_off.copy_(torch.tensor([0, 65, 50], dtype=torch.int32))
+    r.len.copy_(torch.tensor(L, dtype=torch.int32))
+    full = [t.clone() for a in r.attn.values() for t in a["layer"].K + a["layer"].V] + held(st, [0, 0])
+    for _ in range(2):  # (the word stays: the second one is a no-op too)
+        p.run(st.x)
+    torch.cuda.synchronize()
+    assert p.status() == code and r.len.tolist() == L
+    now = [t for a in r.attn.values() for t in a["layer"].K + a["layer"].V] + held(st, [0, 0])
+    assert all(torch.equal(a, b) for a, b in zip(full, now))
+    p.prompt.status.zero_()
+    p.set_rows([65, 40])
+    st.reset()
+    p.run(st.x)
+    torch.cuda.synchronize()
+    assert p.status() == 0 and r.len.tolist() == [65, 40]
+    assert all(bool(torch.isfinite(t).all()) for t in held(st, [65, 40]))
+
+
+def test_span_check_and_advance_by_themselves():
+    from speculative_tree_verify_masked_gb300 import binding as B
+
+    ln = torch.tensor([5, 10, 0], dtype=torch.int32, device="cuda")
+    p = B.Prompt([3, 0, 4], n_total=9, n_max=6)
+    B.tv_prompt_check(p, ln, 10, 13)
+    B.tv_prompt_advance(p, ln)
+    torch.cuda.synchronize()
+    assert p.status_code() == 0 and ln.tolist() == [8, 10, 4]
+    B.tv_prompt_check(p, ln, 10, 10)  # 8 + 3 rows
+    B.tv_prompt_advance(p, ln)
+    torch.cuda.synchronize()
+    assert p.status_code() == 6 and ln.tolist() == [8, 10, 4]
+    p.status.zero_()
+    B.tv_prompt_check(p, ln, 9, 100)
+    torch.cuda.synchronize()
+    assert p.status_code() == 10
+    p.status.zero_()
+    p.row_off.copy_(torch.tensor([0, 7, 7, 9]))
+    B.tv_prompt_advance(p, ln)  # more than n_max rows
+    torch.cuda.synchronize()
+    assert p.status_code() == 12 and ln.tolist() == [8, 10, 4]
