@@ -134,13 +134,30 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
 // Two values times the sigmoids of their gates, by the fast exponential and
 // divide (a few fp32 steps, far below the bf16 rounding that follows) with one
 // reciprocal for both, 1/a = b (1/ab): the special-function unit bounds the
-// epilogue.  e^-g is held below 2^63 so that the product stays finite (a gate
-// under -43.6 then leaves 1e-19 of x, not less).
+// epilogue.  e^-g is held at 2^62 so that the product stays in range; gates that
+// this would touch, under kNearGate or NaN, are seen to by far_gates.
+constexpr float kNearGate = -42.75f;  // the least bf16 with e^-g <= 2^62
 __device__ __forceinline__ f2_t gate2(f2_t x, uint32_t g) {
   float u, v;
   f2_unpack(f2_mul(f2_from_bf16x2(g), f2_dup(-1.4426950408889634f)), u, v);
-  f2_unpack(f2_add(f2_pack(ex2_approx(fminf(u, 63.f)), ex2_approx(fminf(v, 63.f))), f2_dup(1.f)), u, v);
+  f2_unpack(f2_add(f2_pack(ex2_approx(fminf(u, 62.f)), ex2_approx(fminf(v, 62.f))), f2_dup(1.f)), u, v);
   return f2_mul(x, f2_mul(f2_dup(rcp_approx(__fmul_rn(u, v))), f2_pack(v, u)));
+}
+// The smaller of each half of two bf16 pairs, NaN where either is.
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// For gates that are not near: columns of O, before they are read out, times what
+// such a gate has beyond gate2's factor of 2^-62: 2^62 sigmoid(g), or NaN.
+static __device__ __noinline__ void far_gates(uint32_t o, const __nv_bfloat16* gate, int cols, bool act) {
+  for (int c = 0; c < cols; c++) {
+    const float x = tmem_ld1(o + c), g = act ? __bfloat162float(gate[c]) : 0.f;
+    tmem_st1(o + c, g >= kNearGate ? x : __fmul_rn(gate_mul(x, g), 0x1p62f));
+    __syncwarp();
+  }
+  tmem_st_wait();
 }
 __device__ __forceinline__ uint32_t bf16_of(f2_t x) {
   float a, b;
@@ -523,17 +540,17 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
     const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t patch = pbuf + hf * (C::TURNS ? C::PT : 16384) + quad * 4096;  // where this warp writes P: 4 KB of its own between items
     const int tok = lrow / p.G, head = lrow % p.G;
-    uint32_t t = 0, xc = 0, it = 0;  // tiles, exchanges, units before the item
+    uint32_t t = 0, it = 0, id = 0;  // tiles, units before the item, items (this one counted)
     bool ok = true;
     // the two threads of a row exchange a value
     auto exchange = [&](float v, float& other) {
-      float* x = xmax + (C::TURNS ? 0 : xc & 1) * 256;  // (turns: once an item, with QREADY between)
+      const uint32_t xc = C::TURNS ? id - 1 : t + id - 1;  // exchanges before: one an item (turns), or one a tile too
+      float* x = xmax + (C::TURNS ? 0 : xc & 1) * 256;      // (turns: QREADY lies between two)
       x[hf * 128 + lrow] = v;
       __syncwarp();
       if (lane == 0) mbar_arrive(XBAR0 + 8u * quad);
       if (!wait_warp(XBAR0 + 8u * quad, xc & 1, abort_flag, kWaitCycles)) return false;
       other = x[(hf ^ 1) * 128 + lrow];
-      xc++;
       return true;
     };
     // this thread's row of q and out of an item (elements); kNoRow: none
@@ -543,12 +560,11 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
     };
     // Q of an item into tensor memory, each thread its half of its row, once
     // every Q K^T of the item before has completed (its last S has been read)
-    uint32_t qt = 0;
     auto load_q = [&]() {
       if (hf < C::QH) {
 #pragma unroll
-        for (int r = 0; r < C::QR; r++, qt++) {
-          if (!wait_warp(QFULL0 + 8u * hf, qt & 1, abort_flag, kWaitCycles)) return false;
+        for (int r = 0; r < C::QR; r++) {
+          if (!wait_warp(QFULL0 + 8u * hf, (id * C::QR + r) & 1, abort_flag, kWaitCycles)) return false;
           uint32_t v[32];
 #pragma unroll
           for (int i = 0; i < 8; i++) {
@@ -577,9 +593,8 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
       orow = row_of(I);
       ok = load_q();
     }
-    // met[id & 1] = id: item id met a value to zero.  (A warp may be an item
-    // ahead of another, not two: their P arrivals hold them together.)
-    uint16_t id = 0;
+    // met[id & 1] = id (its low bits): item id met a value to zero.  (A warp may be
+    // an item ahead of another, not two: their P arrivals hold them together.)
     while (ok && more) {
       id++;
       const int n = I.t1 - I.t0, L = pl.L[I.s], end = L + pl.n[I.s];
@@ -618,7 +633,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
             const uint4 v = ld_shared16(at(row));
             st_shared16(at(row), make_uint4(v.x & finite2(v.x), v.y & finite2(v.y), v.z & finite2(v.z), v.w & finite2(v.w)));
           }
-          met[id & 1] = id;
+          met[id & 1] = static_cast<uint16_t>(id);
         }
         return true;
       };
@@ -878,6 +893,14 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
       } else {
 #pragma unroll 1
         for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += CW) {
+          if (p.gate) {  // one look at all of the warp's gates of these columns
+            uint32_t least = min_nan2(gv[0].x, gv[0].y);
+#pragma unroll
+            for (int i = 0; i < Q; i++)
+              least = min_nan2(least, min_nan2(min_nan2(gv[i].x, gv[i].y), min_nan2(gv[i].z, gv[i].w)));
+            if (__any_sync(0xffffffffu, !(bf16_lo(least) >= kNearGate && bf16_hi(least) >= kNearGate)))
+              far_gates(tl + C::T_O + c, p.gate + row + c, CW, row >= 0);
+          }
           f2_t y[CW / 2];
           const f2_t inv2 = f2_dup(inv);
 #pragma unroll
@@ -925,7 +948,7 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
         tc_fence_before();
         arrive(OFREE);
       }
-      if (met[id & 1] == id) {
+      if (met[id & 1] == static_cast<uint16_t>(id)) {
         __syncwarp();
         const PromptItem J = item_of(p, pl, piece_index(mine - 1, worker, p.workers));  // this item again
         const int before = pl.L[J.s] + J.i * p.T + 1;  // seen by all rows
@@ -1017,8 +1040,10 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
       for (int e = 0; e < 4; e++) acc[e] = __fmul_rn(acc[e], inv);
       if (p.gate) {
         const uint2 gv = *reinterpret_cast<const uint2*>(p.gate + at_o);
-        f2_unpack(gate2(f2_pack(acc[0], acc[1]), gv.x), acc[0], acc[1]);
-        f2_unpack(gate2(f2_pack(acc[2], acc[3]), gv.y), acc[2], acc[3]);
+        acc[0] = gate_mul(acc[0], bf16_lo(gv.x));
+        acc[1] = gate_mul(acc[1], bf16_hi(gv.x));
+        acc[2] = gate_mul(acc[2], bf16_lo(gv.y));
+        acc[3] = gate_mul(acc[3], bf16_hi(gv.y));
       }
       *reinterpret_cast<uint2*>(p.out + at_o) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
     }

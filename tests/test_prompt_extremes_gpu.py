@@ -1,0 +1,75 @@
+"""Infinities, NaN and far values in a prompt's rows and caches, told apart: what
+comes out is NaN, +inf or -inf where the definition gives that, and as if the rest
+were alone elsewhere.  Bounds as in test_prompt_gpu.py."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import oracle.prompt as OP
+from tests.test_prompt_gpu import BF, F32, NAN, U, Attn
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def same(got, ref, bound, what):
+    """NaN and each infinity where ref has it, within the bound elsewhere."""
+    got = got.double()
+    for name, f in (("nan", torch.isnan), ("+inf", torch.isposinf), ("-inf", torch.isneginf)):
+        bad = f(got) != f(ref)
+        assert not bool(bad.any()), f"{what}: {name} differs at {bad.nonzero()[0].tolist()} ({int(bad.sum())} places)"
+    fin = torch.isfinite(ref)
+    over = torch.where(fin, (got - ref).abs() - bound, torch.full_like(ref, -1.0))
+    assert float(over.max()) <= 0, f"{what}: {float(over.max()):.3e} over its bound"
+
+
+def check_attn(a, what=""):
+    """The call's outputs against the definition, non-finite places told apart."""
+    torch.cuda.synchronize()
+    assert a.prompt.status_code() == 0
+    off = 0
+    for s, (L, n) in enumerate(zip(a.ctx, a.rows)):
+        g = None if a.gate is None else a.gate[off:off + n]
+        ref, _ = OP.attn_prompt(a.K[s], a.V[s], L, a.q[off:off + n], a.scale, g)
+        # a weight of 0 must not meet an unseen value: the definition over each row's own prefix
+        V = a.V[s][:, :L + n].double()
+        if not bool(torch.isfinite(V).all()):
+            fin = torch.where(torch.isfinite(V), V, torch.zeros_like(V))
+            ref, _ = OP.attn_prompt(a.K[s], fin, L, a.q[off:off + n], a.scale)
+            G = ref.shape[1] // V.shape[0]
+            seen = lambda x: (x.cumsum(1) > 0)[:, L:].transpose(0, 1).repeat_interleave(G, 1)
+            nan, pos, neg = seen(torch.isnan(V)), seen(torch.isposinf(V)), seen(torch.isneginf(V))
+            ref = torch.where(pos, ref + INF, ref)
+            ref = torch.where(neg, ref - INF, ref)
+            ref = torch.where(nan, ref + NAN, ref)
+            if g is not None:
+                ref = ref * torch.sigmoid(g.double())
+        fin = torch.where(torch.isfinite(V), V, torch.zeros_like(V))
+        _, reach = OP.attn_prompt(torch.nan_to_num(a.K[s][:, :L + n]), fin, L, torch.nan_to_num(a.q[off:off + n]), a.scale)
+        if g is not None:
+            reach = reach * torch.nan_to_num(torch.sigmoid(g.double()))
+        noise, u = (4e-4, U[BF]) if a.dtype == BF else (8e-5, U[F32])
+        same(a.out[off:off + n], ref, 2 * u * torch.nan_to_num(ref, 0, 0, 0).abs() + (u + noise) * reach + 1e-30,
+             f"{what} sequence {s}")
+        off += n
+
+
+LAYOUTS = [(24, 4, 256, BF), (4, 4, 64, BF), (16, 2, 128, BF), (6, 2, 64, F32)]
+BATCHES = [([150, 40], [30, 0]), ([24], [20000]), ([3, 70], [126, 5]), ([1], [400])]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", LAYOUTS)
+@pytest.mark.parametrize("rows,ctx", BATCHES)
+def test_attn_prompt_far_gates(Hq, Hkv, D, dtype, rows, ctx):
+    """Whole and split items: gates that are NaN, infinite or far out, each beside finite ones."""
+    a = Attn(rows, ctx, Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, gate=True, seed=41)
+    n = sum(rows)
+    for i, x in enumerate([NAN, INF, -INF, -50.0, -100.0, 100.0, -44.0, 3e38, -3e38]):
+        for c in (2 * i, D - 1 - 2 * i):  # the pair's other half stays as it was
+            a.gate[(7 * i) % n, i % Hq, c] = x
+    a.gate[n - 1, Hq - 1, D // 2], a.gate[n - 1, Hq - 1, D // 2 + 1] = -INF, -INF
+    a.gate[n - 1, 0, D // 2], a.gate[n - 1, 0, D // 2 + 1] = -60.0, -61.0
+    a.run()
+    check_attn(a)
