@@ -197,6 +197,17 @@ static __device__ __noinline__ void put_nonfinite(const __nv_bfloat16* v, int st
   }
 }
 
+// Zeroes the values that are not finite in rows row, row + step, .. below `to` of a
+// value tile, a 16-byte piece of a row a lane; b0, b1: its units.
+template <int VROWS>
+static __device__ __noinline__ void zero_nonfinite(uint32_t b0, uint32_t b1, int row, int step, int to) {
+  for (; row < to; row += step) {
+    const uint32_t a = (row >= VROWS ? b1 : b0) + (row % VROWS) * 128;
+    const uint4 v = ld_shared16(a);
+    st_shared16(a, make_uint4(v.x & finite2(v.x), v.y & finite2(v.y), v.z & finite2(v.z), v.w & finite2(v.w)));
+  }
+}
+
 // The first row that is loaded for the key tile at position pos: a tile that
 // would reach past the rows the sequence holds (the cache may end there, or its
 // pages) is taken from further up, and the positions before pos in it are masked.
@@ -635,6 +646,11 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
           }
           met[id & 1] = static_cast<uint16_t>(id);
         }
+        // a tile taken from further up: rows before `pos` have no weight here, whoever
+        // sees them (they count in the tile before)
+        const int again = pos - tile_row(pos, end);
+        if (again > 0)
+          zero_nonfinite<C::VROWS>(at(0), at(C::VROWS % kKeyTile), row0 - first, (C::TURNS ? 4 : 8) * RPW, again);
         return true;
       };
       if constexpr (C::TURNS) {

@@ -73,3 +73,18 @@ def test_attn_prompt_far_gates(Hq, Hkv, D, dtype, rows, ctx):
     a.gate[n - 1, 0, D // 2], a.gate[n - 1, 0, D // 2 + 1] = -60.0, -61.0
     a.run()
     check_attn(a)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", LAYOUTS)
+@pytest.mark.parametrize("rows,ctx", [([40], [500]), ([150, 9], [300, 400]), ([24], [20000]), ([1], [129]), ([200], [0]), ([3, 60], [254, 70])])
+def test_attn_prompt_infinities_ahead_of_the_last_tile(Hq, Hkv, D, dtype, rows, ctx):
+    """Infinities just before the last 128-position boundary, which a last tile that is not
+    whole may load again: they come out as they are, not as NaN."""
+    a = Attn(rows, ctx, Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, seed=43)
+    for s, (L, n) in enumerate(zip(ctx, rows)):
+        edge = (L + n - 1) // 128 * 128
+        for c, back, x in ((0, 1, INF), (1, 1, -INF), (2, 1, NAN), (3, 9, INF), (D - 1, 30, -INF)):
+            if edge - back >= 0:
+                a.V[s][c % Hkv, edge - back, c] = x
+    a.run()
+    check_attn(a)
