@@ -35,7 +35,7 @@
 // would still meet the value: in a tile that some row here does not see whole,
 // values that are not finite are zeroed in shared memory before its PV (one look
 // at the tile, 16 KB a warp at most), and the rows that do see them take them
-// in afterwards, from the cache (put_nonfinite).
+// in afterwards, from the cache (add_nonfinite).
 //
 // Work split.  All CTAs derive the same plan from the device-side offsets and
 // lengths: items in order of falling length, dealt back and forth over the
@@ -179,22 +179,19 @@ __device__ __forceinline__ uint32_t times_zero_plus(uint32_t x, uint32_t acc) { 
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
   return r;
 }
-// The columns in which one of value rows [from, to) is not finite get the sum of
-// those that are not: into a piece's record, or else into the output row.
-static __device__ __noinline__ void put_nonfinite(const __nv_bfloat16* v, int stride, int cols, int from, int to, float* rec,
-                                                  __nv_bfloat16* out) {
+// Columns of O, before they are read out, plus the values of rows [from, to) that
+// are not finite (their weights, all above zero, change nothing).
+static __device__ __noinline__ void add_nonfinite(uint32_t o, const __nv_bfloat16* v, int stride, int cols, int from, int to) {
   for (int c = 0; c < cols; c++) {
-    float sum = 0.f;
-    bool any = false;
+    float x = tmem_ld1(o + c);
     for (int t = from; t < to; t++) {
-      const float x = __bfloat162float(v[static_cast<size_t>(t) * stride + c]);
-      if (isfinite(x)) continue;
-      sum = __fadd_rn(sum, x);
-      any = true;
+      const float y = __bfloat162float(v[static_cast<size_t>(t) * stride + c]);
+      if (!isfinite(y)) x = __fadd_rn(x, y);
     }
-    if (any && rec) rec[c] = sum;
-    else if (any) out[c] = __float2bfloat16_rn(sum);
+    __syncwarp();
+    tmem_st1(o + c, x);
   }
+  tmem_st_wait();
 }
 
 // Zeroes the values that are not finite in rows row, row + step, .. below `to` of a
@@ -880,6 +877,12 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
         break;
       }
       tc_fence_after();
+      if (met[id & 1] == static_cast<uint16_t>(id)) {
+        const PromptItem J = item_of(p, pl, piece_index(mine - 1, worker, p.workers));  // this item again
+        const int before = pl.L[J.s] + J.i * p.T + 1;  // seen by all rows
+        add_nonfinite(tl + C::T_O + hf * (D / 2), p.V[J.s] + static_cast<size_t>(J.g) * p.pr.cap * D + hf * (D / 2), D, D / 2,
+                      max(before, J.t0 * kKeyTile), row >= 0 ? min(before + tok, J.t1 * kKeyTile) : 0);
+      }
       const float inv = __fdiv_rn(1.f, __fadd_rn(l, lo));
       // Rows leave through this warp's patch, where they are turned around so
       // that an instruction covers whole pieces of rows.
@@ -963,16 +966,6 @@ __global__ void __launch_bounds__(384, 1) attn_prompt_tc_kernel(const __grid_con
       if (C::TURNS) {
         tc_fence_before();
         arrive(OFREE);
-      }
-      if (met[id & 1] == static_cast<uint16_t>(id)) {
-        __syncwarp();
-        const PromptItem J = item_of(p, pl, piece_index(mine - 1, worker, p.workers));  // this item again
-        const int before = pl.L[J.s] + J.i * p.T + 1;  // seen by all rows
-        const int end = min(before + tok, J.t1 * kKeyTile);
-        put_nonfinite(p.V[J.s] + static_cast<size_t>(J.g) * p.pr.cap * D + hf * (D / 2), D, D / 2, max(before, J.t0 * kKeyTile),
-                      row >= 0 ? end : 0,
-                      slot >= 0 ? p.ws + (static_cast<size_t>(slot) * 128 + lrow) * (D + 4) + hf * (D / 2) : nullptr,
-                      p.out + row + hf * (D / 2));
       }
       tc_fence_before();
     }

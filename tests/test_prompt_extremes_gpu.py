@@ -88,3 +88,29 @@ def test_attn_prompt_infinities_ahead_of_the_last_tile(Hq, Hkv, D, dtype, rows, 
                 a.V[s][c % Hkv, edge - back, c] = x
     a.run()
     check_attn(a)
+
+
+MEET = [([40], [500]), ([150, 9], [300, 400]), ([24], [20000])]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", LAYOUTS)
+@pytest.mark.parametrize("rows,ctx", MEET)
+@pytest.mark.parametrize("gate", [False, True])
+def test_attn_prompt_values_meet(Hq, Hkv, D, dtype, rows, ctx, gate):
+    """Infinities of both signs and NaN, some seen by all rows, some by the later ones, in one column."""
+    a = Attn(rows, ctx, Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, gate=gate, seed=42)
+    for s, (L, n) in enumerate(zip(ctx, rows)):
+        V = a.V[s]
+        for c, early, late in ((0, -INF, INF), (1, NAN, INF), (2, INF, INF), (3, INF, -INF), (D - 1, INF, None), (D - 2, None, -INF)):
+            if early is not None:
+                V[c % Hkv, 3, c] = early
+            if late is not None:
+                V[c % Hkv, L + n // 3, c] = late
+        V[0, L + n - 1, 5], V[0, L + n // 2, 5] = -INF, INF
+    a.q[rows[0] - 1, 0, 7] = NAN  # a row of one head, whatever its values are
+    if gate:
+        a.gate[:, :, 2] = -INF  # 0 times an infinity
+        a.gate[rows[0] // 2:, :, D - 2] = NAN
+        a.gate[:, :, 3] = INF
+    a.run()
+    check_attn(a)
