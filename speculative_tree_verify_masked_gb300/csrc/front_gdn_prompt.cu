@@ -58,15 +58,13 @@ struct Row8<float> {
   __device__ __forceinline__ f2_t pair(int i) const { return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? b.x : b.y; }
 };
 
-// SiLU of a pair, x / (1 + e^-x), with one reciprocal for both (1/a = b (1/ab)):
-// the special-function unit comes close to bounding this kernel.  e^-x is held
-// below 2^63 so that the product stays finite; an x under -43.6 then gives
-// 1e-19 x instead of something smaller still.
+// SiLU of a pair, x / (1 + e^-x); from -87 on 0, from -inf NaN, as the library's
+// other paths have it.
 __device__ __forceinline__ f2_t silu2(f2_t x) {
-  float u, v;
-  f2_unpack(f2_mul(x, f2_dup(-1.4426950408889634f)), u, v);
-  f2_unpack(f2_add(f2_pack(ex2_approx(fminf(u, 63.f)), ex2_approx(fminf(v, 63.f))), f2_dup(1.f)), u, v);
-  return f2_mul(x, f2_mul(f2_dup(rcp_approx(__fmul_rn(u, v))), f2_pack(v, u)));
+  float a, b;
+  f2_unpack(f2_mul(x, f2_dup(-1.4426950408889634f)), a, b);
+  f2_unpack(f2_add(f2_pack(ex2_approx(a), ex2_approx(b)), f2_dup(1.f)), a, b);
+  return f2_mul(x, f2_pack(rcp_approx(a), rcp_approx(b)));
 }
 
 // What a width needs in registers: the window as a ring of RING rows (even for

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import oracle.prompt as OP
-from tests.test_prompt_gpu import BF, F32, NAN, U, Attn
+from tests.test_prompt_gpu import BF, F32, NAN, U, Attn, Front
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +114,38 @@ def test_attn_prompt_values_meet(Hq, Hkv, D, dtype, rows, ctx, gate):
         a.gate[:, :, 3] = INF
     a.run()
     check_attn(a)
+
+
+@pytest.mark.parametrize("Hk,Hv,d,dtype", [(4, 8, 128, BF), (2, 2, 64, F32), (3, 6, 64, BF)])
+@pytest.mark.parametrize("W", [1, 4, 5])
+def test_gdn_prompt_front_far_inputs(Hk, Hv, d, dtype, W):
+    """Infinities and far negative inputs beside ordinary ones: SiLU as the formula has it (x / (1 + e^-x),
+    NaN from -inf), pairs of channels apart from each other."""
+    rows = [37, 9]
+    f = Front(rows, Hk, Hv, d, W, dtype, seed=44)
+    Hc = 2 * Hk * d  # value channels: SiLU alone
+    f.w[Hc:] = 0
+    f.w[Hc:, W - 1] = 1.0  # the convolution of a value channel is its own row
+    far = [-INF, INF, NAN, -50.0, -60.0, -43.0, -44.0, -80.0, -88.0, -100.0, -1e30, 1e30]
+    for i, x in enumerate(far):
+        f.x[3 * i, Hc + 2 * i] = x
+        f.x[3 * i, Hc + d + 2 * i + 1] = x
+    f.x[1, Hc + 8:Hc + 16] = torch.tensor([-50, -60, -70, -44, 1, -45, -46, -80.0]).to(dtype)
+    old = [t.clone() for t in f.tails]
+    f.run()
+    torch.cuda.synchronize()
+    assert f.prompt.status_code() == 0
+    off = 0
+    for s, n in enumerate(rows):
+        sl = slice(off, off + n)
+        own = f.x[sl, Hc:].double().reshape(n, Hv, d)
+        ref = own / (1 + torch.exp(-own))
+        if W > 1:  # (0 times an infinity of a row before, in the window)
+            z = torch.cat([old[s], f.x[sl]])[:, Hc:].double()
+            ref = ref + sum(0.0 * z[j:j + n] for j in range(W - 1)).reshape(n, Hv, d)
+        # e^-x as 2^u, u = x log2(e): the product's rounding (2^-24 of u) and the constant's (2^-26, at most 2^-25
+        # of u) change 2^u by ln 2 |u| (2^-24 + 2^-25) = 1.5 |x| 2^-24 of itself; exponential, sum, reciprocal and
+        # products are within 16 steps
+        bound = torch.nan_to_num(ref, 0, 0, 0).abs() * (U[dtype] + 2.0 ** -20 + torch.nan_to_num(own, 0, 0, 0).abs() * 2.0 ** -23)
+        same(f.v[sl], ref, bound + 2.0 ** -119, "v")  # (sigmoids below 2^-126 are 0: at most 100 times that)
+        off += n
