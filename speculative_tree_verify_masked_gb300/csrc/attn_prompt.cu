@@ -169,7 +169,7 @@ template <int D, int RPW>
 static tv_status launch_cuda(const AttnPromptCudaParams& p, cudaStream_t st) {
   using C = Cuda<D, RPW>;
   const int64_t rows = static_cast<int64_t>(p.pr.n_max) * (p.Hq / p.Hkv);
-  const int64_t gx = (rows + C::ROWS - 1) / C::ROWS;
+  const int64_t gx = rows > 0 ? (rows + C::ROWS - 1) / C::ROWS : 1;  // (n_max 0: the checks alone)
   if (gx > 0x7fffffff || p.Hkv > 65535) return TV_ERR_SHAPE;
   static bool set = false;
   if (!set) {
