@@ -443,8 +443,9 @@ tv_status tv_prompt_advance(const tv_prompt* prompt, int32_t* len, tv_stream str
  *     x / sqrt(mean(x^2) + eps) * w,
  * with the fp32 weights q_norm [D] for query heads and k_norm [D] for key
  * heads, everything in fp32 and rounded once.  Both weights NULL: rotation
- * alone (eps is then not read).  tree, n_seq, len, max_len, status, aliasing
- * and errors as in tv_attn_rope; eps > 0 finite, weights 16-byte aligned.  A
+ * alone (eps is then not read).  tree, n_seq, len, max_len, status and errors
+ * as in tv_attn_rope; eps > 0 finite, weights 16-byte aligned; q may be q_raw and
+ * k k_raw, memory shared in any other way: TV_ERR_ARG.  A
  * row's bits depend only on its own values and its position: tree, decode and
  * prompt rows are equal bit for bit.  (tv_attn_rope forms its angles in fp64,
  * this call in 64-bit integer fractions of a turn: their results may differ
@@ -458,7 +459,8 @@ tv_status tv_attn_norm_rope(const tv_attn_layer* layer, const tv_tree* tree, int
  * queries go to q, keys (normalised, rotated) and values (bit copies) into
  * rows len[s] + i of the sequence's caches.
  *  q_raw [n_total][Hq][D], k_raw, v [n_total][Hkv][D]; q [n_total][Hq][D]
- *  (may alias q_raw).  The caches must not overlap the packed buffers. */
+ *  (may be q_raw; memory shared with it or k_raw or v in any other way: TV_ERR_ARG).
+ * The caches must not overlap the packed buffers. */
 tv_status tv_attn_prompt_front(const tv_attn_layer* layer, const tv_prompt* prompt, const int32_t* len,
                                int32_t max_len, const float* q_norm, const float* k_norm, float eps,
                                int32_t rot_dims, float theta, const void* q_raw, const void* k_raw, const void* v,

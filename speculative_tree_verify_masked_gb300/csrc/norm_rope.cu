@@ -319,6 +319,14 @@ static tv_status norm_rope_check(const tv_attn_layer* l, int32_t max_len, const 
   return TV_OK;
 }
 
+// Whether rows of `n` of these are formed in place or apart from the raw rows: a
+// warp writes heads of its row while others still read theirs.
+static bool in_place_or_apart(const tv_attn_layer* l, int64_t n, int Hout, const void* out, const void* own_raw, int Hother,
+                              const void* other_raw) {
+  const int64_t c = static_cast<int64_t>(Hout) * l->D, o = static_cast<int64_t>(Hother) * l->D;
+  return (out == own_raw || !overlap(out, own_raw, n, c, c, l->dtype)) && !overlap(out, other_raw, n, c, o, l->dtype);
+}
+
 }  // namespace tv
 
 using namespace tv;
@@ -347,6 +355,10 @@ extern "C" tv_status tv_attn_norm_rope(const tv_attn_layer* l, const tv_tree* t,
     p.n_rows = p.n_seq = n_seq;
     p.pr.status = status;
   }
+  if (!in_place_or_apart(l, p.n_rows, l->Hq, q, q_raw, l->Hkv, k_raw) ||
+      !in_place_or_apart(l, p.n_rows, l->Hkv, k, k_raw, l->Hq, q_raw) ||
+      overlap(q, k, p.n_rows, static_cast<int64_t>(l->Hq) * l->D, static_cast<int64_t>(l->Hkv) * l->D, l->dtype))
+    return TV_ERR_ARG;
   p.pr.len = len;
   p.max_len = max_len;
   p.q_raw = q_raw;
@@ -374,6 +386,9 @@ extern "C" tv_status tv_attn_prompt_front(const tv_attn_layer* l, const tv_promp
   if (pr->n_total == 0) return TV_OK;
   if (!q_raw || !k_raw || !v || !q) return TV_ERR_ARG;
   if (!aligned16(q_raw) || !aligned16(k_raw) || !aligned16(v) || !aligned16(q)) return TV_ERR_ALIGN;
+  if (!in_place_or_apart(l, pr->n_total, l->Hq, q, q_raw, l->Hkv, k_raw) ||
+      !in_place_or_apart(l, pr->n_total, l->Hq, q, q_raw, l->Hkv, v))
+    return TV_ERR_ARG;
   p.form = 2;
   p.pr = prompt_rows(pr, len, max_len, l->cap);
   p.n_rows = p.n_total = pr->n_total;

@@ -17,3 +17,24 @@ def test_span_call_refusals(L):  # noqa: F811
     assert L.tv_prompt_advance(ref(good_prompt()), vp(20), None) == 4
     assert L.tv_prompt_check(ref(good_prompt(0)), vp(16), 8, 64, None) == 0
     assert L.tv_prompt_advance(ref(good_prompt(0)), vp(16), None) == 0
+
+
+def test_norm_rope_shared_memory_refused(L):  # noqa: F811
+    """Rows formed in place, or apart from the raw ones: nothing between, before anything is launched."""
+    from tests.test_prompt_cpu import attn_layer
+
+    a, n = attn_layer(), 8
+    qb, kb = n * 24 * 256 * 2, n * 4 * 256 * 2  # bytes of the packed rows
+    Q, K, V, far = 1 << 24, 1 << 26, 1 << 27, 1 << 28
+
+    def prompt(q):
+        return L.tv_attn_prompt_front(ref(a), ref(good_prompt(n)), vp(16), 8, None, None, 0.0, 64, 1e7, vp(Q), vp(K), vp(V), vp(q), None)
+
+    for q in (Q + 16, Q - 16, Q + qb - 16, Q - qb + 16, K, K + kb - 16, K - qb + 16, V, V + 16):
+        assert prompt(q) == 1, hex(q)
+
+    def decode(q, k):
+        return L.tv_attn_norm_rope(ref(a), None, n, vp(16), 8, None, None, 0.0, 64, 1e7, vp(Q), vp(K), vp(q), vp(k), vp(16), None)
+
+    for q, k in ((Q + 16, far), (K, far), (far, K + 16), (far, Q + 512), (far, far + 16), (Q, Q), (K, Q)):
+        assert decode(q, k) == 1, (hex(q), hex(k))
