@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(128) attn_prompt_cuda_kernel(const __grid_cons
     for (int i = 0; i < RPW; i++) {
       const float mn = fmaxf(m[i], mx[i]);
       const float alpha = mn == m[i] ? 1.f : exp2f(__fsub_rn(m[i], mn));
-      const float pj = t0 + lane <= last[i] ? exp2f(__fsub_rn(sc[i], mn)) : 0.f;
+      // (every score so far -inf: weights of 0, not of -inf - -inf)
+      const float pj = t0 + lane <= last[i] ? exp2f(__fsub_rn(sc[i], mn == -INFINITY ? 0.f : mn)) : 0.f;
       pw[lane * RPW + i] = sum[i] = pj;
       l[i] = __fmul_rn(l[i], alpha);
       m[i] = mn;

@@ -149,3 +149,15 @@ def test_gdn_prompt_front_far_inputs(Hk, Hv, d, dtype, W):
         bound = torch.nan_to_num(ref, 0, 0, 0).abs() * (U[dtype] + 2.0 ** -20 + torch.nan_to_num(own, 0, 0, 0).abs() * 2.0 ** -23)
         same(f.v[sl], ref, bound + 2.0 ** -119, "v")  # (sigmoids below 2^-126 are 0: at most 100 times that)
         off += n
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", LAYOUTS)
+@pytest.mark.parametrize("rows,ctx,upto", [([40], [500], 33), ([40], [500], 130), ([40], [500], 510), ([70, 5], [0, 60], 40), ([24], [20000], 9000)])
+def test_attn_prompt_scores_of_minus_infinity(Hq, Hkv, D, dtype, rows, ctx, upto):
+    """Whole tiles and pieces of keys whose scores are -inf: no weight; a row that sees nothing else is NaN."""
+    a = Attn(rows, ctx, Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, seed=45)
+    a.q[:, :, 3] = a.q[:, :, 3].abs() + 0.1
+    for s in range(len(rows)):
+        a.K[s][0, :min(upto, ctx[s] + rows[s] - 1), 3] = -INF
+    a.run()
+    check_attn(a)
