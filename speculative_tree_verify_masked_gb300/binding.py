@@ -227,6 +227,11 @@ def _dtype_code(dt: torch.dtype) -> int:
     raise TypeError(f"unsupported dtype {dt}")
 
 
+def _alike(tensors, shape, dtype) -> bool:
+    """Whether each of a descriptor's tensors is contiguous GPU memory of this shape and dtype."""
+    return all(tuple(t.shape) == tuple(shape) and t.dtype is dtype and t.is_contiguous() and t.is_cuda for t in tensors)
+
+
 def _ptr_array(tensors):
     arr = (c_void_p * max(1, len(tensors)))()
     for i, t in enumerate(tensors):
@@ -268,6 +273,8 @@ class AttnLayer:
         self.K, self.V = list(K), list(V)
         Hkv, cap, D = self.K[0].shape
         self._k, self._v = _ptr_array(self.K), _ptr_array(self.V)
+        self.n_seq = min(len(self.K), len(self.V))
+        self.sound = _alike(self.K + self.V, self.K[0].shape, self.K[0].dtype)
         self.c = tv_attn_layer(_dtype_code(self.K[0].dtype), Hq, Hkv, D, cap, self._k, self._v)
 
 
@@ -278,6 +285,7 @@ class GdnLayer:
         self.S = list(S)
         Hv, dv, dk = self.S[0].shape
         self._s = _ptr_array(self.S)
+        self.n_seq, self.sound = len(self.S), _alike(self.S, self.S[0].shape, torch.float32)
         self.c = tv_gdn_layer(_dtype_code(dtype), Hk, Hv, dk, dv, self._s)
 
 
@@ -387,6 +395,9 @@ class GdnFrontLayer:
     def __init__(self, Hk: int, Hv: int, dk: int, dv: int, wconv, tails, dtype: torch.dtype):
         self.wconv, self.tails = wconv, list(tails)
         self._tail = _ptr_array(self.tails)
+        C, W = 2 * Hk * dk + Hv * dv, wconv.shape[1]
+        self.n_seq = len(self.tails)
+        self.sound = _alike([wconv], (C, W), torch.float32) and _alike(self.tails, (W - 1, C), dtype)
         self.c = tv_gdn_front_layer(_dtype_code(dtype), Hk, Hv, dk, dv, wconv.shape[1], _ptr(wconv), self._tail)
 
 
@@ -492,6 +503,15 @@ def _need(where: str, **tensors):
                              f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
+def _need_layer(where: str, layer, n_seq: int):
+    """Raises where a layer's caches, states or tails are fewer than the call's
+    sequences (the C side would read past its pointers) or not alike."""
+    if layer.n_seq < n_seq:
+        raise ValueError(f"{where}: {n_seq} sequences, but the layer holds {layer.n_seq}")
+    if not layer.sound:
+        raise ValueError(f"{where}: the layer's tensors must be contiguous GPU memory of one shape and dtype each")
+
+
 def _ws_bytes(ws) -> int:
     if ws is None:
         return 0
@@ -529,6 +549,7 @@ def tv_attn_norm_rope(layer: AttnLayer, tree: Tree | None, n_seq, len_, max_len,
 def tv_attn_prompt_front(layer: AttnLayer, prompt: Prompt, len_, max_len, q_norm, k_norm, eps, rot_dims, theta, q_raw,
                          k_raw, v, q, stream=None):
     """Head norms and rotation of a prompt's rows; keys and values go into the caches."""
+    _need_layer("tv_attn_prompt_front", layer, prompt.n_seq)
     c, dt, n = layer.c, layer.K[0].dtype, prompt.n_total
     nq, nk = n * c.Hq * c.D, n * c.Hkv * c.D
     _need("tv_attn_prompt_front", len=(len_, torch.int32, prompt.n_seq), q_norm=(q_norm, torch.float32, c.D),
@@ -545,6 +566,7 @@ def tv_attn_prompt_workspace_bytes(layer: AttnLayer, prompt: Prompt, max_len: in
 
 def tv_attn_prompt(layer: AttnLayer, prompt: Prompt, len_, max_len, q, gate, out, scale, ws, stream=None):
     """Causal attention of a prompt's rows over the caches that hold them."""
+    _need_layer("tv_attn_prompt", layer, prompt.n_seq)
     c, dt = layer.c, layer.K[0].dtype
     nq = prompt.n_total * c.Hq * c.D
     _need("tv_attn_prompt", len=(len_, torch.int32, prompt.n_seq), q=(q, dt, nq), gate=(gate, dt, nq),
@@ -559,6 +581,7 @@ def tv_gdn_prompt_workspace_bytes(layer: GdnLayer, prompt: Prompt) -> int:
 
 def tv_gdn_prompt(layer: GdnLayer, prompt: Prompt, q, k, v, alpha, beta, out, scale, ws, stream=None):
     """The gated delta rule over a prompt's rows; the states advance in place."""
+    _need_layer("tv_gdn_prompt", layer, prompt.n_seq)
     c, n = layer.c, prompt.n_total
     dt = torch.bfloat16 if c.dtype == TV_BF16 else torch.float32
     nk, nv, nh = n * c.Hk * c.dk, n * c.Hv * c.dv, n * c.Hv
@@ -571,6 +594,7 @@ def tv_gdn_prompt(layer: GdnLayer, prompt: Prompt, q, k, v, alpha, beta, out, sc
 
 def tv_gdn_prompt_front(layer: GdnFrontLayer, prompt: Prompt, x, a_raw, b_raw, q, k, v, alpha, beta, stream=None):
     """The GDN front end over a prompt's rows; the convolution tails advance."""
+    _need_layer("tv_gdn_prompt_front", layer, prompt.n_seq)
     c, n = layer.c, prompt.n_total
     dt = torch.bfloat16 if c.dtype == TV_BF16 else torch.float32
     nk, nv, nh = n * c.Hk * c.dk, n * c.Hv * c.dv, n * c.Hv
