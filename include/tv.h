@@ -474,7 +474,8 @@ size_t tv_attn_prompt_workspace_bytes(const tv_attn_layer* layer, const tv_promp
  * sees cache rows 0 .. len[s] + i, its own included (tv_attn_prompt_front has
  * put the prompt's rows there).
  *  q, out [n_total][Hq][D] in the layer's dtype (memory shared by q and out: TV_ERR_ARG)
- *  gate   [n_total][Hq][D], applied as in tv_attn_tree_verify_gated, or NULL
+ *  gate   [n_total][Hq][D], applied as in tv_attn_tree_verify_gated, or NULL (may
+ *         be out; memory shared with it in any other way: TV_ERR_ARG)
  *  scale  score scale > 0
  *  workspace device scratch of at least tv_attn_prompt_workspace_bytes() bytes,
  *         not shared with work that can run at the same time
@@ -493,7 +494,7 @@ size_t tv_gdn_prompt_workspace_bytes(const tv_gdn_layer* layer, const tv_prompt*
  * tv_gdn_tree_verify, row after row from the sequence's state, which is left
  * advanced by all of them (a sequence without rows keeps its state).
  *  q, k [n_total][Hk][dk]; v [n_total][Hv][dv]; alpha, beta fp32 [n_total][Hv]
- *  out  [n_total][Hv][dv] (memory shared with q, k or v: TV_ERR_ARG); scale output scale > 0
+ *  out  [n_total][Hv][dv] (memory shared with an input: TV_ERR_ARG); scale output scale > 0
  *  workspace as in tv_attn_prompt. */
 tv_status tv_gdn_prompt(const tv_gdn_layer* layer, const tv_prompt* prompt, const void* q, const void* k,
                         const void* v, const float* alpha, const float* beta, void* out, float scale,
@@ -503,7 +504,8 @@ tv_status tv_gdn_prompt(const tv_gdn_layer* layer, const tv_prompt* prompt, cons
  * and continues into its tail; unlike there the tails then advance to the
  * last W-1 raw inputs (a prompt's rows are committed as they are read).
  * Arguments as in tv_gdn_front with n_total rows, every pointer (wconv and
- * tails too) 16-byte aligned; memory shared by x and q, k or v: TV_ERR_ARG. */
+ * tails too) 16-byte aligned; memory shared by inputs and outputs: TV_ERR_ARG,
+ * but alpha and beta may be a_raw and b_raw. */
 tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* layer, const tv_prompt* prompt, const void* x,
                               const float* a_raw, const float* b_raw, void* q, void* k, void* v, float* alpha,
                               float* beta, tv_stream stream);

@@ -237,6 +237,7 @@ extern "C" tv_status tv_attn_prompt(const tv_attn_layer* l, const tv_prompt* pr,
   if (!aligned16(q) || !aligned16(gate) || !aligned16(out)) return TV_ERR_ALIGN;
   const int64_t cols = static_cast<int64_t>(l->Hq) * l->D;
   if (overlap(q, out, pr->n_total, cols, cols, l->dtype)) return TV_ERR_ARG;  // a row's heads are read after others are written
+  if (gate && gate != out && overlap(gate, out, pr->n_total, cols, cols, l->dtype)) return TV_ERR_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (l->dtype == TV_BF16)
     return attn_prompt_tc_launch(AttnPromptCall{l, pr, len, max_len, q, gate, out, scale, ws, ws_bytes}, st);

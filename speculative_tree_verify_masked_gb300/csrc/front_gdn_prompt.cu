@@ -295,9 +295,18 @@ extern "C" tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* f, const tv_p
       !aligned16(alpha) || !aligned16(beta) || !aligned16(f->wconv))
     return TV_ERR_ALIGN;
   const int64_t kc = static_cast<int64_t>(f->Hk) * f->dk, vc = static_cast<int64_t>(f->Hv) * f->dv, C = 2 * kc + vc;
-  if (overlap(x, q, pr->n_total, C, kc, f->dtype) || overlap(x, k, pr->n_total, C, kc, f->dtype) ||
-      overlap(x, v, pr->n_total, C, vc, f->dtype))
+  const int64_t n = pr->n_total, hv = f->Hv;
+  if (overlap(x, q, n, C, kc, f->dtype) || overlap(x, k, n, C, kc, f->dtype) || overlap(x, v, n, C, vc, f->dtype))
     return TV_ERR_ARG;  // a row is read again by the rows after it
+  const float* const raw[2] = {a_raw, b_raw};
+  float* const gates[2] = {alpha, beta};
+  for (int i = 0; i < 2; i++) {  // (gates may be formed in place: a thread reads its two raw values first)
+    if (overlap(raw[i], q, n, hv, kc, TV_F32, f->dtype) || overlap(raw[i], k, n, hv, kc, TV_F32, f->dtype) ||
+        overlap(raw[i], v, n, hv, vc, TV_F32, f->dtype) || overlap(gates[i], x, n, hv, C, TV_F32, f->dtype))
+      return TV_ERR_ARG;
+    for (int j = 0; j < 2; j++)
+      if (raw[i] != gates[j] && overlap(raw[i], gates[j], n, hv, hv, TV_F32)) return TV_ERR_ARG;
+  }
   p.pr = prompt_rows(pr, nullptr, 0, 0);
   p.x = x; p.a_raw = a_raw; p.b_raw = b_raw; p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.beta = beta;
   p.wconv = f->wconv;

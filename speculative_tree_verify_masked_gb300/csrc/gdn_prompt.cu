@@ -170,7 +170,8 @@ extern "C" tv_status tv_gdn_prompt(const tv_gdn_layer* l, const tv_prompt* pr, c
     return TV_ERR_ALIGN;
   const int64_t kc = static_cast<int64_t>(l->Hk) * l->dk, vc = static_cast<int64_t>(l->Hv) * l->dv;
   if (overlap(v, out, pr->n_total, vc, vc, l->dtype) || overlap(q, out, pr->n_total, kc, vc, l->dtype) ||
-      overlap(k, out, pr->n_total, kc, vc, l->dtype))
+      overlap(k, out, pr->n_total, kc, vc, l->dtype) || overlap(alpha, out, pr->n_total, l->Hv, vc, TV_F32, l->dtype) ||
+      overlap(beta, out, pr->n_total, l->Hv, vc, TV_F32, l->dtype))
     return TV_ERR_ARG;  // other heads and blocks still read them
   p.pr = prompt_rows(pr, nullptr, 0, 0);
   p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.beta = beta; p.out = out;

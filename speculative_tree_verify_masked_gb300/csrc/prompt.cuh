@@ -71,10 +71,14 @@ inline bool prompt_ok(const tv_prompt* p) {
          p->n_max >= 0 && p->n_max <= p->n_total && p->row_off && p->status && aligned16(p->row_off) &&
          aligned16(p->status);
 }
-// Whether [n][cols] values of type dt at a and [n][cols2] at b share memory.
+// Whether [n][cols] values of type dt at a and [n][cols2] of type dt2 at b share memory.
+inline bool overlap(const void* a, const void* b, int64_t n, int64_t cols, int64_t cols2, int32_t dt, int32_t dt2) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(n * cols2) * (dt2 == TV_BF16 ? 2 : 4) &&
+         y < x + static_cast<uintptr_t>(n * cols) * (dt == TV_BF16 ? 2 : 4);
+}
 inline bool overlap(const void* a, const void* b, int64_t n, int64_t cols, int64_t cols2, int32_t dt) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b), w = dt == TV_BF16 ? 2 : 4;
-  return x < y + static_cast<uintptr_t>(n * cols2) * w && y < x + static_cast<uintptr_t>(n * cols) * w;
+  return overlap(a, b, n, cols, cols2, dt, dt);
 }
 inline PromptRows prompt_rows(const tv_prompt* p, const int32_t* len, int max_len, int cap) {
   return PromptRows{p->row_off, len, p->status, p->n_seq, p->n_total, p->n_max, max_len, cap};

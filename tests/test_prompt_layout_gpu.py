@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from speculative_tree_verify_masked_gb300 import binding as B
-from tests.test_prompt_gpu import BF, F32, gen_of, rnd
+from tests.test_prompt_gpu import BF, F32, Attn, Front, gen_of, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,29 @@ def test_norm_rope_in_place_and_side_by_side(dtype):
     for out in (q.view(n, Hq, D), views[0]):  # ahead of the raw rows, then over them
         for a, b in zip(ref, run(*views, out)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D", [(F32, 6, 2, 64), (BF, 24, 4, 256), (BF, 16, 2, 128)])
+@pytest.mark.parametrize("rows,ctx", [([90, 40], [30, 200]), ([24], [20000])])
+def test_attn_prompt_gate_in_place(dtype, Hq, Hkv, D, rows, ctx):
+    """The output over its own gates, far ones among them."""
+    a, b = (Attn(rows, ctx, Hq, Hkv, D, dtype, gate=True, seed=82) for _ in range(2))
+    for x in (a, b):
+        x.gate[3, 1, ::9] = -70.0
+        x.gate[4, 0, 5] = float("-inf")
+    b.out = b.gate
+    a.run()
+    b.run()
+    torch.cuda.synchronize()
+    assert a.prompt.status_code() == b.prompt.status_code() == 0
+    assert torch.equal(a.out, b.out)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_gdn_prompt_front_gates_in_place(dtype):
+    a, b = (Front([70, 5], 2, 4, 64, 4, dtype, seed=83) for _ in range(2))
+    b.alpha, b.beta = b.b, b.a  # crossed over, even
+    a.run()
+    b.run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a.outs(), b.outs()))

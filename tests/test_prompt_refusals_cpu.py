@@ -38,3 +38,28 @@ def test_norm_rope_shared_memory_refused(L):  # noqa: F811
 
     for q, k in ((Q + 16, far), (K, far), (far, K + 16), (far, Q + 512), (far, far + 16), (Q, Q), (K, Q)):
         assert decode(q, k) == 1, (hex(q), hex(k))
+
+
+def test_gates_and_shared_memory_refused(L):  # noqa: F811
+    import ctypes
+
+    from speculative_tree_verify_masked_gb300 import binding as B
+    from tests.test_prompt_cpu import attn_layer
+
+    a, n, far = attn_layer(), 8, 1 << 30
+    rows = n * 24 * 256 * 2
+    for gate in (far + 16, far - 16, far + rows - 16, far - rows + 16):
+        assert L.tv_attn_prompt(ref(a), ref(good_prompt(n)), vp(16), 8, vp(1 << 20), vp(gate), vp(far), 0.1, None, 0, None) == 1
+    g = B.tv_gdn_layer(B.TV_BF16, 4, 8, 128, 128, (ctypes.c_void_p * 8)(*[0x3000] * 8))
+    q, k, v = 1 << 20, 2 << 20, 3 << 20
+    for al, be in ((far, 5 << 20), (5 << 20, far + 16), (far - n * 8 * 4 + 16, 5 << 20), (far + n * 8 * 128 * 2 - 16, 5 << 20)):
+        assert L.tv_gdn_prompt(ref(g), ref(good_prompt(n)), vp(q), vp(k), vp(v), vp(al), vp(be), vp(far), 0.1, None, 0, None) == 1
+    f = B.tv_gdn_front_layer(B.TV_BF16, 4, 8, 128, 128, 4, 0x2000, (ctypes.c_void_p * 8)(*[0x3000] * 8))
+    x, ar, br, al, be = far, 5 << 20, 6 << 20, 7 << 20, 8 << 20
+
+    def front(x=x, ar=ar, br=br, q=q, k=k, v=v, al=al, be=be):
+        return L.tv_gdn_prompt_front(ref(f), ref(good_prompt(n)), *map(vp, (x, ar, br, q, k, v, al, be)), None)
+
+    for kw in (dict(ar=q), dict(br=k + 16), dict(ar=v), dict(al=x), dict(be=x + 16), dict(al=ar + 16), dict(be=ar - 16),
+               dict(al=br + 16), dict(be=br + 32)):
+        assert front(**kw) == 1, kw
