@@ -185,10 +185,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _current_gpu() -> int:
+    return torch._C._cuda_getDevice()
+
+
 def _stream(stream):
     if stream is None:
         # the current stream's handle without building a Stream object (a small call's largest host cost)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_current_gpu())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -228,8 +232,10 @@ def _dtype_code(dt: torch.dtype) -> int:
 
 
 def _alike(tensors, shape, dtype) -> bool:
-    """Whether each of a descriptor's tensors is contiguous GPU memory of this shape and dtype."""
-    return all(tuple(t.shape) == tuple(shape) and t.dtype is dtype and t.is_contiguous() and t.is_cuda for t in tensors)
+    """Whether each of a descriptor's tensors is contiguous memory of one GPU, of this shape and dtype."""
+    gpu = tensors[0].get_device() if tensors else 0
+    return gpu >= 0 and all(tuple(t.shape) == tuple(shape) and t.dtype is dtype and t.is_contiguous() and
+                            t.get_device() == gpu for t in tensors)
 
 
 def _ptr_array(tensors):
@@ -275,6 +281,7 @@ class AttnLayer:
         self._k, self._v = _ptr_array(self.K), _ptr_array(self.V)
         self.n_seq = min(len(self.K), len(self.V))
         self.sound = _alike(self.K + self.V, self.K[0].shape, self.K[0].dtype)
+        self.gpu = self.K[0].get_device()
         self.c = tv_attn_layer(_dtype_code(self.K[0].dtype), Hq, Hkv, D, cap, self._k, self._v)
 
 
@@ -286,6 +293,7 @@ class GdnLayer:
         Hv, dv, dk = self.S[0].shape
         self._s = _ptr_array(self.S)
         self.n_seq, self.sound = len(self.S), _alike(self.S, self.S[0].shape, torch.float32)
+        self.gpu = self.S[0].get_device()
         self.c = tv_gdn_layer(_dtype_code(dtype), Hk, Hv, dk, dv, self._s)
 
 
@@ -397,7 +405,9 @@ class GdnFrontLayer:
         self._tail = _ptr_array(self.tails)
         C, W = 2 * Hk * dk + Hv * dv, wconv.shape[1]
         self.n_seq = len(self.tails)
-        self.sound = _alike([wconv], (C, W), torch.float32) and _alike(self.tails, (W - 1, C), dtype)
+        self.gpu = wconv.get_device()
+        self.sound = _alike([wconv], (C, W), torch.float32) and _alike(self.tails, (W - 1, C), dtype) and all(
+            t.get_device() == self.gpu for t in self.tails)
         self.c = tv_gdn_front_layer(_dtype_code(dtype), Hk, Hv, dk, dv, wconv.shape[1], _ptr(wconv), self._tail)
 
 
@@ -495,28 +505,42 @@ def tv_len_advance(len_, by, inc: int, n_seq: int, stream=None):
 # ---------------------------------------------------------------------------
 def _need(where: str, **tensors):
     """Raises where a buffer is not what the C side will take it for: each
-    value is (tensor, dtype, elements); the memory must be contiguous, on a
-    GPU, and hold at least that many elements."""
+    value is (tensor, dtype, elements); the memory must be contiguous, on the
+    current GPU (where the call's kernels run), and hold at least that many
+    elements."""
+    here = -1
     for name, (t, dtype, n) in tensors.items():
-        if t is not None and (t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda or t.numel() < n):
+        if t is None:
+            continue
+        gpu = t.get_device()  # (-1: host memory)
+        if t.dtype is not dtype or not t.is_contiguous() or gpu < 0 or t.numel() < n:
             raise ValueError(f"{where}: {name} must be a contiguous {dtype} GPU tensor of at least {n} elements, got "
                              f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+        if gpu != here:
+            here = _current_gpu()
+            if gpu != here:
+                raise ValueError(f"{where}: {name} is on GPU {gpu}, the current one is {here}")
 
 
-def _need_layer(where: str, layer, n_seq: int):
+def _need_layer(where: str, layer, prompt):
     """Raises where a layer's caches, states or tails are fewer than the call's
-    sequences (the C side would read past its pointers) or not alike."""
-    if layer.n_seq < n_seq:
-        raise ValueError(f"{where}: {n_seq} sequences, but the layer holds {layer.n_seq}")
+    sequences (the C side would read past its pointers), not alike, or not on
+    the current GPU, or the prompt's rows are not there."""
+    if layer.n_seq < prompt.n_seq:
+        raise ValueError(f"{where}: {prompt.n_seq} sequences, but the layer holds {layer.n_seq}")
     if not layer.sound:
-        raise ValueError(f"{where}: the layer's tensors must be contiguous GPU memory of one shape and dtype each")
+        raise ValueError(f"{where}: the layer's tensors must be contiguous memory of one GPU, of one shape and dtype each")
+    here = _current_gpu()
+    if layer.gpu != here or prompt.row_off.get_device() != here:
+        raise ValueError(f"{where}: the layer is on GPU {layer.gpu}, the rows are on {prompt.row_off.device}, the current "
+                         f"GPU is {here}")
 
 
 def _ws_bytes(ws) -> int:
     if ws is None:
         return 0
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("the workspace must be contiguous GPU memory")
+    if not ws.is_cuda or not ws.is_contiguous() or ws.get_device() != _current_gpu():
+        raise ValueError("the workspace must be contiguous memory of the current GPU")
     return ws.numel() * ws.element_size()
 
 
@@ -549,7 +573,7 @@ def tv_attn_norm_rope(layer: AttnLayer, tree: Tree | None, n_seq, len_, max_len,
 def tv_attn_prompt_front(layer: AttnLayer, prompt: Prompt, len_, max_len, q_norm, k_norm, eps, rot_dims, theta, q_raw,
                          k_raw, v, q, stream=None):
     """Head norms and rotation of a prompt's rows; keys and values go into the caches."""
-    _need_layer("tv_attn_prompt_front", layer, prompt.n_seq)
+    _need_layer("tv_attn_prompt_front", layer, prompt)
     c, dt, n = layer.c, layer.K[0].dtype, prompt.n_total
     nq, nk = n * c.Hq * c.D, n * c.Hkv * c.D
     _need("tv_attn_prompt_front", len=(len_, torch.int32, prompt.n_seq), q_norm=(q_norm, torch.float32, c.D),
@@ -566,7 +590,7 @@ def tv_attn_prompt_workspace_bytes(layer: AttnLayer, prompt: Prompt, max_len: in
 
 def tv_attn_prompt(layer: AttnLayer, prompt: Prompt, len_, max_len, q, gate, out, scale, ws, stream=None):
     """Causal attention of a prompt's rows over the caches that hold them."""
-    _need_layer("tv_attn_prompt", layer, prompt.n_seq)
+    _need_layer("tv_attn_prompt", layer, prompt)
     c, dt = layer.c, layer.K[0].dtype
     nq = prompt.n_total * c.Hq * c.D
     _need("tv_attn_prompt", len=(len_, torch.int32, prompt.n_seq), q=(q, dt, nq), gate=(gate, dt, nq),
@@ -581,7 +605,7 @@ def tv_gdn_prompt_workspace_bytes(layer: GdnLayer, prompt: Prompt) -> int:
 
 def tv_gdn_prompt(layer: GdnLayer, prompt: Prompt, q, k, v, alpha, beta, out, scale, ws, stream=None):
     """The gated delta rule over a prompt's rows; the states advance in place."""
-    _need_layer("tv_gdn_prompt", layer, prompt.n_seq)
+    _need_layer("tv_gdn_prompt", layer, prompt)
     c, n = layer.c, prompt.n_total
     dt = torch.bfloat16 if c.dtype == TV_BF16 else torch.float32
     nk, nv, nh = n * c.Hk * c.dk, n * c.Hv * c.dv, n * c.Hv
@@ -594,7 +618,7 @@ def tv_gdn_prompt(layer: GdnLayer, prompt: Prompt, q, k, v, alpha, beta, out, sc
 
 def tv_gdn_prompt_front(layer: GdnFrontLayer, prompt: Prompt, x, a_raw, b_raw, q, k, v, alpha, beta, stream=None):
     """The GDN front end over a prompt's rows; the convolution tails advance."""
-    _need_layer("tv_gdn_prompt_front", layer, prompt.n_seq)
+    _need_layer("tv_gdn_prompt_front", layer, prompt)
     c, n = layer.c, prompt.n_total
     dt = torch.bfloat16 if c.dtype == TV_BF16 else torch.float32
     nk, nv, nh = n * c.Hk * c.dk, n * c.Hv * c.dv, n * c.Hv

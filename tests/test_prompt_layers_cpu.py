@@ -34,18 +34,44 @@ def test_more_sequences_than_the_layer_holds():
 
 def test_layers_must_be_alike_gpu_memory():
     for call in calls(*layers(2), prompt(2)):  # (host memory here)
-        with pytest.raises(ValueError, match="alike|must be contiguous GPU"):
+        with pytest.raises(ValueError, match="one GPU"):
             call()
 
 
 def test_alike():
     class Gpu(torch.Tensor):
-        is_cuda = True
+        def get_device(self):
+            return 1 if self.numel() == 77 else 0
 
     def gpu(*shape, dtype=torch.float32):
         return torch.zeros(*shape, dtype=dtype).as_subclass(Gpu)
+
+    assert not B._alike([gpu(2), gpu(77)], (2,), torch.float32) and B._alike([gpu(77), gpu(77)], (77,), torch.float32)
 
     assert B._alike([gpu(2, 16, 64), gpu(2, 16, 64)], (2, 16, 64), torch.float32)
     for bad in (gpu(2, 15, 64), gpu(2, 16, 64, dtype=torch.bfloat16), gpu(2, 64, 16).transpose(1, 2)):
         assert not B._alike([gpu(2, 16, 64), bad], (2, 16, 64), torch.float32)
     assert not B._alike([torch.zeros(2, 16, 64)], (2, 16, 64), torch.float32)
+
+
+def test_buffers_of_another_gpu_are_refused(monkeypatch):
+    class Gpu(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    t = torch.zeros(16).as_subclass(Gpu)
+    monkeypatch.setattr(B, "_current_gpu", lambda: 0)
+    with pytest.raises(ValueError, match="on GPU 1, the current one is 0"):
+        B._need("call", q=(t, torch.float32, 16))
+    monkeypatch.setattr(B, "_current_gpu", lambda: 1)
+    B._need("call", q=(t, torch.float32, 16), gate=(None, torch.float32, 16))
+
+
+def test_layers_and_rows_of_another_gpu_are_refused(monkeypatch):
+    p = prompt(2)
+    for layer in layers(2):
+        layer.sound, layer.gpu = True, 1
+        for here in (0, 1):  # (the rows are host memory)
+            monkeypatch.setattr(B, "_current_gpu", lambda: here)
+            with pytest.raises(ValueError, match="the layer is on GPU 1"):
+                B._need_layer("call", layer, p)
