@@ -418,7 +418,8 @@ tv_status tv_gdn_conv_commit(const tv_gdn_front_layer* layer, const tv_tree* tre
  *
  * An infinity or NaN in a row reaches what the formulas let it reach: rows
  * before it, other sequences and (where they are apart) other heads and
- * columns are as if it were finite. */
+ * columns are as if it were finite.  (The delta rule in blocks gives NaN for
+ * whatever it reaches.) */
 typedef struct {
   int32_t n_seq;          /* sequences, 1..TV_MAX_SEQ (host) */
   int32_t n_total;        /* rows the packed buffers hold, 0..TV_MAX_PROMPT_ROWS (host) */
@@ -467,7 +468,8 @@ tv_status tv_attn_prompt_front(const tv_attn_layer* layer, const tv_prompt* prom
                                void* q, tv_stream stream);
 
 /* Device scratch bytes tv_attn_prompt needs for this layer, these host bounds
- * and contexts of at most max_len rows. */
+ * and contexts of at most max_len rows: none for fp32 layers and short contexts,
+ * never more than 1,824 pieces of 128 x (D + 4) fp32 (243 MB at D = 256). */
 size_t tv_attn_prompt_workspace_bytes(const tv_attn_layer* layer, const tv_prompt* prompt, int32_t max_len);
 
 /* Causal attention of a prompt's rows over the cache: row i of sequence s
@@ -487,7 +489,10 @@ tv_status tv_attn_prompt(const tv_attn_layer* layer, const tv_prompt* prompt, co
                          size_t workspace_bytes, tv_stream stream);
 
 /* Device scratch bytes tv_gdn_prompt needs for this layer and these host
- * bounds. */
+ * bounds: none row by row (fp32 layers, n_max under 48, dv no multiple of 64),
+ * else for every 64 rows and value head 8,448 + 256 dk bytes, whole prompts at
+ * once (48 heads of 128: 31 KB a row, 255 MB at 8,192 rows, 1 GB at 32,768).  A
+ * longer prompt fed in slices needs a slice's. */
 size_t tv_gdn_prompt_workspace_bytes(const tv_gdn_layer* layer, const tv_prompt* prompt);
 
 /* The gated delta rule over a prompt's rows: the recurrence of
@@ -500,7 +505,8 @@ tv_status tv_gdn_prompt(const tv_gdn_layer* layer, const tv_prompt* prompt, cons
                         const void* v, const float* alpha, const float* beta, void* out, float scale,
                         void* workspace, size_t workspace_bytes, tv_stream stream);
 
-/* tv_gdn_front over a prompt's rows: the convolution runs along each sequence
+/* tv_gdn_front over a prompt's rows, within a few fp32 steps of its values (SiLU
+ * and norms are formed another way): the convolution runs along each sequence
  * and continues into its tail; unlike there the tails then advance to the
  * last W-1 raw inputs (a prompt's rows are committed as they are read).
  * Arguments as in tv_gdn_front with n_total rows, every pointer (wconv and

@@ -45,11 +45,11 @@
 //
 // Bound by the tensor cores: at D = 256 a tile's two products take 2,048 cycles
 // and a tile takes about 2,300 (tensor pipe 77 % active over a whole call of
-// 8,192 rows under a power cap).  24 + 4 heads of 256, and the same operations at
-// the measured rate of a large library product: 8,192 rows 495 us (432), 1,024
-// rows behind 130,048 2,020 us (1,722), packed 2,047 + 1 + 515 + 4,096 rows with a
-// gate 254 us (159; tiles that are half masked and short items), 24 rows behind
-// 65,536 67 us (40 of bytes; pieces of a few tiles, then the join).
+// 8,192 rows under a power cap).  24 + 4 heads of 256, caches cold, and the same
+// operations at the measured rate of a large library product: 8,192 rows 493 us
+// (432), 1,024 rows behind 130,048 1,992 us (1,722), packed 2,047 + 1 + 515 + 4,096
+// rows with a gate 258 us (159; tiles that are half masked and short items), 24
+// rows behind 65,536 60.6 us (40 of bytes; pieces of a few tiles, then the join).
 #include <cmath>
 #include <cstring>
 
@@ -62,7 +62,7 @@ namespace tv {
 constexpr int kKeyTile = 128;
 constexpr float kMoveMax = 8.f;
 constexpr int kPieceTiles = 2;     // shortest piece of a split item
-constexpr int kSlotsPerSm = 12;    // workspace records (pieces) per SM, at most
+constexpr int kMaxPieces = 12 * 152;  // workspace records (pieces), at most: 12 a CTA on 152 SMs
 
 struct PromptPlan {
   int total, S;
@@ -1092,7 +1092,7 @@ static int64_t slots_for(const tv_attn_layer* l, const tv_prompt* pr, int max_le
   const int64_t items = l->Hkv * ((pr->n_total + t - 1) / t + pr->n_seq);
   const int64_t nk = (static_cast<int64_t>(max_len) + pr->n_max + kKeyTile - 1) / kKeyTile;
   if (nk <= kPieceTiles) return 0;
-  const int64_t all = items * ((nk + kPieceTiles - 1) / kPieceTiles), cap = static_cast<int64_t>(kSlotsPerSm) * 152;
+  const int64_t all = items * ((nk + kPieceTiles - 1) / kPieceTiles), cap = kMaxPieces;
   return all < cap ? all : cap;
 }
 

@@ -12,9 +12,10 @@ constexpr float kNormEps = 1e-6f;
 constexpr int kMaxConvWidth = 8;
 
 // SiLU as x / (1 + e^-x) with CUDA's fast exponential and divide (__expf,
-// __fdividef: a few ulp, far below the bf16 rounding that follows); every
-// path of the library forms it with this one function.  For x below -88 the
-// exponential is infinite and the quotient 0, SiLU's limit.
+// __fdividef: a few ulp, far below the bf16 rounding that follows); the tree
+// and decode paths form it with this one function (the prompt front end with a
+// reciprocal, within the same few ulp).  For x below -88 the exponential is
+// infinite and the quotient 0, SiLU's limit; -inf gives NaN.
 __device__ __forceinline__ float silu_f(float x) { return __fdividef(x, __fadd_rn(1.f, __expf(-x))); }
 
 // Gates from the raw values: alpha = exp(-softplus(a)), beta = sigmoid(b).

@@ -9,9 +9,9 @@
 // in fp32 in order, oldest first, as in the tree and decode forms.
 //
 // Bound by HBM, every raw channel read once and written once, with the issue
-// slots close behind (50 % at 58 % of DRAM throughput).  16 + 48 heads of 128,
-// W = 4: 8,192 rows (342 MB) 64.9 us, 5.3 TB/s, 0.79 of a copy's rate; 731 rows
-// in four sequences 11.1 us, two thirds of that one strip's latency.
+// slots behind (45 % at 58 % of DRAM throughput).  16 + 48 heads of 128,
+// W = 4: 8,192 rows (342 MB) 64.8 us, 5.3 TB/s, 0.79 of a copy's rate; 731 rows
+// in four sequences 10.4 us, two thirds of that one strip's latency.
 #include "prompt.cuh"
 #include "front_gdn.cuh"
 #include "launchers.hpp"

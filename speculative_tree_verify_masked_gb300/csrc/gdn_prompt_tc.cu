@@ -39,7 +39,7 @@
 // not by bytes: 16 + 48 heads of 128 x 128, 8,192 rows 335 us (127 + 207; 41.5
 // of bytes), about 3,000 cycles a block and CTA, the tensor pipe busy for 62 % of
 // them; 2,047 + 1 + 515 + 4,096 rows 234 us (104 + 127).  The first kernel waits
-// for its own steps (33 % of issue slots; registers hold it to three CTAs an SM).
+// for its own steps (35 % of issue slots; registers hold it to three CTAs an SM).
 #include <cstring>
 
 #include "gdn_prompt.cuh"
