@@ -180,7 +180,8 @@ __device__ __forceinline__ uint32_t times_zero_plus(uint32_t x, uint32_t acc) { 
   return r;
 }
 // Columns of O, before they are read out, plus the values of rows [from, to) that
-// are not finite (their weights, all above zero, change nothing).
+// are not finite.  Their weights are taken as above zero and so change nothing (one
+// of exactly zero, from a score of -inf, would make NaN of an infinity).
 static __device__ __noinline__ void add_nonfinite(uint32_t o, const __nv_bfloat16* v, int stride, int cols, int from, int to) {
   for (int c = 0; c < cols; c++) {
     float x = tmem_ld1(o + c);
