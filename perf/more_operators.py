@@ -100,6 +100,9 @@ def draw(rng):
             rows = _text([b - a for a, b in zip([0] + cuts, cuts + [total])])
         elif rng.random() < 0.4:
             lens[rng.randrange(n)] = -1
+        if op == "bounds":  # a page that is completed, at least
+            i = rng.choice([i for i, L in enumerate(lens) if L >= 0 and (not rows or _ints(rows)[i])] or [0])
+            lens[i] = max(lens[i], 0) // page * page + page - 1
         extra = {"rot": rng.choice([D, D // 2, D // 4])} if op == "append" else {}
         c = _case("", op, lens, page, heads, dtype, rows=rows, **extra)
     else:
@@ -111,12 +114,12 @@ def draw(rng):
                 sizes = [b - a for a, b in zip([0] + cuts, cuts + [n])]
                 most = int(4e10 / (4 * Hq * D * n))  # no dearer than the largest listed case
                 pre = [min(_log_int(rng, page, max(page, far)), most) // page * page for _ in sizes]
-                own_rows = [rng.randint(0, _log_int(rng, 1, 2048)) for _ in lens]
+                own_rows = [rng.randint(0, _log_int(rng, 1, 1024)) for _ in lens]
                 lens = [p + own_rows[i] for i, p in enumerate(p for p, m in zip(pre, sizes) for _ in range(m))]
                 groups, shared = _text(sizes), _text(pre)
             if rng.random() < 0.3:
                 lens[rng.randrange(n)] = -1
-        cap = int(2e9 / (4 * Hkv * D))  # rows: at most 2 GB of 16-bit keys and values
+        cap = int(5e8 / (4 * Hkv * D))  # rows: at most 0.5 GB of 16-bit keys and values
         own_total = sum(lens) - (sum(p * (m - 1) for p, m in zip(_ints(shared), _ints(groups))) if groups else 0)
         if own_total > cap and not groups:
             lens = [x * cap // own_total if x > 0 else x for x in lens]
@@ -298,13 +301,19 @@ def _plain_append(s):
     return {"q": s["q"], "K": s["K"], "V": s["V"]}
 
 
+def _pow2(e):
+    """2^e in 64 bits, put together from its bits (a power function may be off by a step, and floors and
+    ceilings of whole numbers would see it)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _bounds(K):
     """Codes [n, Hkv, 2, D] and exponents [n, Hkv] of whole pages K [n, Hkv, page, D]: the columns' least
     and largest values in steps of 2^e, rounded outward; e the least with every code within 127."""
     lo, hi = K.amin(2).double(), K.amax(2).double()
     m, x = torch.frexp(torch.maximum(lo.abs(), hi.abs()).amax(-1))
     e = (x - 7 + (m > 127 / 128).int()).clamp(min=-100)
-    step = torch.ldexp(torch.ones_like(m, dtype=torch.float64), e)[..., None]
+    step = _pow2(e)[..., None]
     return torch.stack([torch.floor(lo / step), torch.ceil(hi / step)], 2).to(torch.int8), e.int()
 
 
@@ -348,7 +357,7 @@ def _query_codes(q):
     """q [Hkv, G, D] in whole steps of one power of two a KV head, the least with every code within 127."""
     m, x = torch.frexp(q.abs().amax((1, 2)).double())
     e = x - 7 + (m > 127 / 128).int()
-    return torch.round(torch.ldexp(q.double(), -e[:, None, None]))
+    return torch.round(q.double() / _pow2(e)[:, None, None])
 
 
 def _plain_sparse(s):
@@ -366,7 +375,7 @@ def _plain_sparse(s):
             u = _query_codes(s["q"][i].view(Hkv, -1, D)).float()
             lo, hi = s["code"][pages].float().permute(2, 1, 3, 0)  # [Hkv, D, pages]
             score = (torch.matmul(u.clamp(min=0), hi) + torch.matmul(u.clamp(max=0), lo)).amax(1)  # whole numbers under 2^24
-            score = torch.ldexp(score, s["exp"][pages].T)
+            score = score.double() * _pow2(s["exp"][pages].T)
             best = torch.sort(score, stable=True, dim=-1, descending=True)[1][:, :n_sel - c["first"] - c["last"]] + a
             ends = torch.cat([torch.arange(a, device=DEV), torch.arange(b, nb, device=DEV)]).expand(Hkv, -1)
             sel = torch.sort(torch.cat([ends, best], 1), -1)[0]
@@ -445,11 +454,13 @@ def _exact_append(s):
 def _exact_code(K):
     """Codes and exponent of one page's keys [Hkv, page, D] by trying exponents from the least up."""
     k = K.double()
-    e = torch.full((k.shape[0],), -100, device=DEV, dtype=torch.int32)
-    top = k.abs().flatten(1).amax(1)
-    for _ in range(240):
-        e = torch.where(top > 127 * torch.pow(2.0, e.double()), e + 1, e)
-    step = torch.pow(2.0, e.double())[:, None]
+    e = []
+    for top in k.abs().flatten(1).amax(1).tolist():
+        e.append(-100)
+        while top > 127 * 2.0 ** e[-1]:
+            e[-1] += 1
+    step = torch.tensor([2.0 ** x for x in e], dtype=torch.float64, device=DEV)[:, None]
+    e = torch.tensor(e, dtype=torch.int32, device=DEV)
     return torch.stack([(k.amin(1) / step).floor(), (k.amax(1) / step).ceil()], 1).to(torch.int8), e
 
 
@@ -497,7 +508,7 @@ def _exact_sparse(s):
                 pages = row[middle].long().to(DEV)
                 lo, hi = res["code"][pages, g].double().unbind(1)
                 best = torch.where(u[:, None] > 0, u[:, None] * hi, u[:, None] * lo).sum(-1).amax(0)
-                best = (best * torch.pow(2.0, res["exp"][pages, g].double())).tolist()
+                best = [x * 2.0 ** n for x, n in zip(best.tolist(), res["exp"][pages, g].tolist())]
                 ranked = sorted(range(len(middle)), key=lambda j: (-best[j], j))
                 chosen = sorted(chosen[:c["first"]] + chosen[nb - c["last"]:] +
                                 [middle[j] for j in ranked[:n_sel - c["first"] - c["last"]]])
