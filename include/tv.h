@@ -84,7 +84,8 @@ typedef enum {
   TV_ERR_TIMEOUT = 9,   /* device: a bounded wait inside a kernel expired */
   TV_ERR_LEN = 10,      /* device: a sequence length above the host bound max_len */
   TV_ERR_SCRATCH = 11,  /* host: request larger than the fixed scratch of tv_attn_tree_verify_static */
-  TV_ERR_ROWS = 12      /* device: malformed row offsets of a prompt call */
+  TV_ERR_ROWS = 12,     /* device: malformed row offsets, groups or counts of a prompt or paged call */
+  TV_ERR_PAGE = 13      /* device: a page table or selection entry that names no page */
 } tv_status;
 
 typedef enum { TV_F32 = 0, TV_BF16 = 1 } tv_dtype;
@@ -515,6 +516,143 @@ tv_status tv_gdn_prompt(const tv_gdn_layer* layer, const tv_prompt* prompt, cons
 tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* layer, const tv_prompt* prompt, const void* x,
                               const float* a_raw, const float* b_raw, void* q, void* k, void* v, float* alpha,
                               float* beta, tv_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Caches in pages: decode steps of many sequences
+ * ------------------------------------------------------------------------
+ * "Parallel requests", "The shared KV pool" and "What a slot costs": a server
+ * holds far more sequences than a launch of the calls above, and many of them
+ * begin alike.  Here a layer's keys and values lie in pages of `page` rows that
+ * any sequence may name: row j*page + r of sequence s is row r of page
+ * table[s][j] of the pools.  A prefix that several sequences share is the same
+ * pages, named by each.  One decode step of an attention layer runs
+ *     tv_paged_append, then tv_paged_attn
+ *  or tv_paged_append, tv_paged_bounds, tv_paged_select, tv_paged_attn_selected
+ * and, after the last layer, tv_paged_advance; tv_paged_append also takes the
+ * rows of prompts.  All of them take device-side tables and lengths, so a
+ * captured graph serves every batch within the host bounds.
+ *
+ * An idle slot has len[s] = -1: nothing of it is read, and its rows of q and
+ * out stay as they were.
+ *
+ * Checks on the device: a length outside -1..max_len sets TV_ERR_LEN; rows
+ * past the table's last column set TV_ERR_CAPACITY; a table entry that a call
+ * needs outside 0..n_pages-1 sets TV_ERR_PAGE; row offsets as in tv_prompt set
+ * TV_ERR_ROWS.  Each is found where the row, page or sequence is worked on:
+ * nothing outside the buffers is touched, but what the call writes for other
+ * rows may have been written (rows of a cache behind a length count for
+ * nothing until tv_paged_advance, which does nothing once the word is set).
+ * Later calls given the word do nothing.
+ *
+ * Every call launches with programmatic dependent launch; its first kernel
+ * reads nothing of the caller's before it waits. */
+#define TV_MAX_PAGED_SEQ 1024 /* sequences (slots) of one paged call; n_seq * Hkv < 2^16 (TV_ERR_SHAPE) */
+
+typedef struct {
+  tv_dtype dtype;         /* pools, q, k, v, gate and out: TV_BF16 or TV_F32 */
+  int32_t Hq, Hkv, D;     /* Hq % Hkv == 0, Hq/Hkv <= 128, D in {64,128,256} */
+  int32_t page;           /* rows of a page: 16, 32, 64 or 128 */
+  int32_t n_pages;        /* pages of each pool; n_pages * Hkv * page < 2^31 */
+  void* K;                /* device [n_pages][Hkv][page][D] */
+  void* V;                /* device, the same shape */
+} tv_paged_layer;
+
+typedef struct {
+  int32_t n_seq;          /* slots, 1..TV_MAX_PAGED_SEQ (host) */
+  int32_t cols;           /* entries of a table row (host), max_len < cols * page <= 2^30 */
+  int32_t max_len;        /* host bound on every len[s] */
+  const int32_t* table;   /* device [n_seq][cols]; entries behind a sequence's last page are not read */
+  const int32_t* len;     /* device [n_seq]: rows held before this step, -1: idle */
+  int32_t* status;        /* device [1] error word, as in tv_tree */
+} tv_paged;
+
+/* New rows of a batch, as in tv_prompt, packed behind one another (an idle slot
+ * has none).  Calls that take one also take NULL: one row for each slot, row s
+ * slot s's. */
+typedef struct {
+  int32_t n_total, n_max;  /* rows the packed buffers hold, 0..TV_MAX_PROMPT_ROWS; bound on one sequence's */
+  const int32_t* row_off;  /* device [n_seq+1] */
+} tv_paged_rows;
+
+/* Consecutive slots that share a prefix: group g is slots group_off[g] ..
+ * group_off[g+1]-1, whose first shared[g] rows (a multiple of `page`, at most
+ * any active member's len) are the same pages in every active member's table. */
+typedef struct {
+  int32_t n_group;           /* 1..n_seq (host) */
+  const int32_t* group_off;  /* device [n_group+1], from 0, not falling, to n_seq */
+  const int32_t* shared;     /* device [n_group], 0: nothing */
+} tv_paged_groups;
+
+/* tv_attn_prompt_front into pages: norms and rotation of row i of sequence s
+ * at position len[s] + i, queries to q, keys (normalised, rotated) and values
+ * (bit copies) to the sequence's rows len[s] + i.
+ *  rows   or NULL; q_raw, q [n][Hq][D], k_raw, v [n][Hkv][D], n = rows->n_total or n_seq
+ *  other arguments and the rows' bits as there.
+ * The pages a call writes must each belong to one sequence. */
+tv_status tv_paged_append(const tv_paged_layer* layer, const tv_paged* batch, const tv_paged_rows* rows,
+                          const float* q_norm, const float* k_norm, float eps, int32_t rot_dims, float theta,
+                          const void* q_raw, const void* k_raw, const void* v, void* q, tv_stream stream);
+
+/* len[s] += the rows of each active slot (rows NULL: 1), after a step's last
+ * layer; does nothing once the status word is set.  len is batch->len (the
+ * descriptor's own pointer promises not to write through it). */
+tv_status tv_paged_advance(const tv_paged* batch, const tv_paged_rows* rows, int32_t* len, tv_stream stream);
+
+/* Device scratch bytes of tv_paged_attn (groups NULL: without shared prefixes),
+ * for any lengths within max_len; 0 for TV_F32. */
+size_t tv_paged_attn_workspace_bytes(const tv_paged_layer* layer, const tv_paged* batch,
+                                     const tv_paged_groups* groups);
+
+/* Decode attention: slot s's query rows see its rows 0 .. len[s], the last
+ * of which tv_paged_append has just written,
+ *     out[s,h] = sum_t softmax_t(scale q[s,h] . K[t]) V[t]   (times sigmoid(gate[s,h]))
+ *  groups or NULL: the prefixes of groups with two active members or more are
+ *         read once for all members, from the table of the first active one; the
+ *         result is the same up to rounding.  Offsets or lengths that do not hold
+ *         what is said above set TV_ERR_ROWS.
+ *  q, out [n_seq][Hq][D]; gate the same or NULL (may be out); q and out apart
+ *  scale  score scale > 0
+ *  workspace as in tv_attn_prompt. */
+tv_status tv_paged_attn(const tv_paged_layer* layer, const tv_paged* batch, const tv_paged_groups* groups, const void* q,
+                        const void* gate, void* out, float scale, void* workspace, size_t workspace_bytes,
+                        tv_stream stream);
+
+/* Bounds of the pages that the rows complete (rows NULL: of those whose last
+ * row is len[s]): of each page and KV head, every column's least and largest
+ * key in whole steps of 2^e, rounded outward to code[0] and code[1], e the
+ * least from -100 up with every code within 127.  A page with a key that is
+ * not finite gets codes of 0 and e = 128.
+ *  code   device int8 [n_pages][Hkv][2][D]; exp device int32 [n_pages][Hkv]; kept beside the pools */
+tv_status tv_paged_bounds(const tv_paged_layer* layer, const tv_paged* batch, const tv_paged_rows* rows, int8_t* code,
+                          int32_t* exp, tv_stream stream);
+
+/* The pages each slot's queries look at, chosen for each KV head by the bounds.
+ * Of a slot's pages 0 .. len[s]/page those below `first` and the last `last`
+ * are taken, then those with the highest scores (equal ones: the lower page),
+ * n_sel in all, or every page where there are no more than that.  The score
+ *     2^e max_g sum_d (u[g,d] > 0 ? u[g,d] code[1][d] : u[g,d] code[0][d])
+ * over the G query heads bounds u . k over the page's keys; u are the queries
+ * in whole steps of one power of two a KV head, the least with every |u| <= 127,
+ * rounded to nearest even (all 0 where a query is not finite).  It is a whole
+ * number times a power of two, so the choice is the same for any order of
+ * summing.  e = 128 counts as an infinite score.
+ *  first >= 0, last >= 1, first + last <= n_sel <= 4096
+ *  sel    device [n_seq][Hkv][n_sel]: page indices (columns of the table), rising, -1 behind the last
+ *  count  device [n_seq][Hkv] */
+size_t tv_paged_select_workspace_bytes(const tv_paged_layer* layer, const tv_paged* batch);
+tv_status tv_paged_select(const tv_paged_layer* layer, const tv_paged* batch, const int8_t* code, const int32_t* exp,
+                          int32_t first, int32_t last, int32_t n_sel, const void* q, int32_t* sel, int32_t* count,
+                          void* workspace, size_t workspace_bytes, tv_stream stream);
+
+/* tv_paged_attn over the pages listed by sel and count alone (of the row's own
+ * page the rows up to len[s]).  The list may be any: in any order, a page listed
+ * twice counts twice, pages behind len[s] have no rows to see, a row that sees
+ * none gets zeros; an entry outside 0 .. cols-1 sets TV_ERR_PAGE, a count outside 0 .. n_sel
+ * TV_ERR_ROWS. */
+size_t tv_paged_attn_selected_workspace_bytes(const tv_paged_layer* layer, const tv_paged* batch, int32_t n_sel);
+tv_status tv_paged_attn_selected(const tv_paged_layer* layer, const tv_paged* batch, const int32_t* sel,
+                                 const int32_t* count, int32_t n_sel, const void* q, const void* gate, void* out,
+                                 float scale, void* workspace, size_t workspace_bytes, tv_stream stream);
 
 /* ------------------------------------------------------------------------
  * Accept walk: longest agreeing path plus one token

@@ -20,11 +20,12 @@ LIB_PATH = os.path.join(HERE, "libtreeverify.so")
 TV_MAX_SEQ = 8
 TV_MAX_NODES = 64
 TV_MAX_PATH = 16
+TV_MAX_PAGED_SEQ = 1024
 TV_F32, TV_BF16 = 0, 1
 
 STATUS_NAMES = {0: "TV_OK", 1: "TV_ERR_ARG", 2: "TV_ERR_SHAPE", 3: "TV_ERR_DTYPE", 4: "TV_ERR_ALIGN",
                 5: "TV_ERR_TREE", 6: "TV_ERR_CAPACITY", 7: "TV_ERR_CUDA", 8: "TV_ERR_WORKSPACE",
-                9: "TV_ERR_TIMEOUT", 10: "TV_ERR_LEN", 11: "TV_ERR_SCRATCH", 12: "TV_ERR_ROWS"}
+                9: "TV_ERR_TIMEOUT", 10: "TV_ERR_LEN", 11: "TV_ERR_SCRATCH", 12: "TV_ERR_ROWS", 13: "TV_ERR_PAGE"}
 
 
 class TvError(RuntimeError):
@@ -63,6 +64,24 @@ class tv_plan(ctypes.Structure):
 class tv_prompt(ctypes.Structure):
     _fields_ = [("n_seq", c_int32), ("n_total", c_int32), ("n_max", c_int32), ("row_off", c_void_p),
                 ("status", c_void_p)]
+
+
+class tv_paged_layer(ctypes.Structure):
+    _fields_ = [("dtype", c_int32), ("Hq", c_int32), ("Hkv", c_int32), ("D", c_int32), ("page", c_int32),
+                ("n_pages", c_int32), ("K", c_void_p), ("V", c_void_p)]
+
+
+class tv_paged(ctypes.Structure):
+    _fields_ = [("n_seq", c_int32), ("cols", c_int32), ("max_len", c_int32), ("table", c_void_p), ("len", c_void_p),
+                ("status", c_void_p)]
+
+
+class tv_paged_rows(ctypes.Structure):
+    _fields_ = [("n_total", c_int32), ("n_max", c_int32), ("row_off", c_void_p)]
+
+
+class tv_paged_groups(ctypes.Structure):
+    _fields_ = [("n_group", c_int32), ("group_off", c_void_p), ("shared", c_void_p)]
 
 
 _lib = None
@@ -159,6 +178,25 @@ def lib():
         L.tv_gdn_prompt.argtypes = [G, R, vp, vp, vp, vp, vp, vp, c_float, vp, c_size_t, vp]
         L.tv_gdn_prompt_front.restype = c_int32
         L.tv_gdn_prompt_front.argtypes = [F, R, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        PL, PB, PR, PG = POINTER(tv_paged_layer), POINTER(tv_paged), POINTER(tv_paged_rows), POINTER(tv_paged_groups)
+        L.tv_paged_append.restype = c_int32
+        L.tv_paged_append.argtypes = [PL, PB, PR, vp, vp, c_float, c_int32, c_float, vp, vp, vp, vp, vp]
+        L.tv_paged_advance.restype = c_int32
+        L.tv_paged_advance.argtypes = [PB, PR, vp, vp]
+        L.tv_paged_attn_workspace_bytes.restype = c_size_t
+        L.tv_paged_attn_workspace_bytes.argtypes = [PL, PB, PG]
+        L.tv_paged_attn.restype = c_int32
+        L.tv_paged_attn.argtypes = [PL, PB, PG, vp, vp, vp, c_float, vp, c_size_t, vp]
+        L.tv_paged_bounds.restype = c_int32
+        L.tv_paged_bounds.argtypes = [PL, PB, PR, vp, vp, vp]
+        L.tv_paged_select_workspace_bytes.restype = c_size_t
+        L.tv_paged_select_workspace_bytes.argtypes = [PL, PB]
+        L.tv_paged_select.restype = c_int32
+        L.tv_paged_select.argtypes = [PL, PB, vp, vp, c_int32, c_int32, c_int32, vp, vp, vp, vp, c_size_t, vp]
+        L.tv_paged_attn_selected_workspace_bytes.restype = c_size_t
+        L.tv_paged_attn_selected_workspace_bytes.argtypes = [PL, PB, c_int32]
+        L.tv_paged_attn_selected.restype = c_int32
+        L.tv_paged_attn_selected.argtypes = [PL, PB, vp, vp, c_int32, vp, vp, vp, c_float, vp, c_size_t, vp]
         L.tv_wait_selftest.restype = c_int32
         L.tv_wait_selftest.argtypes = [vp, vp, ctypes.c_int64, vp]
         _lib = L
@@ -173,7 +211,9 @@ EXPORTED = ["tv_status_string", "tv_version", "tv_tree_meta_bytes", "tv_tree_pre
             "tv_attn_tree_verify_gated", "tv_attn_decode_gated", "tv_gdn_front", "tv_gdn_out_norm",
             "tv_gdn_conv_commit", "tv_gdn_tree_verify_fused", "tv_gdn_decode_fused", "tv_wait_selftest",
             "tv_prompt_check", "tv_prompt_advance", "tv_attn_norm_rope", "tv_attn_prompt_front", "tv_attn_prompt_workspace_bytes", "tv_attn_prompt",
-            "tv_gdn_prompt_workspace_bytes", "tv_gdn_prompt", "tv_gdn_prompt_front"]
+            "tv_gdn_prompt_workspace_bytes", "tv_gdn_prompt", "tv_gdn_prompt_front", "tv_paged_append", "tv_paged_advance",
+            "tv_paged_attn_workspace_bytes", "tv_paged_attn", "tv_paged_bounds", "tv_paged_select_workspace_bytes",
+            "tv_paged_select", "tv_paged_attn_selected_workspace_bytes", "tv_paged_attn_selected"]
 
 
 def _check(code: int, where: str):
@@ -337,6 +377,70 @@ class Prompt:
 
     def status_code(self) -> int:
         return int(self.status[0].item())
+
+
+class PagedLayer:
+    """tv_paged_layer over pools K, V of shape [n_pages, Hkv, page, D]."""
+
+    def __init__(self, K, V, Hq: int):
+        self.K, self.V = K, V
+        n_pages, Hkv, page, D = K.shape
+        self.sound = _alike([K, V], K.shape, K.dtype)
+        self.gpu = K.get_device()
+        self.c = tv_paged_layer(_dtype_code(K.dtype), Hq, Hkv, D, page, n_pages, K.data_ptr(), V.data_ptr())
+
+
+class PagedBatch:
+    """tv_paged over a page table [n_seq, cols] and lengths [n_seq] (int32, on
+    the GPU; written to by the caller between steps), lengths up to max_len."""
+
+    def __init__(self, table, len_, max_len: int):
+        self.table, self.len, self.max_len = table, len_, max_len
+        self.n_seq, self.cols = table.shape
+        self.sound = _alike([table], (self.n_seq, self.cols), torch.int32) and _alike([len_], (self.n_seq,), torch.int32) \
+            and table.get_device() == len_.get_device()
+        self.gpu = table.get_device()
+        self.status = torch.zeros(4, dtype=torch.int32, device=table.device)
+        self.c = tv_paged(self.n_seq, self.cols, max_len, table.data_ptr(), len_.data_ptr(), self.status.data_ptr())
+
+    def status_code(self) -> int:
+        return int(self.status[0].item())
+
+
+class PagedRows:
+    """tv_paged_rows for the given rows per slot; n_total, n_max and set_rows as in Prompt."""
+
+    def __init__(self, rows, device="cuda", n_total: int | None = None, n_max: int | None = None):
+        off = Prompt._offsets(rows)
+        self.n_seq = len(rows)
+        self.n_total = off[-1] if n_total is None else n_total
+        self.n_max = max(rows) if n_max is None else n_max
+        self.row_off = torch.tensor(off, dtype=torch.int32, device=device)
+        self.c = tv_paged_rows(self.n_total, self.n_max, self.row_off.data_ptr())
+
+    _offsets = staticmethod(Prompt._offsets)
+    set_rows, counts = Prompt.set_rows, Prompt.counts
+
+
+class PagedGroups:
+    """tv_paged_groups: consecutive groups of `sizes` slots (n_seq together) whose first shared[g] rows are the same pages."""
+
+    def __init__(self, sizes, shared, device="cuda"):
+        if len(sizes) != len(shared) or not len(sizes):
+            raise ValueError("a shared length for each group, one group at least")
+        off = Prompt._offsets(sizes)
+        self.n_group, self.n_seq = len(sizes), off[-1]
+        self.group_off = torch.tensor(off, dtype=torch.int32, device=device)
+        self.shared = torch.tensor(list(shared), dtype=torch.int32, device=device)
+        self.c = tv_paged_groups(self.n_group, self.group_off.data_ptr(), self.shared.data_ptr())
+
+    def set_groups(self, sizes, shared, stream=None):
+        """Other groups in the same buffers (as many), in the stream's order as Prompt.set_rows."""
+        off = Prompt._offsets(sizes)
+        if len(sizes) != self.n_group or len(shared) != self.n_group or off[-1] != self.n_seq:
+            raise ValueError(f"groups {sizes} are not {self.n_group} over {self.n_seq} slots")
+        _upload(self.group_off, off, stream)
+        _upload(self.shared, list(shared), stream)
 
 
 # ---------------------------------------------------------------------------
@@ -628,6 +732,104 @@ def tv_gdn_prompt_front(layer: GdnFrontLayer, prompt: Prompt, x, a_raw, b_raw, q
     _check(lib().tv_gdn_prompt_front(ctypes.byref(c), ctypes.byref(prompt.c), _ptr(x), _ptr(a_raw), _ptr(b_raw),
                                      _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _stream(stream)),
            "tv_gdn_prompt_front")
+
+
+# ---------------------------------------------------------------------------
+# caches in pages
+# ---------------------------------------------------------------------------
+def _need_paged(where: str, layer, batch, rows=None, groups=None):
+    """Raises where a paged call's descriptors are not memory of the current GPU
+    of the shapes they say, or are made for another number of slots."""
+    here = _current_gpu()
+    if not layer.sound or not batch.sound:
+        raise ValueError(f"{where}: pools, table and lengths must be contiguous memory of one GPU, the pools alike, the others int32")
+    if layer.gpu != here or batch.gpu != here:
+        raise ValueError(f"{where}: the pools are on GPU {layer.gpu}, the batch is on {batch.gpu}, the current GPU is {here}")
+    for x in (rows, groups):
+        if x is not None and (x.n_seq != batch.n_seq or (x.row_off if x is rows else x.group_off).get_device() != here):
+            raise ValueError(f"{where}: rows or groups for {x.n_seq} slots, {batch.n_seq} in the batch, or of another GPU than {here}")
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x.c)
+
+
+def tv_paged_append(layer: PagedLayer, batch: PagedBatch, rows: PagedRows | None, q_norm, k_norm, eps, rot_dims, theta,
+                    q_raw, k_raw, v, q, stream=None):
+    """Head norms and rotation of a step's rows (rows None: one a slot) or of
+    prompts' rows; queries to q, keys and values into the slots' pages."""
+    _need_paged("tv_paged_append", layer, batch, rows)
+    c, n = layer.c, batch.n_seq if rows is None else rows.n_total
+    dt = layer.K.dtype
+    _need("tv_paged_append", q_norm=(q_norm, torch.float32, c.D), k_norm=(k_norm, torch.float32, c.D),
+          q_raw=(q_raw, dt, n * c.Hq * c.D), k_raw=(k_raw, dt, n * c.Hkv * c.D), v=(v, dt, n * c.Hkv * c.D),
+          q=(q, dt, n * c.Hq * c.D))
+    _check(lib().tv_paged_append(ctypes.byref(c), ctypes.byref(batch.c), _ref(rows), _ptr(q_norm), _ptr(k_norm), eps,
+                                 rot_dims, theta, _ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(q), _stream(stream)),
+           "tv_paged_append")
+
+
+def tv_paged_advance(batch: PagedBatch, rows: PagedRows | None = None, stream=None):
+    """The batch's lengths past a step's rows, after its last layer."""
+    if not batch.sound or batch.gpu != _current_gpu() or (rows is not None and (
+            rows.n_seq != batch.n_seq or rows.row_off.get_device() != batch.gpu)):
+        raise ValueError("tv_paged_advance: the batch and its rows must be of the current GPU, for as many slots")
+    _check(lib().tv_paged_advance(ctypes.byref(batch.c), _ref(rows), _ptr(batch.len), _stream(stream)), "tv_paged_advance")
+
+
+def tv_paged_attn_workspace_bytes(layer: PagedLayer, batch: PagedBatch, groups: PagedGroups | None = None) -> int:
+    return int(lib().tv_paged_attn_workspace_bytes(ctypes.byref(layer.c), ctypes.byref(batch.c), _ref(groups)))
+
+
+def tv_paged_attn(layer: PagedLayer, batch: PagedBatch, groups: PagedGroups | None, q, gate, out, scale, ws, stream=None):
+    """Decode attention over pages; the prefixes that groups share are read once."""
+    _need_paged("tv_paged_attn", layer, batch, groups=groups)
+    c, dt = layer.c, layer.K.dtype
+    nq = batch.n_seq * c.Hq * c.D
+    _need("tv_paged_attn", q=(q, dt, nq), gate=(gate, dt, nq), out=(out, dt, nq))
+    _check(lib().tv_paged_attn(ctypes.byref(c), ctypes.byref(batch.c), _ref(groups), _ptr(q), _ptr(gate), _ptr(out), scale,
+                               _ptr(ws), _ws_bytes(ws), _stream(stream)), "tv_paged_attn")
+
+
+def tv_paged_bounds(layer: PagedLayer, batch: PagedBatch, rows: PagedRows | None, code, exp, stream=None):
+    """Bounds of the pages that a step's rows complete: code int8 [n_pages, Hkv, 2, D], exp int32 [n_pages, Hkv]."""
+    _need_paged("tv_paged_bounds", layer, batch, rows)
+    c = layer.c
+    heads = c.n_pages * c.Hkv
+    _need("tv_paged_bounds", code=(code, torch.int8, heads * 2 * c.D), exp=(exp, torch.int32, heads))
+    _check(lib().tv_paged_bounds(ctypes.byref(c), ctypes.byref(batch.c), _ref(rows), _ptr(code), _ptr(exp), _stream(stream)),
+           "tv_paged_bounds")
+
+
+def tv_paged_select_workspace_bytes(layer: PagedLayer, batch: PagedBatch) -> int:
+    return int(lib().tv_paged_select_workspace_bytes(ctypes.byref(layer.c), ctypes.byref(batch.c)))
+
+
+def tv_paged_select(layer: PagedLayer, batch: PagedBatch, code, exp, first: int, last: int, q, sel, count, ws, stream=None):
+    """The pages that each slot's queries look at: sel int32 [n_seq, Hkv, n_sel], count int32 [n_seq, Hkv]."""
+    _need_paged("tv_paged_select", layer, batch)
+    c, n = layer.c, batch.n_seq
+    n_sel, heads = sel.shape[-1], c.n_pages * c.Hkv
+    _need("tv_paged_select", code=(code, torch.int8, heads * 2 * c.D), exp=(exp, torch.int32, heads),
+          q=(q, layer.K.dtype, n * c.Hq * c.D), sel=(sel, torch.int32, n * c.Hkv * n_sel), count=(count, torch.int32, n * c.Hkv))
+    _check(lib().tv_paged_select(ctypes.byref(c), ctypes.byref(batch.c), _ptr(code), _ptr(exp), first, last, n_sel, _ptr(q),
+                                 _ptr(sel), _ptr(count), _ptr(ws), _ws_bytes(ws), _stream(stream)), "tv_paged_select")
+
+
+def tv_paged_attn_selected_workspace_bytes(layer: PagedLayer, batch: PagedBatch, n_sel: int) -> int:
+    return int(lib().tv_paged_attn_selected_workspace_bytes(ctypes.byref(layer.c), ctypes.byref(batch.c), n_sel))
+
+
+def tv_paged_attn_selected(layer: PagedLayer, batch: PagedBatch, sel, count, q, gate, out, scale, ws, stream=None):
+    """Decode attention over the listed pages alone."""
+    _need_paged("tv_paged_attn_selected", layer, batch)
+    c, n, dt = layer.c, batch.n_seq, layer.K.dtype
+    n_sel, nq = sel.shape[-1], n * c.Hq * c.D
+    _need("tv_paged_attn_selected", sel=(sel, torch.int32, n * c.Hkv * n_sel), count=(count, torch.int32, n * c.Hkv),
+          q=(q, dt, nq), gate=(gate, dt, nq), out=(out, dt, nq))
+    _check(lib().tv_paged_attn_selected(ctypes.byref(c), ctypes.byref(batch.c), _ptr(sel), _ptr(count), n_sel, _ptr(q),
+                                        _ptr(gate), _ptr(out), scale, _ptr(ws), _ws_bytes(ws), _stream(stream)),
+           "tv_paged_attn_selected")
 
 
 # ---------------------------------------------------------------------------

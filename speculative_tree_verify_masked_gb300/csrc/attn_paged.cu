@@ -1,0 +1,186 @@
+// Decode attention over caches in pages: the entry points, and the fp32 path on
+// the CUDA cores (bf16 runs on the tensor cores, attn_paged_tc.cu).
+//
+//   out[s,h] = sum_t softmax_t(scale q[s,h] . K[t]) V[t], t = 0 .. len[s] or the
+//   rows of the listed pages among them.
+//
+// fp32: a CTA owns a (slot, query head); its eight warps take every eighth run
+// of four rows, a row's D values over the 32 lanes, and keep a running maximum and
+// sum each, which are joined at the end.  Bound by the walk over the rows of the
+// longest slot (sized for the small model of the tests).
+#include "attn_paged.cuh"
+
+namespace tv {
+
+struct PagedCudaParams {
+  PagedView v;
+  const float* K;
+  const float* V;
+  const float* q;
+  const float* gate;  // or null
+  float* out;
+  int Hq, G;
+  float c;  // scale * log2(e)
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) attn_paged_cuda_kernel(const __grid_constant__ PagedCudaParams p) {
+  constexpr int CPL = D / 32, R = 4;  // values a lane, rows of a run (never across pages: R divides them)
+  __shared__ float acc_s[8][D], m_s[8], l_s[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  if (status_bad(p.v.b.status)) return;
+  const int h = blockIdx.x, s = blockIdx.y, g = h / p.G;
+  const int L = paged_len(p.v.b, s);
+  if (L < 0) return;
+  const int n = p.v.pages(s, g, L) << p.v.b.shift, rows = 1 << p.v.b.shift;
+  const size_t row0 = (static_cast<size_t>(s) * p.Hq + h) * D;
+  float q[CPL], acc[CPL], m = -INFINITY, l = 0.f;
+  bool met = false;  // a row that the slot sees
+#pragma unroll
+  for (int c = 0; c < CPL; c++) {
+    q[c] = p.q[row0 + c * 32 + lane];
+    acc[c] = 0.f;
+  }
+  for (int i = warp * R; i < n; i += 8 * R) {
+    const int col = p.v.column(s, g, i >> p.v.b.shift), r = i & (rows - 1);
+    if (col < 0) continue;
+    const int live = min(R, L + 1 - (col * rows + r));  // (col < cols: no overflow)
+    if (live <= 0) continue;
+    const int page = page_at(p.v.b, s, col);
+    if (page < 0) continue;
+    met = true;
+    const size_t base = ((static_cast<size_t>(page) * p.v.Hkv + g) * rows + r) * D + lane;
+    float k[R][CPL], v[R][CPL], sc[R];
+#pragma unroll
+    for (int j = 0; j < R; j++) {
+      const size_t at = base + static_cast<size_t>(min(j, live - 1)) * D;
+#pragma unroll
+      for (int c = 0; c < CPL; c++) {
+        k[j][c] = p.K[at + c * 32];
+        v[j][c] = p.V[at + c * 32];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < R; j++) {
+      sc[j] = 0.f;
+#pragma unroll
+      for (int c = 0; c < CPL; c++) sc[j] = __fmaf_rn(q[c], k[j][c], sc[j]);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < R; j++) sc[j] = __fadd_rn(sc[j], __shfl_xor_sync(0xffffffffu, sc[j], o));
+    float mn = m;
+#pragma unroll
+    for (int j = 0; j < R; j++) {
+      sc[j] = __fmul_rn(sc[j], p.c);
+      if (j < live) mn = fmaxf(mn, sc[j]);
+    }
+    const float alpha = mn == m ? 1.f : exp2f(__fsub_rn(m, mn));
+    l = __fmul_rn(l, alpha);
+#pragma unroll
+    for (int c = 0; c < CPL; c++) acc[c] = __fmul_rn(acc[c], alpha);
+#pragma unroll
+    for (int j = 0; j < R; j++) {
+      if (j >= live) continue;
+      // (every score so far -inf: weights of 0, not of -inf - -inf)
+      const float w = exp2f(__fsub_rn(sc[j], mn == -INFINITY ? 0.f : mn));
+      l = __fadd_rn(l, w);
+#pragma unroll
+      for (int c = 0; c < CPL; c++) acc[c] = __fmaf_rn(w, v[j][c], acc[c]);
+    }
+    m = mn;
+  }
+#pragma unroll
+  for (int c = 0; c < CPL; c++) acc_s[warp][c * 32 + lane] = acc[c];
+  if (lane == 0) {
+    m_s[warp] = m;
+    l_s[warp] = l;
+  }
+  const bool any = __syncthreads_or(met) != 0;
+  if (threadIdx.x >= D) return;
+  float mn = -INFINITY, lt = 0.f, o = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; w++) mn = fmaxf(mn, m_s[w]);
+#pragma unroll
+  for (int w = 0; w < 8; w++) {
+    const float f = exp2f(__fsub_rn(m_s[w], mn == -INFINITY ? 0.f : mn));
+    if (l_s[w] == 0.f) continue;
+    lt = __fmaf_rn(f, l_s[w], lt);
+    o = __fmaf_rn(f, acc_s[w][threadIdx.x], o);
+  }
+  const float y = any ? __fdiv_rn(o, lt) : 0.f;  // (no row seen: zeros; none with a score above -inf: 0 / 0, as the formula has it)
+  const size_t at = row0 + threadIdx.x;
+  p.out[at] = p.gate && any ? gate_mul(y, p.gate[at]) : y;
+}
+
+static tv_status launch_cuda(const PagedAttnCall& a, cudaStream_t st) {
+  const tv_paged_layer* l = a.layer;
+  PagedCudaParams p{};
+  p.v = PagedView{paged_seqs(l, a.batch), a.sel, a.count, a.n_sel, l->Hkv};
+  p.K = static_cast<const float*>(l->K);
+  p.V = static_cast<const float*>(l->V);
+  p.q = static_cast<const float*>(a.q);
+  p.gate = static_cast<const float*>(a.gate);
+  p.out = static_cast<float*>(a.out);
+  p.Hq = l->Hq;
+  p.G = l->Hq / l->Hkv;
+  p.c = a.scale * 1.4426950408889634f;
+  const dim3 g(l->Hq, a.batch->n_seq);
+  switch (l->D) {
+    case 64: launch_k(true, attn_paged_cuda_kernel<64>, g, dim3(256), 0, st, p); break;
+    case 128: launch_k(true, attn_paged_cuda_kernel<128>, g, dim3(256), 0, st, p); break;
+    default: launch_k(true, attn_paged_cuda_kernel<256>, g, dim3(256), 0, st, p);
+  }
+  return launch_status();
+}
+
+static bool groups_ok(const tv_paged* b, const tv_paged_groups* g) {
+  return g->n_group >= 1 && g->n_group <= b->n_seq && g->group_off && g->shared;
+}
+
+static tv_status paged_attn(const PagedAttnCall& a, cudaStream_t st) {
+  const tv_paged_layer* l = a.layer;
+  if (!l->K || !l->V || !a.q || !a.out || !(a.scale > 0.f) || !std::isfinite(a.scale)) return TV_ERR_ARG;
+  if (!aligned16(a.q) || !aligned16(a.gate) || !aligned16(a.out) || !aligned16(a.ws)) return TV_ERR_ALIGN;
+  const size_t n = bytes_of(a.batch->n_seq, static_cast<int64_t>(l->Hq) * l->D, l->dtype);
+  if (share_memory(a.q, n, a.out, n)) return TV_ERR_ARG;  // a slot's heads are read after others are written
+  if (a.gate != a.out && share_memory(a.gate, n, a.out, n)) return TV_ERR_ARG;
+  return l->dtype == TV_BF16 ? paged_attn_tc_launch(a, st) : launch_cuda(a, st);
+}
+
+}  // namespace tv
+
+using namespace tv;
+
+extern "C" size_t tv_paged_attn_workspace_bytes(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g) {
+  if (paged_check(l, b) != TV_OK || l->dtype != TV_BF16 || (g && !groups_ok(b, g))) return 0;
+  return paged_attn_ws_bytes(l, b, g);
+}
+
+extern "C" tv_status tv_paged_attn(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g, const void* q,
+                                   const void* gate, void* out, float scale, void* ws, size_t ws_bytes, tv_stream stream) {
+  const tv_status c = paged_check(l, b);
+  if (c != TV_OK) return c;
+  if (g && !groups_ok(b, g)) return TV_ERR_ARG;
+  if (g && (!aligned16(g->group_off) || !aligned16(g->shared))) return TV_ERR_ALIGN;
+  return paged_attn(PagedAttnCall{l, b, g, nullptr, nullptr, 0, q, gate, out, scale, ws, ws_bytes},
+                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t tv_paged_attn_selected_workspace_bytes(const tv_paged_layer* l, const tv_paged* b, int32_t n_sel) {
+  if (paged_check(l, b) != TV_OK || l->dtype != TV_BF16 || n_sel < 1 || n_sel > 4096) return 0;
+  return paged_attn_ws_bytes(l, b, nullptr);
+}
+
+extern "C" tv_status tv_paged_attn_selected(const tv_paged_layer* l, const tv_paged* b, const int32_t* sel,
+                                            const int32_t* count, int32_t n_sel, const void* q, const void* gate, void* out,
+                                            float scale, void* ws, size_t ws_bytes, tv_stream stream) {
+  const tv_status c = paged_check(l, b);
+  if (c != TV_OK) return c;
+  if (!sel || !count || n_sel < 1 || n_sel > 4096) return TV_ERR_ARG;
+  if (!aligned16(sel) || !aligned16(count)) return TV_ERR_ALIGN;
+  return paged_attn(PagedAttnCall{l, b, nullptr, sel, count, n_sel, q, gate, out, scale, ws, ws_bytes},
+                    reinterpret_cast<cudaStream_t>(stream));
+}

@@ -1,0 +1,687 @@
+// Decode attention over bf16 caches in pages, on the tensor cores.
+//
+// A unit is one slot and KV head: its G query heads (16 at a time, an item)
+// against the keys and values that the slot sees, in tiles of 64 rows.  Each tile
+// is used by 16 rows of queries at most, so the call is bound by the reads of
+// keys and values; the products run on warp-level tiles (16 x 8 x 16), which
+// waste least on so few rows.  An item runs flash style:
+//   S = Q K^T, m = running maximum of the scaled scores, p = 2^(s c - m) rounded
+//   to bf16 for the product with V, l += p (fp32, as they were), O = O a + P V.
+// p is rounded because the tensor cores take P and V in one type; each weight is
+// off by 2^-8 of itself at most, independently, and l adds them unrounded.
+//
+// Work split.  The tiles of all items, one behind another, are cut into one
+// range of equal length for each CTA (one per SM), so every SM streams the same
+// number of bytes whatever the lengths are.  An item that lies in one CTA's range
+// is written by it; one that a cut goes through leaves a piece (O, m and l in fp32)
+// with each of its CTAs, two a CTA at most, and the join adds them up.  Every
+// CTA finds its range from the device-side lengths by itself.
+//
+// Roles.  A producer warp brings keys and values by TMA; it reads the table (and
+// the selection) 32 entries at a time, a batch ahead.  Two teams of four warps take
+// turns at the tiles, each with its own ring of slots, O, m and l, joined at the end
+// of an item.  (One ring for both would not do: a team would wait for a slot's
+// next filling but one without having seen the one between, which the other
+// takes, and copies do not land in order: the parity of a barrier cannot tell them
+// apart.)  Within a team a warp scores 16 of the tile's 64 rows and,
+// when the scores have gone through shared memory, owns a quarter of the columns
+// of O; every warp forms all 16 x 64 weights for itself, in registers, where its
+// products want them.
+//
+// Masked rows (behind len[s], in the last page of the slot): the scores are
+// replaced, and the values zeroed in shared memory (a weight of zero would still
+// make NaN of an infinity there).  Pages hold whole rows behind the last one, so
+// nothing outside the pools is read.
+#include <cstring>
+
+#include "attn_paged.cuh"
+#include "mma_tile.cuh"
+#include "ptx.cuh"
+#include "tensor_map.hpp"
+
+namespace tv {
+
+constexpr int kRows = 64;    // rows of a key tile
+constexpr int kItem = 16;    // query rows of an item
+constexpr int kConsumers = 256, kThreads = kConsumers + 32;
+constexpr float kNoScore = -3.402823466e38f;  // the maximum of a row that sees keys, none with a score above -inf
+
+template <int D>
+struct Pg {
+  static constexpr int SLOT = kRows * D * 2;             // a tile of keys or of values
+  static constexpr int NS = D == 256 ? 3 : D == 128 ? 6 : 8;  // slots of a team's ring
+  static constexpr int CPW = D / 4, NT = CPW / 8;        // columns of O a warp, in tiles of 8
+  static constexpr int SLD = 72;                         // floats of a row of scores (conflict-free pairs)
+  static constexpr int SBUF = kItem * SLD * 4;
+  static constexpr int SOFF = 2 * NS * SLOT;             // scores [team][2]
+  static constexpr int MOFF = SOFF + 4 * SBUF;           // the second team's m, l and half of O on their way to the first
+  static constexpr int MREG = NT * 2 + 4;
+  static constexpr int VOFF = MOFF + 128 * MREG * 4;     // rows seen of each 16 of a slot's tile: [2 NS][4]
+  static constexpr int BOFF = VOFF + 2 * NS * 16;
+  static constexpr int LOFF = BOFF + 4 * NS * 8;
+  static constexpr int SMEM = LOFF + 256;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct PagedTcParams {
+  CUtensorMap tmK, tmV;  // pools as [rows][D], boxes of R rows, 64 columns
+  PagedView v;
+  const int32_t* start;  // [n_seq] rows that another kernel has seen to, or null
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* gate;
+  __nv_bfloat16* out;
+  int64_t* first;  // [units + 1] each unit's first tile in the order of all
+  float* rec;      // [2 * CTAs][16][D + 4]
+  int Hq, G, MT, units;  // MT items a unit
+  int R;  // rows of a box: a page, or 64 of one of 128
+  float c;        // scale * log2(e)
+  uint32_t zero;  // 0
+};
+
+// Tiles of an item of unit u.
+__device__ __forceinline__ int unit_tiles(const PagedTcParams& p, int u) {
+  const int s = u / p.v.Hkv, L = paged_len(p.v.b, s);
+  if (L < 0) return 0;
+  if (p.v.sel) return ((p.v.pages(s, u - s * p.v.Hkv, L) << p.v.b.shift) + kRows - 1) / kRows;
+  return (L + 1 - (p.start ? p.start[s] : 0) + kRows - 1) / kRows;
+}
+
+// The items of a range of tiles, one after another.
+struct PagedPiece {
+  int s, h, m, k0, k1, nt;  // slot, KV head, 16 query heads, tiles [k0, k1) of nt
+};
+struct PagedWalk {
+  int u;        // unit
+  int64_t off;  // tile within the unit, over its items
+  int64_t left;
+  __device__ __forceinline__ bool next(const PagedTcParams& p, PagedPiece& x) {
+    while (left > 0 && u < p.units) {
+      const int nt = unit_tiles(p, u);
+      const int64_t all = static_cast<int64_t>(nt) * p.MT;
+      if (off >= all) {
+        off = 0;
+        u++;
+        continue;
+      }
+      x.s = u / p.v.Hkv;
+      x.h = u - x.s * p.v.Hkv;
+      x.m = static_cast<int>(off / nt);
+      x.k0 = static_cast<int>(off - static_cast<int64_t>(x.m) * nt);
+      x.k1 = static_cast<int>(min(static_cast<int64_t>(nt), x.k0 + left));
+      x.nt = nt;
+      off += x.k1 - x.k0;
+      left -= x.k1 - x.k0;
+      return true;
+    }
+    return false;
+  }
+};
+// CTAs that share `total` tiles, and where CTA c's range starts.
+__device__ __forceinline__ int64_t range_start(int64_t total, int ctas, int c) { return total * c / ctas; }
+__device__ __forceinline__ int range_of(int64_t total, int ctas, int64_t tile) {
+  return static_cast<int>(((tile + 1) * ctas - 1) / total);
+}
+__device__ __forceinline__ int ctas_for(int64_t total, int grid) { return static_cast<int>(min(static_cast<int64_t>(grid), total)); }
+
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void sts2(uint32_t a, float x, float y) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ float2 lds2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid_constant__ PagedTcParams p) {
+  using C = Pg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];  // tiles are swizzled in 1024-byte atoms
+  const uint32_t sb = smem_u32(smem_raw);
+  const uint32_t FULL0 = sb + C::BOFF, EMPTY0 = FULL0 + 16u * C::NS;
+  int32_t* seen_s = reinterpret_cast<int32_t*>(smem_raw + C::VOFF);
+  struct Local {
+    int64_t sums[9];  // tiles of each warp's units
+    int64_t off, left;
+    int u, skip;
+    int abort_flag;
+  };
+  Local& lo = *reinterpret_cast<Local*>(smem_raw + C::LOFF);
+  static_assert(sizeof(Local) <= 256, "local data");
+  volatile int* abort_flag = &lo.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * C::NS; i++) {
+      mbar_init(FULL0 + 8u * i, 1);
+      mbar_init(EMPTY0 + 8u * i, 4);
+    }
+    lo.abort_flag = 0;
+    lo.left = 0;
+    lo.u = 0;
+    lo.off = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  if (threadIdx.x == 0) {
+    lo.skip = status_bad(p.v.b.status) || (sb & 1023u) ? 1 : 0;
+    if (sb & 1023u) set_status(p.v.b.status, TV_ERR_CUDA);
+  }
+  __syncthreads();
+  if (lo.skip) return;
+  // this CTA's range: a run of units for each thread, their tiles summed over the CTA
+  {
+    const int per = (p.units + kThreads - 1) / kThreads;
+    const int u0 = min(static_cast<int>(threadIdx.x) * per, p.units), u1 = min(u0 + per, p.units);
+    int64_t mine = 0;
+    for (int u = u0; u < u1; u++) mine += static_cast<int64_t>(unit_tiles(p, u)) * p.MT;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) lo.sums[warp] = incl;
+    __syncthreads();
+    int64_t base = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; w++) {
+      if (w < warp) base += lo.sums[w];
+      total += lo.sums[w];
+    }
+    const int ctas = ctas_for(total, gridDim.x), me = static_cast<int>(blockIdx.x);
+    if (me == 0) {  // for the join
+      int64_t at = base;
+      for (int u = u0; u < u1; u++) {
+        p.first[u] = at;
+        at += static_cast<int64_t>(unit_tiles(p, u)) * p.MT;
+      }
+      if (threadIdx.x == 0) p.first[p.units] = total;
+    }
+    if (me < ctas) {
+      const int64_t a = range_start(total, ctas, me);
+      if (a >= base && a < base + mine) {
+        int64_t at = base;
+        int u = u0;
+        for (;; u++) {
+          const int64_t n = static_cast<int64_t>(unit_tiles(p, u)) * p.MT;
+          if (a < at + n || u + 1 >= u1) break;
+          at += n;
+        }
+        lo.u = u;
+        lo.off = a - at;
+        lo.left = range_start(total, ctas, me + 1) - a;
+      }
+    }
+    __syncthreads();
+  }
+  PagedWalk walk{lo.u, lo.off, lo.left};
+  PagedPiece x;
+  pdl_trigger();
+
+  if (warp == kConsumers / 32) {
+    // ---------------- producer ----------------
+    const int R = p.R, nsub = kRows / R, per_page = max(1, (1 << p.v.b.shift) / R), rows = 1 << p.v.b.shift;
+    constexpr int CH = D / 64;  // boxes across a row
+    uint32_t tile = 0;          // tiles of the CTA
+    uint32_t fills0 = 0, fills1 = 0;  // of each team's ring
+    bool ok = true;
+    while (ok && walk.next(p, x)) {
+      const int L = paged_len(p.v.b, x.s), from = p.start ? p.start[x.s] >> p.v.b.shift : 0;
+      const int pages = p.v.sel ? p.v.pages(x.s, x.h, L) : (L >> p.v.b.shift) + 1;  // (places in the order, from the first)
+      // part i of the item: box rows i * R .. of its rows
+      auto part = [&](int i, int& seen) -> int {  // its row in the pools, -1: none; rows of it that are seen
+        const int place = from + i / per_page;
+        seen = 0;
+        if (place >= pages || i >= x.k1 * nsub) return -1;
+        const int col = p.v.column(x.s, x.h, place);
+        if (col < 0) return -1;
+        const int r = (i % per_page) * R;
+        seen = min(R, L + 1 - (col * rows + r));
+        if (seen <= 0) {
+          seen = 0;
+          return -1;
+        }
+        const int page = page_at(p.v.b, x.s, col);
+        if (page < 0) {
+          seen = 0;
+          return -1;
+        }
+        return (page * p.v.Hkv + x.h) * rows + r;
+      };
+      int i0 = x.k0 * nsub, seen, seen2 = 0, row, row2 = -1;
+      row = part(i0 + lane, seen);
+      for (int k = x.k0; k < x.k1 && ok; k++, tile++) {
+        const int at = (k - x.k0) * nsub % 32;
+        if (at == 0) {
+          if (k != x.k0) {
+            row = row2;
+            seen = seen2;
+            i0 += 32;
+          }
+          row2 = part(i0 + 32 + lane, seen2);
+        }
+        // of this tile: part y's row and count in lane at + y
+        uint32_t bytes = 0;
+        for (int y = 0; y < nsub; y++) bytes += __shfl_sync(0xffffffffu, row, at + y) >= 0 ? R * D * 2 : 0;
+        const int y = lane / CH, ch = lane % CH;  // this lane's box
+        const int br = __shfl_sync(0xffffffffu, row, min(at + y, 31));
+        // rows seen of each 16 of the tile
+        const int q16 = lane & 3, py = q16 * 16 / R;
+        const int cnt = min(16, max(0, __shfl_sync(0xffffffffu, seen, at + py) - (q16 * 16 - py * R)));
+#pragma unroll
+        for (int kv = 0; kv < 2; kv++) {
+          const uint32_t it = tile & 1 ? fills1 : fills0, slot = (tile & 1) * C::NS + it % C::NS, full = FULL0 + 8u * slot;
+          ok = ok && wait_warp(EMPTY0 + 8u * slot, ((it / C::NS) & 1) ^ 1, abort_flag, kWaitCycles);
+          if (!ok) break;
+          if (tile & 1) fills1++;
+          else fills0++;
+          if (lane < 4) seen_s[slot * 4 + lane] = cnt;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+          __syncwarp();
+          for (int b = lane; b < nsub * CH; b += 32) {  // (16 boxes at most: one round)
+            if (br >= 0)
+              tma_load_2d(sb + slot * C::SLOT + ch * (kRows * 128) + y * R * 128, kv ? &p.tmV : &p.tmK, full, ch * 64, br);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (!ok && lane == 0) set_status(p.v.b.status, TV_ERR_TIMEOUT);
+    // every issued copy lands before shared memory is released
+    for (uint32_t team = 0; team < 2; team++) {
+      const uint32_t it = team ? fills1 : fills0;
+      for (uint32_t i = it > C::NS ? it - C::NS : 0; i < it; i++)
+        mbar_wait(FULL0 + 8u * (team * C::NS + i % C::NS), (i / C::NS) & 1, kWaitCycles);
+    }
+    return;
+  }
+
+  // ---------------- consumers ----------------
+  const int team = warp >> 2, w = warp & 3;
+  const int gr = lane >> 2, gc = (lane & 3) * 2;  // this lane's rows gr, gr + 8 and first column of a tile of 8
+  const uint32_t sc0 = sb + C::SOFF + team * 2 * C::SBUF;
+  float* merge = reinterpret_cast<float*>(smem_raw + C::MOFF) + (threadIdx.x & 127);
+  uint32_t tile = 0, turn = 0;  // tiles of the CTA, tiles of this team
+  int pieces = 0;
+  bool ok = true;  // (a warp whose wait gave up goes on through the barriers, idle)
+  const f2_t c2 = f2_dup(p.c);
+  while (walk.next(p, x)) {
+    // query heads of the item, straight into the first operand's layout
+    const int heads = min(kItem, p.G - x.m * kItem);
+    const size_t row0 = (static_cast<size_t>(x.s) * p.Hq + x.h * p.G + x.m * kItem) * D;
+    uint32_t qa[D / 16][4];
+    {
+      const __nv_bfloat16* q = p.q + row0 + gc;
+      const uint32_t* qlo = reinterpret_cast<const uint32_t*>(q + static_cast<size_t>(gr < heads ? gr : 0) * D);
+      const uint32_t* qhi = reinterpret_cast<const uint32_t*>(q + static_cast<size_t>(gr + 8 < heads ? gr + 8 : 0) * D);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; kk++) {
+        qa[kk][0] = gr < heads ? qlo[kk * 8] : 0u;
+        qa[kk][1] = gr + 8 < heads ? qhi[kk * 8] : 0u;
+        qa[kk][2] = gr < heads ? qlo[kk * 8 + 4] : 0u;
+        qa[kk][3] = gr + 8 < heads ? qhi[kk * 8 + 4] : 0u;
+      }
+    }
+    float o[C::NT][4];
+#pragma unroll
+    for (int n = 0; n < C::NT; n++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) o[n][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    bool met = false;
+    for (int k = x.k0; k < x.k1; k++, tile++) {
+      if ((tile & 1) != static_cast<uint32_t>(team)) continue;
+      const uint32_t r0 = team * C::NS, ki = 2 * turn, vi = ki + 1;  // fills of this team's ring
+      const uint32_t ks = r0 + ki % C::NS, kph = (ki / C::NS) & 1, vs = r0 + vi % C::NS, vph = (vi / C::NS) & 1;
+      const uint32_t sc = sc0 + (turn & 1) * C::SBUF;
+      turn++;
+      // S = Q K^T, 16 rows of keys a warp
+      ok = ok && wait_warp(FULL0 + 8u * ks, kph, abort_flag, kWaitCycles);
+      float s0[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      const int vis = ok ? seen_s[ks * 4 + w] : 0;
+      const int all4 = ok ? min(min(seen_s[ks * 4], seen_s[ks * 4 + 1]), min(seen_s[ks * 4 + 2], seen_s[ks * 4 + 3])) : 0;
+      if (ok) {
+        const int kr = w * 16 + (lane >> 4) * 8 + (lane & 7);
+        const uint32_t kb = sb + ks * C::SLOT + kr * 128;
+        const int half = (lane >> 3) & 1;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; kk++) {
+          uint32_t b[4];
+          ldsm_x4(kb + (kk >> 2) * (kRows * 128) + ((((kk & 3) * 2 + half) ^ (kr & 7)) << 4), b);
+          mma16816(s0[0], qa[kk], b[0], b[1]);
+          mma16816(s0[1], qa[kk], b[2], b[3]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; n++) {
+        const int c = n * 8 + gc;
+        if (c >= vis) s0[n][0] = s0[n][2] = -INFINITY;
+        if (c + 1 >= vis) s0[n][1] = s0[n][3] = -INFINITY;
+        sts2(sc + (gr * C::SLD + w * 16 + c) * 4, s0[n][0], s0[n][1]);
+        sts2(sc + ((gr + 8) * C::SLD + w * 16 + c) * 4, s0[n][2], s0[n][3]);
+      }
+      // Only now: an arrival does not wait for loads, the stores have waited for the
+      // products and these for theirs.
+      __syncwarp();
+      if (lane == 0) mbar_arrive(EMPTY0 + 8u * ks);
+      ok = ok && wait_warp(FULL0 + 8u * vs, vph, abort_flag, kWaitCycles);
+      if (all4 < 16 && ok) {  // values that nothing sees, this warp's 16 rows
+        for (int r = vis; r < 16; r++)
+          for (int e = lane; e < D / 8; e += 32)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(sb + vs * C::SLOT + (e >> 3) * (kRows * 128) +
+                                                                          (w * 16 + r) * 128 + (e & 7) * 16),
+                         "r"(0)
+                         : "memory");
+        fence_proxy_async_smem();  // before the slot's next copy
+      }
+      bar_sync(1 + team, 128);
+      met = met || seen_s[vs * 4] || seen_s[vs * 4 + 1] || seen_s[vs * 4 + 2] || seen_s[vs * 4 + 3];
+      // weights, in the first operand's layout
+      float2 sv[4][4];
+#pragma unroll
+      for (int kk = 0; kk < 4; kk++) {
+        const uint32_t a = sc + (gr * C::SLD + kk * 16 + gc) * 4;
+        sv[kk][0] = lds2(a);
+        sv[kk][1] = lds2(a + 8 * C::SLD * 4);
+        sv[kk][2] = lds2(a + 32);
+        sv[kk][3] = lds2(a + 8 * C::SLD * 4 + 32);
+      }
+      float alpha[2], neg[2];
+#pragma unroll
+      for (int r = 0; r < 2; r++) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int kk = 0; kk < 4; kk++)
+          mx = fmaxf(mx, fmaxf(fmaxf(sv[kk][r].x, sv[kk][r].y), fmaxf(sv[kk][r + 2].x, sv[kk][r + 2].y)));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[r], __fmul_rn(mx, p.c));
+        alpha[r] = mn == m[r] ? 1.f : ex2_approx(__fsub_rn(m[r], mn));
+        neg[r] = mn == -INFINITY ? 0.f : -mn;  // nothing seen yet: every weight is 2^-inf = 0
+        m[r] = mn;
+      }
+      uint32_t pa[4][4];
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int kk = 0; kk < 4; kk++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          float a, b;
+          f2_unpack(f2_fma(f2_pack(sv[kk][e].x, sv[kk][e].y), c2, f2_dup(neg[e & 1])), a, b);
+          a = ex2_approx(a);
+          b = ex2_approx(b);
+          sum[e & 1] = __fadd_rn(sum[e & 1], __fadd_rn(a, b));
+          pa[kk][e] = pack_bf16x2(a, b);
+        }
+#pragma unroll
+      for (int r = 0; r < 2; r++) l[r] = __fmaf_rn(l[r], alpha[r], sum[r]);
+#pragma unroll
+      for (int n = 0; n < C::NT; n++) {
+        o[n][0] = __fmul_rn(o[n][0], alpha[0]);
+        o[n][1] = __fmul_rn(o[n][1], alpha[0]);
+        o[n][2] = __fmul_rn(o[n][2], alpha[1]);
+        o[n][3] = __fmul_rn(o[n][3], alpha[1]);
+      }
+      // O += P V, this warp's columns
+      uint32_t dep = 0;  // (0, but known only when the last load is there)
+      if (ok) {
+        const uint32_t vb = sb + vs * C::SLOT;
+        const int vr = ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int kk = 0; kk < 4; kk++)
+#pragma unroll
+          for (int n = 0; n < C::NT; n += 2) {
+            const int ch = w * (C::CPW / 8) + n + (lane >> 4), r = kk * 16 + vr;  // 16 bytes of the row
+            uint32_t b[4];
+            ldsm_x4_t(vb + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), b);
+            mma16816(o[n], pa[kk], b[0], b[1]);
+            mma16816(o[n + 1], pa[kk], b[2], b[3]);
+            if (kk == 3 && n == C::NT - 2) dep = b[3] & p.zero;
+          }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(EMPTY0 + 8u * vs + dep);
+    }
+    // the teams' parts, joined by the first
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+      l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xffffffffu, l[r], 1));
+      l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xffffffffu, l[r], 2));
+      if (met && m[r] == -INFINITY) m[r] = kNoScore;
+    }
+    // (O in two halves, so that the buffer leaves room for the rings)
+    float fa[2], fb[2];
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+      if (team == 1) {
+        if (pieces + half > 0) bar_sync(4, kConsumers);  // what was there has been taken out
+#pragma unroll
+        for (int n = 0; n < C::NT / 2; n++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) merge[(n * 4 + e) * 128] = o[half * (C::NT / 2) + n][e];
+        if (half == 0)
+#pragma unroll
+          for (int r = 0; r < 2; r++) {
+            merge[(C::NT * 2 + r) * 128] = m[r];
+            merge[(C::NT * 2 + 2 + r) * 128] = l[r];
+          }
+        bar_sync(3, kConsumers);
+      } else {
+        bar_sync(3, kConsumers);
+        if (half == 0)
+#pragma unroll
+          for (int r = 0; r < 2; r++) {
+            const float mo = merge[(C::NT * 2 + r) * 128], lb = merge[(C::NT * 2 + 2 + r) * 128], mn = fmaxf(m[r], mo);
+            fa[r] = mn == m[r] ? 1.f : ex2_approx(__fsub_rn(m[r], mn));
+            fb[r] = mn == mo ? 1.f : ex2_approx(__fsub_rn(mo, mn));
+            l[r] = __fadd_rn(__fmul_rn(l[r], fa[r]), __fmul_rn(lb, fb[r]));
+            m[r] = mn;
+          }
+#pragma unroll
+        for (int n = 0; n < C::NT / 2; n++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            float& y = o[half * (C::NT / 2) + n][e];
+            y = __fadd_rn(__fmul_rn(y, fa[e >> 1]), __fmul_rn(merge[(n * 4 + e) * 128], fb[e >> 1]));
+          }
+        // (an arrival does not wait for loads: what they brought has been used)
+        uint32_t dep = 0;
+#pragma unroll
+        for (int n = 0; n < C::NT / 2; n++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) dep |= __float_as_uint(o[half * (C::NT / 2) + n][e]);
+        bar_arrive(4 + (dep & p.zero), kConsumers);
+      }
+    }
+    if (team == 0) {
+      const bool whole = x.k0 == 0 && x.k1 == x.nt;
+      if (!ok) {
+        // nothing of use: the status word says so
+      } else if (whole) {
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+          const int row = gr + 8 * r;
+          if (row >= heads) continue;
+          const size_t at = row0 + static_cast<size_t>(row) * D + w * C::CPW + gc;
+          const float inv = __fdiv_rn(1.f, l[r]);
+#pragma unroll
+          for (int n = 0; n < C::NT; n++) {
+            float a = __fmul_rn(o[n][2 * r], inv), b = __fmul_rn(o[n][2 * r + 1], inv);
+            if (m[r] == -INFINITY) {
+              a = b = 0.f;  // no row seen
+            } else if (p.gate) {
+              const uint32_t g = *reinterpret_cast<const uint32_t*>(p.gate + at + n * 8);
+              a = gate_mul(a, bf16_lo(g));
+              b = gate_mul(b, bf16_hi(g));
+            }
+            *reinterpret_cast<uint32_t*>(p.out + at + n * 8) = pack_bf16x2(a, b);
+          }
+        }
+      } else {
+        float* rec = p.rec + (static_cast<size_t>(blockIdx.x) * 2 + (x.k0 == 0 ? 1 : 0)) * kItem * (D + 4);
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+          const int row = gr + 8 * r;
+          if (row >= heads) continue;
+          float* at = rec + row * (D + 4) + w * C::CPW + gc;
+#pragma unroll
+          for (int n = 0; n < C::NT; n++) *reinterpret_cast<float2*>(at + n * 8) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+          if (w == 0 && gc == 0) *reinterpret_cast<float2*>(rec + row * (D + 4) + D) = make_float2(m[r], l[r]);
+        }
+      }
+    }
+    pieces++;
+  }
+  if (team == 1 && pieces > 0) bar_sync(4, kConsumers);  // (every arrival is met)
+  if (!ok && lane == 0) set_status(p.v.b.status, TV_ERR_TIMEOUT);
+}
+
+// Joins the pieces of items that were cut, in order, and writes zeros where a
+// slot sees nothing: a warp takes a part of a row, kJ pieces' loads in flight.
+template <int D>
+__global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_constant__ PagedTcParams p, int grid) {
+  constexpr int kJ = 12, CPW = D >= 128 ? 128 : 64, V = CPW / 32, PARTS = D / CPW;  // columns a warp and a lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  if (status_bad(p.v.b.status)) return;
+  const int64_t total = p.first[p.units];
+  const int ctas = ctas_for(total, grid);
+  const int64_t n = static_cast<int64_t>(p.units) * p.G * PARTS;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + warp; i < n; i += static_cast<int64_t>(gridDim.x) * 8) {
+    const int u = static_cast<int>(i / (p.G * PARTS)), r = static_cast<int>(i - static_cast<int64_t>(u) * p.G * PARTS);
+    const int head = r / PARTS, col = (r % PARTS) * CPW + lane * V;
+    const int s = u / p.v.Hkv, h = u - s * p.v.Hkv;
+    const int64_t all = p.first[u + 1] - p.first[u];
+    const size_t at = (static_cast<size_t>(s) * p.Hq + h * p.G + head) * D + col;
+    float acc[V], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; e++) acc[e] = 0.f;
+    if (all == 0) {
+      if (paged_len(p.v.b, s) < 0) continue;  // idle: left as it was
+    } else {
+      const int64_t nt = all / p.MT, t0 = p.first[u] + head / kItem * nt;
+      const int c0 = range_of(total, ctas, t0), c1 = range_of(total, ctas, t0 + nt - 1);
+      if (c0 == c1) continue;  // written whole
+      const float* rec = p.rec + static_cast<size_t>(head % kItem) * (D + 4);
+      for (int j0 = c0; j0 <= c1; j0 += kJ) {
+        float o[kJ][V];
+        float2 ml[kJ];
+#pragma unroll
+        for (int j = 0; j < kJ; j++) {
+          const int c = j0 + j;
+          const float* x = rec + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kItem * (D + 4);
+          ml[j] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int e = 0; e < V; e++) o[j][e] = 0.f;
+          if (c <= c1) {
+            ml[j] = *reinterpret_cast<const float2*>(x + D);
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              const float2 y = *reinterpret_cast<const float2*>(x + col + e);
+              o[j][e] = y.x;
+              o[j][e + 1] = y.y;
+            }
+          }
+        }
+        float mn = m;
+#pragma unroll
+        for (int j = 0; j < kJ; j++) mn = fmaxf(mn, ml[j].x);
+        const float a = m == -INFINITY ? 0.f : exp2f(__fsub_rn(m, mn));
+        l = __fmul_rn(l, a);
+#pragma unroll
+        for (int e = 0; e < V; e++) acc[e] = __fmul_rn(acc[e], a);
+#pragma unroll
+        for (int j = 0; j < kJ; j++) {
+          if (ml[j].y == 0.f) continue;  // nothing of weight in the piece (or no piece)
+          const float f = exp2f(__fsub_rn(ml[j].x, mn));
+          l = __fmaf_rn(f, ml[j].y, l);
+#pragma unroll
+          for (int e = 0; e < V; e++) acc[e] = __fmaf_rn(f, o[j][e], acc[e]);
+        }
+        m = mn;
+      }
+    }
+    const float inv = __fdiv_rn(1.f, l);
+    uint32_t y[V / 2];
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      float a = __fmul_rn(acc[e], inv), b = __fmul_rn(acc[e + 1], inv);
+      if (m == -INFINITY) {
+        a = b = 0.f;  // no row seen
+      } else if (p.gate) {
+        const uint32_t g = *reinterpret_cast<const uint32_t*>(p.gate + at + e);
+        a = gate_mul(a, bf16_lo(g));
+        b = gate_mul(b, bf16_hi(g));
+      }
+      y[e / 2] = pack_bf16x2(a, b);
+    }
+#pragma unroll
+    for (int e = 0; e < V / 2; e++) *reinterpret_cast<uint32_t*>(p.out + at + 2 * e) = y[e];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// A pool as a 2-D tensor of rows, in boxes of `rows` rows and 64 columns.
+static bool encode_pool_map(CUtensorMap* m, void* base, int D, int64_t all, int rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(all)}, strides[1] = {static_cast<cuuint64_t>(D) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(rows)}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static size_t first_bytes(const tv_paged_layer* l, const tv_paged* b) {
+  return (static_cast<size_t>(b->n_seq) * l->Hkv + 1) * 8 / 16 * 16 + 16;
+}
+size_t paged_attn_ws_bytes(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g) {
+  (void)g;
+  return first_bytes(l, b) + static_cast<size_t>(2) * num_sms() * kItem * (l->D + 4) * 4;
+}
+
+template <int D>
+static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_t st) {
+  using C = Pg<D>;
+  const tv_paged_layer* l = a.layer;
+  p.R = l->page < kRows ? l->page : kRows;
+  const int64_t all = static_cast<int64_t>(l->n_pages) * l->Hkv * l->page;
+  if (!encode_pool_map(&p.tmK, l->K, D, all, p.R) || !encode_pool_map(&p.tmV, l->V, D, all, p.R)) return TV_ERR_CUDA;
+  static std::atomic<uint64_t> set{0};
+  if (!allow_smem(attn_paged_tc_kernel<D>, C::SMEM, set)) return TV_ERR_CUDA;
+  const int grid = num_sms();
+  launch_k(true, attn_paged_tc_kernel<D>, dim3(grid), dim3(kThreads), C::SMEM, st, p);
+  const int64_t warps = static_cast<int64_t>(p.units) * p.G * (D > 128 ? D / 128 : 1);
+  const int join = static_cast<int>(warps + 7 < static_cast<int64_t>(16) * grid ? (warps + 7) / 8 : 2 * grid);
+  launch_k(true, attn_paged_join_kernel<D>, dim3(join), dim3(256), 0, st, p, grid);
+  return launch_status();
+}
+
+tv_status paged_attn_tc_launch(const PagedAttnCall& a, cudaStream_t st) {
+  const tv_paged_layer* l = a.layer;
+  if (!a.ws || a.ws_bytes < paged_attn_ws_bytes(l, a.batch, a.groups)) return TV_ERR_WORKSPACE;
+  PagedTcParams p;
+  memset(&p, 0, sizeof(p));
+  p.v = PagedView{paged_seqs(l, a.batch), a.sel, a.count, a.n_sel, l->Hkv};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.gate = static_cast<const __nv_bfloat16*>(a.gate);
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.first = static_cast<int64_t*>(a.ws);
+  p.rec = reinterpret_cast<float*>(static_cast<char*>(a.ws) + first_bytes(l, a.batch));
+  p.Hq = l->Hq;
+  p.G = l->Hq / l->Hkv;
+  p.MT = (p.G + kItem - 1) / kItem;
+  p.units = a.batch->n_seq * l->Hkv;
+  p.c = a.scale * 1.4426950408889634f;
+  switch (l->D) {
+    case 64: return launch_tc<64>(p, a, st);
+    case 128: return launch_tc<128>(p, a, st);
+    default: return launch_tc<256>(p, a, st);
+  }
+}
+
+}  // namespace tv

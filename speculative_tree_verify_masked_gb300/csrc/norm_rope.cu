@@ -1,6 +1,7 @@
 // Head norms of queries and keys with the rotation in the same pass, for a
 // tree's nodes, for decode tokens and for a prompt's packed rows; a prompt's
-// keys and values go straight into the cache rows they belong to.
+// keys and values go straight into the cache rows they belong to, contiguous
+// or in pages.
 //
 //   y = x / sqrt(mean(x^2) + eps) * w     (per head, w the query or key weights)
 //   planes (j, j + rot/2) of y turn by pos * theta^(-2j/rot), the rest pass
@@ -30,6 +31,7 @@
 // tokens: 3.5 us, a launch's latency.
 #include <cmath>
 
+#include "paged.cuh"
 #include "prompt.cuh"
 
 namespace tv {
@@ -49,7 +51,8 @@ struct NormRopeParams {
   const float* k_norm;
   const int32_t* node_off;
   const void* meta;
-  int form;  // 0 tree, 1 decode, 2 prompt
+  PagedSeqs pg;  // paged form: K[0] and V[0] are the pools
+  int form;  // 0 tree, 1 decode, 2 prompt, 3 paged (a row a slot), 4 paged (packed rows)
   int n_rows, n_seq, n_total, Hq, Hkv, rot, max_len, cap;
   int heads_per_warp, q_parts, k_parts, parts;  // warps a row: for queries, for keys, the rest for values
   float eps;
@@ -86,7 +89,40 @@ struct Raw8<float> {
   __device__ __forceinline__ f2_t pair(int i) const { return f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])); }
 };
 
-template <typename T, int D>
+// The slot that packed row `row` belongs to, with its offsets: two looks at 32
+// of them side by side for up to 1,024 slots.  (Offsets that fall are found by
+// the rows that meet them, and by no other: every row checks its own slot's.)
+struct PagedRow {
+  int s, off, n;  // s -1: padding behind the last row, or offsets that are not allowed
+};
+__device__ __forceinline__ PagedRow paged_row(const PagedSeqs& b, const int32_t* row_off, int n_total, int n_max, int row, int lane) {
+  int s = 0;
+  for (int step = b.n_seq > 32 ? 32 : 1;; step = 1) {
+    const int i = s + lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, i <= b.n_seq && row_off[i] <= row);
+    s += m ? (31 - __clz(static_cast<int>(m))) * step : 0;
+    if (step == 1) break;
+  }
+  // (the last of 32 looks may be followed by a boundary: n_seq = 32 k)
+  if (s < b.n_seq && row_off[s + 1] <= row) s++;
+  PagedRow r{-1, 0, 0};
+  const int all = row_off[b.n_seq];
+  if (row_off[0] != 0 || all > n_total) {
+    if (lane == 0) set_status(b.status, TV_ERR_ROWS);
+    return r;
+  }
+  if (s >= b.n_seq) return r;  // padding
+  r.off = row_off[s];
+  r.n = row_off[s + 1] - r.off;
+  if (r.n < 0 || r.n > n_max || row < r.off || row >= r.off + r.n) {
+    if (lane == 0) set_status(b.status, TV_ERR_ROWS);
+    return r;
+  }
+  r.s = s;
+  return r;
+}
+
+template <typename T, int D, bool PAGED>
 __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 5 : 4) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPH = D / 8;                  // lanes per head
   constexpr int GPW = 32 / LPH;               // heads a warp holds at once
@@ -113,7 +149,27 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 5 : 4) norm_rope_kernel(
   // the row's sequence, position and (prompt) cache row
   const bool bad = status_bad(p.pr.status);
   int s, pos;
-  if (p.form == 2) {
+  if constexpr (PAGED) {
+    if (bad) return;
+    int i = 0;
+    s = row;
+    if (p.form == 4) {
+      const PagedRow r = paged_row(p.pg, p.pr.row_off, p.n_total, p.pr.n_max, row, lane);
+      if (r.s < 0) return;
+      s = r.s;
+      i = row - r.off;
+    }
+    const int len = paged_len(p.pg, s);
+    if (len < 0) {
+      if (p.form == 4 && lane == 0) set_status(p.pr.status, TV_ERR_ROWS);  // rows of an idle slot
+      return;
+    }
+    pos = len + i;
+    if ((pos >> p.pg.shift) >= p.pg.cols) {
+      if (lane == 0) set_status(p.pr.status, TV_ERR_CAPACITY);
+      return;
+    }
+  } else if (p.form == 2) {
     const WarpSeqs w = load_seqs(p.pr, lane);
     if (w.code || bad) {
       if (lane == 0 && w.code) set_status(p.pr.status, w.code);
@@ -143,6 +199,11 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 5 : 4) norm_rope_kernel(
   size_t step = D;
   if (kind == 0) {
     dst = static_cast<T*>(p.q) + static_cast<size_t>(row) * H * D + d0;
+  } else if (PAGED) {
+    const int page = page_at(p.pg, s, pos >> p.pg.shift), r = pos & ((1 << p.pg.shift) - 1);
+    if (page < 0) return;
+    dst = static_cast<T*>(kind == 1 ? p.K[0] : p.V[0]) + ((static_cast<size_t>(page) * H << p.pg.shift) + r) * D + d0;
+    step = static_cast<size_t>(D) << p.pg.shift;
   } else if (p.form != 2) {
     dst = static_cast<T*>(p.k) + static_cast<size_t>(row) * H * D + d0;
   } else {
@@ -259,6 +320,20 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 5 : 4) norm_rope_kernel(
 }
 
 // What the calls share: shape checks, rates, launch.
+template <bool PAGED>
+static void norm_rope_enqueue(int D, bool bf, dim3 g, cudaStream_t st, const NormRopeParams& p) {
+  switch (D) {
+    case 64:
+      if (bf) launch_k(true, norm_rope_kernel<__nv_bfloat16, 64, PAGED>, g, dim3(128), 0, st, p); else launch_k(true, norm_rope_kernel<float, 64, PAGED>, g, dim3(128), 0, st, p);
+      break;
+    case 128:
+      if (bf) launch_k(true, norm_rope_kernel<__nv_bfloat16, 128, PAGED>, g, dim3(128), 0, st, p); else launch_k(true, norm_rope_kernel<float, 128, PAGED>, g, dim3(128), 0, st, p);
+      break;
+    default:
+      if (bf) launch_k(true, norm_rope_kernel<__nv_bfloat16, 256, PAGED>, g, dim3(128), 0, st, p); else launch_k(true, norm_rope_kernel<float, 256, PAGED>, g, dim3(128), 0, st, p);
+  }
+}
+
 static tv_status norm_rope_launch(const tv_attn_layer* l, NormRopeParams& p, const float* q_norm, const float* k_norm,
                                   float eps, int rot, float theta, cudaStream_t st) {
   p.q_norm = q_norm;
@@ -284,7 +359,7 @@ static tv_status norm_rope_launch(const tv_attn_layer* l, NormRopeParams& p, con
   auto split = [&]() {
     p.q_parts = (l->Hq + hpw - 1) / hpw;
     p.k_parts = (l->Hkv + hpw - 1) / hpw;
-    p.parts = p.q_parts + p.k_parts + (p.form == 2 ? p.k_parts : 0);
+    p.parts = p.q_parts + p.k_parts + (p.form >= 2 ? p.k_parts : 0);
     return static_cast<int64_t>(p.n_rows) * p.parts;
   };
   while (hpw > 4 * gpw && split() < 16 * num_sms()) hpw >>= 1;
@@ -293,16 +368,8 @@ static tv_status norm_rope_launch(const tv_attn_layer* l, NormRopeParams& p, con
   if (p.parts > 65535) return TV_ERR_SHAPE;
   const dim3 g(static_cast<unsigned>((p.n_rows + 3) / 4), static_cast<unsigned>(p.parts));
   const bool bf = l->dtype == TV_BF16;
-  switch (l->D) {
-    case 64:
-      if (bf) launch_k(true, norm_rope_kernel<__nv_bfloat16, 64>, g, dim3(128), 0, st, p); else launch_k(true, norm_rope_kernel<float, 64>, g, dim3(128), 0, st, p);
-      break;
-    case 128:
-      if (bf) launch_k(true, norm_rope_kernel<__nv_bfloat16, 128>, g, dim3(128), 0, st, p); else launch_k(true, norm_rope_kernel<float, 128>, g, dim3(128), 0, st, p);
-      break;
-    default:
-      if (bf) launch_k(true, norm_rope_kernel<__nv_bfloat16, 256>, g, dim3(128), 0, st, p); else launch_k(true, norm_rope_kernel<float, 256>, g, dim3(128), 0, st, p);
-  }
+  if (p.form >= 3) norm_rope_enqueue<true>(l->D, bf, g, st, p);
+  else norm_rope_enqueue<false>(l->D, bf, g, st, p);
   return launch_status();
 }
 
@@ -399,4 +466,47 @@ extern "C" tv_status tv_attn_prompt_front(const tv_attn_layer* l, const tv_promp
   p.v_raw = v;
   p.q = q;
   return norm_rope_launch(l, p, q_norm, k_norm, eps, rot_dims, theta, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" tv_status tv_paged_append(const tv_paged_layer* l, const tv_paged* b, const tv_paged_rows* rows,
+                                     const float* q_norm, const float* k_norm, float eps, int32_t rot_dims, float theta,
+                                     const void* q_raw, const void* k_raw, const void* v, void* q, tv_stream stream) {
+  tv_status c = paged_check(l, b);
+  if (c == TV_OK) c = paged_rows_check(rows);
+  if (c != TV_OK) return c;
+  if (!l->K || !l->V) return TV_ERR_ARG;
+  const tv_attn_layer a{l->dtype, l->Hq, l->Hkv, l->D, b->max_len + 1, nullptr, nullptr};
+  c = norm_rope_check(&a, b->max_len, q_norm, k_norm, eps, rot_dims, theta);
+  if (c != TV_OK) return c;
+  const int64_t n = rows ? rows->n_total : b->n_seq;
+  if (n == 0) return TV_OK;
+  if (!q_raw || !k_raw || !v || !q) return TV_ERR_ARG;
+  if (!aligned16(q_raw) || !aligned16(k_raw) || !aligned16(v) || !aligned16(q)) return TV_ERR_ALIGN;
+  if (!in_place_or_apart(&a, n, l->Hq, q, q_raw, l->Hkv, k_raw) || !in_place_or_apart(&a, n, l->Hq, q, q_raw, l->Hkv, v))
+    return TV_ERR_ARG;
+  // rows are read while others are written: the pools lie apart from them and from each other
+  const size_t pool = bytes_of(static_cast<int64_t>(l->n_pages) * l->Hkv * l->page, l->D, l->dtype);
+  const size_t nq = bytes_of(n, static_cast<int64_t>(l->Hq) * l->D, l->dtype), nk = bytes_of(n, static_cast<int64_t>(l->Hkv) * l->D, l->dtype);
+  for (const void* x : {l->K, l->V})
+    if (share_memory(x, pool, q_raw, nq) || share_memory(x, pool, q, nq) || share_memory(x, pool, k_raw, nk) ||
+        share_memory(x, pool, v, nk))
+      return TV_ERR_ARG;
+  if (share_memory(l->K, pool, l->V, pool)) return TV_ERR_ARG;
+  NormRopeParams p{};
+  p.form = rows ? 4 : 3;
+  p.pg = paged_seqs(l, b);
+  p.pr.status = b->status;
+  if (rows) {
+    p.pr.row_off = rows->row_off;
+    p.pr.n_max = rows->n_max;
+  }
+  p.K[0] = l->K;
+  p.V[0] = l->V;
+  p.n_rows = p.n_total = static_cast<int>(n);
+  p.n_seq = b->n_seq;
+  p.q_raw = q_raw;
+  p.k_raw = k_raw;
+  p.v_raw = v;
+  p.q = q;
+  return norm_rope_launch(&a, p, q_norm, k_norm, eps, rot_dims, theta, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -1,0 +1,91 @@
+// Caches in pages, as the kernels and the entry points see them: row
+// j * page + r of sequence s is row r of page table[s][j] of the pools
+// [n_pages][Hkv][page][D].  Tables and lengths live on the device, so every
+// kernel checks what it uses of them before it touches a row.
+#pragma once
+#include <atomic>
+#include <cmath>
+
+#include "common.cuh"
+#include "host.hpp"
+
+namespace tv {
+
+struct PagedSeqs {
+  const int32_t* table;  // [n_seq][cols]
+  const int32_t* len;    // [n_seq], -1: an idle slot
+  int32_t* status;
+  int n_seq, cols, max_len, n_pages;
+  int shift;  // log2 of a page's rows
+};
+
+// Rows a slot holds before this step, -1 where it is idle or its length is not allowed.
+__device__ __forceinline__ int paged_len(const PagedSeqs& b, int s) {
+  const int L = b.len[s];
+  if (L < -1 || L > b.max_len) {
+    set_status(b.status, TV_ERR_LEN);
+    return -1;
+  }
+  return L;
+}
+// The page that column j of a table row names, -1 (and the status word set) where it names none.
+__device__ __forceinline__ int page_at(const PagedSeqs& b, int s, int j) {
+  const int id = b.table[static_cast<size_t>(s) * b.cols + j];
+  if (id >= 0 && id < b.n_pages) return id;
+  set_status(b.status, TV_ERR_PAGE);
+  return -1;
+}
+
+// ---------------------------------------------------------------------------
+// the host's half
+// ---------------------------------------------------------------------------
+constexpr int kMaxPagedUnits = (1 << 16) - 1;  // (slot, KV head) pairs of one call
+
+inline int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : 0; }
+
+// What every paged call asks of its layer and batch.
+inline tv_status paged_check(const tv_paged_layer* l, const tv_paged* b) {
+  if (!l || !b || !b->table || !b->len || !b->status) return TV_ERR_ARG;
+  if (l->dtype != TV_F32 && l->dtype != TV_BF16) return TV_ERR_DTYPE;
+  if (l->Hq < 1 || l->Hkv < 1 || l->Hq % l->Hkv || l->Hq > 4096 || l->Hq / l->Hkv > 128 ||
+      (l->D != 64 && l->D != 128 && l->D != 256) || !page_shift(l->page))
+    return TV_ERR_SHAPE;
+  if (b->n_seq < 1 || b->n_seq > TV_MAX_PAGED_SEQ || b->cols < 1 || b->max_len < 0 || l->n_pages < 1 ||
+      static_cast<int64_t>(b->cols) * l->page <= b->max_len || static_cast<int64_t>(b->cols) * l->page > (1ll << 30) ||
+      static_cast<int64_t>(l->n_pages) * l->Hkv * l->page >= (1ll << 31))
+    return TV_ERR_ARG;
+  if (static_cast<int64_t>(b->n_seq) * l->Hkv > kMaxPagedUnits) return TV_ERR_SHAPE;
+  if (!aligned16(b->table) || !aligned16(b->len) || !aligned16(b->status) || !aligned16(l->K) || !aligned16(l->V))
+    return TV_ERR_ALIGN;
+  return TV_OK;
+}
+inline PagedSeqs paged_seqs(const tv_paged_layer* l, const tv_paged* b) {
+  return PagedSeqs{b->table, b->len, b->status, b->n_seq, b->cols, b->max_len, l->n_pages, page_shift(l->page)};
+}
+inline tv_status paged_rows_check(const tv_paged_rows* r) {
+  if (!r) return TV_OK;
+  if (!r->row_off || r->n_total < 0 || r->n_total > TV_MAX_PROMPT_ROWS || r->n_max < 0 || r->n_max > r->n_total)
+    return TV_ERR_ARG;
+  return aligned16(r->row_off) ? TV_OK : TV_ERR_ALIGN;
+}
+
+// Lets a kernel have more than 48 KB of shared memory, once a device.
+template <typename K>
+inline bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
+// Bytes of [rows][cols] values of type dt.
+inline size_t bytes_of(int64_t rows, int64_t cols, tv_dtype dt) { return static_cast<size_t>(rows * cols) * (dt == TV_BF16 ? 2 : 4); }
+inline bool share_memory(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+}  // namespace tv
