@@ -22,6 +22,8 @@ struct PagedAttnCall {
 size_t paged_attn_ws_bytes(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g);
 tv_status paged_attn_tc_launch(const PagedAttnCall& a, cudaStream_t st);
 
+constexpr float kNoScore = -3.402823466e38f;  // the maximum of a row that sees keys, none with a score above -inf
+
 // The pages that a slot's queries look at, in order: all up to the row's own,
 // or the listed ones.
 struct PagedView {

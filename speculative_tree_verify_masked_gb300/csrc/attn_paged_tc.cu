@@ -35,6 +35,7 @@
 #include <cstring>
 
 #include "attn_paged.cuh"
+#include "attn_paged_prefix.cuh"
 #include "mma_tile.cuh"
 #include "ptx.cuh"
 #include "tensor_map.hpp"
@@ -44,7 +45,6 @@ namespace tv {
 constexpr int kRows = 64;    // rows of a key tile
 constexpr int kItem = 16;    // query rows of an item
 constexpr int kConsumers = 256, kThreads = kConsumers + 32;
-constexpr float kNoScore = -3.402823466e38f;  // the maximum of a row that sees keys, none with a score above -inf
 
 template <int D>
 struct Pg {
@@ -66,12 +66,16 @@ struct Pg {
 struct PagedTcParams {
   CUtensorMap tmK, tmV;  // pools as [rows][D], boxes of R rows, 64 columns
   PagedView v;
-  const int32_t* start;  // [n_seq] rows that another kernel has seen to, or null
+  const int32_t* start;  // [n_seq] rows that the kernel for shared prefixes has seen to, or null
   const __nv_bfloat16* q;
   const __nv_bfloat16* gate;
   __nv_bfloat16* out;
   int64_t* first;  // [units + 1] each unit's first tile in the order of all
   float* rec;      // [2 * CTAs][16][D + 4]
+  float* rec_item;  // [items][16][D + 4]: items of slots with a shared prefix
+  const float* rec_prefix;  // [pieces][128][D + 4]
+  const int4* info;         // [groups] and
+  const int32_t* group_of;  // [n_seq], as the kernel for shared prefixes left them
   int Hq, G, MT, units;  // MT items a unit
   int R;  // rows of a box: a page, or 64 of one of 128
   float c;        // scale * log2(e)
@@ -497,10 +501,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       }
     }
     if (team == 0) {
-      const bool whole = x.k0 == 0 && x.k1 == x.nt;
+      const bool whole = x.k0 == 0 && x.k1 == x.nt, alone = !p.start || p.start[x.s] == 0;
       if (!ok) {
         // nothing of use: the status word says so
-      } else if (whole) {
+      } else if (whole && alone) {
 #pragma unroll
         for (int r = 0; r < 2; r++) {
           const int row = gr + 8 * r;
@@ -521,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
           }
         }
       } else {
-        float* rec = p.rec + (static_cast<size_t>(blockIdx.x) * 2 + (x.k0 == 0 ? 1 : 0)) * kItem * (D + 4);
+        float* rec = whole ? p.rec_item + (static_cast<size_t>(x.s * p.v.Hkv + x.h) * p.MT + x.m) * kItem * (D + 4)
+                           : p.rec + (static_cast<size_t>(blockIdx.x) * 2 + (x.k0 == 0 ? 1 : 0)) * kItem * (D + 4);
 #pragma unroll
         for (int r = 0; r < 2; r++) {
           const int row = gr + 8 * r;
@@ -550,8 +555,8 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_const
   const int64_t total = p.first[p.units];
   const int ctas = ctas_for(total, grid);
   const int64_t n = static_cast<int64_t>(p.units) * p.G * PARTS;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + warp; i < n; i += static_cast<int64_t>(gridDim.x) * 8) {
-    const int u = static_cast<int>(i / (p.G * PARTS)), r = static_cast<int>(i - static_cast<int64_t>(u) * p.G * PARTS);
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + warp; w < n; w += static_cast<int64_t>(gridDim.x) * 8) {
+    const int u = static_cast<int>(w / (p.G * PARTS)), r = static_cast<int>(w - static_cast<int64_t>(u) * p.G * PARTS);
     const int head = r / PARTS, col = (r % PARTS) * CPW + lane * V;
     const int s = u / p.v.Hkv, h = u - s * p.v.Hkv;
     const int64_t all = p.first[u + 1] - p.first[u];
@@ -564,19 +569,32 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_const
     } else {
       const int64_t nt = all / p.MT, t0 = p.first[u] + head / kItem * nt;
       const int c0 = range_of(total, ctas, t0), c1 = range_of(total, ctas, t0 + nt - 1);
-      if (c0 == c1) continue;  // written whole
-      const float* rec = p.rec + static_cast<size_t>(head % kItem) * (D + 4);
-      for (int j0 = c0; j0 <= c1; j0 += kJ) {
+      const float *rec = p.rec + static_cast<size_t>(head % kItem) * (D + 4), *pre = nullptr;
+      int np = 0;  // pieces of the shared prefix, which come first
+      size_t step = 0;
+      if (p.start && p.start[s] > 0) {
+        const int4 g = p.info[p.group_of[s]];
+        const int row = (s - g.w) * p.G + head;
+        np = g.z;
+        step = static_cast<size_t>(g.y) * 128 * (D + 4);
+        pre = p.rec_prefix + (static_cast<size_t>(g.x + h * np * g.y + row / 128) * 128 + row % 128) * (D + 4);
+      } else if (c0 == c1) {
+        continue;  // written whole
+      }
+      const int n_rec = np + c1 - c0 + 1;
+      for (int j0 = 0; j0 < n_rec; j0 += kJ) {
         float o[kJ][V];
         float2 ml[kJ];
 #pragma unroll
         for (int j = 0; j < kJ; j++) {
-          const int c = j0 + j;
-          const float* x = rec + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kItem * (D + 4);
+          const int i = j0 + j, c = c0 + i - np;
+          const float* x = i < np ? pre + step * i
+                           : c0 == c1 ? p.rec_item + ((static_cast<size_t>(u) * p.MT + head / kItem) * kItem + head % kItem) * (D + 4)
+                                      : rec + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kItem * (D + 4);
           ml[j] = make_float2(-INFINITY, 0.f);
 #pragma unroll
           for (int e = 0; e < V; e++) o[j][e] = 0.f;
-          if (c <= c1) {
+          if (i < n_rec) {
             ml[j] = *reinterpret_cast<const float2*>(x + D);
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
@@ -636,13 +654,33 @@ static bool encode_pool_map(CUtensorMap* m, void* base, int D, int64_t all, int 
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static size_t first_bytes(const tv_paged_layer* l, const tv_paged* b) {
-  return (static_cast<size_t>(b->n_seq) * l->Hkv + 1) * 8 / 16 * 16 + 16;
+// A call's scratch, in bytes from its start.
+struct PagedSpace {
+  size_t rec, rec_item, rec_prefix, info, group_of, start, all;
+};
+static PagedSpace space_of(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g) {
+  const size_t line = static_cast<size_t>(l->D + 4) * 4, units = static_cast<size_t>(b->n_seq) * l->Hkv;
+  const size_t items = units * ((l->Hq / l->Hkv + kItem - 1) / kItem);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t x = at;
+    at += (n + 15) / 16 * 16;
+    return x;
+  };
+  PagedSpace s{};
+  take((units + 1) * 8);
+  s.rec = take(static_cast<size_t>(2) * num_sms() * kItem * line);
+  if (g) {
+    s.rec_item = take(items * kItem * line);
+    s.rec_prefix = take(static_cast<size_t>(paged_prefix_slots(l, b, g->n_group)) * 128 * line);
+    s.info = take(static_cast<size_t>(g->n_group) * 16);
+    s.group_of = take(static_cast<size_t>(b->n_seq) * 4);
+    s.start = take(static_cast<size_t>(b->n_seq) * 4);
+  }
+  s.all = at;
+  return s;
 }
-size_t paged_attn_ws_bytes(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g) {
-  (void)g;
-  return first_bytes(l, b) + static_cast<size_t>(2) * num_sms() * kItem * (l->D + 4) * 4;
-}
+size_t paged_attn_ws_bytes(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g) { return space_of(l, b, g).all; }
 
 template <int D>
 static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_t st) {
@@ -654,6 +692,29 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
   static std::atomic<uint64_t> set{0};
   if (!allow_smem(attn_paged_tc_kernel<D>, C::SMEM, set)) return TV_ERR_CUDA;
   const int grid = num_sms();
+  if (a.groups) {
+    PagedPrefixParams x;
+    memset(&x, 0, sizeof(x));
+    x.tmK = p.tmK;
+    x.tmV = p.tmV;
+    x.b = p.v.b;
+    x.group_off = a.groups->group_off;
+    x.shared = a.groups->shared;
+    x.q = p.q;
+    x.rec = const_cast<float*>(p.rec_prefix);
+    x.info = const_cast<int4*>(p.info);
+    x.group_of = const_cast<int32_t*>(p.group_of);
+    x.start = const_cast<int32_t*>(p.start);
+    x.n_group = a.groups->n_group;
+    x.slots = paged_prefix_slots(l, a.batch, x.n_group);
+    x.Hq = p.Hq;
+    x.Hkv = l->Hkv;
+    x.G = p.G;
+    x.R = p.R;
+    x.all_rows = static_cast<int>(all);
+    x.c = p.c;
+    if (!paged_prefix_launch(x, D, st)) return TV_ERR_CUDA;
+  }
   launch_k(true, attn_paged_tc_kernel<D>, dim3(grid), dim3(kThreads), C::SMEM, st, p);
   const int64_t warps = static_cast<int64_t>(p.units) * p.G * (D > 128 ? D / 128 : 1);
   const int join = static_cast<int>(warps + 7 < static_cast<int64_t>(16) * grid ? (warps + 7) / 8 : 2 * grid);
@@ -670,8 +731,17 @@ tv_status paged_attn_tc_launch(const PagedAttnCall& a, cudaStream_t st) {
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.gate = static_cast<const __nv_bfloat16*>(a.gate);
   p.out = static_cast<__nv_bfloat16*>(a.out);
-  p.first = static_cast<int64_t*>(a.ws);
-  p.rec = reinterpret_cast<float*>(static_cast<char*>(a.ws) + first_bytes(l, a.batch));
+  char* ws = static_cast<char*>(a.ws);
+  const PagedSpace x = space_of(l, a.batch, a.groups);
+  p.first = reinterpret_cast<int64_t*>(ws);
+  p.rec = reinterpret_cast<float*>(ws + x.rec);
+  if (a.groups) {
+    p.rec_item = reinterpret_cast<float*>(ws + x.rec_item);
+    p.rec_prefix = reinterpret_cast<const float*>(ws + x.rec_prefix);
+    p.info = reinterpret_cast<const int4*>(ws + x.info);
+    p.group_of = reinterpret_cast<const int32_t*>(ws + x.group_of);
+    p.start = reinterpret_cast<const int32_t*>(ws + x.start);
+  }
   p.Hq = l->Hq;
   p.G = l->Hq / l->Hkv;
   p.MT = (p.G + kItem - 1) / kItem;

@@ -65,6 +65,48 @@ def test_attn_long_pieces(heads, page):
     assert p.status() == 0
 
 
+GROUPS = [
+    ("one group", [300, 257, 256, 900], [(4, 256)]),
+    ("groups and lone slots", [700, 640, 700, 5, 64, 1300, 1290, 1280], [(3, 640), (1, 0), (1, 64), (3, 1280)]),
+    ("idle members, an empty group", [-1, 400, 384, -1, 500, -1, 300, 384], [(5, 384), (0, 128), (3, 0)]),
+    ("one active member", [-1, 400, -1, 70], [(3, 384), (1, 64)]),
+    ("nothing shared", [400, 0, 1, -1], [(2, 0), (2, 0)]),
+    ("many members", [128 + (i * 31) % 150 for i in range(90)], [(50, 128), (40, 128)]),
+    ("long", [20000 + 128 * 3 + i for i in range(9)], [(9, 19968)]),
+    ("many groups", [128 + i % 3 for i in range(240)], [(2, 128)] * 120),
+]
+
+
+@pytest.mark.parametrize("name,lens,groups", GROUPS, ids=[g[0] for g in GROUPS])
+@pytest.mark.parametrize("heads,page", [((24, 4, 256), 64), ((24, 4, 256), 16), ((16, 2, 128), 32), ((16, 2, 128), 128), ((8, 8, 64), 64),
+                                        ((40, 1, 64), 16)])
+def test_attn_groups(heads, page, name, lens, groups):
+    if page == 128:
+        groups = [(m, s // 128 * 128) for m, s in groups]
+    p = Pools(lens, page, heads, seed=page, groups=groups)
+    slots = range(0, len(lens), max(1, len(lens) // 9))
+    gate = p.gate if "long" in name else None
+    p.expect(p.attn(gate, p.groups), gate, slots=slots)
+    got = p.out.clone()
+    p.out.fill_(7.0)
+    for _ in range(3):
+        assert torch.equal(got, p.attn(gate, p.groups))
+    assert p.status() == 0
+
+
+def test_attn_groups_prefix_tiles_end_inside():
+    """Prefixes of every number of pages up to two tiles of keys and a page more."""
+    for n in range(1, 18):
+        p = Pools([16 * n + 3, 16 * n, 16 * n + 40], 16, (12, 2, 128), seed=n, groups=[(3, 16 * n)])
+        p.expect(p.attn(None, p.groups))
+        assert p.status() == 0
+
+
+def test_attn_groups_fp32():
+    p = Pools([300, 256, 256 + 17], 32, (4, 2, 128), F32, groups=[(3, 256)])
+    p.expect(p.attn(p.gate, p.groups), p.gate)
+
+
 def test_attn_many_slots():
     p = Pools([(i * 37) % 90 for i in range(1024)], 16, (4, 2, 64), seed=1)
     p.expect(p.attn(), slots=range(0, 1024, 53))
