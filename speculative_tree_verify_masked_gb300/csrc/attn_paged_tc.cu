@@ -1,8 +1,8 @@
 // Decode attention over bf16 caches in pages, on the tensor cores.
 //
 // A unit is one slot and KV head: its G query heads (16 at a time, an item)
-// against the keys and values that the slot sees, in tiles of 64 rows.  Each tile
-// is used by 16 rows of queries at most, so the call is bound by the reads of
+// against the keys and values that the slot sees, in tiles of 64 rows (128
+// of 64 columns).  Each tile is used by 16 rows of queries at most, so the call is bound by the reads of
 // keys and values; the products run on warp-level tiles (16 x 8 x 16), which
 // waste least on so few rows.  An item runs flash style:
 //   S = Q K^T, m = running maximum of the scaled scores, p = 2^(s c - m) rounded
@@ -42,65 +42,72 @@
 
 namespace tv {
 
-constexpr int kRows = 64;    // rows of a key tile
 constexpr int kItem = 16;    // query rows of an item
 constexpr int kConsumers = 256, kThreads = kConsumers + 32;
 
 template <int D>
 struct Pg {
-  static constexpr int SLOT = kRows * D * 2;             // a tile of keys or of values
-  static constexpr int NS = D == 256 ? 3 : D == 128 ? 6 : 8;  // slots of a team's ring
+  // Rows of a key tile: with 64 columns a tile of 64 rows is over before the next
+  // barrier: 8 slots of 65,536 rows, 8 + 8 heads of 64, 171 us with 128 rows, 296 with 64.
+  static constexpr int ROWS = D == 64 ? 128 : 64;
+  static constexpr int WR = ROWS / 4, SG = ROWS / 16;    // rows a warp scores, groups of 16 rows
+  static constexpr int SLOT = ROWS * D * 2;              // a tile of keys or of values
+  static constexpr int NS = D == 256 ? 3 : D == 128 ? 6 : 5;  // slots of a team's ring
   static constexpr int CPW = D / 4, NT = CPW / 8;        // columns of O a warp, in tiles of 8
-  static constexpr int SLD = 72;                         // floats of a row of scores (conflict-free pairs)
+  static constexpr int SLD = ROWS + 8;                   // floats of a row of scores (conflict-free pairs)
   static constexpr int SBUF = kItem * SLD * 4;
   static constexpr int SOFF = 2 * NS * SLOT;             // scores [team][2]
   static constexpr int MOFF = SOFF + 4 * SBUF;           // the second team's m, l and half of O on their way to the first
   static constexpr int MREG = NT * 2 + 4;
-  static constexpr int VOFF = MOFF + 128 * MREG * 4;     // rows seen of each 16 of a slot's tile: [2 NS][4]
-  static constexpr int BOFF = VOFF + 2 * NS * 16;
+  static constexpr int VOFF = MOFF + 128 * MREG * 4;     // rows seen of each 16 of a slot's tile: [2 NS][SG]
+  static constexpr int BOFF = VOFF + 2 * NS * SG * 4;
   static constexpr int LOFF = BOFF + 4 * NS * 8;
   static constexpr int SMEM = LOFF + 256;
   static_assert(SMEM <= 232448, "shared memory");
 };
 
 struct PagedTcParams {
-  CUtensorMap tmK, tmV;  // pools as [rows][D], boxes of R rows, 64 columns
+  CUtensorMap tmK, tmV;  // pools as [D / 64][rows][64], boxes of R whole rows
   PagedView v;
   const int32_t* start;  // [n_seq] rows that the kernel for shared prefixes has seen to, or null
   const __nv_bfloat16* q;
   const __nv_bfloat16* gate;
   __nv_bfloat16* out;
-  int64_t* first;  // [units + 1] each unit's first tile in the order of all
+  int64_t* first;  // [units + 1] each unit's first tile in the order of all (with shared prefixes)
+  int4* cut;       // [CTAs] the item that a CTA's range starts within, where it is the item's first cut:
+                   // slot, KV head, its 16 heads, last CTA; -1: none
   float* rec;      // [2 * CTAs][16][D + 4]
   float* rec_item;  // [items][16][D + 4]: items of slots with a shared prefix
   const float* rec_prefix;  // [pieces][128][D + 4]
   const int4* info;         // [groups] and
   const int32_t* group_of;  // [n_seq], as the kernel for shared prefixes left them
   int Hq, G, MT, units;  // MT items a unit
-  int R;  // rows of a box: a page, or 64 of one of 128
+  int R;  // rows of a box: a page's, or a tile's
   float c;        // scale * log2(e)
   uint32_t zero;  // 0
 };
 
 // Tiles of an item of unit u.
+template <int ROWS>
 __device__ __forceinline__ int unit_tiles(const PagedTcParams& p, int u) {
   const int s = u / p.v.Hkv, L = paged_len(p.v.b, s);
   if (L < 0) return 0;
-  if (p.v.sel) return ((p.v.pages(s, u - s * p.v.Hkv, L) << p.v.b.shift) + kRows - 1) / kRows;
-  return (L + 1 - (p.start ? p.start[s] : 0) + kRows - 1) / kRows;
+  if (p.v.sel) return ((p.v.pages(s, u - s * p.v.Hkv, L) << p.v.b.shift) + ROWS - 1) / ROWS;
+  return (L + 1 - (p.start ? p.start[s] : 0) + ROWS - 1) / ROWS;
 }
 
 // The items of a range of tiles, one after another.
 struct PagedPiece {
   int s, h, m, k0, k1, nt;  // slot, KV head, 16 query heads, tiles [k0, k1) of nt
 };
+template <int ROWS>
 struct PagedWalk {
   int u;        // unit
   int64_t off;  // tile within the unit, over its items
   int64_t left;
   __device__ __forceinline__ bool next(const PagedTcParams& p, PagedPiece& x) {
     while (left > 0 && u < p.units) {
-      const int nt = unit_tiles(p, u);
+      const int nt = unit_tiles<ROWS>(p, u);
       const int64_t all = static_cast<int64_t>(nt) * p.MT;
       if (off >= all) {
         off = 0;
@@ -147,8 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   int32_t* seen_s = reinterpret_cast<int32_t*>(smem_raw + C::VOFF);
   struct Local {
     int64_t sums[9];  // tiles of each warp's units
-    int64_t off, left;
-    int u, skip;
+    int64_t off, left, before, total, at;
+    int u, skip, ctas;
     int abort_flag;
   };
   Local& lo = *reinterpret_cast<Local*>(smem_raw + C::LOFF);
@@ -179,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     const int per = (p.units + kThreads - 1) / kThreads;
     const int u0 = min(static_cast<int>(threadIdx.x) * per, p.units), u1 = min(u0 + per, p.units);
     int64_t mine = 0;
-    for (int u = u0; u < u1; u++) mine += static_cast<int64_t>(unit_tiles(p, u)) * p.MT;
+    for (int u = u0; u < u1; u++) mine += static_cast<int64_t>(unit_tiles<C::ROWS>(p, u)) * p.MT;
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -195,84 +202,93 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       total += lo.sums[w];
     }
     const int ctas = ctas_for(total, gridDim.x), me = static_cast<int>(blockIdx.x);
-    if (me == 0) {  // for the join
+    if (me == 0 && p.start) {  // for the join
       int64_t at = base;
       for (int u = u0; u < u1; u++) {
         p.first[u] = at;
-        at += static_cast<int64_t>(unit_tiles(p, u)) * p.MT;
+        at += static_cast<int64_t>(unit_tiles<C::ROWS>(p, u)) * p.MT;
       }
       if (threadIdx.x == 0) p.first[p.units] = total;
     }
+    if (threadIdx.x == 0) lo.ctas = ctas;
     if (me < ctas) {
       const int64_t a = range_start(total, ctas, me);
       if (a >= base && a < base + mine) {
         int64_t at = base;
         int u = u0;
         for (;; u++) {
-          const int64_t n = static_cast<int64_t>(unit_tiles(p, u)) * p.MT;
+          const int64_t n = static_cast<int64_t>(unit_tiles<C::ROWS>(p, u)) * p.MT;
           if (a < at + n || u + 1 >= u1) break;
           at += n;
         }
         lo.u = u;
         lo.off = a - at;
         lo.left = range_start(total, ctas, me + 1) - a;
+        lo.before = me > 0 ? a - range_start(total, ctas, me - 1) : 0;
+        lo.total = total;
+        lo.at = a;
       }
     }
     __syncthreads();
   }
-  PagedWalk walk{lo.u, lo.off, lo.left};
+  PagedWalk<C::ROWS> walk{lo.u, lo.off, lo.left};
   PagedPiece x;
   pdl_trigger();
+  if (p.v.sel && warp < kConsumers / 32) {  // slots that see nothing: zeros
+    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+      const int s = u / p.v.Hkv;
+      if (paged_len(p.v.b, s) < 0 || unit_tiles<C::ROWS>(p, u) > 0) continue;
+      uint32_t* out = reinterpret_cast<uint32_t*>(p.out + (static_cast<size_t>(s) * p.Hq + (u - s * p.v.Hkv) * p.G) * D);
+      for (int i = threadIdx.x; i < p.G * D / 2; i += kConsumers) out[i] = 0u;
+    }
+  }
 
   if (warp == kConsumers / 32) {
     // ---------------- producer ----------------
-    const int R = p.R, nsub = kRows / R, per_page = max(1, (1 << p.v.b.shift) / R), rows = 1 << p.v.b.shift;
-    constexpr int CH = D / 64;  // boxes across a row
-    uint32_t tile = 0;          // tiles of the CTA
+    const int R = p.R, nsub = C::ROWS / R, rows = 1 << p.v.b.shift, per_page = rows / R;
+    uint32_t tile = 0;                // tiles of the CTA
     uint32_t fills0 = 0, fills1 = 0;  // of each team's ring
     bool ok = true;
-    while (ok && walk.next(p, x)) {
-      const int L = paged_len(p.v.b, x.s), from = p.start ? p.start[x.s] >> p.v.b.shift : 0;
-      const int pages = p.v.sel ? p.v.pages(x.s, x.h, L) : (L >> p.v.b.shift) + 1;  // (places in the order, from the first)
-      // part i of the item: box rows i * R .. of its rows
-      auto part = [&](int i, int& seen) -> int {  // its row in the pools, -1: none; rows of it that are seen
-        const int place = from + i / per_page;
-        seen = 0;
-        if (place >= pages || i >= x.k1 * nsub) return -1;
-        const int col = p.v.column(x.s, x.h, place);
-        if (col < 0) return -1;
-        const int r = (i % per_page) * R;
-        seen = min(R, L + 1 - (col * rows + r));
-        if (seen <= 0) {
-          seen = 0;
-          return -1;
-        }
-        const int page = page_at(p.v.b, x.s, col);
-        if (page < 0) {
-          seen = 0;
-          return -1;
-        }
-        return (page * p.v.Hkv + x.h) * rows + r;
-      };
-      int i0 = x.k0 * nsub, seen, seen2 = 0, row, row2 = -1;
-      row = part(i0 + lane, seen);
+    // part i of a piece's item: box rows i * R .. of its rows: its row in the pools, -1: none; rows of it that are seen
+    auto part = [&](const PagedPiece& x, int i, int& seen) -> int {
+      seen = 0;
+      if (i >= x.k1 * nsub) return -1;
+      const int L = paged_len(p.v.b, x.s), place = (p.start ? p.start[x.s] >> p.v.b.shift : 0) + i / per_page;
+      if (place >= p.v.pages(x.s, x.h, L)) return -1;
+      const int col = p.v.column(x.s, x.h, place);
+      if (col < 0) return -1;
+      const int r = (i % per_page) * R, n = min(R, L + 1 - (col * rows + r));
+      if (n <= 0) return -1;
+      const int page = page_at(p.v.b, x.s, col);
+      if (page < 0) return -1;
+      seen = n;
+      return (page * p.v.Hkv + x.h) * rows + r;
+    };
+    PagedPiece y;
+    bool more = walk.next(p, x);
+    int row = -1, seen = 0, row2 = -1, seen2 = 0, next_row = -1, next_seen = 0;
+    if (more) row = part(x, x.k0 * nsub + lane, seen);
+    if (lane == 0) {  // where this CTA's range starts within an item, for the join
+      int4 c = make_int4(-1, 0, 0, 0);
+      if (more && x.k0 > 0 && x.k0 <= lo.before)
+        c = make_int4(x.s, x.h, x.m, range_of(lo.total, lo.ctas, lo.at - x.k0 + x.nt - 1));
+      p.cut[blockIdx.x] = c;
+    }
+    while (ok && more) {
+      bool following = false;
+      int i0 = x.k0 * nsub;
       for (int k = x.k0; k < x.k1 && ok; k++, tile++) {
         const int at = (k - x.k0) * nsub % 32;
-        if (at == 0) {
-          if (k != x.k0) {
-            row = row2;
-            seen = seen2;
-            i0 += 32;
-          }
-          row2 = part(i0 + 32 + lane, seen2);
+        if (at == 0 && k != x.k0) {
+          row = row2;
+          seen = seen2;
+          i0 += 32;
         }
         // of this tile: part y's row and count in lane at + y
-        uint32_t bytes = 0;
-        for (int y = 0; y < nsub; y++) bytes += __shfl_sync(0xffffffffu, row, at + y) >= 0 ? R * D * 2 : 0;
-        const int y = lane / CH, ch = lane % CH;  // this lane's box
-        const int br = __shfl_sync(0xffffffffu, row, min(at + y, 31));
+        const int mine = __shfl_sync(0xffffffffu, row, min(at + lane, 31));  // this lane's box
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, lane < nsub && mine >= 0)) * R * D * 2;
         // rows seen of each 16 of the tile
-        const int q16 = lane & 3, py = q16 * 16 / R;
+        const int q16 = lane & (C::SG - 1), py = q16 * 16 / R;
         const int cnt = min(16, max(0, __shfl_sync(0xffffffffu, seen, at + py) - (q16 * 16 - py * R)));
 #pragma unroll
         for (int kv = 0; kv < 2; kv++) {
@@ -281,17 +297,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
           if (!ok) break;
           if (tile & 1) fills1++;
           else fills0++;
-          if (lane < 4) seen_s[slot * 4 + lane] = cnt;
+          if (lane < C::SG) seen_s[slot * C::SG + lane] = cnt;
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(full, bytes);
           __syncwarp();
-          for (int b = lane; b < nsub * CH; b += 32) {  // (16 boxes at most: one round)
-            if (br >= 0)
-              tma_load_2d(sb + slot * C::SLOT + ch * (kRows * 128) + y * R * 128, kv ? &p.tmV : &p.tmK, full, ch * 64, br);
-          }
+          if (lane < nsub && mine >= 0) tma_load_3d(sb + slot * C::SLOT + lane * R * D * 2, kv ? &p.tmV : &p.tmK, full, 0, mine, 0);
           __syncwarp();
         }
+        if (at == 0) row2 = part(x, i0 + 32 + lane, seen2);  // the next 32, under this tile's copies
+        if (k == x.k0) {                                     // and the next piece's first
+          following = walk.next(p, y);
+          if (following) next_row = part(y, y.k0 * nsub + lane, next_seen);
+        }
       }
+      x = y;
+      more = following;
+      row = next_row;
+      seen = next_seen;
     }
     if (!ok && lane == 0) set_status(p.v.b.status, TV_ERR_TIMEOUT);
     // every issued copy lands before shared memory is released
@@ -312,6 +334,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   int pieces = 0;
   bool ok = true;  // (a warp whose wait gave up goes on through the barriers, idle)
   const f2_t c2 = f2_dup(p.c);
+  // a tile lies as its boxes do: [box][64 columns][R rows][128 bytes]
+  const uint32_t chunk = p.R * 128, rmask = p.R - 1;
+  auto row_at = [&](uint32_t r) { return (r & ~rmask) * (D * 2) + (r & rmask) * 128; };
   while (walk.next(p, x)) {
     // query heads of the item, straight into the first operand's layout
     const int heads = min(kItem, p.G - x.m * kItem);
@@ -344,49 +369,63 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       turn++;
       // S = Q K^T, 16 rows of keys a warp
       ok = ok && wait_warp(FULL0 + 8u * ks, kph, abort_flag, kWaitCycles);
-      float s0[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      const int vis = ok ? seen_s[ks * 4 + w] : 0;
-      const int all4 = ok ? min(min(seen_s[ks * 4], seen_s[ks * 4 + 1]), min(seen_s[ks * 4 + 2], seen_s[ks * 4 + 3])) : 0;
+      float s0[C::WR / 8][4];
+#pragma unroll
+      for (int n = 0; n < C::WR / 8; n++) s0[n][0] = s0[n][1] = s0[n][2] = s0[n][3] = 0.f;
+      int vis[C::SG / 4], most = 0;  // rows seen of this warp's groups of 16
+      bool whole_tile = ok;
+#pragma unroll
+      for (int i = 0; i < C::SG; i++) {
+        const int n = ok ? seen_s[ks * C::SG + i] : 0;
+        whole_tile = whole_tile && n == 16;
+        most = max(most, n);
+      }
+#pragma unroll
+      for (int i = 0; i < C::SG / 4; i++) vis[i] = ok ? seen_s[ks * C::SG + w * (C::SG / 4) + i] : 0;
+      met = met || most > 0;
       if (ok) {
-        const int kr = w * 16 + (lane >> 4) * 8 + (lane & 7);
-        const uint32_t kb = sb + ks * C::SLOT + kr * 128;
         const int half = (lane >> 3) & 1;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; kk++) {
-          uint32_t b[4];
-          ldsm_x4(kb + (kk >> 2) * (kRows * 128) + ((((kk & 3) * 2 + half) ^ (kr & 7)) << 4), b);
-          mma16816(s0[0], qa[kk], b[0], b[1]);
-          mma16816(s0[1], qa[kk], b[2], b[3]);
+        for (int i = 0; i < C::WR / 16; i++) {  // 16 rows: within one box
+          const int r16 = w * C::WR + i * 16, kr = (lane >> 4) * 8 + (lane & 7);
+          const uint32_t kb = sb + ks * C::SLOT + row_at(r16) + kr * 128;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; kk++) {
+            uint32_t b[4];
+            ldsm_x4(kb + (kk >> 2) * chunk + ((((kk & 3) * 2 + half) ^ (kr & 7)) << 4), b);
+            mma16816(s0[2 * i], qa[kk], b[0], b[1]);
+            mma16816(s0[2 * i + 1], qa[kk], b[2], b[3]);
+          }
         }
       }
 #pragma unroll
-      for (int n = 0; n < 2; n++) {
-        const int c = n * 8 + gc;
-        if (c >= vis) s0[n][0] = s0[n][2] = -INFINITY;
-        if (c + 1 >= vis) s0[n][1] = s0[n][3] = -INFINITY;
-        sts2(sc + (gr * C::SLD + w * 16 + c) * 4, s0[n][0], s0[n][1]);
-        sts2(sc + ((gr + 8) * C::SLD + w * 16 + c) * 4, s0[n][2], s0[n][3]);
+      for (int n = 0; n < C::WR / 8; n++) {
+        const int c = (n & 1) * 8 + gc, v = vis[n / 2];
+        if (c >= v) s0[n][0] = s0[n][2] = -INFINITY;
+        if (c + 1 >= v) s0[n][1] = s0[n][3] = -INFINITY;
+        sts2(sc + (gr * C::SLD + w * C::WR + n * 8 + gc) * 4, s0[n][0], s0[n][1]);
+        sts2(sc + ((gr + 8) * C::SLD + w * C::WR + n * 8 + gc) * 4, s0[n][2], s0[n][3]);
       }
       // Only now: an arrival does not wait for loads, the stores have waited for the
       // products and these for theirs.
       __syncwarp();
       if (lane == 0) mbar_arrive(EMPTY0 + 8u * ks);
       ok = ok && wait_warp(FULL0 + 8u * vs, vph, abort_flag, kWaitCycles);
-      if (all4 < 16 && ok) {  // values that nothing sees, this warp's 16 rows
-        for (int r = vis; r < 16; r++)
-          for (int e = lane; e < D / 8; e += 32)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(sb + vs * C::SLOT + (e >> 3) * (kRows * 128) +
-                                                                          (w * 16 + r) * 128 + (e & 7) * 16),
-                         "r"(0)
-                         : "memory");
+      if (!whole_tile && ok) {  // values that nothing sees, of this warp's rows
+#pragma unroll
+        for (int i = 0; i < C::SG / 4; i++) {
+          const uint32_t vb = sb + vs * C::SLOT + row_at(w * C::WR + i * 16);
+          for (int r = vis[i]; r < 16; r++)
+            for (int e = lane; e < D / 8; e += 32)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (e >> 3) * chunk + r * 128 + (e & 7) * 16), "r"(0) : "memory");
+        }
         fence_proxy_async_smem();  // before the slot's next copy
       }
       bar_sync(1 + team, 128);
-      met = met || seen_s[vs * 4] || seen_s[vs * 4 + 1] || seen_s[vs * 4 + 2] || seen_s[vs * 4 + 3];
       // weights, in the first operand's layout
-      float2 sv[4][4];
+      float2 sv[C::SG][4];
 #pragma unroll
-      for (int kk = 0; kk < 4; kk++) {
+      for (int kk = 0; kk < C::SG; kk++) {
         const uint32_t a = sc + (gr * C::SLD + kk * 16 + gc) * 4;
         sv[kk][0] = lds2(a);
         sv[kk][1] = lds2(a + 8 * C::SLD * 4);
@@ -398,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       for (int r = 0; r < 2; r++) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int kk = 0; kk < 4; kk++)
+        for (int kk = 0; kk < C::SG; kk++)
           mx = fmaxf(mx, fmaxf(fmaxf(sv[kk][r].x, sv[kk][r].y), fmaxf(sv[kk][r + 2].x, sv[kk][r + 2].y)));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -407,10 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
         neg[r] = mn == -INFINITY ? 0.f : -mn;  // nothing seen yet: every weight is 2^-inf = 0
         m[r] = mn;
       }
-      uint32_t pa[4][4];
+      uint32_t pa[C::SG][4];
       float sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int kk = 0; kk < 4; kk++)
+      for (int kk = 0; kk < C::SG; kk++)
 #pragma unroll
         for (int e = 0; e < 4; e++) {
           float a, b;
@@ -432,19 +471,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       // O += P V, this warp's columns
       uint32_t dep = 0;  // (0, but known only when the last load is there)
       if (ok) {
-        const uint32_t vb = sb + vs * C::SLOT;
         const int vr = ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
-        for (int kk = 0; kk < 4; kk++)
+        for (int kk = 0; kk < C::SG; kk++) {
+          const uint32_t vb = sb + vs * C::SLOT + row_at(kk * 16) + vr * 128;
 #pragma unroll
           for (int n = 0; n < C::NT; n += 2) {
-            const int ch = w * (C::CPW / 8) + n + (lane >> 4), r = kk * 16 + vr;  // 16 bytes of the row
+            const int ch = w * (C::CPW / 8) + n + (lane >> 4);  // 16 bytes of the row
             uint32_t b[4];
-            ldsm_x4_t(vb + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), b);
+            ldsm_x4_t(vb + (ch >> 3) * chunk + (((ch & 7) ^ (vr & 7)) << 4), b);
             mma16816(o[n], pa[kk], b[0], b[1]);
             mma16816(o[n + 1], pa[kk], b[2], b[3]);
-            if (kk == 3 && n == C::NT - 2) dep = b[3] & p.zero;
+            if (kk == C::SG - 1 && n == C::NT - 2) dep = b[3] & p.zero;
           }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(EMPTY0 + 8u * vs + dep);
@@ -544,8 +584,85 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   if (!ok && lane == 0) set_status(p.v.b.status, TV_ERR_TIMEOUT);
 }
 
-// Joins the pieces of items that were cut, in order, and writes zeros where a
-// slot sees nothing: a warp takes a part of a row, kJ pieces' loads in flight.
+// Joins the pieces of items that were cut, in order.  A CTA takes a row of an
+// item (blockIdx.x: the item's first cut), four columns a thread, the pieces dealt to
+// groups of threads that cover a row each, kJ loads in flight.  It is small enough
+// to wait beside the kernel before it.
+template <int D>
+__global__ void __launch_bounds__(256, 4) attn_paged_join_cuts_kernel(const __grid_constant__ PagedTcParams p) {
+  constexpr int kJ = 6, LANES = D / 4, GROUPS = 256 / LANES;
+  __shared__ float acc_s[GROUPS][D];
+  __shared__ float2 ml_s[GROUPS];
+  const int grp = threadIdx.x / LANES, col = threadIdx.x % LANES * 4;
+  pdl_wait();
+  const int4 c = p.cut[blockIdx.x];
+  const int head = c.z * kItem + static_cast<int>(blockIdx.y);
+  if (c.x < 0 || head >= p.G || status_bad(p.v.b.status)) return;
+  const int c0 = static_cast<int>(blockIdx.x) - 1, n = c.w - c0 + 1;  // CTAs that hold a piece
+  const float* rec = p.rec + static_cast<size_t>(blockIdx.y) * (D + 4);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+  for (int j0 = grp; j0 < n; j0 += kJ * GROUPS) {
+    float4 o[kJ];
+    float2 ml[kJ];
+#pragma unroll
+    for (int j = 0; j < kJ; j++) {
+      const int i = j0 + j * GROUPS;
+      const float* x = rec + (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * kItem * (D + 4);
+      o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      ml[j] = make_float2(-INFINITY, 0.f);
+      if (i < n) {
+        o[j] = *reinterpret_cast<const float4*>(x + col);
+        ml[j] = *reinterpret_cast<const float2*>(x + D);
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int j = 0; j < kJ; j++) mn = fmaxf(mn, ml[j].x);
+    const float a = m == -INFINITY ? 0.f : exp2f(__fsub_rn(m, mn));
+    l = __fmul_rn(l, a);
+    acc = make_float4(__fmul_rn(acc.x, a), __fmul_rn(acc.y, a), __fmul_rn(acc.z, a), __fmul_rn(acc.w, a));
+#pragma unroll
+    for (int j = 0; j < kJ; j++) {
+      if (ml[j].y == 0.f) continue;  // nothing of weight in the piece (or no piece)
+      const float f = exp2f(__fsub_rn(ml[j].x, mn));
+      l = __fmaf_rn(f, ml[j].y, l);
+      acc = make_float4(__fmaf_rn(f, o[j].x, acc.x), __fmaf_rn(f, o[j].y, acc.y), __fmaf_rn(f, o[j].z, acc.z), __fmaf_rn(f, o[j].w, acc.w));
+    }
+    m = mn;
+  }
+  *reinterpret_cast<float4*>(&acc_s[grp][col]) = acc;
+  if (col == 0) ml_s[grp] = make_float2(m, l);
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t >= D / 2) return;  // two columns a thread
+  float mn = -INFINITY, lt = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+  for (int g = 0; g < GROUPS; g++) mn = fmaxf(mn, ml_s[g].x);
+#pragma unroll
+  for (int g = 0; g < GROUPS; g++) {
+    if (ml_s[g].y == 0.f) continue;
+    const float f = exp2f(__fsub_rn(ml_s[g].x, mn));
+    lt = __fmaf_rn(f, ml_s[g].y, lt);
+    y0 = __fmaf_rn(f, acc_s[g][2 * t], y0);
+    y1 = __fmaf_rn(f, acc_s[g][2 * t + 1], y1);
+  }
+  const size_t at = (static_cast<size_t>(c.x) * p.Hq + c.y * p.G + head) * D + 2 * t;
+  const float inv = __fdiv_rn(1.f, lt);
+  y0 = __fmul_rn(y0, inv);
+  y1 = __fmul_rn(y1, inv);
+  if (mn == -INFINITY) {
+    y0 = y1 = 0.f;  // no row seen
+  } else if (p.gate) {
+    const uint32_t g = *reinterpret_cast<const uint32_t*>(p.gate + at);
+    y0 = gate_mul(y0, bf16_lo(g));
+    y1 = gate_mul(y1, bf16_hi(g));
+  }
+  *reinterpret_cast<uint32_t*>(p.out + at) = pack_bf16x2(y0, y1);
+}
+
+// The same where slots share prefixes: the prefix's pieces, then the slot's own.  A
+// warp takes a part of a row, kJ pieces' loads in flight.
 template <int D>
 __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_constant__ PagedTcParams p, int grid) {
   constexpr int kJ = 12, CPW = D >= 128 ? 128 : 64, V = CPW / 32, PARTS = D / CPW;  // columns a warp and a lane
@@ -564,9 +681,8 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_const
     float acc[V], m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int e = 0; e < V; e++) acc[e] = 0.f;
-    if (all == 0) {
-      if (paged_len(p.v.b, s) < 0) continue;  // idle: left as it was
-    } else {
+    if (all == 0) continue;  // idle: left as it was
+    {
       const int64_t nt = all / p.MT, t0 = p.first[u] + head / kItem * nt;
       const int c0 = range_of(total, ctas, t0), c1 = range_of(total, ctas, t0 + nt - 1);
       const float *rec = p.rec + static_cast<size_t>(head % kItem) * (D + 4), *pre = nullptr;
@@ -644,19 +760,21 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// A pool as a 2-D tensor of rows, in boxes of `rows` rows and 64 columns.
-static bool encode_pool_map(CUtensorMap* m, void* base, int D, int64_t all, int rows) {
+// A pool as a tensor of rows, in boxes of `rows` rows and 64 columns, or of whole rows.
+static bool encode_pool_map(CUtensorMap* m, void* base, int D, int64_t all, int rows, bool whole) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(all)}, strides[1] = {static_cast<cuuint64_t>(D) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(rows)}, estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t d = static_cast<cuuint64_t>(D), a = static_cast<cuuint64_t>(all);
+  const cuuint64_t dims2[2] = {d, a}, dims3[3] = {64, a, d / 64}, strides[2] = {d * 2, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(D / 64)}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, whole ? 3 : 2, base, whole ? dims3 : dims2, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A call's scratch, in bytes from its start.
 struct PagedSpace {
-  size_t rec, rec_item, rec_prefix, info, group_of, start, all;
+  size_t cut, rec, first, rec_item, rec_prefix, info, group_of, start, all;
 };
 static PagedSpace space_of(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g) {
   const size_t line = static_cast<size_t>(l->D + 4) * 4, units = static_cast<size_t>(b->n_seq) * l->Hkv;
@@ -668,9 +786,10 @@ static PagedSpace space_of(const tv_paged_layer* l, const tv_paged* b, const tv_
     return x;
   };
   PagedSpace s{};
-  take((units + 1) * 8);
+  s.cut = take(static_cast<size_t>(num_sms()) * 16);
   s.rec = take(static_cast<size_t>(2) * num_sms() * kItem * line);
   if (g) {
+    s.first = take((units + 1) * 8);
     s.rec_item = take(items * kItem * line);
     s.rec_prefix = take(static_cast<size_t>(paged_prefix_slots(l, b, g->n_group)) * 128 * line);
     s.info = take(static_cast<size_t>(g->n_group) * 16);
@@ -686,17 +805,17 @@ template <int D>
 static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_t st) {
   using C = Pg<D>;
   const tv_paged_layer* l = a.layer;
-  p.R = l->page < kRows ? l->page : kRows;
+  p.R = l->page < C::ROWS ? l->page : C::ROWS;
   const int64_t all = static_cast<int64_t>(l->n_pages) * l->Hkv * l->page;
-  if (!encode_pool_map(&p.tmK, l->K, D, all, p.R) || !encode_pool_map(&p.tmV, l->V, D, all, p.R)) return TV_ERR_CUDA;
+  if (!encode_pool_map(&p.tmK, l->K, D, all, p.R, true) || !encode_pool_map(&p.tmV, l->V, D, all, p.R, true)) return TV_ERR_CUDA;
   static std::atomic<uint64_t> set{0};
   if (!allow_smem(attn_paged_tc_kernel<D>, C::SMEM, set)) return TV_ERR_CUDA;
   const int grid = num_sms();
   if (a.groups) {
     PagedPrefixParams x;
     memset(&x, 0, sizeof(x));
-    x.tmK = p.tmK;
-    x.tmV = p.tmV;
+    x.R = l->page < 64 ? l->page : 64;
+    if (!encode_pool_map(&x.tmK, l->K, D, all, x.R, false) || !encode_pool_map(&x.tmV, l->V, D, all, x.R, false)) return TV_ERR_CUDA;
     x.b = p.v.b;
     x.group_off = a.groups->group_off;
     x.shared = a.groups->shared;
@@ -710,15 +829,18 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
     x.Hq = p.Hq;
     x.Hkv = l->Hkv;
     x.G = p.G;
-    x.R = p.R;
     x.all_rows = static_cast<int>(all);
     x.c = p.c;
     if (!paged_prefix_launch(x, D, st)) return TV_ERR_CUDA;
   }
   launch_k(true, attn_paged_tc_kernel<D>, dim3(grid), dim3(kThreads), C::SMEM, st, p);
-  const int64_t warps = static_cast<int64_t>(p.units) * p.G * (D > 128 ? D / 128 : 1);
-  const int join = static_cast<int>(warps + 7 < static_cast<int64_t>(16) * grid ? (warps + 7) / 8 : 2 * grid);
-  launch_k(true, attn_paged_join_kernel<D>, dim3(join), dim3(256), 0, st, p, grid);
+  if (a.groups) {
+    const int64_t warps = static_cast<int64_t>(p.units) * p.G * (D > 128 ? D / 128 : 1);
+    const int join = static_cast<int>(warps + 7 < static_cast<int64_t>(16) * grid ? (warps + 7) / 8 : 2 * grid);
+    launch_k(true, attn_paged_join_kernel<D>, dim3(join), dim3(256), 0, st, p, grid);
+  } else {
+    launch_k(true, attn_paged_join_cuts_kernel<D>, dim3(grid, p.G < kItem ? p.G : kItem), dim3(256), 0, st, p);
+  }
   return launch_status();
 }
 
@@ -733,9 +855,10 @@ tv_status paged_attn_tc_launch(const PagedAttnCall& a, cudaStream_t st) {
   p.out = static_cast<__nv_bfloat16*>(a.out);
   char* ws = static_cast<char*>(a.ws);
   const PagedSpace x = space_of(l, a.batch, a.groups);
-  p.first = reinterpret_cast<int64_t*>(ws);
+  p.cut = reinterpret_cast<int4*>(ws + x.cut);
   p.rec = reinterpret_cast<float*>(ws + x.rec);
   if (a.groups) {
+    p.first = reinterpret_cast<int64_t*>(ws + x.first);
     p.rec_item = reinterpret_cast<float*>(ws + x.rec_item);
     p.rec_prefix = reinterpret_cast<const float*>(ws + x.rec_prefix);
     p.info = reinterpret_cast<const int4*>(ws + x.info);
