@@ -637,6 +637,7 @@ tv_status tv_paged_bounds(const tv_paged_layer* layer, const tv_paged* batch, co
  * number times a power of two, so the choice is the same for any order of
  * summing.  e = 128 counts as an infinite score.
  *  first >= 0, last >= 1, first + last <= n_sel <= 4096
+ *  workspace as in tv_attn_prompt (none is needed up to 16,384 pages a slot)
  *  sel    device [n_seq][Hkv][n_sel]: page indices (columns of the table), rising, -1 behind the last
  *  count  device [n_seq][Hkv] */
 size_t tv_paged_select_workspace_bytes(const tv_paged_layer* layer, const tv_paged* batch);

@@ -1,12 +1,13 @@
 // Decode attention over bf16 caches in pages, on the tensor cores.
 //
-// A unit is one slot and KV head: its G query heads (16 at a time, an item)
-// against the keys and values that the slot sees, in tiles of 64 rows (128
-// of 64 columns).  Each tile is used by 16 rows of queries at most, so the call is bound by the reads of
-// keys and values; the products run on warp-level tiles (16 x 8 x 16), which
-// waste least on so few rows.  An item runs flash style:
-//   S = Q K^T, m = running maximum of the scaled scores, p = 2^(s c - m) rounded
-//   to bf16 for the product with V, l += p (fp32, as they were), O = O a + P V.
+// A unit is one slot and KV head: its G query heads (eight at a time, or sixteen: an
+// item) against the keys and values that the slot sees, in tiles of 64 rows (128
+// of 64 columns).  Each tile is used by so few query rows that the call is bound by
+// the reads of keys and values; the products run on warp-level tiles (16 x 8 x 16)
+// with the cache on the long side, S^T = K Q^T and O^T = V^T P^T, so that eight heads
+// fill them.  An item runs flash style:
+//   m = running maximum of the scaled scores, p = 2^(s c - m) rounded to bf16 for
+//   the product with V, l += p (fp32, as they were), O = O a + P V.
 // p is rounded because the tensor cores take P and V in one type; each weight is
 // off by 2^-8 of itself at most, independently, and l adds them unrounded.
 //
@@ -42,10 +43,10 @@
 
 namespace tv {
 
-constexpr int kItem = 16;    // query rows of an item
+constexpr int kItemMax = 16;  // query heads of an item, at most
 constexpr int kConsumers = 256, kThreads = kConsumers + 32;
 
-template <int D>
+template <int D, int NB>
 struct Pg {
   // Rows of a key tile: with 64 columns a tile of 64 rows is over before the next
   // barrier: 8 slots of 65,536 rows, 8 + 8 heads of 64, 171 us with 128 rows, 296 with 64.
@@ -53,16 +54,18 @@ struct Pg {
   static constexpr int WR = ROWS / 4, SG = ROWS / 16;    // rows a warp scores, groups of 16 rows
   static constexpr int SLOT = ROWS * D * 2;              // a tile of keys or of values
   static constexpr int NS = D == 256 ? 3 : D == 128 ? 6 : 5;  // slots of a team's ring
-  static constexpr int CPW = D / 4, NT = CPW / 8;        // columns of O a warp, in tiles of 8
-  static constexpr int SLD = ROWS + 8;                   // floats of a row of scores (conflict-free pairs)
-  static constexpr int SBUF = kItem * SLD * 4;
+  static constexpr int HEADS = 8 * NB;                   // query heads of an item
+  static constexpr int CPW = D / 4, MT = CPW / 16;       // columns of O a warp, in tiles of 16
+  static constexpr int SLD = ROWS + 8;                   // floats of a head's scores (conflict-free pairs)
+  static constexpr int SBUF = HEADS * SLD * 4;
+  static constexpr int OLD = D + 4;                      // floats of a head of O
   static constexpr int SOFF = 2 * NS * SLOT;             // scores [team][2]
-  static constexpr int MOFF = SOFF + 4 * SBUF;           // the second team's m, l and half of O on their way to the first
-  static constexpr int MREG = NT * 2 + 4;
-  static constexpr int VOFF = MOFF + 128 * MREG * 4;     // rows seen of each 16 of a slot's tile: [2 NS][SG]
+  static constexpr int OOFF = SOFF + 4 * SBUF;           // the teams' O, eight heads at a time: [team][8]
+  static constexpr int MOFF = OOFF + 2 * 8 * OLD * 4;    // and m, l: [team][HEADS]
+  static constexpr int VOFF = MOFF + 2 * HEADS * 8;      // rows seen of each 16 of a slot's tile: [2 NS][SG]
   static constexpr int BOFF = VOFF + 2 * NS * SG * 4;
   static constexpr int LOFF = BOFF + 4 * NS * 8;
-  static constexpr int SMEM = LOFF + 256;
+  static constexpr int SMEM = LOFF + 128 + 128;
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -75,13 +78,14 @@ struct PagedTcParams {
   __nv_bfloat16* out;
   int64_t* first;  // [units + 1] each unit's first tile in the order of all (with shared prefixes)
   int4* cut;       // [CTAs] the item that a CTA's range starts within, where it is the item's first cut:
-                   // slot, KV head, its 16 heads, last CTA; -1: none
-  float* rec;      // [2 * CTAs][16][D + 4]
-  float* rec_item;  // [items][16][D + 4]: items of slots with a shared prefix
+                   // slot, KV head, item of it, last CTA; -1: none
+  float* rec;      // [2 * CTAs][heads][D + 4]
+  float* rec_item;  // [items][heads][D + 4]: items of slots with a shared prefix
   const float* rec_prefix;  // [pieces][128][D + 4]
   const int4* info;         // [groups] and
   const int32_t* group_of;  // [n_seq], as the kernel for shared prefixes left them
   int Hq, G, MT, units;  // MT items a unit
+  int item;              // query heads of an item
   int R;  // rows of a box: a page's, or a tile's
   float c;        // scale * log2(e)
   uint32_t zero;  // 0
@@ -96,28 +100,35 @@ __device__ __forceinline__ int unit_tiles(const PagedTcParams& p, int u) {
   return (L + 1 - (p.start ? p.start[s] : 0) + ROWS - 1) / ROWS;
 }
 
+constexpr int kNear = 32;
+
 // The items of a range of tiles, one after another.
 struct PagedPiece {
-  int s, h, m, k0, k1, nt;  // slot, KV head, 16 query heads, tiles [k0, k1) of nt
+  int s, h, m, k0, k1, nt;  // slot, KV head, item of it, tiles [k0, k1) of nt
 };
 template <int ROWS>
 struct PagedWalk {
-  int u;        // unit
-  int64_t off;  // tile within the unit, over its items
+  int u, s, h;          // unit: slot and KV head
+  int u0;               // the first unit of the range, and
+  const int* near;      // the tiles of that one and the kNear - 1 after it
+  int off;  // tile within the unit, over its items (under 2^27: a slot has 2^30 rows at most, a unit 8 items)
   int64_t left;
   __device__ __forceinline__ bool next(const PagedTcParams& p, PagedPiece& x) {
     while (left > 0 && u < p.units) {
-      const int nt = unit_tiles<ROWS>(p, u);
-      const int64_t all = static_cast<int64_t>(nt) * p.MT;
-      if (off >= all) {
+      const int nt = u - u0 < kNear ? near[u - u0] : unit_tiles<ROWS>(p, u);
+      if (off >= nt * p.MT) {
         off = 0;
         u++;
+        if (++h == p.v.Hkv) {
+          h = 0;
+          s++;
+        }
         continue;
       }
-      x.s = u / p.v.Hkv;
-      x.h = u - x.s * p.v.Hkv;
-      x.m = static_cast<int>(off / nt);
-      x.k0 = static_cast<int>(off - static_cast<int64_t>(x.m) * nt);
+      x.s = s;
+      x.h = h;
+      x.m = off < nt ? 0 : off / nt;
+      x.k0 = off - x.m * nt;
       x.k1 = static_cast<int>(min(static_cast<int64_t>(nt), x.k0 + left));
       x.nt = nt;
       off += x.k1 - x.k0;
@@ -135,31 +146,29 @@ __device__ __forceinline__ int range_of(int64_t total, int ctas, int64_t tile) {
 __device__ __forceinline__ int ctas_for(int64_t total, int grid) { return static_cast<int>(min(static_cast<int64_t>(grid), total)); }
 
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ void sts2(uint32_t a, float x, float y) {
-  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
-}
+__device__ __forceinline__ void sts1(uint32_t a, float x) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory"); }
 __device__ __forceinline__ float2 lds2(uint32_t a) {
   float2 v;
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
   return v;
 }
 
-template <int D>
+template <int D, int NB>
 __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid_constant__ PagedTcParams p) {
-  using C = Pg<D>;
+  using C = Pg<D, NB>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];  // tiles are swizzled in 1024-byte atoms
   const uint32_t sb = smem_u32(smem_raw);
   const uint32_t FULL0 = sb + C::BOFF, EMPTY0 = FULL0 + 16u * C::NS;
   int32_t* seen_s = reinterpret_cast<int32_t*>(smem_raw + C::VOFF);
   struct Local {
-    int64_t sums[9];  // tiles of each warp's units
-    int64_t off, left, before, total, at;
-    int u, skip, ctas;
+    int64_t left, before, total, at;
+    int u, off, skip, ctas;
     int abort_flag;
   };
   Local& lo = *reinterpret_cast<Local*>(smem_raw + C::LOFF);
-  static_assert(sizeof(Local) <= 256, "local data");
+  int64_t* sums = reinterpret_cast<int64_t*>(smem_raw + C::SOFF);  // tiles of each warp's units (scores are not in use yet)
+  static_assert(sizeof(Local) <= 128, "local data");
+  int* lo_near = reinterpret_cast<int*>(smem_raw + C::LOFF + 128);
   volatile int* abort_flag = &lo.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -193,13 +202,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    if (lane == 31) lo.sums[warp] = incl;
+    if (lane == 31) sums[warp] = incl;
     __syncthreads();
     int64_t base = incl - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; w++) {
-      if (w < warp) base += lo.sums[w];
-      total += lo.sums[w];
+      if (w < warp) base += sums[w];
+      total += sums[w];
     }
     const int ctas = ctas_for(total, gridDim.x), me = static_cast<int>(blockIdx.x);
     if (me == 0 && p.start) {  // for the join
@@ -222,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
           at += n;
         }
         lo.u = u;
-        lo.off = a - at;
+        lo.off = static_cast<int>(a - at);
         lo.left = range_start(total, ctas, me + 1) - a;
         lo.before = me > 0 ? a - range_start(total, ctas, me - 1) : 0;
         lo.total = total;
@@ -231,7 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     }
     __syncthreads();
   }
-  PagedWalk<C::ROWS> walk{lo.u, lo.off, lo.left};
+  if (lo.left > 0 && threadIdx.x < kNear) lo_near[threadIdx.x] = lo.u + static_cast<int>(threadIdx.x) < p.units ? unit_tiles<C::ROWS>(p, lo.u + threadIdx.x) : 0;
+  __syncthreads();
+  PagedWalk<C::ROWS> walk{lo.u, lo.u / p.v.Hkv, lo.u % p.v.Hkv, lo.u, lo_near, lo.off, lo.left};
   PagedPiece x;
   pdl_trigger();
   if (p.v.sel && warp < kConsumers / 32) {  // slots that see nothing: zeros
@@ -327,39 +338,52 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
 
   // ---------------- consumers ----------------
   const int team = warp >> 2, w = warp & 3;
-  const int gr = lane >> 2, gc = (lane & 3) * 2;  // this lane's rows gr, gr + 8 and first column of a tile of 8
+  // in a 16 x 8 result this lane has rows gr, gr + 8 and columns gc, gc + 1; in a second operand column gr
+  const int gr = lane >> 2, gc = (lane & 3) * 2;
   const uint32_t sc0 = sb + C::SOFF + team * 2 * C::SBUF;
-  float* merge = reinterpret_cast<float*>(smem_raw + C::MOFF) + (threadIdx.x & 127);
+  float* o_s = reinterpret_cast<float*>(smem_raw + C::OOFF);
+  float2* ml_s = reinterpret_cast<float2*>(smem_raw + C::MOFF);
   uint32_t tile = 0, turn = 0;  // tiles of the CTA, tiles of this team
-  int pieces = 0;
   bool ok = true;  // (a warp whose wait gave up goes on through the barriers, idle)
   const f2_t c2 = f2_dup(p.c);
   // a tile lies as its boxes do: [box][64 columns][R rows][128 bytes]
   const uint32_t chunk = p.R * 128, rmask = p.R - 1;
   auto row_at = [&](uint32_t r) { return (r & ~rmask) * (D * 2) + (r & rmask) * 128; };
-  while (walk.next(p, x)) {
-    // query heads of the item, straight into the first operand's layout
-    const int heads = min(kItem, p.G - x.m * kItem);
-    const size_t row0 = (static_cast<size_t>(x.s) * p.Hq + x.h * p.G + x.m * kItem) * D;
-    uint32_t qa[D / 16][4];
-    {
-      const __nv_bfloat16* q = p.q + row0 + gc;
-      const uint32_t* qlo = reinterpret_cast<const uint32_t*>(q + static_cast<size_t>(gr < heads ? gr : 0) * D);
-      const uint32_t* qhi = reinterpret_cast<const uint32_t*>(q + static_cast<size_t>(gr + 8 < heads ? gr + 8 : 0) * D);
+  // query heads of an item, straight into the second operand's layout
+  uint32_t qb[NB][D / 16][2];
+  auto load_q = [&](const PagedPiece& x) {
+    const int heads = min(C::HEADS, p.G - x.m * C::HEADS);
+    const __nv_bfloat16* q = p.q + (static_cast<size_t>(x.s) * p.Hq + x.h * p.G + x.m * C::HEADS) * D + gc;
+#pragma unroll
+    for (int b = 0; b < NB; b++) {  // (past the last head: the first again, never written)
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(q + static_cast<size_t>(gr + 8 * b < heads ? gr + 8 * b : 0) * D);
 #pragma unroll
       for (int kk = 0; kk < D / 16; kk++) {
-        qa[kk][0] = gr < heads ? qlo[kk * 8] : 0u;
-        qa[kk][1] = gr + 8 < heads ? qhi[kk * 8] : 0u;
-        qa[kk][2] = gr < heads ? qlo[kk * 8 + 4] : 0u;
-        qa[kk][3] = gr + 8 < heads ? qhi[kk * 8 + 4] : 0u;
+        qb[b][kk][0] = src[kk * 8];
+        qb[b][kk][1] = src[kk * 8 + 4];
       }
     }
-    float o[C::NT][4];
+  };
+  bool more = walk.next(p, x);
+  if (more) load_q(x);
+  while (more) {
+    const int heads = min(C::HEADS, p.G - x.m * C::HEADS);
+    PagedPiece y;
+    const bool following = walk.next(p, y);
+    bool loaded = !following;  // the next piece's queries: under this one's last tile
+    float o[NB][C::MT][4];     // O transposed: columns of the cache by query heads
 #pragma unroll
-    for (int n = 0; n < C::NT; n++)
+    for (int b = 0; b < NB; b++)
 #pragma unroll
-      for (int e = 0; e < 4; e++) o[n][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int n = 0; n < C::MT; n++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) o[b][n][e] = 0.f;
+    float m[NB], l[NB];  // of head gr (+ 8)
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+      m[b] = -INFINITY;
+      l[b] = 0.f;
+    }
     bool met = false;
     for (int k = x.k0; k < x.k1; k++, tile++) {
       if ((tile & 1) != static_cast<uint32_t>(team)) continue;
@@ -367,11 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       const uint32_t ks = r0 + ki % C::NS, kph = (ki / C::NS) & 1, vs = r0 + vi % C::NS, vph = (vi / C::NS) & 1;
       const uint32_t sc = sc0 + (turn & 1) * C::SBUF;
       turn++;
-      // S = Q K^T, 16 rows of keys a warp
+      // S transposed = K Q^T, this warp's rows of keys
       ok = ok && wait_warp(FULL0 + 8u * ks, kph, abort_flag, kWaitCycles);
-      float s0[C::WR / 8][4];
-#pragma unroll
-      for (int n = 0; n < C::WR / 8; n++) s0[n][0] = s0[n][1] = s0[n][2] = s0[n][3] = 0.f;
       int vis[C::SG / 4], most = 0;  // rows seen of this warp's groups of 16
       bool whole_tile = ok;
 #pragma unroll
@@ -383,33 +404,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
 #pragma unroll
       for (int i = 0; i < C::SG / 4; i++) vis[i] = ok ? seen_s[ks * C::SG + w * (C::SG / 4) + i] : 0;
       met = met || most > 0;
-      if (ok) {
-        const int half = (lane >> 3) & 1;
 #pragma unroll
-        for (int i = 0; i < C::WR / 16; i++) {  // 16 rows: within one box
-          const int r16 = w * C::WR + i * 16, kr = (lane >> 4) * 8 + (lane & 7);
-          const uint32_t kb = sb + ks * C::SLOT + row_at(r16) + kr * 128;
+      for (int i = 0; i < C::SG / 4; i++) {  // 16 rows: within one box
+        float s0[NB][2][4];                  // (two sums: products that follow one another wait)
+#pragma unroll
+        for (int b = 0; b < NB; b++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) s0[b][0][e] = s0[b][1][e] = 0.f;
+        if (ok) {
+          const int kr = ((lane >> 3) & 1) * 8 + (lane & 7), half = lane >> 4;
+          const uint32_t kb = sb + ks * C::SLOT + row_at(w * C::WR + i * 16) + kr * 128;
 #pragma unroll
           for (int kk = 0; kk < D / 16; kk++) {
-            uint32_t b[4];
-            ldsm_x4(kb + (kk >> 2) * chunk + ((((kk & 3) * 2 + half) ^ (kr & 7)) << 4), b);
-            mma16816(s0[2 * i], qa[kk], b[0], b[1]);
-            mma16816(s0[2 * i + 1], qa[kk], b[2], b[3]);
+            uint32_t a[4];
+            ldsm_x4(kb + (kk >> 2) * chunk + ((((kk & 3) * 2 + half) ^ (kr & 7)) << 4), a);
+#pragma unroll
+            for (int b = 0; b < NB; b++) mma16816(s0[b][kk & 1], a, qb[b][kk][0], qb[b][kk][1]);
           }
         }
-      }
+        const bool lo_in = gr < vis[i], hi_in = gr + 8 < vis[i];
+        const uint32_t at = sc + (gc * C::SLD + w * C::WR + i * 16 + gr) * 4;
 #pragma unroll
-      for (int n = 0; n < C::WR / 8; n++) {
-        const int c = (n & 1) * 8 + gc, v = vis[n / 2];
-        if (c >= v) s0[n][0] = s0[n][2] = -INFINITY;
-        if (c + 1 >= v) s0[n][1] = s0[n][3] = -INFINITY;
-        sts2(sc + (gr * C::SLD + w * C::WR + n * 8 + gc) * 4, s0[n][0], s0[n][1]);
-        sts2(sc + ((gr + 8) * C::SLD + w * C::WR + n * 8 + gc) * 4, s0[n][2], s0[n][3]);
+        for (int b = 0; b < NB; b++) {
+          float s[4];
+#pragma unroll
+          for (int e = 0; e < 4; e++) s[e] = (e < 2 ? lo_in : hi_in) ? __fadd_rn(s0[b][0][e], s0[b][1][e]) : -INFINITY;
+          sts1(at + b * 8 * C::SLD * 4, s[0]);
+          sts1(at + (b * 8 + 1) * C::SLD * 4, s[1]);
+          sts1(at + b * 8 * C::SLD * 4 + 32, s[2]);
+          sts1(at + (b * 8 + 1) * C::SLD * 4 + 32, s[3]);
+        }
       }
       // Only now: an arrival does not wait for loads, the stores have waited for the
       // products and these for theirs.
       __syncwarp();
       if (lane == 0) mbar_arrive(EMPTY0 + 8u * ks);
+      if (!loaded && k + 2 >= x.k1) {
+        load_q(y);
+        loaded = true;
+      }
       ok = ok && wait_warp(FULL0 + 8u * vs, vph, abort_flag, kWaitCycles);
       if (!whole_tile && ok) {  // values that nothing sees, of this warp's rows
 #pragma unroll
@@ -422,165 +455,135 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
         fence_proxy_async_smem();  // before the slot's next copy
       }
       bar_sync(1 + team, 128);
-      // weights, in the first operand's layout
-      float2 sv[C::SG][4];
+      // weights of head gr (+ 8), in the second operand's layout
+      uint32_t pb[NB][C::SG][2];
 #pragma unroll
-      for (int kk = 0; kk < C::SG; kk++) {
-        const uint32_t a = sc + (gr * C::SLD + kk * 16 + gc) * 4;
-        sv[kk][0] = lds2(a);
-        sv[kk][1] = lds2(a + 8 * C::SLD * 4);
-        sv[kk][2] = lds2(a + 32);
-        sv[kk][3] = lds2(a + 8 * C::SLD * 4 + 32);
-      }
-      float alpha[2], neg[2];
-#pragma unroll
-      for (int r = 0; r < 2; r++) {
+      for (int b = 0; b < NB; b++) {
+        float2 sv[C::SG][2];
         float mx = -INFINITY;
 #pragma unroll
-        for (int kk = 0; kk < C::SG; kk++)
-          mx = fmaxf(mx, fmaxf(fmaxf(sv[kk][r].x, sv[kk][r].y), fmaxf(sv[kk][r + 2].x, sv[kk][r + 2].y)));
+        for (int kk = 0; kk < C::SG; kk++) {
+          const uint32_t a = sc + ((b * 8 + gr) * C::SLD + kk * 16 + gc) * 4;
+          sv[kk][0] = lds2(a);
+          sv[kk][1] = lds2(a + 32);
+          mx = fmaxf(mx, fmaxf(fmaxf(sv[kk][0].x, sv[kk][0].y), fmaxf(sv[kk][1].x, sv[kk][1].y)));
+        }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[r], __fmul_rn(mx, p.c));
-        alpha[r] = mn == m[r] ? 1.f : ex2_approx(__fsub_rn(m[r], mn));
-        neg[r] = mn == -INFINITY ? 0.f : -mn;  // nothing seen yet: every weight is 2^-inf = 0
-        m[r] = mn;
-      }
-      uint32_t pa[C::SG][4];
-      float sum[2] = {0.f, 0.f};
+        const float mn = fmaxf(m[b], __fmul_rn(mx, p.c));
+        const float alpha = mn == m[b] ? 1.f : ex2_approx(__fsub_rn(m[b], mn));
+        const f2_t neg2 = f2_dup(mn == -INFINITY ? 0.f : -mn);  // nothing seen yet: every weight is 2^-inf = 0
+        m[b] = mn;
+        float sum = 0.f;
 #pragma unroll
-      for (int kk = 0; kk < C::SG; kk++)
+        for (int kk = 0; kk < C::SG; kk++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          float a, b;
-          f2_unpack(f2_fma(f2_pack(sv[kk][e].x, sv[kk][e].y), c2, f2_dup(neg[e & 1])), a, b);
-          a = ex2_approx(a);
-          b = ex2_approx(b);
-          sum[e & 1] = __fadd_rn(sum[e & 1], __fadd_rn(a, b));
-          pa[kk][e] = pack_bf16x2(a, b);
+          for (int e = 0; e < 2; e++) {
+            float u, v;
+            f2_unpack(f2_fma(f2_pack(sv[kk][e].x, sv[kk][e].y), c2, neg2), u, v);
+            u = ex2_approx(u);
+            v = ex2_approx(v);
+            sum = __fadd_rn(sum, __fadd_rn(u, v));
+            pb[b][kk][e] = pack_bf16x2(u, v);
+          }
+        l[b] = __fmaf_rn(l[b], alpha, sum);
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {  // heads gc, gc + 1 of O
+          const float a0 = __shfl_sync(0xffffffffu, alpha, gc * 4), a1 = __shfl_sync(0xffffffffu, alpha, gc * 4 + 4);
+#pragma unroll
+          for (int n = 0; n < C::MT; n++) {
+            o[b][n][0] = __fmul_rn(o[b][n][0], a0);
+            o[b][n][1] = __fmul_rn(o[b][n][1], a1);
+            o[b][n][2] = __fmul_rn(o[b][n][2], a0);
+            o[b][n][3] = __fmul_rn(o[b][n][3], a1);
+          }
         }
-#pragma unroll
-      for (int r = 0; r < 2; r++) l[r] = __fmaf_rn(l[r], alpha[r], sum[r]);
-#pragma unroll
-      for (int n = 0; n < C::NT; n++) {
-        o[n][0] = __fmul_rn(o[n][0], alpha[0]);
-        o[n][1] = __fmul_rn(o[n][1], alpha[0]);
-        o[n][2] = __fmul_rn(o[n][2], alpha[1]);
-        o[n][3] = __fmul_rn(o[n][3], alpha[1]);
       }
-      // O += P V, this warp's columns
+      // O transposed += V^T P^T, this warp's columns
       uint32_t dep = 0;  // (0, but known only when the last load is there)
       if (ok) {
-        const int vr = ((lane >> 3) & 1) * 8 + (lane & 7);
+        const int vr = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
         for (int kk = 0; kk < C::SG; kk++) {
           const uint32_t vb = sb + vs * C::SLOT + row_at(kk * 16) + vr * 128;
 #pragma unroll
-          for (int n = 0; n < C::NT; n += 2) {
-            const int ch = w * (C::CPW / 8) + n + (lane >> 4);  // 16 bytes of the row
-            uint32_t b[4];
-            ldsm_x4_t(vb + (ch >> 3) * chunk + (((ch & 7) ^ (vr & 7)) << 4), b);
-            mma16816(o[n], pa[kk], b[0], b[1]);
-            mma16816(o[n + 1], pa[kk], b[2], b[3]);
-            if (kk == C::SG - 1 && n == C::NT - 2) dep = b[3] & p.zero;
+          for (int n = 0; n < C::MT; n++) {
+            const int ch = w * (C::CPW / 8) + n * 2 + ((lane >> 3) & 1);  // 16 bytes of the row
+            uint32_t a[4];
+            ldsm_x4_t(vb + (ch >> 3) * chunk + (((ch & 7) ^ (vr & 7)) << 4), a);
+#pragma unroll
+            for (int b = 0; b < NB; b++) mma16816(o[b][n], a, pb[b][kk][0], pb[b][kk][1]);
+            if (kk == C::SG - 1 && n == C::MT - 1) dep = a[3] & p.zero;
           }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(EMPTY0 + 8u * vs + dep);
     }
-    // the teams' parts, joined by the first
+    if (!loaded) load_q(y);
+    // the teams' parts, joined by all eight warps, eight heads at a time
 #pragma unroll
-    for (int r = 0; r < 2; r++) {
-      l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xffffffffu, l[r], 1));
-      l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xffffffffu, l[r], 2));
-      if (met && m[r] == -INFINITY) m[r] = kNoScore;
+    for (int b = 0; b < NB; b++) {
+      l[b] = __fadd_rn(l[b], __shfl_xor_sync(0xffffffffu, l[b], 1));
+      l[b] = __fadd_rn(l[b], __shfl_xor_sync(0xffffffffu, l[b], 2));
+      if (met && m[b] == -INFINITY) m[b] = kNoScore;
+      if (w == 0 && gc == 0) ml_s[team * C::HEADS + b * 8 + gr] = make_float2(m[b], l[b]);
     }
-    // (O in two halves, so that the buffer leaves room for the rings)
-    float fa[2], fb[2];
+    const bool whole = x.k0 == 0 && x.k1 == x.nt, alone = !p.start || p.start[x.s] == 0;
 #pragma unroll
-    for (int half = 0; half < 2; half++) {
-      if (team == 1) {
-        if (pieces + half > 0) bar_sync(4, kConsumers);  // what was there has been taken out
+    for (int b = 0; b < NB; b++) {
+      float* mine = o_s + (team * 8 + gc) * C::OLD + w * C::CPW + gr;
 #pragma unroll
-        for (int n = 0; n < C::NT / 2; n++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) merge[(n * 4 + e) * 128] = o[half * (C::NT / 2) + n][e];
-        if (half == 0)
-#pragma unroll
-          for (int r = 0; r < 2; r++) {
-            merge[(C::NT * 2 + r) * 128] = m[r];
-            merge[(C::NT * 2 + 2 + r) * 128] = l[r];
-          }
-        bar_sync(3, kConsumers);
-      } else {
-        bar_sync(3, kConsumers);
-        if (half == 0)
-#pragma unroll
-          for (int r = 0; r < 2; r++) {
-            const float mo = merge[(C::NT * 2 + r) * 128], lb = merge[(C::NT * 2 + 2 + r) * 128], mn = fmaxf(m[r], mo);
-            fa[r] = mn == m[r] ? 1.f : ex2_approx(__fsub_rn(m[r], mn));
-            fb[r] = mn == mo ? 1.f : ex2_approx(__fsub_rn(mo, mn));
-            l[r] = __fadd_rn(__fmul_rn(l[r], fa[r]), __fmul_rn(lb, fb[r]));
-            m[r] = mn;
-          }
-#pragma unroll
-        for (int n = 0; n < C::NT / 2; n++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) {
-            float& y = o[half * (C::NT / 2) + n][e];
-            y = __fadd_rn(__fmul_rn(y, fa[e >> 1]), __fmul_rn(merge[(n * 4 + e) * 128], fb[e >> 1]));
-          }
-        // (an arrival does not wait for loads: what they brought has been used)
-        uint32_t dep = 0;
-#pragma unroll
-        for (int n = 0; n < C::NT / 2; n++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) dep |= __float_as_uint(o[half * (C::NT / 2) + n][e]);
-        bar_arrive(4 + (dep & p.zero), kConsumers);
+      for (int n = 0; n < C::MT; n++) {
+        mine[n * 16] = o[b][n][0];
+        mine[C::OLD + n * 16] = o[b][n][1];
+        mine[n * 16 + 8] = o[b][n][2];
+        mine[C::OLD + n * 16 + 8] = o[b][n][3];
       }
-    }
-    if (team == 0) {
-      const bool whole = x.k0 == 0 && x.k1 == x.nt, alone = !p.start || p.start[x.s] == 0;
-      if (!ok) {
-        // nothing of use: the status word says so
-      } else if (whole && alone) {
+      bar_sync(3, kConsumers);
+      constexpr int V = D / 32;  // columns a thread, a warp a head
+      const int head = b * 8 + warp, col = lane * V;
+      if (head < heads && ok) {
+        const float2 ma = ml_s[head], mb = ml_s[C::HEADS + head];
+        const float mn = fmaxf(ma.x, mb.x);
+        const float fa = mn == ma.x ? 1.f : ex2_approx(__fsub_rn(ma.x, mn)), fb = mn == mb.x ? 1.f : ex2_approx(__fsub_rn(mb.x, mn));
+        const float lt = __fadd_rn(__fmul_rn(ma.y, fa), __fmul_rn(mb.y, fb));
+        float v[V];
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
-          const int row = gr + 8 * r;
-          if (row >= heads) continue;
-          const size_t at = row0 + static_cast<size_t>(row) * D + w * C::CPW + gc;
-          const float inv = __fdiv_rn(1.f, l[r]);
+        for (int e = 0; e < V; e++)
+          v[e] = __fadd_rn(__fmul_rn(o_s[warp * C::OLD + col + e], fa), __fmul_rn(o_s[(8 + warp) * C::OLD + col + e], fb));
+        if (whole && alone) {
+          const size_t at = (static_cast<size_t>(x.s) * p.Hq + x.h * p.G + x.m * C::HEADS + head) * D + col;
+          const float inv = mn == -INFINITY ? 0.f : __fdiv_rn(1.f, lt);  // (no row seen: O is 0)
+          uint32_t y2[V / 2];
 #pragma unroll
-          for (int n = 0; n < C::NT; n++) {
-            float a = __fmul_rn(o[n][2 * r], inv), b = __fmul_rn(o[n][2 * r + 1], inv);
-            if (m[r] == -INFINITY) {
-              a = b = 0.f;  // no row seen
-            } else if (p.gate) {
-              const uint32_t g = *reinterpret_cast<const uint32_t*>(p.gate + at + n * 8);
-              a = gate_mul(a, bf16_lo(g));
-              b = gate_mul(b, bf16_hi(g));
+          for (int e = 0; e < V; e++) v[e] = __fmul_rn(v[e], inv);
+          if (p.gate && mn != -INFINITY) {
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              const uint32_t g = *reinterpret_cast<const uint32_t*>(p.gate + at + e);
+              v[e] = gate_mul(v[e], bf16_lo(g));
+              v[e + 1] = gate_mul(v[e + 1], bf16_hi(g));
             }
-            *reinterpret_cast<uint32_t*>(p.out + at + n * 8) = pack_bf16x2(a, b);
           }
-        }
-      } else {
-        float* rec = whole ? p.rec_item + (static_cast<size_t>(x.s * p.v.Hkv + x.h) * p.MT + x.m) * kItem * (D + 4)
-                           : p.rec + (static_cast<size_t>(blockIdx.x) * 2 + (x.k0 == 0 ? 1 : 0)) * kItem * (D + 4);
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
-          const int row = gr + 8 * r;
-          if (row >= heads) continue;
-          float* at = rec + row * (D + 4) + w * C::CPW + gc;
+          for (int e = 0; e < V / 2; e++) y2[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+          if constexpr (V == 8) *reinterpret_cast<uint4*>(p.out + at) = make_uint4(y2[0], y2[1], y2[2], y2[3]);
+          else if constexpr (V == 4) *reinterpret_cast<uint2*>(p.out + at) = make_uint2(y2[0], y2[1]);
+          else *reinterpret_cast<uint32_t*>(p.out + at) = y2[0];
+        } else {
+          float* rec = (whole ? p.rec_item + (static_cast<size_t>(x.s * p.v.Hkv + x.h) * p.MT + x.m) * C::HEADS * (D + 4)
+                              : p.rec + (static_cast<size_t>(blockIdx.x) * 2 + (x.k0 == 0 ? 1 : 0)) * C::HEADS * (D + 4)) +
+                       head * (D + 4);
 #pragma unroll
-          for (int n = 0; n < C::NT; n++) *reinterpret_cast<float2*>(at + n * 8) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
-          if (w == 0 && gc == 0) *reinterpret_cast<float2*>(rec + row * (D + 4) + D) = make_float2(m[r], l[r]);
+          for (int e = 0; e < V; e += 2) *reinterpret_cast<float2*>(rec + col + e) = make_float2(v[e], v[e + 1]);
+          if (lane == 0) *reinterpret_cast<float2*>(rec + D) = make_float2(mn, lt);
         }
       }
+      bar_sync(3, kConsumers);  // before the buffer is written again
     }
-    pieces++;
+    x = y;
+    more = following;
   }
-  if (team == 1 && pieces > 0) bar_sync(4, kConsumers);  // (every arrival is met)
   if (!ok && lane == 0) set_status(p.v.b.status, TV_ERR_TIMEOUT);
 }
 
@@ -596,7 +599,7 @@ __global__ void __launch_bounds__(256, 4) attn_paged_join_cuts_kernel(const __gr
   const int grp = threadIdx.x / LANES, col = threadIdx.x % LANES * 4;
   pdl_wait();
   const int4 c = p.cut[blockIdx.x];
-  const int head = c.z * kItem + static_cast<int>(blockIdx.y);
+  const int head = c.z * p.item + static_cast<int>(blockIdx.y);
   if (c.x < 0 || head >= p.G || status_bad(p.v.b.status)) return;
   const int c0 = static_cast<int>(blockIdx.x) - 1, n = c.w - c0 + 1;  // CTAs that hold a piece
   const float* rec = p.rec + static_cast<size_t>(blockIdx.y) * (D + 4);
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(256, 4) attn_paged_join_cuts_kernel(const __gr
 #pragma unroll
     for (int j = 0; j < kJ; j++) {
       const int i = j0 + j * GROUPS;
-      const float* x = rec + (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * kItem * (D + 4);
+      const float* x = rec + (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.item * (D + 4);
       o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       ml[j] = make_float2(-INFINITY, 0.f);
       if (i < n) {
@@ -683,9 +686,9 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_const
     for (int e = 0; e < V; e++) acc[e] = 0.f;
     if (all == 0) continue;  // idle: left as it was
     {
-      const int64_t nt = all / p.MT, t0 = p.first[u] + head / kItem * nt;
+      const int64_t nt = all / p.MT, t0 = p.first[u] + head / p.item * nt;
       const int c0 = range_of(total, ctas, t0), c1 = range_of(total, ctas, t0 + nt - 1);
-      const float *rec = p.rec + static_cast<size_t>(head % kItem) * (D + 4), *pre = nullptr;
+      const float *rec = p.rec + static_cast<size_t>(head % p.item) * (D + 4), *pre = nullptr;
       int np = 0;  // pieces of the shared prefix, which come first
       size_t step = 0;
       if (p.start && p.start[s] > 0) {
@@ -705,8 +708,8 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_const
         for (int j = 0; j < kJ; j++) {
           const int i = j0 + j, c = c0 + i - np;
           const float* x = i < np ? pre + step * i
-                           : c0 == c1 ? p.rec_item + ((static_cast<size_t>(u) * p.MT + head / kItem) * kItem + head % kItem) * (D + 4)
-                                      : rec + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kItem * (D + 4);
+                           : c0 == c1 ? p.rec_item + ((static_cast<size_t>(u) * p.MT + head / p.item) * p.item + head % p.item) * (D + 4)
+                                      : rec + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * p.item * (D + 4);
           ml[j] = make_float2(-INFINITY, 0.f);
 #pragma unroll
           for (int e = 0; e < V; e++) o[j][e] = 0.f;
@@ -772,13 +775,18 @@ static bool encode_pool_map(CUtensorMap* m, void* base, int D, int64_t all, int 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Query heads of an item: eight, a tile's columns, or sixteen, two tiles that share the
+// reads of keys and values, for groups of more.
+static int item_heads(const tv_paged_layer* l) { return l->Hq / l->Hkv <= 8 ? 8 : kItemMax; }
+
 // A call's scratch, in bytes from its start.
 struct PagedSpace {
   size_t cut, rec, first, rec_item, rec_prefix, info, group_of, start, all;
 };
 static PagedSpace space_of(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g) {
   const size_t line = static_cast<size_t>(l->D + 4) * 4, units = static_cast<size_t>(b->n_seq) * l->Hkv;
-  const size_t items = units * ((l->Hq / l->Hkv + kItem - 1) / kItem);
+  const int item = item_heads(l);
+  const size_t items = units * ((l->Hq / l->Hkv + item - 1) / item);
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t x = at;
@@ -787,10 +795,10 @@ static PagedSpace space_of(const tv_paged_layer* l, const tv_paged* b, const tv_
   };
   PagedSpace s{};
   s.cut = take(static_cast<size_t>(num_sms()) * 16);
-  s.rec = take(static_cast<size_t>(2) * num_sms() * kItem * line);
+  s.rec = take(static_cast<size_t>(2) * num_sms() * item * line);
   if (g) {
     s.first = take((units + 1) * 8);
-    s.rec_item = take(items * kItem * line);
+    s.rec_item = take(items * item * line);
     s.rec_prefix = take(static_cast<size_t>(paged_prefix_slots(l, b, g->n_group)) * 128 * line);
     s.info = take(static_cast<size_t>(g->n_group) * 16);
     s.group_of = take(static_cast<size_t>(b->n_seq) * 4);
@@ -801,15 +809,15 @@ static PagedSpace space_of(const tv_paged_layer* l, const tv_paged* b, const tv_
 }
 size_t paged_attn_ws_bytes(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g) { return space_of(l, b, g).all; }
 
-template <int D>
+template <int D, int NB>
 static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_t st) {
-  using C = Pg<D>;
+  using C = Pg<D, NB>;
   const tv_paged_layer* l = a.layer;
   p.R = l->page < C::ROWS ? l->page : C::ROWS;
   const int64_t all = static_cast<int64_t>(l->n_pages) * l->Hkv * l->page;
   if (!encode_pool_map(&p.tmK, l->K, D, all, p.R, true) || !encode_pool_map(&p.tmV, l->V, D, all, p.R, true)) return TV_ERR_CUDA;
   static std::atomic<uint64_t> set{0};
-  if (!allow_smem(attn_paged_tc_kernel<D>, C::SMEM, set)) return TV_ERR_CUDA;
+  if (!allow_smem(attn_paged_tc_kernel<D, NB>, C::SMEM, set)) return TV_ERR_CUDA;
   const int grid = num_sms();
   if (a.groups) {
     PagedPrefixParams x;
@@ -833,13 +841,13 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
     x.c = p.c;
     if (!paged_prefix_launch(x, D, st)) return TV_ERR_CUDA;
   }
-  launch_k(true, attn_paged_tc_kernel<D>, dim3(grid), dim3(kThreads), C::SMEM, st, p);
+  launch_k(true, attn_paged_tc_kernel<D, NB>, dim3(grid), dim3(kThreads), C::SMEM, st, p);
   if (a.groups) {
     const int64_t warps = static_cast<int64_t>(p.units) * p.G * (D > 128 ? D / 128 : 1);
     const int join = static_cast<int>(warps + 7 < static_cast<int64_t>(16) * grid ? (warps + 7) / 8 : 2 * grid);
     launch_k(true, attn_paged_join_kernel<D>, dim3(join), dim3(256), 0, st, p, grid);
   } else {
-    launch_k(true, attn_paged_join_cuts_kernel<D>, dim3(grid, p.G < kItem ? p.G : kItem), dim3(256), 0, st, p);
+    launch_k(true, attn_paged_join_cuts_kernel<D>, dim3(grid, p.G < p.item ? p.G : p.item), dim3(256), 0, st, p);
   }
   return launch_status();
 }
@@ -867,13 +875,14 @@ tv_status paged_attn_tc_launch(const PagedAttnCall& a, cudaStream_t st) {
   }
   p.Hq = l->Hq;
   p.G = l->Hq / l->Hkv;
-  p.MT = (p.G + kItem - 1) / kItem;
+  p.item = item_heads(l);
+  p.MT = (p.G + p.item - 1) / p.item;
   p.units = a.batch->n_seq * l->Hkv;
   p.c = a.scale * 1.4426950408889634f;
   switch (l->D) {
-    case 64: return launch_tc<64>(p, a, st);
-    case 128: return launch_tc<128>(p, a, st);
-    default: return launch_tc<256>(p, a, st);
+    case 64: return p.item == 8 ? launch_tc<64, 1>(p, a, st) : launch_tc<64, 2>(p, a, st);
+    case 128: return p.item == 8 ? launch_tc<128, 1>(p, a, st) : launch_tc<128, 2>(p, a, st);
+    default: return p.item == 8 ? launch_tc<256, 1>(p, a, st) : launch_tc<256, 2>(p, a, st);
   }
 }
 

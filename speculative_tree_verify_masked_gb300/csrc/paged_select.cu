@@ -16,9 +16,13 @@
 // lies.)  Bound by the reads of the codes, a 128th of the keys and values at pages
 // of 64 rows, and for few slots by latency.
 //
-// The choice is a radix selection of the n-th highest key in four passes of eight
-// bits, then one pass that writes the pages in rising order, of equal keys the
-// lower ones.
+// The choice is a radix selection of the n-th highest key by digits of eight bits,
+// from the highest bit in which the keys differ down, until a digit leaves no
+// choice; then one pass writes the pages in rising order, of equal keys the lower
+// ones.  A cluster of CTAs shares a slot's KV head: each scores its part of the pages
+// into the first one's shared memory, which then chooses.
+#include <climits>
+
 #include "paged.cuh"
 #include "prompt.cuh"
 
@@ -147,10 +151,11 @@ struct SelectParams {
   const void* q;
   const int8_t* code;
   const int32_t* exp;
-  float* score;  // [units][pages]
+  uint32_t* far;  // [units][pages]: keys that do not fit in shared memory
   int32_t* sel;
   int32_t* count;
   int Hq, Hkv, G, first, last, n_sel, pages;  // pages a slot has at most
+  int keys;                                   // keys that shared memory holds
 };
 
 // d += a b for one 16 x 8 x 32 tile of signed bytes
@@ -160,58 +165,139 @@ __device__ __forceinline__ void mma16832_s8(int (&d)[4], uint32_t a0, uint32_t a
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int kScorePages = 128;  // pages of a CTA: 32 a warp
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) { widen8(*reinterpret_cast<const uint4*>(p), x); }
 
+constexpr int kSelect = 256;        // threads of a CTA: each warp scores eight pages at a time
+constexpr int kSelectKeys = 16384;  // pages whose keys fit in shared memory
+
+// A rising key for a score (no NaN).
+__device__ __forceinline__ uint32_t rising(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores into the shared memory of the cluster's first CTA.
+__device__ __forceinline__ void store_first(uint32_t addr, uint32_t v) {
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.u32 [a], %1;\n\t}" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint32_t load_first(uint32_t addr) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, 0;\n\tld.shared::cluster.u32 %0, [a];\n\t}" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Dynamic shared memory: the keys (first CTA of a cluster; in the workspace where they do not fit).
 template <typename T, int D>
-__global__ void __launch_bounds__(128) paged_score_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kSelect) paged_select_kernel(const __grid_constant__ SelectParams p) {
   constexpr int LINE = 2 * D + 16;  // bytes of a query's [u-, u+] (rows 4 banks apart)
   constexpr int Q = 2 * D / 64;     // 16-byte pieces a lane of a row
+  constexpr int W = kSelect / 32;
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(16) int8_t code_s[16 * LINE];
-  __shared__ float top_s[4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ int hist[256], part[W][2];
+  __shared__ uint32_t red_s[W], red2_s[W];
+  __shared__ uint32_t prefix_s;
+  __shared__ int need_s, left_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_rank()), ctas = static_cast<int>(cluster_ctas());
+  // (No CTA may store into another's shared memory before that one has started, or after it
+  // has left: what the CTAs of a cluster do depends on the lengths alone, which they all read alike; an error
+  // that some of them meet first keeps the first CTA from writing, no more.)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
-  if (status_bad(p.b.status)) return;
+  const bool bad = status_bad(p.b.status);
   const int u = blockIdx.y, s = u / p.Hkv, h = u - s * p.Hkv;
   const int L = paged_len(p.b, s);
   const int nb = (L >> p.b.shift) + 1;
-  const int j0 = p.first + static_cast<int>(blockIdx.x) * kScorePages, end = nb - p.last;
-  if (L < 0 || nb <= p.n_sel || j0 >= end) return;
+  int32_t* sel = p.sel + static_cast<size_t>(u) * p.n_sel;
+  if (L < 0 || nb <= p.n_sel || p.n_sel == p.first + p.last) {  // (the whole cluster)
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (L < 0 || rank > 0 || bad) return;
+    const int ends = nb <= p.n_sel ? nb : p.first;
+    for (int i = tid; i < p.n_sel; i += kSelect) sel[i] = i < ends ? i : nb <= p.n_sel ? -1 : nb - p.n_sel + i;
+    if (tid == 0) p.count[u] = min(nb, p.n_sel);
+    return;
+  }
+  const int n = nb - p.first - p.last;  // pages to choose from
+  const bool kept = n <= p.keys;
+  uint32_t* far = p.far + static_cast<size_t>(u) * p.pages;
+  const uint32_t keys_at = static_cast<uint32_t>(__cvta_generic_to_shared(keys));
+  // the first pages' codes are on their way while the queries are looked at
+  const int tiles = (n + 7) / 8, stride = W * ctas, tile0 = rank * W + warp;
+  uint4 b[Q];
+  int64_t at = -1;  // this lane's page of a tile (as the second operand's column)
+  auto fetch = [&](int tile) {
+    const int j = tile * 8 + (lane >> 2);
+    const int page = j < n ? page_at(p.b, s, p.first + j) : -1;
+    at = page < 0 ? -1 : static_cast<int64_t>(page) * p.Hkv + h;
+    const uint4* src = reinterpret_cast<const uint4*>(p.code + (at < 0 ? 0 : at) * 2 * D) + (lane & 3);
+#pragma unroll
+    for (int i = 0; i < Q; i++) b[i] = src[i * 4];
+  };
+  if (tile0 < tiles) fetch(tile0);
   // the group's queries in whole steps
   const T* q = static_cast<const T*>(p.q) + (static_cast<size_t>(s) * p.Hq + h * p.G) * D;
-  float top = 0.f;
-  bool finite = true;
-  for (int i = threadIdx.x; i < p.G * D; i += 128) {
-    const float x = to_f32(q[i]);
-    finite = finite && isfinite(x);
-    top = fmaxf(top, fabsf(x));
-  }
+  uint32_t top = 0;  // the largest size, as bits (what is not finite comes out above every finite one)
+  for (int i = tid; i < p.G * D / 8; i += kSelect) {
+    float x[8];
+    load8(q + i * 8, x);
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) top_s[warp] = top;
-  finite = __syncthreads_and(finite) != 0;
-  top = fmaxf(fmaxf(top_s[0], top_s[1]), fmaxf(top_s[2], top_s[3]));
+    for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) red_s[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; w++) top = max(top, red_s[w]);
+  const bool finite = top < 0x7f800000u;
   int f = 0;
-  if (finite && top > 0.f) {
-    const float m = frexpf(top, &f);
+  if (finite && top > 0) {
+    const float m = frexpf(__uint_as_float(top), &f);
     f = f - 7 + (m > 127.f / 128.f ? 1 : 0);
   }
-  constexpr int NTW = kScorePages / 4 / 8;  // tiles of eight pages a warp
-  int best[NTW][2];
-  int64_t at[NTW];  // this lane's page of a tile (as the second operand's column)
-#pragma unroll
-  for (int t = 0; t < NTW; t++) {
-    best[t][0] = best[t][1] = INT_MIN;
-    const int j = j0 + (warp * NTW + t) * 8 + (lane >> 2);
-    const int page = j < end ? page_at(p.b, s, j) : -1;
-    at[t] = page < 0 ? -1 : static_cast<int64_t>(page) * p.Hkv + h;
-  }
+  // times 2^-f in two steps, each a power of two that fp32 holds (a product that is rounded on the way is under 1/2 in the end)
+  const int f1 = -f / 2;
+  const float by1 = finite ? ldexpf(1.f, f1) : 0.f, by2 = finite ? ldexpf(1.f, -f - f1) : 0.f;
+  const int pages0 = p.first;
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   for (int g0 = 0; g0 < p.G; g0 += 16) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * D; i += 128) {
-      const int g = g0 + i / D, d = i % D;
-      const int v = finite && g < p.G ? static_cast<int>(rintf(ldexpf(to_f32(q[static_cast<size_t>(g) * D + d]), -f))) : 0;
-      code_s[(i / D) * LINE + d] = static_cast<int8_t>(min(v, 0));
-      code_s[(i / D) * LINE + D + d] = static_cast<int8_t>(max(v, 0));
+    if (g0 > 0) __syncthreads();
+    for (int i = tid; i < 16 * D / 8; i += kSelect) {
+      const int g = i / (D / 8), d = i % (D / 8) * 8;
+      float x[8];
+      if (finite && g0 + g < p.G) {
+        load8(q + static_cast<size_t>(g0 + g) * D + d, x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++) x[e] = 0.f;
+      }
+      uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const int v = __float2int_rn(__fmul_rn(__fmul_rn(x[e], by1), by2));
+        lo[e / 4] |= (static_cast<uint32_t>(min(v, 0)) & 255u) << (e % 4 * 8);
+        hi[e / 4] |= (static_cast<uint32_t>(max(v, 0)) & 255u) << (e % 4 * 8);
+      }
+      *reinterpret_cast<uint2*>(code_s + g * LINE + d) = make_uint2(lo[0], lo[1]);
+      *reinterpret_cast<uint2*>(code_s + g * LINE + D + d) = make_uint2(hi[0], hi[1]);
     }
     __syncthreads();
     uint4 a[Q][2];
@@ -221,87 +307,83 @@ __global__ void __launch_bounds__(128) paged_score_kernel(const __grid_constant_
       for (int r = 0; r < 2; r++)
         a[i][r] = *reinterpret_cast<const uint4*>(code_s + ((lane >> 2) + 8 * r) * LINE + i * 64 + (lane & 3) * 16);
     const int live = min(16, p.G - g0);
+    for (int tile = tile0; tile < tiles; tile += stride) {
+      if (g0 > 0 && tile == tile0) fetch(tile);
+      uint4 c[Q];
 #pragma unroll
-    for (int t = 0; t < NTW; t++) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.code + (at[t] < 0 ? 0 : at[t]) * 2 * D) + (lane & 3);
-      uint4 b[Q];
-#pragma unroll
-      for (int i = 0; i < Q; i++) b[i] = at[t] < 0 ? make_uint4(0u, 0u, 0u, 0u) : src[i * 4];
+      for (int i = 0; i < Q; i++) c[i] = b[i];
+      const int64_t mine = at;
+      if (tile + stride < tiles) fetch(tile + stride);  // the next ones under these
       int d[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < Q; i++) {
-        mma16832_s8(d, a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, b[i].x, b[i].y);
-        mma16832_s8(d, a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, b[i].z, b[i].w);
+        mma16832_s8(d, a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, c[i].x, c[i].y);
+        mma16832_s8(d, a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, c[i].z, c[i].w);
       }
-      // the highest of the heads there are
+      // the highest of the heads there are, of pages 2 (lane & 3) and 2 (lane & 3) + 1
+      int best[2];
 #pragma unroll
-      for (int c = 0; c < 2; c++) {
-        int x = (lane >> 2) < live ? d[c] : INT_MIN;
-        if ((lane >> 2) + 8 < live) x = max(x, d[2 + c]);
+      for (int e = 0; e < 2; e++) {
+        int x = (lane >> 2) < live ? d[e] : INT_MIN;
+        if ((lane >> 2) + 8 < live) x = max(x, d[2 + e]);
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-        best[t][c] = max(best[t][c], x);
+        best[e] = x;
+      }
+      const int v0 = __shfl_sync(0xffffffffu, best[0], (lane & 7) >> 1), v1 = __shfl_sync(0xffffffffu, best[1], (lane & 7) >> 1);
+      const int64_t page = __shfl_sync(0xffffffffu, mine, (lane & 7) * 4);
+      const int j = tile * 8 + lane;
+      if (lane < 8 && j < n) {
+        const int e = page < 0 ? 0 : p.exp[page];
+        uint32_t key = rising(e >= 128 ? INFINITY : ldexpf(static_cast<float>(lane & 1 ? v1 : v0), e));
+        if (kept) {  // (later heads' scores of a page are this lane's own again)
+          if (g0 > 0) key = max(key, load_first(keys_at + j * 4));
+          store_first(keys_at + j * 4, key);
+        } else {
+          far[j] = g0 > 0 ? max(key, far[j]) : key;
+        }
       }
     }
   }
-#pragma unroll
-  for (int t = 0; t < NTW; t++) {
-    const int c = lane & 7, v = __shfl_sync(0xffffffffu, best[t][0], c >> 1), w = __shfl_sync(0xffffffffu, best[t][1], c >> 1);
-    const int64_t mine = __shfl_sync(0xffffffffu, at[t], c * 4);
-    const int j = j0 + (warp * NTW + t) * 8 + c;
-    if (lane < 8 && j < end) {
-      const int e = mine < 0 ? 0 : p.exp[mine];
-      p.score[static_cast<size_t>(u) * p.pages + j] = e >= 128 ? INFINITY : ldexpf(static_cast<float>(c & 1 ? w : v), e);
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// choice
-// ---------------------------------------------------------------------------
-constexpr int kPick = 512, kPickKeys = 8192;  // threads; keys kept in shared memory
-
-// A rising key for a score (no NaN).
-__device__ __forceinline__ uint32_t rising(float x) {
-  const uint32_t b = __float_as_uint(x);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-
-__global__ void __launch_bounds__(kPick) paged_pick_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ uint32_t keys[kPickKeys];
-  __shared__ int hist[256], part[kPick / 32][2];
-  __shared__ uint32_t prefix_s;
-  __shared__ int need_s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = blockIdx.x, s = u / p.Hkv;
-  pdl_wait();
-  if (status_bad(p.b.status)) return;
-  const int L = paged_len(p.b, s);
-  if (L < 0) return;
-  int32_t* sel = p.sel + static_cast<size_t>(u) * p.n_sel;
-  const int nb = (L >> p.b.shift) + 1;
-  if (nb <= p.n_sel) {
-    for (int i = threadIdx.x; i < p.n_sel; i += kPick) sel[i] = i < nb ? i : -1;
-    if (threadIdx.x == 0) p.count[u] = nb;
-    return;
-  }
-  const int n = nb - p.first - p.last, want = p.n_sel - p.first - p.last;
-  for (int i = threadIdx.x; i < p.first; i += kPick) sel[i] = i;
-  for (int i = threadIdx.x; i < p.last; i += kPick) sel[p.n_sel - p.last + i] = nb - p.last + i;
-  if (threadIdx.x == 0) p.count[u] = p.n_sel;
-  if (want == 0) return;
-  const float* score = p.score + static_cast<size_t>(u) * p.pages + p.first;
-  const bool kept = n <= kPickKeys;
-  auto key = [&](int i) { return kept ? keys[i] : rising(score[i]); };
-  if (kept)
-    for (int i = threadIdx.x; i < n; i += kPick) keys[i] = rising(score[i]);
-  uint32_t prefix = 0;
-  int need = want;  // of the keys that share the bits found so far
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+  if (ctas > 1) {
+    if (!kept) __threadfence();
+    cluster_sync();
+    if (rank > 0) return;
+  } else {
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kPick) {
-      const uint32_t k = key(i);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
+  }
+  if (bad) return;
+  // ---- the choice
+  auto key = [&](int i) { return kept ? keys[i] : __ldcg(far + i); };
+  uint32_t low = 0xffffffffu, high = 0;
+  for (int i = tid; i < n; i += kSelect) {
+    const uint32_t k = key(i);
+    low = min(low, k);
+    high = max(high, k);
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) {
+    red_s[warp] = low;
+    red2_s[warp] = high;
+  }
+  hist[tid] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; w++) {
+    low = min(low, red_s[w]);
+    high = max(high, red2_s[w]);
+  }
+  // Keys are low plus an offset of `bits` bits; of those whose offset starts with prefix, `need` are to be taken.
+  int bits = 32 - __clz(static_cast<int>(high - low)), need = p.n_sel - p.first - p.last;
+  uint32_t prefix = 0;
+  bool all = false;
+  while (bits > 0 && !all) {
+    const int shift = max(bits - 8, 0);
+    const uint32_t mask = (1u << (bits - shift)) - 1u;
+    for (int i = tid; i < n; i += kSelect) {
+      const uint32_t k = key(i) - low;
+      if (bits == 32 || (k >> bits) == (prefix >> bits)) atomicAdd(&hist[(k >> shift) & mask], 1);
     }
     __syncthreads();
     if (warp == 0) {  // from the top: lane 0 holds bins 255 .. 248
@@ -316,43 +398,61 @@ __global__ void __launch_bounds__(kPick) paged_pick_kernel(const __grid_constant
       }
       above -= sum;
       if (above < need && need <= above + sum) {
-        int i = 0;
-        while (above + c[i] < need) above += c[i++];
-        prefix_s = prefix | (static_cast<uint32_t>(255 - lane * 8 - i) << shift);
-        need_s = need - above;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          if (above < need && need <= above + c[i]) {
+            prefix_s = prefix | (static_cast<uint32_t>(255 - lane * 8 - i) << shift);
+            need_s = need - above;
+            left_s = c[i];
+            break;
+          }
+          above += c[i];
+        }
       }
     }
     __syncthreads();
     prefix = prefix_s;
     need = need_s;
-  }
-  // every higher key, and of those equal to it the first `need`
-  int out = 0, equal = 0;
-  for (int i0 = 0; i0 < n; i0 += kPick) {
-    const int i = i0 + threadIdx.x;
-    const uint32_t k = i < n ? key(i) : 0u;
-    const bool more = i < n && k > prefix, same = i < n && k == prefix;
-    const unsigned ms = __ballot_sync(0xffffffffu, same), low = (1u << lane) - 1u;
-    if (lane == 0) part[warp][0] = __popc(ms);
+    all = left_s == need;  // the whole digit is taken
+    bits = shift;
+    hist[tid] = 0;
     __syncthreads();
-    int rank = equal + __popc(ms & low), all_same = 0;
+  }
+  // every higher key, and of those that share all bits found the first `need`
+  const uint32_t border = prefix >> bits;  // (bits 32: no key differs in any)
+  int out = 0, equal = 0;
+  for (int i = tid; i < p.first; i += kSelect) sel[i] = i;
+  for (int i = tid; i < p.last; i += kSelect) sel[p.n_sel - p.last + i] = nb - p.last + i;
+  if (tid == 0) p.count[u] = p.n_sel;
+  for (int i0 = 0; i0 < n; i0 += kSelect) {
+    const int i = i0 + tid;
+    const uint32_t k = i < n ? (key(i) - low) >> bits : 0u;
+    const bool more = i < n && k > border, same = i < n && k == border;
+    const unsigned ms = __ballot_sync(0xffffffffu, same), below = (1u << lane) - 1u;
+    bool take = more || same;
+    int all_same = 0;
+    if (!all) {  // (else every equal one is taken)
+      if (lane == 0) part[warp][0] = __popc(ms);
+      __syncthreads();
+      int before = equal + __popc(ms & below);
 #pragma unroll
-    for (int w = 0; w < kPick / 32; w++) {
-      if (w < warp) rank += part[w][0];
-      all_same += part[w][0];
+      for (int w = 0; w < W; w++) {
+        if (w < warp) before += part[w][0];
+        all_same += part[w][0];
+      }
+      take = more || (same && before < need);
     }
-    const bool take = more || (same && rank < need);
     const unsigned mt = __ballot_sync(0xffffffffu, take);
     if (lane == 0) part[warp][1] = __popc(mt);
     __syncthreads();
-    int place = out + __popc(mt & low), all = 0;
+    int place = out + __popc(mt & below), sum = 0;
 #pragma unroll
-    for (int w = 0; w < kPick / 32; w++) {
+    for (int w = 0; w < W; w++) {
       if (w < warp) place += part[w][1];
-      all += part[w][1];
+      sum += part[w][1];
     }
-    if (take) sel[p.first + place] = p.first + i;
-    out += all;
+    if (take) sel[pages0 + place] = pages0 + i;
+    out += sum;
     equal += all_same;
     __syncthreads();
   }
@@ -383,10 +483,17 @@ static void launch_bounds_d(const BoundsParams& p, bool bf, dim3 g, cudaStream_t
   if (bf) launch_k(true, paged_bounds_kernel<__nv_bfloat16, D>, g, dim3(128), 0, st, p);
   else launch_k(true, paged_bounds_kernel<float, D>, g, dim3(128), 0, st, p);
 }
+template <typename T, int D>
+static bool launch_select_t(const SelectParams& p, int ctas, int units, cudaStream_t st) {
+  static std::atomic<uint64_t> set{0};
+  const int bytes = p.keys * 4;
+  if (!allow_smem(paged_select_kernel<T, D>, kSelectKeys * 4, set)) return false;
+  launch_k_cluster(true, ctas, paged_select_kernel<T, D>, dim3(ctas, units), dim3(kSelect), bytes, st, p);
+  return true;
+}
 template <int D>
-static void launch_score_d(const SelectParams& p, bool bf, dim3 g, cudaStream_t st) {
-  if (bf) launch_k(true, paged_score_kernel<__nv_bfloat16, D>, g, dim3(128), 0, st, p);
-  else launch_k(true, paged_score_kernel<float, D>, g, dim3(128), 0, st, p);
+static bool launch_select_d(const SelectParams& p, bool bf, int ctas, int units, cudaStream_t st) {
+  return bf ? launch_select_t<__nv_bfloat16, D>(p, ctas, units, st) : launch_select_t<float, D>(p, ctas, units, st);
 }
 
 }  // namespace tv
@@ -432,7 +539,7 @@ extern "C" tv_status tv_paged_bounds(const tv_paged_layer* l, const tv_paged* b,
 static int pages_at_most(const tv_paged_layer* l, const tv_paged* b) { return b->max_len / l->page + 1; }
 
 extern "C" size_t tv_paged_select_workspace_bytes(const tv_paged_layer* l, const tv_paged* b) {
-  if (paged_check(l, b) != TV_OK) return 0;
+  if (paged_check(l, b) != TV_OK || pages_at_most(l, b) <= kSelectKeys) return 0;
   return static_cast<size_t>(b->n_seq) * l->Hkv * pages_at_most(l, b) * 4;
 }
 
@@ -444,13 +551,14 @@ extern "C" tv_status tv_paged_select(const tv_paged_layer* l, const tv_paged* b,
   if (!code || !exp || !q || !sel || !count || first < 0 || last < 1 || n_sel < 1 || n_sel > 4096 || first > n_sel || last > n_sel - first)
     return TV_ERR_ARG;
   if (!aligned16(code) || !aligned16(exp) || !aligned16(q) || !aligned16(sel) || !aligned16(count) || !aligned16(ws)) return TV_ERR_ALIGN;
-  if (!ws || ws_bytes < tv_paged_select_workspace_bytes(l, b)) return TV_ERR_WORKSPACE;
+  const size_t need = tv_paged_select_workspace_bytes(l, b);
+  if (need > 0 && (!ws || ws_bytes < need)) return TV_ERR_WORKSPACE;
   SelectParams p{};
   p.b = paged_seqs(l, b);
   p.q = q;
   p.code = code;
   p.exp = exp;
-  p.score = static_cast<float*>(ws);
+  p.far = static_cast<uint32_t*>(ws);
   p.sel = sel;
   p.count = count;
   p.Hq = l->Hq;
@@ -460,19 +568,18 @@ extern "C" tv_status tv_paged_select(const tv_paged_layer* l, const tv_paged* b,
   p.last = last;
   p.n_sel = n_sel;
   p.pages = pages_at_most(l, b);
+  const int units = b->n_seq * l->Hkv;
+  const int most = p.pages > n_sel && n_sel > first + last ? p.pages - first - last : 0;  // pages to choose from, at most
+  p.keys = most < kSelectKeys ? most : kSelectKeys;
+  // CTAs for a slot's KV head: up to eight, while the GPU has room and each has 128 pages (the queries' codes take each as
+  // long as some 100 pages)
+  int ctas = 1;
+  while (ctas < 8 && units * ctas < 2 * num_sms() && ctas * 2 * 128 <= most) ctas *= 2;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int units = b->n_seq * l->Hkv, mid = p.pages - first - last;
-  if (p.pages > n_sel && n_sel > first + last) {
-    const dim3 g((mid + kScorePages - 1) / kScorePages, units);
-    const bool bf = l->dtype == TV_BF16;
-    switch (l->D) {
-      case 64: launch_score_d<64>(p, bf, g, st); break;
-      case 128: launch_score_d<128>(p, bf, g, st); break;
-      default: launch_score_d<256>(p, bf, g, st);
-    }
-  }
-  launch_k(true, paged_pick_kernel, dim3(units), dim3(kPick), 0, st, p);
-  return launch_status();
+  const bool bf = l->dtype == TV_BF16;
+  const bool ok = l->D == 64 ? launch_select_d<64>(p, bf, ctas, units, st) : l->D == 128 ? launch_select_d<128>(p, bf, ctas, units, st)
+                                                                                        : launch_select_d<256>(p, bf, ctas, units, st);
+  return ok ? launch_status() : TV_ERR_CUDA;
 }
 
 extern "C" tv_status tv_paged_advance(const tv_paged* b, const tv_paged_rows* rows, int32_t* len, tv_stream stream) {

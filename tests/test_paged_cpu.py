@@ -164,8 +164,11 @@ def test_select_and_bounds_refused(L):
     for bad in ({"code": K_RAW + 4}, {"exp": V_RAW + 4}, {"q": Q + 8}, {"sel": 0x7004}, {"cnt": 0x8004}, {"ws": FAR + 4}):
         assert select(L, **bad) == ALIGN, bad
     need = L.tv_paged_select_workspace_bytes(ref(layer()), ref(batch()))
-    assert need == 8 * 4 * 16 * 4
-    assert select(L, n=need - 1) == WORKSPACE and select(L, ws=0) == WORKSPACE
+    assert need == 0  # up to 16,384 pages
+    far = dict(l=layer(page=16), b=batch(cols=20000, max_len=16384 * 16))
+    need = L.tv_paged_select_workspace_bytes(ref(far["l"]), ref(far["b"]))
+    assert need == 8 * 4 * 16385 * 4
+    assert select(L, n=need - 1, **far) == WORKSPACE and select(L, ws=0, **far) == WORKSPACE
     for bad in ({"code": 0}, {"exp": 0}, {"code": K}, {"exp": K + 16}, {"exp": OUT + 16}):
         assert bounds(L, **bad) == ARG, bad
     assert bounds(L, code=OUT + 8) == ALIGN

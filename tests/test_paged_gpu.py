@@ -287,15 +287,17 @@ def test_select(dtype, heads, first, last, n_sel):
     assert p.status() == 0
 
 
-def test_select_long():
-    """More pages than the selection keeps in shared memory, all drawn from a few."""
-    lens, page, cols = [200000, 135008], 16, 12600
+@pytest.mark.parametrize("lens", [[200000, 135008], [16 * 16385 + 30, 400000]])
+@pytest.mark.parametrize("Hq", [8, 64])
+def test_select_long(lens, Hq):
+    """Many pages, all drawn from a few; more than shared memory holds."""
+    page, cols, G = 16, 26000, Hq // 2
     K = torch.randn(50, 2, page, 64, device="cuda").to(BF)
     table = torch.randint(0, 50, (2, cols), device="cuda", dtype=torch.int32)
-    layer, batch = B.PagedLayer(K, K, 8), B.PagedBatch(table, torch.tensor(lens, dtype=torch.int32, device="cuda"), 200010)
+    layer, batch = B.PagedLayer(K, K, Hq), B.PagedBatch(table, torch.tensor(lens, dtype=torch.int32, device="cuda"), 400010 if max(lens) > 200000 else 200010)
     code = torch.randint(-127, 128, (50, 2, 2, 64), device="cuda", dtype=torch.int8)
     exp = torch.randint(-3, 0, (50, 2), device="cuda", dtype=torch.int32)
-    q = torch.randn(2, 8, 64, device="cuda").to(BF)
+    q = torch.randn(2, Hq, 64, device="cuda").to(BF)
     for n_sel in (1000, 4096, 40):
         sel, count = torch.zeros(2, 2, n_sel, dtype=torch.int32, device="cuda"), torch.zeros(2, 2, dtype=torch.int32, device="cuda")
         ws = torch.empty(B.tv_paged_select_workspace_bytes(layer, batch), dtype=torch.uint8, device="cuda")
@@ -303,7 +305,7 @@ def test_select_long():
         for i, L in enumerate(lens):
             ids = table[i, 1:L // page - 1].tolist()
             for g in range(2):
-                want = O.select(f64(q[i, g * 4:g * 4 + 4]), code[ids, g].cpu().numpy().astype(np.int64), exp[ids, g].cpu().numpy(),
+                want = O.select(f64(q[i, g * G:g * G + G]), code[ids, g].cpu().numpy().astype(np.int64), exp[ids, g].cpu().numpy(),
                                 L // page + 1, 1, 2, n_sel)
                 assert sel[i, g].tolist() == want and int(count[i, g]) == n_sel
     assert batch.status_code() == 0
