@@ -100,22 +100,23 @@ __device__ __forceinline__ int unit_tiles(const PagedTcParams& p, int u) {
   return (L + 1 - (p.start ? p.start[s] : 0) + ROWS - 1) / ROWS;
 }
 
-constexpr int kNear = 32;
+constexpr int kNear = 16;
 
 // The items of a range of tiles, one after another.
 struct PagedPiece {
-  int s, h, m, k0, k1, nt;  // slot, KV head, item of it, tiles [k0, k1) of nt
+  int s, h, L, m, k0, k1, nt;  // slot, KV head, the slot's length, item, tiles [k0, k1) of nt
 };
 template <int ROWS>
 struct PagedWalk {
   int u, s, h;          // unit: slot and KV head
   int u0;               // the first unit of the range, and
-  const int* near;      // the tiles of that one and the kNear - 1 after it
+  const int2* near;     // tiles and length of that one and the kNear - 1 after it
   int off;  // tile within the unit, over its items (under 2^27: a slot has 2^30 rows at most, a unit 8 items)
   int64_t left;
   __device__ __forceinline__ bool next(const PagedTcParams& p, PagedPiece& x) {
     while (left > 0 && u < p.units) {
-      const int nt = u - u0 < kNear ? near[u - u0] : unit_tiles<ROWS>(p, u);
+      const int2 n = u - u0 < kNear ? near[u - u0] : make_int2(unit_tiles<ROWS>(p, u), paged_len(p.v.b, s));
+      const int nt = n.x;
       if (off >= nt * p.MT) {
         off = 0;
         u++;
@@ -127,6 +128,7 @@ struct PagedWalk {
       }
       x.s = s;
       x.h = h;
+      x.L = n.y;
       x.m = off < nt ? 0 : off / nt;
       x.k0 = off - x.m * nt;
       x.k1 = static_cast<int>(min(static_cast<int64_t>(nt), x.k0 + left));
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   Local& lo = *reinterpret_cast<Local*>(smem_raw + C::LOFF);
   int64_t* sums = reinterpret_cast<int64_t*>(smem_raw + C::SOFF);  // tiles of each warp's units (scores are not in use yet)
   static_assert(sizeof(Local) <= 128, "local data");
-  int* lo_near = reinterpret_cast<int*>(smem_raw + C::LOFF + 128);
+  int2* lo_near = reinterpret_cast<int2*>(smem_raw + C::LOFF + 128);
   volatile int* abort_flag = &lo.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -240,7 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     }
     __syncthreads();
   }
-  if (lo.left > 0 && threadIdx.x < kNear) lo_near[threadIdx.x] = lo.u + static_cast<int>(threadIdx.x) < p.units ? unit_tiles<C::ROWS>(p, lo.u + threadIdx.x) : 0;
+  if (lo.left > 0 && threadIdx.x < kNear && lo.u + static_cast<int>(threadIdx.x) < p.units) {
+    const int u = lo.u + threadIdx.x;
+    lo_near[threadIdx.x] = make_int2(unit_tiles<C::ROWS>(p, u), paged_len(p.v.b, u / p.v.Hkv));
+  }
   __syncthreads();
   PagedWalk<C::ROWS> walk{lo.u, lo.u / p.v.Hkv, lo.u % p.v.Hkv, lo.u, lo_near, lo.off, lo.left};
   PagedPiece x;
@@ -264,11 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     auto part = [&](const PagedPiece& x, int i, int& seen) -> int {
       seen = 0;
       if (i >= x.k1 * nsub) return -1;
-      const int L = paged_len(p.v.b, x.s), place = (p.start ? p.start[x.s] >> p.v.b.shift : 0) + i / per_page;
-      if (place >= p.v.pages(x.s, x.h, L)) return -1;
+      const int place = (p.start ? p.start[x.s] >> p.v.b.shift : 0) + i / per_page;
+      if (place >= p.v.pages(x.s, x.h, x.L)) return -1;
       const int col = p.v.column(x.s, x.h, place);
       if (col < 0) return -1;
-      const int r = (i % per_page) * R, n = min(R, L + 1 - (col * rows + r));
+      const int r = (i % per_page) * R, n = min(R, x.L + 1 - (col * rows + r));
       if (n <= 0) return -1;
       const int page = page_at(p.v.b, x.s, col);
       if (page < 0) return -1;

@@ -206,8 +206,8 @@ __device__ __forceinline__ uint32_t load_first(uint32_t addr) {
 
 // Dynamic shared memory: the keys (first CTA of a cluster; in the workspace where they do not fit).
 template <typename T, int D>
-__global__ void __launch_bounds__(kSelect) paged_select_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int LINE = 2 * D + 16;  // bytes of a query's [u-, u+] (rows 4 banks apart)
+__global__ void __launch_bounds__(kSelect, 2) paged_select_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int LINE = 2 * D + 64;  // bytes of a query's [u-, u+] (rows half a line of banks apart)
   constexpr int Q = 2 * D / 64;     // 16-byte pieces a lane of a row
   constexpr int W = kSelect / 32;
   extern __shared__ __align__(16) uint32_t keys[];
@@ -240,27 +240,34 @@ __global__ void __launch_bounds__(kSelect) paged_select_kernel(const __grid_cons
   const bool kept = n <= p.keys;
   uint32_t* far = p.far + static_cast<size_t>(u) * p.pages;
   const uint32_t keys_at = static_cast<uint32_t>(__cvta_generic_to_shared(keys));
-  // the first pages' codes are on their way while the queries are looked at
+  // Pages are dealt to the warps eight at a time, a tile; a warp looks up four tiles' pages and exponents at once.
+  // The first tile's codes are on their way while the queries are looked at.
   const int tiles = (n + 7) / 8, stride = W * ctas, tile0 = rank * W + warp;
   uint4 b[Q];
-  int64_t at = -1;  // this lane's page of a tile (as the second operand's column)
-  auto fetch = [&](int tile) {
-    const int j = tile * 8 + (lane >> 2);
-    const int page = j < n ? page_at(p.b, s, p.first + j) : -1;
-    at = page < 0 ? -1 : static_cast<int64_t>(page) * p.Hkv + h;
-    const uint4* src = reinterpret_cast<const uint4*>(p.code + (at < 0 ? 0 : at) * 2 * D) + (lane & 3);
-#pragma unroll
-    for (int i = 0; i < Q; i++) b[i] = src[i * 4];
+  int page = -1, e = 0;  // of place (lane & 7) of tile `first of four` + (lane >> 3) * stride
+  auto look = [&](int tile) {
+    const int j = (tile + (lane >> 3) * stride) * 8 + (lane & 7);
+    page = j < n ? page_at(p.b, s, p.first + j) : -1;
+    e = page < 0 ? 0 : p.exp[static_cast<size_t>(page) * p.Hkv + h];
   };
-  if (tile0 < tiles) fetch(tile0);
+  auto fetch = [&](int i) {  // codes of the i-th of the four: this lane's page as the second operand's column
+    const int x = __shfl_sync(0xffffffffu, page, i * 8 + (lane >> 2));
+    const uint4* src = reinterpret_cast<const uint4*>(p.code + (static_cast<size_t>(x < 0 ? 0 : x) * p.Hkv + h) * 2 * D) + (lane & 3);
+#pragma unroll
+    for (int k = 0; k < Q; k++) b[k] = src[k * 4];
+  };
+  if (tile0 < tiles) {
+    look(tile0);
+    fetch(0);
+  }
   // the group's queries in whole steps
   const T* q = static_cast<const T*>(p.q) + (static_cast<size_t>(s) * p.Hq + h * p.G) * D;
   uint32_t top = 0;  // the largest size, as bits (what is not finite comes out above every finite one)
+  float mine[8];     // this thread's last eight values (its only ones in a small group)
   for (int i = tid; i < p.G * D / 8; i += kSelect) {
-    float x[8];
-    load8(q + i * 8, x);
+    load8(q + i * 8, mine);
 #pragma unroll
-    for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+    for (int c = 0; c < 8; c++) top = max(top, __float_as_uint(mine[c]) & 0x7fffffffu);
   }
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) red_s[warp] = top;
@@ -284,7 +291,12 @@ __global__ void __launch_bounds__(kSelect) paged_select_kernel(const __grid_cons
       const int g = i / (D / 8), d = i % (D / 8) * 8;
       float x[8];
       if (finite && g0 + g < p.G) {
-        load8(q + static_cast<size_t>(g0 + g) * D + d, x);
+        if (p.G <= 16 && p.G * D <= kSelect * 8) {
+#pragma unroll
+          for (int c = 0; c < 8; c++) x[c] = mine[c];
+        } else {
+          load8(q + static_cast<size_t>(g0 + g) * D + d, x);
+        }
       } else {
 #pragma unroll
         for (int e = 0; e < 8; e++) x[e] = 0.f;
@@ -300,42 +312,38 @@ __global__ void __launch_bounds__(kSelect) paged_select_kernel(const __grid_cons
       *reinterpret_cast<uint2*>(code_s + g * LINE + D + d) = make_uint2(hi[0], hi[1]);
     }
     __syncthreads();
-    uint4 a[Q][2];
-#pragma unroll
-    for (int i = 0; i < Q; i++)
-#pragma unroll
-      for (int r = 0; r < 2; r++)
-        a[i][r] = *reinterpret_cast<const uint4*>(code_s + ((lane >> 2) + 8 * r) * LINE + i * 64 + (lane & 3) * 16);
     const int live = min(16, p.G - g0);
-    for (int tile = tile0; tile < tiles; tile += stride) {
-      if (g0 > 0 && tile == tile0) fetch(tile);
-      uint4 c[Q];
-#pragma unroll
-      for (int i = 0; i < Q; i++) c[i] = b[i];
-      const int64_t mine = at;
-      if (tile + stride < tiles) fetch(tile + stride);  // the next ones under these
+    const int8_t* row = code_s + (lane >> 2) * LINE + (lane & 3) * 16;
+    int i = 0;
+    for (int tile = tile0; tile < tiles; tile += stride, i = (i + 1) & 3) {
+      if (i == 0 && (g0 > 0 || tile > tile0)) {
+        look(tile);
+        fetch(0);
+      }
       int d[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < Q; i++) {
-        mma16832_s8(d, a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, c[i].x, c[i].y);
-        mma16832_s8(d, a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, c[i].z, c[i].w);
+      for (int k = 0; k < Q; k++) {
+        const uint4 x = *reinterpret_cast<const uint4*>(row + k * 64);
+        uint4 y = make_uint4(0u, 0u, 0u, 0u);
+        if (live > 8) y = *reinterpret_cast<const uint4*>(row + 8 * LINE + k * 64);
+        mma16832_s8(d, x.x, y.x, x.y, y.y, b[k].x, b[k].y);
+        mma16832_s8(d, x.z, y.z, x.w, y.w, b[k].z, b[k].w);
       }
+      if (i < 3 && tile + stride < tiles) fetch(i + 1);  // the next ones under what follows
       // the highest of the heads there are, of pages 2 (lane & 3) and 2 (lane & 3) + 1
       int best[2];
 #pragma unroll
-      for (int e = 0; e < 2; e++) {
-        int x = (lane >> 2) < live ? d[e] : INT_MIN;
-        if ((lane >> 2) + 8 < live) x = max(x, d[2 + e]);
+      for (int c = 0; c < 2; c++) {
+        int x = (lane >> 2) < live ? d[c] : INT_MIN;
+        if ((lane >> 2) + 8 < live) x = max(x, d[2 + c]);
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-        best[e] = x;
+        best[c] = x;
       }
       const int v0 = __shfl_sync(0xffffffffu, best[0], (lane & 7) >> 1), v1 = __shfl_sync(0xffffffffu, best[1], (lane & 7) >> 1);
-      const int64_t page = __shfl_sync(0xffffffffu, mine, (lane & 7) * 4);
-      const int j = tile * 8 + lane;
+      const int ex = __shfl_sync(0xffffffffu, e, i * 8 + (lane & 7)), j = tile * 8 + lane;
       if (lane < 8 && j < n) {
-        const int e = page < 0 ? 0 : p.exp[page];
-        uint32_t key = rising(e >= 128 ? INFINITY : ldexpf(static_cast<float>(lane & 1 ? v1 : v0), e));
+        uint32_t key = rising(ex >= 128 ? INFINITY : ldexpf(static_cast<float>(lane & 1 ? v1 : v0), ex));
         if (kept) {  // (later heads' scores of a page are this lane's own again)
           if (g0 > 0) key = max(key, load_first(keys_at + j * 4));
           store_first(keys_at + j * 4, key);
