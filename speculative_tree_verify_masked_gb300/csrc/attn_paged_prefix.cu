@@ -22,6 +22,9 @@
 // P goes through shared memory.  PV of tile t-1 sits between Q K^T of t and of t+1
 // on the tensor pipe: S(t) is read out during it, and one S buffer is enough.
 //
+// It follows the kernel for what each slot sees by itself and starts on SMs as that one
+// leaves them.
+//
 // Work split.  Every CTA derives the same plan from the device-side groups and
 // lengths: S with the fewest tiles for the busiest CTA; pieces of the same keys lie
 // next to each other in the order of all, so CTAs that run at the same time read
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
                  PFULL = SFULL + 16u, ODONE = SFULL + 24u, QREADY = SFULL + 32u, XBAR0 = SFULL + 40u, DRAIN = XBAR0 + 32u;
   struct Local {
     uint32_t tmem;
-    int abort_flag, skip, S;
+    int abort_flag, most;
     unsigned long long best;
   };
   Local& lo = *reinterpret_cast<Local*>(smem_raw + C::LOFF);
@@ -140,62 +143,35 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
     mbar_init(DRAIN + 8u, 1);
     lo.abort_flag = 0;
     lo.best = ~0ull;
+    lo.most = 0;
     fence_mbar_init();
   }
-  pdl_wait();
-  // the groups: checked, and what each shares
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&lo.tmem), C::COLS);
+    tmem_relinquish();
+  }
+  // (The kernel before on the stream is the call's own, for what each slot sees by itself; it has waited before it let
+  // this one in, and writes nothing that is read here, nor the other way round.)
+  pdl_trigger();
+  const int NG = p.n_group;
+  int* count = reinterpret_cast<int*>(smem_raw);  // (the ring is not in use yet)
+  GroupCheck<kPrefixThreads> check{gr.off, count, count + TV_MAX_PAGED_SEQ, gr.src, gr.nk};
   int code = sb & 1023u ? TV_ERR_CUDA : 0;
-  const bool bad = status_bad(p.b.status);
-  const int NG = p.n_group, rows = 1 << p.b.shift;
-  int* active = reinterpret_cast<int*>(smem_raw);  // (the ring is not in use yet)
-  int* least = active + TV_MAX_PAGED_SEQ;
-  for (int g = tid; g <= NG; g += kPrefixThreads) {
-    const int o = p.group_off[g];
-    gr.off[g] = o;
-    if ((g == 0 && o != 0) || (g == NG && o != p.b.n_seq) || (g < NG && p.group_off[g + 1] < o)) code = TV_ERR_ROWS;
-    if (g < NG) {
-      active[g] = 0;
-      least[g] = INT_MAX;
-      gr.src[g] = INT_MAX;
-    }
-  }
-  if (__syncthreads_or(code != 0 || bad)) {
+  code = check.run(p.b, p.group_off, p.shared, NG, code);
+  if (code || __syncthreads_or(status_bad(p.b.status))) {
     if (code) set_status(p.b.status, code);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(lo.tmem, C::COLS);
+    pdl_wait();
     return;
   }
-  for (int s = tid; s < p.b.n_seq; s += kPrefixThreads) {
-    int a = 0, z = NG;  // the last group that starts at or before slot s: the one that holds it
-    while (z - a > 1) {
-      const int mid = (a + z) >> 1;
-      if (gr.off[mid] <= s) a = mid;
-      else z = mid;
-    }
-    const int L = paged_len(p.b, s);
-    if (L >= 0) {
-      atomicAdd(&active[a], 1);
-      atomicMin(&least[a], L);
-      atomicMin(&gr.src[a], s);
-    }
-    if (blockIdx.x == 0) p.group_of[s] = a;
-  }
-  __syncthreads();
+  // (nk holds the shared rows so far)
   int most = 0;
-  for (int g = tid; g < NG; g += kPrefixThreads) {
-    const int sh = p.shared[g];
-    if (sh < 0 || (sh & (rows - 1)) || (active[g] > 0 && sh > least[g])) code = TV_ERR_ROWS;
-    gr.nk[g] = code == 0 && active[g] > 1 ? ceil_div(sh, kKeyTile) : 0;
-    most = max(most, gr.nk[g]);
-    // (slots of other groups see all their rows by themselves)
-  }
-  if (__syncthreads_or(code != 0)) {
-    if (code) set_status(p.b.status, code);
-    return;
-  }
-  lo.skip = 0;
+  for (int g = tid; g < NG; g += kPrefixThreads) most = max(most, gr.nk[g] = ceil_div(gr.nk[g], kKeyTile));
+  if (most > 0) atomicMax(&lo.most, most);
   __syncthreads();
-  atomicMax(&lo.skip, most);
-  __syncthreads();
-  most = lo.skip;  // key tiles of the longest prefix
+  most = lo.most;  // key tiles of the longest prefix
   // S: candidates by the pieces that the longest prefix is cut into, a thread each; the cost is the tiles of
   // the CTA with most pieces, and about four for each to start, to end and to be joined
   if (most > 0) {
@@ -224,21 +200,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
     }
     if (lane == 0) gr.cum[NG] = before;
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(&lo.tmem), C::COLS);
-    tmem_relinquish();
-  }
   fence_proxy_async_smem();  // (the ring has held the groups' counts)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (blockIdx.x == 0) {  // for the kernels that follow
+  if (blockIdx.x == 0) {  // for the join
     for (int g = tid; g < NG; g += kPrefixThreads)
-      p.info[g] = make_int4(gr.cum[g], ceil_div((gr.off[g + 1] - gr.off[g]) * p.G, 128), ceil_div(gr.nk[g], S), gr.off[g]);
-    for (int s = tid; s < p.b.n_seq; s += kPrefixThreads) {
-      const int g = p.group_of[s];  // (this thread's own write)
-      p.start[s] = gr.nk[g] > 0 ? p.shared[g] : 0;
-    }
+      for (int s = gr.off[g]; s < gr.off[g + 1]; s++)
+        p.info[s] = make_int4(gr.cum[g], ceil_div((gr.off[g + 1] - gr.off[g]) * p.G, 128), ceil_div(gr.nk[g], S), s - gr.off[g]);
   }
   const uint32_t tbase = lo.tmem;
   const int total = gr.cum[NG];
@@ -249,7 +218,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    const int R = p.R, parts = kKeyTile / R, per_page = max(1, rows / R);  // boxes of R rows
+    const int R = p.R, parts = kKeyTile / R, rows = 1 << p.b.shift, per_page = rows / R;  // boxes of R rows
     uint32_t it = 0;
     bool ok = true;
     for (int x = blockIdx.x; ok && x < total; x += gridDim.x) {
@@ -286,13 +255,25 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(full, C::UNIT);
           __syncwarp();
-          // boxes of the unit, one a lane: parts x columns (16 at most)
-          const int up = is_k ? parts : C::VROWS / R, cols = is_k ? C::KBU : C::VB;
-          const int pt = lane % up, ch = lane / up;
-          const int from = __shfl_sync(0xffffffffu, row, at + (is_k ? 0 : u * up) + pt);
-          if (ch < cols)
-            tma_load_2d(dst + ch * (is_k ? C::KBOX : C::VBOX) + pt * R * 128, is_k ? &p.tmK : &p.tmV, full,
-                        (is_k ? u * C::KBU + ch : ch) * 64, from);
+          // one thread issues (a copy takes its operands from uniform registers: lanes of a
+          // warp that issue different ones take turns, at twice the time a tile)
+          if (is_k) {
+            for (int pt = 0; pt < parts; pt++) {
+              const int from = __shfl_sync(0xffffffffu, row, at + pt);
+              if (lane == 0)
+#pragma unroll
+                for (int ch = 0; ch < C::KBU; ch++)
+                  tma_load_2d(dst + ch * C::KBOX + pt * R * 128, &p.tmK, full, (u * C::KBU + ch) * 64, from);
+            }
+          } else {
+            const int up = C::VROWS / R;
+            for (int pt = 0; pt < up; pt++) {
+              const int from = __shfl_sync(0xffffffffu, row, at + u * up + pt);
+              if (lane == 0)
+#pragma unroll
+                for (int ch = 0; ch < C::VB; ch++) tma_load_2d(dst + ch * C::VBOX + pt * R * 128, &p.tmV, full, ch * 64, from);
+            }
+          }
           __syncwarp();
         }
       }
@@ -372,36 +353,47 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
       xc++;
       return true;
     };
-    // Q of an item into tensor memory, each thread its half of its row, once every Q K^T of the item before has completed
+    // Q of an item into tensor memory, a warp its rows' half, 64 columns at a time turned around in its patch (free: every
+    // P V of the item before has completed)
     auto load_q = [&](const PrefixItem& I) {
       if (hf < C::QH) {
-        const int row = I.r * 128 + lrow;
-        const bool act = row < I.n;
-        const int m = act ? row / p.G : 0, head = act ? row % p.G : 0;
-        const __nv_bfloat16* q = p.q + ((static_cast<size_t>(gr.off[I.g]) + m) * p.Hq + I.h * p.G + head) * D + hf * (D / 2);
+        const int cl = lane & 7;  // 16 bytes of a row's 128
         uint4 v[C::QR][8];
 #pragma unroll
-        for (int r = 0; r < C::QR; r++)
+        for (int i = 0; i < 8; i++) {
+          const int row = I.r * 128 + quad * 32 + i * 4 + (lane >> 3);
+          const int m = row < I.n ? row / p.G : 0, head = row < I.n ? row % p.G : 0;
+          const __nv_bfloat16* q = p.q + ((static_cast<size_t>(gr.off[I.g]) + m) * p.Hq + I.h * p.G + head) * D + hf * (D / 2) + cl * 8;
 #pragma unroll
-          for (int i = 0; i < 8; i++) v[r][i] = ldg16(q + r * 64 + i * 8);
+          for (int r = 0; r < C::QR; r++) v[r][i] = ldg16(q + r * 64);
+        }
 #pragma unroll
         for (int r = 0; r < C::QR; r++) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const int rr = i * 4 + (lane >> 3);
+            sts16(patch + rr * 128 + (((cl ^ rr) & 7) << 4), v[r][i].x, v[r][i].y, v[r][i].z, v[r][i].w);
+          }
+          __syncwarp();
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 8; i++) {
-            w[4 * i] = v[r][i].x;
-            w[4 * i + 1] = v[r][i].y;
-            w[4 * i + 2] = v[r][i].z;
-            w[4 * i + 3] = v[r][i].w;
+            const uint4 x = lds16(patch + lane * 128 + (((i ^ lane) & 7) << 4));
+            w[4 * i] = x.x;
+            w[4 * i + 1] = x.y;
+            w[4 * i + 2] = x.z;
+            w[4 * i + 3] = x.w;
           }
           tmem_st32(tl + C::T_Q + (hf * C::QR + r) * 32, w);
         }
         tmem_st_wait();
+        __syncwarp();
       }
       tc_fence_before();
       arrive(QREADY);
     };
-    PrefixItem I, J;
+    PrefixItem I;
     int x = blockIdx.x;
     if (x < total) {
       I = prefix_item(p, gr, S, x);
@@ -486,10 +478,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
         arrive(PFULL);
       }
       if (!ok) break;
-      if (x + static_cast<int>(gridDim.x) < total) {  // the next item's first Q K^T runs beside this one's last P V and output
-        J = prefix_item(p, gr, S, x + gridDim.x);
-        load_q(J);
-      }
       if (!exchange(l, other) || !wait_warp(ODONE, (t - 1) & 1, abort_flag, kWaitCycles)) {
         ok = false;
         break;
@@ -519,8 +507,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
         rec[D + 1] = __fadd_rn(l, other);
       }
       __syncwarp();
+      if (x + static_cast<int>(gridDim.x) < total) {
+        I = prefix_item(p, gr, S, x + gridDim.x);
+        load_q(I);
+      }
       tc_fence_before();
-      I = J;
     }
     if (!ok && lane == 0) set_status(p.b.status, TV_ERR_TIMEOUT);
   }
@@ -528,6 +519,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tbase, C::COLS);
+  pdl_wait();  // the join, which waits for this kernel, needs both
 }
 
 template <int D>

@@ -14,13 +14,61 @@ struct PagedPrefixParams {
   const int32_t* shared;     // [n_group]
   const __nv_bfloat16* q;
   float* rec;       // [slots][128][D + 4]: O, m and l of a piece's rows
-  int4* info;       // [n_group]: first piece, row tiles, pieces along the keys, first slot
-  int32_t* group_of;  // [n_seq]
-  int32_t* start;     // [n_seq]: rows that the pieces cover, 0: none
+  int4* info;       // [n_seq], for the join: the group's first piece, row tiles, pieces along the keys (0: nothing shared), place in it
   int n_group, slots, Hq, Hkv, G, R;
   int all_rows;  // of a pool
   float c;       // scale * log2(e)
 };
+// The groups of a call, checked by a whole CTA of THREADS: first slots [n + 1] into off; active members,
+// their least length and first one into count, least and src [n]; into rows [n] how many
+// rows a group shares (0 where fewer than two members are active).  All in shared memory.
+template <int THREADS>
+struct GroupCheck {
+  int *off, *count, *least, *src, *rows;
+
+  // The group that slot s belongs to: the last that starts at or before it.
+  __device__ __forceinline__ int of(int n, int s) const {
+    int a = 0, z = n;
+    while (z - a > 1) {
+      const int mid = (a + z) >> 1;
+      if (off[mid] <= s) a = mid;
+      else z = mid;
+    }
+    return a;
+  }
+  // 0, or what is wrong (every thread gets it).
+  __device__ int run(const PagedSeqs& b, const int32_t* group_off, const int32_t* shared, int n, int code) {
+    const int tid = threadIdx.x;
+    const int L0 = tid < b.n_seq ? paged_len(b, tid) : -1;  // (these loads are on their way together)
+    for (int g = tid; g <= n; g += THREADS) {
+      const int o = group_off[g];
+      off[g] = o;
+      if ((g == 0 && o != 0) || (g == n && o != b.n_seq) || (g < n && group_off[g + 1] < o)) code = TV_ERR_ROWS;
+      if (g < n) {
+        rows[g] = shared[g];
+        count[g] = 0;
+        least[g] = src[g] = INT_MAX;
+      }
+    }
+    if (__syncthreads_or(code)) return code ? code : TV_ERR_ROWS;
+    for (int s = tid; s < b.n_seq; s += THREADS) {
+      const int L = s == tid ? L0 : paged_len(b, s);
+      if (L < 0) continue;
+      const int g = of(n, s);
+      atomicAdd(&count[g], 1);
+      atomicMin(&least[g], L);
+      atomicMin(&src[g], s);
+    }
+    __syncthreads();
+    for (int g = tid; g < n; g += THREADS) {
+      const int x = rows[g];
+      if (x < 0 || (x & ((1 << b.shift) - 1)) || (count[g] > 0 && x > least[g])) code = TV_ERR_ROWS;
+      if (count[g] < 2) rows[g] = 0;
+    }
+    return __syncthreads_or(code) ? TV_ERR_ROWS : 0;
+  }
+};
+
 int paged_prefix_slots(const tv_paged_layer* l, const tv_paged* b, int n_group);
 bool paged_prefix_launch(const PagedPrefixParams& p, int D, cudaStream_t st);
 

@@ -72,7 +72,10 @@ struct Pg {
 struct PagedTcParams {
   CUtensorMap tmK, tmV;  // pools as [D / 64][rows][64], boxes of R whole rows
   PagedView v;
-  const int32_t* start;  // [n_seq] rows that the kernel for shared prefixes has seen to, or null
+  const int32_t* group_off;  // groups of slots with shared prefixes, or null
+  const int32_t* shared;
+  int n_group;
+  int32_t* start;        // [n_seq] rows that the kernel for shared prefixes sees to, or null
   const __nv_bfloat16* q;
   const __nv_bfloat16* gate;
   __nv_bfloat16* out;
@@ -82,8 +85,7 @@ struct PagedTcParams {
   float* rec;      // [2 * CTAs][heads][D + 4]
   float* rec_item;  // [items][heads][D + 4]: items of slots with a shared prefix
   const float* rec_prefix;  // [pieces][128][D + 4]
-  const int4* info;         // [groups] and
-  const int32_t* group_of;  // [n_seq], as the kernel for shared prefixes left them
+  const int4* info;         // [n_seq], as the kernel for shared prefixes leaves it
   int Hq, G, MT, units;  // MT items a unit
   int item;              // query heads of an item
   int R;  // rows of a box: a page's, or a tile's
@@ -192,6 +194,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   }
   __syncthreads();
   if (lo.skip) return;
+  if (p.start) {  // (every CTA writes the same)
+    int* at = reinterpret_cast<int*>(smem_raw);  // (the rings are not in use yet)
+    constexpr int N = TV_MAX_PAGED_SEQ + 4;
+    GroupCheck<kThreads> check{at, at + N, at + 2 * N, at + 3 * N, at + 4 * N};
+    const int code = check.run(p.v.b, p.group_off, p.shared, p.n_group, 0);
+    if (code) {
+      set_status(p.v.b.status, code);
+      return;
+    }
+    for (int s = threadIdx.x; s < p.v.b.n_seq; s += kThreads) p.start[s] = check.rows[check.of(p.n_group, s)];
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
   // this CTA's range: a run of units for each thread, their tiles summed over the CTA
   {
     const int per = (p.units + kThreads - 1) / kThreads;
@@ -685,6 +700,7 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_const
     const int head = r / PARTS, col = (r % PARTS) * CPW + lane * V;
     const int s = u / p.v.Hkv, h = u - s * p.v.Hkv;
     const int64_t all = p.first[u + 1] - p.first[u];
+    const int4 g = p.info[s];
     const size_t at = (static_cast<size_t>(s) * p.Hq + h * p.G + head) * D + col;
     float acc[V], m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -696,9 +712,8 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_const
       const float *rec = p.rec + static_cast<size_t>(head % p.item) * (D + 4), *pre = nullptr;
       int np = 0;  // pieces of the shared prefix, which come first
       size_t step = 0;
-      if (p.start && p.start[s] > 0) {
-        const int4 g = p.info[p.group_of[s]];
-        const int row = (s - g.w) * p.G + head;
+      if (g.z > 0) {
+        const int row = g.w * p.G + head;
         np = g.z;
         step = static_cast<size_t>(g.y) * 128 * (D + 4);
         pre = p.rec_prefix + (static_cast<size_t>(g.x + h * np * g.y + row / 128) * 128 + row % 128) * (D + 4);
@@ -786,7 +801,7 @@ static int item_heads(const tv_paged_layer* l) { return l->Hq / l->Hkv <= 8 ? 8 
 
 // A call's scratch, in bytes from its start.
 struct PagedSpace {
-  size_t cut, rec, first, rec_item, rec_prefix, info, group_of, start, all;
+  size_t cut, rec, first, rec_item, rec_prefix, info, start, all;
 };
 static PagedSpace space_of(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g) {
   const size_t line = static_cast<size_t>(l->D + 4) * 4, units = static_cast<size_t>(b->n_seq) * l->Hkv;
@@ -805,8 +820,7 @@ static PagedSpace space_of(const tv_paged_layer* l, const tv_paged* b, const tv_
     s.first = take((units + 1) * 8);
     s.rec_item = take(items * item * line);
     s.rec_prefix = take(static_cast<size_t>(paged_prefix_slots(l, b, g->n_group)) * 128 * line);
-    s.info = take(static_cast<size_t>(g->n_group) * 16);
-    s.group_of = take(static_cast<size_t>(b->n_seq) * 4);
+    s.info = take(static_cast<size_t>(b->n_seq) * 16);
     s.start = take(static_cast<size_t>(b->n_seq) * 4);
   }
   s.all = at;
@@ -824,6 +838,7 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
   static std::atomic<uint64_t> set{0};
   if (!allow_smem(attn_paged_tc_kernel<D, NB>, C::SMEM, set)) return TV_ERR_CUDA;
   const int grid = num_sms();
+  launch_k(true, attn_paged_tc_kernel<D, NB>, dim3(grid), dim3(kThreads), C::SMEM, st, p);
   if (a.groups) {
     PagedPrefixParams x;
     memset(&x, 0, sizeof(x));
@@ -835,8 +850,6 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
     x.q = p.q;
     x.rec = const_cast<float*>(p.rec_prefix);
     x.info = const_cast<int4*>(p.info);
-    x.group_of = const_cast<int32_t*>(p.group_of);
-    x.start = const_cast<int32_t*>(p.start);
     x.n_group = a.groups->n_group;
     x.slots = paged_prefix_slots(l, a.batch, x.n_group);
     x.Hq = p.Hq;
@@ -846,7 +859,6 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
     x.c = p.c;
     if (!paged_prefix_launch(x, D, st)) return TV_ERR_CUDA;
   }
-  launch_k(true, attn_paged_tc_kernel<D, NB>, dim3(grid), dim3(kThreads), C::SMEM, st, p);
   if (a.groups) {
     const int64_t warps = static_cast<int64_t>(p.units) * p.G * (D > 128 ? D / 128 : 1);
     const int join = static_cast<int>(warps + 7 < static_cast<int64_t>(16) * grid ? (warps + 7) / 8 : 2 * grid);
@@ -875,8 +887,10 @@ tv_status paged_attn_tc_launch(const PagedAttnCall& a, cudaStream_t st) {
     p.rec_item = reinterpret_cast<float*>(ws + x.rec_item);
     p.rec_prefix = reinterpret_cast<const float*>(ws + x.rec_prefix);
     p.info = reinterpret_cast<const int4*>(ws + x.info);
-    p.group_of = reinterpret_cast<const int32_t*>(ws + x.group_of);
-    p.start = reinterpret_cast<const int32_t*>(ws + x.start);
+    p.start = reinterpret_cast<int32_t*>(ws + x.start);
+    p.group_off = a.groups->group_off;
+    p.shared = a.groups->shared;
+    p.n_group = a.groups->n_group;
   }
   p.Hq = l->Hq;
   p.G = l->Hq / l->Hkv;
