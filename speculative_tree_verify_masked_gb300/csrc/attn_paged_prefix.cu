@@ -14,10 +14,9 @@
 // because the tensor cores take P and V in one type (by 2^-8 of itself at most; l
 // adds them as they were).
 //
-// Roles (384 threads, one CTA per SM, persistent).  Warp 0 looks up pages, 32 boxes'
-// worth at a time, and streams key and value units by TMA through one ring in the
-// order the tensor core takes them: K0, K1 V0, K2 V1, ...  Warp 1 issues Q K^T,
-// warp 10 P V.  Warps 2-9 do the softmax, two threads to a row (64 scores each).
+// Roles (384 threads, one CTA per SM, persistent).  Warp 11 looks up pages, a thread of
+// warp 0 streams key and value units by TMA through one ring in the order the tensor
+// core takes them: K0, K1 V0, K2 V1, ...  Warp 1 issues Q K^T, warp 10 P V.  Warps 2-9 do the softmax, two threads to a row (64 scores each).
 // Tensor memory holds O [D columns], S [128] and Q [D/2, the A operand of Q K^T];
 // P goes through shared memory.  PV of tile t-1 sits between Q K^T of t and of t+1
 // on the tensor pipe: S(t) is read out during it, and one S buffer is enough.
@@ -41,6 +40,7 @@ namespace {
 constexpr int kKeyTile = 128;
 constexpr float kMoveMax = 8.f;
 constexpr int kPrefixThreads = 384;
+constexpr int kIds = 128;  // parts that are looked up at once (a multiple of a tile's)
 
 template <int D>
 struct Px {
@@ -61,8 +61,9 @@ struct Px {
   static constexpr int POFF = NU * UNIT;
   static constexpr int XOFF = POFF + PT;                    // exchanged values [2][2][128]
   static constexpr int GOFF = XOFF + 2 * 2 * 128 * 4;       // groups: first slot, pieces before, key tiles, table row
-  static constexpr int BOFF = GOFF + 4 * (TV_MAX_PAGED_SEQ + 4) * 4;
-  static constexpr int NBAR = 2 * NU + 5 + 4 + 2;
+  static constexpr int IOFF = GOFF + 4 * (TV_MAX_PAGED_SEQ + 4) * 4;  // rows of the parts [2][kIds]
+  static constexpr int BOFF = IOFF + 2 * kIds * 4;
+  static constexpr int NBAR = 2 * NU + 5 + 4 + 2 + 4;
   static constexpr int LOFF = (BOFF + NBAR * 8 + 15) / 16 * 16;
   static constexpr int SMEM = LOFF + 64;
   static_assert(SMEM <= 232448, "shared memory");
@@ -112,7 +113,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
   const uint32_t sb = smem_u32(smem_raw), ring = sb, pbuf = sb + C::POFF;
   float* xmax = reinterpret_cast<float*>(smem_raw + C::XOFF);
   const uint32_t UFULL0 = sb + C::BOFF, UEMPTY0 = UFULL0 + 8u * C::NU, SFULL = UEMPTY0 + 8u * C::NU, SFREE = SFULL + 8u,
-                 PFULL = SFULL + 16u, ODONE = SFULL + 24u, QREADY = SFULL + 32u, XBAR0 = SFULL + 40u, DRAIN = XBAR0 + 32u;
+                 PFULL = SFULL + 16u, ODONE = SFULL + 24u, QREADY = SFULL + 32u, XBAR0 = SFULL + 40u, DRAIN = XBAR0 + 32u, IDFULL0 = DRAIN + 16u, IDEMPTY0 = IDFULL0 + 16u;
+  volatile int* ids = reinterpret_cast<volatile int*>(smem_raw + C::IOFF);
   struct Local {
     uint32_t tmem;
     int abort_flag, most;
@@ -141,6 +143,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
     for (int i = 0; i < 4; i++) mbar_init(XBAR0 + 8u * i, 2);
     mbar_init(DRAIN, 1);
     mbar_init(DRAIN + 8u, 1);
+    for (int i = 0; i < 4; i++) mbar_init(IDFULL0 + 8u * i, 1);
     lo.abort_flag = 0;
     lo.best = ~0ull;
     lo.most = 0;
@@ -216,69 +219,82 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
     if (lane == 0) mbar_arrive(bar);
   };
 
-  if (warp == 0) {
-    // ---------------- TMA producer ----------------
-    const int R = p.R, parts = kKeyTile / R, rows = 1 << p.b.shift, per_page = rows / R;  // boxes of R rows
-    uint32_t it = 0;
+  const int parts = kKeyTile / p.R;  // boxes' worth of rows in a tile
+  if (warp == 11) {
+    // ---------------- page lookups: where the prefix's rows lie, kIds parts at a time ----------------
+    const int rows = 1 << p.b.shift, per_page = rows / p.R;
+    uint32_t c = 0;  // chunks
     bool ok = true;
     for (int x = blockIdx.x; ok && x < total; x += gridDim.x) {
       const PrefixItem I = prefix_item(p, gr, S, x);
-      const int n = I.k1 - I.k0, s = gr.src[I.g], end = p.shared[I.g] / R;
-      // part i of the prefix: its row in the pools; behind it, and for entries that name no page, a row behind the pools (zeros)
-      auto part = [&](int i) -> int {
-        if (i >= min(end, I.k1 * parts)) return p.all_rows;
-        const int page = page_at(p.b, s, i / per_page);
-        return page < 0 ? p.all_rows : (page * p.Hkv + I.h) * rows + (i % per_page) * R;
-      };
-      // keys run a tile ahead of values: 32 parts of each, and the next 32
-      const int i0 = I.k0 * parts;
-      int kb = part(i0 + lane), kn = part(i0 + 32 + lane), vb = kb, vn = kn;
+      const int s = gr.src[I.g], end = min(p.shared[I.g] / p.R, I.k1 * parts);
+      for (int i0 = I.k0 * parts; ok && i0 < I.k1 * parts; i0 += kIds, c++) {
+        ok = wait_warp(IDEMPTY0 + 8u * (c & 1), ((c >> 1) & 1) ^ 1, abort_flag, kWaitCycles);
+        if (!ok) break;
+#pragma unroll
+        for (int j = lane; j < kIds; j += 32) {
+          // behind the prefix, and for entries that name no page, a row behind the pools (zeros)
+          const int i = i0 + j, page = i < end ? page_at(p.b, s, i / per_page) : -1;
+          ids[(c & 1) * kIds + j] = page < 0 ? p.all_rows : (page * p.Hkv + I.h) * rows + (i % per_page) * p.R;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(IDFULL0 + 8u * (c & 1));
+      }
+    }
+    if (!ok && lane == 0) set_status(p.b.status, TV_ERR_TIMEOUT);
+  } else if (warp == 0 && lane == 0) {
+    // ---------------- TMA producer, one thread (with a warp's votes and shuffles a unit took 760 cycles,
+    // and a tile 3,800) ----------------
+    const bool kwhole = p.RK == kKeyTile, vwhole = p.RV == C::VROWS;  // a unit is one box, else a box a part and 64 columns
+    uint32_t it = 0, chunks = 0;  // units; chunks of the items before
+    bool ok = true;
+    for (int x = blockIdx.x; ok && x < total; x += gridDim.x) {
+      const PrefixItem I = prefix_item(p, gr, S, x);
+      const int n = I.k1 - I.k0;
       for (int e = 0; e < 2 * n && ok; e++) {
         // load order K0, K1 V0, K2 V1, ..., V(n-1)
         const bool is_k = e == 0 || ((e & 1) && e != 2 * n - 1);
         const int k = e == 0 ? 0 : is_k ? (e + 1) / 2 : (e == 2 * n - 1 ? n - 1 : (e - 2) / 2);
-        const int at = k * parts % 32;
-        if (at == 0 && k > 0) {
-          if (is_k) {
-            kb = kn;
-            kn = part(i0 + k * parts + 32 + lane);
-          } else {
-            vb = vn;
-            vn = part(i0 + k * parts + 32 + lane);
-          }
-        }
-        const int row = is_k ? kb : vb;
+        const uint32_t c = chunks + static_cast<uint32_t>(k * parts / kIds);
+        if (is_k && k * parts % kIds == 0) ok = wait_role(IDFULL0 + 8u * (c & 1), (c >> 1) & 1, abort_flag, kWaitCycles);
+        const volatile int* id = ids + (c & 1) * kIds + k * parts % kIds;
 #pragma unroll
         for (int u = 0; u < C::UPT; u++, it++) {
           const uint32_t slot = it % C::NU, full = UFULL0 + 8u * slot, dst = ring + slot * C::UNIT;
-          ok = ok && wait_warp(UEMPTY0 + 8u * slot, ((it / C::NU) & 1) ^ 1, abort_flag, kWaitCycles);
+          ok = ok && wait_role(UEMPTY0 + 8u * slot, ((it / C::NU) & 1) ^ 1, abort_flag, kWaitCycles);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(full, C::UNIT);
-          __syncwarp();
-          // one thread issues (a copy takes its operands from uniform registers: lanes of a
-          // warp that issue different ones take turns, at twice the time a tile)
+          mbar_arrive_expect_tx(full, C::UNIT);
           if (is_k) {
-            for (int pt = 0; pt < parts; pt++) {
-              const int from = __shfl_sync(0xffffffffu, row, at + pt);
-              if (lane == 0)
+            if (kwhole) {
+              tma_load_3d(dst, &p.tmK, full, 0, id[0], u * C::KBU);
+            } else {
+#pragma unroll 2
+              for (int pt = 0; pt < parts; pt++) {
+                const int from = id[pt];
 #pragma unroll
                 for (int ch = 0; ch < C::KBU; ch++)
-                  tma_load_2d(dst + ch * C::KBOX + pt * R * 128, &p.tmK, full, (u * C::KBU + ch) * 64, from);
+                  tma_load_3d(dst + ch * C::KBOX + pt * p.R * 128, &p.tmK, full, 0, from, u * C::KBU + ch);
+              }
             }
           } else {
-            const int up = C::VROWS / R;
-            for (int pt = 0; pt < up; pt++) {
-              const int from = __shfl_sync(0xffffffffu, row, at + u * up + pt);
-              if (lane == 0)
+            const int up = parts / C::UPT;
+            if (vwhole) {
+              tma_load_3d(dst, &p.tmV, full, 0, id[u * up], 0);
+            } else {
+#pragma unroll 2
+              for (int pt = 0; pt < up; pt++) {
+                const int from = id[u * up + pt];
 #pragma unroll
-                for (int ch = 0; ch < C::VB; ch++) tma_load_2d(dst + ch * C::VBOX + pt * R * 128, &p.tmV, full, ch * 64, from);
+                for (int ch = 0; ch < C::VB; ch++) tma_load_3d(dst + ch * C::VBOX + pt * p.R * 128, &p.tmV, full, 0, from, ch);
+              }
             }
           }
-          __syncwarp();
         }
+        if (!is_k && ((k + 1) * parts % kIds == 0 || k + 1 == n)) mbar_arrive(IDEMPTY0 + 8u * (c & 1));  // the chunk's last use
       }
+      chunks += static_cast<uint32_t>((n * parts + kIds - 1) / kIds);
     }
-    if (!ok && lane == 0) set_status(p.b.status, TV_ERR_TIMEOUT);
+    if (!ok) set_status(p.b.status, TV_ERR_TIMEOUT);
     // every issued copy lands before shared memory is released
     for (uint32_t i = it > C::NU ? it - C::NU : 0; i < it; i++) mbar_wait(UFULL0 + 8u * (i % C::NU), (i / C::NU) & 1, kWaitCycles);
   } else if (warp == 1 || warp == 10) {
@@ -334,7 +350,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
     if (elect_one_sync()) tc_commit(drain);
     __syncwarp();
     mbar_wait(drain, 0, kWaitCycles);
-  } else if (warp < 10) {
+  } else if (warp >= 2 && warp < 10) {
     // ---------------- softmax, a row's scores (and columns of O) to two threads ----------------
     const int hf = (warp - 2) >> 2, quad = warp & 3, lrow = quad * 32 + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
@@ -531,6 +547,21 @@ bool launch(const PagedPrefixParams& p, cudaStream_t st) {
 }
 
 }  // namespace
+
+template <int D>
+static void boxes(int page, PagedPrefixParams& p, int& k_cols, int& v_cols) {
+  using C = Px<D>;
+  p.R = page < 64 ? page : 64;
+  p.RK = page < kKeyTile ? p.R : kKeyTile;
+  p.RV = page < C::VROWS ? p.R : C::VROWS;
+  k_cols = p.RK == kKeyTile ? C::KBU : 1;
+  v_cols = p.RV == C::VROWS ? C::VB : 1;
+}
+void paged_prefix_boxes(int D, int page, PagedPrefixParams& p, int& k_cols, int& v_cols) {
+  if (D == 64) boxes<64>(page, p, k_cols, v_cols);
+  else if (D == 128) boxes<128>(page, p, k_cols, v_cols);
+  else boxes<256>(page, p, k_cols, v_cols);
+}
 
 int paged_prefix_slots(const tv_paged_layer* l, const tv_paged* b, int n_group) {
   const int64_t G = l->Hq / l->Hkv, items = l->Hkv * ((b->n_seq * G + 127) / 128 + n_group);

@@ -8,14 +8,15 @@
 namespace tv {
 
 struct PagedPrefixParams {
-  CUtensorMap tmK, tmV;  // pools as [rows][D], boxes of R rows, 64 columns
+  CUtensorMap tmK, tmV;  // pools as [D / 64][rows][64], boxes of RK and RV rows, of a unit's columns where they are a whole unit's rows, else of 64
   PagedSeqs b;
   const int32_t* group_off;  // [n_group + 1]
   const int32_t* shared;     // [n_group]
   const __nv_bfloat16* q;
   float* rec;       // [slots][128][D + 4]: O, m and l of a piece's rows
   int4* info;       // [n_seq], for the join: the group's first piece, row tiles, pieces along the keys (0: nothing shared), place in it
-  int n_group, slots, Hq, Hkv, G, R;
+  int n_group, slots, Hq, Hkv, G;
+  int R, RK, RV;  // rows of a part: a page's, up to 64; of a box of keys and of values
   int all_rows;  // of a pool
   float c;       // scale * log2(e)
 };
@@ -69,6 +70,8 @@ struct GroupCheck {
   }
 };
 
+// Rows and 64-column blocks of the boxes for pages of `page` rows.
+void paged_prefix_boxes(int D, int page, PagedPrefixParams& p, int& k_cols, int& v_cols);
 int paged_prefix_slots(const tv_paged_layer* l, const tv_paged* b, int n_group);
 bool paged_prefix_launch(const PagedPrefixParams& p, int D, cudaStream_t st);
 

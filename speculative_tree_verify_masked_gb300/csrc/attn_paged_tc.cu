@@ -783,16 +783,14 @@ __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// A pool as a tensor of rows, in boxes of `rows` rows and 64 columns, or of whole rows.
-static bool encode_pool_map(CUtensorMap* m, void* base, int D, int64_t all, int rows, bool whole) {
+// A pool as a tensor of rows cut into blocks of 64 columns, in boxes of `rows` rows and `cols` blocks.
+static bool encode_pool_map(CUtensorMap* m, void* base, int D, int64_t all, int rows, int cols) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t d = static_cast<cuuint64_t>(D), a = static_cast<cuuint64_t>(all);
-  const cuuint64_t dims2[2] = {d, a}, dims3[3] = {64, a, d / 64}, strides[2] = {d * 2, 128};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(D / 64)}, estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, whole ? 3 : 2, base, whole ? dims3 : dims2, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t d = static_cast<cuuint64_t>(D), dims[3] = {64, static_cast<cuuint64_t>(all), d / 64}, strides[2] = {d * 2, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(cols)}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Query heads of an item: eight, a tile's columns, or sixteen, two tiles that share the
@@ -834,7 +832,7 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
   const tv_paged_layer* l = a.layer;
   p.R = l->page < C::ROWS ? l->page : C::ROWS;
   const int64_t all = static_cast<int64_t>(l->n_pages) * l->Hkv * l->page;
-  if (!encode_pool_map(&p.tmK, l->K, D, all, p.R, true) || !encode_pool_map(&p.tmV, l->V, D, all, p.R, true)) return TV_ERR_CUDA;
+  if (!encode_pool_map(&p.tmK, l->K, D, all, p.R, D / 64) || !encode_pool_map(&p.tmV, l->V, D, all, p.R, D / 64)) return TV_ERR_CUDA;
   static std::atomic<uint64_t> set{0};
   if (!allow_smem(attn_paged_tc_kernel<D, NB>, C::SMEM, set)) return TV_ERR_CUDA;
   const int grid = num_sms();
@@ -842,8 +840,9 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
   if (a.groups) {
     PagedPrefixParams x;
     memset(&x, 0, sizeof(x));
-    x.R = l->page < 64 ? l->page : 64;
-    if (!encode_pool_map(&x.tmK, l->K, D, all, x.R, false) || !encode_pool_map(&x.tmV, l->V, D, all, x.R, false)) return TV_ERR_CUDA;
+    int k_cols, v_cols;
+    paged_prefix_boxes(D, l->page, x, k_cols, v_cols);
+    if (!encode_pool_map(&x.tmK, l->K, D, all, x.RK, k_cols) || !encode_pool_map(&x.tmV, l->V, D, all, x.RV, v_cols)) return TV_ERR_CUDA;
     x.b = p.v.b;
     x.group_off = a.groups->group_off;
     x.shared = a.groups->shared;
