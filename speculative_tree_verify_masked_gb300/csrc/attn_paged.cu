@@ -4,9 +4,10 @@
 //   out[s,h] = sum_t softmax_t(scale q[s,h] . K[t]) V[t], t = 0 .. len[s] or the
 //   rows of the listed pages among them.
 //
-// fp32: a CTA owns a (slot, query head); its eight warps take every eighth run
-// of four rows, a row's D values over the 32 lanes, and keep a running maximum and
-// sum each, which are joined at the end.  Bound by the walk over the rows of the
+// fp32: a CTA owns a (slot, query head); its sixteen warps take every sixteenth run
+// of eight rows (four of 256 columns), a row's D values over the 32 lanes, all loads of a run
+// in flight, and keep a running maximum and sum each, which are joined at the end.  A
+// warp looks up the pages of 32 runs at once.  Bound by the walk over the rows of the
 // longest slot (sized for the small model of the tests).
 #include "attn_paged.cuh"
 
@@ -23,17 +24,16 @@ struct PagedCudaParams {
   float c;  // scale * log2(e)
 };
 
+constexpr int kCudaWarps = 16;
+
 template <int D>
-__global__ void __launch_bounds__(256) attn_paged_cuda_kernel(const __grid_constant__ PagedCudaParams p) {
-  constexpr int CPL = D / 32, R = 4;  // values a lane, rows of a run (never across pages: R divides them)
-  __shared__ float acc_s[8][D], m_s[8], l_s[8];
+__global__ void __launch_bounds__(32 * kCudaWarps, 1) attn_paged_cuda_kernel(const __grid_constant__ PagedCudaParams p) {
+  constexpr int CPL = D / 32, R = D == 256 ? 4 : 8;  // values a lane, rows of a run (never across pages: R divides them)
+  __shared__ float acc_s[kCudaWarps][D], m_s[kCudaWarps], l_s[kCudaWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  if (status_bad(p.v.b.status)) return;
+  const bool bad = status_bad(p.v.b.status);
   const int h = blockIdx.x, s = blockIdx.y, g = h / p.G;
-  const int L = paged_len(p.v.b, s);
-  if (L < 0) return;
-  const int n = p.v.pages(s, g, L) << p.v.b.shift, rows = 1 << p.v.b.shift;
   const size_t row0 = (static_cast<size_t>(s) * p.Hq + h) * D;
   float q[CPL], acc[CPL], m = -INFINITY, l = 0.f;
   bool met = false;  // a row that the slot sees
@@ -42,15 +42,29 @@ __global__ void __launch_bounds__(256) attn_paged_cuda_kernel(const __grid_const
     q[c] = p.q[row0 + c * 32 + lane];
     acc[c] = 0.f;
   }
-  for (int i = warp * R; i < n; i += 8 * R) {
-    const int col = p.v.column(s, g, i >> p.v.b.shift), r = i & (rows - 1);
-    if (col < 0) continue;
-    const int live = min(R, L + 1 - (col * rows + r));  // (col < cols: no overflow)
-    if (live <= 0) continue;
-    const int page = page_at(p.v.b, s, col);
-    if (page < 0) continue;
+  const int L = paged_len(p.v.b, s);
+  if (bad || L < 0) return;
+  const int shift = p.v.b.shift, rows = 1 << shift;
+  const int n = p.v.pages(s, g, L) << shift;
+  int64_t row = -1;  // of a run of this warp's next 32, a lane each: its first row in the pools, -1: none
+  int seen = 0;      // and the rows of it that are seen
+  for (int i = warp * R, x = 0; i < n; i += kCudaWarps * R, x = (x + 1) & 31) {
+    if (x == 0) {
+      const int j = i + lane * kCudaWarps * R;
+      row = -1;
+      seen = 0;
+      if (j < n) {
+        const int col = p.v.column(s, g, j >> shift), r = j & (rows - 1);
+        seen = col < 0 ? 0 : min(R, L + 1 - (col * rows + r));  // (col < cols: no overflow)
+        const int page = seen > 0 ? page_at(p.v.b, s, col) : -1;
+        if (page >= 0) row = (static_cast<int64_t>(page) * p.v.Hkv + g) * rows + r;
+      }
+    }
+    const int64_t first = __shfl_sync(0xffffffffu, row, x);
+    const int live = __shfl_sync(0xffffffffu, seen, x);
+    if (first < 0) continue;
     met = true;
-    const size_t base = ((static_cast<size_t>(page) * p.v.Hkv + g) * rows + r) * D + lane;
+    const size_t base = static_cast<size_t>(first) * D + lane;
     float k[R][CPL], v[R][CPL], sc[R];
 #pragma unroll
     for (int j = 0; j < R; j++) {
@@ -102,11 +116,11 @@ __global__ void __launch_bounds__(256) attn_paged_cuda_kernel(const __grid_const
   if (threadIdx.x >= D) return;
   float mn = -INFINITY, lt = 0.f, o = 0.f;
 #pragma unroll
-  for (int w = 0; w < 8; w++) mn = fmaxf(mn, m_s[w]);
+  for (int w = 0; w < kCudaWarps; w++) mn = fmaxf(mn, m_s[w]);
 #pragma unroll
-  for (int w = 0; w < 8; w++) {
-    const float f = exp2f(__fsub_rn(m_s[w], mn == -INFINITY ? 0.f : mn));
+  for (int w = 0; w < kCudaWarps; w++) {
     if (l_s[w] == 0.f) continue;
+    const float f = exp2f(__fsub_rn(m_s[w], mn == -INFINITY ? 0.f : mn));
     lt = __fmaf_rn(f, l_s[w], lt);
     o = __fmaf_rn(f, acc_s[w][threadIdx.x], o);
   }
@@ -129,9 +143,9 @@ static tv_status launch_cuda(const PagedAttnCall& a, cudaStream_t st) {
   p.c = a.scale * 1.4426950408889634f;
   const dim3 g(l->Hq, a.batch->n_seq);
   switch (l->D) {
-    case 64: launch_k(true, attn_paged_cuda_kernel<64>, g, dim3(256), 0, st, p); break;
-    case 128: launch_k(true, attn_paged_cuda_kernel<128>, g, dim3(256), 0, st, p); break;
-    default: launch_k(true, attn_paged_cuda_kernel<256>, g, dim3(256), 0, st, p);
+    case 64: launch_k(true, attn_paged_cuda_kernel<64>, g, dim3(32 * kCudaWarps), 0, st, p); break;
+    case 128: launch_k(true, attn_paged_cuda_kernel<128>, g, dim3(32 * kCudaWarps), 0, st, p); break;
+    default: launch_k(true, attn_paged_cuda_kernel<256>, g, dim3(32 * kCudaWarps), 0, st, p);
   }
   return launch_status();
 }

@@ -158,9 +158,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
   pdl_trigger();
   const int NG = p.n_group;
   int* count = reinterpret_cast<int*>(smem_raw);  // (the ring is not in use yet)
-  GroupCheck<kPrefixThreads> check{gr.off, count, count + TV_MAX_PAGED_SEQ, gr.src, gr.nk};
+  GroupCheck<kPrefixThreads> check{gr.off, count, count + TV_MAX_PAGED_SEQ, gr.src, gr.nk,
+                                   reinterpret_cast<unsigned long long*>(count + 2 * TV_MAX_PAGED_SEQ)};
   int code = sb & 1023u ? TV_ERR_CUDA : 0;
-  code = check.run(p.b, p.group_off, p.shared, NG, code);
+  code = check.run(p.b, p.group_off, p.shared, NG, kv_row_bytes(p.Hkv, D), code);
   if (code || __syncthreads_or(status_bad(p.b.status))) {
     if (code) set_status(p.b.status, code);
     tc_fence_before();
@@ -179,11 +180,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
   // the CTA with most pieces, and about four for each to start, to end and to be joined
   if (most > 0) {
     const int S = max(ceil_div(most, tid + 1), 2);
-    int64_t pieces = 0;
+    float pieces = 0.f;  // (whole numbers, exact where they count: the workspace holds fewer than 2^24)
     for (int g = 0; g < NG; g++)
-      if (gr.nk[g] > 0) pieces += static_cast<int64_t>(p.Hkv) * ceil_div((gr.off[g + 1] - gr.off[g]) * p.G, 128) * ceil_div(gr.nk[g], S);
-    const int64_t cost = (pieces + gridDim.x - 1) / gridDim.x * (min(S, most) + 4);
-    if (pieces <= p.slots || tid == 0) atomicMin(&lo.best, static_cast<unsigned long long>(cost) << 10 | tid);
+      if (gr.nk[g] > 0) pieces += static_cast<float>(p.Hkv * ceil_div((gr.off[g + 1] - gr.off[g]) * p.G, 128)) * static_cast<float>(ceil_div(gr.nk[g], S));
+    const float cost = ceilf(__fdividef(pieces, static_cast<float>(gridDim.x))) * static_cast<float>(min(S, most) + 4);
+    if (pieces <= static_cast<float>(p.slots) || tid == 0) atomicMin(&lo.best, static_cast<unsigned long long>(__float_as_uint(cost)) << 10 | tid);
   }
   __syncthreads();
   const int S = most > 0 ? max(ceil_div(most, static_cast<int>(lo.best & 1023u) + 1), 2) : 2;
@@ -375,13 +376,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
       if (hf < C::QH) {
         const int cl = lane & 7;  // 16 bytes of a row's 128
         uint4 v[C::QR][8];
+        const __nv_bfloat16* q0 = p.q + (static_cast<size_t>(gr.off[I.g]) * p.Hq + I.h * p.G) * D + hf * (D / 2) + cl * 8;
+        int row = I.r * 128 + quad * 32 + (lane >> 3), m = row / p.G, head = row - m * p.G;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          const int row = I.r * 128 + quad * 32 + i * 4 + (lane >> 3);
-          const int m = row < I.n ? row / p.G : 0, head = row < I.n ? row % p.G : 0;
-          const __nv_bfloat16* q = p.q + ((static_cast<size_t>(gr.off[I.g]) + m) * p.Hq + I.h * p.G + head) * D + hf * (D / 2) + cl * 8;
+          const __nv_bfloat16* q = q0 + (row < I.n ? (static_cast<size_t>(m) * p.Hq + head) * D : 0);
 #pragma unroll
           for (int r = 0; r < C::QR; r++) v[r][i] = ldg16(q + r * 64);
+          row += 4;
+          for (head += 4; head >= p.G; head -= p.G) m++;
         }
 #pragma unroll
         for (int r = 0; r < C::QR; r++) {

@@ -20,12 +20,22 @@ struct PagedPrefixParams {
   int all_rows;  // of a pool
   float c;       // scale * log2(e)
 };
+// What sharing has to save to pay for its launch, its start and the longer join: so many bytes of keys
+// and values that members would read again (from L2, mostly).  24 + 4 heads of 256, us a call shared
+// and slot by slot: 8 members of 16,384 rows (470 MB saved) 33.4 and 43.9, 4 (201 MB) 30.3 and 28.4; of 4,096 rows
+// 16 members (252 MB) 26.2 and 28.9, 8 (117 MB) 24.8 and 21.0; 2 of 65,536 (268 MB) 67.3 and 67.6.  16 + 2
+// heads of 128: 4 of 65,536 (201 MB) 39.9 and 38.8, 8 67.6 and 41.3.
+constexpr int64_t kSharedBytes = 200 << 20;
+// Bytes of a row's keys and values in bf16.
+__host__ __device__ inline int64_t kv_row_bytes(int Hkv, int D) { return static_cast<int64_t>(Hkv) * D * 4; }
+
 // The groups of a call, checked by a whole CTA of THREADS: first slots [n + 1] into off; active members,
 // their least length and first one into count, least and src [n]; into rows [n] how many
-// rows a group shares (0 where fewer than two members are active).  All in shared memory.
+// rows a group shares (0 where that would not pay).  All in shared memory.
 template <int THREADS>
 struct GroupCheck {
   int *off, *count, *least, *src, *rows;
+  unsigned long long* again;  // rows that members would read again
 
   // The group that slot s belongs to: the last that starts at or before it.
   __device__ __forceinline__ int of(int n, int s) const {
@@ -38,8 +48,9 @@ struct GroupCheck {
     return a;
   }
   // 0, or what is wrong (every thread gets it).
-  __device__ int run(const PagedSeqs& b, const int32_t* group_off, const int32_t* shared, int n, int code) {
+  __device__ int run(const PagedSeqs& b, const int32_t* group_off, const int32_t* shared, int n, int64_t row_bytes, int code) {
     const int tid = threadIdx.x;
+    if (tid == 0) *again = 0;
     const int L0 = tid < b.n_seq ? paged_len(b, tid) : -1;  // (these loads are on their way together)
     for (int g = tid; g <= n; g += THREADS) {
       const int o = group_off[g];
@@ -65,8 +76,14 @@ struct GroupCheck {
       const int x = rows[g];
       if (x < 0 || (x & ((1 << b.shift) - 1)) || (count[g] > 0 && x > least[g])) code = TV_ERR_ROWS;
       if (count[g] < 2) rows[g] = 0;
+      else if (!code) atomicAdd(again, static_cast<unsigned long long>(count[g] - 1) * rows[g]);
     }
-    return __syncthreads_or(code) ? TV_ERR_ROWS : 0;
+    if (__syncthreads_or(code)) return TV_ERR_ROWS;
+    if (static_cast<int64_t>(*again) * row_bytes < kSharedBytes) {
+      for (int g = tid; g < n; g += THREADS) rows[g] = 0;
+      __syncthreads();
+    }
+    return 0;
   }
 };
 

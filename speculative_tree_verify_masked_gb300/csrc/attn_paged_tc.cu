@@ -194,16 +194,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   }
   __syncthreads();
   if (lo.skip) return;
-  if (p.start) {  // (every CTA writes the same)
+  if (p.group_off) {  // (every CTA writes the same)
     int* at = reinterpret_cast<int*>(smem_raw);  // (the rings are not in use yet)
     constexpr int N = TV_MAX_PAGED_SEQ + 4;
-    GroupCheck<kThreads> check{at, at + N, at + 2 * N, at + 3 * N, at + 4 * N};
-    const int code = check.run(p.v.b, p.group_off, p.shared, p.n_group, 0);
+    GroupCheck<kThreads> check{at, at + N, at + 2 * N, at + 3 * N, at + 4 * N, reinterpret_cast<unsigned long long*>(at + 5 * N)};
+    const int code = check.run(p.v.b, p.group_off, p.shared, p.n_group, kv_row_bytes(p.v.Hkv, D), 0);
     if (code) {
       set_status(p.v.b.status, code);
       return;
     }
-    for (int s = threadIdx.x; s < p.v.b.n_seq; s += kThreads) p.start[s] = check.rows[check.of(p.n_group, s)];
+    for (int s = threadIdx.x; p.start && s < p.v.b.n_seq; s += kThreads) p.start[s] = check.rows[check.of(p.n_group, s)];
     fence_proxy_async_smem();
     __syncthreads();
   }
@@ -836,8 +836,9 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
   static std::atomic<uint64_t> set{0};
   if (!allow_smem(attn_paged_tc_kernel<D, NB>, C::SMEM, set)) return TV_ERR_CUDA;
   const int grid = num_sms();
+  const bool may_share = p.start != nullptr;
   launch_k(true, attn_paged_tc_kernel<D, NB>, dim3(grid), dim3(kThreads), C::SMEM, st, p);
-  if (a.groups) {
+  if (may_share) {
     PagedPrefixParams x;
     memset(&x, 0, sizeof(x));
     int k_cols, v_cols;
@@ -858,7 +859,7 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
     x.c = p.c;
     if (!paged_prefix_launch(x, D, st)) return TV_ERR_CUDA;
   }
-  if (a.groups) {
+  if (may_share) {
     const int64_t warps = static_cast<int64_t>(p.units) * p.G * (D > 128 ? D / 128 : 1);
     const int join = static_cast<int>(warps + 7 < static_cast<int64_t>(16) * grid ? (warps + 7) / 8 : 2 * grid);
     launch_k(true, attn_paged_join_kernel<D>, dim3(join), dim3(256), 0, st, p, grid);
@@ -882,14 +883,17 @@ tv_status paged_attn_tc_launch(const PagedAttnCall& a, cudaStream_t st) {
   p.cut = reinterpret_cast<int4*>(ws + x.cut);
   p.rec = reinterpret_cast<float*>(ws + x.rec);
   if (a.groups) {
+    p.group_off = a.groups->group_off;
+    p.shared = a.groups->shared;
+    p.n_group = a.groups->n_group;
+  }
+  // (where no lengths within the bound could save enough, the groups are only checked)
+  if (a.groups && (a.batch->n_seq - 1) * static_cast<int64_t>(a.batch->max_len) * kv_row_bytes(l->Hkv, l->D) >= kSharedBytes) {
     p.first = reinterpret_cast<int64_t*>(ws + x.first);
     p.rec_item = reinterpret_cast<float*>(ws + x.rec_item);
     p.rec_prefix = reinterpret_cast<const float*>(ws + x.rec_prefix);
     p.info = reinterpret_cast<const int4*>(ws + x.info);
     p.start = reinterpret_cast<int32_t*>(ws + x.start);
-    p.group_off = a.groups->group_off;
-    p.shared = a.groups->shared;
-    p.n_group = a.groups->n_group;
   }
   p.Hq = l->Hq;
   p.G = l->Hq / l->Hkv;

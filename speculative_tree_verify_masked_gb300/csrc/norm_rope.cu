@@ -89,36 +89,53 @@ struct Raw8<float> {
   __device__ __forceinline__ f2_t pair(int i) const { return f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])); }
 };
 
-// The slot that packed row `row` belongs to, with its offsets: two looks at 32
-// of them side by side for up to 1,024 slots.  (Offsets that fall are found by
-// the rows that meet them, and by no other: every row checks its own slot's.)
+// The slot that packed row `row` belongs to, where its rows start and the rows it holds
+// already: for up to 31 slots from one round of loads, a lane a slot; else by two looks
+// at 32 offsets side by side.  (Offsets that fall are found by the rows that meet them, and
+// by no other: every row checks its own slot's.)
 struct PagedRow {
-  int s, off, n;  // s -1: padding behind the last row, or offsets that are not allowed
+  int s, off, len;  // s -1: padding behind the last row, or what is not allowed
 };
 __device__ __forceinline__ PagedRow paged_row(const PagedSeqs& b, const int32_t* row_off, int n_total, int n_max, int row, int lane) {
-  int s = 0;
-  for (int step = b.n_seq > 32 ? 32 : 1;; step = 1) {
-    const int i = s + lane * step;
-    const unsigned m = __ballot_sync(0xffffffffu, i <= b.n_seq && row_off[i] <= row);
-    s += m ? (31 - __clz(static_cast<int>(m))) * step : 0;
-    if (step == 1) break;
-  }
-  // (the last of 32 looks may be followed by a boundary: n_seq = 32 k)
-  if (s < b.n_seq && row_off[s + 1] <= row) s++;
   PagedRow r{-1, 0, 0};
-  const int all = row_off[b.n_seq];
-  if (row_off[0] != 0 || all > n_total) {
-    if (lane == 0) set_status(b.status, TV_ERR_ROWS);
-    return r;
+  int s, start, end, all, zero, len;
+  if (b.n_seq < 32) {
+    const int o = row_off[min(lane, b.n_seq)], l = b.len[min(lane, b.n_seq - 1)];
+    const unsigned m = __ballot_sync(0xffffffffu, lane <= b.n_seq && o <= row);
+    s = m ? 31 - __clz(static_cast<int>(m)) : 0;
+    zero = __shfl_sync(0xffffffffu, o, 0);
+    all = __shfl_sync(0xffffffffu, o, b.n_seq);
+    start = __shfl_sync(0xffffffffu, o, s);
+    end = __shfl_sync(0xffffffffu, o, min(s + 1, b.n_seq));
+    len = __shfl_sync(0xffffffffu, l, min(s, b.n_seq - 1));
+  } else {
+    s = 0;
+    for (int step = 32;; step = 1) {
+      const int i = s + lane * step;
+      const unsigned m = __ballot_sync(0xffffffffu, i <= b.n_seq && row_off[i] <= row);
+      s += m ? (31 - __clz(static_cast<int>(m))) * step : 0;
+      if (step == 1) break;
+    }
+    // (the last of 32 looks may be followed by a boundary: n_seq = 32 k)
+    if (s < b.n_seq && row_off[s + 1] <= row) s++;
+    zero = row_off[0];
+    all = row_off[b.n_seq];
+    start = row_off[s];
+    end = row_off[min(s + 1, b.n_seq)];
+    len = b.len[min(s, b.n_seq - 1)];
   }
-  if (s >= b.n_seq) return r;  // padding
-  r.off = row_off[s];
-  r.n = row_off[s + 1] - r.off;
-  if (r.n < 0 || r.n > n_max || row < r.off || row >= r.off + r.n) {
-    if (lane == 0) set_status(b.status, TV_ERR_ROWS);
+  int code = 0;
+  if (zero != 0 || all > n_total) code = TV_ERR_ROWS;
+  else if (s >= b.n_seq) return r;  // padding
+  else if (end - start < 0 || end - start > n_max || row < start || row >= end || len == -1) code = TV_ERR_ROWS;
+  else if (len < -1 || len > b.max_len) code = TV_ERR_LEN;
+  if (code) {
+    if (lane == 0) set_status(b.status, code);
     return r;
   }
   r.s = s;
+  r.off = start;
+  r.len = len;
   return r;
 }
 
@@ -151,20 +168,16 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 5 : 4) norm_rope_kernel(
   int s, pos;
   if constexpr (PAGED) {
     if (bad) return;
-    int i = 0;
     s = row;
     if (p.form == 4) {
       const PagedRow r = paged_row(p.pg, p.pr.row_off, p.n_total, p.pr.n_max, row, lane);
       if (r.s < 0) return;
       s = r.s;
-      i = row - r.off;
+      pos = r.len + row - r.off;
+    } else {
+      pos = paged_len(p.pg, s);
+      if (pos < 0) return;
     }
-    const int len = paged_len(p.pg, s);
-    if (len < 0) {
-      if (p.form == 4 && lane == 0) set_status(p.pr.status, TV_ERR_ROWS);  // rows of an idle slot
-      return;
-    }
-    pos = len + i;
     if ((pos >> p.pg.shift) >= p.pg.cols) {
       if (lane == 0) set_status(p.pr.status, TV_ERR_CAPACITY);
       return;
