@@ -388,6 +388,9 @@ class PagedLayer:
         self.sound = _alike([K, V], K.shape, K.dtype)
         self.gpu = K.get_device()
         self.c = tv_paged_layer(_dtype_code(K.dtype), Hq, Hkv, D, page, n_pages, K.data_ptr(), V.data_ptr())
+        # what a call needs of them, at hand (a small call's time is the host's)
+        self.ref, self.dtype = ctypes.byref(self.c), K.dtype
+        self.Hkv, self.q_row, self.kv_row, self.D, self.heads = Hkv, Hq * D, Hkv * D, D, n_pages * Hkv
 
 
 class PagedBatch:
@@ -402,6 +405,7 @@ class PagedBatch:
         self.gpu = table.get_device()
         self.status = torch.zeros(4, dtype=torch.int32, device=table.device)
         self.c = tv_paged(self.n_seq, self.cols, max_len, table.data_ptr(), len_.data_ptr(), self.status.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
     def status_code(self) -> int:
         return int(self.status[0].item())
@@ -417,6 +421,7 @@ class PagedRows:
         self.n_max = max(rows) if n_max is None else n_max
         self.row_off = torch.tensor(off, dtype=torch.int32, device=device)
         self.c = tv_paged_rows(self.n_total, self.n_max, self.row_off.data_ptr())
+        self.ref, self.gpu = ctypes.byref(self.c), self.row_off.get_device()
 
     _offsets = staticmethod(Prompt._offsets)
     set_rows, counts = Prompt.set_rows, Prompt.counts
@@ -433,6 +438,7 @@ class PagedGroups:
         self.group_off = torch.tensor(off, dtype=torch.int32, device=device)
         self.shared = torch.tensor(list(shared), dtype=torch.int32, device=device)
         self.c = tv_paged_groups(self.n_group, self.group_off.data_ptr(), self.shared.data_ptr())
+        self.ref, self.gpu = ctypes.byref(self.c), self.group_off.get_device()
 
     def set_groups(self, sizes, shared, stream=None):
         """Other groups in the same buffers (as many), in the stream's order as Prompt.set_rows."""
@@ -737,99 +743,128 @@ def tv_gdn_prompt_front(layer: GdnFrontLayer, prompt: Prompt, x, a_raw, b_raw, q
 # ---------------------------------------------------------------------------
 # caches in pages
 # ---------------------------------------------------------------------------
-def _need_paged(where: str, layer, batch, rows=None, groups=None):
+def _need_paged(where: str, layer, batch, extra, here):
     """Raises where a paged call's descriptors are not memory of the current GPU
-    of the shapes they say, or are made for another number of slots."""
-    here = _current_gpu()
+    of the shapes they say, or its rows or groups are for another number of slots."""
     if not layer.sound or not batch.sound:
         raise ValueError(f"{where}: pools, table and lengths must be contiguous memory of one GPU, the pools alike, the others int32")
     if layer.gpu != here or batch.gpu != here:
         raise ValueError(f"{where}: the pools are on GPU {layer.gpu}, the batch is on {batch.gpu}, the current GPU is {here}")
-    for x in (rows, groups):
-        if x is not None and (x.n_seq != batch.n_seq or (x.row_off if x is rows else x.group_off).get_device() != here):
-            raise ValueError(f"{where}: rows or groups for {x.n_seq} slots, {batch.n_seq} in the batch, or of another GPU than {here}")
+    if extra is not None and (extra.n_seq != batch.n_seq or extra.gpu != here):
+        raise ValueError(f"{where}: rows or groups for {extra.n_seq} slots, {batch.n_seq} in the batch, or of another GPU than {here}")
+
+
+def _paged(where: str, layer, batch, extra, stream):
+    """What every paged call begins with: its descriptors checked; the current GPU and the stream."""
+    here = _current_gpu()
+    if not (layer.sound and batch.sound and layer.gpu == here and batch.gpu == here and
+            (extra is None or (extra.n_seq == batch.n_seq and extra.gpu == here))):
+        _need_paged(where, layer, batch, extra, here)
+    return here, torch._C._cuda_getCurrentRawStream(here) if stream is None else _stream(stream)
+
+
+def _fits(t, dtype, n, here):
+    """Whether a buffer is what the C side will take it for (None: not given); _need says what is not."""
+    return t is None or (t.dtype is dtype and t.get_device() == here and t.is_contiguous() and t.numel() >= n)
+
+
+def _space(ws, here) -> int:
+    """Bytes of a workspace, which must be contiguous memory of the current GPU."""
+    if ws is None:
+        return 0
+    return ws.nbytes if ws.get_device() == here and ws.is_contiguous() else _ws_bytes(ws)
 
 
 def _ref(x):
-    return None if x is None else ctypes.byref(x.c)
+    return None if x is None else x.ref
 
 
 def tv_paged_append(layer: PagedLayer, batch: PagedBatch, rows: PagedRows | None, q_norm, k_norm, eps, rot_dims, theta,
                     q_raw, k_raw, v, q, stream=None):
     """Head norms and rotation of a step's rows (rows None: one a slot) or of
     prompts' rows; queries to q, keys and values into the slots' pages."""
-    _need_paged("tv_paged_append", layer, batch, rows)
-    c, n = layer.c, batch.n_seq if rows is None else rows.n_total
-    dt = layer.K.dtype
-    _need("tv_paged_append", q_norm=(q_norm, torch.float32, c.D), k_norm=(k_norm, torch.float32, c.D),
-          q_raw=(q_raw, dt, n * c.Hq * c.D), k_raw=(k_raw, dt, n * c.Hkv * c.D), v=(v, dt, n * c.Hkv * c.D),
-          q=(q, dt, n * c.Hq * c.D))
-    _check(lib().tv_paged_append(ctypes.byref(c), ctypes.byref(batch.c), _ref(rows), _ptr(q_norm), _ptr(k_norm), eps,
-                                 rot_dims, theta, _ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(q), _stream(stream)),
-           "tv_paged_append")
+    here, st = _paged("tv_paged_append", layer, batch, rows, stream)
+    n, dt, f32 = batch.n_seq if rows is None else rows.n_total, layer.dtype, torch.float32
+    nq, nk = n * layer.q_row, n * layer.kv_row
+    if not (_fits(q_norm, f32, layer.D, here) and _fits(k_norm, f32, layer.D, here) and _fits(q_raw, dt, nq, here) and
+            _fits(k_raw, dt, nk, here) and _fits(v, dt, nk, here) and _fits(q, dt, nq, here)):
+        _need("tv_paged_append", q_norm=(q_norm, f32, layer.D), k_norm=(k_norm, f32, layer.D), q_raw=(q_raw, dt, nq),
+              k_raw=(k_raw, dt, nk), v=(v, dt, nk), q=(q, dt, nq))
+    code = lib().tv_paged_append(layer.ref, batch.ref, _ref(rows), _ptr(q_norm), _ptr(k_norm), eps, rot_dims, theta,
+                                 _ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(q), st)
+    if code:
+        _check(code, "tv_paged_append")
 
 
 def tv_paged_advance(batch: PagedBatch, rows: PagedRows | None = None, stream=None):
     """The batch's lengths past a step's rows, after its last layer."""
-    if not batch.sound or batch.gpu != _current_gpu() or (rows is not None and (
-            rows.n_seq != batch.n_seq or rows.row_off.get_device() != batch.gpu)):
-        raise ValueError("tv_paged_advance: the batch and its rows must be of the current GPU, for as many slots")
-    _check(lib().tv_paged_advance(ctypes.byref(batch.c), _ref(rows), _ptr(batch.len), _stream(stream)), "tv_paged_advance")
+    here, st = _paged("tv_paged_advance", batch, batch, rows, stream)
+    _check(lib().tv_paged_advance(batch.ref, _ref(rows), _ptr(batch.len), st), "tv_paged_advance")
 
 
 def tv_paged_attn_workspace_bytes(layer: PagedLayer, batch: PagedBatch, groups: PagedGroups | None = None) -> int:
-    return int(lib().tv_paged_attn_workspace_bytes(ctypes.byref(layer.c), ctypes.byref(batch.c), _ref(groups)))
+    return int(lib().tv_paged_attn_workspace_bytes(layer.ref, batch.ref, _ref(groups)))
 
 
 def tv_paged_attn(layer: PagedLayer, batch: PagedBatch, groups: PagedGroups | None, q, gate, out, scale, ws, stream=None):
     """Decode attention over pages; the prefixes that groups share are read once."""
-    _need_paged("tv_paged_attn", layer, batch, groups=groups)
-    c, dt = layer.c, layer.K.dtype
-    nq = batch.n_seq * c.Hq * c.D
-    _need("tv_paged_attn", q=(q, dt, nq), gate=(gate, dt, nq), out=(out, dt, nq))
-    _check(lib().tv_paged_attn(ctypes.byref(c), ctypes.byref(batch.c), _ref(groups), _ptr(q), _ptr(gate), _ptr(out), scale,
-                               _ptr(ws), _ws_bytes(ws), _stream(stream)), "tv_paged_attn")
+    here, st = _paged("tv_paged_attn", layer, batch, groups, stream)
+    dt, nq = layer.dtype, batch.n_seq * layer.q_row
+    if not (_fits(q, dt, nq, here) and _fits(gate, dt, nq, here) and _fits(out, dt, nq, here)):
+        _need("tv_paged_attn", q=(q, dt, nq), gate=(gate, dt, nq), out=(out, dt, nq))
+    code = lib().tv_paged_attn(layer.ref, batch.ref, _ref(groups), _ptr(q), _ptr(gate), _ptr(out), scale, _ptr(ws),
+                               _space(ws, here), st)
+    if code:
+        _check(code, "tv_paged_attn")
 
 
 def tv_paged_bounds(layer: PagedLayer, batch: PagedBatch, rows: PagedRows | None, code, exp, stream=None):
     """Bounds of the pages that a step's rows complete: code int8 [n_pages, Hkv, 2, D], exp int32 [n_pages, Hkv]."""
-    _need_paged("tv_paged_bounds", layer, batch, rows)
-    c = layer.c
-    heads = c.n_pages * c.Hkv
-    _need("tv_paged_bounds", code=(code, torch.int8, heads * 2 * c.D), exp=(exp, torch.int32, heads))
-    _check(lib().tv_paged_bounds(ctypes.byref(c), ctypes.byref(batch.c), _ref(rows), _ptr(code), _ptr(exp), _stream(stream)),
-           "tv_paged_bounds")
+    here, st = _paged("tv_paged_bounds", layer, batch, rows, stream)
+    nc = layer.heads * 2 * layer.D
+    if not (_fits(code, torch.int8, nc, here) and _fits(exp, torch.int32, layer.heads, here)):
+        _need("tv_paged_bounds", code=(code, torch.int8, nc), exp=(exp, torch.int32, layer.heads))
+    status = lib().tv_paged_bounds(layer.ref, batch.ref, _ref(rows), _ptr(code), _ptr(exp), st)
+    if status:
+        _check(status, "tv_paged_bounds")
 
 
 def tv_paged_select_workspace_bytes(layer: PagedLayer, batch: PagedBatch) -> int:
-    return int(lib().tv_paged_select_workspace_bytes(ctypes.byref(layer.c), ctypes.byref(batch.c)))
+    return int(lib().tv_paged_select_workspace_bytes(layer.ref, batch.ref))
 
 
-def tv_paged_select(layer: PagedLayer, batch: PagedBatch, code, exp, first: int, last: int, q, sel, count, ws, stream=None):
+def tv_paged_select(layer: PagedLayer, batch: PagedBatch, code, exp, first: int, last: int, q, sel, count, ws=None, stream=None):
     """The pages that each slot's queries look at: sel int32 [n_seq, Hkv, n_sel], count int32 [n_seq, Hkv]."""
-    _need_paged("tv_paged_select", layer, batch)
-    c, n = layer.c, batch.n_seq
-    n_sel, heads = sel.shape[-1], c.n_pages * c.Hkv
-    _need("tv_paged_select", code=(code, torch.int8, heads * 2 * c.D), exp=(exp, torch.int32, heads),
-          q=(q, layer.K.dtype, n * c.Hq * c.D), sel=(sel, torch.int32, n * c.Hkv * n_sel), count=(count, torch.int32, n * c.Hkv))
-    _check(lib().tv_paged_select(ctypes.byref(c), ctypes.byref(batch.c), _ptr(code), _ptr(exp), first, last, n_sel, _ptr(q),
-                                 _ptr(sel), _ptr(count), _ptr(ws), _ws_bytes(ws), _stream(stream)), "tv_paged_select")
+    here, st = _paged("tv_paged_select", layer, batch, None, stream)
+    n_sel, units, i32 = sel.shape[-1], batch.n_seq * layer.Hkv, torch.int32
+    nc, nq = layer.heads * 2 * layer.D, batch.n_seq * layer.q_row
+    if not (_fits(code, torch.int8, nc, here) and _fits(exp, i32, layer.heads, here) and _fits(q, layer.dtype, nq, here) and
+            _fits(sel, i32, units * n_sel, here) and _fits(count, i32, units, here)):
+        _need("tv_paged_select", code=(code, torch.int8, nc), exp=(exp, i32, layer.heads), q=(q, layer.dtype, nq),
+              sel=(sel, i32, units * n_sel), count=(count, i32, units))
+    status = lib().tv_paged_select(layer.ref, batch.ref, _ptr(code), _ptr(exp), first, last, n_sel, _ptr(q), _ptr(sel),
+                                   _ptr(count), _ptr(ws), _space(ws, here), st)
+    if status:
+        _check(status, "tv_paged_select")
 
 
 def tv_paged_attn_selected_workspace_bytes(layer: PagedLayer, batch: PagedBatch, n_sel: int) -> int:
-    return int(lib().tv_paged_attn_selected_workspace_bytes(ctypes.byref(layer.c), ctypes.byref(batch.c), n_sel))
+    return int(lib().tv_paged_attn_selected_workspace_bytes(layer.ref, batch.ref, n_sel))
 
 
 def tv_paged_attn_selected(layer: PagedLayer, batch: PagedBatch, sel, count, q, gate, out, scale, ws, stream=None):
     """Decode attention over the listed pages alone."""
-    _need_paged("tv_paged_attn_selected", layer, batch)
-    c, n, dt = layer.c, batch.n_seq, layer.K.dtype
-    n_sel, nq = sel.shape[-1], n * c.Hq * c.D
-    _need("tv_paged_attn_selected", sel=(sel, torch.int32, n * c.Hkv * n_sel), count=(count, torch.int32, n * c.Hkv),
-          q=(q, dt, nq), gate=(gate, dt, nq), out=(out, dt, nq))
-    _check(lib().tv_paged_attn_selected(ctypes.byref(c), ctypes.byref(batch.c), _ptr(sel), _ptr(count), n_sel, _ptr(q),
-                                        _ptr(gate), _ptr(out), scale, _ptr(ws), _ws_bytes(ws), _stream(stream)),
-           "tv_paged_attn_selected")
+    here, st = _paged("tv_paged_attn_selected", layer, batch, None, stream)
+    n_sel, units, dt, i32 = sel.shape[-1], batch.n_seq * layer.Hkv, layer.dtype, torch.int32
+    nq = batch.n_seq * layer.q_row
+    if not (_fits(sel, i32, units * n_sel, here) and _fits(count, i32, units, here) and _fits(q, dt, nq, here) and
+            _fits(gate, dt, nq, here) and _fits(out, dt, nq, here)):
+        _need("tv_paged_attn_selected", sel=(sel, i32, units * n_sel), count=(count, i32, units), q=(q, dt, nq),
+              gate=(gate, dt, nq), out=(out, dt, nq))
+    code = lib().tv_paged_attn_selected(layer.ref, batch.ref, _ptr(sel), _ptr(count), n_sel, _ptr(q), _ptr(gate), _ptr(out),
+                                        scale, _ptr(ws), _space(ws, here), st)
+    if code:
+        _check(code, "tv_paged_attn_selected")
 
 
 # ---------------------------------------------------------------------------

@@ -10,11 +10,13 @@
 // 2^22), and so is its product with 2^e: no rounding decides between two pages.
 // (2^f is the same for all pages of a choice and is left out.)
 //
-// Scores run on the integer tensor tiles (16 x 8 x 32): the group's queries as
-// [u-, u+] against the codes of eight pages, read once from memory in 16-byte
-// pieces.  (The order of the 2 D products is free, so a lane's piece is used as it
-// lies.)  Bound by the reads of the codes, a 128th of the keys and values at pages
-// of 64 rows, and for few slots by latency.
+// Scores run on 16 x 8 x 16 tensor-core tiles, sixteen pages by eight query heads,
+// with codes and queries as fp16 and sums in fp32, which hold these whole numbers exactly
+// (the integer tiles of this GPU take 190 cycles a product of half the size: 12,000
+// cycles a CTA against 4,500).  Codes are read once from memory in 16-byte pieces and widened in
+// registers; the order of the 2 D products is free, so a lane's piece is used as it
+// lies.  Bound by latency for few slots, by the reads of the codes (a 128th of the keys and
+// values at pages of 64 rows) for many.
 //
 // The choice is a radix selection of the n-th highest key by digits of eight bits,
 // from the highest bit in which the keys differ down, until a digit leaves no
@@ -22,6 +24,7 @@
 // ones.  A cluster of CTAs shares a slot's KV head: each scores its part of the pages
 // into the first one's shared memory, which then chooses.
 #include <climits>
+#include <cuda_fp16.h>
 
 #include "paged.cuh"
 #include "prompt.cuh"
@@ -158,11 +161,20 @@ struct SelectParams {
   int keys;                                   // keys that shared memory holds
 };
 
-// d += a b for one 16 x 8 x 32 tile of signed bytes
-__device__ __forceinline__ void mma16832_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+// d += a b for one 16 x 8 x 16 tile of fp16 with fp32 sums
+__device__ __forceinline__ void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four codes as two fp16 pairs: behind 0x64 a byte is 1024 and itself, and the code's sign bit turned makes it 128 more.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  const __half2 off = __float2half2_rn(1152.f);
+  uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off), y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
@@ -172,7 +184,7 @@ __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
 }
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) { widen8(*reinterpret_cast<const uint4*>(p), x); }
 
-constexpr int kSelect = 256;        // threads of a CTA: each warp scores eight pages at a time
+constexpr int kSelect = 256;        // threads of a CTA: each warp scores sixteen pages at a time
 constexpr int kSelectKeys = 16384;  // pages whose keys fit in shared memory
 
 // A rising key for a score (no NaN).
@@ -207,11 +219,11 @@ __device__ __forceinline__ uint32_t load_first(uint32_t addr) {
 // Dynamic shared memory: the keys (first CTA of a cluster; in the workspace where they do not fit).
 template <typename T, int D>
 __global__ void __launch_bounds__(kSelect, 2) paged_select_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int LINE = 2 * D + 64;  // bytes of a query's [u-, u+] (rows half a line of banks apart)
+  constexpr int LINE = 2 * D + 8;   // fp16 values of a query's [u-, u+] (rows 4 banks apart)
   constexpr int Q = 2 * D / 64;     // 16-byte pieces a lane of a row
   constexpr int W = kSelect / 32;
   extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ __align__(16) int8_t code_s[16 * LINE];
+  __shared__ __align__(16) __half u_s[8 * LINE];
   __shared__ int hist[256], part[W][2];
   __shared__ uint32_t red_s[W], red2_s[W];
   __shared__ uint32_t prefix_s;
@@ -240,30 +252,36 @@ __global__ void __launch_bounds__(kSelect, 2) paged_select_kernel(const __grid_c
   const bool kept = n <= p.keys;
   uint32_t* far = p.far + static_cast<size_t>(u) * p.pages;
   const uint32_t keys_at = static_cast<uint32_t>(__cvta_generic_to_shared(keys));
-  // Pages are dealt to the warps eight at a time, a tile; a warp looks up four tiles' pages and exponents at once.
-  // The first tile's codes are on their way while the queries are looked at.
-  const int tiles = (n + 7) / 8, stride = W * ctas, tile0 = rank * W + warp;
-  uint4 b[Q];
-  int page = -1, e = 0;  // of place (lane & 7) of tile `first of four` + (lane >> 3) * stride
+  // Pages are dealt to the warps sixteen at a time, a tile; a warp looks up two tiles' pages and exponents at once.
+  // The first tile's codes are on their way while the queries are looked at, each later one's under the products before.
+  const int tiles = (n + 15) / 16, stride = W * ctas, tile0 = rank * W + warp;
+  uint4 c[2][Q];         // of pages (lane >> 2) and 8 + (lane >> 2): bytes 64 k + 16 (lane & 3) .. of their codes
+  int page = -1, e = 0;  // of place (lane & 15) of tile `first of two` + (lane >> 4) * stride
   auto look = [&](int tile) {
-    const int j = (tile + (lane >> 3) * stride) * 8 + (lane & 7);
+    const int j = (tile + (lane >> 4) * stride) * 16 + (lane & 15);
     page = j < n ? page_at(p.b, s, p.first + j) : -1;
     e = page < 0 ? 0 : p.exp[static_cast<size_t>(page) * p.Hkv + h];
   };
-  auto fetch = [&](int i) {  // codes of the i-th of the four: this lane's page as the second operand's column
-    const int x = __shfl_sync(0xffffffffu, page, i * 8 + (lane >> 2));
-    const uint4* src = reinterpret_cast<const uint4*>(p.code + (static_cast<size_t>(x < 0 ? 0 : x) * p.Hkv + h) * 2 * D) + (lane & 3);
+  auto codes = [&](int i, int r) {  // of the i-th of the two
+    const int x = __shfl_sync(0xffffffffu, page, i * 16 + r * 8 + (lane >> 2));
+    return reinterpret_cast<const uint4*>(p.code + (static_cast<size_t>(x < 0 ? 0 : x) * p.Hkv + h) * 2 * D) + (lane & 3);
+  };
+  auto fetch = [&]() {
+    const uint4 *x = codes(0, 0), *y = codes(0, 1);
 #pragma unroll
-    for (int k = 0; k < Q; k++) b[k] = src[k * 4];
+    for (int k = 0; k < Q; k++) {
+      c[0][k] = x[k * 4];
+      c[1][k] = y[k * 4];
+    }
   };
   if (tile0 < tiles) {
     look(tile0);
-    fetch(0);
+    fetch();
   }
   // the group's queries in whole steps
   const T* q = static_cast<const T*>(p.q) + (static_cast<size_t>(s) * p.Hq + h * p.G) * D;
   uint32_t top = 0;  // the largest size, as bits (what is not finite comes out above every finite one)
-  float mine[8];     // this thread's last eight values (its only ones in a small group)
+  float mine[8];     // this thread's last eight values (its only ones where the group has eight heads or fewer)
   for (int i = tid; i < p.G * D / 8; i += kSelect) {
     load8(q + i * 8, mine);
 #pragma unroll
@@ -283,72 +301,90 @@ __global__ void __launch_bounds__(kSelect, 2) paged_select_kernel(const __grid_c
   // times 2^-f in two steps, each a power of two that fp32 holds (a product that is rounded on the way is under 1/2 in the end)
   const int f1 = -f / 2;
   const float by1 = finite ? ldexpf(1.f, f1) : 0.f, by2 = finite ? ldexpf(1.f, -f - f1) : 0.f;
-  const int pages0 = p.first;
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  for (int g0 = 0; g0 < p.G; g0 += 16) {
+  for (int g0 = 0; g0 < p.G; g0 += 8) {
     if (g0 > 0) __syncthreads();
-    for (int i = tid; i < 16 * D / 8; i += kSelect) {
-      const int g = i / (D / 8), d = i % (D / 8) * 8;
+    {
+      const int g = tid / (D / 8), d = tid % (D / 8) * 8;  // (D = 256: a thread an eighth of 64 values, else some have none)
       float x[8];
-      if (finite && g0 + g < p.G) {
-        if (p.G <= 16 && p.G * D <= kSelect * 8) {
+      if (g < 8) {
+        if (finite && g0 + g < p.G) {
+          if (p.G <= 8) {
 #pragma unroll
-          for (int c = 0; c < 8; c++) x[c] = mine[c];
+            for (int i = 0; i < 8; i++) x[i] = mine[i];
+          } else {
+            load8(q + static_cast<size_t>(g0 + g) * D + d, x);
+          }
         } else {
-          load8(q + static_cast<size_t>(g0 + g) * D + d, x);
+#pragma unroll
+          for (int i = 0; i < 8; i++) x[i] = 0.f;
         }
-      } else {
+        uint32_t lo[4], hi[4];
 #pragma unroll
-        for (int e = 0; e < 8; e++) x[e] = 0.f;
+        for (int i = 0; i < 8; i += 2) {
+          const float v0 = rintf(__fmul_rn(__fmul_rn(x[i], by1), by2)), v1 = rintf(__fmul_rn(__fmul_rn(x[i + 1], by1), by2));
+          const __half2 a = __floats2half2_rn(fminf(v0, 0.f), fminf(v1, 0.f)), b = __floats2half2_rn(fmaxf(v0, 0.f), fmaxf(v1, 0.f));
+          lo[i / 2] = *reinterpret_cast<const uint32_t*>(&a);
+          hi[i / 2] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(u_s + g * LINE + d) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(u_s + g * LINE + D + d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       }
-      uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const int v = __float2int_rn(__fmul_rn(__fmul_rn(x[e], by1), by2));
-        lo[e / 4] |= (static_cast<uint32_t>(min(v, 0)) & 255u) << (e % 4 * 8);
-        hi[e / 4] |= (static_cast<uint32_t>(max(v, 0)) & 255u) << (e % 4 * 8);
-      }
-      *reinterpret_cast<uint2*>(code_s + g * LINE + d) = make_uint2(lo[0], lo[1]);
-      *reinterpret_cast<uint2*>(code_s + g * LINE + D + d) = make_uint2(hi[0], hi[1]);
     }
     __syncthreads();
-    const int live = min(16, p.G - g0);
-    const int8_t* row = code_s + (lane >> 2) * LINE + (lane & 3) * 16;
-    int i = 0;
-    for (int tile = tile0; tile < tiles; tile += stride, i = (i + 1) & 3) {
-      if (i == 0 && (g0 > 0 || tile > tile0)) {
-        look(tile);
-        fetch(0);
+    const int live = min(8, p.G - g0);
+    const __half* row = u_s + (lane >> 2) * LINE + (lane & 3) * 16;
+    for (int two = tile0; two < tiles; two += 2 * stride) {
+      if (g0 > 0 || two > tile0) {
+        look(two);
+        fetch();
       }
-      int d[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int k = 0; k < Q; k++) {
-        const uint4 x = *reinterpret_cast<const uint4*>(row + k * 64);
-        uint4 y = make_uint4(0u, 0u, 0u, 0u);
-        if (live > 8) y = *reinterpret_cast<const uint4*>(row + 8 * LINE + k * 64);
-        mma16832_s8(d, x.x, y.x, x.y, y.y, b[k].x, b[k].y);
-        mma16832_s8(d, x.z, y.z, x.w, y.w, b[k].z, b[k].w);
-      }
-      if (i < 3 && tile + stride < tiles) fetch(i + 1);  // the next ones under what follows
-      // the highest of the heads there are, of pages 2 (lane & 3) and 2 (lane & 3) + 1
-      int best[2];
+      for (int i = 0; i < 2; i++) {
+        const int tile = two + i * stride;
+        if (tile >= tiles) break;
+        const bool next = i == 0 && tile + stride < tiles;
+        const uint4 *x = codes(1, 0), *y = codes(1, 1);
+        float d[2][4];  // (two sums: products that follow one another wait)
 #pragma unroll
-      for (int c = 0; c < 2; c++) {
-        int x = (lane >> 2) < live ? d[c] : INT_MIN;
-        if ((lane >> 2) + 8 < live) x = max(x, d[2 + c]);
+        for (int k = 0; k < 4; k++) d[0][k] = d[1][k] = 0.f;
 #pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-        best[c] = x;
-      }
-      const int v0 = __shfl_sync(0xffffffffu, best[0], (lane & 7) >> 1), v1 = __shfl_sync(0xffffffffu, best[1], (lane & 7) >> 1);
-      const int ex = __shfl_sync(0xffffffffu, e, i * 8 + (lane & 7)), j = tile * 8 + lane;
-      if (lane < 8 && j < n) {
-        uint32_t key = rising(ex >= 128 ? INFINITY : ldexpf(static_cast<float>(lane & 1 ? v1 : v0), ex));
-        if (kept) {  // (later heads' scores of a page are this lane's own again)
-          if (g0 > 0) key = max(key, load_first(keys_at + j * 4));
-          store_first(keys_at + j * 4, key);
-        } else {
-          far[j] = g0 > 0 ? max(key, far[j]) : key;
+        for (int k = 0; k < Q; k++) {
+          const uint4 u0 = *reinterpret_cast<const uint4*>(row + k * 64), u1 = *reinterpret_cast<const uint4*>(row + k * 64 + 8);
+          const uint32_t w0[4] = {c[0][k].x, c[0][k].y, c[0][k].z, c[0][k].w}, w1[4] = {c[1][k].x, c[1][k].y, c[1][k].z, c[1][k].w};
+          const uint32_t u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            uint32_t a0, a1, a2, a3;
+            widen4(w0[j], a0, a2);
+            widen4(w1[j], a1, a3);
+            mma16816_f16(d[j & 1], a0, a1, a2, a3, u[2 * j], u[2 * j + 1]);
+          }
+          if (next) {
+            c[0][k] = x[k * 4];
+            c[1][k] = y[k * 4];
+          }
+        }
+        // the highest of the heads there are, of pages (lane >> 2) and 8 + (lane >> 2)
+        const int h0 = (lane & 3) * 2;
+        float best[2];
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+          float v = h0 < live ? __fadd_rn(d[0][2 * r], d[1][2 * r]) : -INFINITY;
+          if (h0 + 1 < live) v = fmaxf(v, __fadd_rn(d[0][2 * r + 1], d[1][2 * r + 1]));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+          best[r] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+        }
+        const int r = lane & 1, at = r * 8 + (lane >> 2), j = tile * 16 + at;
+        const int ex = __shfl_sync(0xffffffffu, e, i * 16 + at);
+        if ((lane & 2) == 0 && j < n) {
+          uint32_t key = rising(ex >= 128 ? INFINITY : ldexpf(best[r], ex));
+          if (kept) {  // (later heads' scores of a page are this lane's own again)
+            if (g0 > 0) key = max(key, load_first(keys_at + j * 4));
+            store_first(keys_at + j * 4, key);
+          } else {
+            far[j] = g0 > 0 ? max(key, far[j]) : key;
+          }
         }
       }
     }
@@ -361,14 +397,28 @@ __global__ void __launch_bounds__(kSelect, 2) paged_select_kernel(const __grid_c
     __syncthreads();
   }
   if (bad) return;
-  // ---- the choice
+  // ---- the choice: a run of keys a thread, in registers where eight do
+  constexpr int RUN = 8;
+  const bool few = n <= RUN * kSelect;  // (shared memory then holds all of them)
   auto key = [&](int i) { return kept ? keys[i] : __ldcg(far + i); };
+  const int run = (n + kSelect - 1) / kSelect, i0 = min(tid * run, n), i1 = min(i0 + run, n);
+  uint32_t own[RUN];
+#pragma unroll
+  for (int j = 0; j < RUN; j++) own[j] = few && i0 + j < i1 ? keys[i0 + j] : 0u;
+  auto each = [&](auto f) {
+    if (few) {
+#pragma unroll
+      for (int j = 0; j < RUN; j++)
+        if (i0 + j < i1) f(i0 + j, own[j]);
+    } else {
+      for (int i = i0; i < i1; i++) f(i, key(i));
+    }
+  };
   uint32_t low = 0xffffffffu, high = 0;
-  for (int i = tid; i < n; i += kSelect) {
-    const uint32_t k = key(i);
+  each([&](int, uint32_t k) {
     low = min(low, k);
     high = max(high, k);
-  }
+  });
   low = __reduce_min_sync(0xffffffffu, low);
   high = __reduce_max_sync(0xffffffffu, high);
   if (lane == 0) {
@@ -389,10 +439,10 @@ __global__ void __launch_bounds__(kSelect, 2) paged_select_kernel(const __grid_c
   while (bits > 0 && !all) {
     const int shift = max(bits - 8, 0);
     const uint32_t mask = (1u << (bits - shift)) - 1u;
-    for (int i = tid; i < n; i += kSelect) {
-      const uint32_t k = key(i) - low;
+    each([&](int, uint32_t x) {
+      const uint32_t k = x - low;
       if (bits == 32 || (k >> bits) == (prefix >> bits)) atomicAdd(&hist[(k >> shift) & mask], 1);
-    }
+    });
     __syncthreads();
     if (warp == 0) {  // from the top: lane 0 holds bins 255 .. 248
       int c[8], sum = 0;
@@ -421,49 +471,48 @@ __global__ void __launch_bounds__(kSelect, 2) paged_select_kernel(const __grid_c
     __syncthreads();
     prefix = prefix_s;
     need = need_s;
-    all = left_s == need;  // the whole digit is taken
+    all = left_s == need_s;  // the whole digit is taken
     bits = shift;
     hist[tid] = 0;
     __syncthreads();
   }
-  // every higher key, and of those that share all bits found the first `need`
-  const uint32_t border = prefix >> bits;  // (bits 32: no key differs in any)
-  int out = 0, equal = 0;
+  // every higher key, and of those that share all bits found the first `need`: the threads' counts summed over the CTA
+  const uint32_t border = prefix >> bits;
+  int higher = 0, equal = 0;
+  each([&](int, uint32_t x) {
+    const uint32_t k = (x - low) >> bits;
+    higher += k > border;
+    equal += k == border;
+  });
+  int more_in = higher, same_in = equal;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, more_in, o), y = __shfl_up_sync(0xffffffffu, same_in, o);
+    if (lane >= o) {
+      more_in += x;
+      same_in += y;
+    }
+  }
+  if (lane == 31) {
+    part[warp][0] = more_in;
+    part[warp][1] = same_in;
+  }
+  __syncthreads();
+  int before = more_in - higher, same = same_in - equal;
+#pragma unroll
+  for (int w = 0; w < W; w++)
+    if (w < warp) {
+      before += part[w][0];
+      same += part[w][1];
+    }
+  int place = p.first + before + min(same, need);  // (where a digit was taken whole, need is all of the equal ones)
+  each([&](int i, uint32_t x) {
+    const uint32_t k = (x - low) >> bits;
+    if (k > border || (k == border && same++ < need)) sel[place++] = p.first + i;
+  });
   for (int i = tid; i < p.first; i += kSelect) sel[i] = i;
   for (int i = tid; i < p.last; i += kSelect) sel[p.n_sel - p.last + i] = nb - p.last + i;
   if (tid == 0) p.count[u] = p.n_sel;
-  for (int i0 = 0; i0 < n; i0 += kSelect) {
-    const int i = i0 + tid;
-    const uint32_t k = i < n ? (key(i) - low) >> bits : 0u;
-    const bool more = i < n && k > border, same = i < n && k == border;
-    const unsigned ms = __ballot_sync(0xffffffffu, same), below = (1u << lane) - 1u;
-    bool take = more || same;
-    int all_same = 0;
-    if (!all) {  // (else every equal one is taken)
-      if (lane == 0) part[warp][0] = __popc(ms);
-      __syncthreads();
-      int before = equal + __popc(ms & below);
-#pragma unroll
-      for (int w = 0; w < W; w++) {
-        if (w < warp) before += part[w][0];
-        all_same += part[w][0];
-      }
-      take = more || (same && before < need);
-    }
-    const unsigned mt = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) part[warp][1] = __popc(mt);
-    __syncthreads();
-    int place = out + __popc(mt & below), sum = 0;
-#pragma unroll
-    for (int w = 0; w < W; w++) {
-      if (w < warp) place += part[w][1];
-      sum += part[w][1];
-    }
-    if (take) sel[pages0 + place] = pages0 + i;
-    out += sum;
-    equal += all_same;
-    __syncthreads();
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -496,7 +545,8 @@ static bool launch_select_t(const SelectParams& p, int ctas, int units, cudaStre
   static std::atomic<uint64_t> set{0};
   const int bytes = p.keys * 4;
   if (!allow_smem(paged_select_kernel<T, D>, kSelectKeys * 4, set)) return false;
-  launch_k_cluster(true, ctas, paged_select_kernel<T, D>, dim3(ctas, units), dim3(kSelect), bytes, st, p);
+  if (ctas > 1) launch_k_cluster(true, ctas, paged_select_kernel<T, D>, dim3(ctas, units), dim3(kSelect), bytes, st, p);
+  else launch_k(true, paged_select_kernel<T, D>, dim3(1, units), dim3(kSelect), bytes, st, p);
   return true;
 }
 template <int D>
@@ -579,10 +629,10 @@ extern "C" tv_status tv_paged_select(const tv_paged_layer* l, const tv_paged* b,
   const int units = b->n_seq * l->Hkv;
   const int most = p.pages > n_sel && n_sel > first + last ? p.pages - first - last : 0;  // pages to choose from, at most
   p.keys = most < kSelectKeys ? most : kSelectKeys;
-  // CTAs for a slot's KV head: up to eight, while the GPU has room and each has 128 pages (the queries' codes take each as
+  // CTAs for a slot's KV head: up to eight, while all run at once (two an SM) and each has 128 pages (the queries' codes take each as
   // long as some 100 pages)
   int ctas = 1;
-  while (ctas < 8 && units * ctas < 2 * num_sms() && ctas * 2 * 128 <= most) ctas *= 2;
+  while (ctas < 8 && units * ctas <= num_sms() && ctas * 2 * 128 <= most) ctas *= 2;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = l->dtype == TV_BF16;
   const bool ok = l->D == 64 ? launch_select_d<64>(p, bf, ctas, units, st) : l->D == 128 ? launch_select_d<128>(p, bf, ctas, units, st)

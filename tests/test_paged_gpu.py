@@ -289,6 +289,22 @@ def test_select(dtype, heads, first, last, n_sel):
     assert p.status() == 0
 
 
+def test_select_largest_sums():
+    """Codes and queries at their ends: scores of 127 * 127 * 256, and neighbours that differ by one step."""
+    p = Pools([64 * 16 + 3], 16, (24, 4, 256), seed=1, fill=None)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    sign = torch.randint(0, 2, (1, 4, 1, 256), generator=gen, device="cuda") * 2 - 1
+    p.q.copy_((sign.expand(1, 4, 6, 256).reshape(1, 24, 256) * 127.0).to(BF))
+    code = torch.zeros(p.n_pages, 4, 2, 256, dtype=torch.int8, device="cuda")
+    code[:, :, 1], code[:, :, 0] = 127, -127
+    for x in range(p.n_pages):  # one column of each page a step or two lower
+        code[x, :, :, (7 * x) % 256] = torch.tensor([-127 + x % 3, 127 - x % 3], dtype=torch.int8, device="cuda")
+    exp = torch.zeros(p.n_pages, 4, dtype=torch.int32, device="cuda")
+    sel, count = _select(p, code, exp, 1, 2, 20)
+    for g in range(4):
+        assert sel[0, g].tolist() == _want(p, code, exp, 1, 2, 20, 0, g) and int(count[0, g]) == 20
+
+
 @pytest.mark.parametrize("lens", [[200000, 135008], [16 * 16385 + 30, 400000]])
 @pytest.mark.parametrize("Hq", [8, 64])
 def test_select_long(lens, Hq):
