@@ -545,7 +545,13 @@ tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* layer, const tv_prompt* 
  * Later calls given the word do nothing.
  *
  * Every call launches with programmatic dependent launch; its first kernel
- * reads nothing of the caller's before it waits. */
+ * reads nothing of the caller's before it waits, and lets later ones of the call
+ * in when it has.
+ *
+ * An infinity or NaN among the rows that a slot sees reaches what the formulas
+ * let it reach; rows that it does not see (behind len[s], in pages of others)
+ * may hold anything.  (A score of -inf has a weight of 0: an infinite value
+ * beside it gives NaN, as 0 times infinity does.) */
 #define TV_MAX_PAGED_SEQ 1024 /* sequences (slots) of one paged call; n_seq * Hkv < 2^16 (TV_ERR_SHAPE) */
 
 typedef struct {
@@ -607,10 +613,13 @@ size_t tv_paged_attn_workspace_bytes(const tv_paged_layer* layer, const tv_paged
  * of which tv_paged_append has just written,
  *     out[s,h] = sum_t softmax_t(scale q[s,h] . K[t]) V[t]   (times sigmoid(gate[s,h]))
  *  groups or NULL: the prefixes of groups with two active members or more are
- *         read once for all members, from the table of the first active one; the
- *         result is the same up to rounding.  Offsets or lengths that do not hold
- *         what is said above set TV_ERR_ROWS.
- *  q, out [n_seq][Hq][D]; gate the same or NULL (may be out); q and out apart
+ *         read once for all members, from the table of the first active one, where
+ *         that saves the call 200 MB of reads or more (it costs about as long as
+ *         those); the result is the same up to rounding.  fp32 layers read every
+ *         slot's own.  Offsets or lengths that do not hold what is said above set
+ *         TV_ERR_ROWS (bf16 layers).
+ *  q, out [n_seq][Hq][D]; gate the same or NULL (may be out); out shares memory with nothing
+ *         else that is read (TV_ERR_ARG)
  *  scale  score scale > 0
  *  workspace as in tv_attn_prompt. */
 tv_status tv_paged_attn(const tv_paged_layer* layer, const tv_paged* batch, const tv_paged_groups* groups, const void* q,
@@ -639,7 +648,7 @@ tv_status tv_paged_bounds(const tv_paged_layer* layer, const tv_paged* batch, co
  *  first >= 0, last >= 1, first + last <= n_sel <= 4096
  *  workspace as in tv_attn_prompt (none is needed up to 16,384 pages a slot)
  *  sel    device [n_seq][Hkv][n_sel]: page indices (columns of the table), rising, -1 behind the last
- *  count  device [n_seq][Hkv] */
+ *  count  device [n_seq][Hkv]; both share memory with nothing that is read (TV_ERR_ARG) */
 size_t tv_paged_select_workspace_bytes(const tv_paged_layer* layer, const tv_paged* batch);
 tv_status tv_paged_select(const tv_paged_layer* layer, const tv_paged* batch, const int8_t* code, const int32_t* exp,
                           int32_t first, int32_t last, int32_t n_sel, const void* q, int32_t* sel, int32_t* count,

@@ -161,6 +161,11 @@ static tv_status paged_attn(const PagedAttnCall& a, cudaStream_t st) {
   const size_t n = bytes_of(a.batch->n_seq, static_cast<int64_t>(l->Hq) * l->D, l->dtype);
   if (share_memory(a.q, n, a.out, n)) return TV_ERR_ARG;  // a slot's heads are read after others are written
   if (a.gate != a.out && share_memory(a.gate, n, a.out, n)) return TV_ERR_ARG;
+  const size_t pool = bytes_of(static_cast<int64_t>(l->n_pages) * l->Hkv * l->page, l->D, l->dtype);
+  const size_t ns = static_cast<size_t>(a.batch->n_seq) * l->Hkv * 4;
+  if (share_memory(a.out, n, l->K, pool) || share_memory(a.out, n, l->V, pool) || share_memory(a.out, n, a.sel, ns * a.n_sel) ||
+      share_memory(a.out, n, a.count, ns))
+    return TV_ERR_ARG;
   return l->dtype == TV_BF16 ? paged_attn_tc_launch(a, st) : launch_cuda(a, st);
 }
 

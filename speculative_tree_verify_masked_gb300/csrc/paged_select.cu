@@ -609,6 +609,15 @@ extern "C" tv_status tv_paged_select(const tv_paged_layer* l, const tv_paged* b,
   if (!code || !exp || !q || !sel || !count || first < 0 || last < 1 || n_sel < 1 || n_sel > 4096 || first > n_sel || last > n_sel - first)
     return TV_ERR_ARG;
   if (!aligned16(code) || !aligned16(exp) || !aligned16(q) || !aligned16(sel) || !aligned16(count) || !aligned16(ws)) return TV_ERR_ALIGN;
+  // lists are written while others' bounds and queries are read
+  const size_t units_b = static_cast<size_t>(b->n_seq) * l->Hkv, heads = static_cast<size_t>(l->n_pages) * l->Hkv;
+  const size_t nq = bytes_of(b->n_seq, static_cast<int64_t>(l->Hq) * l->D, l->dtype);
+  if (share_memory(sel, units_b * n_sel * 4, count, units_b * 4)) return TV_ERR_ARG;
+  for (const auto& o : {std::pair<const void*, size_t>(sel, units_b * n_sel * 4), std::pair<const void*, size_t>(count, units_b * 4)})
+    if (share_memory(o.first, o.second, code, heads * 2 * l->D) || share_memory(o.first, o.second, exp, heads * 4) ||
+        share_memory(o.first, o.second, q, nq) || share_memory(o.first, o.second, b->table, static_cast<size_t>(b->n_seq) * b->cols * 4) ||
+        share_memory(o.first, o.second, b->len, static_cast<size_t>(b->n_seq) * 4))
+      return TV_ERR_ARG;
   const size_t need = tv_paged_select_workspace_bytes(l, b);
   if (need > 0 && (!ws || ws_bytes < need)) return TV_ERR_WORKSPACE;
   SelectParams p{};

@@ -135,6 +135,8 @@ def test_attn_refused(L, call):
     n = 8 * 24 * 256 * 2
     for out in (Q, Q + 16, Q - n + 16):
         assert call(L, out=out) == ARG
+    for out in (K, K + 100 * 4 * 64 * 256 * 2 - 16, V - n + 16):
+        assert call(L, out=out) == ARG
     for gate in (OUT + 16, OUT - 16, OUT + n - 16):
         assert call(L, gate=gate) == ARG
     for bad in ({"q": Q + 8}, {"out": OUT + 8}, {"gate": Q + 8}, {"ws": FAR + 8}):
@@ -151,6 +153,7 @@ def test_groups_and_lists_refused(L):
         assert attn(L, g=g) == ARG
     for g in (groups(off=0x5004), groups(shared=0x6008)):
         assert attn(L, g=g) == ALIGN
+    assert selected(L, out=0x7000 - 16) == ARG and selected(L, out=0x8010) == ARG
     for bad in ({"sel": 0}, {"cnt": 0}, {"n_sel": 0}, {"n_sel": 4097}):
         assert selected(L, **bad) == ARG, bad
     for bad in ({"sel": 0x7008}, {"cnt": 0x8004}):
@@ -163,11 +166,14 @@ def test_select_and_bounds_refused(L):
         assert select(L, **bad) == ARG, bad
     for bad in ({"code": K_RAW + 4}, {"exp": V_RAW + 4}, {"q": Q + 8}, {"sel": 0x7004}, {"cnt": 0x8004}, {"ws": FAR + 4}):
         assert select(L, **bad) == ALIGN, bad
+    for bad in ({"sel": 0x8000, "cnt": 0x8010}, {"sel": K_RAW}, {"cnt": V_RAW + 16}, {"sel": Q}, {"cnt": 0x2010}, {"sel": 0x1010}):
+        assert select(L, **bad) == ARG, bad
     need = L.tv_paged_select_workspace_bytes(ref(layer()), ref(batch()))
     assert need == 0  # up to 16,384 pages
     far = dict(l=layer(page=16), b=batch(cols=20000, max_len=16384 * 16))
     need = L.tv_paged_select_workspace_bytes(ref(far["l"]), ref(far["b"]))
     assert need == 8 * 4 * 16385 * 4
+    far.update(sel=9 << 30, cnt=10 << 30)
     assert select(L, n=need - 1, **far) == WORKSPACE and select(L, ws=0, **far) == WORKSPACE
     for bad in ({"code": 0}, {"exp": 0}, {"code": K}, {"exp": K + 16}, {"exp": OUT + 16}):
         assert bounds(L, **bad) == ARG, bad
