@@ -786,12 +786,16 @@ def tv_paged_append(layer: PagedLayer, batch: PagedBatch, rows: PagedRows | None
     here, st = _paged("tv_paged_append", layer, batch, rows, stream)
     n, dt, f32 = batch.n_seq if rows is None else rows.n_total, layer.dtype, torch.float32
     nq, nk = n * layer.q_row, n * layer.kv_row
-    if not (_fits(q_norm, f32, layer.D, here) and _fits(k_norm, f32, layer.D, here) and _fits(q_raw, dt, nq, here) and
-            _fits(k_raw, dt, nk, here) and _fits(v, dt, nk, here) and _fits(q, dt, nq, here)):
+    # (_fits written out: its calls were a tenth of a small call's time)
+    if not (q_raw.dtype is dt and q_raw.get_device() == here and q_raw.is_contiguous() and q_raw.numel() >= nq and
+            k_raw.dtype is dt and k_raw.get_device() == here and k_raw.is_contiguous() and k_raw.numel() >= nk and
+            v.dtype is dt and v.get_device() == here and v.is_contiguous() and v.numel() >= nk and
+            q.dtype is dt and q.get_device() == here and q.is_contiguous() and q.numel() >= nq and
+            _fits(q_norm, f32, layer.D, here) and _fits(k_norm, f32, layer.D, here)):
         _need("tv_paged_append", q_norm=(q_norm, f32, layer.D), k_norm=(k_norm, f32, layer.D), q_raw=(q_raw, dt, nq),
               k_raw=(k_raw, dt, nk), v=(v, dt, nk), q=(q, dt, nq))
-    code = lib().tv_paged_append(layer.ref, batch.ref, _ref(rows), _ptr(q_norm), _ptr(k_norm), eps, rot_dims, theta,
-                                 _ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(q), st)
+    code = lib().tv_paged_append(layer.ref, batch.ref, None if rows is None else rows.ref, _ptr(q_norm), _ptr(k_norm), eps,
+                                 rot_dims, theta, q_raw.data_ptr(), k_raw.data_ptr(), v.data_ptr(), q.data_ptr(), st)
     if code:
         _check(code, "tv_paged_append")
 
@@ -838,12 +842,15 @@ def tv_paged_select(layer: PagedLayer, batch: PagedBatch, code, exp, first: int,
     here, st = _paged("tv_paged_select", layer, batch, None, stream)
     n_sel, units, i32 = sel.shape[-1], batch.n_seq * layer.Hkv, torch.int32
     nc, nq = layer.heads * 2 * layer.D, batch.n_seq * layer.q_row
-    if not (_fits(code, torch.int8, nc, here) and _fits(exp, i32, layer.heads, here) and _fits(q, layer.dtype, nq, here) and
-            _fits(sel, i32, units * n_sel, here) and _fits(count, i32, units, here)):
+    if not (code.dtype is torch.int8 and code.get_device() == here and code.is_contiguous() and code.numel() >= nc and
+            exp.dtype is i32 and exp.get_device() == here and exp.is_contiguous() and exp.numel() >= layer.heads and
+            q.dtype is layer.dtype and q.get_device() == here and q.is_contiguous() and q.numel() >= nq and
+            sel.dtype is i32 and sel.get_device() == here and sel.is_contiguous() and sel.numel() >= units * n_sel and
+            count.dtype is i32 and count.get_device() == here and count.is_contiguous() and count.numel() >= units):
         _need("tv_paged_select", code=(code, torch.int8, nc), exp=(exp, i32, layer.heads), q=(q, layer.dtype, nq),
               sel=(sel, i32, units * n_sel), count=(count, i32, units))
-    status = lib().tv_paged_select(layer.ref, batch.ref, _ptr(code), _ptr(exp), first, last, n_sel, _ptr(q), _ptr(sel),
-                                   _ptr(count), _ptr(ws), _space(ws, here), st)
+    status = lib().tv_paged_select(layer.ref, batch.ref, code.data_ptr(), exp.data_ptr(), first, last, n_sel, q.data_ptr(),
+                                   sel.data_ptr(), count.data_ptr(), _ptr(ws), _space(ws, here), st)
     if status:
         _check(status, "tv_paged_select")
 
