@@ -95,14 +95,19 @@ struct PagedTcParams {
 
 // Tiles of an item of unit u.
 template <int ROWS>
-__device__ __forceinline__ int unit_tiles(const PagedTcParams& p, int u) {
-  const int s = u / p.v.Hkv, L = paged_len(p.v.b, s);
+__device__ __forceinline__ int unit_tiles(const PagedTcParams& p, int u, int s, int L) {
   if (L < 0) return 0;
   if (p.v.sel) return ((p.v.pages(s, u - s * p.v.Hkv, L) << p.v.b.shift) + ROWS - 1) / ROWS;
   return (L + 1 - (p.start ? p.start[s] : 0) + ROWS - 1) / ROWS;
 }
 
 constexpr int kNear = 16;
+
+template <int ROWS>
+__device__ __forceinline__ int unit_tiles(const PagedTcParams& p, int u) {
+  const int s = u / p.v.Hkv;
+  return unit_tiles<ROWS>(p, u, s, paged_len(p.v.b, s));
+}
 
 // The items of a range of tiles, one after another.
 struct PagedPiece {
@@ -143,8 +148,14 @@ struct PagedWalk {
   }
 };
 // CTAs that share `total` tiles, and where CTA c's range starts.
-__device__ __forceinline__ int64_t range_start(int64_t total, int ctas, int c) { return total * c / ctas; }
+// (in 32 bits where they do: 64-bit divisions took a sixth of a small call)
+constexpr int64_t kFewTiles = 1 << 22;  // times 1,024 CTAs at most
+__device__ __forceinline__ int64_t range_start(int64_t total, int ctas, int c) {
+  if (total < kFewTiles) return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ctas);
+  return total * c / ctas;
+}
 __device__ __forceinline__ int range_of(int64_t total, int ctas, int64_t tile) {
+  if (total < kFewTiles) return static_cast<int>((static_cast<uint32_t>(tile + 1) * static_cast<uint32_t>(ctas) - 1u) / static_cast<uint32_t>(total));
   return static_cast<int>(((tile + 1) * ctas - 1) / total);
 }
 __device__ __forceinline__ int ctas_for(int64_t total, int grid) { return static_cast<int>(min(static_cast<int64_t>(grid), total)); }
@@ -212,7 +223,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     const int per = (p.units + kThreads - 1) / kThreads;
     const int u0 = min(static_cast<int>(threadIdx.x) * per, p.units), u1 = min(u0 + per, p.units);
     int64_t mine = 0;
-    for (int u = u0; u < u1; u++) mine += static_cast<int64_t>(unit_tiles<C::ROWS>(p, u)) * p.MT;
+    int2 last = make_int2(0, -1);  // of the thread's only unit, where it has one
+    for (int u = u0; u < u1; u++) {
+      const int s = u / p.v.Hkv;
+      last.y = paged_len(p.v.b, s);
+      last.x = unit_tiles<C::ROWS>(p, u, s, last.y);
+      mine += static_cast<int64_t>(last.x) * p.MT;
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -242,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       if (a >= base && a < base + mine) {
         int64_t at = base;
         int u = u0;
-        for (;; u++) {
+        for (; per > 1; u++) {
           const int64_t n = static_cast<int64_t>(unit_tiles<C::ROWS>(p, u)) * p.MT;
           if (a < at + n || u + 1 >= u1) break;
           at += n;
@@ -256,12 +273,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       }
     }
     __syncthreads();
+    if (lo.left > 0) {  // what the next units hold
+      if (per == 1) {
+        if (u0 < u1 && u0 >= lo.u && u0 < lo.u + kNear) lo_near[u0 - lo.u] = last;
+      } else if (threadIdx.x < kNear && lo.u + static_cast<int>(threadIdx.x) < p.units) {
+        const int u = lo.u + threadIdx.x, s = u / p.v.Hkv, L = paged_len(p.v.b, s);
+        lo_near[threadIdx.x] = make_int2(unit_tiles<C::ROWS>(p, u, s, L), L);
+      }
+    }
+    __syncthreads();
   }
-  if (lo.left > 0 && threadIdx.x < kNear && lo.u + static_cast<int>(threadIdx.x) < p.units) {
-    const int u = lo.u + threadIdx.x;
-    lo_near[threadIdx.x] = make_int2(unit_tiles<C::ROWS>(p, u), paged_len(p.v.b, u / p.v.Hkv));
-  }
-  __syncthreads();
   PagedWalk<C::ROWS> walk{lo.u, lo.u / p.v.Hkv, lo.u % p.v.Hkv, lo.u, lo_near, lo.off, lo.left};
   PagedPiece x;
   pdl_trigger();
