@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(32 * kCudaWarps, 1) attn_paged_cuda_kernel(con
   __shared__ float acc_s[kCudaWarps][D], m_s[kCudaWarps], l_s[kCudaWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  const bool bad = status_bad(p.v.b.status);
+  const bool bad = status_set(p.v.b.status);
   const int h = blockIdx.x, s = blockIdx.y, g = h / p.G;
   const size_t row0 = (static_cast<size_t>(s) * p.Hq + h) * D;
   float q[CPL], acc[CPL], m = -INFINITY, l = 0.f;

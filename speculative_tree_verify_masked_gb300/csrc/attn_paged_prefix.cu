@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) attn_paged_prefix_kernel(co
                                    reinterpret_cast<unsigned long long*>(count + 2 * TV_MAX_PAGED_SEQ)};
   int code = sb & 1023u ? TV_ERR_CUDA : 0;
   code = check.run(p.b, p.group_off, p.shared, NG, kv_row_bytes(p.Hkv, D), code);
-  if (code || __syncthreads_or(status_bad(p.b.status))) {
+  if (code || __syncthreads_or(status_set(p.b.status))) {
     if (code) set_status(p.b.status, code);
     tc_fence_before();
     __syncthreads();

@@ -51,6 +51,7 @@ struct Pg {
   // Rows of a key tile: with 64 columns a tile of 64 rows is over before the next
   // barrier: 8 slots of 65,536 rows, 8 + 8 heads of 64, 171 us with 128 rows, 296 with 64.
   static constexpr int ROWS = D == 64 ? 128 : 64;
+  static constexpr int EXTRA = D == 256 ? 1 : 2;         // steps of an item beside its tiles
   static constexpr int WR = ROWS / 4, SG = ROWS / 16;    // rows a warp scores, groups of 16 rows
   static constexpr int SLOT = ROWS * D * 2;              // a tile of keys or of values
   static constexpr int NS = D == 256 ? 3 : D == 128 ? 6 : 5;  // slots of a team's ring
@@ -79,7 +80,7 @@ struct PagedTcParams {
   const __nv_bfloat16* q;
   const __nv_bfloat16* gate;
   __nv_bfloat16* out;
-  int64_t* first;  // [units + 1] each unit's first tile in the order of all (with shared prefixes)
+  int64_t* first;  // [units + 1] each unit's first step in the order of all (with shared prefixes)
   int4* cut;       // [CTAs] the item that a CTA's range starts within, where it is the item's first cut:
                    // slot, KV head, item of it, last CTA; -1: none
   float* rec;      // [2 * CTAs][heads][D + 4]
@@ -103,6 +104,11 @@ __device__ __forceinline__ int unit_tiles(const PagedTcParams& p, int u, int s, 
 
 constexpr int kNear = 16;
 
+// Ranges are cut in steps: an item's tiles, and before them what it costs beside them (its start, the teams' join, its
+// end: some 2,500 cycles, while a tile of 256 columns has 3,000 cycles of the memory's rate and a smaller one 1,500).
+// 96 ragged slots of 16 + 2 heads of 128: 94.9 us, 97.5 by tiles alone.
+__device__ __forceinline__ int steps_of(int tiles, int extra) { return tiles > 0 ? tiles + extra : 0; }
+
 template <int ROWS>
 __device__ __forceinline__ int unit_tiles(const PagedTcParams& p, int u) {
   const int s = u / p.v.Hkv;
@@ -113,18 +119,18 @@ __device__ __forceinline__ int unit_tiles(const PagedTcParams& p, int u) {
 struct PagedPiece {
   int s, h, L, m, k0, k1, nt;  // slot, KV head, the slot's length, item, tiles [k0, k1) of nt
 };
-template <int ROWS>
+template <int ROWS, int EXTRA>
 struct PagedWalk {
   int u, s, h;          // unit: slot and KV head
   int u0;               // the first unit of the range, and
   const int2* near;     // tiles and length of that one and the kNear - 1 after it
-  int off;  // tile within the unit, over its items (under 2^27: a slot has 2^30 rows at most, a unit 8 items)
+  int off;  // step within the unit, over its items (under 2^28: a slot has 2^30 rows at most, a unit 8 items)
   int64_t left;
   __device__ __forceinline__ bool next(const PagedTcParams& p, PagedPiece& x) {
     while (left > 0 && u < p.units) {
       const int2 n = u - u0 < kNear ? near[u - u0] : make_int2(unit_tiles<ROWS>(p, u), paged_len(p.v.b, s));
-      const int nt = n.x;
-      if (off >= nt * p.MT) {
+      const int steps = steps_of(n.x, EXTRA);
+      if (off >= steps * p.MT) {
         off = 0;
         u++;
         if (++h == p.v.Hkv) {
@@ -136,13 +142,14 @@ struct PagedWalk {
       x.s = s;
       x.h = h;
       x.L = n.y;
-      x.m = off < nt ? 0 : off / nt;
-      x.k0 = off - x.m * nt;
-      x.k1 = static_cast<int>(min(static_cast<int64_t>(nt), x.k0 + left));
-      x.nt = nt;
-      off += x.k1 - x.k0;
-      left -= x.k1 - x.k0;
-      return true;
+      x.m = off < steps ? 0 : off / steps;
+      const int from = off - x.m * steps, to = static_cast<int>(min(static_cast<int64_t>(steps), from + left));
+      off += to - from;
+      left -= to - from;
+      x.k0 = max(from - EXTRA, 0);
+      x.k1 = max(to - EXTRA, 0);
+      x.nt = n.x;
+      if (x.k0 < x.k1) return true;
     }
     return false;
   }
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   }
   pdl_wait();
   if (threadIdx.x == 0) {
-    lo.skip = status_bad(p.v.b.status) || (sb & 1023u) ? 1 : 0;
+    lo.skip = status_set(p.v.b.status) || (sb & 1023u) ? 1 : 0;
     if (sb & 1023u) set_status(p.v.b.status, TV_ERR_CUDA);
   }
   __syncthreads();
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       const int s = u / p.v.Hkv;
       last.y = paged_len(p.v.b, s);
       last.x = unit_tiles<C::ROWS>(p, u, s, last.y);
-      mine += static_cast<int64_t>(last.x) * p.MT;
+      mine += static_cast<int64_t>(steps_of(last.x, C::EXTRA)) * p.MT;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -249,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       int64_t at = base;
       for (int u = u0; u < u1; u++) {
         p.first[u] = at;
-        at += static_cast<int64_t>(unit_tiles<C::ROWS>(p, u)) * p.MT;
+        at += static_cast<int64_t>(steps_of(unit_tiles<C::ROWS>(p, u), C::EXTRA)) * p.MT;
       }
       if (threadIdx.x == 0) p.first[p.units] = total;
     }
@@ -260,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
         int64_t at = base;
         int u = u0;
         for (; per > 1; u++) {
-          const int64_t n = static_cast<int64_t>(unit_tiles<C::ROWS>(p, u)) * p.MT;
+          const int64_t n = static_cast<int64_t>(steps_of(unit_tiles<C::ROWS>(p, u), C::EXTRA)) * p.MT;
           if (a < at + n || u + 1 >= u1) break;
           at += n;
         }
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     }
     __syncthreads();
   }
-  PagedWalk<C::ROWS> walk{lo.u, lo.u / p.v.Hkv, lo.u % p.v.Hkv, lo.u, lo_near, lo.off, lo.left};
+  PagedWalk<C::ROWS, C::EXTRA> walk{lo.u, lo.u / p.v.Hkv, lo.u % p.v.Hkv, lo.u, lo_near, lo.off, lo.left};
   PagedPiece x;
   pdl_trigger();
   if (p.v.sel && warp < kConsumers / 32) {  // slots that see nothing: zeros
@@ -628,22 +635,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   if (!ok && lane == 0) set_status(p.v.b.status, TV_ERR_TIMEOUT);
 }
 
-// Joins the pieces of items that were cut, in order.  A CTA takes a row of an
-// item (blockIdx.x: the item's first cut), four columns a thread, the pieces dealt to
-// groups of threads that cover a row each, kJ loads in flight.  It is small enough
-// to wait beside the kernel before it.
-template <int D>
-__global__ void __launch_bounds__(256, 4) attn_paged_join_cuts_kernel(const __grid_constant__ PagedTcParams p) {
+// Joins pieces, in order: of items that were cut, or, where slots share prefixes, of every row with pieces (the prefix's,
+// then the slot's own).  A CTA takes a row (blockIdx.x: the item's first cut, or the slot's query head), four columns a
+// thread, the pieces dealt to groups of threads that cover a row each, kJ loads in flight.  It is
+// small enough to wait beside the kernel before it.
+template <int D, bool SHARED>
+__global__ void __launch_bounds__(256, 4) attn_paged_join_kernel(const __grid_constant__ PagedTcParams p, int grid, int extra) {
   constexpr int kJ = 6, LANES = D / 4, GROUPS = 256 / LANES;
   __shared__ float acc_s[GROUPS][D];
   __shared__ float2 ml_s[GROUPS];
   const int grp = threadIdx.x / LANES, col = threadIdx.x % LANES * 4;
+  const uint32_t line = static_cast<uint32_t>(p.item) * (D + 4);  // (offsets in 32 bits: all pieces are under 2^32 values)
   pdl_wait();
-  const int4 c = p.cut[blockIdx.x];
-  const int head = c.z * p.item + static_cast<int>(blockIdx.y);
-  if (c.x < 0 || head >= p.G || status_bad(p.v.b.status)) return;
-  const int c0 = static_cast<int>(blockIdx.x) - 1, n = c.w - c0 + 1;  // CTAs that hold a piece
-  const float* rec = p.rec + static_cast<size_t>(blockIdx.y) * (D + 4);
+  const bool bad = status_set(p.v.b.status);
+  int s, h, head, c0, n, np = 0;  // head: of the KV head's; CTAs c0 .. hold pieces, n with the np of a prefix
+  const float *own, *pre = nullptr;
+  uint32_t step = 0;
+  if constexpr (SHARED) {
+    s = static_cast<int>(blockIdx.x) / p.Hq;
+    h = (static_cast<int>(blockIdx.x) - s * p.Hq) / p.G;
+    head = static_cast<int>(blockIdx.x) - s * p.Hq - h * p.G;
+    const int u = s * p.v.Hkv + h, m = head / p.item;
+    const int64_t at = p.first[u], all = p.first[u + 1] - at, total = p.first[p.units];
+    const int4 g = p.info[s];
+    if (bad || all == 0) return;  // (an idle slot's row is left as it was)
+    const int nt = static_cast<int>(all / p.MT) - extra, ctas = ctas_for(total, grid);
+    const int64_t t0 = at + static_cast<int64_t>(m) * (nt + extra) + extra;
+    c0 = range_of(total, ctas, t0);
+    const int c1 = range_of(total, ctas, t0 + nt - 1), row = g.w * p.G + head;
+    np = g.z;
+    if (np == 0 && c0 == c1) return;  // written whole
+    n = np + c1 - c0 + 1;
+    step = static_cast<uint32_t>(g.y) * 128 * (D + 4);
+    if (np > 0) pre = p.rec_prefix + (static_cast<size_t>(g.x + h * np * g.y + row / 128) * 128 + row % 128) * (D + 4);
+    own = (c0 == c1 ? p.rec_item + (static_cast<size_t>(u) * p.MT + m) * line : p.rec + (static_cast<size_t>(c0) * 2 + 1) * line) +
+          static_cast<size_t>(head - m * p.item) * (D + 4);
+  } else {
+    const int4 c = p.cut[blockIdx.x];
+    s = c.x;
+    h = c.y;
+    head = c.z * p.item + static_cast<int>(blockIdx.y);
+    if (s < 0 || head >= p.G || bad) return;
+    c0 = static_cast<int>(blockIdx.x) - 1;
+    n = c.w - c0 + 1;
+    own = p.rec + (static_cast<size_t>(c0) * 2 + 1) * line + static_cast<size_t>(blockIdx.y) * (D + 4);
+  }
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
   for (int j0 = grp; j0 < n; j0 += kJ * GROUPS) {
@@ -651,8 +687,9 @@ __global__ void __launch_bounds__(256, 4) attn_paged_join_cuts_kernel(const __gr
     float2 ml[kJ];
 #pragma unroll
     for (int j = 0; j < kJ; j++) {
-      const int i = j0 + j * GROUPS;
-      const float* x = rec + (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.item * (D + 4);
+      // the prefix's pieces; the first CTA's second record; the others' first
+      const int i = j0 + j * GROUPS, k = i - np;
+      const float* x = SHARED && k < 0 ? pre + step * static_cast<uint32_t>(i) : own + (k == 0 ? 0u : (2u * static_cast<uint32_t>(k) - 1u) * line);
       o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       ml[j] = make_float2(-INFINITY, 0.f);
       if (i < n) {
@@ -691,7 +728,7 @@ __global__ void __launch_bounds__(256, 4) attn_paged_join_cuts_kernel(const __gr
     y0 = __fmaf_rn(f, acc_s[g][2 * t], y0);
     y1 = __fmaf_rn(f, acc_s[g][2 * t + 1], y1);
   }
-  const size_t at = (static_cast<size_t>(c.x) * p.Hq + c.y * p.G + head) * D + 2 * t;
+  const size_t at = (static_cast<size_t>(s) * p.Hq + h * p.G + head) * D + 2 * t;
   const float inv = __fdiv_rn(1.f, lt);
   y0 = __fmul_rn(y0, inv);
   y1 = __fmul_rn(y1, inv);
@@ -703,102 +740,6 @@ __global__ void __launch_bounds__(256, 4) attn_paged_join_cuts_kernel(const __gr
     y1 = gate_mul(y1, bf16_hi(g));
   }
   *reinterpret_cast<uint32_t*>(p.out + at) = pack_bf16x2(y0, y1);
-}
-
-// The same where slots share prefixes: the prefix's pieces, then the slot's own.  A
-// warp takes a part of a row, kJ pieces' loads in flight.
-template <int D>
-__global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_constant__ PagedTcParams p, int grid) {
-  constexpr int kJ = 12, CPW = D >= 128 ? 128 : 64, V = CPW / 32, PARTS = D / CPW;  // columns a warp and a lane
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  if (status_bad(p.v.b.status)) return;
-  const int64_t total = p.first[p.units];
-  const int ctas = ctas_for(total, grid);
-  const int64_t n = static_cast<int64_t>(p.units) * p.G * PARTS;
-  for (int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + warp; w < n; w += static_cast<int64_t>(gridDim.x) * 8) {
-    const int u = static_cast<int>(w / (p.G * PARTS)), r = static_cast<int>(w - static_cast<int64_t>(u) * p.G * PARTS);
-    const int head = r / PARTS, col = (r % PARTS) * CPW + lane * V;
-    const int s = u / p.v.Hkv, h = u - s * p.v.Hkv;
-    const int64_t all = p.first[u + 1] - p.first[u];
-    const int4 g = p.info[s];
-    const size_t at = (static_cast<size_t>(s) * p.Hq + h * p.G + head) * D + col;
-    float acc[V], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < V; e++) acc[e] = 0.f;
-    if (all == 0) continue;  // idle: left as it was
-    {
-      const int64_t nt = all / p.MT, t0 = p.first[u] + head / p.item * nt;
-      const int c0 = range_of(total, ctas, t0), c1 = range_of(total, ctas, t0 + nt - 1);
-      const float *rec = p.rec + static_cast<size_t>(head % p.item) * (D + 4), *pre = nullptr;
-      int np = 0;  // pieces of the shared prefix, which come first
-      size_t step = 0;
-      if (g.z > 0) {
-        const int row = g.w * p.G + head;
-        np = g.z;
-        step = static_cast<size_t>(g.y) * 128 * (D + 4);
-        pre = p.rec_prefix + (static_cast<size_t>(g.x + h * np * g.y + row / 128) * 128 + row % 128) * (D + 4);
-      } else if (c0 == c1) {
-        continue;  // written whole
-      }
-      const int n_rec = np + c1 - c0 + 1;
-      for (int j0 = 0; j0 < n_rec; j0 += kJ) {
-        float o[kJ][V];
-        float2 ml[kJ];
-#pragma unroll
-        for (int j = 0; j < kJ; j++) {
-          const int i = j0 + j, c = c0 + i - np;
-          const float* x = i < np ? pre + step * i
-                           : c0 == c1 ? p.rec_item + ((static_cast<size_t>(u) * p.MT + head / p.item) * p.item + head % p.item) * (D + 4)
-                                      : rec + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * p.item * (D + 4);
-          ml[j] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-          for (int e = 0; e < V; e++) o[j][e] = 0.f;
-          if (i < n_rec) {
-            ml[j] = *reinterpret_cast<const float2*>(x + D);
-#pragma unroll
-            for (int e = 0; e < V; e += 2) {
-              const float2 y = *reinterpret_cast<const float2*>(x + col + e);
-              o[j][e] = y.x;
-              o[j][e + 1] = y.y;
-            }
-          }
-        }
-        float mn = m;
-#pragma unroll
-        for (int j = 0; j < kJ; j++) mn = fmaxf(mn, ml[j].x);
-        const float a = m == -INFINITY ? 0.f : exp2f(__fsub_rn(m, mn));
-        l = __fmul_rn(l, a);
-#pragma unroll
-        for (int e = 0; e < V; e++) acc[e] = __fmul_rn(acc[e], a);
-#pragma unroll
-        for (int j = 0; j < kJ; j++) {
-          if (ml[j].y == 0.f) continue;  // nothing of weight in the piece (or no piece)
-          const float f = exp2f(__fsub_rn(ml[j].x, mn));
-          l = __fmaf_rn(f, ml[j].y, l);
-#pragma unroll
-          for (int e = 0; e < V; e++) acc[e] = __fmaf_rn(f, o[j][e], acc[e]);
-        }
-        m = mn;
-      }
-    }
-    const float inv = __fdiv_rn(1.f, l);
-    uint32_t y[V / 2];
-#pragma unroll
-    for (int e = 0; e < V; e += 2) {
-      float a = __fmul_rn(acc[e], inv), b = __fmul_rn(acc[e + 1], inv);
-      if (m == -INFINITY) {
-        a = b = 0.f;  // no row seen
-      } else if (p.gate) {
-        const uint32_t g = *reinterpret_cast<const uint32_t*>(p.gate + at + e);
-        a = gate_mul(a, bf16_lo(g));
-        b = gate_mul(b, bf16_hi(g));
-      }
-      y[e / 2] = pack_bf16x2(a, b);
-    }
-#pragma unroll
-    for (int e = 0; e < V / 2; e++) *reinterpret_cast<uint32_t*>(p.out + at + 2 * e) = y[e];
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -880,13 +821,8 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
     x.c = p.c;
     if (!paged_prefix_launch(x, D, st)) return TV_ERR_CUDA;
   }
-  if (may_share) {
-    const int64_t warps = static_cast<int64_t>(p.units) * p.G * (D > 128 ? D / 128 : 1);
-    const int join = static_cast<int>(warps + 7 < static_cast<int64_t>(16) * grid ? (warps + 7) / 8 : 2 * grid);
-    launch_k(true, attn_paged_join_kernel<D>, dim3(join), dim3(256), 0, st, p, grid);
-  } else {
-    launch_k(true, attn_paged_join_cuts_kernel<D>, dim3(grid, p.G < p.item ? p.G : p.item), dim3(256), 0, st, p);
-  }
+  if (may_share) launch_k(true, attn_paged_join_kernel<D, true>, dim3(a.batch->n_seq * l->Hq), dim3(256), 0, st, p, grid, C::EXTRA);
+  else launch_k(true, attn_paged_join_kernel<D, false>, dim3(grid, p.G < p.item ? p.G : p.item), dim3(256), 0, st, p, grid, C::EXTRA);
   return launch_status();
 }
 

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 5 : 4) norm_rope_kernel(
   };
   fetch(h_first, raw);
   // the row's sequence, position and (prompt) cache row
-  const bool bad = status_bad(p.pr.status);
+  const bool bad = PAGED ? status_set(p.pr.status) : status_bad(p.pr.status);
   int s, pos;
   if constexpr (PAGED) {
     if (bad) return;

@@ -19,6 +19,10 @@ struct PagedSeqs {
   int shift;  // log2 of a page's rows
 };
 
+// Whether a call before has set the word.  A plain load, which L1 serves after an SM's first: what
+// earlier kernels wrote is visible behind the wait for them, and read past L1 by every warp of a
+// large grid the one line costs a microsecond or more (the join of cut items 4.3 us and 3.4).
+__device__ __forceinline__ bool status_set(const int32_t* st) { return *st != 0; }
 // Rows a slot holds before this step, -1 where it is idle or its length is not allowed.
 __device__ __forceinline__ int paged_len(const PagedSeqs& b, int s) {
   const int L = b.len[s];

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(128) paged_bounds_kernel(const __grid_constant
   __shared__ float lo_s[STEP][D], hi_s[STEP][D];
   __shared__ float top_s[4];
   pdl_wait();
-  if (status_bad(p.b.status)) return;
+  if (status_set(p.b.status)) return;
   const int s = blockIdx.y, h = blockIdx.z;
   const int L = paged_len(p.b, s);
   if (L < 0) return;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kSelect, 2) paged_select_kernel(const __grid_c
   // that some of them meet first keeps the first CTA from writing, no more.)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
-  const bool bad = status_bad(p.b.status);
+  const bool bad = status_set(p.b.status);
   const int u = blockIdx.y, s = u / p.Hkv, h = u - s * p.Hkv;
   const int L = paged_len(p.b, s);
   const int nb = (L >> p.b.shift) + 1;
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kSelect, 2) paged_select_kernel(const __grid_c
 __global__ void paged_advance_kernel(int32_t* len, const int32_t* row_off, PagedSeqs b, int n_total, int n_max) {
   const int s = blockIdx.x * blockDim.x + threadIdx.x;
   pdl_wait();
-  if (s >= b.n_seq || status_bad(b.status)) return;
+  if (s >= b.n_seq || status_set(b.status)) return;
   const int L = paged_len(b, s);
   int n = 1;
   if (row_off) {
