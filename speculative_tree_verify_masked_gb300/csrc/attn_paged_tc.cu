@@ -80,7 +80,7 @@ struct PagedTcParams {
   const __nv_bfloat16* q;
   const __nv_bfloat16* gate;
   __nv_bfloat16* out;
-  int64_t* first;  // [units + 1] each unit's first step in the order of all (with shared prefixes)
+  int2* span;      // [items] first and last CTA of an item's tiles (with shared prefixes; 0, -1: none)
   int4* cut;       // [CTAs] the item that a CTA's range starts within, where it is the item's first cut:
                    // slot, KV head, item of it, last CTA; -1: none
   float* rec;      // [2 * CTAs][heads][D + 4]
@@ -255,10 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     if (me == 0 && p.start) {  // for the join
       int64_t at = base;
       for (int u = u0; u < u1; u++) {
-        p.first[u] = at;
-        at += static_cast<int64_t>(steps_of(unit_tiles<C::ROWS>(p, u), C::EXTRA)) * p.MT;
+        const int tiles = per == 1 ? last.x : unit_tiles<C::ROWS>(p, u), steps = steps_of(tiles, C::EXTRA);
+        for (int m = 0; m < p.MT; m++, at += steps)
+          p.span[u * p.MT + m] = tiles > 0 ? make_int2(range_of(total, ctas, at + C::EXTRA), range_of(total, ctas, at + steps - 1)) : make_int2(0, -1);
       }
-      if (threadIdx.x == 0) p.first[p.units] = total;
     }
     if (threadIdx.x == 0) lo.ctas = ctas;
     if (me < ctas) {
@@ -637,11 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
 
 // Joins pieces, in order: of items that were cut, or, where slots share prefixes, of every row with pieces (the prefix's,
 // then the slot's own).  A CTA takes a row (blockIdx.x: the item's first cut, or the slot's query head), four columns a
-// thread, the pieces dealt to groups of threads that cover a row each, kJ loads in flight.  It is
-// small enough to wait beside the kernel before it.
+// thread, the pieces dealt to groups of threads that cover a row each, kJ loads in flight.  For cut
+// items it is small enough to wait beside the kernel before it; where slots share prefixes there are many rows with some
+// dozen pieces, and more CTAs serve better than more loads each.
 template <int D, bool SHARED>
-__global__ void __launch_bounds__(256, 4) attn_paged_join_kernel(const __grid_constant__ PagedTcParams p, int grid, int extra) {
-  constexpr int kJ = 6, LANES = D / 4, GROUPS = 256 / LANES;
+__global__ void __launch_bounds__(256, SHARED ? 6 : 4) attn_paged_join_kernel(const __grid_constant__ PagedTcParams p) {
+  constexpr int kJ = SHARED ? 3 : 6, LANES = D / 4, GROUPS = 256 / LANES;
   __shared__ float acc_s[GROUPS][D];
   __shared__ float2 ml_s[GROUPS];
   const int grp = threadIdx.x / LANES, col = threadIdx.x % LANES * 4;
@@ -652,17 +653,15 @@ __global__ void __launch_bounds__(256, 4) attn_paged_join_kernel(const __grid_co
   const float *own, *pre = nullptr;
   uint32_t step = 0;
   if constexpr (SHARED) {
-    s = static_cast<int>(blockIdx.x) / p.Hq;
-    h = (static_cast<int>(blockIdx.x) - s * p.Hq) / p.G;
-    head = static_cast<int>(blockIdx.x) - s * p.Hq - h * p.G;
-    const int u = s * p.v.Hkv + h, m = head / p.item;
-    const int64_t at = p.first[u], all = p.first[u + 1] - at, total = p.first[p.units];
+    s = static_cast<int>(blockIdx.y);
+    h = static_cast<int>(blockIdx.x) / p.G;
+    head = static_cast<int>(blockIdx.x) - h * p.G;
+    const int u = s * p.v.Hkv + h, m = p.MT > 1 ? head / p.item : 0;
+    const int2 span = p.span[u * p.MT + m];
     const int4 g = p.info[s];
-    if (bad || all == 0) return;  // (an idle slot's row is left as it was)
-    const int nt = static_cast<int>(all / p.MT) - extra, ctas = ctas_for(total, grid);
-    const int64_t t0 = at + static_cast<int64_t>(m) * (nt + extra) + extra;
-    c0 = range_of(total, ctas, t0);
-    const int c1 = range_of(total, ctas, t0 + nt - 1), row = g.w * p.G + head;
+    if (bad || span.y < 0) return;  // (an idle slot's row is left as it was)
+    c0 = span.x;
+    const int c1 = span.y, row = g.w * p.G + head;
     np = g.z;
     if (np == 0 && c0 == c1) return;  // written whole
     n = np + c1 - c0 + 1;
@@ -761,7 +760,7 @@ static int item_heads(const tv_paged_layer* l) { return l->Hq / l->Hkv <= 8 ? 8 
 
 // A call's scratch, in bytes from its start.
 struct PagedSpace {
-  size_t cut, rec, first, rec_item, rec_prefix, info, start, all;
+  size_t cut, rec, span, rec_item, rec_prefix, info, start, all;
 };
 static PagedSpace space_of(const tv_paged_layer* l, const tv_paged* b, const tv_paged_groups* g) {
   const size_t line = static_cast<size_t>(l->D + 4) * 4, units = static_cast<size_t>(b->n_seq) * l->Hkv;
@@ -777,7 +776,7 @@ static PagedSpace space_of(const tv_paged_layer* l, const tv_paged* b, const tv_
   s.cut = take(static_cast<size_t>(num_sms()) * 16);
   s.rec = take(static_cast<size_t>(2) * num_sms() * item * line);
   if (g) {
-    s.first = take((units + 1) * 8);
+    s.span = take(items * 8);
     s.rec_item = take(items * item * line);
     s.rec_prefix = take(static_cast<size_t>(paged_prefix_slots(l, b, g->n_group)) * 128 * line);
     s.info = take(static_cast<size_t>(b->n_seq) * 16);
@@ -821,8 +820,8 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
     x.c = p.c;
     if (!paged_prefix_launch(x, D, st)) return TV_ERR_CUDA;
   }
-  if (may_share) launch_k(true, attn_paged_join_kernel<D, true>, dim3(a.batch->n_seq * l->Hq), dim3(256), 0, st, p, grid, C::EXTRA);
-  else launch_k(true, attn_paged_join_kernel<D, false>, dim3(grid, p.G < p.item ? p.G : p.item), dim3(256), 0, st, p, grid, C::EXTRA);
+  if (may_share) launch_k(true, attn_paged_join_kernel<D, true>, dim3(l->Hq, a.batch->n_seq), dim3(256), 0, st, p);
+  else launch_k(true, attn_paged_join_kernel<D, false>, dim3(grid, p.G < p.item ? p.G : p.item), dim3(256), 0, st, p);
   return launch_status();
 }
 
@@ -846,7 +845,7 @@ tv_status paged_attn_tc_launch(const PagedAttnCall& a, cudaStream_t st) {
   }
   // (where no lengths within the bound could save enough, the groups are only checked)
   if (a.groups && (a.batch->n_seq - 1) * static_cast<int64_t>(a.batch->max_len) * kv_row_bytes(l->Hkv, l->D) >= kSharedBytes) {
-    p.first = reinterpret_cast<int64_t*>(ws + x.first);
+    p.span = reinterpret_cast<int2*>(ws + x.span);
     p.rec_item = reinterpret_cast<float*>(ws + x.rec_item);
     p.rec_prefix = reinterpret_cast<const float*>(ws + x.rec_prefix);
     p.info = reinterpret_cast<const int4*>(ws + x.info);
