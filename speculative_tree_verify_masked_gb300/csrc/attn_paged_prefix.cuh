@@ -22,9 +22,9 @@ struct PagedPrefixParams {
 };
 // What sharing has to save to pay for its launch, its start and the longer join: so many bytes of keys
 // and values that members would read again (from L2, mostly).  24 + 4 heads of 256, us a call shared
-// and slot by slot: 8 members of 16,384 rows (470 MB saved) 33.4 and 43.9, 4 (201 MB) 30.3 and 28.4; of 4,096 rows
-// 16 members (252 MB) 26.2 and 28.9, 8 (117 MB) 24.8 and 21.0; 2 of 65,536 (268 MB) 67.3 and 67.6.  16 + 2
-// heads of 128: 4 of 65,536 (201 MB) 39.9 and 38.8, 8 67.6 and 41.3.
+// and slot by slot: 8 members of 16,384 rows (470 MB saved) 32.5 and 42.8, 4 (201 MB) 30.3 and 28.4; of 4,096 rows
+// 16 members (252 MB) 26.0 and 28.6, 8 (117 MB) 24.8 and 21.0; 2 of 65,536 (268 MB) 67.2 and 67.2.  16 + 2
+// heads of 128: 8 of 65,536 (470 MB) 32.8 and 67.7, 4 (201 MB) 39.9 and 38.8.
 constexpr int64_t kSharedBytes = 200 << 20;
 // Bytes of a row's keys and values in bf16.
 __host__ __device__ inline int64_t kv_row_bytes(int Hkv, int D) { return static_cast<int64_t>(Hkv) * D * 4; }
