@@ -7,8 +7,9 @@
 //   score = 2^e max_g sum_d (u > 0 ? u code[1] : u code[0])
 //         = 2^e max_g (u+ . code[1] + u- . code[0])
 // Codes are whole numbers within 127, so a sum is exact whatever its order (under
-// 2^22), and so is its product with 2^e: no rounding decides between two pages.
-// (2^f is the same for all pages of a choice and is left out.)
+// 2^22), and so is its product with 2^(e - 24), which fp32 holds for every e from -100 to
+// 127: no rounding decides between two pages.  (2^f and 2^24 are the same for all
+// pages of a choice and are left out.)
 //
 // Scores run on 16 x 8 x 16 tensor-core tiles, sixteen pages by eight query heads,
 // with codes and queries as fp16 and sums in fp32, which hold these whole numbers exactly
@@ -187,7 +188,7 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) { w
 constexpr int kSelect = 256;        // threads of a CTA: each warp scores sixteen pages at a time
 constexpr int kSelectKeys = 16384;  // pages whose keys fit in shared memory
 
-// A rising key for a score (no NaN).
+// A rising key for a score (no NaN, no -0).
 __device__ __forceinline__ uint32_t rising(float x) {
   const uint32_t b = __float_as_uint(x);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kSelect, 2) paged_select_kernel(const __grid_c
         const int r = lane & 1, at = r * 8 + (lane >> 2), j = tile * 16 + at;
         const int ex = __shfl_sync(0xffffffffu, e, i * 16 + at);
         if ((lane & 2) == 0 && j < n) {
-          uint32_t key = rising(ex >= 128 ? INFINITY : ldexpf(best[r], ex));
+          uint32_t key = rising(ex >= 128 ? INFINITY : ldexpf(__fadd_rn(best[r], 0.f), ex - 24));
           if (kept) {  // (later heads' scores of a page are this lane's own again)
             if (g0 > 0) key = max(key, load_first(keys_at + j * 4));
             store_first(keys_at + j * 4, key);

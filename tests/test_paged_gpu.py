@@ -305,6 +305,23 @@ def test_select_largest_sums():
         assert sel[0, g].tolist() == _want(p, code, exp, 1, 2, 20, 0, g) and int(count[0, g]) == 20
 
 
+@pytest.mark.parametrize("exps", [range(100, 128), range(-100, -72)], ids=["large", "small"])
+def test_select_exponents_at_their_ends(exps):
+    """Scores whose sizes leave fp32 are still told apart, and those of 0 are equal, whatever their signs of zero."""
+    p = Pools([64 * 16 + 3], 16, (24, 4, 256), seed=2, fill=None)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    code = torch.randint(-127, 128, (p.n_pages, 4, 2, 256), generator=gen, device="cuda").sort(2).values.to(torch.int8)
+    exp = torch.randint(exps[0], exps[-1] + 1, (p.n_pages, 4), generator=gen, device="cuda", dtype=torch.int32)
+    code[torch.arange(0, p.n_pages, 5, device="cuda")] = 0
+    for sign in (1.0, -1.0):
+        p.q.copy_(sign * p.q.abs())
+        for n_sel in (9, 30, 60):
+            sel, count = _select(p, code, exp, 1, 2, n_sel)
+            for g in range(4):
+                assert sel[0, g].tolist() == _want(p, code, exp, 1, 2, n_sel, 0, g) and int(count[0, g]) == n_sel
+    assert p.status() == 0
+
+
 @pytest.mark.parametrize("lens", [[200000, 135008], [16 * 16385 + 30, 400000]])
 @pytest.mark.parametrize("Hq", [8, 64])
 def test_select_long(lens, Hq):
