@@ -119,7 +119,6 @@ __global__ void __launch_bounds__(32 * kCudaWarps, 1) attn_paged_cuda_kernel(con
   for (int w = 0; w < kCudaWarps; w++) mn = fmaxf(mn, m_s[w]);
 #pragma unroll
   for (int w = 0; w < kCudaWarps; w++) {
-    if (l_s[w] == 0.f) continue;
     const float f = exp2f(__fsub_rn(m_s[w], mn == -INFINITY ? 0.f : mn));
     lt = __fmaf_rn(f, l_s[w], lt);
     o = __fmaf_rn(f, acc_s[w][threadIdx.x], o);

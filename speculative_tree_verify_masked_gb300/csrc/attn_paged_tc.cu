@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(256, SHARED ? 6 : 4) attn_paged_join_kernel(co
     acc = make_float4(__fmul_rn(acc.x, a), __fmul_rn(acc.y, a), __fmul_rn(acc.z, a), __fmul_rn(acc.w, a));
 #pragma unroll
     for (int j = 0; j < kJ; j++) {
-      if (ml[j].y == 0.f) continue;  // nothing of weight in the piece (or no piece)
+      if (ml[j].x == -INFINITY) continue;  // no row seen in the piece (or no piece)
       const float f = exp2f(__fsub_rn(ml[j].x, mn));
       l = __fmaf_rn(f, ml[j].y, l);
       acc = make_float4(__fmaf_rn(f, o[j].x, acc.x), __fmaf_rn(f, o[j].y, acc.y), __fmaf_rn(f, o[j].z, acc.z), __fmaf_rn(f, o[j].w, acc.w));
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(256, SHARED ? 6 : 4) attn_paged_join_kernel(co
   for (int g = 0; g < GROUPS; g++) mn = fmaxf(mn, ml_s[g].x);
 #pragma unroll
   for (int g = 0; g < GROUPS; g++) {
-    if (ml_s[g].y == 0.f) continue;
+    if (ml_s[g].x == -INFINITY) continue;
     const float f = exp2f(__fsub_rn(ml_s[g].x, mn));
     lt = __fmaf_rn(f, ml_s[g].y, lt);
     y0 = __fmaf_rn(f, acc_s[g][2 * t], y0);

@@ -396,6 +396,22 @@ def test_scores_of_minus_infinity():
     assert p.status() == 0
 
 
+@pytest.mark.parametrize("dtype,heads,lens", [(F32, (4, 2, 64), [300, 90]), (BF, (24, 4, 256), [20000, 70]), (BF, (16, 2, 128), [9000, 500])])
+def test_infinite_values_without_weight(dtype, heads, lens):
+    """An infinite value whose score is -inf is 0 times infinity wherever it lies: among scores of -inf alone, too."""
+    for slot, first, n in ((0, 0, 8), (0, lens[0] // 8, lens[0] // 4), (1, 40, 8)):
+        p = Pools(lens, 32, heads, dtype, seed=9)
+        p.q[:] = p.q.abs() + 0.1
+        for t in range(first, first + n):
+            p.K[p.rows[slot][t // 32], 1, t % 32] = -float("inf")
+        pg, r = p.rows[slot][(first + n // 2) // 32], (first + n // 2) % 32
+        p.V[pg, 1, r, 3] = float("inf")
+        got, G = p.attn(), heads[0] // heads[1]
+        assert got[slot, G:2 * G, 3].isnan().all()
+        got[slot, G:2 * G, 3] = 0
+        assert got.isfinite().all() and p.status() == 0
+
+
 def test_far_pages():
     """Offsets in the pools past 2^31 bytes and elements."""
     Hkv, page, D = 4, 128, 256
