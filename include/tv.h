@@ -551,7 +551,11 @@ tv_status tv_gdn_prompt_front(const tv_gdn_front_layer* layer, const tv_prompt* 
  * An infinity or NaN among the rows that a slot sees reaches what the formulas
  * let it reach; rows that it does not see (behind len[s], in pages of others)
  * may hold anything.  (A score of -inf has a weight of 0: an infinite value
- * beside it gives NaN, as 0 times infinity does.) */
+ * beside it gives NaN, as 0 times infinity does.)
+ *
+ * What a call writes, its workspace too, shares memory with nothing else that it
+ * reads or writes, the table, the lengths and the word among them, except where
+ * it says so (TV_ERR_ARG). */
 #define TV_MAX_PAGED_SEQ 1024 /* sequences (slots) of one paged call; n_seq * Hkv < 2^16 (TV_ERR_SHAPE) */
 
 typedef struct {
@@ -592,7 +596,8 @@ typedef struct {
 /* tv_attn_prompt_front into pages: norms and rotation of row i of sequence s
  * at position len[s] + i, queries to q, keys (normalised, rotated) and values
  * (bit copies) to the sequence's rows len[s] + i.
- *  rows   or NULL; q_raw, q [n][Hq][D], k_raw, v [n][Hkv][D], n = rows->n_total or n_seq
+ *  rows   or NULL; q_raw, q [n][Hq][D], k_raw, v [n][Hkv][D], n = rows->n_total or n_seq; q may
+ *         be q_raw
  *  other arguments and the rows' bits as there.
  * The pages a call writes must each belong to one sequence. */
 tv_status tv_paged_append(const tv_paged_layer* layer, const tv_paged* batch, const tv_paged_rows* rows,
@@ -618,8 +623,7 @@ size_t tv_paged_attn_workspace_bytes(const tv_paged_layer* layer, const tv_paged
  *         those); the result is the same up to rounding.  fp32 layers read every
  *         slot's own.  Offsets or lengths that do not hold what is said above set
  *         TV_ERR_ROWS (bf16 layers).
- *  q, out [n_seq][Hq][D]; gate the same or NULL (may be out); out shares memory with nothing
- *         else that is read (TV_ERR_ARG)
+ *  q, out [n_seq][Hq][D]; gate the same or NULL (may be out)
  *  scale  score scale > 0
  *  workspace as in tv_attn_prompt. */
 tv_status tv_paged_attn(const tv_paged_layer* layer, const tv_paged* batch, const tv_paged_groups* groups, const void* q,
@@ -648,7 +652,7 @@ tv_status tv_paged_bounds(const tv_paged_layer* layer, const tv_paged* batch, co
  *  first >= 0, last >= 1, first + last <= n_sel <= 4096
  *  workspace as in tv_attn_prompt (none is needed up to 16,384 pages a slot)
  *  sel    device [n_seq][Hkv][n_sel]: page indices (columns of the table), rising, -1 behind the last
- *  count  device [n_seq][Hkv]; both share memory with nothing that is read (TV_ERR_ARG) */
+ *  count  device [n_seq][Hkv] */
 size_t tv_paged_select_workspace_bytes(const tv_paged_layer* layer, const tv_paged* batch);
 tv_status tv_paged_select(const tv_paged_layer* layer, const tv_paged* batch, const int8_t* code, const int32_t* exp,
                           int32_t first, int32_t last, int32_t n_sel, const void* q, int32_t* sel, int32_t* count,

@@ -9,6 +9,8 @@
 // in flight, and keep a running maximum and sum each, which are joined at the end.  A
 // warp looks up the pages of 32 runs at once.  Bound by the walk over the rows of the
 // longest slot (sized for the small model of the tests).
+#include <utility>
+
 #include "attn_paged.cuh"
 
 namespace tv {
@@ -163,9 +165,19 @@ static tv_status paged_attn(const PagedAttnCall& a, cudaStream_t st) {
   const size_t pool = bytes_of(static_cast<int64_t>(l->n_pages) * l->Hkv * l->page, l->D, l->dtype);
   const size_t ns = static_cast<size_t>(a.batch->n_seq) * l->Hkv * 4;
   if (share_memory(a.out, n, l->K, pool) || share_memory(a.out, n, l->V, pool) || share_memory(a.out, n, a.sel, ns * a.n_sel) ||
-      share_memory(a.out, n, a.count, ns))
+      share_memory(a.out, n, a.count, ns) || shares_batch(a.out, n, a.batch))
     return TV_ERR_ARG;
-  return l->dtype == TV_BF16 ? paged_attn_tc_launch(a, st) : launch_cuda(a, st);
+  if (const tv_paged_groups* g = a.groups)
+    if (share_memory(a.out, n, g->group_off, static_cast<size_t>(g->n_group + 1) * 4) ||
+        share_memory(a.out, n, g->shared, static_cast<size_t>(g->n_group) * 4))
+      return TV_ERR_ARG;
+  if (l->dtype != TV_BF16) return launch_cuda(a, st);
+  const size_t need = paged_attn_ws_bytes(l, a.batch, a.groups);
+  if (!a.ws || a.ws_bytes < need) return TV_ERR_WORKSPACE;
+  for (const auto& x : {std::pair<const void*, size_t>(a.q, n), {a.gate, n}, {a.out, n}, {l->K, pool}, {l->V, pool}, {a.sel, ns * a.n_sel}, {a.count, ns}})
+    if (share_memory(a.ws, need, x.first, x.second)) return TV_ERR_ARG;
+  if (shares_batch(a.ws, need, a.batch)) return TV_ERR_ARG;
+  return paged_attn_tc_launch(a, st);
 }
 
 }  // namespace tv

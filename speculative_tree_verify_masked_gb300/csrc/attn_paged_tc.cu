@@ -827,7 +827,6 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
 
 tv_status paged_attn_tc_launch(const PagedAttnCall& a, cudaStream_t st) {
   const tv_paged_layer* l = a.layer;
-  if (!a.ws || a.ws_bytes < paged_attn_ws_bytes(l, a.batch, a.groups)) return TV_ERR_WORKSPACE;
   PagedTcParams p;
   memset(&p, 0, sizeof(p));
   p.v = PagedView{paged_seqs(l, a.batch), a.sel, a.count, a.n_sel, l->Hkv};

@@ -504,7 +504,7 @@ extern "C" tv_status tv_paged_append(const tv_paged_layer* l, const tv_paged* b,
     if (share_memory(x, pool, q_raw, nq) || share_memory(x, pool, q, nq) || share_memory(x, pool, k_raw, nk) ||
         share_memory(x, pool, v, nk))
       return TV_ERR_ARG;
-  if (share_memory(l->K, pool, l->V, pool)) return TV_ERR_ARG;
+  if (share_memory(l->K, pool, l->V, pool) || shares_batch(l->K, pool, b) || shares_batch(l->V, pool, b) || shares_batch(q, nq, b)) return TV_ERR_ARG;
   NormRopeParams p{};
   p.form = rows ? 4 : 3;
   p.pg = paged_seqs(l, b);

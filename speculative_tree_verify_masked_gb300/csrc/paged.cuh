@@ -91,5 +91,10 @@ inline bool share_memory(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && x < y + nb && y < x + na;
 }
+// Whether what a call writes shares memory with the table, the lengths or the status word.
+inline bool shares_batch(const void* a, size_t n, const tv_paged* b) {
+  return share_memory(a, n, b->table, static_cast<size_t>(b->n_seq) * b->cols * 4) ||
+         share_memory(a, n, b->len, static_cast<size_t>(b->n_seq) * 4) || share_memory(a, n, b->status, 4);
+}
 
 }  // namespace tv

@@ -26,6 +26,7 @@
 // into the first one's shared memory, which then chooses.
 #include <climits>
 #include <cuda_fp16.h>
+#include <utility>
 
 #include "paged.cuh"
 #include "prompt.cuh"
@@ -568,7 +569,7 @@ extern "C" tv_status tv_paged_bounds(const tv_paged_layer* l, const tv_paged* b,
   if (!aligned16(code) || !aligned16(exp)) return TV_ERR_ALIGN;
   const size_t heads = static_cast<size_t>(l->n_pages) * l->Hkv, pool = bytes_of(static_cast<int64_t>(heads) * l->page, l->D, l->dtype);
   if (share_memory(code, heads * 2 * l->D, l->K, pool) || share_memory(exp, heads * 4, l->K, pool) ||
-      share_memory(code, heads * 2 * l->D, exp, heads * 4))
+      share_memory(code, heads * 2 * l->D, exp, heads * 4) || shares_batch(code, heads * 2 * l->D, b) || shares_batch(exp, heads * 4, b))
     return TV_ERR_ARG;
   if (l->Hkv > 65535) return TV_ERR_SHAPE;
   BoundsParams p{};
@@ -616,11 +617,15 @@ extern "C" tv_status tv_paged_select(const tv_paged_layer* l, const tv_paged* b,
   if (share_memory(sel, units_b * n_sel * 4, count, units_b * 4)) return TV_ERR_ARG;
   for (const auto& o : {std::pair<const void*, size_t>(sel, units_b * n_sel * 4), std::pair<const void*, size_t>(count, units_b * 4)})
     if (share_memory(o.first, o.second, code, heads * 2 * l->D) || share_memory(o.first, o.second, exp, heads * 4) ||
-        share_memory(o.first, o.second, q, nq) || share_memory(o.first, o.second, b->table, static_cast<size_t>(b->n_seq) * b->cols * 4) ||
-        share_memory(o.first, o.second, b->len, static_cast<size_t>(b->n_seq) * 4))
+        share_memory(o.first, o.second, q, nq) || shares_batch(o.first, o.second, b))
       return TV_ERR_ARG;
   const size_t need = tv_paged_select_workspace_bytes(l, b);
   if (need > 0 && (!ws || ws_bytes < need)) return TV_ERR_WORKSPACE;
+  if (need > 0) {
+    for (const auto& x : {std::pair<const void*, size_t>(sel, units_b * n_sel * 4), {count, units_b * 4}, {code, heads * 2 * l->D}, {exp, heads * 4}, {q, nq}})
+      if (share_memory(ws, need, x.first, x.second)) return TV_ERR_ARG;
+    if (shares_batch(ws, need, b)) return TV_ERR_ARG;
+  }
   SelectParams p{};
   p.b = paged_seqs(l, b);
   p.q = q;

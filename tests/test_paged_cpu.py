@@ -189,6 +189,30 @@ def test_advance_refused(L):
     assert adv(batch(len_=0x2004), len_=0x2004) == ALIGN and adv(r=rows(off=0)) == ARG
 
 
+TABLE, LEN, WORD = 0x1000, 0x2000, 0x3000
+
+
+@pytest.mark.parametrize("where", [TABLE, TABLE + 8 * 16 * 4 - 16, LEN, LEN + 16, WORD])
+def test_writes_into_the_batch_refused(L, where):
+    for call in (attn, selected):
+        assert call(L, out=where) == ARG and call(L, ws=where) == ARG
+    assert append(L, q=where) == ARG and append(L, l=layer(k=where)) == ARG and append(L, l=layer(v=where)) == ARG
+    assert bounds(L, code=where) == ARG and bounds(L, exp=where) == ARG
+    assert select(L, sel=where) == ARG and select(L, cnt=where) == ARG
+
+
+def test_workspaces_apart(L):
+    need = L.tv_paged_attn_workspace_bytes(ref(layer()), ref(batch()), None)
+    n, pool = 8 * 24 * 256 * 2, 100 * 4 * 64 * 256 * 2
+    for ws in (Q, Q + n - 16, OUT - need + 16, K + pool - 16, V):
+        assert attn(L, ws=ws) == ARG and selected(L, ws=ws) == ARG
+    assert attn(L, gate=FAR + 16) == ARG and selected(L, sel=FAR) == ARG and selected(L, cnt=FAR + need // 16 * 16 - 16) == ARG
+    assert attn(L, g=groups(), out=0x5000) == ARG and attn(L, g=groups(shared=1 << 20), out=(1 << 20) - n + 16) == ARG
+    far = dict(l=layer(page=16), b=batch(cols=20000, max_len=16384 * 16), sel=9 << 30, cnt=10 << 30)
+    for ws in (9 << 30, 10 << 30, K_RAW, V_RAW, Q + n - 16, TABLE):
+        assert select(L, ws=ws, **far) == ARG
+
+
 def test_bindings_refuse_host_memory():
     k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
     b = B.PagedBatch(torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), 32)
