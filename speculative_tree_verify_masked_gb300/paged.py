@@ -48,7 +48,7 @@ class PagedCaches:
         self.users = [0] * n_pages
         self.pages = [[] for _ in range(n_slots)]  # of each slot, in order
         self.lens = [-1] * n_slots                 # the lengths, as the host knows them
-        self.ws = None
+        self.ws, self.outgrown = None, []
         if sparse:
             n_sel = sparse[0]
             self.code = [torch.zeros((n_pages, Hkv, 2, D), dtype=torch.int8, device=device) for _ in range(n_layers)]
@@ -62,10 +62,12 @@ class PagedCaches:
 
     def _space(self, need: int):
         if self.ws is None or self.ws.numel() < need:
+            if self.ws is not None:
+                self.outgrown.append(self.ws)  # (steps that are captured already go on in it)
             self.ws = torch.empty(max(16, need), dtype=torch.uint8, device=self.table.device)
 
     def groups(self, sizes, shared) -> B.PagedGroups:
-        """Groups for decode(); the workspace then holds what they need (make them before a capture)."""
+        """Groups for decode(); the workspace then holds what they need (make them before the capture of steps that take them)."""
         g = B.PagedGroups(sizes, shared, device=self.table.device)
         self._space(B.tv_paged_attn_workspace_bytes(self.layers[0], self.batch, g))
         return g
@@ -95,9 +97,11 @@ class PagedCaches:
     def grow(self, rows=None, stream=None):
         """Pages for the next rows of each slot (None: one for each active one), before they are appended."""
         rows = self._rows(rows)
+        if len(rows) != self.n_slots or any(n < 0 or (n and L < 0) for L, n in zip(self.lens, rows)):
+            raise ValueError(f"rows {rows} are not of {self.n_slots} slots, or of idle ones")
         need = [max(0, -(-(L + n) // self.page) - len(p)) if n else 0 for L, n, p in zip(self.lens, rows, self.pages)]
-        if any(L >= 0 and n and L + n > self.max_len + 1 for L, n in zip(self.lens, rows)):
-            raise ValueError(f"a slot would hold more than {self.max_len + 1} rows")
+        if any(n and L + n > self.max_len for L, n in zip(self.lens, rows)):
+            raise ValueError(f"a slot would hold more than {self.max_len} rows")
         if sum(need) > len(self.free):
             raise MemoryError(f"{sum(need)} pages wanted, {len(self.free)} free")
         for slot, n in enumerate(need):

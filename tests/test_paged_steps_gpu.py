@@ -175,6 +175,50 @@ def test_sparse_steps():
     assert c.status() == 0
 
 
+def test_slots_up_to_their_bound():
+    """A slot takes max_len rows and no more; a full one beside it troubles no other slot; idle ones get no pages."""
+    page, Hq, Hkv, D = 16, 4, 2, 64
+    c = PagedCaches(1, 40, page, Hq, Hkv, D, 3, 64, sparse=(3, 1, 1))
+    gen = torch.Generator(device="cuda").manual_seed(0)
+
+    def prompt(counts):
+        c.grow(counts)
+        n = sum(counts)
+        r = B.PagedRows(counts)
+        q = _raw(gen, n, Hq, D)
+        c.append(0, r, q, _raw(gen, n, Hkv, D), _raw(gen, n, Hkv, D), q)
+        c.advance(r)
+        c.advanced(counts)
+
+    c.admit(0)
+    c.admit(1)
+    for bad in ([65, 0, 0], [0, 0, 1], [1, 0], [1, -1, 0]):
+        with pytest.raises(ValueError):
+            c.grow(bad)
+    assert len(c.free) == 40
+    prompt([64, 3, 0])
+    with pytest.raises(ValueError):
+        c.grow([1, 0, 0])
+    prompt([0, 20, 0])
+    assert c.lens == [64, 23, -1] and c.len.tolist() == [64, 23, -1] and c.status() == 0
+    with pytest.raises(ValueError):
+        c.decode([])  # the full slot would take a row
+    c.retire(0)
+    out = torch.full((3, Hq, D), 7.0, dtype=BF, device="cuda")
+    c.decode([{"q": _raw(gen, 3, Hq, D), "k": _raw(gen, 3, Hkv, D), "v": _raw(gen, 3, Hkv, D), "out": out}])
+    assert c.lens == [-1, 24, -1] and c.len.tolist() == [-1, 24, -1] and c.status() == 0
+    assert (out[[0, 2]] == 7).all() and out[1].isfinite().all()
+
+
+def test_groups_after_a_capture():
+    """Groups that need a larger workspace leave the one of captured steps where it is."""
+    page, Hq, Hkv, D = 64, 24, 4, 256
+    c = PagedCaches(1, 20, page, Hq, Hkv, D, 2, 500)
+    ws = c.ws
+    c.groups([2], [0])
+    assert c.ws.numel() > ws.numel() and any(x is ws for x in c.outgrown)
+
+
 @pytest.mark.parametrize("sparse", [None, (5, 1, 1)])
 def test_captured_steps(sparse):
     """One graph serves steps whose lengths, pages, active slots and groups change between replays."""
