@@ -656,7 +656,7 @@ extern "C" tv_status tv_paged_select(const tv_paged_layer* l, const tv_paged* b,
 }
 
 extern "C" tv_status tv_paged_advance(const tv_paged* b, const tv_paged_rows* rows, int32_t* len, tv_stream stream) {
-  if (!b || !b->len || !b->status || !len || b->n_seq < 1 || b->n_seq > TV_MAX_PAGED_SEQ || b->max_len < 0 || len != b->len) return TV_ERR_ARG;
+  if (!b || !b->len || !b->status || !len || b->n_seq < 1 || b->n_seq > TV_MAX_PAGED_SEQ || b->max_len < 0 || b->max_len >= 1 << 30 || len != b->len) return TV_ERR_ARG;
   if (!aligned16(b->len) || !aligned16(b->status)) return TV_ERR_ALIGN;
   const tv_status c = paged_rows_check(rows);
   if (c != TV_OK) return c;

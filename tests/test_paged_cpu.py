@@ -183,7 +183,7 @@ def test_select_and_bounds_refused(L):
 def test_advance_refused(L):
     def adv(b=None, r=None, len_=0x2000):
         return L.tv_paged_advance(ref(batch() if b is None else b), ref(r) if r is not None else None, vp(len_), None)
-    for bad in ({"n_seq": 0}, {"n_seq": 1025}, {"max_len": -1}, {"len_": 0}, {"status": 0}):
+    for bad in ({"n_seq": 0}, {"n_seq": 1025}, {"max_len": -1}, {"max_len": 1 << 30}, {"len_": 0}, {"status": 0}):
         assert adv(batch(**bad)) == ARG, bad
     assert adv(len_=0) == ARG and adv(len_=0x2010) == ARG
     assert adv(batch(len_=0x2004), len_=0x2004) == ALIGN and adv(r=rows(off=0)) == ARG
