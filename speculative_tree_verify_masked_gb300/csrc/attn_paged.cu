@@ -8,7 +8,8 @@
 // of eight rows (four of 256 columns), a row's D values over the 32 lanes, all loads of a run
 // in flight, and keep a running maximum and sum each, which are joined at the end.  A
 // warp looks up the pages of 32 runs at once.  Bound by the walk over the rows of the
-// longest slot (sized for the small model of the tests).
+// longest slot (sized for the small model of the tests): 5 slots of up to 301 rows, 2 + 1 heads of 64,
+// 5.8 us (four warps, one row of each in flight: 12.2).
 #include <utility>
 
 #include "attn_paged.cuh"

@@ -22,13 +22,17 @@
 // pair of factors a dimension, y_d = inv (x_d (w_d cos) + x_p (w_p sin)), formed
 // once a warp, so a head costs two packed products a pair of dimensions and its
 // partners travel unwidened.
-// A row's bits depend only on its own values and position, and the three forms
-// run the same code, so verified, decoded and prompt rows are equal.
+// A row's bits depend only on its own values and position, and all forms
+// run the same code, so verified, decoded, prompt and paged rows are equal.
+// (Pages allow 2^30 positions: the fractions' fp64 then leaves up to 2^-24 of a turn.)
 //
 // Bound by HBM, each row read once and written once, with the issue slots close
 // behind (59 % at 53 % of DRAM throughput).  8,192 prompt rows of 24 + 4 + 4
 // heads of 256 (268 MB): 51.4 us, 5.2 TB/s, 0.78 of a copy's rate; four decode
-// tokens: 3.5 us, a launch's latency.
+// tokens: 3.5 us, a launch's latency.  Into pages of 16 rows, 4,629 rows of four
+// prompts (152 MB) 31.2 us, 4.9 TB/s, 0.73 of a copy's rate: a row's slot and page are two
+// more reads in a row before its first store; 192 decode rows 4.3 us.  (Up to 16, 12 or 8 heads a
+// warp for more warps: 34.4, 34.0 and 37.7 us.)
 #include <cmath>
 
 #include "paged.cuh"
