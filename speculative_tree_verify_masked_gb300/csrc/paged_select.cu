@@ -21,9 +21,10 @@
 // the reads of the codes (a 128th of the keys and values at pages of 64 rows), in pieces of 512 bytes all over, for many:
 // 24 slots of up to 65,536 rows 12.5 us for 18 MB.
 //
-// The bounds are bound by reads of whole pages, one CTA each: 16,421 rows of two prompts (33.6 MB of keys) 9.4 us, 3.6
-// TB/s in a grid of 1,032 CTAs that runs once; a step of 192 slots 2.7 us, a launch's latency.  (Eight rows of a lane in flight
-// instead of four: 9.0 us, but 3.6 against 3.2 a step, whose code is cold.)
+// The bounds are bound by reads of whole pages, one CTA each: 16,421 rows of two prompts (33.6 MB of keys) 8.9 us, 3.8
+// TB/s in a grid of 1,032 CTAs that runs once; a step of 192 slots 2.7 us, a launch's latency.  (Up to eight rows of a lane
+// are in flight, two of small pages; four in one loop 9.3 us, and 5.3 against 4.6 for a few pages of 128 rows of 256; CTAs of
+// 256 threads 11.0, and 3.4 a step.)
 //
 // The choice is a radix selection of the n-th highest key by digits of eight bits,
 // from the highest bit in which the keys differ down, until a digit leaves no
@@ -32,6 +33,7 @@
 // into the first one's shared memory, which then chooses.
 #include <climits>
 #include <cuda_fp16.h>
+#include <type_traits>
 #include <utility>
 
 #include "paged.cuh"
@@ -51,6 +53,13 @@ struct BoundsParams {
   int32_t* exp;
   int Hkv;
 };
+
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) { widen8(*reinterpret_cast<const uint4*>(p), x); }
 
 // A CTA takes a page's rows of one KV head: eight columns a lane and row.
 template <typename T, int D>
@@ -91,23 +100,36 @@ __global__ void __launch_bounds__(128) paged_bounds_kernel(const __grid_constant
     lo[e] = INFINITY;
     hi[e] = -INFINITY;
   }
-#pragma unroll 4
-  for (int r = r0; r < rows; r += STEP, src += STEP * D) {
-    float x[8];
-    if constexpr (sizeof(T) == 2) {
-      widen8(*reinterpret_cast<const uint4*>(src), x);
-    } else {
-      const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
+  auto take = [&](auto n) {  // so many rows of this lane, all on their way together
+    constexpr int N = decltype(n)::value;
+    uint4 raw[N][sizeof(T) / 2];
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-      finite = finite && isfinite(x[e]);
-      lo[e] = fminf(lo[e], x[e]);
-      hi[e] = fmaxf(hi[e], x[e]);
+    for (int k = 0; k < N; k++)
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(T) / 2); i++)
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(raw[k][i].x), "=r"(raw[k][i].y), "=r"(raw[k][i].z), "=r"(raw[k][i].w)
+                     : "l"(reinterpret_cast<const uint4*>(src + k * STEP * D) + i));
+    src += N * STEP * D;
+#pragma unroll
+    for (int k = 0; k < N; k++) {
+      float x[8];
+      if constexpr (sizeof(T) == 2) widen8(raw[k][0], x);
+      else memcpy(x, raw[k], 32);
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        finite = finite && isfinite(x[e]);
+        lo[e] = fminf(lo[e], x[e]);
+        hi[e] = fmaxf(hi[e], x[e]);
+      }
     }
-  }
+  };
+  int left = (rows - r0 + STEP - 1) / STEP;
+#pragma unroll 1
+  for (; left >= 8; left -= 8) take(std::integral_constant<int, 8>());
+#pragma unroll 1
+  for (; left >= 2; left -= 2) take(std::integral_constant<int, 2>());
+  if (left > 0) take(std::integral_constant<int, 1>());
 #pragma unroll
   for (int e = 0; e < 8; e++) {
     lo_s[r0][c0 + e] = lo[e];
@@ -184,13 +206,6 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   lo = *reinterpret_cast<const uint32_t*>(&x);
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
-
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) { widen8(*reinterpret_cast<const uint4*>(p), x); }
 
 constexpr int kSelect = 256;        // threads of a CTA: each warp scores sixteen pages at a time
 constexpr int kSelectKeys = 16384;  // pages whose keys fit in shared memory
