@@ -244,6 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
       last.y = paged_len(p.v.b, s);
       last.x = unit_tiles<C::ROWS>(p, u, s, last.y);
       mine += static_cast<int64_t>(steps_of(last.x, C::EXTRA)) * p.MT;
+      // an empty list: zeros (by the thread that has met it: a look at a CTA's share of the units takes a read of the
+      // count behind one of the length for each, one by one; 46 slots 18.5 us with their selection and 20.1)
+      if (last.x == 0 && last.y >= 0 && u % gridDim.x == blockIdx.x) {
+        uint4* out = reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(s) * p.Hq + (u - s * p.v.Hkv) * p.G) * D);
+        for (int i = 0; i < p.G * D / 8; i++) out[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
     }
     int64_t incl = mine;
 #pragma unroll
@@ -301,15 +307,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   PagedWalk<C::ROWS, C::EXTRA> walk{lo.u, lo.u / p.v.Hkv, lo.u % p.v.Hkv, lo.u, lo_near, lo.off, lo.left};
   PagedPiece x;
   pdl_trigger();
-  if (p.v.sel && warp < kConsumers / 32) {  // slots that see nothing: zeros
-    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
-      const int s = u / p.v.Hkv;
-      if (paged_len(p.v.b, s) < 0 || unit_tiles<C::ROWS>(p, u) > 0) continue;
-      uint32_t* out = reinterpret_cast<uint32_t*>(p.out + (static_cast<size_t>(s) * p.Hq + (u - s * p.v.Hkv) * p.G) * D);
-      for (int i = threadIdx.x; i < p.G * D / 2; i += kConsumers) out[i] = 0u;
-    }
-  }
-
   if (warp == kConsumers / 32) {
     // ---------------- producer ----------------
     const int R = p.R, nsub = C::ROWS / R, rows = 1 << p.v.b.shift, per_page = rows / R;
