@@ -15,7 +15,8 @@
 // range of equal length for each CTA (one per SM), so every SM streams the same
 // number of bytes whatever the lengths are.  An item that lies in one CTA's range
 // is written by it; one that a cut goes through leaves a piece (O, m and l in fp32)
-// with each of its CTAs, two a CTA at most, and the join adds them up.  Every
+// with each of its CTAs, two a CTA at most, and the join adds them up.  Where the host's bounds
+// leave no item more than a few tiles, ranges end with items and there is no join.  Every
 // CTA finds its range from the device-side lengths by itself.
 //
 // Roles.  A producer warp brings keys and values by TMA; it reads the table (and
@@ -41,6 +42,7 @@
 // 9.9 us, of which the lengths, the table, keys and values are reads one behind the other, some 3.4 the join.
 // Heads of 64 in pages of 16 rows reach 0.66: a copy of 2 KB a page is too small.
 // (Query heads on the long side of the tiles, as many as 16 fill: 256 slots of 100 rows 46 us against 35.)
+#include <algorithm>
 #include <cstring>
 
 #include "attn_paged.cuh"
@@ -98,6 +100,7 @@ struct PagedTcParams {
   int Hq, G, MT, units;  // MT items a unit
   int item;              // query heads of an item
   int R;  // rows of a box: a page's, or a tile's
+  int uncut;  // 1: ranges end with items, and there is nothing to join
   float c;        // scale * log2(e)
   uint32_t zero;  // 0
 };
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
   const uint32_t FULL0 = sb + C::BOFF, EMPTY0 = FULL0 + 16u * C::NS;
   int32_t* seen_s = reinterpret_cast<int32_t*>(smem_raw + C::VOFF);
   struct Local {
-    int64_t left, before, total, at;
+    int64_t left, before, total, at, end;
     int u, off, skip, ctas;
     int abort_flag;
   };
@@ -234,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     __syncthreads();
   }
   // this CTA's range: a run of units for each thread, their tiles summed over the CTA
+  int64_t left;
   {
     const int per = (p.units + kThreads - 1) / kThreads;
     const int u0 = min(static_cast<int>(threadIdx.x) * per, p.units), u1 = min(u0 + per, p.units);
@@ -276,25 +280,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     }
     if (threadIdx.x == 0) lo.ctas = ctas;
     if (me < ctas) {
-      const int64_t a = range_start(total, ctas, me);
-      if (a >= base && a < base + mine) {
+      const int64_t a = range_start(total, ctas, me), b = range_start(total, ctas, me + 1);
+#pragma unroll 1
+      for (int k = 0; k <= p.uncut; k++) {
+        const int64_t t = k ? b : a;
+        if (t < base || t >= base + mine) continue;
         int64_t at = base;
-        int u = u0;
-        for (; per > 1; u++) {
-          const int64_t n = static_cast<int64_t>(steps_of(unit_tiles<C::ROWS>(p, u), C::EXTRA)) * p.MT;
-          if (a < at + n || u + 1 >= u1) break;
-          at += n;
+        int u = u0, steps;
+        for (;; u++) {
+          steps = steps_of(per == 1 ? last.x : unit_tiles<C::ROWS>(p, u), C::EXTRA);
+          if (t < at + static_cast<int64_t>(steps) * p.MT || u + 1 >= u1) break;
+          at += static_cast<int64_t>(steps) * p.MT;
         }
-        lo.u = u;
-        lo.off = static_cast<int>(a - at);
-        lo.left = range_start(total, ctas, me + 1) - a;
-        lo.before = me > 0 ? a - range_start(total, ctas, me - 1) : 0;
-        lo.total = total;
-        lo.at = a;
+        int off = static_cast<int>(t - at);
+        if (p.uncut) off = (off + steps - 1) / steps * steps;  // where the next item starts
+        if (k) {
+          lo.end = at + off;
+        } else {
+          lo.u = u;
+          lo.off = off;
+          lo.left = b - a;
+          lo.before = me > 0 ? a - range_start(total, ctas, me - 1) : 0;
+          lo.total = total;
+          lo.at = at + off;
+        }
       }
+      if (b == total && threadIdx.x == 0) lo.end = total;
     }
     __syncthreads();
-    if (lo.left > 0) {  // what the next units hold
+    left = p.uncut && me < ctas ? lo.end - lo.at : lo.left;
+    if (left > 0) {  // what the next units hold
       if (per == 1) {
         if (u0 < u1 && u0 >= lo.u && u0 < lo.u + kNear) lo_near[u0 - lo.u] = last;
       } else if (threadIdx.x < kNear && lo.u + static_cast<int>(threadIdx.x) < p.units) {
@@ -304,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
     }
     __syncthreads();
   }
-  PagedWalk<C::ROWS, C::EXTRA> walk{lo.u, lo.u / p.v.Hkv, lo.u % p.v.Hkv, lo.u, lo_near, lo.off, lo.left};
+  PagedWalk<C::ROWS, C::EXTRA> walk{lo.u, lo.u / p.v.Hkv, lo.u % p.v.Hkv, lo.u, lo_near, lo.off, left};
   PagedPiece x;
   pdl_trigger();
   if (warp == kConsumers / 32) {
@@ -803,6 +818,11 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
   if (!allow_smem(attn_paged_tc_kernel<D, NB>, C::SMEM, set)) return TV_ERR_CUDA;
   const int grid = num_sms();
   const bool may_share = p.start != nullptr;
+  // Where no item can have more than four tiles, each is one CTA's, and the call saves the join, which takes longer than the
+  // tiles that others would have taken: 24 + 4 heads of 256 or 32 + 4 of 128, 2 slots of up to 98 rows 7.6 us and 9.3
+  // with ranges cut evenly, 30 of up to 250 9.4 and 11.8, 3 of up to 216 9.4 and 10.2 (seven tiles would lose).
+  const int64_t most = a.sel ? std::min<int64_t>(static_cast<int64_t>(a.n_sel) * l->page, a.batch->max_len + 1) : a.batch->max_len + 1;
+  p.uncut = !may_share && most <= 4 * C::ROWS ? 1 : 0;
   launch_k(true, attn_paged_tc_kernel<D, NB>, dim3(grid), dim3(kThreads), C::SMEM, st, p);
   if (may_share) {
     PagedPrefixParams x;
@@ -825,6 +845,7 @@ static tv_status launch_tc(PagedTcParams& p, const PagedAttnCall& a, cudaStream_
     x.c = p.c;
     if (!paged_prefix_launch(x, D, st)) return TV_ERR_CUDA;
   }
+  if (p.uncut) return launch_status();
   if (may_share) launch_k(true, attn_paged_join_kernel<D, true>, dim3(l->Hq, a.batch->n_seq), dim3(256), 0, st, p);
   else launch_k(true, attn_paged_join_kernel<D, false>, dim3(grid, p.G < p.item ? p.G : p.item), dim3(256), 0, st, p);
   return launch_status();

@@ -54,6 +54,21 @@ def test_attn_splits(heads, lens):
     assert p.status() == 0
 
 
+@pytest.mark.parametrize("heads,n,most", [((24, 4, 256), 200, 255), ((24, 4, 256), 3, 255), ((16, 2, 128), 90, 254), ((40, 2, 64), 70, 511),
+                                          ((8, 8, 64), 40, 511), ((34, 2, 256), 60, 100), ((8, 1, 128), 500, 40)])
+@pytest.mark.parametrize("idle", [0, 1])
+def test_attn_items_uncut(heads, n, most, idle):
+    """Slots short enough for ranges that end with items: more items than CTAs and fewer, idle slots in runs."""
+    rng = np.random.default_rng(n + most)
+    lens = rng.integers(0, most + 1, n)
+    lens[rng.integers(0, n)] = most
+    if idle:
+        lens[n // 4:n - n // 4] = -1
+    p = Pools(lens.tolist(), 32, heads, seed=n)
+    p.expect(p.attn())
+    assert p.status() == 0
+
+
 @pytest.mark.parametrize("heads,page", [((24, 4, 256), 64), ((16, 2, 128), 32), ((8, 8, 64), 128)])
 def test_attn_long_pieces(heads, page):
     """Hundreds of tiles a CTA, some from memory and some from L2: copies land out of order."""
