@@ -516,9 +516,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < C::SG / 4; i++) {
           const uint32_t vb = sb + vs * C::SLOT + row_at(w * C::WR + i * 16);
-          for (int r = vis[i]; r < 16; r++)
-            for (int e = lane; e < D / 8; e += 32)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (e >> 3) * chunk + r * 128 + (e & 7) * 16), "r"(0) : "memory");
+          constexpr int RW = 256 / D;  // rows at a time
+          const int e = lane % (D / 8);
+          for (int r = vis[i] + lane / (D / 8); r < 16; r += RW)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (e >> 3) * chunk + r * 128 + (e & 7) * 16), "r"(0) : "memory");
         }
         fence_proxy_async_smem();  // before the slot's next copy
       }
