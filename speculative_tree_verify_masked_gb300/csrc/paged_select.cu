@@ -419,21 +419,24 @@ __global__ void __launch_bounds__(TH, 512 / TH) paged_select_kernel(const __grid
     __syncthreads();
   }
   if (bad) return;
-  // ---- the choice: a run of keys a thread, in registers where eight do
+  // ---- the choice: a run of keys a thread; three to eight in registers (shared memory then holds all of them), one or two in
+  // a loop, since all of this runs once, from cold code (64 pages 4.2 us, 4.7 from registers; 2,048 pages 8.7, 10.0 in a loop)
   constexpr int RUN = 8;
-  const bool few = n <= RUN * TH;  // (shared memory then holds all of them)
-  auto key = [&](int i) { return kept ? keys[i] : __ldcg(far + i); };
   const int run = (n + TH - 1) / TH, i0 = min(tid * run, n), i1 = min(i0 + run, n);
+  const bool few = run > 2 && run <= RUN;
   uint32_t own[RUN];
+  if (few) {
 #pragma unroll
-  for (int j = 0; j < RUN; j++) own[j] = few && i0 + j < i1 ? keys[i0 + j] : 0u;
+    for (int j = 0; j < RUN; j++) own[j] = i0 + j < i1 ? keys[i0 + j] : 0u;
+  }
   auto each = [&](auto f) {
     if (few) {
 #pragma unroll
       for (int j = 0; j < RUN; j++)
         if (i0 + j < i1) f(i0 + j, own[j]);
     } else {
-      for (int i = i0; i < i1; i++) f(i, key(i));
+#pragma unroll 1
+      for (int i = i0; i < i1; i++) f(i, kept ? keys[i] : __ldcg(far + i));
     }
   };
   uint32_t low = 0xffffffffu, high = 0;
