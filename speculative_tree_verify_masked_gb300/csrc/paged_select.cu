@@ -258,14 +258,16 @@ __global__ void __launch_bounds__(TH, 512 / TH) paged_select_kernel(const __grid
   // that some of them meet first keeps the first CTA from writing, no more.)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
-  const bool bad = status_set(p.b.status);
+  // Another CTA of this launch may set the word between two warps' looks at it, so a CTA leaves by what all its
+  // threads have seen: warps that went on alone would place pages by counts that the others never wrote.
+  bool bad = status_set(p.b.status);
   const int u = blockIdx.y, s = u / p.Hkv, h = u - s * p.Hkv;
   const int L = paged_len(p.b, s);
   const int nb = (L >> p.b.shift) + 1;
   int32_t* sel = p.sel + static_cast<size_t>(u) * p.n_sel;
   if (L < 0 || nb <= p.n_sel || p.n_sel == p.first + p.last) {  // (the whole cluster)
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    if (L < 0 || rank > 0 || bad) return;
+    if (__syncthreads_or(bad) || L < 0 || rank > 0) return;
     const int ends = nb <= p.n_sel ? nb : p.first;
     for (int i = tid; i < p.n_sel; i += TH) sel[i] = i < ends ? i : nb <= p.n_sel ? -1 : nb - p.n_sel + i;
     if (tid == 0) p.count[u] = min(nb, p.n_sel);
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(TH, 512 / TH) paged_select_kernel(const __grid
   }
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) red_s[warp] = top;
-  __syncthreads();
+  bad = __syncthreads_or(bad) != 0;
 #pragma unroll
   for (int w = 0; w < W; w++) top = max(top, red_s[w]);
   const bool finite = top < 0x7f800000u;
