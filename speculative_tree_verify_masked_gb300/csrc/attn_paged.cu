@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(32 * kCudaWarps, 1) attn_paged_cuda_kernel(con
     acc[c] = 0.f;
   }
   const int L = paged_len(p.v.b, s);
-  if (bad || L < 0) return;
+  if (__syncthreads_or(bad) || L < 0) return;  // (another CTA may set the word between two warps' looks at it)
   const int shift = p.v.b.shift, rows = 1 << shift;
   const int n = p.v.pages(s, g, L) << shift;
   int64_t row = -1;  // of a run of this warp's next 32, a lane each: its first row in the pools, -1: none

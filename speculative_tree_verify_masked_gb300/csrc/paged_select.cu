@@ -68,10 +68,10 @@ __global__ void __launch_bounds__(128) paged_bounds_kernel(const __grid_constant
   __shared__ float lo_s[STEP][D], hi_s[STEP][D];
   __shared__ float top_s[4];
   pdl_wait();
-  if (status_set(p.b.status)) return;
+  const bool bad = status_set(p.b.status);
   const int s = blockIdx.y, h = blockIdx.z;
   const int L = paged_len(p.b, s);
-  if (L < 0) return;
+  if (__syncthreads_or(bad) || L < 0) return;  // (another CTA may set the word between two warps' looks at it)
   int n = 1;
   if (p.row_off) {
     const int off = p.row_off[s], end = p.row_off[s + 1];

@@ -98,3 +98,72 @@ def test_choice_given_the_word():
     p.batch.status[0] = ERR_PAGE
     sel, count, clean = _selected(p, code, exp, 24)
     assert (sel == 77).all() and (count == 77).all() and clean and p.status() == ERR_PAGE
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("page", [16, 64])
+def test_bounds_beside_an_entry_that_names_no_page(dtype, page):
+    """Hundreds of slots' pages, each bound by its keys or not at all."""
+    lens = [(37 * i) % 500 for i in range(300)]
+    counts = [4 * page + i % 9 for i in range(300)]
+    p = Pools(lens, page, (8, 4, 128), dtype, extra=5 * page, fill=None)
+    rows = B.PagedRows(counts)
+
+    def run():
+        code, code_all = _framed((p.n_pages, p.Hkv, 2, p.D), torch.int8, 99)
+        exp, exp_all = _framed((p.n_pages, p.Hkv), torch.int32, 99)
+        B.tv_paged_bounds(p.layer, p.batch, rows, code, exp)
+        return code, exp, _margins(code_all, 99) and _margins(exp_all, 99)
+
+    want_code, want_exp, clean = run()
+    assert clean and p.status() == 0
+    for bad in (0, 150, 299):
+        j = lens[bad] // page + 1
+        keep = int(p.table[bad, j])
+        for entry in (p.n_pages, -1, -(1 << 31)):
+            p.table[bad, j] = entry
+            code, exp, clean = run()
+            assert p.status() == ERR_PAGE and clean
+            left = (code == 99).all(-1).all(-1) & (exp == 99)
+            right = (code == want_code).all(-1).all(-1) & (exp == want_exp)
+            assert (left | right).all() and left[keep].all()
+            p.batch.status.zero_()
+        p.table[bad, j] = keep
+    p.batch.status[0] = ERR_PAGE
+    code, exp, clean = run()
+    assert (code == 99).all() and (exp == 99).all() and clean
+
+
+@pytest.mark.parametrize("dtype,heads,lens", [(F32, (4, 2, 64), [(61 * i) % 400 for i in range(400)]),
+                                              (BF, (8, 2, 128), [(61 * i) % 400 for i in range(400)]),
+                                              (BF, (24, 4, 256), [9000, 300, 4001, -1, 64, 20000])])
+@pytest.mark.parametrize("chosen", [False, True])
+def test_attention_beside_an_entry_that_names_no_page(dtype, heads, lens, chosen):
+    """Rows of out as they are without the bad entry, or as they were: cut items, whole ones, every page or listed ones."""
+    p = Pools(lens, 16, heads, dtype)
+    sel = torch.tensor([[list(range(5))] * p.Hkv] * len(lens), dtype=torch.int32, device="cuda")
+    count = torch.tensor([[min(5, L // 16 + 1)] * p.Hkv for L in lens], dtype=torch.int32, device="cuda")
+
+    def run():
+        p.out, whole = _framed((len(lens), p.Hq, p.D), dtype, 7.0)
+        p.selected(sel, count, p.gate) if chosen else p.attn(p.gate)
+        return p.out, _margins(whole, 7.0)
+
+    want, clean = run()
+    assert clean and p.status() == 0 and want.isfinite().all()
+    for bad in (i for i, L in enumerate(lens) if i in (1, 4, 200, 399) and L >= 16):
+        keep = int(p.table[bad, 1])
+        for entry in (p.n_pages, -1, -(1 << 31)):
+            p.table[bad, 1] = entry
+            out, clean = run()
+            assert p.status() == ERR_PAGE and clean
+            ok = (out == 7).all(-1) | (out == want).all(-1)
+            ok[bad] = True
+            assert ok.all()
+            p.batch.status.zero_()
+        p.table[bad, 1] = keep
+    out, _ = run()
+    assert torch.equal(out, want) and p.status() == 0
+    p.batch.status[0] = ERR_PAGE
+    out, clean = run()
+    assert (out == 7).all() and clean
