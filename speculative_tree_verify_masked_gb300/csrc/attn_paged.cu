@@ -10,8 +10,6 @@
 // warp looks up the pages of 32 runs at once.  Bound by the walk over the rows of the
 // longest slot (sized for the small model of the tests): 5 slots of up to 301 rows, 2 + 1 heads of 64,
 // 5.8 us (four warps, one row of each in flight: 12.2).
-#include <utility>
-
 #include "attn_paged.cuh"
 
 namespace tv {
@@ -160,24 +158,17 @@ static tv_status paged_attn(const PagedAttnCall& a, cudaStream_t st) {
   const tv_paged_layer* l = a.layer;
   if (!l->K || !l->V || !a.q || !a.out || !(a.scale > 0.f) || !std::isfinite(a.scale)) return TV_ERR_ARG;
   if (!aligned16(a.q) || !aligned16(a.gate) || !aligned16(a.out) || !aligned16(a.ws)) return TV_ERR_ALIGN;
-  const size_t n = bytes_of(a.batch->n_seq, static_cast<int64_t>(l->Hq) * l->D, l->dtype);
-  if (share_memory(a.q, n, a.out, n)) return TV_ERR_ARG;  // a slot's heads are read after others are written
-  if (a.gate != a.out && share_memory(a.gate, n, a.out, n)) return TV_ERR_ARG;
+  // (a slot's heads, lists and lengths are read after others' rows are written; out may be gate)
+  const tv_paged_groups* g = a.groups;
+  const size_t n = bytes_of(a.batch->n_seq, static_cast<int64_t>(l->Hq) * l->D, l->dtype), units = static_cast<size_t>(a.batch->n_seq) * l->Hkv;
   const size_t pool = bytes_of(static_cast<int64_t>(l->n_pages) * l->Hkv * l->page, l->D, l->dtype);
-  const size_t ns = static_cast<size_t>(a.batch->n_seq) * l->Hkv * 4;
-  if (share_memory(a.out, n, l->K, pool) || share_memory(a.out, n, l->V, pool) || share_memory(a.out, n, a.sel, ns * a.n_sel) ||
-      share_memory(a.out, n, a.count, ns) || shares_batch(a.out, n, a.batch))
-    return TV_ERR_ARG;
-  if (const tv_paged_groups* g = a.groups)
-    if (share_memory(a.out, n, g->group_off, static_cast<size_t>(g->n_group + 1) * 4) ||
-        share_memory(a.out, n, g->shared, static_cast<size_t>(g->n_group) * 4))
-      return TV_ERR_ARG;
-  if (l->dtype != TV_BF16) return launch_cuda(a, st);
-  const size_t need = paged_attn_ws_bytes(l, a.batch, a.groups);
+  const Mem reads[] = {{a.q, n}, {a.gate == a.out ? nullptr : a.gate, n}, {l->K, pool}, {l->V, pool}, {a.sel, units * a.n_sel * 4}, {a.count, units * 4},
+                       {g ? g->group_off : nullptr, g ? static_cast<size_t>(g->n_group + 1) * 4 : 0}, {g ? g->shared : nullptr, g ? static_cast<size_t>(g->n_group) * 4 : 0},
+                       table_of(a.batch), lens_of(a.batch)};
+  if (l->dtype != TV_BF16) return apart(a.batch->status, {{a.out, n}}, reads) ? launch_cuda(a, st) : TV_ERR_ARG;
+  const size_t need = paged_attn_ws_bytes(l, a.batch, g);
+  if (!apart(a.batch->status, {{a.out, n}, {a.ws, a.ws_bytes < need ? 0 : need}}, reads)) return TV_ERR_ARG;
   if (!a.ws || a.ws_bytes < need) return TV_ERR_WORKSPACE;
-  for (const auto& x : {std::pair<const void*, size_t>(a.q, n), {a.gate, n}, {a.out, n}, {l->K, pool}, {l->V, pool}, {a.sel, ns * a.n_sel}, {a.count, ns}})
-    if (share_memory(a.ws, need, x.first, x.second)) return TV_ERR_ARG;
-  if (shares_batch(a.ws, need, a.batch)) return TV_ERR_ARG;
   return paged_attn_tc_launch(a, st);
 }
 

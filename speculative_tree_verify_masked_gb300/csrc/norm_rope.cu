@@ -499,16 +499,13 @@ extern "C" tv_status tv_paged_append(const tv_paged_layer* l, const tv_paged* b,
   if (n == 0) return TV_OK;
   if (!q_raw || !k_raw || !v || !q) return TV_ERR_ARG;
   if (!aligned16(q_raw) || !aligned16(k_raw) || !aligned16(v) || !aligned16(q)) return TV_ERR_ALIGN;
-  if (!in_place_or_apart(&a, n, l->Hq, q, q_raw, l->Hkv, k_raw) || !in_place_or_apart(&a, n, l->Hq, q, q_raw, l->Hkv, v))
-    return TV_ERR_ARG;
-  // rows are read while others are written: the pools lie apart from them and from each other
+  // rows, offsets and weights are read while others' rows are written; q may be q_raw
   const size_t pool = bytes_of(static_cast<int64_t>(l->n_pages) * l->Hkv * l->page, l->D, l->dtype);
   const size_t nq = bytes_of(n, static_cast<int64_t>(l->Hq) * l->D, l->dtype), nk = bytes_of(n, static_cast<int64_t>(l->Hkv) * l->D, l->dtype);
-  for (const void* x : {l->K, l->V})
-    if (share_memory(x, pool, q_raw, nq) || share_memory(x, pool, q, nq) || share_memory(x, pool, k_raw, nk) ||
-        share_memory(x, pool, v, nk))
-      return TV_ERR_ARG;
-  if (share_memory(l->K, pool, l->V, pool) || shares_batch(l->K, pool, b) || shares_batch(l->V, pool, b) || shares_batch(q, nq, b)) return TV_ERR_ARG;
+  const size_t nw = static_cast<size_t>(l->D) * 4;
+  if (!apart(b->status, {{l->K, pool}, {l->V, pool}, {q, nq}},
+             {{q == q_raw ? nullptr : q_raw, nq}, {k_raw, nk}, {v, nk}, {q_norm, nw}, {k_norm, nw}, offsets_of(b, rows), table_of(b), lens_of(b)}))
+    return TV_ERR_ARG;
   NormRopeParams p{};
   p.form = rows ? 4 : 3;
   p.pg = paged_seqs(l, b);

@@ -87,14 +87,34 @@ inline bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
 
 // Bytes of [rows][cols] values of type dt.
 inline size_t bytes_of(int64_t rows, int64_t cols, tv_dtype dt) { return static_cast<size_t>(rows * cols) * (dt == TV_BF16 ? 2 : 4); }
-inline bool share_memory(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
+// Memory that a call reads or writes; null: not there.
+struct Mem {
+  const void* at;
+  size_t bytes;
+};
+inline bool share_memory(const Mem& a, const Mem& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.at && b.at && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
 }
-// Whether what a call writes shares memory with the table, the lengths or the status word.
-inline bool shares_batch(const void* a, size_t n, const tv_paged* b) {
-  return share_memory(a, n, b->table, static_cast<size_t>(b->n_seq) * b->cols * 4) ||
-         share_memory(a, n, b->len, static_cast<size_t>(b->n_seq) * 4) || share_memory(a, n, b->status, 4);
+// Whether what a call writes, the status word among it, shares memory with nothing else that it writes or reads.
+template <size_t W, size_t R>
+inline bool apart(const int32_t* status, const Mem (&writes)[W], const Mem (&reads)[R]) {
+  const Mem word{status, 4};
+  for (size_t i = 0; i < W; i++) {
+    if (share_memory(writes[i], word)) return false;
+    for (size_t j = i + 1; j < W; j++)
+      if (share_memory(writes[i], writes[j])) return false;
+    for (const Mem& r : reads)
+      if (share_memory(writes[i], r)) return false;
+  }
+  for (const Mem& r : reads)
+    if (share_memory(word, r)) return false;
+  return true;
+}
+inline Mem table_of(const tv_paged* b) { return {b->table, static_cast<size_t>(b->n_seq) * b->cols * 4}; }
+inline Mem lens_of(const tv_paged* b) { return {b->len, static_cast<size_t>(b->n_seq) * 4}; }
+inline Mem offsets_of(const tv_paged* b, const tv_paged_rows* r) {
+  return {r ? r->row_off : nullptr, static_cast<size_t>(b->n_seq + 1) * 4};
 }
 
 }  // namespace tv

@@ -34,7 +34,6 @@
 #include <climits>
 #include <cuda_fp16.h>
 #include <type_traits>
-#include <utility>
 
 #include "paged.cuh"
 #include "prompt.cuh"
@@ -596,9 +595,7 @@ extern "C" tv_status tv_paged_bounds(const tv_paged_layer* l, const tv_paged* b,
   if (!l->K || !code || !exp) return TV_ERR_ARG;
   if (!aligned16(code) || !aligned16(exp)) return TV_ERR_ALIGN;
   const size_t heads = static_cast<size_t>(l->n_pages) * l->Hkv, pool = bytes_of(static_cast<int64_t>(heads) * l->page, l->D, l->dtype);
-  if (share_memory(code, heads * 2 * l->D, l->K, pool) || share_memory(exp, heads * 4, l->K, pool) ||
-      share_memory(code, heads * 2 * l->D, exp, heads * 4) || shares_batch(code, heads * 2 * l->D, b) || shares_batch(exp, heads * 4, b))
-    return TV_ERR_ARG;
+  if (!apart(b->status, {{code, heads * 2 * l->D}, {exp, heads * 4}}, {{l->K, pool}, offsets_of(b, rows), table_of(b), lens_of(b)})) return TV_ERR_ARG;
   if (l->Hkv > 65535) return TV_ERR_SHAPE;
   BoundsParams p{};
   p.b = paged_seqs(l, b);
@@ -639,21 +636,13 @@ extern "C" tv_status tv_paged_select(const tv_paged_layer* l, const tv_paged* b,
   if (!code || !exp || !q || !sel || !count || first < 0 || last < 1 || n_sel < 1 || n_sel > 4096 || first > n_sel || last > n_sel - first)
     return TV_ERR_ARG;
   if (!aligned16(code) || !aligned16(exp) || !aligned16(q) || !aligned16(sel) || !aligned16(count) || !aligned16(ws)) return TV_ERR_ALIGN;
-  // lists are written while others' bounds and queries are read
   const size_t units_b = static_cast<size_t>(b->n_seq) * l->Hkv, heads = static_cast<size_t>(l->n_pages) * l->Hkv;
-  const size_t nq = bytes_of(b->n_seq, static_cast<int64_t>(l->Hq) * l->D, l->dtype);
-  if (share_memory(sel, units_b * n_sel * 4, count, units_b * 4)) return TV_ERR_ARG;
-  for (const auto& o : {std::pair<const void*, size_t>(sel, units_b * n_sel * 4), std::pair<const void*, size_t>(count, units_b * 4)})
-    if (share_memory(o.first, o.second, code, heads * 2 * l->D) || share_memory(o.first, o.second, exp, heads * 4) ||
-        share_memory(o.first, o.second, q, nq) || shares_batch(o.first, o.second, b))
-      return TV_ERR_ARG;
   const size_t need = tv_paged_select_workspace_bytes(l, b);
   if (need > 0 && (!ws || ws_bytes < need)) return TV_ERR_WORKSPACE;
-  if (need > 0) {
-    for (const auto& x : {std::pair<const void*, size_t>(sel, units_b * n_sel * 4), {count, units_b * 4}, {code, heads * 2 * l->D}, {exp, heads * 4}, {q, nq}})
-      if (share_memory(ws, need, x.first, x.second)) return TV_ERR_ARG;
-    if (shares_batch(ws, need, b)) return TV_ERR_ARG;
-  }
+  // lists are written while others' bounds and queries are read
+  if (!apart(b->status, {{sel, units_b * n_sel * 4}, {count, units_b * 4}, {ws, need}},
+             {{code, heads * 2 * l->D}, {exp, heads * 4}, {q, bytes_of(b->n_seq, static_cast<int64_t>(l->Hq) * l->D, l->dtype)}, table_of(b), lens_of(b)}))
+    return TV_ERR_ARG;
   SelectParams p{};
   p.b = paged_seqs(l, b);
   p.q = q;
@@ -688,6 +677,7 @@ extern "C" tv_status tv_paged_advance(const tv_paged* b, const tv_paged_rows* ro
   if (!aligned16(b->len) || !aligned16(b->status)) return TV_ERR_ALIGN;
   const tv_status c = paged_rows_check(rows);
   if (c != TV_OK) return c;
+  if (!apart(b->status, {lens_of(b)}, {offsets_of(b, rows)})) return TV_ERR_ARG;
   const PagedSeqs v{nullptr, b->len, b->status, b->n_seq, 0, b->max_len, 0, 0};
   launch_k(true, paged_advance_kernel, dim3((b->n_seq + 127) / 128), dim3(128), 0, reinterpret_cast<cudaStream_t>(stream), len,
            rows ? rows->row_off : nullptr, v, rows ? rows->n_total : 0, rows ? rows->n_max : 0);
