@@ -75,9 +75,12 @@ class PagedCaches:
     # ---- slots and pages (host calls between steps; device writes in the order of `stream`)
     def admit(self, slot: int, like: int | None = None, rows: int = 0, stream=None):
         """Makes an idle slot active: empty, or with the first `rows` rows of slot `like` (whole pages, shared)."""
+        self._one(slot)
+        if like is not None:
+            self._one(like)
         if self.lens[slot] >= 0:
             raise ValueError(f"slot {slot} is in use")
-        if rows % self.page or (like is None and rows) or (like is not None and rows > self.lens[like]):
+        if rows < 0 or rows % self.page or (like is None and rows) or (like is not None and rows > self.lens[like]):
             raise ValueError(f"{rows} rows of slot {like} are not whole pages that it holds")
         self.pages[slot] = list(self.pages[like][:rows // self.page]) if rows else []
         for p in self.pages[slot]:
@@ -87,6 +90,7 @@ class PagedCaches:
 
     def retire(self, slot: int, stream=None):
         """Makes a slot idle and gives back the pages that no other one shares."""
+        self._one(slot)
         for p in self.pages[slot]:
             self.users[p] -= 1
             if self.users[p] == 0:
@@ -111,6 +115,10 @@ class PagedCaches:
                     self.users[p] = 1
                     self.pages[slot].append(p)
                 self._write(slot, stream, lengths=False)
+
+    def _one(self, slot):
+        if not 0 <= slot < self.n_slots:
+            raise ValueError(f"slot {slot} of {self.n_slots}")
 
     def _rows(self, rows):
         return [int(L >= 0) for L in self.lens] if rows is None else list(rows)
