@@ -247,6 +247,14 @@ def _torch_stream(stream):
     return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
 
 
+def _need_no_capture(dst, stream):
+    """Raises inside a graph's capture: what the host writes to a device buffer goes before a replay."""
+    if dst.is_cuda:
+        with torch.cuda.stream(_torch_stream(stream)):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("rows are written from the host: before a graph's replay, not inside its capture")
+
+
 def _upload(dst, values, stream):
     """Writes a few int32 to a device buffer in the stream's order: without
     waiting for it, or, on the current stream (None), until they are there."""
@@ -254,9 +262,8 @@ def _upload(dst, values, stream):
     if not dst.is_cuda:
         dst.copy_(src)
         return
+    _need_no_capture(dst, stream)
     with torch.cuda.stream(_torch_stream(stream)):
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("rows are written from the host: before a graph's replay, not inside its capture")
         if stream is None:
             dst.copy_(src)
         else:

@@ -82,6 +82,7 @@ class PagedCaches:
             raise ValueError(f"slot {slot} is in use")
         if rows < 0 or rows % self.page or (like is None and rows) or (like is not None and rows > self.lens[like]):
             raise ValueError(f"{rows} rows of slot {like} are not whole pages that it holds")
+        B._need_no_capture(self.table, stream)
         self.pages[slot] = list(self.pages[like][:rows // self.page]) if rows else []
         for p in self.pages[slot]:
             self.users[p] += 1
@@ -91,6 +92,7 @@ class PagedCaches:
     def retire(self, slot: int, stream=None):
         """Makes a slot idle and gives back the pages that no other one shares."""
         self._one(slot)
+        B._need_no_capture(self.table, stream)
         for p in self.pages[slot]:
             self.users[p] -= 1
             if self.users[p] == 0:
@@ -108,6 +110,8 @@ class PagedCaches:
             raise ValueError(f"a slot would hold more than {self.max_len} rows")
         if sum(need) > len(self.free):
             raise MemoryError(f"{sum(need)} pages wanted, {len(self.free)} free")
+        if any(need):
+            B._need_no_capture(self.table, stream)
         for slot, n in enumerate(need):
             if n:
                 for _ in range(n):
@@ -159,7 +163,9 @@ class PagedCaches:
         self.lens = [L + n if L >= 0 else L for L, n in zip(self.lens, self._rows(rows))]
 
     def decode(self, inputs, groups: B.PagedGroups | None = None, stream=None):
-        """One step through every layer, inputs by layer: room for its rows, the layers, the lengths."""
+        """One step through every layer, inputs by layer: room for its rows, the layers, the lengths.  (A captured step is
+        layer() and advance(); grow() and advanced() go with each replay.)"""
+        B._need_no_capture(self.table, stream)
         self.grow(stream=stream)
         for li, x in enumerate(inputs):
             self.layer(li, x, groups, stream)
