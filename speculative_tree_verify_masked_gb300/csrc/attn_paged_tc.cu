@@ -669,7 +669,9 @@ __global__ void __launch_bounds__(256, SHARED ? 6 : 4) attn_paged_join_kernel(co
   const int grp = threadIdx.x / LANES, col = threadIdx.x % LANES * 4;
   const uint32_t line = static_cast<uint32_t>(p.item) * (D + 4);  // (offsets in 32 bits: all pieces are under 2^32 values)
   pdl_wait();
-  const bool bad = status_set(p.v.b.status);  // (a thread that finds it set reads nothing more; the CTA leaves at the barrier)
+  // (A warp that finds the word set leaves; another stream's call may set it between two warps' looks, so those that
+  // stay write only where all have come to the barrier.  The decision at a barrier up here is 0.25 us of a call.)
+  const bool bad = status_set(p.v.b.status);
   int s, h, head, c0, n, np = 0;  // head: of the KV head's; CTAs c0 .. hold pieces, n with the np of a prefix
   const float *own, *pre = nullptr;
   uint32_t step = 0;
@@ -680,12 +682,12 @@ __global__ void __launch_bounds__(256, SHARED ? 6 : 4) attn_paged_join_kernel(co
     const int u = s * p.v.Hkv + h, m = p.MT > 1 ? head / p.item : 0;
     const int2 span = p.span[u * p.MT + m];
     const int4 g = p.info[s];
-    if (span.y < 0) return;  // (an idle slot's row is left as it was)
+    if (bad || span.y < 0) return;  // (an idle slot's row is left as it was)
     c0 = span.x;
     const int c1 = span.y, row = g.w * p.G + head;
     np = g.z;
     if (np == 0 && c0 == c1) return;  // written whole
-    n = bad ? 0 : np + c1 - c0 + 1;
+    n = np + c1 - c0 + 1;
     step = static_cast<uint32_t>(g.y) * 128 * (D + 4);
     if (np > 0) pre = p.rec_prefix + (static_cast<size_t>(g.x + h * np * g.y + row / 128) * 128 + row % 128) * (D + 4);
     own = (c0 == c1 ? p.rec_item + (static_cast<size_t>(u) * p.MT + m) * line : p.rec + (static_cast<size_t>(c0) * 2 + 1) * line) +
@@ -695,9 +697,9 @@ __global__ void __launch_bounds__(256, SHARED ? 6 : 4) attn_paged_join_kernel(co
     s = c.x;
     h = c.y;
     head = c.z * p.item + static_cast<int>(blockIdx.y);
-    if (s < 0 || head >= p.G) return;
+    if (s < 0 || head >= p.G || bad) return;
     c0 = static_cast<int>(blockIdx.x) - 1;
-    n = bad ? 0 : c.w - c0 + 1;
+    n = c.w - c0 + 1;
     own = p.rec + (static_cast<size_t>(c0) * 2 + 1) * line + static_cast<size_t>(blockIdx.y) * (D + 4);
   }
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(256, SHARED ? 6 : 4) attn_paged_join_kernel(co
   }
   *reinterpret_cast<float4*>(&acc_s[grp][col]) = acc;
   if (col == 0) ml_s[grp] = make_float2(m, l);
-  if (__syncthreads_or(bad)) return;
+  if (__syncthreads_count(1) != static_cast<int>(blockDim.x)) return;
   const int t = threadIdx.x;
   if (t >= D / 2) return;  // two columns a thread
   float mn = -INFINITY, lt = 0.f, y0 = 0.f, y1 = 0.f;
