@@ -237,3 +237,22 @@ def test_caches_share_prefixes_that_pay():
         # both sides round each weight and the output (half a step each), over values whose largest is under 6
         assert (x["out"].float() - z["out"].float()).abs().max() <= 4 * 2.0 ** -8 * 6
     assert a.status() == 0 and b.status() == 0 and plain.status() == 0
+
+
+@pytest.mark.parametrize("sizes,shared", [([1] * 1024, [0] * 1024), ([2, 3, 5, 1, 0, 4] * 68 + [4], [512, 448, 320, 64, 512, 512] * 68 + [512]),
+                                          ([700, 0, 324], [512, 64, 512])])
+def test_as_many_slots_as_a_call_takes(sizes, shared):
+    """1,024 slots in up to as many groups, more of both than a CTA has threads; idle ones among them."""
+    n = sum(sizes)
+    assert n == 1024
+    lens = [512 + (i * 7) % 60 if i % 23 else -1 for i in range(n)]
+    p = Pools(lens, 16, (4, 2, 128), groups=list(zip(sizes, shared)))
+    saved = sum(max(0, sum(lens[i] >= 0 for i in range(a, a + m)) - 1) * x for a, m, x in
+                zip([sum(sizes[:g]) for g in range(len(sizes))], sizes, shared)) * 2 * 128 * 4
+    assert saved >= 1.05 * (200 << 20) or max(sizes) == 1
+    got = p.attn(p.gate, p.groups).clone()
+    p.expect(got, p.gate, slots=sorted({0, 1, 2, 23, 287, 288, 383, 384, 699, 700, 1022, 1023}))
+    assert torch.equal(got, p.attn(p.gate, p.groups)) and p.status() == 0
+    # all of them, beside the call that shares nothing: each side rounds every weight and the output, over values under 6
+    plain = p.attn(p.gate).float()
+    assert (got.float() - plain).abs().max() <= 4 * 2.0 ** -8 * 6
