@@ -619,13 +619,15 @@ size_t tv_paged_attn_workspace_bytes(const tv_paged_layer* layer, const tv_paged
  *     out[s,h] = sum_t softmax_t(scale q[s,h] . K[t]) V[t]   (times sigmoid(gate[s,h]))
  *  groups or NULL: the prefixes of groups with two active members or more are
  *         read once for all members, from the table of the first active one, where
- *         that saves the call 200 MB of reads or more (it costs about as long as
- *         those); the result is the same up to rounding.  fp32 layers read every
+ *         that saves the call 210 MB (200 << 20 bytes) of reads or more (it costs about as
+ *         long as those); the result is the same up to rounding.  fp32 layers read every
  *         slot's own.  Offsets or lengths that do not hold what is said above set
  *         TV_ERR_ROWS (bf16 layers).
  *  q, out [n_seq][Hq][D]; gate the same or NULL (may be out)
  *  scale  score scale > 0
- *  workspace as in tv_attn_prompt. */
+ *  workspace as in tv_attn_prompt.
+ * What a slot sees by itself is read once for each sixteen query heads of a KV
+ * head (bf16), or for each one (fp32). */
 tv_status tv_paged_attn(const tv_paged_layer* layer, const tv_paged* batch, const tv_paged_groups* groups, const void* q,
                         const void* gate, void* out, float scale, void* workspace, size_t workspace_bytes,
                         tv_stream stream);

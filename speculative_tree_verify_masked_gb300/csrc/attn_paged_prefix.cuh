@@ -24,8 +24,10 @@ struct PagedPrefixParams {
 // and values that members would read again (from L2, mostly).  24 + 4 heads of 256, us a call shared
 // and slot by slot: 8 members of 16,384 rows (470 MB saved) 32.5 and 42.8, 4 (201 MB) 30.3 and 28.4; of 4,096 rows
 // 16 members (252 MB) 26.0 and 28.6, 8 (117 MB) 24.8 and 21.0; 2 of 65,536 (268 MB) 67.2 and 67.2.  16 + 2
-// heads of 128: 8 of 65,536 (470 MB) 32.8 and 67.7, 4 (201 MB) 39.9 and 38.8.
-constexpr int64_t kSharedBytes = 200 << 20;
+// heads of 128: 8 of 65,536 (470 MB) 32.8 and 67.7, 4 (201 MB) 39.9 and 38.8.  All of that in pages of 64 rows.  In
+// pages of 16, whose copies bind the kernel for prefixes, the bound is low: 8 members of 16,384 39.6 and 50.1, 5 (268 MB) 37.0 and
+// 35.2, 56 of 1,024 (231 MB) 32.2 and 30.1; of 32, 34.2 and 43.9, 31.2 and 31.7, 29.3 and 28.1.
+constexpr int64_t kSharedBytes = 200 << 20;  // 210 MB
 // Bytes of a row's keys and values in bf16.
 __host__ __device__ inline int64_t kv_row_bytes(int Hkv, int D) { return static_cast<int64_t>(Hkv) * D * 4; }
 

@@ -37,10 +37,12 @@
 //
 // Bound by HBM while slots are long: 8 slots of 65,536 rows (1.07 GB, pages of 64) 161 to 169 us for
 // heads of 64, 128 and 256, 0.95 to 0.99 of a copy's rate; 96 ragged slots up to 32,768 rows
-// (16 + 2 heads of 128, pages of 32, 563 MB) 92.9 us, 6.1 TB/s, 0.90: some 3 us until the first tile is there, the
+// (16 + 2 heads of 128, pages of 32, 563 MB) 94.3 us, 6.0 TB/s, 0.88: some 3 us until the first tile is there, the
 // pieces and the join are the rest.  Short slots are bound by latency: 4 up to 1,025 rows (24 + 4 heads of 256)
 // 9.9 us, of which the lengths, the table, keys and values are reads one behind the other, some 3.4 the join.
-// Heads of 64 in pages of 16 rows reach 0.66: a copy of 2 KB a page is too small.
+// Heads of 64 in pages of 16 rows reach 0.66: a copy of 2 KB a page is too small.  More than sixteen query heads a KV head
+// walk its keys and values once for each sixteen: 8 slots of 65,536 rows, 1 KV head of 128 (39.8 us of bytes), 49.7 us with 8 query heads,
+// 51.9 with 16, 91.0 with 32, 165 with 64, 314 with 128.
 // (Query heads on the long side of the tiles, as many as 16 fill: 256 slots of 100 rows 46 us against 35.)
 #include <algorithm>
 #include <cstring>

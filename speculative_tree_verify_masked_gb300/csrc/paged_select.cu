@@ -24,7 +24,8 @@
 // The bounds are bound by reads of whole pages, one CTA each: 16,421 rows of two prompts (33.6 MB of keys) 8.9 us, 3.8
 // TB/s in a grid of 1,032 CTAs that runs once; a step of 192 slots 2.7 us, a launch's latency.  (Up to eight rows of a lane
 // are in flight, two of small pages; four in one loop 9.3 us, and 5.3 against 4.6 for a few pages of 128 rows of 256; CTAs of
-// 256 threads 11.0, and 3.4 a step.)
+// 256 threads 11.0, and 3.4 a step.)  The grid has the pages of n_max rows for every slot, whatever rows it has: one slice of
+// 4,096 rows beside 191 decode rows, 24 + 4 heads of 256, 100 us in pages of 16 and 27 in pages of 64, nearly all of it CTAs that find no page.
 //
 // The choice is a radix selection of the n-th highest key by digits of eight bits,
 // from the highest bit in which the keys differ down, until a digit leaves no
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(TH, 512 / TH) paged_select_kernel(const __grid
   }
   if (bad) return;
   // ---- the choice: a run of keys a thread; three to eight in registers (shared memory then holds all of them), one or two in
-  // a loop, since all of this runs once, from cold code (64 pages 4.2 us, 4.7 from registers; 2,048 pages 8.7, 10.0 in a loop)
+  // a loop, since all of this runs once, from cold code (64 pages 4.5 us, 4.7 from registers; 2,048 pages 8.7, 10.0 in a loop)
   constexpr int RUN = 8;
   const int run = (n + TH - 1) / TH, i0 = min(tid * run, n), i1 = min(i0 + run, n);
   const bool few = run > 2 && run <= RUN;
